@@ -175,8 +175,6 @@ def prepare(case, seed):
     st["table"] = torch.from_numpy(order.permutation(pages).reshape(B, per).astype(np.int32)).cuda()
     st["lens"] = torch.from_numpy(lens.astype(np.int32)).cuda()
     st["news"] = torch.from_numpy(news.astype(np.int32)).cuda()
-    # upper bounds that a serving program knows on the host: of all lengths, and of the read-back
-    st["max_len"] = int((lens + news).max())
     if c["op"] == "cache":
         st["k"], st["v"] = _randn(gen, B, T, c["H"], d).to(dt), _randn(gen, B, T, c["H"], d).to(dt)
         first = (lens // c["page"]) * c["page"]
@@ -190,7 +188,7 @@ def prepare(case, seed):
         st["cache"] = binding.KvCache(pages, c["H"], d, page=c["page"], code=c["code"],
                                       buffers=(st["k_codes"], st["v_codes"], st["k_scale"], st["v_scale"]))
         if c["op"] == "attn":
-            st["plan"] = binding.CacheAttention(st["cache"], B, T, c["Hq"], max_len=st["max_len"],
+            st["plan"] = binding.CacheAttention(st["cache"], B, T, c["Hq"],
                                                 io=c["io"], out=c["out"], scale=1 / math.sqrt(d),
                                                 window=c["window"])
     return st
