@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libdr.so")
 
 DR_OK, DR_ERR_INVALID_ARG, DR_ERR_UNSUPPORTED, DR_ERR_WORKSPACE, DR_ERR_ALIGNMENT, \
-    DR_ERR_CUDA, DR_ERR_TIMEOUT, DR_ERR_SCRATCH_LIMIT = range(8)
+    DR_ERR_CUDA, DR_ERR_TIMEOUT, DR_ERR_SCRATCH_LIMIT, DR_ERR_INDEX = range(9)
 DR_DELTANET, DR_GDN, DR_KDA, DR_GDN2 = 0, 1, 2, 3
 DR_BF16, DR_F32 = 0, 1
 DR_FLAG_REUSE_FWD = 1
@@ -33,6 +33,32 @@ class DrDesc(ctypes.Structure):
         ("chunk_table", ctypes.c_void_p), ("chunk_offsets", ctypes.c_void_p),
         ("num_chunks", ctypes.c_int),
     ]
+
+
+ROPE_STYLES = {"halves": 0, "pairs": 1}
+CACHE_CODES = {"i8": 0, "e4m3": 1}
+
+
+class DrRopeDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "Hq", "Hk", "d", "rot", "style", "io_dtype",
+                                            "out_dtype", "grad_dtype", "table_rows")]
+    _fields_ += [("eps", ctypes.c_float)]
+    _fields_ += [(n, ctypes.c_longlong) for n in ("ld_q", "ld_k", "ld_oq", "ld_ok")]
+
+
+class DrCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("num_pages", "H", "d", "page", "code")]
+    _fields_ += [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "status")]
+
+
+class DrCacheSeqs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("page_table", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int), ("lens", ctypes.c_void_p), ("counts", ctypes.c_void_p)]
+
+
+class DrAttnDesc(ctypes.Structure):
+    _fields_ = [("Hq", ctypes.c_int), ("io_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int),
+                ("window", ctypes.c_int), ("scale", ctypes.c_float), ("ld_q", ctypes.c_longlong)]
 
 
 class DrError(RuntimeError):
@@ -82,6 +108,22 @@ def load(path: str = LIB_PATH):
     lib.dr_gdn2_fwd.restype = I
     lib.dr_gdn2_bwd.argtypes = [D] + [P] * 16 + [P, S, P]
     lib.dr_gdn2_bwd.restype = I
+    R, C, Q, A = (ctypes.POINTER(x) for x in (DrRopeDesc, DrCache, DrCacheSeqs, DrAttnDesc))
+    L = ctypes.c_longlong
+    lib.dr_norm_rope_fwd.argtypes = [R] + [P] * 11
+    lib.dr_norm_rope_fwd.restype = I
+    lib.dr_norm_rope_workspace_bytes.argtypes = [R]
+    lib.dr_norm_rope_workspace_bytes.restype = S
+    lib.dr_norm_rope_bwd.argtypes = [R] + [P] * 15 + [S, P]
+    lib.dr_norm_rope_bwd.restype = I
+    lib.dr_cache_write.argtypes = [C, Q, P, L, P, L, I, P]
+    lib.dr_cache_write.restype = I
+    lib.dr_cache_read.argtypes = [C, Q, P, P, I, P]
+    lib.dr_cache_read.restype = I
+    lib.dr_cache_attn_workspace_bytes.argtypes = [C, A, I, I]
+    lib.dr_cache_attn_workspace_bytes.restype = S
+    lib.dr_cache_attn.argtypes = [C, Q, A] + [P] * 4 + [S, P]
+    lib.dr_cache_attn.restype = I
     lib.dr_trace_enable.argtypes = [I]
     lib.dr_trace_enable.restype = I
     lib.dr_trace_count.argtypes = []
@@ -387,3 +429,248 @@ class Gdn2Problem(Problem):
         finally:
             d.flags = 0
         return out
+
+
+# ------------------------------------------------------------------ softmax-attention layer
+def _rows(t, heads, d, what):
+    """Elements between the token rows of t [B, T, heads, d]: contiguous, or a range of heads of a
+    wider contiguous tensor."""
+    B, T, H, D = t.shape
+    if B * T == 0 and (H, D) == (heads, d):
+        return H * D
+    ld = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else H * D)
+    ok = (H, D) == (heads, d) and (D == 1 or t.stride(3) == 1) and (H == 1 or t.stride(2) == D) \
+        and (T == 1 or B == 1 or t.stride(0) == T * ld)
+    if not ok:
+        raise ValueError(f"{what}: shape {tuple(t.shape)} strides {t.stride()} is no [B, T, {heads}, {d}] "
+                         "with whole token rows at one distance")
+    return ld
+
+
+def _expect(t, dtype, shape, what, device=None):
+    import torch  # noqa: F401
+    if t is None:
+        return
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+
+
+_TORCH_TYPES = {"bf16": "bfloat16", "f32": "float32"}
+_TYPE_CODES = {"bf16": DR_BF16, "f32": DR_F32}
+
+
+def _torch_type(name):
+    import torch
+    return getattr(torch, _TORCH_TYPES[name])
+
+
+class HeadNormRope:
+    """RMS norm of queries and keys for each head with the position rotation in the same pass
+    (dr_norm_rope_fwd / dr_norm_rope_bwd) for one problem shape.
+
+    q [B, T, Hq, d] and k [B, T, Hk, d] may be head ranges of one packed projection.  The position
+    of token (b, t) is ``positions[b, t]`` (default t) plus ``start[b]`` (default 0), a row of the
+    tables cos, sin [rows, rot / 2]."""
+
+    def __init__(self, B, T, Hq, Hk, d, rot=None, style="halves", io="bf16", out="bf16", grad="bf16",
+                 eps=1e-6, device="cuda"):
+        import torch
+        self.device = torch.device(device)
+        e = DrRopeDesc()
+        e.B, e.T, e.Hq, e.Hk, e.d = B, T, Hq, Hk, d
+        e.rot = d if rot is None else rot
+        e.style = ROPE_STYLES[style]
+        e.io_dtype, e.out_dtype, e.grad_dtype = _TYPE_CODES[io], _TYPE_CODES[out], _TYPE_CODES[grad]
+        e.eps = float(eps)
+        e.ld_q = e.ld_oq = Hq * d
+        e.ld_k = e.ld_ok = Hk * d
+        e.table_rows = 0
+        self.desc = e
+        self.io_dtype, self.out_dtype, self.grad_dtype = map(_torch_type, (io, out, grad))
+        self.ws = None
+        if int(load().dr_norm_rope_workspace_bytes(ctypes.byref(e))) == 0:
+            raise DrError(DR_ERR_UNSUPPORTED, "dr_norm_rope_workspace_bytes")
+
+    def _fill(self, q, k, wq, wk, cos, sin, positions, start, oq, ok):
+        import torch
+        e = self.desc
+        for t, H, what in ((q, e.Hq, "q"), (k, e.Hk, "k")):
+            if t is not None and (t.dtype != self.io_dtype or tuple(t.shape[:2]) != (e.B, e.T)):
+                raise ValueError(f"{what}: expected {self.io_dtype} [{e.B}, {e.T}, {H}, {e.d}]")
+        e.ld_q, e.ld_oq = (_rows(q, e.Hq, e.d, "q"), _rows(oq, e.Hq, e.d, "output of q")) if e.Hq else (0, 0)
+        e.ld_k, e.ld_ok = (_rows(k, e.Hk, e.d, "k"), _rows(ok, e.Hk, e.d, "output of k")) if e.Hk else (0, 0)
+        for w, what in ((wq, "wq"), (wk, "wk")):
+            _expect(w, torch.float32, (e.d,), what)
+        if e.rot:
+            e.table_rows = cos.shape[0]
+            _expect(cos, torch.float32, (e.table_rows, e.rot // 2), "cos")
+            _expect(sin, torch.float32, (e.table_rows, e.rot // 2), "sin")
+        _expect(positions, torch.int32, (e.B, e.T), "positions")
+        _expect(start, torch.int32, (e.B,), "start")
+
+    def _stream(self):
+        import torch
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def _empty(self, H, dtype):
+        import torch
+        return torch.empty(self.desc.B, self.desc.T, H, self.desc.d, dtype=dtype, device=self.device)
+
+    def forward(self, q, k, wq, wk, cos, sin, positions=None, start=None, yq=None, yk=None):
+        """yq, yk in the output type (given: written there, in place where it is q or k itself)."""
+        e = self.desc
+        yq = self._empty(e.Hq, self.out_dtype) if yq is None else yq
+        yk = self._empty(e.Hk, self.out_dtype) if yk is None else yk
+        if yq.dtype != self.out_dtype or yk.dtype != self.out_dtype:
+            raise ValueError(f"yq, yk: expected {self.out_dtype}")
+        self._fill(q, k, wq, wk, cos, sin, positions, start, yq, yk)
+        _check(load().dr_norm_rope_fwd(ctypes.byref(e), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos),
+                                       _ptr(sin), _ptr(positions), _ptr(start), _ptr(yq), _ptr(yk),
+                                       self._stream()), "dr_norm_rope_fwd")
+        return yq, yk
+
+    def backward(self, q, k, wq, wk, cos, sin, dyq, dyk, positions=None, start=None, out=None):
+        """{dq, dk, dwq, dwk} for the incoming gradients dyq, dyk (contiguous, of the input type)."""
+        import torch
+        e = self.desc
+        if out is None:
+            out = {"dq": self._empty(e.Hq, self.grad_dtype), "dk": self._empty(e.Hk, self.grad_dtype),
+                   "dwq": None if wq is None else torch.empty_like(wq),
+                   "dwk": None if wk is None else torch.empty_like(wk)}
+        if out["dq"].dtype != self.grad_dtype or out["dk"].dtype != self.grad_dtype:
+            raise ValueError(f"dq, dk: expected {self.grad_dtype}")
+        self._fill(q, k, wq, wk, cos, sin, positions, start, out["dq"], out["dk"])
+        for t, H, what in ((dyq, e.Hq, "dyq"), (dyk, e.Hk, "dyk")):
+            if H:
+                _expect(t, self.io_dtype, (e.B, e.T, H, e.d), what)
+        if self.ws is None:
+            n = int(load().dr_norm_rope_workspace_bytes(ctypes.byref(e)))
+            self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
+        _check(load().dr_norm_rope_bwd(ctypes.byref(e), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos),
+                                       _ptr(sin), _ptr(positions), _ptr(start), _ptr(dyq), _ptr(dyk),
+                                       _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dwq"]), _ptr(out["dwk"]),
+                                       self.ws.data_ptr(), self.ws.numel(), self._stream()),
+               "dr_norm_rope_bwd")
+        return out
+
+
+class KvCache:
+    """A paged cache of keys and values in 8 bits ("i8" or "e4m3") with one scale for each page and
+    head (dr_cache_write / dr_cache_read).  ``buffers`` = (k codes, v codes, k scales, v scales)
+    takes existing device memory: codes [num_pages, H, page, d] of one byte each, scales
+    [num_pages, H] fp32."""
+
+    def __init__(self, num_pages, H, d, page=64, code="i8", buffers=None, device="cuda"):
+        import torch
+        self.device = torch.device(device)
+        kind = torch.int8 if code == "i8" else torch.float8_e4m3fn
+        if buffers is None:
+            buffers = [torch.zeros(num_pages, H, page, d, dtype=torch.int8, device=self.device).view(kind)
+                       for _ in range(2)]
+            buffers += [torch.zeros(num_pages, H, dtype=torch.float32, device=self.device) for _ in range(2)]
+        self.k, self.v, self.k_scale, self.v_scale = buffers
+        for t, what in ((self.k, "k codes"), (self.v, "v codes")):
+            _expect(t, kind, (num_pages, H, page, d), what)
+        for t, what in ((self.k_scale, "k scales"), (self.v_scale, "v scales")):
+            _expect(t, torch.float32, (num_pages, H), what)
+        self.word = torch.zeros(4, dtype=torch.int32, device=self.device)
+        c = DrCache()
+        c.num_pages, c.H, c.d, c.page, c.code = num_pages, H, d, page, CACHE_CODES[code]
+        c.k, c.v = self.k.data_ptr(), self.v.data_ptr()
+        c.k_scale, c.v_scale = self.k_scale.data_ptr(), self.v_scale.data_ptr()
+        c.status = self.word.data_ptr()
+        self.desc = c
+
+    def _stream(self):
+        import torch
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def seqs(self, table, lens, counts, T):
+        """The call's positions: T tokens (or counts[b] <= T) after lens[b], in the pages of table
+        [B, pages]."""
+        import torch
+        B = lens.shape[0]
+        _expect(table, torch.int32, (B, table.shape[1]), "table")
+        _expect(lens, torch.int32, (B,), "lens")
+        _expect(counts, torch.int32, (B,), "counts")
+        s = DrCacheSeqs()
+        s.B, s.T, s.table_stride = B, T, table.shape[1]
+        s.page_table, s.lens, s.counts = table.data_ptr(), lens.data_ptr(), _ptr(counts)
+        return s
+
+    def write(self, k, v, table, lens, counts=None):
+        """Append k, v [B, T, H, d] (bf16 or fp32, or head ranges of a packed projection) after the
+        first lens[b] positions of every sequence."""
+        import torch
+        c = self.desc
+        if k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float32) or k.shape != v.shape:
+            raise ValueError("k, v: expected two bf16 or two fp32 tensors of one shape")
+        if k.shape[0] != lens.shape[0]:
+            raise ValueError("k, v: one sequence for each of lens")
+        s = self.seqs(table, lens, counts, k.shape[1])
+        _check(load().dr_cache_write(ctypes.byref(c), ctypes.byref(s), _ptr(k), _rows(k, c.H, c.d, "k"),
+                                     _ptr(v), _rows(v, c.H, c.d, "v"), _dt(k), self._stream()),
+               "dr_cache_write")
+
+    def read(self, table, lens, counts, T, out="bf16", k=None, v=None):
+        """k, v [B, T, H, d]: the values at positions lens[b] .. lens[b] + counts[b] - 1, zeros after."""
+        import torch
+        c = self.desc
+        s = self.seqs(table, lens, counts, T)
+        shape = (s.B, T, c.H, c.d)
+        k = torch.empty(shape, dtype=_torch_type(out), device=self.device) if k is None else k
+        v = torch.empty(shape, dtype=_torch_type(out), device=self.device) if v is None else v
+        _expect(k, _torch_type(out), shape, "k")
+        _expect(v, _torch_type(out), shape, "v")
+        _check(load().dr_cache_read(ctypes.byref(c), ctypes.byref(s), _ptr(k), _ptr(v), _TYPE_CODES[out],
+                                    self._stream()), "dr_cache_read")
+        return k, v
+
+    def status(self) -> int:
+        """DR_OK, or DR_ERR_INDEX after a call met a page number, length or count out of range."""
+        return check_status(self.word.data_ptr(), self._stream())
+
+    def clear_status(self) -> None:
+        self.word.zero_()
+
+
+class CacheAttention:
+    """Attention of up to T query tokens of each of B sequences over a KvCache (dr_cache_attn)."""
+
+    def __init__(self, cache, B, T, Hq, io="bf16", out="bf16", scale=None, window=0):
+        import torch
+        self.cache, self.B, self.T = cache, B, T
+        a = DrAttnDesc()
+        a.Hq, a.io_dtype, a.out_dtype, a.window = Hq, _TYPE_CODES[io], _TYPE_CODES[out], window
+        a.scale = cache.desc.d ** -0.5 if scale is None else float(scale)
+        a.ld_q = Hq * cache.desc.d
+        self.desc = a
+        self.io_dtype, self.out_dtype = _torch_type(io), _torch_type(out)
+        n = int(load().dr_cache_attn_workspace_bytes(ctypes.byref(cache.desc), ctypes.byref(a), B, T))
+        if n == 0:
+            raise DrError(DR_ERR_UNSUPPORTED, "dr_cache_attn_workspace_bytes")
+        self.ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+
+    def forward(self, q, table, lens, counts=None, o=None, lse=None, want_lse=False):
+        """o [B, T, Hq, d] and lse [B, T, Hq] (or None): query t of sequence b is the position
+        lens[b] + t, which the cache already holds."""
+        import torch
+        a, c = self.desc, self.cache.desc
+        shape = (self.B, self.T, a.Hq, c.d)
+        if q.dtype != self.io_dtype or tuple(q.shape) != shape:
+            raise ValueError(f"q: expected {self.io_dtype} {shape}, got {q.dtype} {tuple(q.shape)}")
+        if lens.shape[0] != self.B:
+            raise ValueError(f"lens: expected {self.B} lengths")
+        a.ld_q = _rows(q, a.Hq, c.d, "q")
+        s = self.cache.seqs(table, lens, counts, self.T)
+        if o is None:
+            o = torch.empty(shape, dtype=self.out_dtype, device=self.cache.device)
+        if lse is None and want_lse:
+            lse = torch.empty(shape[:3], dtype=torch.float32, device=self.cache.device)
+        _expect(o, self.out_dtype, shape, "o")
+        _expect(lse, torch.float32, shape[:3], "lse")
+        _check(load().dr_cache_attn(ctypes.byref(c), ctypes.byref(s), ctypes.byref(a), _ptr(q), _ptr(o),
+                                    _ptr(lse), self.ws.data_ptr(), self.ws.numel(), self.cache._stream()),
+               "dr_cache_attn")
+        return o, lse

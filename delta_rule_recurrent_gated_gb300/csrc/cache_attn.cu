@@ -1,0 +1,645 @@
+// cache_attn.cu -- attention of a few query tokens of each sequence over the paged 8-bit cache
+// (dr.h, dr_cache_attn): one pass over the codes with running softmax statistics.
+//
+// The rows of a sequence and cache head are its query tokens times the G query heads that share
+// the cache head, row = t * G + g.  A block works on a tile of 8 NT rows of one (sequence, cache
+// head) over a stretch of its positions, in stages of 64; warp w takes positions 16 w .. 16 w + 15
+// of each stage on its own, from global memory to registers, so that warps never wait for one
+// another before the rows are joined at the end.
+//
+// Matrix products (m16n8k16, 16-bit operands, fp32 accumulation), with the 16 positions as rows:
+//   S^T = K Q^T    A = K codes (16 positions x d), B = Q^T (d x 8 rows)
+//   O^T += V^T P^T A = V^T codes (16 channels x 16 positions), B = P^T (16 positions x 8 rows)
+// Which channels a thread supplies is free as long as both operands agree, so every thread loads
+// 16 consecutive bytes and no operand passes through shared memory.  A code is exact in 16 bits.
+//
+// Softmax in base 2.  The page scales enter in fp32: the key scale multiplies S, the value scale
+// vs multiplies the weights.  Both references are whole numbers, so that every rescaling is exact:
+//   m >= max s, weights p = 2^(s - m), l = sum p;
+//   M >= max (s + log2 vs), w = p vs 2^(m - M + 14) <= 2^14 is the 16-bit operand.
+// With PREC (fp32 queries or outputs) queries and weights are split into two 16-bit terms.
+//
+// Work is divided evenly: the stages of all tiles form one line, block i of n takes the i-th part
+// of it.  A tile that lies in one block is finished there; of the others each block leaves its
+// rows (sums, l, m, M) in the workspace, and a second kernel joins them.
+#include <cuda_fp16.h>
+
+#include "cache_attn.cuh"
+#include "trace.cuh"
+
+namespace dr {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kStage = 16 * kWarps;
+constexpr float kNegInf = -INFINITY;
+constexpr int kBias = 14;  // weights as 16-bit operands reach 2^14
+
+// ------------------------------------------------------------------ the line of stages
+// Stages of sequence b that its tokens see, tiles of rows, and their product with the heads.
+struct Seq {
+    int len, n;         // positions before the call's tokens, tokens (0: nothing to do)
+    int s0, stages;     // first stage, stages
+    int tiles;          // tiles of rows
+};
+template <int ROWS>
+__device__ __forceinline__ Seq make_seq(const AttnParams& p, int b) {
+    Seq s;
+    if (!cache_seq(p.c, b, s.len, s.n)) s.n = 0;
+    s.s0 = s.stages = s.tiles = 0;
+    if (s.n > 0) {
+        const int lo = p.window > 0 ? max(0, s.len - p.window + 1) : 0;
+        s.s0 = lo / kStage;
+        s.stages = (s.len + s.n + kStage - 1) / kStage - s.s0;
+        s.tiles = (s.n * p.G + ROWS - 1) / ROWS;
+    }
+    return s;
+}
+__device__ __forceinline__ long long work_of(const AttnParams& p, const Seq& s) {
+    return (long long)s.tiles * s.stages * p.c.H;
+}
+__device__ __forceinline__ long long warp_scan(long long x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    return x;
+}
+// The whole line (every lane gets it).
+template <int ROWS>
+__device__ __forceinline__ long long line_length(const AttnParams& p, int lane) {
+    long long total = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+        if (b0 + lane < p.c.B) total += work_of(p, make_seq<ROWS>(p, b0 + lane));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    return total;
+}
+// The sequence that holds place `at` of the line, and where its own stretch begins.
+template <int ROWS>
+__device__ __forceinline__ int find_seq(const AttnParams& p, int lane, long long at, long long& begin) {
+    long long before = 0;
+    for (int b0 = 0; b0 < p.c.B; b0 += 32) {
+        const long long x = b0 + lane < p.c.B ? work_of(p, make_seq<ROWS>(p, b0 + lane)) : 0;
+        const long long upto = before + warp_scan(x, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, upto > at);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            begin = __shfl_sync(0xffffffffu, upto - x, l);
+            return b0 + l;
+        }
+        before = __shfl_sync(0xffffffffu, upto, 31);
+    }
+    begin = before;
+    return p.c.B;
+}
+// Block i of n takes places share(i) .. share(i + 1) - 1 of the line.
+__device__ __forceinline__ long long share(long long total, int i, int n) { return total * i / n; }
+
+// ------------------------------------------------------------------ operands
+__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
+    return __byte_perm(a, b, sel);
+}
+// Two codes of `w` (bytes 0, 1 or 2, 3) as a pair of 16-bit floats.
+template <bool E4M3>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    if (E4M3) {
+        asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n"
+            " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    } else {
+        // x + 128 in the low bits of 1024 .. 2047, whose spacing is 1; minus 1152 is x exactly
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
+        uint32_t a = prmt(u, 0x64646464u, 0x4140), b = prmt(u, 0x64646464u, 0x4342);
+        const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off);
+        const __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+        lo = *reinterpret_cast<const uint32_t*>(&x);
+        hi = *reinterpret_cast<const uint32_t*>(&y);
+    }
+}
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                    uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half(uint32_t x) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&x));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 2^x for a whole x, the ends of the range standing for what is beyond them; 0 for -inf and NaN.
+__device__ __forceinline__ float pow2i(float x) {
+    if (!(x >= -126.f)) return 0.f;
+    return __uint_as_float((uint32_t)((int)fminf(x, 127.f) + 127) << 23);
+}
+
+// The codes of a warp's 16 positions.  Thread (g, c) = (lane / 4, lane % 4) holds of the keys
+// positions g and g + 8, channels 64 i + 16 c .. + 15; of the values positions 2c, 2c + 1, 2c + 8,
+// 2c + 9, channels g d/8 .. + d/8 - 1.
+template <int D>
+struct Codes {
+    uint32_t k[2][D / 16], v[4][D / 32];
+};
+template <int D>
+__device__ __forceinline__ void load_codes(Codes<D>& f, const uint8_t* kp, const uint8_t* vp, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(kp + (g + 8 * r) * D + 64 * i + 16 * c));
+            f.k[r][4 * i] = u.x; f.k[r][4 * i + 1] = u.y; f.k[r][4 * i + 2] = u.z; f.k[r][4 * i + 3] = u.w;
+        }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const uint8_t* at = vp + (2 * c + (r & 1) + 8 * (r >> 1)) * D + g * (D / 8);
+        if constexpr (D == 128) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(at));
+            f.v[r][0] = u.x; f.v[r][1] = u.y; f.v[r][2] = u.z; f.v[r][3] = u.w;
+        } else {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(at));
+            f.v[r][0] = u.x; f.v[r][1] = u.y;
+        }
+    }
+}
+
+// What a warp needs of its 16 positions of a stage: the page and its scales.  Lane i holds those
+// of step (batch * 32 + i).
+struct Meta {
+    int id;            // page, -1 where the entry is out of range, -2 where nothing is visible
+    float ks, vs, ve;  // scales; whole number with vs <= 2^ve
+};
+
+template <int D, int NT, bool PREC>
+struct Tile {
+    uint32_t q[NT][D / 16][2], ql[NT][PREC ? D / 16 : 1][2];  // Q^T as B operands
+    float qs[NT][2];       // factor of S for rows 2c, 2c + 1
+    int pos[NT][2];        // their positions (-1: no such row)
+    float o[NT][D / 16][4], l[NT][2], m[NT][2], M[NT][2];
+};
+
+__device__ __forceinline__ float load_q(const AttnParams& p, long long at) { return ld_any(p.q, at, p.io); }
+
+// The queries of rows row0 .. row0 + 8 NT - 1, each scaled by a power of two to largest magnitude
+// 2^9 .. 2^10, which keeps a bf16 value exact unless it is 2^-24 of the row's largest.
+template <int D, int NT, bool PREC>
+__device__ __forceinline__ void load_tile(Tile<D, NT, PREC>& t, const AttnParams& p, int b, int h, int row0,
+                                          const Seq& s, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int row = row0 + 8 * n + g;
+        const bool on = row < s.n * p.G;
+        const int tok = on ? row / p.G : 0, head = h * p.G + (on ? row % p.G : 0);
+        const long long at = ((long long)b * p.c.T + tok) * p.ld_q + (long long)head * D;
+        float x[D / 4], top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                x[16 * i + j] = on ? load_q(p, at + 64 * i + 16 * c + j) : 0.f;
+                top = fmaxf(top, fabsf(x[16 * i + j]));
+            }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        int e = 0;
+        if (top > 0.f && top < INFINITY) frexpf(top, &e), e -= 10;
+        const float up = ldexpf(1.f, -max(-100, min(100, e)));
+        const float rest = ldexpf(1.f, -e + max(-100, min(100, e)));
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+            for (int w = 0; w < 4; ++w)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float a = x[16 * i + 4 * w + 2 * r] * up * rest;
+                    const float d = x[16 * i + 4 * w + 2 * r + 1] * up * rest;
+                    const uint32_t hi = pack_half(a, d);
+                    t.q[n][4 * i + w][r] = hi;
+                    if constexpr (PREC) {
+                        const float2 f = unpack_half(hi);
+                        // an infinity or NaN stays in the first term
+                        t.ql[n][4 * i + w][r] = pack_half(isfinite(f.x) ? a - f.x : 0.f,
+                                                          isfinite(f.y) ? d - f.y : 0.f);
+                    }
+                }
+        // factors and positions belong to rows 2c, 2c + 1: held by the lanes with g = 2c, 2c + 1
+        const float f = ldexpf(p.scale * 1.44269504088896340736f, e);
+        const int ps = on ? s.len + tok : -1;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            t.qs[n][j] = __shfl_sync(0xffffffffu, f, (2 * c + j) * 4);
+            t.pos[n][j] = __shfl_sync(0xffffffffu, ps, (2 * c + j) * 4);
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) { t.l[n][j] = 0.f; t.m[n][j] = t.M[n][j] = kNegInf; }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) t.o[n][j][i] = 0.f;
+    }
+}
+
+// One step: 16 positions from `first` on.
+template <int D, int NT, bool E4M3, bool PREC>
+__device__ __forceinline__ void step(Tile<D, NT, PREC>& t, Codes<D>& f, const AttnParams& p, const Seq& s,
+                                     int first, float ks, float vs, float ve, bool edge, int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    float sc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        uint32_t a0, a1, a2, a3;
+        codes_to_half<E4M3>(f.k[0][j], a0, a2);
+        codes_to_half<E4M3>(f.k[1][j], a1, a3);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            mma(sc[n], a0, a1, a2, a3, t.q[n][j][0], t.q[n][j][1]);
+            if constexpr (PREC) mma(sc[n], a0, a1, a2, a3, t.ql[n][j][0], t.ql[n][j][1]);
+        }
+    }
+    if (edge) {
+        // codes behind the last position may be anything: as values they count as zero
+        const int end = s.len + s.n;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (first + 2 * c + (r & 1) + 8 * (r >> 1) >= end) {
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) f.v[r][i] = 0;
+            }
+    }
+    uint32_t pb[NT][2], pl[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float top[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float k = t.qs[n][j] * ks;
+            sc[n][j] *= k;
+            sc[n][2 + j] *= k;
+            if (edge) {
+                const int back0 = t.pos[n][j] - (first + g), back1 = back0 - 8;
+                if (back0 < 0 || (p.window > 0 && back0 >= p.window)) sc[n][j] = kNegInf;
+                if (back1 < 0 || (p.window > 0 && back1 >= p.window)) sc[n][2 + j] = kNegInf;
+            }
+            top[j] = fmaxf(sc[n][j], sc[n][2 + j]);
+        }
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
+            top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
+        }
+        float mref[2], fac[2], oscale[2];
+        bool grew = false;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float up = ceilf(top[j]);
+            const float m = fmaxf(t.m[n][j], up), M = fmaxf(t.M[n][j], up + ve);
+            grew |= M > t.M[n][j];
+            t.l[n][j] *= pow2i(t.m[n][j] - m);
+            oscale[j] = pow2i(t.M[n][j] - M);
+            t.m[n][j] = m;
+            t.M[n][j] = M;
+            mref[j] = m == kNegInf ? 0.f : m;
+            // held inside the range of fp32 where a far larger value scale is past
+            fac[j] = vs * pow2i(fminf(m - M + kBias, 126.f));
+        }
+        if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                t.o[n][i][0] *= oscale[0];
+                t.o[n][i][1] *= oscale[1];
+                t.o[n][i][2] *= oscale[0];
+                t.o[n][i][3] *= oscale[1];
+            }
+        }
+        float w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float e = ex2(sc[n][i] - mref[i & 1]);
+            t.l[n][i & 1] += e;
+            // a hidden position weighs nothing even where the page's value scale is NaN
+            w[i] = sc[n][i] == kNegInf ? 0.f : e * fac[i & 1];
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t hi = pack_half(w[2 * r], w[2 * r + 1]);
+            pb[n][r] = transpose8x8(hi);
+            if constexpr (PREC) {
+                const float2 x = unpack_half(hi);
+                pl[n][r] = transpose8x8(pack_half(w[2 * r] - x.x, w[2 * r + 1] - x.y));
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+        uint32_t a[2][4];  // channels 4j, 4j + 1 and 4j + 2, 4j + 3 of the thread's D / 8
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const uint32_t x = f.v[2 * r][j], y = f.v[2 * r + 1][j];
+            codes_to_half<E4M3>(prmt(x, y, 0x5140), a[0][2 * r], a[0][2 * r + 1]);
+            codes_to_half<E4M3>(prmt(x, y, 0x7362), a[1][2 * r], a[1][2 * r + 1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma(t.o[n][2 * j + i], a[i][0], a[i][1], a[i][2], a[i][3], pb[n][0], pb[n][1]);
+                if constexpr (PREC)
+                    mma(t.o[n][2 * j + i], a[i][0], a[i][1], a[i][2], a[i][3], pl[n][0], pl[n][1]);
+            }
+    }
+}
+
+// ------------------------------------------------------------------ rows that leave a block
+// Part of the workspace of block i: two unfinished tiles, each [rows][d] sums, then [rows] of l, m, M.
+__host__ __device__ constexpr size_t tile_floats(int d, int rows) { return (size_t)rows * (d + 3); }
+
+__device__ __forceinline__ void write_row(const AttnParams& p, int b, int h, int row, int ch, int d, float sum,
+                                          float l, float m, float M) {
+    const int tok = row / p.G, head = h * p.G + row % p.G;
+    const size_t at = ((size_t)b * p.c.T + tok) * p.Hq + head;
+    // sums are in units of 2^(M - 14), l in units of 2^m
+    float f = M - m - kBias;
+    float y = sum / l;
+    if (f > 100.f || f < -100.f) { y = ldexpf(y, (int)fminf(fmaxf(f, -400.f), 400.f)); }
+    else y *= pow2i(f);
+    if (M == kNegInf && sum == 0.f) y = l == l ? 0.f : sum / l;  // every value scale is zero
+    st_any(p.o, at * d + ch, p.out, y);
+    if (ch == 0 && p.lse) p.lse[at] = (m + log2f(l)) * 0.69314718055994530942f;
+}
+
+template <int D, int NT, bool E4M3, bool PREC>
+__global__ void __launch_bounds__(kThreads) cache_attn_kernel(const AttnParams p) {
+    constexpr int ROWS = 8 * NT;
+    __shared__ float so[kWarps][ROWS][D + 4];
+    __shared__ float sl[kWarps][ROWS], sm[kWarps][ROWS], sM[kWarps][ROWS];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+
+    const long long total = line_length<ROWS>(p, lane);
+    const long long begin = share(total, blockIdx.x, gridDim.x);
+    const long long end = share(total, blockIdx.x + 1, gridDim.x);
+    if (begin >= end) return;
+    long long at = begin, seq_begin;
+    int b = find_seq<ROWS>(p, lane, at, seq_begin);
+    while (at < end) {
+        Seq s = make_seq<ROWS>(p, b);
+        while (work_of(p, s) == 0 || at >= seq_begin + work_of(p, s)) {
+            seq_begin += work_of(p, s);
+            if (++b >= p.c.B) return;
+            s = make_seq<ROWS>(p, b);
+        }
+        // stretches of one sequence: head by head, tile by tile, stage by stage
+        const long long in = at - seq_begin;
+        const int unit = (int)(in / s.stages), from = (int)(in % s.stages);
+        const int h = unit / s.tiles, row0 = (unit % s.tiles) * ROWS;
+        const int upto = (int)min((long long)s.stages, from + (end - at));
+        Tile<D, NT, PREC> t;
+        load_tile(t, p, b, h, row0, s, lane);
+        // positions that the tile's rows see
+        const int t0 = row0 / p.G, t1 = min(s.n - 1, (row0 + ROWS - 1) / p.G);
+        const int hi = s.len + t1 + 1, lo = p.window > 0 ? max(0, s.len + t0 - p.window + 1) : 0;
+        // positions that every row sees need no mask
+        const int all_hi = s.len + t0 + 1, all_lo = p.window > 0 ? max(0, s.len + t1 - p.window + 1) : 0;
+
+        const uint8_t* kbase = p.c.k;
+        const uint8_t* vbase = p.c.v;
+        auto meta = [&](int st) {
+            Meta x;
+            x.id = -2;
+            x.ks = x.vs = 0.f;
+            x.ve = kNegInf;
+            const int first = (s.s0 + st) * kStage + 16 * warp;
+            if (st < upto && first < hi && first + 16 > lo) {
+                x.id = cache_page(p.c, b, first / p.c.page);
+                if (x.id >= 0) {
+                    const size_t ph = (size_t)x.id * p.c.H + h;
+                    x.ks = p.c.k_scale[ph];
+                    x.vs = p.c.v_scale[ph];
+                    int e;
+                    frexpf(x.vs, &e);
+                    x.ve = x.vs > 0.f ? (float)e : x.vs == 0.f ? kNegInf : 0.f;
+                } else {
+                    flag_index_error(p.c);
+                    x.ks = x.vs = __uint_as_float(0x7fc00000u);
+                    x.ve = 0.f;
+                }
+            }
+            return x;
+        };
+        Meta now = meta(from + lane), next = meta(from + 32 + lane);
+        Codes<D> f[2];
+        auto fetch = [&](Codes<D>& x, int st) {
+            const int k = st - from;
+            const int id = __shfl_sync(0xffffffffu, k & 32 ? next.id : now.id, k & 31);
+            if (id >= 0) {
+                const int first = (s.s0 + st) * kStage + 16 * warp;
+                const size_t off = (((size_t)id * p.c.H + h) * p.c.page + first % p.c.page) * D;
+                load_codes<D>(x, kbase + off, vbase + off, lane);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) x.k[r][i] = 0;
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) x.v[r][i] = 0;
+            }
+        };
+        // st - from runs through batches of 32 steps: bit 5 tells in which of two the step's meta is
+        auto consume = [&](Codes<D>& x, int st) {
+            const int k = st - from;
+            const bool second = k & 32;
+            const int id = __shfl_sync(0xffffffffu, second ? next.id : now.id, k & 31);
+            const float ks = __shfl_sync(0xffffffffu, second ? next.ks : now.ks, k & 31);
+            const float vs = __shfl_sync(0xffffffffu, second ? next.vs : now.vs, k & 31);
+            const float ve = __shfl_sync(0xffffffffu, second ? next.ve : now.ve, k & 31);
+            if (id != -2) {
+                const int first = (s.s0 + st) * kStage + 16 * warp;
+                const bool edge = first + 16 > all_hi || first < all_lo;
+                step<D, NT, E4M3, PREC>(t, x, p, s, first, ks, vs, ve, edge, lane);
+            }
+            if ((k & 31) == 31) {  // the batch is used up: the one after next takes its place
+                const Meta m2 = meta(from + (k | 31) + 1 + 32 + lane);
+                if (second) next = m2; else now = m2;
+            }
+        };
+        fetch(f[0], from);
+        for (int st = from; st < upto; st += 2) {
+            if (st + 1 < upto) fetch(f[1], st + 1);
+            consume(f[0], st);
+            if (st + 1 < upto) {
+                if (st + 2 < upto) fetch(f[0], st + 2);
+                consume(f[1], st + 1);
+            }
+        }
+
+        // join the warps: rows 2c, 2c + 1 of each 8, channels g d/8 ..
+        __syncthreads();  // the arrays are free again
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float l = t.l[n][j];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                const int row = 8 * n + 2 * c + j;
+                if (g == 0) { sl[warp][row] = l; sm[warp][row] = t.m[n][j]; sM[warp][row] = t.M[n][j]; }
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    so[warp][row][g * (D / 8) + 2 * i] = t.o[n][i][j];
+                    so[warp][row][g * (D / 8) + 2 * i + 1] = t.o[n][i][2 + j];
+                }
+            }
+        __syncthreads();
+        const bool whole = from == 0 && upto == s.stages;
+        float* out = p.part + ((size_t)blockIdx.x * 2 + (at == begin ? 0 : 1)) * tile_floats(D, ROWS);
+        for (int i = threadIdx.x; i < ROWS * D; i += kThreads) {
+            const int r = i / D, ch = i % D, row = row0 + r;
+            float m = kNegInf, M = kNegInf, l = 0.f, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) { m = fmaxf(m, sm[w][r]); M = fmaxf(M, sM[w][r]); }
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                // a warp without weight adds nothing, one that met a NaN hands it on
+                l += sl[w][r] * (sl[w][r] == sl[w][r] ? pow2i(sm[w][r] - m) : 1.f);
+                sum += so[w][r][ch] * (so[w][r][ch] == so[w][r][ch] ? pow2i(sM[w][r] - M) : 1.f);
+            }
+            if (whole) {
+                if (row < s.n * p.G) write_row(p, b, h, row, ch, D, sum, l, m, M);
+            } else {
+                out[(size_t)r * D + ch] = sum;
+                if (ch == 0) {
+                    out[ROWS * D + r] = l;
+                    out[ROWS * D + ROWS + r] = m;
+                    out[ROWS * D + 2 * ROWS + r] = M;
+                }
+            }
+        }
+        at += upto - from;
+    }
+}
+
+// Joins the parts of a tile that several blocks worked on.  Block x: the tile; y: 8 of its rows.
+// Rows of no query get zeros (behind a sequence's tokens) or NaN (a sequence out of range).
+template <int D, int NT>
+__global__ void __launch_bounds__(D) cache_attn_join_kernel(const AttnParams p, int blocks, int max_tiles) {
+    constexpr int ROWS = 8 * NT;
+    const int lane = threadIdx.x & 31, ch = threadIdx.x;
+    const int b = blockIdx.x / (p.c.H * max_tiles), rest = blockIdx.x % (p.c.H * max_tiles);
+    const int h = rest / max_tiles, tile = rest % max_tiles;
+    const Seq s = make_seq<ROWS>(p, b);
+    int len, n;
+    const bool ok = cache_seq(p.c, b, len, n);
+    if (!ok && threadIdx.x == 0) flag_index_error(p.c);
+    const int row0 = tile * ROWS + blockIdx.y * 8, rows = min(8, p.c.T * p.G - row0);
+    for (int r = max(0, s.n * p.G - row0); r < rows; ++r) {
+        const int tok = (row0 + r) / p.G, head = h * p.G + (row0 + r) % p.G;
+        const size_t at = ((size_t)b * p.c.T + tok) * p.Hq + head;
+        st_any(p.o, at * D + ch, p.out, ok ? 0.f : __uint_as_float(0x7fc00000u));
+        if (ch == 0 && p.lse) p.lse[at] = ok ? kNegInf : __uint_as_float(0x7fc00000u);
+    }
+    if (row0 >= s.n * p.G) return;
+    const long long total = line_length<ROWS>(p, lane);
+    long long before = 0;  // the line up to this sequence
+    for (int b0 = 0; b0 < b; b0 += 32)
+        if (b0 + lane < b) before += work_of(p, make_seq<ROWS>(p, b0 + lane));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    const long long a = before + ((long long)h * s.tiles + tile) * s.stages, e = a + s.stages;
+    // the blocks whose shares meet a .. e - 1
+    int first = (int)(a * blocks / total);
+    while (first > 0 && share(total, first, blocks) > a) --first;
+    while (share(total, first + 1, blocks) <= a) ++first;
+    int last = first;
+    while (share(total, last + 1, blocks) < e) ++last;
+    if (first == last) return;  // finished by its block
+    for (int r = blockIdx.y * 8; r < blockIdx.y * 8 + 8; ++r) {
+        const int row = tile * ROWS + r;
+        if (row >= s.n * p.G) return;
+        float m = kNegInf, M = kNegInf, l = 0.f, sum = 0.f;
+        for (int i = first; i <= last; ++i) {
+            if (share(total, i, blocks) == share(total, i + 1, blocks)) continue;
+            // a block that began before the tile holds it as its second part
+            const float* in = p.part + ((size_t)i * 2 + (share(total, i, blocks) >= a ? 0 : 1)) * tile_floats(D, ROWS);
+            const float pl = in[ROWS * D + r], pm = in[ROWS * D + ROWS + r], pM = in[ROWS * D + 2 * ROWS + r];
+            const float ps = in[(size_t)r * D + ch];
+            const float m2 = fmaxf(m, pm), M2 = fmaxf(M, pM);
+            l = (l == l ? l * pow2i(m - m2) : l) + (pl == pl ? pl * pow2i(pm - m2) : pl);
+            sum = (sum == sum ? sum * pow2i(M - M2) : sum) + (ps == ps ? ps * pow2i(pM - M2) : ps);
+            m = m2;
+            M = M2;
+        }
+        write_row(p, b, h, row, ch, D, sum, l, m, M);
+    }
+}
+
+template <typename K>
+int resident_blocks(K kernel) {
+    int sms = 0, per = 0, dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, 0) != cudaSuccess) return 0;
+    return sms * per;
+}
+
+constexpr int kMaxBlocks = 152 * 8;
+
+template <int D, int NT, bool E4M3, bool PREC>
+cudaError_t launch(const AttnParams& p, cudaStream_t st) {
+    static const int resident = resident_blocks(cache_attn_kernel<D, NT, E4M3, PREC>);
+    if (resident <= 0) return cudaErrorUnknown;
+    const int blocks = resident < kMaxBlocks ? resident : kMaxBlocks;
+    {
+        TraceScope ts("cache_attn", st);
+        cache_attn_kernel<D, NT, E4M3, PREC><<<blocks, kThreads, 0, st>>>(p);
+        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    }
+    const int max_tiles = (p.c.T * p.G + 8 * NT - 1) / (8 * NT);
+    TraceScope ts("cache_attn_join", st);
+    cache_attn_join_kernel<D, NT><<<dim3((unsigned)p.c.B * p.c.H * max_tiles, NT), D, 0, st>>>(p, blocks, max_tiles);
+    return cudaGetLastError();
+}
+
+// Rows of a tile: 16 halve the reads of the cache where a sequence and head have more than 8.  The
+// split operands of 16 rows do not fit the registers, there the tiles stay at 8.
+template <int D, bool E4M3>
+cudaError_t by_rows(const AttnParams& p, cudaStream_t st) {
+    if (p.io == DR_F32 || p.out == DR_F32) return launch<D, 1, E4M3, true>(p, st);
+    return p.c.T * p.G > 8 ? launch<D, 2, E4M3, false>(p, st) : launch<D, 1, E4M3, false>(p, st);
+}
+
+}  // namespace
+
+size_t cache_attn_part_bytes(int d) {
+    return (size_t)kMaxBlocks * 2 * tile_floats(d, 16) * sizeof(float);
+}
+
+cudaError_t cache_attn(const AttnParams& p, cudaStream_t st) {
+    if (p.c.B == 0 || p.c.T == 0) return cudaSuccess;
+    if (p.c.code == DR_CODE_E4M3) return p.c.d == 128 ? by_rows<128, true>(p, st) : by_rows<64, true>(p, st);
+    return p.c.d == 128 ? by_rows<128, false>(p, st) : by_rows<64, false>(p, st);
+}
+
+}  // namespace dr

@@ -13,6 +13,8 @@ namespace dr {
 // Device-side error word (first 4 bytes of the workspace): nonzero after a
 // bounded wait ran out.
 constexpr int kErrTimeout = 1;
+// Status word of a cache (dr_cache.status): a page number, length or count out of range.
+constexpr int kErrIndex = 2;
 // Bound on any single wait of a kernel on its own asynchronous copies / MMAs.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s
 

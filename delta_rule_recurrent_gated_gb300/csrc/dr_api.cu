@@ -138,6 +138,8 @@ const char* dr_error_string(int code) {
         case DR_ERR_SCRATCH_LIMIT:
             return "DR_ERR_SCRATCH_LIMIT: problem larger than the library's static scratch "
                    "(dr_fwd_noalloc)";
+        case DR_ERR_INDEX:
+            return "DR_ERR_INDEX: a page number, length or count outside its range";
         default: return "unknown dr status code";
     }
 }
@@ -462,7 +464,7 @@ int dr_check_status(const void* ws, void* stream) {
     if (cudaMemcpyAsync(&word, ws, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess)
         return DR_ERR_CUDA;
     if (cudaStreamSynchronize(st) != cudaSuccess) return DR_ERR_CUDA;
-    return word == 0 ? DR_OK : DR_ERR_TIMEOUT;
+    return word == 0 ? DR_OK : word == dr::kErrIndex ? DR_ERR_INDEX : DR_ERR_TIMEOUT;
 }
 
 }  // extern "C"

@@ -61,7 +61,8 @@ enum dr_status_code {
     DR_ERR_ALIGNMENT = 4,     /* a pointer is not 16-byte aligned                    */
     DR_ERR_CUDA = 5,          /* a CUDA call or launch failed                        */
     DR_ERR_TIMEOUT = 6,       /* a bounded device-side wait ran out                  */
-    DR_ERR_SCRATCH_LIMIT = 7  /* dr_fwd_noalloc: problem larger than its static scratch */
+    DR_ERR_SCRATCH_LIMIT = 7, /* dr_fwd_noalloc: problem larger than its static scratch */
+    DR_ERR_INDEX = 8          /* a kernel met a page number or length outside its range  */
 };
 
 enum dr_variant { DR_DELTANET = 0, DR_GDN = 1, DR_KDA = 2, DR_GDN2 = 3 /* dr_gdn2_* only */ };
@@ -286,6 +287,142 @@ int dr_gdn2_decode(const dr_desc* desc, const void* q, const void* k, const void
                    void* o, void* stream);
 
 /*
+ * The softmax-attention layer of a hybrid stack (page "Un Analisis Sistematico de la
+ * Atencion Lineal Hibrida": a few softmax-attention layers among the delta-rule ones):
+ * the norm and position rotation of its queries and keys, the paged 8-bit cache of its
+ * keys and values, and the attention over that cache.  The pages name the layer only; the
+ * equations are the standard ones, stated at each entry point.
+ *
+ * Norm of queries and keys for each head, with the position rotation in the same pass.
+ * For every token (b, t), head and channel c < d:
+ *   r = 1 / sqrt(mean_c x_c^2 + eps);  n_c = x_c r w_c   (w NULL: all ones)
+ *   y = n with every pair (n_i, n_j) of its first `rot` channels turned by the angle of the
+ *   token's position p:  y_i = n_i cos - n_j sin,  y_j = n_j cos + n_i sin,  angle index a:
+ *   DR_ROPE_HALVES (i, j) = (a, a + rot/2);  DR_ROPE_PAIRS (i, j) = (2a, 2a + 1);  a < rot/2.
+ *   p = (positions ? positions[b*T + t] : t) + (start ? start[b] : 0);  cos_table[p][a],
+ *   sin_table[p][a]: [table_rows][rot/2] fp32.  A token whose position lies outside the
+ *   table gets NaN outputs (and NaN gradients); nothing outside the table is read.
+ * The norm runs whether or not channels are rotated (rot = 0: cos_table, sin_table NULL).
+ * q: [B*T] rows of Hq*d values, ld_q elements from one row to the next (>= Hq*d: q and k
+ *   may be column ranges of one packed projection), k: the same with Hk heads (Hk = 0: no
+ *   keys); io dtype.  yq, yk: rows ld_oq, ld_ok elements apart, out dtype.  A y may be its x.
+ * dr_norm_rope_bwd: with dyq, dyk (contiguous [B, T, H, d], io dtype) the gradients
+ *   dq, dk (grad dtype, rows ld_oq, ld_ok apart) and dwq, dwk ([d] fp32, summed over all
+ *   tokens and heads in a fixed order; NULL where the weight is NULL or not wanted).
+ *   Workspace: dr_norm_rope_workspace_bytes (0 when desc is invalid).
+ * Supported: d a multiple of 8 up to 256; rot a multiple of 16 up to d; io bf16 or fp32;
+ *   any B, T >= 0.  Row distances are multiples of 16 bytes.  fp32 arithmetic, one rounding
+ *   at the output.  Errors as dr_fwd.
+ */
+enum dr_rope_style { DR_ROPE_HALVES = 0, DR_ROPE_PAIRS = 1 };
+
+typedef struct dr_rope_desc {
+    int B, T, Hq, Hk, d;
+    int rot;                      /* rotated channels, 0 .. d                          */
+    int style;                    /* enum dr_rope_style                                */
+    int io_dtype, out_dtype, grad_dtype;
+    int table_rows;               /* rows of cos_table and sin_table                   */
+    float eps;
+    long long ld_q, ld_k;         /* elements between token rows of q, k               */
+    long long ld_oq, ld_ok;       /* of yq, yk (forward), dq, dk (backward)            */
+} dr_rope_desc;
+
+int dr_norm_rope_fwd(const dr_rope_desc* desc, const void* q, const void* k, const float* wq,
+                     const float* wk, const float* cos_table, const float* sin_table,
+                     const int32_t* positions, const int32_t* start, void* yq, void* yk,
+                     void* stream);
+size_t dr_norm_rope_workspace_bytes(const dr_rope_desc* desc);
+int dr_norm_rope_bwd(const dr_rope_desc* desc, const void* q, const void* k, const float* wq,
+                     const float* wk, const float* cos_table, const float* sin_table,
+                     const int32_t* positions, const int32_t* start, const void* dyq,
+                     const void* dyk, void* dq, void* dk, float* dwq, float* dwk,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * A paged cache of keys and values in 8 bits with one fp32 scale for each page and head.
+ * A page holds `page` consecutive positions of one sequence; value = code * scale.
+ *   codes  k, v:              [num_pages][H][page][d], one byte each
+ *   scales k_scale, v_scale:  [num_pages][H], >= 0 (NaN: the page holds a value that was not
+ *                             finite, and reads as NaN)
+ *   DR_CODE_I8: two's complement, -127 .. 127 (Q = 127); DR_CODE_E4M3: 8-bit floating point,
+ *   4 exponent and 3 fraction bits, no infinities (Q = 448).
+ *   status: one device int32 the caller sets to zero, or NULL.  A kernel that meets a page
+ *   number outside 0 .. num_pages-1, a negative length, a count outside 0 .. T or a position
+ *   past the table's row records it there (dr_check_status: DR_ERR_INDEX; it stays until the
+ *   caller clears it) and touches nothing through it.
+ * dr_cache_seqs names the positions of one call: position p of sequence b is row p % page of
+ *   page page_table[b * table_stride + p / page]; the call's tokens t < n_b of sequence b
+ *   (n_b = counts ? counts[b] : T, at most T) are the positions lens[b] + t.  Only table
+ *   entries of pages that hold such positions (attention: or earlier, visible ones) are read.
+ * Supported: d 64 or 128; page 16, 32, 64 or 128; any H >= 1, B, T >= 0.
+ *
+ * dr_cache_write appends the tokens k, v ([B*T] rows of H*d, ld_k / ld_v elements apart, io
+ * dtype).  For each page and head it touches, with s_old the page's scale if the page holds
+ * earlier positions of the sequence and 0 otherwise (what a page held before is forgotten
+ * when its first position is written):
+ *   s = max(s_old, max |x| * fl(1/Q)) over the new values;  NaN when one is not finite
+ *   new codes: x / s, rounded to the nearest code, ties to even (0 where s = 0 or NaN)
+ *   where s > s_old > 0: the earlier codes c become c s_old / s, rounded the same way
+ * (fp32 arithmetic throughout).  A page that is written must belong to one sequence.
+ * dr_cache_read writes the values at the call's tokens to k, v ([B, T, H, d] contiguous, out
+ * dtype, each rounded once; either may be NULL), zeros for t >= n_b, NaN where an index is
+ * out of range.
+ */
+enum dr_code { DR_CODE_I8 = 0, DR_CODE_E4M3 = 1 };
+
+typedef struct dr_cache {
+    int num_pages, H, d, page;
+    int code;                     /* enum dr_code */
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int32_t* status;
+} dr_cache;
+
+typedef struct dr_cache_seqs {
+    int B, T;
+    const int32_t* page_table;    /* device [B][table_stride]                          */
+    int table_stride;             /* pages that a sequence can have                    */
+    const int32_t* lens;          /* device [B]: positions before the call's tokens    */
+    const int32_t* counts;        /* device [B]: the call's tokens, or NULL (T each)   */
+} dr_cache_seqs;
+
+int dr_cache_write(const dr_cache* cache, const dr_cache_seqs* seqs, const void* k, long long ld_k,
+                   const void* v, long long ld_v, int io_dtype, void* stream);
+int dr_cache_read(const dr_cache* cache, const dr_cache_seqs* seqs, void* k, void* v, int out_dtype,
+                  void* stream);
+
+/*
+ * Attention of the call's tokens over the cache (which already holds them): token t < n_b of
+ * sequence b is the query at position p = lens[b] + t and sees the positions j <= p, and
+ * with window > 0 only j > p - window.  Query head h reads cache head h / (Hq / H).
+ *   s_j = scale * sum_c q_c k_jc;  o = sum_j e^{s_j} v_j / sum_j e^{s_j};
+ *   lse = ln sum_j e^{s_j}
+ * Tokens t >= n_b: o = 0, lse = -inf.  Where a sequence's length, count or a page number that
+ * a token needs is out of range, its o and lse are NaN.
+ * q: [B*T] rows of Hq*d, ld_q elements apart (io dtype); o [B, T, Hq, d] (out dtype); lse
+ *   [B, T, Hq] fp32 or NULL.
+ * Arithmetic: 16-bit floating-point operands that hold the codes and bf16 queries exactly and
+ *   the weights (softmax weight times value scale) to 11 bits, or to 2^-37 of the row's
+ *   largest weight where that is more (22 bits for queries and weights when io or out is fp32);
+ *   fp32 accumulation, fp32 softmax statistics.
+ * Workspace: dr_cache_attn_workspace_bytes, the same for every length (0 when desc is invalid
+ *   or unsupported; needs the device current that will run the call).  Results of one call do
+ *   not depend on what it held.  Hq must be a multiple of the cache's H.  Errors as dr_fwd.
+ */
+typedef struct dr_attn_desc {
+    int Hq;
+    int io_dtype, out_dtype;
+    int window;                   /* 0: none                                           */
+    float scale;
+    long long ld_q;
+} dr_attn_desc;
+
+size_t dr_cache_attn_workspace_bytes(const dr_cache* cache, const dr_attn_desc* desc, int B, int T);
+int dr_cache_attn(const dr_cache* cache, const dr_cache_seqs* seqs, const dr_attn_desc* desc,
+                  const void* q, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                  void* stream);
+
+/*
  * Self-test of the device failure path (no counterpart on the pages).  Launches one
  * warp that waits, with the bounded wait every tensor-core kernel uses, on an mbarrier
  * phase that only completes when `arrive` is non-zero (the warp completes it itself);
@@ -301,7 +438,8 @@ int dr_selftest_wait(void* workspace, int arrive, long long limit_ns, void* stre
 
 /* Synchronise `stream` and report any device-side error recorded in the
    workspace by the last call that used it (DR_OK or DR_ERR_TIMEOUT), or
-   DR_ERR_CUDA when the stream itself failed. */
+   DR_ERR_CUDA when the stream itself failed.  The same call reads the status word of a
+   dr_cache (pass its address): DR_OK, DR_ERR_INDEX or DR_ERR_TIMEOUT. */
 int dr_check_status(const void* workspace, void* stream);
 
 /*
