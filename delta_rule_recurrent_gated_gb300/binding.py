@@ -432,26 +432,25 @@ class Gdn2Problem(Problem):
 
 
 # ------------------------------------------------------------------ softmax-attention layer
-def _rows(t, heads, d, what):
-    """Elements between the token rows of t [B, T, heads, d]: contiguous, or a range of heads of a
-    wider contiguous tensor."""
-    B, T, H, D = t.shape
-    if B * T == 0 and (H, D) == (heads, d):
-        return H * D
-    ld = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else H * D)
-    ok = (H, D) == (heads, d) and (D == 1 or t.stride(3) == 1) and (H == 1 or t.stride(2) == D) \
-        and (T == 1 or B == 1 or t.stride(0) == T * ld)
-    if not ok:
-        raise ValueError(f"{what}: shape {tuple(t.shape)} strides {t.stride()} is no [B, T, {heads}, {d}] "
-                         "with whole token rows at one distance")
-    return ld
+# A step of a serving loop makes these calls for a few microseconds of work on the device, so the
+# argument checks compare whole shapes and ask for strides only where a tensor is not contiguous.
+def _rows(t, shape, what):
+    """Elements between the token rows of t, a tensor of the given shape [B, T, heads, d]:
+    contiguous, or a range of heads of a wider contiguous tensor."""
+    if t.shape == shape:
+        B, T, H, D = shape
+        if t.is_contiguous():
+            return H * D
+        s = t.stride()
+        ld = s[1] if T > 1 else s[0]
+        if (D == 1 or s[3] == 1) and (H == 1 or s[2] == D) and (T == 1 or B == 1 or s[0] == T * ld):
+            return ld if B * T > 1 else H * D
+    raise ValueError(f"{what}: shape {tuple(t.shape)} strides {t.stride()} is no {tuple(shape)} with whole "
+                     "token rows at one distance")
 
 
-def _expect(t, dtype, shape, what, device=None):
-    import torch  # noqa: F401
-    if t is None:
-        return
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+def _expect(t, dtype, shape, what):
+    if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
         raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got "
                          f"{t.dtype} {tuple(t.shape)}")
 
@@ -465,7 +464,23 @@ def _torch_type(name):
     return getattr(torch, _TORCH_TYPES[name])
 
 
-class HeadNormRope:
+class _Calls:
+    """The device of a plan, its current stream and its allocations."""
+
+    def _at(self, device):
+        import torch
+        self.device = torch.device(device)
+        self._torch = torch
+        self._lib = load()
+
+    def _stream(self):
+        return self._torch.cuda.current_stream(self.device).cuda_stream
+
+    def _empty(self, shape, dtype):
+        return self._torch.empty(shape, dtype=dtype, device=self.device)
+
+
+class HeadNormRope(_Calls):
     """RMS norm of queries and keys for each head with the position rotation in the same pass
     (dr_norm_rope_fwd / dr_norm_rope_bwd) for one problem shape.
 
@@ -475,8 +490,7 @@ class HeadNormRope:
 
     def __init__(self, B, T, Hq, Hk, d, rot=None, style="halves", io="bf16", out="bf16", grad="bf16",
                  eps=1e-6, device="cuda"):
-        import torch
-        self.device = torch.device(device)
+        self._at(device)
         e = DrRopeDesc()
         e.B, e.T, e.Hq, e.Hk, e.d = B, T, Hq, Hk, d
         e.rot = d if rot is None else rot
@@ -486,76 +500,72 @@ class HeadNormRope:
         e.ld_q = e.ld_oq = Hq * d
         e.ld_k = e.ld_ok = Hk * d
         e.table_rows = 0
-        self.desc = e
+        self.desc, self._ref = e, ctypes.byref(e)
         self.io_dtype, self.out_dtype, self.grad_dtype = map(_torch_type, (io, out, grad))
+        self._q, self._k, self._rot = (B, T, Hq, d), (B, T, Hk, d), e.rot
         self.ws = None
-        if int(load().dr_norm_rope_workspace_bytes(ctypes.byref(e))) == 0:
+        if int(self._lib.dr_norm_rope_workspace_bytes(self._ref)) == 0:
             raise DrError(DR_ERR_UNSUPPORTED, "dr_norm_rope_workspace_bytes")
 
-    def _fill(self, q, k, wq, wk, cos, sin, positions, start, oq, ok):
-        import torch
-        e = self.desc
-        for t, H, what in ((q, e.Hq, "q"), (k, e.Hk, "k")):
-            if t is not None and (t.dtype != self.io_dtype or tuple(t.shape[:2]) != (e.B, e.T)):
-                raise ValueError(f"{what}: expected {self.io_dtype} [{e.B}, {e.T}, {H}, {e.d}]")
-        e.ld_q, e.ld_oq = (_rows(q, e.Hq, e.d, "q"), _rows(oq, e.Hq, e.d, "output of q")) if e.Hq else (0, 0)
-        e.ld_k, e.ld_ok = (_rows(k, e.Hk, e.d, "k"), _rows(ok, e.Hk, e.d, "output of k")) if e.Hk else (0, 0)
-        for w, what in ((wq, "wq"), (wk, "wk")):
-            _expect(w, torch.float32, (e.d,), what)
-        if e.rot:
-            e.table_rows = cos.shape[0]
-            _expect(cos, torch.float32, (e.table_rows, e.rot // 2), "cos")
-            _expect(sin, torch.float32, (e.table_rows, e.rot // 2), "sin")
-        _expect(positions, torch.int32, (e.B, e.T), "positions")
-        _expect(start, torch.int32, (e.B,), "start")
-
-    def _stream(self):
-        import torch
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def _empty(self, H, dtype):
-        import torch
-        return torch.empty(self.desc.B, self.desc.T, H, self.desc.d, dtype=dtype, device=self.device)
+    def _fill(self, q, k, wq, wk, cos, sin, positions, start, oq, ok, out_dtype):
+        """Checks the tensors of a call and notes their row distances in the descriptor."""
+        torch, e = self._torch, self.desc
+        f32, i32 = torch.float32, torch.int32
+        for t, o, shape, what in ((q, oq, self._q, "q"), (k, ok, self._k, "k")):
+            if shape[2] == 0:
+                continue
+            if t.dtype is not self.io_dtype or o.dtype is not out_dtype:
+                raise ValueError(f"{what}: expected {self.io_dtype} and an output of {out_dtype}, got {t.dtype} "
+                                 f"and {o.dtype}")
+            ld, ldo = _rows(t, shape, what), _rows(o, shape, "output of " + what)
+            if what == "q":
+                e.ld_q, e.ld_oq = ld, ldo
+            else:
+                e.ld_k, e.ld_ok = ld, ldo
+        w = (e.d,)
+        _expect(wq, f32, w, "wq")
+        _expect(wk, f32, w, "wk")
+        if self._rot:
+            e.table_rows = rows = cos.shape[0]
+            table = (rows, self._rot // 2)
+            _expect(cos, f32, table, "cos")
+            _expect(sin, f32, table, "sin")
+        _expect(positions, i32, self._q[:2], "positions")
+        _expect(start, i32, self._q[:1], "start")
 
     def forward(self, q, k, wq, wk, cos, sin, positions=None, start=None, yq=None, yk=None):
         """yq, yk in the output type (given: written there, in place where it is q or k itself)."""
-        e = self.desc
-        yq = self._empty(e.Hq, self.out_dtype) if yq is None else yq
-        yk = self._empty(e.Hk, self.out_dtype) if yk is None else yk
-        if yq.dtype != self.out_dtype or yk.dtype != self.out_dtype:
-            raise ValueError(f"yq, yk: expected {self.out_dtype}")
-        self._fill(q, k, wq, wk, cos, sin, positions, start, yq, yk)
-        _check(load().dr_norm_rope_fwd(ctypes.byref(e), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos),
-                                       _ptr(sin), _ptr(positions), _ptr(start), _ptr(yq), _ptr(yk),
-                                       self._stream()), "dr_norm_rope_fwd")
+        yq = self._empty(self._q, self.out_dtype) if yq is None else yq
+        yk = self._empty(self._k, self.out_dtype) if yk is None else yk
+        self._fill(q, k, wq, wk, cos, sin, positions, start, yq, yk, self.out_dtype)
+        _check(self._lib.dr_norm_rope_fwd(self._ref, _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin),
+                                          _ptr(positions), _ptr(start), _ptr(yq), _ptr(yk), self._stream()),
+               "dr_norm_rope_fwd")
         return yq, yk
 
     def backward(self, q, k, wq, wk, cos, sin, dyq, dyk, positions=None, start=None, out=None):
         """{dq, dk, dwq, dwk} for the incoming gradients dyq, dyk (contiguous, of the input type)."""
-        import torch
-        e = self.desc
+        w = (self.desc.d,)
         if out is None:
-            out = {"dq": self._empty(e.Hq, self.grad_dtype), "dk": self._empty(e.Hk, self.grad_dtype),
-                   "dwq": None if wq is None else torch.empty_like(wq),
-                   "dwk": None if wk is None else torch.empty_like(wk)}
-        if out["dq"].dtype != self.grad_dtype or out["dk"].dtype != self.grad_dtype:
-            raise ValueError(f"dq, dk: expected {self.grad_dtype}")
-        self._fill(q, k, wq, wk, cos, sin, positions, start, out["dq"], out["dk"])
-        for t, H, what in ((dyq, e.Hq, "dyq"), (dyk, e.Hk, "dyk")):
-            if H:
-                _expect(t, self.io_dtype, (e.B, e.T, H, e.d), what)
+            f32 = self._torch.float32
+            out = {"dq": self._empty(self._q, self.grad_dtype), "dk": self._empty(self._k, self.grad_dtype),
+                   "dwq": None if wq is None else self._empty(w, f32),
+                   "dwk": None if wk is None else self._empty(w, f32)}
+        self._fill(q, k, wq, wk, cos, sin, positions, start, out["dq"], out["dk"], self.grad_dtype)
+        _expect(dyq, self.io_dtype, self._q, "dyq")
+        _expect(dyk, self.io_dtype, self._k, "dyk")
+        _expect(out["dwq"], self._torch.float32, w, "dwq")
+        _expect(out["dwk"], self._torch.float32, w, "dwk")
         if self.ws is None:
-            n = int(load().dr_norm_rope_workspace_bytes(ctypes.byref(e)))
-            self.ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        _check(load().dr_norm_rope_bwd(ctypes.byref(e), _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos),
-                                       _ptr(sin), _ptr(positions), _ptr(start), _ptr(dyq), _ptr(dyk),
-                                       _ptr(out["dq"]), _ptr(out["dk"]), _ptr(out["dwq"]), _ptr(out["dwk"]),
-                                       self.ws.data_ptr(), self.ws.numel(), self._stream()),
-               "dr_norm_rope_bwd")
+            self.ws = self._empty(int(self._lib.dr_norm_rope_workspace_bytes(self._ref)), self._torch.uint8)
+        _check(self._lib.dr_norm_rope_bwd(self._ref, _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin),
+                                          _ptr(positions), _ptr(start), _ptr(dyq), _ptr(dyk), _ptr(out["dq"]),
+                                          _ptr(out["dk"]), _ptr(out["dwq"]), _ptr(out["dwk"]), _ptr(self.ws),
+                                          self.ws.numel(), self._stream()), "dr_norm_rope_bwd")
         return out
 
 
-class KvCache:
+class KvCache(_Calls):
     """A paged cache of keys and values in 8 bits ("i8" or "e4m3") with one scale for each page and
     head (dr_cache_write / dr_cache_read).  ``buffers`` = (k codes, v codes, k scales, v scales)
     takes existing device memory: codes [num_pages, H, page, d] of one byte each, scales
@@ -563,7 +573,7 @@ class KvCache:
 
     def __init__(self, num_pages, H, d, page=64, code="i8", buffers=None, device="cuda"):
         import torch
-        self.device = torch.device(device)
+        self._at(device)
         kind = torch.int8 if code == "i8" else torch.float8_e4m3fn
         if buffers is None:
             buffers = [torch.zeros(num_pages, H, page, d, dtype=torch.int8, device=self.device).view(kind)
@@ -580,51 +590,41 @@ class KvCache:
         c.k, c.v = self.k.data_ptr(), self.v.data_ptr()
         c.k_scale, c.v_scale = self.k_scale.data_ptr(), self.v_scale.data_ptr()
         c.status = self.word.data_ptr()
-        self.desc = c
+        self.desc, self._ref = c, ctypes.byref(c)
+        self._heads = (H, d)
 
-    def _stream(self):
-        import torch
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def seqs(self, table, lens, counts, T):
+    def seqs(self, B, table, lens, counts, T):
         """The call's positions: T tokens (or counts[b] <= T) after lens[b], in the pages of table
         [B, pages]."""
-        import torch
-        B = lens.shape[0]
-        _expect(table, torch.int32, (B, table.shape[1]), "table")
-        _expect(lens, torch.int32, (B,), "lens")
-        _expect(counts, torch.int32, (B,), "counts")
-        s = DrCacheSeqs()
-        s.B, s.T, s.table_stride = B, T, table.shape[1]
-        s.page_table, s.lens, s.counts = table.data_ptr(), lens.data_ptr(), _ptr(counts)
-        return s
+        i32 = self._torch.int32
+        pages = table.shape[-1]
+        _expect(table, i32, (B, pages), "table")
+        _expect(lens, i32, (B,), "lens")
+        _expect(counts, i32, (B,), "counts")
+        return DrCacheSeqs(B, T, table.data_ptr(), pages, lens.data_ptr(), _ptr(counts))
 
     def write(self, k, v, table, lens, counts=None):
         """Append k, v [B, T, H, d] (bf16 or fp32, or head ranges of a packed projection) after the
         first lens[b] positions of every sequence."""
-        import torch
-        c = self.desc
-        if k.dtype != v.dtype or k.dtype not in (torch.bfloat16, torch.float32) or k.shape != v.shape:
-            raise ValueError("k, v: expected two bf16 or two fp32 tensors of one shape")
-        if k.shape[0] != lens.shape[0]:
-            raise ValueError("k, v: one sequence for each of lens")
-        s = self.seqs(table, lens, counts, k.shape[1])
-        _check(load().dr_cache_write(ctypes.byref(c), ctypes.byref(s), _ptr(k), _rows(k, c.H, c.d, "k"),
-                                     _ptr(v), _rows(v, c.H, c.d, "v"), _dt(k), self._stream()),
-               "dr_cache_write")
+        torch = self._torch
+        if k.dtype is not v.dtype or k.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("k, v: expected two bf16 or two fp32 tensors")
+        shape = (*k.shape[:2], *self._heads)
+        s = self.seqs(shape[0], table, lens, counts, shape[1])
+        _check(self._lib.dr_cache_write(self._ref, ctypes.byref(s), _ptr(k), _rows(k, shape, "k"), _ptr(v),
+                                        _rows(v, shape, "v"), _dt(k), self._stream()), "dr_cache_write")
 
     def read(self, table, lens, counts, T, out="bf16", k=None, v=None):
         """k, v [B, T, H, d]: the values at positions lens[b] .. lens[b] + counts[b] - 1, zeros after."""
-        import torch
-        c = self.desc
-        s = self.seqs(table, lens, counts, T)
-        shape = (s.B, T, c.H, c.d)
-        k = torch.empty(shape, dtype=_torch_type(out), device=self.device) if k is None else k
-        v = torch.empty(shape, dtype=_torch_type(out), device=self.device) if v is None else v
-        _expect(k, _torch_type(out), shape, "k")
-        _expect(v, _torch_type(out), shape, "v")
-        _check(load().dr_cache_read(ctypes.byref(c), ctypes.byref(s), _ptr(k), _ptr(v), _TYPE_CODES[out],
-                                    self._stream()), "dr_cache_read")
+        B, dtype = lens.shape[0], _torch_type(out)
+        s = self.seqs(B, table, lens, counts, T)
+        shape = (B, T, *self._heads)
+        k = self._empty(shape, dtype) if k is None else k
+        v = self._empty(shape, dtype) if v is None else v
+        _expect(k, dtype, shape, "k")
+        _expect(v, dtype, shape, "v")
+        _check(self._lib.dr_cache_read(self._ref, ctypes.byref(s), _ptr(k), _ptr(v), _TYPE_CODES[out],
+                                       self._stream()), "dr_cache_read")
         return k, v
 
     def status(self) -> int:
@@ -635,42 +635,35 @@ class KvCache:
         self.word.zero_()
 
 
-class CacheAttention:
+class CacheAttention(_Calls):
     """Attention of up to T query tokens of each of B sequences over a KvCache (dr_cache_attn)."""
 
     def __init__(self, cache, B, T, Hq, io="bf16", out="bf16", scale=None, window=0):
-        import torch
+        self._at(cache.device)
         self.cache, self.B, self.T = cache, B, T
-        a = DrAttnDesc()
-        a.Hq, a.io_dtype, a.out_dtype, a.window = Hq, _TYPE_CODES[io], _TYPE_CODES[out], window
-        a.scale = cache.desc.d ** -0.5 if scale is None else float(scale)
-        a.ld_q = Hq * cache.desc.d
-        self.desc = a
+        d = cache.desc.d
+        a = DrAttnDesc(Hq, _TYPE_CODES[io], _TYPE_CODES[out], window,
+                       d ** -0.5 if scale is None else float(scale), Hq * d)
+        self.desc, self._ref = a, ctypes.byref(a)
         self.io_dtype, self.out_dtype = _torch_type(io), _torch_type(out)
-        n = int(load().dr_cache_attn_workspace_bytes(ctypes.byref(cache.desc), ctypes.byref(a), B, T))
+        self._shape = (B, T, Hq, d)
+        n = int(self._lib.dr_cache_attn_workspace_bytes(cache._ref, self._ref, B, T))
         if n == 0:
             raise DrError(DR_ERR_UNSUPPORTED, "dr_cache_attn_workspace_bytes")
-        self.ws = torch.empty(n, dtype=torch.uint8, device=cache.device)
+        self.ws = self._empty(n, self._torch.uint8)
 
     def forward(self, q, table, lens, counts=None, o=None, lse=None, want_lse=False):
         """o [B, T, Hq, d] and lse [B, T, Hq] (or None): query t of sequence b is the position
         lens[b] + t, which the cache already holds."""
-        import torch
-        a, c = self.desc, self.cache.desc
-        shape = (self.B, self.T, a.Hq, c.d)
-        if q.dtype != self.io_dtype or tuple(q.shape) != shape:
-            raise ValueError(f"q: expected {self.io_dtype} {shape}, got {q.dtype} {tuple(q.shape)}")
-        if lens.shape[0] != self.B:
-            raise ValueError(f"lens: expected {self.B} lengths")
-        a.ld_q = _rows(q, a.Hq, c.d, "q")
-        s = self.cache.seqs(table, lens, counts, self.T)
-        if o is None:
-            o = torch.empty(shape, dtype=self.out_dtype, device=self.cache.device)
-        if lse is None and want_lse:
-            lse = torch.empty(shape[:3], dtype=torch.float32, device=self.cache.device)
+        shape, f32 = self._shape, self._torch.float32
+        if q.dtype is not self.io_dtype:
+            raise ValueError(f"q: expected {self.io_dtype}, got {q.dtype}")
+        self.desc.ld_q = _rows(q, shape, "q")
+        s = self.cache.seqs(self.B, table, lens, counts, self.T)
+        o = self._empty(shape, self.out_dtype) if o is None else o
+        lse = self._empty(shape[:3], f32) if lse is None and want_lse else lse
         _expect(o, self.out_dtype, shape, "o")
-        _expect(lse, torch.float32, shape[:3], "lse")
-        _check(load().dr_cache_attn(ctypes.byref(c), ctypes.byref(s), ctypes.byref(a), _ptr(q), _ptr(o),
-                                    _ptr(lse), self.ws.data_ptr(), self.ws.numel(), self.cache._stream()),
-               "dr_cache_attn")
+        _expect(lse, f32, shape[:3], "lse")
+        _check(self._lib.dr_cache_attn(self.cache._ref, ctypes.byref(s), self._ref, _ptr(q), _ptr(o), _ptr(lse),
+                                       _ptr(self.ws), self.ws.numel(), self._stream()), "dr_cache_attn")
         return o, lse

@@ -4,14 +4,15 @@
 // The rows of a sequence and cache head are its query tokens times the G query heads that share
 // the cache head, row = t * G + g.  A block works on a tile of 8 NT rows of one (sequence, cache
 // head) over a stretch of its positions, in stages of 64; warp w takes positions 16 w .. 16 w + 15
-// of each stage on its own, from global memory to registers, so that warps never wait for one
-// another before the rows are joined at the end.
+// of each stage on its own, through a ring in shared memory that it fills with asynchronous copies
+// several stages ahead, so that warps never wait for one another before the rows are joined.
 //
 // Matrix products (m16n8k16, 16-bit operands, fp32 accumulation), with the 16 positions as rows:
 //   S^T = K Q^T    A = K codes (16 positions x d), B = Q^T (d x 8 rows)
 //   O^T += V^T P^T A = V^T codes (16 channels x 16 positions), B = P^T (16 positions x 8 rows)
 // Which channels a thread supplies is free as long as both operands agree, so every thread loads
-// 16 consecutive bytes and no operand passes through shared memory.  A code is exact in 16 bits.
+// 16 consecutive bytes at a time, and a code is exact in 16 bits.  16-byte chunk j of row r sits at
+// chunk j ^ swizzle(r) of the row in the ring, which spreads the reads of both products over the banks.
 //
 // Softmax in base 2.  The page scales enter in fp32: the key scale multiplies S, the value scale
 // vs multiplies the weights.  Both references are whole numbers, so that every rescaling is exact:
@@ -21,7 +22,8 @@
 //
 // Work is divided evenly: the stages of all tiles form one line, block i of n takes the i-th part
 // of it.  A tile that lies in one block is finished there; of the others each block leaves its
-// rows (sums, l, m, M) in the workspace, and a second kernel joins them.
+// rows (sums, l, m, M) in the workspace, and a second kernel joins them, one warp to a row.  It is
+// launched early and waits on the device for the first one to end.
 #include <cuda_fp16.h>
 
 #include "cache_attn.cuh"
@@ -94,8 +96,15 @@ __device__ __forceinline__ int find_seq(const AttnParams& p, int lane, long long
     begin = before;
     return p.c.B;
 }
-// Block i of n takes places share(i) .. share(i + 1) - 1 of the line.
+// Block i of n <= total takes places share(i) .. share(i + 1) - 1 of the line, at least one;
+// holder(at) is the block that has place `at`: total i / n <= at where total i < (at + 1) n.
 __device__ __forceinline__ long long share(long long total, int i, int n) { return total * i / n; }
+__device__ __forceinline__ int holder(long long total, long long at, int n) {
+    return (int)(((at + 1) * n - 1) / total);
+}
+__device__ __forceinline__ int blocks_used(long long total, int blocks) {
+    return total < blocks ? (int)total : blocks;
+}
 
 // ------------------------------------------------------------------ operands
 __device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
@@ -151,13 +160,25 @@ __device__ __forceinline__ float pow2i(float x) {
     return __uint_as_float((uint32_t)((int)fminf(x, 127.f) + 127) << 23);
 }
 
-// The codes of a warp's 16 positions.  Thread (g, c) = (lane / 4, lane % 4) holds of the keys
-// positions g and g + 8, channels 64 i + 16 c .. + 15; of the values positions 2c, 2c + 1, 2c + 8,
-// 2c + 9, channels g d/8 .. + d/8 - 1.
+// The codes of a warp's 16 positions.  Thread (g, c) = (lane / 4, lane % 4) takes of the keys
+// positions g and g + 8, 16-byte chunks c d/64 .. + d/64 - 1 of the row; of the values positions
+// 2c, 2c + 1, 2c + 8, 2c + 9, channels g d/8 .. + d/8 - 1.
 template <int D>
 struct Codes {
     uint32_t k[2][D / 16], v[4][D / 32];
 };
+template <int D> __device__ __forceinline__ int swizzle(int row) { return D == 128 ? row & 7 : (row >> 1) & 3; }
+template <int D>
+__device__ __forceinline__ void copy_codes(uint32_t ring, const uint8_t* src, int lane) {
+#pragma unroll
+    for (int j = 0; j < D / 32; ++j) {
+        const int at = 32 * j + lane, row = at / (D / 16), chunk = at % (D / 16);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ring + row * D +
+                                                                        ((chunk ^ swizzle<D>(row)) << 4)),
+                     "l"(src + 16 * at)
+                     : "memory");
+    }
+}
 template <int D>
 __device__ __forceinline__ void load_codes(Codes<D>& f, const uint8_t* kp, const uint8_t* vp, int lane) {
     const int g = lane >> 2, c = lane & 3;
@@ -165,17 +186,19 @@ __device__ __forceinline__ void load_codes(Codes<D>& f, const uint8_t* kp, const
     for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(kp + (g + 8 * r) * D + 64 * i + 16 * c));
+            const int row = g + 8 * r, chunk = c * (D / 64) + i;
+            const uint4 u = *reinterpret_cast<const uint4*>(kp + row * D + ((chunk ^ swizzle<D>(row)) << 4));
             f.k[r][4 * i] = u.x; f.k[r][4 * i + 1] = u.y; f.k[r][4 * i + 2] = u.z; f.k[r][4 * i + 3] = u.w;
         }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        const uint8_t* at = vp + (2 * c + (r & 1) + 8 * (r >> 1)) * D + g * (D / 8);
+        const int row = 2 * c + (r & 1) + 8 * (r >> 1);
         if constexpr (D == 128) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(at));
+            const uint4 u = *reinterpret_cast<const uint4*>(vp + row * D + ((g ^ swizzle<D>(row)) << 4));
             f.v[r][0] = u.x; f.v[r][1] = u.y; f.v[r][2] = u.z; f.v[r][3] = u.w;
         } else {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(at));
+            const uint2 u = *reinterpret_cast<const uint2*>(vp + row * D + (((g >> 1) ^ swizzle<D>(row)) << 4) +
+                                                            8 * (g & 1));
             f.v[r][0] = u.x; f.v[r][1] = u.y;
         }
     }
@@ -215,7 +238,7 @@ __device__ __forceinline__ void load_tile(Tile<D, NT, PREC>& t, const AttnParams
         for (int i = 0; i < D / 64; ++i)
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-                x[16 * i + j] = on ? load_q(p, at + 64 * i + 16 * c + j) : 0.f;
+                x[16 * i + j] = on ? load_q(p, at + c * (D / 4) + 16 * i + j) : 0.f;
                 top = fmaxf(top, fabsf(x[16 * i + j]));
             }
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -261,7 +284,7 @@ __device__ __forceinline__ void load_tile(Tile<D, NT, PREC>& t, const AttnParams
 // One step: 16 positions from `first` on.
 template <int D, int NT, bool E4M3, bool PREC>
 __device__ __forceinline__ void step(Tile<D, NT, PREC>& t, Codes<D>& f, const AttnParams& p, const Seq& s,
-                                     int first, float ks, float vs, float ve, bool edge, int lane) {
+                                     int first, int end, float ks, float vs, float ve, bool edge, int lane) {
     const int g = lane >> 2, c = lane & 3;
     float sc[NT][4];
 #pragma unroll
@@ -278,8 +301,7 @@ __device__ __forceinline__ void step(Tile<D, NT, PREC>& t, Codes<D>& f, const At
         }
     }
     if (edge) {
-        // codes behind the last position may be anything: as values they count as zero
-        const int end = s.len + s.n;
+        // codes from position `end` on may be anything: as values they count as zero
 #pragma unroll
         for (int r = 0; r < 4; ++r)
             if (first + 2 * c + (r & 1) + 8 * (r >> 1) >= end) {
@@ -388,17 +410,33 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int b, int h, int
     if (ch == 0 && p.lse) p.lse[at] = (m + log2f(l)) * 0.69314718055994530942f;
 }
 
-template <int D, int NT, bool E4M3, bool PREC>
-__global__ void __launch_bounds__(kThreads) cache_attn_kernel(const AttnParams p) {
-    constexpr int ROWS = 8 * NT;
-    __shared__ float so[kWarps][ROWS][D + 4];
-    __shared__ float sl[kWarps][ROWS], sm[kWarps][ROWS], sM[kWarps][ROWS];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+constexpr int kRing = 4;  // stages of a warp's ring
+template <int D> __host__ __device__ constexpr int ring_bytes() { return kRing * 2 * 16 * D; }
+// The rows of the warps, when they are joined, take the place of the rings.
+template <int D, int NT> struct Joined {
+    float o[kWarps][8 * NT][D + 4];
+    float l[kWarps][8 * NT], m[kWarps][8 * NT], M[kWarps][8 * NT];
+};
+template <int D, int NT> __host__ __device__ constexpr int smem_bytes() {
+    return kWarps * ring_bytes<D>() > (int)sizeof(Joined<D, NT>) ? kWarps * ring_bytes<D>()
+                                                                 : (int)sizeof(Joined<D, NT>);
+}
 
+template <int D, int NT, bool E4M3, bool PREC>
+__global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 3 : 2) cache_attn_kernel(const AttnParams p) {
+    constexpr int ROWS = 8 * NT;
+    extern __shared__ __align__(128) uint8_t smem[];
+    Joined<D, NT>& joined = *reinterpret_cast<Joined<D, NT>*>(smem);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
+    uint8_t* ring = smem + warp * ring_bytes<D>();
+    const uint32_t ring32 = (uint32_t)__cvta_generic_to_shared(ring);
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long total = line_length<ROWS>(p, lane);
-    const long long begin = share(total, blockIdx.x, gridDim.x);
-    const long long end = share(total, blockIdx.x + 1, gridDim.x);
-    if (begin >= end) return;
+    const int used = blocks_used(total, gridDim.x);
+    if ((int)blockIdx.x >= used) return;
+    const long long begin = share(total, blockIdx.x, used);
+    const long long end = share(total, blockIdx.x + 1, used);
     long long at = begin, seq_begin;
     int b = find_seq<ROWS>(p, lane, at, seq_begin);
     while (at < end) {
@@ -410,19 +448,15 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const AttnParams p
         }
         // stretches of one sequence: head by head, tile by tile, stage by stage
         const long long in = at - seq_begin;
-        const int unit = (int)(in / s.stages), from = (int)(in % s.stages);
+        const int unit = (int)(in / s.stages), from = (int)(in - (long long)unit * s.stages);
         const int h = unit / s.tiles, row0 = (unit % s.tiles) * ROWS;
         const int upto = (int)min((long long)s.stages, from + (end - at));
-        Tile<D, NT, PREC> t;
-        load_tile(t, p, b, h, row0, s, lane);
         // positions that the tile's rows see
         const int t0 = row0 / p.G, t1 = min(s.n - 1, (row0 + ROWS - 1) / p.G);
         const int hi = s.len + t1 + 1, lo = p.window > 0 ? max(0, s.len + t0 - p.window + 1) : 0;
         // positions that every row sees need no mask
         const int all_hi = s.len + t0 + 1, all_lo = p.window > 0 ? max(0, s.len + t1 - p.window + 1) : 0;
 
-        const uint8_t* kbase = p.c.k;
-        const uint8_t* vbase = p.c.v;
         auto meta = [&](int st) {
             Meta x;
             x.id = -2;
@@ -446,88 +480,88 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const AttnParams p
             }
             return x;
         };
+        // Step k = 0 .. n - 1 of the stretch; lane k % 32 of batch k / 32 has its meta, in `now` or
+        // `next` by the batch's parity.  The copies run kRing - 1 < 32 steps ahead.
+        const int n = upto - from;
         Meta now = meta(from + lane), next = meta(from + 32 + lane);
-        Codes<D> f[2];
-        auto fetch = [&](Codes<D>& x, int st) {
-            const int k = st - from;
+        auto fetch = [&](int k) {
             const int id = __shfl_sync(0xffffffffu, k & 32 ? next.id : now.id, k & 31);
-            if (id >= 0) {
-                const int first = (s.s0 + st) * kStage + 16 * warp;
+            if (k < n && id >= 0) {
+                const int first = (s.s0 + from + k) * kStage + 16 * warp;
                 const size_t off = (((size_t)id * p.c.H + h) * p.c.page + first % p.c.page) * D;
-                load_codes<D>(x, kbase + off, vbase + off, lane);
-            } else {
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-#pragma unroll
-                    for (int i = 0; i < D / 16; ++i) x.k[r][i] = 0;
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-#pragma unroll
-                    for (int i = 0; i < D / 32; ++i) x.v[r][i] = 0;
+                const uint32_t slot = ring32 + (k % kRing) * 32 * D;
+                copy_codes<D>(slot, p.c.k + off, lane);
+                copy_codes<D>(slot + 16 * D, p.c.v + off, lane);
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        // st - from runs through batches of 32 steps: bit 5 tells in which of two the step's meta is
-        auto consume = [&](Codes<D>& x, int st) {
-            const int k = st - from;
+#pragma unroll
+        for (int k = 0; k < kRing - 1; ++k) fetch(k);
+        Tile<D, NT, PREC> t;
+        load_tile(t, p, b, h, row0, s, lane);
+        for (int k = 0; k < n; ++k) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+            __syncwarp();  // every lane's copies of step k are there, and step k - 1 is read
+            fetch(k + kRing - 1);
             const bool second = k & 32;
             const int id = __shfl_sync(0xffffffffu, second ? next.id : now.id, k & 31);
             const float ks = __shfl_sync(0xffffffffu, second ? next.ks : now.ks, k & 31);
             const float vs = __shfl_sync(0xffffffffu, second ? next.vs : now.vs, k & 31);
             const float ve = __shfl_sync(0xffffffffu, second ? next.ve : now.ve, k & 31);
             if (id != -2) {
-                const int first = (s.s0 + st) * kStage + 16 * warp;
-                const bool edge = first + 16 > all_hi || first < all_lo;
-                step<D, NT, E4M3, PREC>(t, x, p, s, first, ks, vs, ve, edge, lane);
+                const int first = (s.s0 + from + k) * kStage + 16 * warp;
+                const bool edge = first + 16 > all_hi || first < all_lo || id < 0;
+                const uint8_t* slot = ring + (k % kRing) * 32 * D;
+                Codes<D> f;
+                load_codes<D>(f, slot, slot + 16 * D, lane);
+                step<D, NT, E4M3, PREC>(t, f, p, s, first, id < 0 ? 0 : s.len + s.n, ks, vs, ve, edge, lane);
             }
             if ((k & 31) == 31) {  // the batch is used up: the one after next takes its place
-                const Meta m2 = meta(from + (k | 31) + 1 + 32 + lane);
+                const Meta m2 = meta(from + k + 1 + 32 + lane);
                 if (second) next = m2; else now = m2;
-            }
-        };
-        fetch(f[0], from);
-        for (int st = from; st < upto; st += 2) {
-            if (st + 1 < upto) fetch(f[1], st + 1);
-            consume(f[0], st);
-            if (st + 1 < upto) {
-                if (st + 2 < upto) fetch(f[0], st + 2);
-                consume(f[1], st + 1);
             }
         }
 
         // join the warps: rows 2c, 2c + 1 of each 8, channels g d/8 ..
-        __syncthreads();  // the arrays are free again
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();  // the rings are free
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n8 = 0; n8 < NT; ++n8)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float l = t.l[n][j];
+                float l = t.l[n8][j];
                 l += __shfl_xor_sync(0xffffffffu, l, 4);
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
-                const int row = 8 * n + 2 * c + j;
-                if (g == 0) { sl[warp][row] = l; sm[warp][row] = t.m[n][j]; sM[warp][row] = t.M[n][j]; }
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    so[warp][row][g * (D / 8) + 2 * i] = t.o[n][i][j];
-                    so[warp][row][g * (D / 8) + 2 * i + 1] = t.o[n][i][2 + j];
+                const int row = 8 * n8 + 2 * c + j;
+                if (g == 0) {
+                    joined.l[warp][row] = l;
+                    joined.m[warp][row] = t.m[n8][j];
+                    joined.M[warp][row] = t.M[n8][j];
                 }
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    *reinterpret_cast<float2*>(&joined.o[warp][row][g * (D / 8) + 2 * i]) =
+                        make_float2(t.o[n8][i][j], t.o[n8][i][2 + j]);
             }
         __syncthreads();
         const bool whole = from == 0 && upto == s.stages;
         float* out = p.part + ((size_t)blockIdx.x * 2 + (at == begin ? 0 : 1)) * tile_floats(D, ROWS);
         for (int i = threadIdx.x; i < ROWS * D; i += kThreads) {
             const int r = i / D, ch = i % D, row = row0 + r;
+            if (row >= s.n * p.G) break;
             float m = kNegInf, M = kNegInf, l = 0.f, sum = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) { m = fmaxf(m, sm[w][r]); M = fmaxf(M, sM[w][r]); }
+            for (int w = 0; w < kWarps; ++w) { m = fmaxf(m, joined.m[w][r]); M = fmaxf(M, joined.M[w][r]); }
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 // a warp without weight adds nothing, one that met a NaN hands it on
-                l += sl[w][r] * (sl[w][r] == sl[w][r] ? pow2i(sm[w][r] - m) : 1.f);
-                sum += so[w][r][ch] * (so[w][r][ch] == so[w][r][ch] ? pow2i(sM[w][r] - M) : 1.f);
+                const float wl = joined.l[w][r], wo = joined.o[w][r][ch];
+                l += wl * (wl == wl ? pow2i(joined.m[w][r] - m) : 1.f);
+                sum += wo * (wo == wo ? pow2i(joined.M[w][r] - M) : 1.f);
             }
             if (whole) {
-                if (row < s.n * p.G) write_row(p, b, h, row, ch, D, sum, l, m, M);
+                write_row(p, b, h, row, ch, D, sum, l, m, M);
             } else {
                 out[(size_t)r * D + ch] = sum;
                 if (ch == 0) {
@@ -537,70 +571,91 @@ __global__ void __launch_bounds__(kThreads) cache_attn_kernel(const AttnParams p
                 }
             }
         }
-        at += upto - from;
+        __syncthreads();  // the rings are filled again
+        at += n;
     }
 }
 
-// Joins the parts of a tile that several blocks worked on.  Block x: the tile; y: 8 of its rows.
-// Rows of no query get zeros (behind a sequence's tokens) or NaN (a sequence out of range).
+// Until the first kernel has ended and its writes are there.  Every thread of the second one comes
+// here, so that its end also means the end of the first.
+__device__ __forceinline__ void wait_for_parts() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Joins the parts of a tile that several blocks worked on.  Block x: the tile; y: 8 of its rows, a
+// warp each.  Rows of no query get zeros (behind a sequence's tokens) or NaN (a sequence out of range).
 template <int D, int NT>
-__global__ void __launch_bounds__(D) cache_attn_join_kernel(const AttnParams p, int blocks, int max_tiles) {
-    constexpr int ROWS = 8 * NT;
-    const int lane = threadIdx.x & 31, ch = threadIdx.x;
+__global__ void __launch_bounds__(256) cache_attn_join_kernel(const AttnParams p, int blocks, int max_tiles) {
+    constexpr int ROWS = 8 * NT, V = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.x / (p.c.H * max_tiles), rest = blockIdx.x % (p.c.H * max_tiles);
     const int h = rest / max_tiles, tile = rest % max_tiles;
+    const int r = blockIdx.y * 8 + warp, row = tile * ROWS + r;
     const Seq s = make_seq<ROWS>(p, b);
-    int len, n;
-    const bool ok = cache_seq(p.c, b, len, n);
-    if (!ok && threadIdx.x == 0) flag_index_error(p.c);
-    const int row0 = tile * ROWS + blockIdx.y * 8, rows = min(8, p.c.T * p.G - row0);
-    for (int r = max(0, s.n * p.G - row0); r < rows; ++r) {
-        const int tok = (row0 + r) / p.G, head = h * p.G + (row0 + r) % p.G;
-        const size_t at = ((size_t)b * p.c.T + tok) * p.Hq + head;
-        st_any(p.o, at * D + ch, p.out, ok ? 0.f : __uint_as_float(0x7fc00000u));
-        if (ch == 0 && p.lse) p.lse[at] = ok ? kNegInf : __uint_as_float(0x7fc00000u);
-    }
-    if (row0 >= s.n * p.G) return;
-    const long long total = line_length<ROWS>(p, lane);
-    long long before = 0;  // the line up to this sequence
-    for (int b0 = 0; b0 < b; b0 += 32)
-        if (b0 + lane < b) before += work_of(p, make_seq<ROWS>(p, b0 + lane));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-    const long long a = before + ((long long)h * s.tiles + tile) * s.stages, e = a + s.stages;
-    // the blocks whose shares meet a .. e - 1
-    int first = (int)(a * blocks / total);
-    while (first > 0 && share(total, first, blocks) > a) --first;
-    while (share(total, first + 1, blocks) <= a) ++first;
-    int last = first;
-    while (share(total, last + 1, blocks) < e) ++last;
-    if (first == last) return;  // finished by its block
-    for (int r = blockIdx.y * 8; r < blockIdx.y * 8 + 8; ++r) {
-        const int row = tile * ROWS + r;
-        if (row >= s.n * p.G) return;
-        float m = kNegInf, M = kNegInf, l = 0.f, sum = 0.f;
-        for (int i = first; i <= last; ++i) {
-            if (share(total, i, blocks) == share(total, i + 1, blocks)) continue;
-            // a block that began before the tile holds it as its second part
-            const float* in = p.part + ((size_t)i * 2 + (share(total, i, blocks) >= a ? 0 : 1)) * tile_floats(D, ROWS);
-            const float pl = in[ROWS * D + r], pm = in[ROWS * D + ROWS + r], pM = in[ROWS * D + 2 * ROWS + r];
-            const float ps = in[(size_t)r * D + ch];
-            const float m2 = fmaxf(m, pm), M2 = fmaxf(M, pM);
-            l = (l == l ? l * pow2i(m - m2) : l) + (pl == pl ? pl * pow2i(pm - m2) : pl);
-            sum = (sum == sum ? sum * pow2i(M - M2) : sum) + (ps == ps ? ps * pow2i(pM - M2) : ps);
-            m = m2;
-            M = M2;
+    if (row >= s.n * p.G) {
+        int len, n;
+        const bool ok = cache_seq(p.c, b, len, n);
+        if (!ok && lane == 0) flag_index_error(p.c);
+        if (row < p.c.T * p.G) {
+            const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
+            const float bad = __uint_as_float(0x7fc00000u);
+            for (int ch = lane; ch < D; ch += 32) st_any(p.o, at * D + ch, p.out, ok ? 0.f : bad);
+            if (lane == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
         }
-        write_row(p, b, h, row, ch, D, sum, l, m, M);
+        wait_for_parts();
+        return;
     }
+    long long total = 0, before = 0;  // the line, and up to this sequence
+    for (int i = lane; i < p.c.B; i += 32) {
+        const long long x = work_of(p, make_seq<ROWS>(p, i));
+        total += x;
+        if (i < b) before += x;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+    }
+    const long long a = before + ((long long)h * s.tiles + tile) * s.stages;
+    const int used = blocks_used(total, blocks);
+    const int first = holder(total, a, used), last = holder(total, a + s.stages - 1, used);
+    wait_for_parts();
+    if (first == last) return;  // finished by its block
+    // a block that began before the tile holds it as its second part
+    const float* head = p.part + ((size_t)first * 2 + (share(total, first, used) >= a ? 0 : 1)) * tile_floats(D, ROWS);
+    // lane i looks at parts i, i + 32, ..: the references, then the sums in the order of the parts
+    float m = kNegInf, M = kNegInf;
+    for (int i = first + lane; i <= last; i += 32) {
+        const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, ROWS);
+        m = fmaxf(m, in[ROWS * D + ROWS + r]);
+        M = fmaxf(M, in[ROWS * D + 2 * ROWS + r]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    }
+    float l = 0.f, sum[V] = {};
+#pragma unroll 4
+    for (int i = first; i <= last; ++i) {
+        const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, ROWS);
+        const float pl = in[ROWS * D + r], fl = pow2i(in[ROWS * D + ROWS + r] - m);
+        const float fs = pow2i(in[ROWS * D + 2 * ROWS + r] - M);
+        l += pl == pl ? pl * fl : pl;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float x = in[(size_t)r * D + 32 * j + lane];
+            sum[j] += x == x ? x * fs : x;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < V; ++j) write_row(p, b, h, row, 32 * j + lane, D, sum[j], l, m, M);
 }
 
 template <typename K>
-int resident_blocks(K kernel) {
+int resident_blocks(K kernel, int smem) {
     int sms = 0, per = 0, dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, 0) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem) != cudaSuccess) return 0;
     return sms * per;
 }
 
@@ -608,18 +663,29 @@ constexpr int kMaxBlocks = 152 * 8;
 
 template <int D, int NT, bool E4M3, bool PREC>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
-    static const int resident = resident_blocks(cache_attn_kernel<D, NT, E4M3, PREC>);
+    static std::atomic<unsigned long long> ready{0};
+    constexpr int smem = smem_bytes<D, NT>();
+    if (cudaError_t e = set_smem_once(cache_attn_kernel<D, NT, E4M3, PREC>, smem, ready); e != cudaSuccess) return e;
+    static const int resident = resident_blocks(cache_attn_kernel<D, NT, E4M3, PREC>, smem);
     if (resident <= 0) return cudaErrorUnknown;
     const int blocks = resident < kMaxBlocks ? resident : kMaxBlocks;
     {
         TraceScope ts("cache_attn", st);
-        cache_attn_kernel<D, NT, E4M3, PREC><<<blocks, kThreads, 0, st>>>(p);
+        cache_attn_kernel<D, NT, E4M3, PREC><<<blocks, kThreads, smem, st>>>(p);
         if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     }
     const int max_tiles = (p.c.T * p.G + 8 * NT - 1) / (8 * NT);
     TraceScope ts("cache_attn_join", st);
-    cache_attn_join_kernel<D, NT><<<dim3((unsigned)p.c.B * p.c.H * max_tiles, NT), D, 0, st>>>(p, blocks, max_tiles);
-    return cudaGetLastError();
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.c.B * p.c.H * max_tiles, NT);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, NT>, p, blocks, max_tiles);
 }
 
 // Rows of a tile: 16 halve the reads of the cache where a sequence and head have more than 8.  The
