@@ -470,11 +470,18 @@ class _Calls:
     def _at(self, device):
         import torch
         self.device = torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None and torch.cuda.is_available():
+            self.device = torch.device("cuda", torch.cuda.current_device())
         self._torch = torch
         self._lib = load()
+        # the handle alone where torch offers it: building a Stream object costs more than a launch
+        self._raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
     def _stream(self):
-        return self._torch.cuda.current_stream(self.device).cuda_stream
+        index = self.device.index
+        if self._raw is None or index is None:
+            return self._torch.cuda.current_stream(self.device).cuda_stream
+        return self._raw(index)
 
     def _empty(self, shape, dtype):
         return self._torch.empty(shape, dtype=dtype, device=self.device)

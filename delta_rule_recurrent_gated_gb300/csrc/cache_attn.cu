@@ -3,11 +3,11 @@
 //
 // The rows of a sequence and cache head are its query tokens times the G query heads that share
 // the cache head, row = t * G + g.  A block works on a tile of 8 NT rows of one (sequence, cache
-// head) over a stretch of its positions, in stages of 64; warp w takes positions 16 w .. 16 w + 15
+// head) over a stretch of its positions, in stages of 64; warp w takes positions 32 w .. 32 w + 31
 // of each stage on its own, through a ring in shared memory that it fills with asynchronous copies
-// several stages ahead, so that warps never wait for one another before the rows are joined.
+// a stage ahead, so that warps never wait for one another before the rows are joined.
 //
-// Matrix products (m16n8k16, 16-bit operands, fp32 accumulation), with the 16 positions as rows:
+// Matrix products (m16n8k16, 16-bit operands, fp32 accumulation), with 16 positions as rows:
 //   S^T = K Q^T    A = K codes (16 positions x d), B = Q^T (d x 8 rows)
 //   O^T += V^T P^T A = V^T codes (16 channels x 16 positions), B = P^T (16 positions x 8 rows)
 // Which channels a thread supplies is free as long as both operands agree, so every thread loads
@@ -20,10 +20,10 @@
 //   M >= max (s + log2 vs), w = p vs 2^(m - M + 14) <= 2^14 is the 16-bit operand.
 // With PREC (fp32 queries or outputs) queries and weights are split into two 16-bit terms.
 //
-// Work is divided evenly: the stages of all tiles form one line, block i of n takes the i-th part
-// of it.  A tile that lies in one block is finished there; of the others each block leaves its
-// rows (sums, l, m, M) in the workspace, and a second kernel joins them, one warp to a row.  It is
-// launched early and waits on the device for the first one to end.
+// Work is divided evenly: the stages of all tiles, each tile with a few more for its start and end,
+// form one line, block i of n takes the i-th part of it.  A tile that lies in one block is finished
+// there; of the others each block leaves its rows (sums, l, m, M) in the workspace, and a second
+// kernel joins them, a block to a row.  It is launched early and waits on the device for the first.
 #include <cuda_fp16.h>
 
 #include "cache_attn.cuh"
@@ -32,7 +32,9 @@
 namespace dr {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps, kStage = 16 * kWarps;
+constexpr int kWarps = 2, kThreads = 32 * kWarps;
+constexpr int kStep = 32, kStage = kStep * kWarps;  // positions of a warp's step, of a stage
+constexpr int kOver = 4;  // what a tile costs beside its stages, in stages
 constexpr float kNegInf = -INFINITY;
 constexpr int kBias = 14;  // weights as 16-bit operands reach 2^14
 
@@ -57,7 +59,7 @@ __device__ __forceinline__ Seq make_seq(const AttnParams& p, int b) {
     return s;
 }
 __device__ __forceinline__ long long work_of(const AttnParams& p, const Seq& s) {
-    return (long long)s.tiles * s.stages * p.c.H;
+    return s.n > 0 ? (long long)s.tiles * (s.stages + kOver) * p.c.H : 0;
 }
 __device__ __forceinline__ long long warp_scan(long long x, int lane) {
 #pragma unroll
@@ -107,27 +109,28 @@ __device__ __forceinline__ int blocks_used(long long total, int blocks) {
 }
 
 // ------------------------------------------------------------------ operands
-__device__ __forceinline__ uint32_t prmt(uint32_t a, uint32_t b, uint32_t sel) {
-    return __byte_perm(a, b, sel);
-}
-// Two codes of `w` (bytes 0, 1 or 2, 3) as a pair of 16-bit floats.
+// The four codes of `w` as two pairs of 16-bit floats: bytes (0, 2) and (1, 3) of int8 codes,
+// bytes (0, 1) and (2, 3) of e4m3 codes.
 template <bool E4M3>
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& a, uint32_t& b) {
     if (E4M3) {
-        asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n"
-            " cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-            : "=r"(lo), "=r"(hi)
+        asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %2;\n"
+            " cvt.rn.f16x2.e4m3x2 %0, x;\n cvt.rn.f16x2.e4m3x2 %1, y;\n}\n"
+            : "=r"(a), "=r"(b)
             : "r"(w));
     } else {
         // x + 128 in the low bits of 1024 .. 2047, whose spacing is 1; minus 1152 is x exactly
-        const uint32_t u = w ^ 0x80808080u;
         const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
-        uint32_t a = prmt(u, 0x64646464u, 0x4140), b = prmt(u, 0x64646464u, 0x4342);
-        const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off);
-        const __half2 y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
-        lo = *reinterpret_cast<const uint32_t*>(&x);
-        hi = *reinterpret_cast<const uint32_t*>(&y);
+        uint32_t u = (w & 0x00ff00ffu) ^ 0x64806480u, v = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
+        const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&u), off);
+        const __half2 y = __hsub2(*reinterpret_cast<__half2*>(&v), off);
+        a = *reinterpret_cast<const uint32_t*>(&x);
+        b = *reinterpret_cast<const uint32_t*>(&y);
     }
+}
+// Bytes 0, 1 (HI: 2, 3) of the words of two positions, so that codes_to_half pairs the positions.
+template <bool E4M3, bool HI> __device__ __forceinline__ uint32_t pair_up(uint32_t x, uint32_t y) {
+    return __byte_perm(x, y, E4M3 ? (HI ? 0x7362 : 0x5140) : (HI ? 0x7632 : 0x5410));
 }
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                     uint32_t b0, uint32_t b1) {
@@ -160,13 +163,9 @@ __device__ __forceinline__ float pow2i(float x) {
     return __uint_as_float((uint32_t)((int)fminf(x, 127.f) + 127) << 23);
 }
 
-// The codes of a warp's 16 positions.  Thread (g, c) = (lane / 4, lane % 4) takes of the keys
-// positions g and g + 8, 16-byte chunks c d/64 .. + d/64 - 1 of the row; of the values positions
-// 2c, 2c + 1, 2c + 8, 2c + 9, channels g d/8 .. + d/8 - 1.
-template <int D>
-struct Codes {
-    uint32_t k[2][D / 16], v[4][D / 32];
-};
+// 16 positions in the ring.  Thread (g, c) = (lane / 4, lane % 4) takes of the keys positions g and
+// g + 8, 16-byte chunks c d/64 .. + d/64 - 1 of the row; of the values positions 2c, 2c + 1, 2c + 8,
+// 2c + 9, channels g d/8 .. + d/8 - 1.
 template <int D> __device__ __forceinline__ int swizzle(int row) { return D == 128 ? row & 7 : (row >> 1) & 3; }
 template <int D>
 __device__ __forceinline__ void copy_codes(uint32_t ring, const uint8_t* src, int lane) {
@@ -180,7 +179,7 @@ __device__ __forceinline__ void copy_codes(uint32_t ring, const uint8_t* src, in
     }
 }
 template <int D>
-__device__ __forceinline__ void load_codes(Codes<D>& f, const uint8_t* kp, const uint8_t* vp, int lane) {
+__device__ __forceinline__ void load_keys(uint32_t (&k)[2][D / 16], const uint8_t* kp, int lane) {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int r = 0; r < 2; ++r)
@@ -188,26 +187,29 @@ __device__ __forceinline__ void load_codes(Codes<D>& f, const uint8_t* kp, const
         for (int i = 0; i < D / 64; ++i) {
             const int row = g + 8 * r, chunk = c * (D / 64) + i;
             const uint4 u = *reinterpret_cast<const uint4*>(kp + row * D + ((chunk ^ swizzle<D>(row)) << 4));
-            f.k[r][4 * i] = u.x; f.k[r][4 * i + 1] = u.y; f.k[r][4 * i + 2] = u.z; f.k[r][4 * i + 3] = u.w;
+            k[r][4 * i] = u.x; k[r][4 * i + 1] = u.y; k[r][4 * i + 2] = u.z; k[r][4 * i + 3] = u.w;
         }
+}
+template <int D>
+__device__ __forceinline__ void load_values(uint32_t (&v)[4][D / 32], const uint8_t* vp, int lane) {
+    const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
         const int row = 2 * c + (r & 1) + 8 * (r >> 1);
         if constexpr (D == 128) {
             const uint4 u = *reinterpret_cast<const uint4*>(vp + row * D + ((g ^ swizzle<D>(row)) << 4));
-            f.v[r][0] = u.x; f.v[r][1] = u.y; f.v[r][2] = u.z; f.v[r][3] = u.w;
+            v[r][0] = u.x; v[r][1] = u.y; v[r][2] = u.z; v[r][3] = u.w;
         } else {
             const uint2 u = *reinterpret_cast<const uint2*>(vp + row * D + (((g >> 1) ^ swizzle<D>(row)) << 4) +
                                                             8 * (g & 1));
-            f.v[r][0] = u.x; f.v[r][1] = u.y;
+            v[r][0] = u.x; v[r][1] = u.y;
         }
     }
 }
 
-// What a warp needs of its 16 positions of a stage: the page and its scales.  Lane i holds those
-// of step (batch * 32 + i).
-struct Meta {
-    int id;            // page, -1 where the entry is out of range, -2 where nothing is visible
+// What a warp needs to know of 16 positions.
+struct __align__(16) Meta {
+    int id;            // page, -1 where the entry is out of range, -2 where no row sees a position
     float ks, vs, ve;  // scales; whole number with vs <= 2^ve
 };
 
@@ -217,63 +219,97 @@ struct Tile {
     float qs[NT][2];       // factor of S for rows 2c, 2c + 1
     int pos[NT][2];        // their positions (-1: no such row)
     float o[NT][D / 16][4], l[NT][2], m[NT][2], M[NT][2];
+    float f[NT][2];        // 2^(m - M + 14)
 };
 
-__device__ __forceinline__ float load_q(const AttnParams& p, long long at) { return ld_any(p.q, at, p.io); }
+// Queries as loaded: the thread's channels c d/4 .. + d/4 - 1 of row g of each 8.
+template <int D, int NT> struct RawQ {
+    uint4 b[NT][D / 32];  // bf16
+    float x[D / 4];       // fp32, one group of 8 rows at a time
+};
+__device__ __forceinline__ long long q_at(const AttnParams& p, int b, int h, int row, const Seq& s, int d, int c) {
+    const int tok = row / p.G, head = h * p.G + row % p.G;
+    return ((long long)b * p.c.T + tok) * p.ld_q + (long long)head * d + c * (d / 4);
+}
+template <int D, int NT>
+__device__ __forceinline__ void fetch_q(RawQ<D, NT>& r, const AttnParams& p, int b, int h, int row0, const Seq& s,
+                                        int lane) {
+    if (p.io == DR_F32) return;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int row = row0 + 8 * n + (lane >> 2);
+        const bool on = row < s.n * p.G;
+        const uint4* at = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                         (on ? q_at(p, b, h, row, s, D, lane & 3) : 0));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) r.b[n][i] = on ? __ldg(at + i) : make_uint4(0, 0, 0, 0);
+    }
+}
 
 // The queries of rows row0 .. row0 + 8 NT - 1, each scaled by a power of two to largest magnitude
 // 2^9 .. 2^10, which keeps a bf16 value exact unless it is 2^-24 of the row's largest.
-template <int D, int NT, bool PREC>
-__device__ __forceinline__ void load_tile(Tile<D, NT, PREC>& t, const AttnParams& p, int b, int h, int row0,
-                                          const Seq& s, int lane) {
+template <int D, int NT, bool E4M3, bool PREC>
+__device__ __forceinline__ void load_tile(Tile<D, NT, PREC>& t, RawQ<D, NT>& raw, const AttnParams& p, int b, int h,
+                                          int row0, const Seq& s, int lane) {
     const int g = lane >> 2, c = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int row = row0 + 8 * n + g;
         const bool on = row < s.n * p.G;
-        const int tok = on ? row / p.G : 0, head = h * p.G + (on ? row % p.G : 0);
-        const long long at = ((long long)b * p.c.T + tok) * p.ld_q + (long long)head * D;
-        float x[D / 4], top = 0.f;
+        float (&x)[D / 4] = raw.x;
+        if (p.io == DR_F32) {
+            const float4* at = reinterpret_cast<const float4*>(static_cast<const float*>(p.q) +
+                                                               (on ? q_at(p, b, h, row, s, D, c) : 0));
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i)
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                x[16 * i + j] = on ? load_q(p, at + c * (D / 4) + 16 * i + j) : 0.f;
-                top = fmaxf(top, fabsf(x[16 * i + j]));
+            for (int i = 0; i < D / 16; ++i) {
+                const float4 u = on ? __ldg(at + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+                x[4 * i] = u.x; x[4 * i + 1] = u.y; x[4 * i + 2] = u.z; x[4 * i + 3] = u.w;
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                const uint32_t w[4] = {raw.b[n][i].x, raw.b[n][i].y, raw.b[n][i].z, raw.b[n][i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                    x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                }
+            }
+        }
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         int e = 0;
         if (top > 0.f && top < INFINITY) frexpf(top, &e), e -= 10;
-        const float up = ldexpf(1.f, -max(-100, min(100, e)));
-        const float rest = ldexpf(1.f, -e + max(-100, min(100, e)));
+        const int e1 = max(-100, min(100, e));  // 2^-e as a product of two powers in range
+        const float up = pow2i(-(float)e1), rest = pow2i((float)(e1 - e));
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i)
+        for (int w = 0; w < D / 16; ++w)
 #pragma unroll
-            for (int w = 0; w < 4; ++w)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float a = x[16 * i + 4 * w + 2 * r] * up * rest;
-                    const float d = x[16 * i + 4 * w + 2 * r + 1] * up * rest;
-                    const uint32_t hi = pack_half(a, d);
-                    t.q[n][4 * i + w][r] = hi;
-                    if constexpr (PREC) {
-                        const float2 f = unpack_half(hi);
-                        // an infinity or NaN stays in the first term
-                        t.ql[n][4 * i + w][r] = pack_half(isfinite(f.x) ? a - f.x : 0.f,
-                                                          isfinite(f.y) ? d - f.y : 0.f);
-                    }
+            for (int r = 0; r < 2; ++r) {
+                // the channels of the pairs that codes_to_half makes
+                const float a = x[4 * w + (E4M3 ? 2 * r : r)] * up * rest;
+                const float d = x[4 * w + (E4M3 ? 2 * r + 1 : r + 2)] * up * rest;
+                const uint32_t hi = pack_half(a, d);
+                t.q[n][w][r] = hi;
+                if constexpr (PREC) {
+                    const float2 f = unpack_half(hi);
+                    // an infinity or NaN stays in the first term
+                    t.ql[n][w][r] = pack_half(isfinite(f.x) ? a - f.x : 0.f, isfinite(f.y) ? d - f.y : 0.f);
                 }
+            }
         // factors and positions belong to rows 2c, 2c + 1: held by the lanes with g = 2c, 2c + 1
         const float f = ldexpf(p.scale * 1.44269504088896340736f, e);
-        const int ps = on ? s.len + tok : -1;
+        const int ps = on ? s.len + row / p.G : -1;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             t.qs[n][j] = __shfl_sync(0xffffffffu, f, (2 * c + j) * 4);
             t.pos[n][j] = __shfl_sync(0xffffffffu, ps, (2 * c + j) * 4);
+            t.l[n][j] = t.f[n][j] = 0.f;
+            t.m[n][j] = t.M[n][j] = kNegInf;
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) { t.l[n][j] = 0.f; t.m[n][j] = t.M[n][j] = kNegInf; }
 #pragma unroll
         for (int j = 0; j < D / 16; ++j)
 #pragma unroll
@@ -281,71 +317,82 @@ __device__ __forceinline__ void load_tile(Tile<D, NT, PREC>& t, const AttnParams
     }
 }
 
-// One step: 16 positions from `first` on.
+// One step: 32 positions from `first` on, as two halves of 16 with their pages' scales.
+// Positions from `end` on hold no value (edge).  `same`: both halves lie in one page.
 template <int D, int NT, bool E4M3, bool PREC>
-__device__ __forceinline__ void step(Tile<D, NT, PREC>& t, Codes<D>& f, const AttnParams& p, const Seq& s,
-                                     int first, int end, float ks, float vs, float ve, bool edge, int lane) {
+__device__ __forceinline__ void step(Tile<D, NT, PREC>& t, const uint8_t* slot, const AttnParams& p, int first,
+                                     int end, const Meta& m0, const Meta& m1, bool same, bool edge, int lane) {
     const int g = lane >> 2, c = lane & 3;
-    float sc[NT][4];
+    float sc[NT][2][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = sc[n][2] = sc[n][3] = 0.f;
+    for (int hf = 0; hf < 2; ++hf) {
+        uint32_t k[2][D / 16];
+        load_keys<D>(k, slot + hf * 16 * D, lane);
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j) {
-        uint32_t a0, a1, a2, a3;
-        codes_to_half<E4M3>(f.k[0][j], a0, a2);
-        codes_to_half<E4M3>(f.k[1][j], a1, a3);
+        for (int n = 0; n < NT; ++n) sc[n][hf][0] = sc[n][hf][1] = sc[n][hf][2] = sc[n][hf][3] = 0.f;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            mma(sc[n], a0, a1, a2, a3, t.q[n][j][0], t.q[n][j][1]);
-            if constexpr (PREC) mma(sc[n], a0, a1, a2, a3, t.ql[n][j][0], t.ql[n][j][1]);
+        for (int j = 0; j < D / 16; ++j) {
+            uint32_t a0, a1, a2, a3;
+            codes_to_half<E4M3>(k[0][j], a0, a2);
+            codes_to_half<E4M3>(k[1][j], a1, a3);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma(sc[n][hf], a0, a1, a2, a3, t.q[n][j][0], t.q[n][j][1]);
+                if constexpr (PREC) mma(sc[n][hf], a0, a1, a2, a3, t.ql[n][j][0], t.ql[n][j][1]);
+            }
         }
     }
-    if (edge) {
-        // codes from position `end` on may be anything: as values they count as zero
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            if (first + 2 * c + (r & 1) + 8 * (r >> 1) >= end) {
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) f.v[r][i] = 0;
-            }
-    }
-    uint32_t pb[NT][2], pl[NT][2];
+    uint32_t pb[NT][2][2], pl[NT][2][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        float top[2];
+        float top[2], topv[2];  // largest s; largest whole number s + log2 vs
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float k = t.qs[n][j] * ks;
-            sc[n][j] *= k;
-            sc[n][2 + j] *= k;
+            const float k0 = t.qs[n][j] * m0.ks, k1 = t.qs[n][j] * m1.ks;
+            sc[n][0][j] *= k0;
+            sc[n][0][2 + j] *= k0;
+            sc[n][1][j] *= k1;
+            sc[n][1][2 + j] *= k1;
             if (edge) {
-                const int back0 = t.pos[n][j] - (first + g), back1 = back0 - 8;
-                if (back0 < 0 || (p.window > 0 && back0 >= p.window)) sc[n][j] = kNegInf;
-                if (back1 < 0 || (p.window > 0 && back1 >= p.window)) sc[n][2 + j] = kNegInf;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {  // positions first + g + 8 i
+                    const int back = t.pos[n][j] - (first + g + 8 * i);
+                    if (back < 0 || (p.window > 0 && back >= p.window)) sc[n][i >> 1][2 * (i & 1) + j] = kNegInf;
+                }
             }
-            top[j] = fmaxf(sc[n][j], sc[n][2 + j]);
+            const float h0 = fmaxf(sc[n][0][j], sc[n][0][2 + j]), h1 = fmaxf(sc[n][1][j], sc[n][1][2 + j]);
+            top[j] = fmaxf(h0, h1);
+            topv[j] = fmaxf(ceilf(h0) + m0.ve, ceilf(h1) + m1.ve);
         }
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) {
             top[0] = fmaxf(top[0], __shfl_xor_sync(0xffffffffu, top[0], o));
             top[1] = fmaxf(top[1], __shfl_xor_sync(0xffffffffu, top[1], o));
         }
-        float mref[2], fac[2], oscale[2];
-        bool grew = false;
+        if (same) {
+            const float ve = fmaxf(m0.ve, m1.ve);  // a half that no row sees has none
+            topv[0] = ceilf(top[0]) + ve;
+            topv[1] = ceilf(top[1]) + ve;
+        } else {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float up = ceilf(top[j]);
-            const float m = fmaxf(t.m[n][j], up), M = fmaxf(t.M[n][j], up + ve);
-            grew |= M > t.M[n][j];
-            t.l[n][j] *= pow2i(t.m[n][j] - m);
-            oscale[j] = pow2i(t.M[n][j] - M);
-            t.m[n][j] = m;
-            t.M[n][j] = M;
-            mref[j] = m == kNegInf ? 0.f : m;
-            // held inside the range of fp32 where a far larger value scale is past
-            fac[j] = vs * pow2i(fminf(m - M + kBias, 126.f));
+            for (int o = 4; o < 32; o <<= 1) {
+                topv[0] = fmaxf(topv[0], __shfl_xor_sync(0xffffffffu, topv[0], o));
+                topv[1] = fmaxf(topv[1], __shfl_xor_sync(0xffffffffu, topv[1], o));
+            }
         }
+        const bool grew = top[0] > t.m[n][0] || top[1] > t.m[n][1] || topv[0] > t.M[n][0] || topv[1] > t.M[n][1];
         if (__any_sync(0xffffffffu, grew)) {
+            float oscale[2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float m = fmaxf(t.m[n][j], ceilf(top[j])), M = fmaxf(t.M[n][j], topv[j]);
+                t.l[n][j] *= pow2i(t.m[n][j] - m);
+                oscale[j] = pow2i(t.M[n][j] - M);
+                t.m[n][j] = m;
+                t.M[n][j] = M;
+                // held inside the range of fp32 where a far larger value scale is past
+                t.f[n][j] = pow2i(fminf(m - M + kBias, 126.f));
+            }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 t.o[n][i][0] *= oscale[0];
@@ -354,41 +401,70 @@ __device__ __forceinline__ void step(Tile<D, NT, PREC>& t, Codes<D>& f, const At
                 t.o[n][i][3] *= oscale[1];
             }
         }
-        float w[4];
+        float w[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float e = ex2(sc[n][i] - mref[i & 1]);
-            t.l[n][i & 1] += e;
-            // a hidden position weighs nothing even where the page's value scale is NaN
-            w[i] = sc[n][i] == kNegInf ? 0.f : e * fac[i & 1];
-        }
+        for (int j = 0; j < 2; ++j) {
+            const float mref = t.m[n][j] == kNegInf ? 0.f : t.m[n][j];
+            const float f0 = t.f[n][j] * m0.vs, f1 = t.f[n][j] * m1.vs;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint32_t hi = pack_half(w[2 * r], w[2 * r + 1]);
-            pb[n][r] = transpose8x8(hi);
-            if constexpr (PREC) {
-                const float2 x = unpack_half(hi);
-                pl[n][r] = transpose8x8(pack_half(w[2 * r] - x.x, w[2 * r + 1] - x.y));
+            for (int i = 0; i < 2; ++i) {
+                const float e0 = ex2(sc[n][0][2 * i + j] - mref), e1 = ex2(sc[n][1][2 * i + j] - mref);
+                t.l[n][j] += e0 + e1;
+                w[0][2 * i + j] = e0 * f0;
+                w[1][2 * i + j] = e1 * f1;
             }
         }
+        if (edge) {  // a hidden position weighs nothing even where the page's value scale is NaN
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (sc[n][0][i] == kNegInf) w[0][i] = 0.f;
+                if (sc[n][1][i] == kNegInf) w[1][i] = 0.f;
+            }
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t hi = pack_half(w[hf][2 * r], w[hf][2 * r + 1]);
+                pb[n][hf][r] = transpose8x8(hi);
+                if constexpr (PREC) {
+                    const float2 x = unpack_half(hi);
+                    pl[n][hf][r] = transpose8x8(pack_half(w[hf][2 * r] - x.x, w[hf][2 * r + 1] - x.y));
+                }
+            }
     }
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
-        uint32_t a[2][4];  // channels 4j, 4j + 1 and 4j + 2, 4j + 3 of the thread's D / 8
+    for (int hf = 0; hf < 2; ++hf) {
+        uint32_t v[4][D / 32];
+        load_values<D>(v, slot + (2 + hf) * 16 * D, lane);
+        if (edge) {
+            // what lies in the ring there may be anything: as values it counts as zero
+            const bool none = (hf ? m1.id : m0.id) < 0;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const uint32_t x = f.v[2 * r][j], y = f.v[2 * r + 1][j];
-            codes_to_half<E4M3>(prmt(x, y, 0x5140), a[0][2 * r], a[0][2 * r + 1]);
-            codes_to_half<E4M3>(prmt(x, y, 0x7362), a[1][2 * r], a[1][2 * r + 1]);
+            for (int r = 0; r < 4; ++r)
+                if (none || first + 16 * hf + 2 * c + (r & 1) + 8 * (r >> 1) >= end) {
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) v[r][i] = 0;
+                }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < D / 32; ++j) {
+            uint32_t a[2][4];  // channels 4j, 4j + 1 and 4j + 2, 4j + 3 of the thread's D / 8
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                mma(t.o[n][2 * j + i], a[i][0], a[i][1], a[i][2], a[i][3], pb[n][0], pb[n][1]);
-                if constexpr (PREC)
-                    mma(t.o[n][2 * j + i], a[i][0], a[i][1], a[i][2], a[i][3], pl[n][0], pl[n][1]);
+            for (int r = 0; r < 2; ++r) {
+                const uint32_t x = v[2 * r][j], y = v[2 * r + 1][j];
+                codes_to_half<E4M3>(pair_up<E4M3, false>(x, y), a[0][2 * r], a[0][2 * r + 1]);
+                codes_to_half<E4M3>(pair_up<E4M3, true>(x, y), a[1][2 * r], a[1][2 * r + 1]);
             }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    mma(t.o[n][2 * j + i], a[i][0], a[i][1], a[i][2], a[i][3], pb[n][hf][0], pb[n][hf][1]);
+                    if constexpr (PREC)
+                        mma(t.o[n][2 * j + i], a[i][0], a[i][1], a[i][2], a[i][3], pl[n][hf][0], pl[n][hf][1]);
+                }
+        }
     }
 }
 
@@ -410,26 +486,32 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int b, int h, int
     if (ch == 0 && p.lse) p.lse[at] = (m + log2f(l)) * 0.69314718055994530942f;
 }
 
-constexpr int kRing = 4;  // stages of a warp's ring
-template <int D> __host__ __device__ constexpr int ring_bytes() { return kRing * 2 * 16 * D; }
+constexpr int kRing = 2;  // steps of a warp's ring
+template <int D> __host__ __device__ constexpr int ring_bytes() { return kRing * 2 * kStep * D; }
+constexpr int kMetas = 64;  // of 16 positions each, a power of two
 // The rows of the warps, when they are joined, take the place of the rings.
 template <int D, int NT> struct Joined {
     float o[kWarps][8 * NT][D + 4];
     float l[kWarps][8 * NT], m[kWarps][8 * NT], M[kWarps][8 * NT];
 };
-template <int D, int NT> __host__ __device__ constexpr int smem_bytes() {
+template <int D, int NT> __host__ __device__ constexpr int rows_or_rings() {
     return kWarps * ring_bytes<D>() > (int)sizeof(Joined<D, NT>) ? kWarps * ring_bytes<D>()
                                                                  : (int)sizeof(Joined<D, NT>);
 }
+template <int D, int NT> __host__ __device__ constexpr int smem_bytes() {
+    return rows_or_rings<D, NT>() + kWarps * kMetas * (int)sizeof(Meta);
+}
 
 template <int D, int NT, bool E4M3, bool PREC>
-__global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 3 : 2) cache_attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 6 : 4) cache_attn_kernel(const AttnParams p) {
     constexpr int ROWS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     Joined<D, NT>& joined = *reinterpret_cast<Joined<D, NT>*>(smem);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, c = lane & 3;
     uint8_t* ring = smem + warp * ring_bytes<D>();
     const uint32_t ring32 = (uint32_t)__cvta_generic_to_shared(ring);
+    Meta* metas = reinterpret_cast<Meta*>(smem + rows_or_rings<D, NT>()) + warp * kMetas;
+    const bool same = p.c.page > 16;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const long long total = line_length<ROWS>(p, lane);
@@ -439,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 3 : 2) cache_attn
     const long long end = share(total, blockIdx.x + 1, used);
     long long at = begin, seq_begin;
     int b = find_seq<ROWS>(p, lane, at, seq_begin);
+    bool first_part = true;  // of the block: the part that may continue another block's
     while (at < end) {
         Seq s = make_seq<ROWS>(p, b);
         while (work_of(p, s) == 0 || at >= seq_begin + work_of(p, s)) {
@@ -448,22 +531,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 3 : 2) cache_attn
         }
         // stretches of one sequence: head by head, tile by tile, stage by stage
         const long long in = at - seq_begin;
-        const int unit = (int)(in / s.stages), from = (int)(in - (long long)unit * s.stages);
+        const int cost = s.stages + kOver, unit = (int)(in / cost), place = (int)(in - (long long)unit * cost);
         const int h = unit / s.tiles, row0 = (unit % s.tiles) * ROWS;
-        const int upto = (int)min((long long)s.stages, from + (end - at));
+        const int span = (int)min((long long)cost - place, end - at);  // of the line
+        const int from = max(0, place - kOver), upto = place + span - kOver;
+        if (upto <= from) {  // the tile's start alone
+            at += span;
+            continue;
+        }
         // positions that the tile's rows see
         const int t0 = row0 / p.G, t1 = min(s.n - 1, (row0 + ROWS - 1) / p.G);
         const int hi = s.len + t1 + 1, lo = p.window > 0 ? max(0, s.len + t0 - p.window + 1) : 0;
         // positions that every row sees need no mask
         const int all_hi = s.len + t0 + 1, all_lo = p.window > 0 ? max(0, s.len + t1 - p.window + 1) : 0;
 
-        auto meta = [&](int st) {
+        // Step k = 0 .. n - 1 of the stretch is its stage from + k; the meta of its halves are entries 2k
+        // and 2k + 1 modulo kMetas.  A batch of 32 entries is written while the one before is in use.
+        const int n = upto - from, base = (s.s0 + from) * kStage + kStep * warp;
+        auto fill_metas = [&](int entry) {
             Meta x;
             x.id = -2;
             x.ks = x.vs = 0.f;
             x.ve = kNegInf;
-            const int first = (s.s0 + st) * kStage + 16 * warp;
-            if (st < upto && first < hi && first + 16 > lo) {
+            const int first = base + (entry >> 1) * kStage + (entry & 1) * 16;
+            if (entry < 2 * n && first < hi && first + 16 > lo) {
                 x.id = cache_page(p.c, b, first / p.c.page);
                 if (x.id >= 0) {
                     const size_t ph = (size_t)x.id * p.c.H + h;
@@ -478,47 +569,47 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 3 : 2) cache_attn
                     x.ve = 0.f;
                 }
             }
-            return x;
+            metas[entry & (kMetas - 1)] = x;
         };
-        // Step k = 0 .. n - 1 of the stretch; lane k % 32 of batch k / 32 has its meta, in `now` or
-        // `next` by the batch's parity.  The copies run kRing - 1 < 32 steps ahead.
-        const int n = upto - from;
-        Meta now = meta(from + lane), next = meta(from + 32 + lane);
         auto fetch = [&](int k) {
-            const int id = __shfl_sync(0xffffffffu, k & 32 ? next.id : now.id, k & 31);
-            if (k < n && id >= 0) {
-                const int first = (s.s0 + from + k) * kStage + 16 * warp;
-                const size_t off = (((size_t)id * p.c.H + h) * p.c.page + first % p.c.page) * D;
-                const uint32_t slot = ring32 + (k % kRing) * 32 * D;
-                copy_codes<D>(slot, p.c.k + off, lane);
-                copy_codes<D>(slot + 16 * D, p.c.v + off, lane);
+            if (k < n) {
+                const uint32_t slot = ring32 + (k % kRing) * 2 * kStep * D;
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int id = metas[(2 * k + hf) & (kMetas - 1)].id;
+                    if (id < 0) continue;
+                    const int first = base + k * kStage + 16 * hf;
+                    const size_t off = (((size_t)id * p.c.H + h) * p.c.page + (first & (p.c.page - 1))) * D;
+                    copy_codes<D>(slot + hf * 16 * D, p.c.k + off, lane);
+                    copy_codes<D>(slot + (2 + hf) * 16 * D, p.c.v + off, lane);
+                }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        RawQ<D, NT> raw;
+        fetch_q<D, NT>(raw, p, b, h, row0, s, lane);
+        fill_metas(lane);
+        __syncwarp();
 #pragma unroll
         for (int k = 0; k < kRing - 1; ++k) fetch(k);
+        fill_metas(32 + lane);
         Tile<D, NT, PREC> t;
-        load_tile(t, p, b, h, row0, s, lane);
+        load_tile<D, NT, E4M3, PREC>(t, raw, p, b, h, row0, s, lane);
         for (int k = 0; k < n; ++k) {
-            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
-            __syncwarp();  // every lane's copies of step k are there, and step k - 1 is read
+            __syncwarp();  // step k - 1 is read
             fetch(k + kRing - 1);
-            const bool second = k & 32;
-            const int id = __shfl_sync(0xffffffffu, second ? next.id : now.id, k & 31);
-            const float ks = __shfl_sync(0xffffffffu, second ? next.ks : now.ks, k & 31);
-            const float vs = __shfl_sync(0xffffffffu, second ? next.vs : now.vs, k & 31);
-            const float ve = __shfl_sync(0xffffffffu, second ? next.ve : now.ve, k & 31);
-            if (id != -2) {
-                const int first = (s.s0 + from + k) * kStage + 16 * warp;
-                const bool edge = first + 16 > all_hi || first < all_lo || id < 0;
-                const uint8_t* slot = ring + (k % kRing) * 32 * D;
-                Codes<D> f;
-                load_codes<D>(f, slot, slot + 16 * D, lane);
-                step<D, NT, E4M3, PREC>(t, f, p, s, first, id < 0 ? 0 : s.len + s.n, ks, vs, ve, edge, lane);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+            __syncwarp();  // every lane's copies of step k are there
+            const Meta m0 = metas[(2 * k) & (kMetas - 1)], m1 = metas[(2 * k + 1) & (kMetas - 1)];
+            if (m0.id != -2 || m1.id != -2) {
+                const int first = base + k * kStage;
+                const bool edge = first + kStep > all_hi || first < all_lo || m0.id < 0 || m1.id < 0;
+                step<D, NT, E4M3, PREC>(t, ring + (k % kRing) * 2 * kStep * D, p, first, s.len + s.n, m0, m1, same,
+                                        edge, lane);
             }
-            if ((k & 31) == 31) {  // the batch is used up: the one after next takes its place
-                const Meta m2 = meta(from + k + 1 + 32 + lane);
-                if (second) next = m2; else now = m2;
+            if ((k & 15) == 15) {  // entries 2k - 30 .. 2k + 1 are used up
+                __syncwarp();
+                fill_metas(2 * k + 34 + lane);
             }
         }
 
@@ -545,8 +636,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 3 : 2) cache_attn
                         make_float2(t.o[n8][i][j], t.o[n8][i][2 + j]);
             }
         __syncthreads();
-        const bool whole = from == 0 && upto == s.stages;
-        float* out = p.part + ((size_t)blockIdx.x * 2 + (at == begin ? 0 : 1)) * tile_floats(D, ROWS);
+        const bool whole = n == s.stages;
+        float* out = p.part + ((size_t)blockIdx.x * 2 + (first_part ? 0 : 1)) * tile_floats(D, ROWS);
+        first_part = false;
         for (int i = threadIdx.x; i < ROWS * D; i += kThreads) {
             const int r = i / D, ch = i % D, row = row0 + r;
             if (row >= s.n * p.G) break;
@@ -572,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 3 : 2) cache_attn
             }
         }
         __syncthreads();  // the rings are filled again
-        at += n;
+        at += span;
     }
 }
 
@@ -580,25 +672,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 3 : 2) cache_attn
 // here, so that its end also means the end of the first.
 __device__ __forceinline__ void wait_for_parts() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Joins the parts of a tile that several blocks worked on.  Block x: the tile; y: 8 of its rows, a
-// warp each.  Rows of no query get zeros (behind a sequence's tokens) or NaN (a sequence out of range).
+// Joins the parts of a tile that several blocks worked on.  Block x: the tile, y: its row.  Rows of
+// no query get zeros (behind a sequence's tokens) or NaN (a sequence out of range).
+constexpr int kJoinWarps = 8;
 template <int D, int NT>
-__global__ void __launch_bounds__(256) cache_attn_join_kernel(const AttnParams p, int blocks, int max_tiles) {
+__global__ void __launch_bounds__(32 * kJoinWarps) cache_attn_join_kernel(const AttnParams p, int blocks,
+                                                                          int max_tiles) {
     constexpr int ROWS = 8 * NT, V = D / 32;
+    __shared__ float sums[kJoinWarps][D], ls[kJoinWarps], ms[kJoinWarps], Ms[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.x / (p.c.H * max_tiles), rest = blockIdx.x % (p.c.H * max_tiles);
     const int h = rest / max_tiles, tile = rest % max_tiles;
-    const int r = blockIdx.y * 8 + warp, row = tile * ROWS + r;
+    const int r = blockIdx.y, row = tile * ROWS + r;
     const Seq s = make_seq<ROWS>(p, b);
     if (row >= s.n * p.G) {
         int len, n;
         const bool ok = cache_seq(p.c, b, len, n);
-        if (!ok && lane == 0) flag_index_error(p.c);
+        if (!ok && threadIdx.x == 0) flag_index_error(p.c);
         if (row < p.c.T * p.G) {
             const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
             const float bad = __uint_as_float(0x7fc00000u);
-            for (int ch = lane; ch < D; ch += 32) st_any(p.o, at * D + ch, p.out, ok ? 0.f : bad);
-            if (lane == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
+            if (threadIdx.x < D) st_any(p.o, at * D + threadIdx.x, p.out, ok ? 0.f : bad);
+            if (threadIdx.x == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
         }
         wait_for_parts();
         return;
@@ -614,16 +709,17 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const AttnParams p
         total += __shfl_xor_sync(0xffffffffu, total, o);
         before += __shfl_xor_sync(0xffffffffu, before, o);
     }
-    const long long a = before + ((long long)h * s.tiles + tile) * s.stages;
+    // the tile's stages on the line, and the blocks that hold them
+    const long long a = before + ((long long)h * s.tiles + tile) * (s.stages + kOver) + kOver;
     const int used = blocks_used(total, blocks);
     const int first = holder(total, a, used), last = holder(total, a + s.stages - 1, used);
     wait_for_parts();
     if (first == last) return;  // finished by its block
-    // a block that began before the tile holds it as its second part
-    const float* head = p.part + ((size_t)first * 2 + (share(total, first, used) >= a ? 0 : 1)) * tile_floats(D, ROWS);
-    // lane i looks at parts i, i + 32, ..: the references, then the sums in the order of the parts
+    // the tile is the first part of a block with stages of it that begins in it or in its start
+    const float* head = p.part + ((size_t)first * 2 + (share(total, first, used) >= a - kOver ? 0 : 1)) * tile_floats(D, ROWS);
+    // warp w takes parts w, w + 8, ..: the references first, then the sums in the order of the parts
     float m = kNegInf, M = kNegInf;
-    for (int i = first + lane; i <= last; i += 32) {
+    for (int i = first + threadIdx.x; i <= last; i += 32 * kJoinWarps) {
         const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, ROWS);
         m = fmaxf(m, in[ROWS * D + ROWS + r]);
         M = fmaxf(M, in[ROWS * D + 2 * ROWS + r]);
@@ -633,9 +729,13 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const AttnParams p
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     }
+    if (lane == 0) { ms[warp] = m; Ms[warp] = M; }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kJoinWarps; ++i) { m = fmaxf(m, ms[i]); M = fmaxf(M, Ms[i]); }
     float l = 0.f, sum[V] = {};
 #pragma unroll 4
-    for (int i = first; i <= last; ++i) {
+    for (int i = first + warp; i <= last; i += kJoinWarps) {
         const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, ROWS);
         const float pl = in[ROWS * D + r], fl = pow2i(in[ROWS * D + ROWS + r] - m);
         const float fs = pow2i(in[ROWS * D + 2 * ROWS + r] - M);
@@ -647,7 +747,15 @@ __global__ void __launch_bounds__(256) cache_attn_join_kernel(const AttnParams p
         }
     }
 #pragma unroll
-    for (int j = 0; j < V; ++j) write_row(p, b, h, row, 32 * j + lane, D, sum[j], l, m, M);
+    for (int j = 0; j < V; ++j) sums[warp][32 * j + lane] = sum[j];
+    if (lane == 0) ls[warp] = l;
+    __syncthreads();
+    if (threadIdx.x < D) {
+        float x = 0.f, tot = 0.f;
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) { x += sums[i][threadIdx.x]; tot += ls[i]; }
+        write_row(p, b, h, row, threadIdx.x, D, x, tot, m, M);
+    }
 }
 
 template <typename K>
@@ -680,8 +788,8 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.c.B * p.c.H * max_tiles, NT);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)p.c.B * p.c.H * max_tiles, 8 * NT);
+    cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = st;
     cfg.attrs = &early;
     cfg.numAttrs = 1;
