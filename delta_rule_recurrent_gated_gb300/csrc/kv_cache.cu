@@ -5,6 +5,8 @@
 // magnitude of the new values, joins it with the scale of what the page already holds, rounds
 // the new values to codes and, where the scale grew, the earlier codes again.  No other block
 // touches that page and head, so nothing is exchanged between blocks.
+#include <type_traits>
+
 #include <cuda_fp8.h>
 
 #include "kv_cache.cuh"
@@ -12,9 +14,6 @@
 
 namespace dr {
 namespace {
-
-constexpr int kWriteThreads = 128;
-constexpr int kReadThreads = 256;
 
 template <bool E4M3> __device__ __forceinline__ float inv_code_max() {
     return E4M3 ? 1.f / 448.f : 1.f / 127.f;
@@ -33,20 +32,6 @@ template <bool E4M3> __device__ __forceinline__ float from_code(uint32_t byte) {
     return (float)(int8_t)byte;
 }
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        x[2 * j] = __uint_as_float(w[j] << 16);
-        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&y)[8]) {
     uint32_t w[4];
 #pragma unroll
@@ -61,12 +46,56 @@ __device__ __forceinline__ void store8(float* p, const float (&y)[8]) {
     reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
 }
 
-// Block x: sequence and its i-th touched page; y: head; z: keys or values.
-template <typename IN, bool E4M3>
-__global__ void __launch_bounds__(kWriteThreads)
+// x / s, correctly rounded, for many x and one s: with y the correctly rounded 1 / s and q within a
+// unit of the quotient, q + (x - q s) y is the rounded quotient (P. Markstein, IBM J. Res. Dev. 34,
+// 1990); a first such step brings x y to within a unit.  A remainder that underflows belongs to a
+// quotient below 2^-20, whose code is zero whatever its last bits are; scales outside
+// 1e-18 .. 1e18 take the division itself.  A zero keeps its sign.
+struct Divisor {
+    float s, y;
+    bool plain;
+    __device__ __forceinline__ explicit Divisor(float d) : s(d), y(1.f / d), plain(!(d > 1e-18f && d < 1e18f)) {}
+    __device__ __forceinline__ float operator()(float x) const {
+        if (plain) return x / s;
+        float q = x * y;
+        if (q == 0.f) return q;
+        q = fmaf(fmaf(-q, s, x), y, q);
+        return fmaf(fmaf(-q, s, x), y, q);
+    }
+};
+
+template <typename T> struct Vec8;  // 8 values as loaded
+template <> struct Vec8<__nv_bfloat16> {
+    uint4 u;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x[2 * j] = __uint_as_float(w[j] << 16);
+            x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+    }
+};
+template <> struct Vec8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = reinterpret_cast<const float4*>(p)[0];
+        b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+        x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+};
+
+// Block x: sequence and its i-th touched page; y: head; z: keys or values.  A page is 128 to 2048
+// pieces of 8 values, NV of them a thread.  The new values are read once, into registers: 8 prompts of up to 4096 tokens (4 heads of 128, bf16) take 75 MB of traffic.
+template <typename IN, bool E4M3, int THREADS, int NV>
+__global__ void __launch_bounds__(THREADS)
     cache_write_kernel(const CacheParams c, const IN* __restrict__ k, long long ld_k,
                        const IN* __restrict__ v, long long ld_v, int pages_per_seq) {
-    __shared__ uint32_t red[kWriteThreads / 32];
+    __shared__ uint32_t red[THREADS / 32];
     const int b = blockIdx.x / pages_per_seq, i = blockIdx.x % pages_per_seq, h = blockIdx.y;
     const bool keys = blockIdx.z == 0;
     int len, n;
@@ -79,132 +108,178 @@ __global__ void __launch_bounds__(kWriteThreads)
     const int lo = i == 0 ? len - (int)first : 0;    // rows lo .. hi - 1 of the page are new
     const int hi = (int)min((long long)c.page, (long long)len + n - first);
     if (lo >= hi) return;
+    const int shift = c.d == 128 ? 4 : 3;  // pieces of a row: 16 or 8
+    const int from = lo << shift, to = hi << shift;
+    const long long ld = keys ? ld_k : ld_v;
+    // row r of the page is token first + r - len
+    const IN* src = (keys ? k : v) + ((long long)b * c.T + (first - len)) * ld + (long long)h * c.d;
+    Vec8<IN> x[NV];
+#pragma unroll
+    for (int e = 0; e < NV; ++e) {
+        const int j = e * THREADS + threadIdx.x;
+        if (j >= from && j < to) x[e].load(src + (j >> shift) * ld + (j & ((1 << shift) - 1)) * 8);
+    }
     const int id = cache_page(c, b, index);
     if (id < 0) {
         if (threadIdx.x == 0) flag_index_error(c);
         return;
     }
-    const int vecs = c.d / 8;  // 8-value pieces of a row
     const size_t ph = (size_t)id * c.H + h;
     uint8_t* codes = (keys ? c.k : c.v) + ph * c.page * c.d;
     float* scale = (keys ? c.k_scale : c.v_scale) + ph;
-    const long long ld = keys ? ld_k : ld_v;
-    // row r of the page is token first + r - len
-    const IN* src = (keys ? k : v) + ((long long)b * c.T + (first - len)) * ld + (long long)h * c.d;
+    const float s_old = lo > 0 ? *scale : 0.f;
 
     // largest magnitude, as bits: what is not finite is at least 0x7f800000
     uint32_t top = 0;
-    for (int j = lo * vecs + threadIdx.x; j < hi * vecs; j += kWriteThreads) {
-        float x[8];
-        load8(src + (long long)(j / vecs) * ld + (j % vecs) * 8, x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+    for (int e = 0; e < NV; ++e) {
+        const int j = e * THREADS + threadIdx.x;
+        if (j >= from && j < to) {
+            float y[8];
+            x[e].get(y);
+#pragma unroll
+            for (int m = 0; m < 8; ++m) top = max(top, __float_as_uint(y[m]) & 0x7fffffffu);
+        }
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
-    const float s_old = lo > 0 ? *scale : 0.f;
     __syncthreads();  // every thread has read the scale too
 #pragma unroll
-    for (int w = 0; w < kWriteThreads / 32; ++w) top = max(top, red[w]);
+    for (int w = 0; w < THREADS / 32; ++w) top = max(top, red[w]);
     const bool finite = top < 0x7f800000u && s_old < __uint_as_float(0x7f800000u);
     const float s = finite ? fmaxf(s_old, __uint_as_float(top) * inv_code_max<E4M3>())
                            : __uint_as_float(0x7fc00000u);
     if (threadIdx.x == 0) *scale = s;
 
-    for (int j = lo * vecs + threadIdx.x; j < hi * vecs; j += kWriteThreads) {
-        float x[8];
-        load8(src + (long long)(j / vecs) * ld + (j % vecs) * 8, x);
-        uint32_t w[2] = {0, 0};
-        if (s > 0.f) {
+    const Divisor over(s);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e >> 2] |= to_code<E4M3>(x[e] / s) << (8 * (e & 3));
+    for (int e = 0; e < NV; ++e) {
+        const int j = e * THREADS + threadIdx.x;
+        if (j >= from && j < to) {
+            float y[8];
+            x[e].get(y);
+            uint32_t w[2] = {0, 0};
+            if (s > 0.f) {
+#pragma unroll
+                for (int m = 0; m < 8; ++m) w[m >> 2] |= to_code<E4M3>(over(y[m])) << (8 * (m & 3));
+            }
+            *reinterpret_cast<uint2*>(codes + (size_t)j * 8) = make_uint2(w[0], w[1]);
         }
-        *reinterpret_cast<uint2*>(codes + (size_t)j * 8) = make_uint2(w[0], w[1]);
     }
     if (s > s_old && s_old > 0.f) {  // false for NaN
-        for (int j = threadIdx.x; j < lo * vecs; j += kWriteThreads) {
+        for (int j = threadIdx.x; j < from; j += THREADS) {
             const uint2 u = *reinterpret_cast<const uint2*>(codes + (size_t)j * 8);
             const uint32_t in[2] = {u.x, u.y};
             uint32_t w[2] = {0, 0};
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float was = from_code<E4M3>((in[e >> 2] >> (8 * (e & 3))) & 0xffu);
-                w[e >> 2] |= to_code<E4M3>(__fmul_rn(was, s_old) / s) << (8 * (e & 3));
+            for (int m = 0; m < 8; ++m) {
+                const float was = from_code<E4M3>((in[m >> 2] >> (8 * (m & 3))) & 0xffu);
+                w[m >> 2] |= to_code<E4M3>(over(__fmul_rn(was, s_old))) << (8 * (m & 3));
             }
             *reinterpret_cast<uint2*>(codes + (size_t)j * 8) = make_uint2(w[0], w[1]);
         }
     }
 }
 
-// A thread reads 8 values of one token and head, of keys (y = 0) or values (y = 1).
-template <typename OUT, bool E4M3>
-__global__ void __launch_bounds__(kReadThreads)
-    cache_read_kernel(const CacheParams c, OUT* __restrict__ k, OUT* __restrict__ v) {
-    const bool keys = blockIdx.y == 0;
+// Block x: sequence and its i-th page of the call's positions; y: head; z: keys or values.
+template <typename OUT, bool E4M3, int THREADS, int NV>
+__global__ void __launch_bounds__(THREADS)
+    cache_read_kernel(const CacheParams c, OUT* __restrict__ k, OUT* __restrict__ v, int pages_per_seq) {
+    const int b = blockIdx.x / pages_per_seq, i = blockIdx.x % pages_per_seq, h = blockIdx.y;
+    const bool keys = blockIdx.z == 0;
     OUT* out = keys ? k : v;
     if (!out) return;
-    const int vecs = c.d / 8;
-    const long long total = (long long)c.B * c.T * c.H * vecs;
-    for (long long j = (long long)blockIdx.x * kReadThreads + threadIdx.x; j < total;
-         j += (long long)gridDim.x * kReadThreads) {
-        const int piece = (int)(j % vecs);
-        const long long row = j / vecs;
-        const int h = (int)(row % c.H);
-        const long long tok = row / c.H;
-        const int b = (int)(tok / c.T), t = (int)(tok % c.T);
-        int len, n;
-        float y[8];
+    int len, n;
+    const bool in = cache_seq(c, b, len, n);
+    if (!in) {
+        if (threadIdx.x == 0) flag_index_error(c);
+        len = n = 0;
+    }
+    const int index = len / c.page + i;
+    const int t0 = i * c.page - len % c.page;  // token of the page's first row
+    if (t0 >= c.T) return;
+    const int lo = max(0, -t0), hi = min(c.page, c.T - t0), full = min(hi, n - t0);  // rows; with a value
+    const int shift = c.d == 128 ? 4 : 3;
+    int id = -1;
+    if (full > lo) {
+        id = cache_page(c, b, index);
+        if (id < 0 && threadIdx.x == 0) flag_index_error(c);
+    }
+    float s = __uint_as_float(0x7fc00000u);
+    const uint8_t* codes = c.k;
+    if (id >= 0) {
+        const size_t ph = (size_t)id * c.H + h;
+        s = (keys ? c.k_scale : c.v_scale)[ph];
+        codes = (keys ? c.k : c.v) + ph * c.page * c.d;
+    }
+    uint2 u[NV];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = 0.f;
-        const bool in = cache_seq(c, b, len, n);
-        int id = -1;
-        if (in && t < n) id = cache_page(c, b, (len + t) / c.page);
-        if (id >= 0) {
-            const size_t ph = (size_t)id * c.H + h;
-            const float s = (keys ? c.k_scale : c.v_scale)[ph];
-            const uint2 u = *reinterpret_cast<const uint2*>(
-                (keys ? c.k : c.v) + (ph * c.page + (len + t) % c.page) * c.d + piece * 8);
-            const uint32_t w[2] = {u.x, u.y};
+    for (int e = 0; e < NV; ++e) {
+        const int j = e * THREADS + threadIdx.x;
+        u[e] = make_uint2(0, 0);
+        if (id >= 0 && j >= lo << shift && j < full << shift)
+            u[e] = *reinterpret_cast<const uint2*>(codes + (size_t)j * 8);
+    }
+    OUT* dst = out + (((long long)b * c.T + t0) * c.H + h) * c.d;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                y[e] = from_code<E4M3>((w[e >> 2] >> (8 * (e & 3))) & 0xffu) * s;
-        } else if (!in || t < n) {
-            flag_index_error(c);
+    for (int e = 0; e < NV; ++e) {
+        const int j = e * THREADS + threadIdx.x, row = j >> shift;
+        if (row >= lo && row < hi) {
+            const bool zero = in && row >= full;
+            const uint32_t w[2] = {u[e].x, u[e].y};
+            float y[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(0x7fc00000u);
+            for (int m = 0; m < 8; ++m)
+                y[m] = zero ? 0.f : from_code<E4M3>((w[m >> 2] >> (8 * (m & 3))) & 0xffu) * s;
+            store8(dst + (long long)row * c.H * c.d + (j & ((1 << shift) - 1)) * 8, y);
         }
-        store8(out + j * 8, y);
     }
 }
 
-template <typename IN>
-cudaError_t write_as(const CacheParams& c, const void* k, long long ld_k, const void* v,
-                     long long ld_v, cudaStream_t st) {
-    const int pages = 1 + (c.page - 2 + c.T) / c.page;  // pages that T tokens can touch
-    const dim3 grid((unsigned)c.B * pages, c.H, 2);
+int pages_of(const CacheParams& c) { return 1 + (c.page - 2 + c.T) / c.page; }  // that T tokens can touch
+
+template <typename IN, bool E4M3, int THREADS, int NV>
+cudaError_t write_page(const CacheParams& c, const void* k, long long ld_k, const void* v, long long ld_v,
+                       cudaStream_t st) {
+    const int pages = pages_of(c);
     TraceScope ts("cache_write", st);
-    if (c.code == DR_CODE_E4M3)
-        cache_write_kernel<IN, true><<<grid, kWriteThreads, 0, st>>>(
-            c, static_cast<const IN*>(k), ld_k, static_cast<const IN*>(v), ld_v, pages);
-    else
-        cache_write_kernel<IN, false><<<grid, kWriteThreads, 0, st>>>(
-            c, static_cast<const IN*>(k), ld_k, static_cast<const IN*>(v), ld_v, pages);
+    cache_write_kernel<IN, E4M3, THREADS, NV><<<dim3((unsigned)c.B * pages, c.H, 2), THREADS, 0, st>>>(
+        c, static_cast<const IN*>(k), ld_k, static_cast<const IN*>(v), ld_v, pages);
+    return cudaGetLastError();
+}
+template <typename OUT, bool E4M3, int THREADS, int NV>
+cudaError_t read_page(const CacheParams& c, void* k, void* v, cudaStream_t st) {
+    const int pages = pages_of(c);
+    TraceScope ts("cache_read", st);
+    cache_read_kernel<OUT, E4M3, THREADS, NV><<<dim3((unsigned)c.B * pages, c.H, 2), THREADS, 0, st>>>(
+        c, static_cast<OUT*>(k), static_cast<OUT*>(v), pages);
     return cudaGetLastError();
 }
 
-template <typename OUT>
+// f(threads, pieces of each) for the page's size, as compile-time values
+template <typename F> cudaError_t by_page(const CacheParams& c, F f) {
+    using std::integral_constant;
+    switch (c.page * c.d / 8) {
+        case 128: return f(integral_constant<int, 128>(), integral_constant<int, 1>());
+        case 256: return f(integral_constant<int, 128>(), integral_constant<int, 2>());
+        case 512: return f(integral_constant<int, 128>(), integral_constant<int, 4>());
+        case 1024: return f(integral_constant<int, 256>(), integral_constant<int, 4>());
+        default: return f(integral_constant<int, 256>(), integral_constant<int, 8>());
+    }
+}
+
+template <typename IN, bool E4M3>
+cudaError_t write_as(const CacheParams& c, const void* k, long long ld_k, const void* v, long long ld_v,
+                     cudaStream_t st) {
+    return by_page(c, [&](auto threads, auto nv) {
+        return write_page<IN, E4M3, decltype(threads)::value, decltype(nv)::value>(c, k, ld_k, v, ld_v, st);
+    });
+}
+template <typename OUT, bool E4M3>
 cudaError_t read_as(const CacheParams& c, void* k, void* v, cudaStream_t st) {
-    const long long total = (long long)c.B * c.T * c.H * (c.d / 8);
-    const long long blocks = (total + kReadThreads - 1) / kReadThreads;
-    const dim3 grid((unsigned)(blocks < 152 * 64 ? blocks : 152 * 64), 2);
-    TraceScope ts("cache_read", st);
-    if (c.code == DR_CODE_E4M3)
-        cache_read_kernel<OUT, true><<<grid, kReadThreads, 0, st>>>(c, static_cast<OUT*>(k),
-                                                                    static_cast<OUT*>(v));
-    else
-        cache_read_kernel<OUT, false><<<grid, kReadThreads, 0, st>>>(c, static_cast<OUT*>(k),
-                                                                     static_cast<OUT*>(v));
-    return cudaGetLastError();
+    return by_page(c, [&](auto threads, auto nv) {
+        return read_page<OUT, E4M3, decltype(threads)::value, decltype(nv)::value>(c, k, v, st);
+    });
 }
 
 }  // namespace
@@ -212,13 +287,20 @@ cudaError_t read_as(const CacheParams& c, void* k, void* v, cudaStream_t st) {
 cudaError_t cache_write(const CacheParams& c, const void* k, long long ld_k, const void* v,
                         long long ld_v, int io, cudaStream_t st) {
     if (c.B == 0 || c.T == 0) return cudaSuccess;
-    return io == DR_BF16 ? write_as<__nv_bfloat16>(c, k, ld_k, v, ld_v, st)
-                         : write_as<float>(c, k, ld_k, v, ld_v, st);
+    const bool e4m3 = c.code == DR_CODE_E4M3;
+    if (io == DR_BF16)
+        return e4m3 ? write_as<__nv_bfloat16, true>(c, k, ld_k, v, ld_v, st)
+                    : write_as<__nv_bfloat16, false>(c, k, ld_k, v, ld_v, st);
+    return e4m3 ? write_as<float, true>(c, k, ld_k, v, ld_v, st)
+                : write_as<float, false>(c, k, ld_k, v, ld_v, st);
 }
 
 cudaError_t cache_read(const CacheParams& c, void* k, void* v, int out, cudaStream_t st) {
     if (c.B == 0 || c.T == 0 || (!k && !v)) return cudaSuccess;
-    return out == DR_BF16 ? read_as<__nv_bfloat16>(c, k, v, st) : read_as<float>(c, k, v, st);
+    const bool e4m3 = c.code == DR_CODE_E4M3;
+    if (out == DR_BF16)
+        return e4m3 ? read_as<__nv_bfloat16, true>(c, k, v, st) : read_as<__nv_bfloat16, false>(c, k, v, st);
+    return e4m3 ? read_as<float, true>(c, k, v, st) : read_as<float, false>(c, k, v, st);
 }
 
 }  // namespace dr

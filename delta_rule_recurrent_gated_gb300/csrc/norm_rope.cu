@@ -20,6 +20,9 @@ namespace dr {
 namespace {
 
 constexpr int kRopeThreads = 256;
+constexpr int kRun = 4;                           // heads of a run, at most; bf16: all loaded at once
+constexpr int kBwdResident = 2;                   // blocks of the backward kernel on an SM
+constexpr int kBwdBlocks = 152 * kBwdResident;    // over all runs of heads
 
 template <typename T>
 struct Vec8;  // 8 consecutive values as loaded
@@ -190,9 +193,19 @@ __device__ __forceinline__ Run make_run(const RopeParams& p) {
     return r;
 }
 
+// The thread's channels of heads h .. h + U - 1, zeros from h1 on and where the thread has none.
+template <typename T, int U>
+__device__ __forceinline__ void load_heads(Vec8<T> (&v)[U], const T* row, bool on, int h, int h1, int d) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (on && h + u < h1) v[u].load(row + (long long)(h + u) * d);
+        else v[u].zero();
+    }
+}
+
 template <typename IN, typename OUT, int LANES>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_fwd_kernel(const RopeParams p) {
-    constexpr int kGroups = kRopeThreads / LANES, U = 4;
+__global__ void __launch_bounds__(kRopeThreads, 3) norm_rope_fwd_kernel(const RopeParams p) {
+    constexpr int kGroups = kRopeThreads / LANES, U = sizeof(IN) == 2 ? kRun : kRun / 2;
     const Lane a = make_lane<LANES>(p);
     const Run run = make_run(p);
     const bool pairs = p.style == DR_ROPE_PAIRS;
@@ -207,6 +220,10 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_fwd_kernel(const RopeP
          base += (long long)gridDim.x * kGroups) {
         const long long tok = base + threadIdx.x / LANES;
         const bool on = tok < p.tokens && a.active;
+        const IN* xt = x0 + tok * ld + a.ch;
+        OUT* yt = y0 + tok * ldo + a.ch;
+        Vec8<IN> v[U];
+        load_heads<IN, U>(v, xt, on, run.h0, run.h1, p.d);
         float A[8], Bc[8], wp[8];
         coefficients(p, a, tok < p.tokens ? tok : 0, A, Bc);
         if (pairs) {
@@ -218,15 +235,8 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_fwd_kernel(const RopeP
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) { A[i] *= w[i]; Bc[i] *= wp[i]; }
-        const IN* xt = x0 + tok * ld + a.ch;
-        OUT* yt = y0 + tok * ldo + a.ch;
         for (int h = run.h0; h < run.h1; h += U) {
-            Vec8<IN> v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (on && h + u < run.h1) v[u].load(xt + (long long)(h + u) * p.d);
-                else v[u].zero();
-            }
+            if (h > run.h0) load_heads<IN, U>(v, xt, on, h, run.h1, p.d);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (h + u >= run.h1) break;  // uniform
@@ -246,9 +256,10 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_fwd_kernel(const RopeP
 }
 
 template <typename IN, typename OUT, int LANES>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_bwd_kernel(const RopeParams p) {
-    constexpr int kGroups = kRopeThreads / LANES, U = 2;
+__global__ void __launch_bounds__(kRopeThreads, kBwdResident) norm_rope_bwd_kernel(const RopeParams p) {
+    constexpr int kGroups = kRopeThreads / LANES, U = sizeof(IN) == 2 ? kRun : kRun / 2;
     __shared__ float sums[kGroups][LANES * 8 + 1];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Lane a = make_lane<LANES>(p);
     const Run run = make_run(p);
     const bool pairs = p.style == DR_ROPE_PAIRS;
@@ -263,22 +274,18 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_bwd_kernel(const RopeP
          base += (long long)gridDim.x * kGroups) {
         const long long tok = base + threadIdx.x / LANES;
         const bool on = tok < p.tokens && a.active;
-        float C[8], S[8];
-        coefficients(p, a, tok < p.tokens ? tok : 0, C, S);
         const IN* xt = x0 + tok * ld + a.ch;
         const IN* gt = g0 + tok * run.H * p.d + a.ch;
         OUT* yt = y0 + tok * ldo + a.ch;
+        Vec8<IN> v[U], dv[U];
+        load_heads<IN, U>(v, xt, on, run.h0, run.h1, p.d);
+        load_heads<IN, U>(dv, gt, on, run.h0, run.h1, p.d);
+        float C[8], S[8];
+        coefficients(p, a, tok < p.tokens ? tok : 0, C, S);
         for (int h = run.h0; h < run.h1; h += U) {
-            Vec8<IN> v[U], dv[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (on && h + u < run.h1) {
-                    v[u].load(xt + (long long)(h + u) * p.d);
-                    dv[u].load(gt + (long long)(h + u) * p.d);
-                } else {
-                    v[u].zero();
-                    dv[u].zero();
-                }
+            if (h > run.h0) {
+                load_heads<IN, U>(v, xt, on, h, run.h1, p.d);
+                load_heads<IN, U>(dv, gt, on, h, run.h1, p.d);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -326,6 +333,9 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_dw_kernel(const RopePa
     __shared__ float sums[32][9];
     const bool is_q = blockIdx.y == 0;
     float* dw = is_q ? p.dwq : p.dwk;
+    // launched early: until the parts are there (all threads wait, so that the end of this kernel is
+    // also the end of the one before)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (!dw) return;
     const int c = threadIdx.x & 7, j = threadIdx.x >> 3, ch = blockIdx.x * 8 + c;
     const long long lo = is_q ? 0 : (long long)p.nq * blocks;
@@ -342,23 +352,22 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_dw_kernel(const RopePa
     }
 }
 
-constexpr int kBwdBlocks = 152 * 4;  // blocks of the backward kernel over all runs of heads
-
 int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
 // Heads that a group of threads takes: all threads of the GPU get work before a group gets a
-// second head; from then on up to 16 heads share one token's coefficients.
+// second head; from then on four heads share one token's coefficients (runs of equal length keep
+// the backward's blocks, whose number is fixed, equally long).
 void split_heads(RopeParams& p, int lanes) {
     const long long rows = p.tokens * (p.Hq + p.Hk), groups = 152ll * 2048 / lanes;
-    long long hp = rows / groups;
-    p.hp = (int)(hp < 1 ? 1 : hp > 16 ? 16 : hp);
+    p.hp = rows < 2 * groups ? 1 : rows < 4 * groups ? 2 : kRun;
     p.nq = (p.Hq + p.hp - 1) / p.hp;
     p.nk = (p.Hk + p.hp - 1) / p.hp;
 }
 
+// Blocks of each run in the backward: all of them resident at once.
 int bwd_blocks(const RopeParams& p, int lanes) {
     const long long tiles = (p.tokens + kRopeThreads / lanes - 1) / (kRopeThreads / lanes);
-    const int per = (kBwdBlocks + p.nq + p.nk - 1) / (p.nq + p.nk);
+    const int runs = p.nq + p.nk, per = runs < kBwdBlocks ? kBwdBlocks / runs : 1;
     return (int)(tiles < per ? tiles : per);
 }
 
@@ -380,8 +389,16 @@ cudaError_t launch(const RopeParams& p, bool bwd, cudaStream_t st) {
     }
     if (!p.dwq && !p.dwk) return cudaSuccess;
     TraceScope ts("norm_rope_dw", st);
-    norm_rope_dw_kernel<<<dim3(p.d / 8, 2), kRopeThreads, 0, st>>>(p, blocks);
-    return cudaGetLastError();
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.d / 8, 2);
+    cfg.blockDim = dim3(kRopeThreads);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, p, blocks);
 }
 
 template <typename IN, typename OUT>
