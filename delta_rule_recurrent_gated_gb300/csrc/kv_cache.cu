@@ -18,10 +18,16 @@ namespace {
 template <bool E4M3> __device__ __forceinline__ float inv_code_max() {
     return E4M3 ? 1.f / 448.f : 1.f / 127.f;
 }
-// The nearest code of x, ties to even.
-template <bool E4M3> __device__ __forceinline__ uint32_t to_code(float x) {
-    if (E4M3) return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
-    return (uint32_t)(int)fminf(fmaxf(rintf(x), -127.f), 127.f) & 0xffu;
+// The nearest codes of four values, ties to even, the first in the lowest byte.
+template <bool E4M3> __device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d) {
+    if (E4M3) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+        return lo | hi << 16;
+    }
+    // 1.5 * 2^23 + x has spacing 1: rounded to nearest even, its low byte is the whole number
+    auto whole = [](float x) { return __float_as_uint(fminf(fmaxf(x, -127.f), 127.f) + 12582912.f); };
+    return __byte_perm(__byte_perm(whole(a), whole(b), 0x0040), __byte_perm(whole(c), whole(d), 0x0040), 0x5410);
 }
 template <bool E4M3> __device__ __forceinline__ float from_code(uint32_t byte) {
     if (E4M3) {
@@ -161,7 +167,9 @@ __global__ void __launch_bounds__(THREADS)
             uint32_t w[2] = {0, 0};
             if (s > 0.f) {
 #pragma unroll
-                for (int m = 0; m < 8; ++m) w[m >> 2] |= to_code<E4M3>(over(y[m])) << (8 * (m & 3));
+                for (int m = 0; m < 8; ++m) y[m] = over(y[m]);
+                w[0] = to_codes<E4M3>(y[0], y[1], y[2], y[3]);
+                w[1] = to_codes<E4M3>(y[4], y[5], y[6], y[7]);
             }
             *reinterpret_cast<uint2*>(codes + (size_t)j * 8) = make_uint2(w[0], w[1]);
         }
@@ -170,13 +178,12 @@ __global__ void __launch_bounds__(THREADS)
         for (int j = threadIdx.x; j < from; j += THREADS) {
             const uint2 u = *reinterpret_cast<const uint2*>(codes + (size_t)j * 8);
             const uint32_t in[2] = {u.x, u.y};
-            uint32_t w[2] = {0, 0};
+            float y[8];
 #pragma unroll
-            for (int m = 0; m < 8; ++m) {
-                const float was = from_code<E4M3>((in[m >> 2] >> (8 * (m & 3))) & 0xffu);
-                w[m >> 2] |= to_code<E4M3>(over(__fmul_rn(was, s_old))) << (8 * (m & 3));
-            }
-            *reinterpret_cast<uint2*>(codes + (size_t)j * 8) = make_uint2(w[0], w[1]);
+            for (int m = 0; m < 8; ++m)
+                y[m] = over(__fmul_rn(from_code<E4M3>((in[m >> 2] >> (8 * (m & 3))) & 0xffu), s_old));
+            *reinterpret_cast<uint2*>(codes + (size_t)j * 8) =
+                make_uint2(to_codes<E4M3>(y[0], y[1], y[2], y[3]), to_codes<E4M3>(y[4], y[5], y[6], y[7]));
         }
     }
 }
