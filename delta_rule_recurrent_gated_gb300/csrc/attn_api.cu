@@ -93,6 +93,16 @@ int check_attn(const dr_cache* c, const dr_attn_desc* d, int B, int T) {
     return check_row(d->ld_q, (long long)d->Hq * c->d, d->io_dtype);
 }
 
+// Which kernel: 128 rows (query tokens times the query heads of a cache head) fill a tile of the
+// tensor cores; fp32 types need the split operands of the other kernel.
+constexpr int kTcRows = 64;
+bool on_tensor_cores(const dr_cache* c, const dr_attn_desc* d, int T) {
+    return d->io_dtype == DR_BF16 && d->out_dtype == DR_BF16 && (long long)T * (d->Hq / c->H) >= kTcRows;
+}
+size_t attn_bytes(const dr_cache* c, const dr_attn_desc* d, int T) {
+    return on_tensor_cores(c, d, T) ? dr::cache_attn_tc_bytes(c->d) : dr::cache_attn_rows_bytes(c->d);
+}
+
 }  // namespace
 
 extern "C" {
@@ -181,7 +191,7 @@ int dr_cache_read(const dr_cache* cache, const dr_cache_seqs* seqs, void* k, voi
 
 size_t dr_cache_attn_workspace_bytes(const dr_cache* cache, const dr_attn_desc* desc, int B, int T) {
     if (check_attn(cache, desc, B, T) != DR_OK) return 0;
-    return dr::cache_attn_part_bytes(cache->d);
+    return attn_bytes(cache, desc, T);
 }
 
 int dr_cache_attn(const dr_cache* cache, const dr_cache_seqs* seqs, const dr_attn_desc* desc,
@@ -195,7 +205,7 @@ int dr_cache_attn(const dr_cache* cache, const dr_cache_seqs* seqs, const dr_att
     const void* ptrs[] = {q, o, lse, workspace};
     for (const void* ptr : ptrs)
         if (misaligned(ptr)) return DR_ERR_ALIGNMENT;
-    if (!workspace || workspace_bytes < dr::cache_attn_part_bytes(cache->d)) return DR_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < attn_bytes(cache, desc, seqs->T)) return DR_ERR_WORKSPACE;
     dr::AttnParams p = {};
     p.c = cache_params(cache, seqs);
     p.Hq = desc->Hq;
@@ -206,7 +216,9 @@ int dr_cache_attn(const dr_cache* cache, const dr_cache_seqs* seqs, const dr_att
     p.q = q; p.o = o; p.lse = lse;
     p.io = desc->io_dtype; p.out = desc->out_dtype;
     p.part = static_cast<float*>(workspace);
-    return cuda_status(dr::cache_attn(p, static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(on_tensor_cores(cache, desc, seqs->T) ? dr::cache_attn_tc(p, st)
+                                                             : dr::cache_attn_rows(p, st));
 }
 
 }  // extern "C"

@@ -24,9 +24,7 @@
 // form one line, block i of n takes the i-th part of it.  A tile that lies in one block is finished
 // there; of the others each block leaves its rows (sums, l, m, M) in the workspace, and a second
 // kernel joins them, a block to a row.  It is launched early and waits on the device for the first.
-#include <cuda_fp16.h>
-
-#include "cache_attn.cuh"
+#include "attn_util.cuh"
 #include "trace.cuh"
 
 namespace dr {
@@ -35,8 +33,6 @@ namespace {
 constexpr int kWarps = 2, kThreads = 32 * kWarps;
 constexpr int kStep = 32, kStage = kStep * kWarps;  // positions of a warp's step, of a stage
 constexpr int kOver = 4;  // what a tile costs beside its stages, in stages
-constexpr float kNegInf = -INFINITY;
-constexpr int kBias = 14;  // weights as 16-bit operands reach 2^14
 
 // ------------------------------------------------------------------ the line of stages
 // Stages of sequence b that its tokens see, tiles of rows, and their product with the heads.
@@ -60,14 +56,6 @@ __device__ __forceinline__ Seq make_seq(const AttnParams& p, int b) {
 }
 __device__ __forceinline__ long long work_of(const AttnParams& p, const Seq& s) {
     return s.n > 0 ? (long long)s.tiles * (s.stages + kOver) * p.c.H : 0;
-}
-__device__ __forceinline__ long long warp_scan(long long x, int lane) {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    return x;
 }
 // The whole line (every lane gets it).
 template <int ROWS>
@@ -98,36 +86,7 @@ __device__ __forceinline__ int find_seq(const AttnParams& p, int lane, long long
     begin = before;
     return p.c.B;
 }
-// Block i of n <= total takes places share(i) .. share(i + 1) - 1 of the line, at least one;
-// holder(at) is the block that has place `at`: total i / n <= at where total i < (at + 1) n.
-__device__ __forceinline__ long long share(long long total, int i, int n) { return total * i / n; }
-__device__ __forceinline__ int holder(long long total, long long at, int n) {
-    return (int)(((at + 1) * n - 1) / total);
-}
-__device__ __forceinline__ int blocks_used(long long total, int blocks) {
-    return total < blocks ? (int)total : blocks;
-}
-
 // ------------------------------------------------------------------ operands
-// The four codes of `w` as two pairs of 16-bit floats: bytes (0, 2) and (1, 3) of int8 codes,
-// bytes (0, 1) and (2, 3) of e4m3 codes.
-template <bool E4M3>
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& a, uint32_t& b) {
-    if (E4M3) {
-        asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %2;\n"
-            " cvt.rn.f16x2.e4m3x2 %0, x;\n cvt.rn.f16x2.e4m3x2 %1, y;\n}\n"
-            : "=r"(a), "=r"(b)
-            : "r"(w));
-    } else {
-        // x + 128 in the low bits of 1024 .. 2047, whose spacing is 1; minus 1152 is x exactly
-        const __half2 off = __half2half2(__ushort_as_half(0x6480));  // 1152
-        uint32_t u = (w & 0x00ff00ffu) ^ 0x64806480u, v = ((w >> 8) & 0x00ff00ffu) ^ 0x64806480u;
-        const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&u), off);
-        const __half2 y = __hsub2(*reinterpret_cast<__half2*>(&v), off);
-        a = *reinterpret_cast<const uint32_t*>(&x);
-        b = *reinterpret_cast<const uint32_t*>(&y);
-    }
-}
 // Bytes 0, 1 (HI: 2, 3) of the words of two positions, so that codes_to_half pairs the positions.
 template <bool E4M3, bool HI> __device__ __forceinline__ uint32_t pair_up(uint32_t x, uint32_t y) {
     return __byte_perm(x, y, E4M3 ? (HI ? 0x7362 : 0x5140) : (HI ? 0x7632 : 0x5410));
@@ -145,24 +104,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack_half(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ float2 unpack_half(uint32_t x) {
-    return __half22float2(*reinterpret_cast<const __half2*>(&x));
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// 2^x for a whole x, the ends of the range standing for what is beyond them; 0 for -inf and NaN.
-__device__ __forceinline__ float pow2i(float x) {
-    if (!(x >= -126.f)) return 0.f;
-    return __uint_as_float((uint32_t)((int)fminf(x, 127.f) + 127) << 23);
-}
-
 // 16 positions in the ring.  Thread (g, c) = (lane / 4, lane % 4) takes of the keys positions g and
 // g + 8, 16-byte chunks c d/64 .. + d/64 - 1 of the row; of the values positions 2c, 2c + 1, 2c + 8,
 // 2c + 9, channels g d/8 .. + d/8 - 1.
@@ -207,12 +148,6 @@ __device__ __forceinline__ void load_values(uint32_t (&v)[4][D / 32], const uint
     }
 }
 
-// What a warp needs to know of 16 positions.
-struct __align__(16) Meta {
-    int id;            // page, -1 where the entry is out of range, -2 where no row sees a position
-    float ks, vs, ve;  // scales; whole number with vs <= 2^ve
-};
-
 template <int D, int NT, bool PREC>
 struct Tile {
     uint32_t q[NT][D / 16][2], ql[NT][PREC ? D / 16 : 1][2];  // Q^T as B operands
@@ -246,8 +181,7 @@ __device__ __forceinline__ void fetch_q(RawQ<D, NT>& r, const AttnParams& p, int
     }
 }
 
-// The queries of rows row0 .. row0 + 8 NT - 1, each scaled by a power of two to largest magnitude
-// 2^9 .. 2^10, which keeps a bf16 value exact unless it is 2^-24 of the row's largest.
+// The queries of rows row0 .. row0 + 8 NT - 1 as operands, their factors, and empty sums.
 template <int D, int NT, bool E4M3, bool PREC>
 __device__ __forceinline__ void load_tile(Tile<D, NT, PREC>& t, RawQ<D, NT>& raw, const AttnParams& p, int b, int h,
                                           int row0, const Seq& s, int lane) {
@@ -281,10 +215,9 @@ __device__ __forceinline__ void load_tile(Tile<D, NT, PREC>& t, RawQ<D, NT>& raw
         for (int i = 0; i < D / 4; ++i) top = fmaxf(top, fabsf(x[i]));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        int e = 0;
-        if (top > 0.f && top < INFINITY) frexpf(top, &e), e -= 10;
-        const int e1 = max(-100, min(100, e));  // 2^-e as a product of two powers in range
-        const float up = pow2i(-(float)e1), rest = pow2i((float)(e1 - e));
+        int e;
+        float up, rest;
+        query_scale(top, e, up, rest);
 #pragma unroll
         for (int w = 0; w < D / 16; ++w)
 #pragma unroll
@@ -301,7 +234,7 @@ __device__ __forceinline__ void load_tile(Tile<D, NT, PREC>& t, RawQ<D, NT>& raw
                 }
             }
         // factors and positions belong to rows 2c, 2c + 1: held by the lanes with g = 2c, 2c + 1
-        const float f = ldexpf(p.scale * 1.44269504088896340736f, e);
+        const float f = ldexpf(p.scale * kLog2e, e);
         const int ps = on ? s.len + row / p.G : -1;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -468,24 +401,7 @@ __device__ __forceinline__ void step(Tile<D, NT, PREC>& t, const uint8_t* slot, 
     }
 }
 
-// ------------------------------------------------------------------ rows that leave a block
-// Part of the workspace of block i: two unfinished tiles, each [rows][d] sums, then [rows] of l, m, M.
-__host__ __device__ constexpr size_t tile_floats(int d, int rows) { return (size_t)rows * (d + 3); }
-
-__device__ __forceinline__ void write_row(const AttnParams& p, int b, int h, int row, int ch, int d, float sum,
-                                          float l, float m, float M) {
-    const int tok = row / p.G, head = h * p.G + row % p.G;
-    const size_t at = ((size_t)b * p.c.T + tok) * p.Hq + head;
-    // sums are in units of 2^(M - 14), l in units of 2^m
-    float f = M - m - kBias;
-    float y = sum / l;
-    if (f > 100.f || f < -100.f) { y = ldexpf(y, (int)fminf(fmaxf(f, -400.f), 400.f)); }
-    else y *= pow2i(f);
-    if (M == kNegInf && sum == 0.f) y = l == l ? 0.f : sum / l;  // every value scale is zero
-    st_any(p.o, at * d + ch, p.out, y);
-    if (ch == 0 && p.lse) p.lse[at] = (m + log2f(l)) * 0.69314718055994530942f;
-}
-
+// ------------------------------------------------------------------ the kernel
 constexpr int kRing = 2;  // steps of a warp's ring
 template <int D> __host__ __device__ constexpr int ring_bytes() { return kRing * 2 * kStep * D; }
 constexpr int kMetas = 64;  // of 16 positions each, a power of two
@@ -560,9 +476,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 6 : 4) cache_attn
                     const size_t ph = (size_t)x.id * p.c.H + h;
                     x.ks = p.c.k_scale[ph];
                     x.vs = p.c.v_scale[ph];
-                    int e;
-                    frexpf(x.vs, &e);
-                    x.ve = x.vs > 0.f ? (float)e : x.vs == 0.f ? kNegInf : 0.f;
+                    x.ve = scale_exponent(x.vs);
                 } else {
                     flag_index_error(p.c);
                     x.ks = x.vs = __uint_as_float(0x7fc00000u);
@@ -668,10 +582,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 6 : 4) cache_attn
     }
 }
 
-// Until the first kernel has ended and its writes are there.  Every thread of the second one comes
-// here, so that its end also means the end of the first.
-__device__ __forceinline__ void wait_for_parts() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // Joins the parts of a tile that several blocks worked on.  Block x: the tile, y: its row.  Rows of
 // no query get zeros (behind a sequence's tokens) or NaN (a sequence out of range).
 constexpr int kJoinWarps = 8;
@@ -758,15 +668,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_attn_join_kernel(const 
     }
 }
 
-template <typename K>
-int resident_blocks(K kernel, int smem) {
-    int sms = 0, per = 0, dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, kThreads, smem) != cudaSuccess) return 0;
-    return sms * per;
-}
-
 constexpr int kMaxBlocks = 152 * 8;
 
 template <int D, int NT, bool E4M3, bool PREC>
@@ -774,7 +675,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
     constexpr int smem = smem_bytes<D, NT>();
     if (cudaError_t e = set_smem_once(cache_attn_kernel<D, NT, E4M3, PREC>, smem, ready); e != cudaSuccess) return e;
-    static const int resident = resident_blocks(cache_attn_kernel<D, NT, E4M3, PREC>, smem);
+    static const int resident = resident_blocks(cache_attn_kernel<D, NT, E4M3, PREC>, kThreads, smem);
     if (resident <= 0) return cudaErrorUnknown;
     const int blocks = resident < kMaxBlocks ? resident : kMaxBlocks;
     {
@@ -806,12 +707,9 @@ cudaError_t by_rows(const AttnParams& p, cudaStream_t st) {
 
 }  // namespace
 
-size_t cache_attn_part_bytes(int d) {
-    return (size_t)kMaxBlocks * 2 * tile_floats(d, 16) * sizeof(float);
-}
+size_t cache_attn_rows_bytes(int d) { return (size_t)kMaxBlocks * 2 * tile_floats(d, 16) * sizeof(float); }
 
-cudaError_t cache_attn(const AttnParams& p, cudaStream_t st) {
-    if (p.c.B == 0 || p.c.T == 0) return cudaSuccess;
+cudaError_t cache_attn_rows(const AttnParams& p, cudaStream_t st) {
     if (p.c.code == DR_CODE_E4M3) return p.c.d == 128 ? by_rows<128, true>(p, st) : by_rows<64, true>(p, st);
     return p.c.d == 128 ? by_rows<128, false>(p, st) : by_rows<64, false>(p, st);
 }

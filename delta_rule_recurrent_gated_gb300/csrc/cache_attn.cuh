@@ -16,6 +16,10 @@ struct AttnParams {
     float* part;             // workspace: the blocks' unfinished rows
 };
 
-size_t cache_attn_part_bytes(int d);
-cudaError_t cache_attn(const AttnParams& p, cudaStream_t st);
+// A few rows of a sequence and cache head at a time, any type (cache_attn.cu).
+size_t cache_attn_rows_bytes(int d);
+cudaError_t cache_attn_rows(const AttnParams& p, cudaStream_t st);
+// 128 rows at a time on the tensor cores, bf16 queries and outputs (cache_attn_tc.cu).
+size_t cache_attn_tc_bytes(int d);
+cudaError_t cache_attn_tc(const AttnParams& p, cudaStream_t st);
 }  // namespace dr

@@ -1,0 +1,670 @@
+// cache_attn_tc.cu -- attention of many query tokens of each sequence over the paged 8-bit cache
+// (dr.h, dr_cache_attn; bf16 queries and outputs): the products on the fifth-generation tensor cores.
+//
+// A block works on a tile of 128 rows (query tokens times the G query heads that share a cache head,
+// row = t * G + g) over a stretch of positions, in stages of 64:
+//   S = Q K^T   128 x 64, contraction d; two accumulators in tensor memory, used in turn
+//   O += P V    128 x d, contraction 64; one accumulator, which stays in tensor memory
+// Warps 4-7 read the codes and write them as 16-bit floats (exact) into the operand tiles of K and V,
+// two of each; warp 8 issues the products; warps 0-3 hold a row per thread: they read S, keep the
+// softmax statistics and write the weights P as operand tile.  Two blocks share an SM, so that the
+// products of one run while the other's warps convert.
+//
+// Softmax in base 2 with whole-number references, as in cache_attn.cu: p = 2^(s - m), l = sum p,
+// operand w = p vs 2^(m - M + 14).  The accumulator is rescaled (exactly, by a power of two) only when
+// a row's largest s + log2 vs passes M by more than 1, so an operand reaches 2^15 at most.
+//
+// The stages of all tiles form one line that is divided evenly among the blocks (two per SM); a tile
+// that several blocks worked on is joined by a second kernel from their rows in the workspace.
+#include "attn_util.cuh"
+#include "tc.cuh"
+#include "trace.cuh"
+
+namespace dr {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128, kStage = 64;
+constexpr int kTcThreads = 288;  // four warps of rows, four of codes, one that issues
+constexpr int kTcOver = 4;       // what a tile costs beside its stages, in stages
+constexpr int kMetas = 8;        // stages whose scales are kept: more than the warps can be apart
+constexpr int kMaxTcBlocks = 152 * 2;
+
+// ------------------------------------------------------------------ the line of stages
+struct TcTile {
+    int row0, t0, t1;    // first row; tokens of the first and last row
+    int lo, hi;          // positions that its rows see
+    int s0, stages;
+};
+__device__ __forceinline__ int tiles_of(const AttnParams& p, int n) { return (n * p.G + kRows - 1) / kRows; }
+__device__ __forceinline__ TcTile make_tile(const AttnParams& p, int len, int n, int tile) {
+    TcTile t;
+    t.row0 = tile * kRows;
+    t.t0 = t.row0 / p.G;
+    t.t1 = min(n - 1, (t.row0 + kRows - 1) / p.G);
+    t.hi = len + t.t1 + 1;
+    t.lo = p.window > 0 ? max(0, len + t.t0 - p.window + 1) : 0;
+    t.s0 = t.lo / kStage;
+    t.stages = (t.hi + kStage - 1) / kStage - t.s0;
+    return t;
+}
+// Places on the line of one head of sequence b (0: nothing to do).
+__device__ __forceinline__ long long head_work(const AttnParams& p, int b) {
+    int len, n;
+    if (!cache_seq(p.c, b, len, n)) return 0;
+    long long w = 0;
+    for (int i = 0, tiles = tiles_of(p, n); i < tiles; ++i) w += make_tile(p, len, n, i).stages + kTcOver;
+    return w;
+}
+
+// A block's stretch of a tile: stages from .. upto - 1.
+struct Stretch {
+    int b, h, len, n, from, upto;
+    bool whole, first;   // the whole tile; the block's first stretch
+    TcTile t;
+};
+// Walks through a block's part of the line; every warp does so for itself, with the same result.
+struct Walk {
+    long long at, end;
+    int b, h, tile, place, len, n;
+    bool first;
+
+    __device__ __forceinline__ void start(const AttnParams& p, int lane) {
+        long long total = 0;
+        for (int i = lane; i < p.c.B; i += 32) total += head_work(p, i) * p.c.H;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        const int used = blocks_used(total, gridDim.x);
+        at = end = 0;
+        first = true;
+        if ((int)blockIdx.x >= used) return;
+        at = share(total, blockIdx.x, used);
+        end = share(total, blockIdx.x + 1, used);
+        long long before = 0, mine = 0;
+        b = -1;
+        for (int b0 = 0; b0 < p.c.B && b < 0; b0 += 32) {
+            const long long w = b0 + lane < p.c.B ? head_work(p, b0 + lane) : 0;
+            const long long upto = before + warp_scan(w * p.c.H, lane);
+            const unsigned hit = __ballot_sync(0xffffffffu, upto > at);
+            if (hit) {
+                const int l = __ffs(hit) - 1;
+                before = __shfl_sync(0xffffffffu, upto - w * p.c.H, l);
+                mine = __shfl_sync(0xffffffffu, w, l);
+                b = b0 + l;
+            } else {
+                before = __shfl_sync(0xffffffffu, upto, 31);
+            }
+        }
+        if (b < 0) {  // the lengths changed under the call
+            at = end;
+            return;
+        }
+        cache_seq(p.c, b, len, n);
+        h = (int)((at - before) / mine);
+        long long rest = (at - before) % mine;
+        tile = 0;
+        for (int tiles = tiles_of(p, n); tile < tiles; ++tile) {
+            const int cost = make_tile(p, len, n, tile).stages + kTcOver;
+            if (rest < cost) break;
+            rest -= cost;
+        }
+        place = (int)rest;
+    }
+    __device__ __forceinline__ bool next(const AttnParams& p, Stretch& s) {
+        while (at < end) {
+            s.t = make_tile(p, len, n, tile);
+            s.b = b;
+            s.h = h;
+            s.len = len;
+            s.n = n;
+            const int cost = s.t.stages + kTcOver, span = (int)min((long long)cost - place, end - at);
+            if (span <= 0) break;  // the lengths changed under the call
+            s.from = max(0, place - kTcOver);
+            s.upto = place + span - kTcOver;
+            at += span;
+            place += span;
+            if (place >= cost) {
+                place = 0;
+                if (++tile >= tiles_of(p, n)) {
+                    tile = 0;
+                    if (++h >= p.c.H) {
+                        h = 0;
+                        do {
+                            if (++b >= p.c.B) { at = end; break; }
+                        } while (!cache_seq(p.c, b, len, n) || n == 0);
+                    }
+                }
+            }
+            if (s.upto > s.from) {
+                s.whole = s.upto - s.from == s.t.stages;
+                s.first = first;
+                first = false;
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
+// ------------------------------------------------------------------ shared memory
+struct __align__(16) StageMeta {  // read as 16-byte words
+    float ks[4], vs[4], ve[4];  // of the four 16-position parts
+    int bad;                    // a part whose page number is out of range
+    int pad[3];
+};
+struct Control {
+    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], sempty[2], pfull, pvdone, qfull, drain;
+    uint32_t tmem;
+    volatile int dead;
+    StageMeta meta[kMetas];
+};
+template <int D> struct Smem {
+    static constexpr int q = 0, k = kRows * D * 2, v = k + 2 * kStage * D * 2, pw = v + 2 * kStage * D * 2,
+                         control = pw + kRows * kStage * 2, bytes = control + 1024;
+    static_assert(sizeof(Control) <= 1024, "control block");
+};
+
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Bounded wait of a whole warp; false once it or any other of the block's waits has run out.
+__device__ __forceinline__ bool wait(Control& ct, uint64_t* bar, uint32_t parity) {
+    bool done = mbar_try_wait(bar, parity);
+    if (!done) {
+        const uint64_t t0 = globaltimer_ns();
+        while (true) {
+            for (int i = 0; i < 64 && !done; ++i) done = mbar_try_wait(bar, parity);
+            if (done || ct.dead) break;
+            if (globaltimer_ns() - t0 > kWaitLimitNs) {
+                ct.dead = 1;
+                break;
+            }
+        }
+    }
+    return __all_sync(0xffffffffu, done);
+}
+// D[tmem] (+)= A B, 16-bit floats, fp32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+    return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+// 16 codes as 16-bit floats: two 16-byte chunks.  The four channels of a word come in the order of
+// codes_to_half: 0, 2, 1, 3 for int8 codes (queries and outputs follow), 0, 1, 2, 3 for e4m3.
+template <bool E4M3>
+__device__ __forceinline__ void convert16(const uint4& u, uint4& x, uint4& y) {
+    codes_to_half<E4M3>(u.x, x.x, x.y);
+    codes_to_half<E4M3>(u.y, x.z, x.w);
+    codes_to_half<E4M3>(u.z, y.x, y.y);
+    codes_to_half<E4M3>(u.w, y.z, y.w);
+}
+
+// ------------------------------------------------------------------ warps 4-7: codes to operand tiles
+// Thread: row t % 64 of the stage, half t / 64 of its channels.
+template <int D, bool E4M3>
+__device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
+    constexpr int V = D / 32;  // 16-byte pieces of a thread's half row
+    const int t = threadIdx.x - 128, row = t & 63, half = t >> 6;
+    uint32_t n = 0;  // stages so far
+    Stretch s;
+    while (walk.next(p, s)) {
+        struct Src { int id; float ks, vs; bool value; };
+        const int end = s.len + s.n, stages = s.upto - s.from;
+        auto lookup = [&](int i) {
+            const int pos = (s.t.s0 + s.from + i) * kStage + row, part = pos & ~15;
+            return i < stages && part < s.t.hi && part + 16 > s.t.lo ? cache_page(p.c, s.b, pos / p.c.page) : -2;
+        };
+        auto fetch = [&](uint4 (&x)[V], const uint8_t* pool, int i, int id) {
+            const int pos = (s.t.s0 + s.from + i) * kStage + row;
+            const bool on = id >= 0 && pos < end;  // behind the last position: zeros
+            const uint4* at = reinterpret_cast<const uint4*>(
+                pool + (((size_t)(on ? id : 0) * p.c.H + s.h) * p.c.page + pos % p.c.page) * D + half * (D / 2));
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = on ? __ldg(at + j) : make_uint4(0, 0, 0, 0);
+        };
+        auto write = [&](uint8_t* tile, const uint4 (&x)[V]) {
+            uint8_t* at = tile + (D == 128 ? half * kStage * 128 : 0) + row * 128;
+            const int c0 = D == 128 ? 0 : 4 * half;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                uint4 a, b;
+                convert16<E4M3>(x[j], a, b);
+                *reinterpret_cast<uint4*>(at + (((c0 + 2 * j) ^ (row & 7)) << 4)) = a;
+                *reinterpret_cast<uint4*>(at + (((c0 + 2 * j + 1) ^ (row & 7)) << 4)) = b;
+            }
+        };
+        const bool tells = half == 0 && (row & 15) == 0;  // notes its part's scales
+        auto scales = [&](int id, float& ks, float& vs) {
+            ks = vs = id == -1 ? __uint_as_float(0x7fc00000u) : 0.f;
+            if (tells && id >= 0) {
+                const size_t ph = (size_t)id * p.c.H + s.h;
+                ks = p.c.k_scale[ph];
+                vs = p.c.v_scale[ph];
+            }
+        };
+        uint4 k[V], v[V];
+        float ks, vs;
+        int id = lookup(0), ahead = lookup(1);
+        fetch(k, p.c.k, 0, id);
+        fetch(v, p.c.v, 0, id);
+        scales(id, ks, vs);
+        for (int i = 0; i < stages; ++i, ++n) {
+            const uint32_t buf = n & 1, parity = (n >> 1) & 1;
+            if (!wait(ct, &ct.kempty[buf], parity ^ 1)) return;
+            if (tells) {
+                StageMeta& m = ct.meta[n % kMetas];
+                m.ks[row >> 4] = ks;
+                m.vs[row >> 4] = vs;
+                m.ve[row >> 4] = id >= 0 ? scale_exponent(vs) : id == -1 ? 0.f : kNegInf;
+                if (id == -1) flag_index_error(p.c);
+            }
+            write(smem + Smem<D>::k + buf * kStage * D * 2, k);
+            fence_async_smem();
+            mbar_arrive(&ct.kfull[buf]);
+            fetch(k, p.c.k, i + 1, ahead);
+            if (!wait(ct, &ct.vempty[buf], parity ^ 1)) return;
+            write(smem + Smem<D>::v + buf * kStage * D * 2, v);
+            fence_async_smem();
+            mbar_arrive(&ct.vfull[buf]);
+            fetch(v, p.c.v, i + 1, ahead);
+            scales(ahead, ks, vs);
+            id = ahead;
+            ahead = lookup(i + 2);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ warp 8: the products
+template <int D>
+__device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t base = smem_u32(smem), tm = ct.tmem;
+    const Tile q{base + Smem<D>::q, kRows}, pw{base + Smem<D>::pw, kRows};
+    uint32_t n = 0, tiles = 0;
+    auto scores = [&](uint32_t i) {
+        const uint32_t buf = i & 1, parity = (i >> 1) & 1;
+        if (!wait(ct, &ct.kfull[buf], parity) || !wait(ct, &ct.sempty[buf], parity ^ 1)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+            const Tile k{base + Smem<D>::k + buf * kStage * D * 2, kStage};
+#pragma unroll
+            for (int kk = 0; kk < D; kk += 16)
+                mma_bf16(tm + buf * kStage, desc_kmajor(q, kk), desc_kmajor(k, kk), idesc_f16(kRows, kStage, false),
+                         kk > 0);
+            mma_commit(&ct.kempty[buf]);
+            mbar_arrive(&ct.sfull[buf]);  // hands on the scales, which came with kfull
+            mma_commit(&ct.sfull[buf]);
+        }
+        __syncwarp();
+        return true;
+    };
+    auto values = [&](uint32_t i, bool accumulate) {
+        const uint32_t buf = i & 1, parity = (i >> 1) & 1;
+        if (!wait(ct, &ct.vfull[buf], parity) || !wait(ct, &ct.pfull, i & 1)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+            const Tile v{base + Smem<D>::v + buf * kStage * D * 2, kStage};
+#pragma unroll
+            for (int kk = 0; kk < kStage; kk += 16)
+                mma_bf16(tm + 2 * kStage, desc_kmajor(pw, kk), desc_mnmajor(v, kk), idesc_f16(kRows, D, true),
+                         accumulate || kk > 0);
+            mma_commit(&ct.vempty[buf]);
+            mma_commit(&ct.pvdone);
+        }
+        __syncwarp();
+        return true;
+    };
+    Stretch s;
+    bool ok = true;
+    while (ok && walk.next(p, s)) {
+        const int stages = s.upto - s.from;
+        ok = wait(ct, &ct.qfull, tiles & 1);
+        ++tiles;
+        for (int i = 0; ok && i < stages; ++i) {
+            ok = scores(n + i);
+            if (ok && i > 0) ok = values(n + i - 1, i > 1);
+        }
+        if (ok) ok = values(n + stages - 1, stages > 1);
+        n += stages;
+    }
+    if (!ok) {  // let what is in flight end before the tensor memory goes
+        if (lane == 0) mma_commit(&ct.drain);
+        mbar_wait(&ct.drain, 0, kWaitLimitNs);
+    }
+}
+
+// ------------------------------------------------------------------ warps 0-3: a row per thread
+template <int D, bool E4M3>
+__device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
+    const int r = threadIdx.x;
+    const uint32_t tm = warp_lane_base(ct.tmem);
+    const uint32_t so = tm + 2 * kStage;  // this row of O
+    uint32_t n = 0;
+    Stretch s;
+    while (walk.next(p, s)) {
+        const int stages = s.upto - s.from, row = s.t.row0 + r;
+        const bool on = row < s.n * p.G;
+        const int tok = on ? row / p.G : 0, head = s.h * p.G + (on ? row % p.G : 0), pos = on ? s.len + tok : -1;
+        // the row's queries, scaled, as operand
+        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                         ((long long)s.b * p.c.T + tok) * p.ld_q + (long long)head * D);
+        float top = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < D / 8; ++j) {
+            float x[8];
+            unpack8(on ? __ldg(qp + j) : make_uint4(0, 0, 0, 0), x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+        }
+        int e;
+        float up, rest;
+        query_scale(top, e, up, rest);
+#pragma unroll 4
+        for (int j = 0; j < D / 8; ++j) {
+            float x[8];
+            unpack8(on ? __ldg(qp + j) : make_uint4(0, 0, 0, 0), x);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = x[i] * up * rest;
+            uint4 u;
+            if (E4M3) {
+                u = make_uint4(pack_half(x[0], x[1]), pack_half(x[2], x[3]), pack_half(x[4], x[5]), pack_half(x[6], x[7]));
+            } else {
+                u = make_uint4(pack_half(x[0], x[2]), pack_half(x[1], x[3]), pack_half(x[4], x[6]), pack_half(x[5], x[7]));
+            }
+            *reinterpret_cast<uint4*>(smem + Smem<D>::q + (j >> 3) * kRows * 128 + r * 128 + (((j & 7) ^ (r & 7)) << 4)) = u;
+        }
+        fence_async_smem();
+        mbar_arrive(&ct.qfull);
+        const float qs = ldexpf(p.scale * kLog2e, e);
+        // positions that every row sees need no mask
+        const int all_hi = s.len + s.t.t0 + 1, all_lo = p.window > 0 ? max(0, s.len + s.t.t1 - p.window + 1) : 0;
+        float l = 0.f, m = kNegInf, M = kNegInf;
+        for (int i = 0; i < stages; ++i, ++n) {
+            const uint32_t buf = n & 1;
+            const int first = (s.t.s0 + s.from + i) * kStage;
+            if (!wait(ct, &ct.sfull[buf], (n >> 1) & 1)) return;
+            tc_fence_after();
+            float x[4][16];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) tmem_ld16(tm + buf * kStage + 16 * g, x[g]);
+            tmem_ld_wait();
+            tc_fence_before();
+            mbar_arrive(&ct.sempty[buf]);
+            const StageMeta& mt = ct.meta[n % kMetas];
+            const float4 ks4 = *reinterpret_cast<const float4*>(mt.ks), vs4 = *reinterpret_cast<const float4*>(mt.vs);
+            const float4 ve4 = *reinterpret_cast<const float4*>(mt.ve);
+            const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
+            const float ve[4] = {ve4.x, ve4.y, ve4.z, ve4.w};
+            const bool edge = first + kStage > all_hi || first < all_lo || ks[0] != ks[0] || ks[1] != ks[1] ||
+                              ks[2] != ks[2] || ks[3] != ks[3];
+            float mx = kNegInf, need = kNegInf;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float kf = qs * ks[g];
+                float gm = kNegInf;
+#pragma unroll
+                for (int j = 0; j < 16; ++j) x[g][j] *= kf;
+                if (edge) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int back = pos - (first + 16 * g + j);
+                        if (back < 0 || (p.window > 0 && back >= p.window)) x[g][j] = kNegInf;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) gm = fmaxf(gm, x[g][j]);
+                mx = fmaxf(mx, gm);
+                need = fmaxf(need, ceilf(gm) + ve[g]);
+            }
+            const float m2 = fmaxf(m, ceilf(mx));
+            l *= pow2i(m - m2);
+            m = m2;
+            // the products of the stage before have read P and written O
+            if (n > 0 && !wait(ct, &ct.pvdone, (n - 1) & 1)) return;
+            tc_fence_after();
+            const bool grow = need > M + 1.f;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float f = grow ? pow2i(M - need) : 1.f;
+                if (grow) M = need;
+                if (i > 0) {
+#pragma unroll 2
+                    for (int j = 0; j < D; j += 16) {
+                        float y[16];
+                        tmem_ld16(so + j, y);
+                        tmem_ld_wait();
+                        float a[8], b[8];
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) { a[q] = y[q] * f; b[q] = y[8 + q] * f; }
+                        tmem_st8(so + j, a);
+                        tmem_st8(so + j + 8, b);
+                    }
+                    tmem_st_wait();
+                }
+            }
+            const float mref = m == kNegInf ? 0.f : m, fm = pow2i(fminf(m - M + kBias, 126.f));
+            uint8_t* prow = smem + Smem<D>::pw + r * 128;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const float f = fm * vs[g];
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float e0 = ex2(x[g][2 * j] - mref), e1 = ex2(x[g][2 * j + 1] - mref);
+                    l += e0 + e1;
+                    float w0 = e0 * f, w1 = e1 * f;
+                    if (edge) {  // a hidden position weighs nothing even where the value scale is NaN
+                        if (x[g][2 * j] == kNegInf) w0 = 0.f;
+                        if (x[g][2 * j + 1] == kNegInf) w1 = 0.f;
+                    }
+                    w[j] = pack_half(w0, w1);
+                }
+                *reinterpret_cast<uint4*>(prow + (((2 * g) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(prow + (((2 * g + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+            fence_async_smem();
+            tc_fence_before();
+            mbar_arrive(&ct.pfull);
+        }
+        // the row leaves
+        if (!wait(ct, &ct.pvdone, (n - 1) & 1)) return;
+        tc_fence_after();
+        float* part = p.part + ((size_t)blockIdx.x * 2 + (s.first ? 0 : 1)) * tile_floats(D, kRows);
+        const size_t at = ((size_t)s.b * p.c.T + tok) * p.Hq + head;
+        const float f = M - m - kBias;  // sums are in units of 2^(M - 14), l in units of 2^m
+        const float inv = M == kNegInf ? (l == l ? 0.f : l) : ldexpf(1.f / l, (int)fminf(fmaxf(f, -140.f), 120.f));
+#pragma unroll 2
+        for (int j = 0; j < D; j += 16) {
+            float y[16];
+            __syncwarp();
+            tmem_ld16(so + j, y);
+            tmem_ld_wait();
+            if (!E4M3) {  // back to the order of the channels
+#pragma unroll
+                for (int q = 0; q < 16; q += 4) {
+                    const float z = y[q + 1];
+                    y[q + 1] = y[q + 2];
+                    y[q + 2] = z;
+                }
+            }
+            if (on && s.whole) {
+                uint4 u[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+                    u[q] = make_uint4(pack_bf16(y[8 * q] * inv, y[8 * q + 1] * inv), pack_bf16(y[8 * q + 2] * inv, y[8 * q + 3] * inv),
+                                      pack_bf16(y[8 * q + 4] * inv, y[8 * q + 5] * inv), pack_bf16(y[8 * q + 6] * inv, y[8 * q + 7] * inv));
+                uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + j);
+                o[0] = u[0];
+                o[1] = u[1];
+            } else if (on) {
+                float4* o = reinterpret_cast<float4*>(part + (size_t)r * D + j);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) o[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+            }
+        }
+        tc_fence_before();
+        if (on) {
+            if (!s.whole) {
+                part[kRows * D + r] = l;
+                part[kRows * D + kRows + r] = m;
+                part[kRows * D + 2 * kRows + r] = M;
+            } else if (p.lse) {
+                p.lse[at] = (m + log2f(l)) * kLn2;
+            }
+        }
+    }
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(const AttnParams p) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Control& ct = *reinterpret_cast<Control*>(smem + Smem<D>::control);
+    const int warp = threadIdx.x >> 5;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (warp == 0) {
+        tmem_alloc(&ct.tmem, 256);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 32) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ct.kfull[i], 128);
+            mbar_init(&ct.kempty[i], 1);
+            mbar_init(&ct.vfull[i], 128);
+            mbar_init(&ct.vempty[i], 1);
+            mbar_init(&ct.sfull[i], 2);
+            mbar_init(&ct.sempty[i], 128);
+        }
+        mbar_init(&ct.pfull, 128);
+        mbar_init(&ct.pvdone, 1);
+        mbar_init(&ct.qfull, 128);
+        mbar_init(&ct.drain, 1);
+        ct.dead = 0;
+        fence_barrier_init();
+    }
+    Walk walk;
+    walk.start(p, threadIdx.x & 31);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp < 4) soften_rows<D, E4M3>(p, smem, ct, walk);
+    else if (warp < 8) convert_codes<D, E4M3>(p, smem, ct, walk);
+    else issue_products<D>(p, smem, ct, walk);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (ct.dead && threadIdx.x == 0 && p.c.status) *reinterpret_cast<volatile int32_t*>(p.c.status) = kErrTimeout;
+    if (warp == 0) tmem_dealloc(ct.tmem, 256);
+}
+
+// Joins the parts of a tile that several blocks worked on.  Block x: the tile, y: 32 of its rows, four
+// a warp.  Rows of no query get zeros (behind a sequence's tokens) or NaN (a sequence out of range).
+template <int D>
+__global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParams p, int blocks, int max_tiles) {
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b = blockIdx.x / (p.c.H * max_tiles), other = blockIdx.x % (p.c.H * max_tiles);
+    const int h = other / max_tiles, tile = other % max_tiles;
+    const int r0 = blockIdx.y * 32 + warp * 4;
+    int len, n;
+    const bool ok = cache_seq(p.c, b, len, n);
+    if (!ok) {
+        if (threadIdx.x == 0) flag_index_error(p.c);
+        n = 0;
+    }
+    for (int r = r0; r < r0 + 4; ++r) {
+        const int row = tile * kRows + r;
+        if (row < n * p.G || row >= p.c.T * p.G) continue;
+        const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
+        const float bad = __uint_as_float(0x7fc00000u);
+#pragma unroll
+        for (int j = 0; j < V; ++j) st_any(p.o, at * D + V * lane + j, p.out, ok ? 0.f : bad);
+        if (lane == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
+    }
+    if (tile * kRows >= n * p.G) {
+        wait_for_parts();
+        return;
+    }
+    long long total = 0, before = 0;
+    for (int i = lane; i < p.c.B; i += 32) {
+        const long long w = head_work(p, i) * p.c.H;
+        total += w;
+        if (i < b) before += w;
+    }
+    long long mine = 0, upto = 0;  // a head of this sequence; its tiles before this one
+    for (int i = lane; i < tiles_of(p, n); i += 32) {
+        const int cost = make_tile(p, len, n, i).stages + kTcOver;
+        mine += cost;
+        if (i < tile) upto += cost;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        total += __shfl_xor_sync(0xffffffffu, total, o);
+        before += __shfl_xor_sync(0xffffffffu, before, o);
+        mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        upto += __shfl_xor_sync(0xffffffffu, upto, o);
+    }
+    const long long a = before + h * mine + upto + kTcOver;  // the tile's first stage on the line
+    const int stages = make_tile(p, len, n, tile).stages, used = blocks_used(total, blocks);
+    const int first = holder(total, a, used), last = holder(total, a + stages - 1, used);
+    wait_for_parts();
+    if (first == last) return;  // finished by its block
+    const float* head = p.part + ((size_t)first * 2 + (share(total, first, used) >= a - kTcOver ? 0 : 1)) * tile_floats(D, kRows);
+    for (int r = r0; r < r0 + 4; ++r) {
+        const int row = tile * kRows + r;
+        if (row >= n * p.G) return;
+        float m = kNegInf, M = kNegInf, l = 0.f, sum[V] = {};
+        for (int i = first; i <= last; ++i) {
+            const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, kRows);
+            const float pl = in[kRows * D + r], pm = in[kRows * D + kRows + r], pM = in[kRows * D + 2 * kRows + r];
+            const float m2 = fmaxf(m, pm), M2 = fmaxf(M, pM);
+            const float l1 = pow2i(m - m2), l2 = pow2i(pm - m2), s1 = pow2i(M - M2), s2 = pow2i(pM - M2);
+            l = (l == l ? l * l1 : l) + (pl == pl ? pl * l2 : pl);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float x = in[(size_t)r * D + V * lane + j];
+                sum[j] = (sum[j] == sum[j] ? sum[j] * s1 : sum[j]) + (x == x ? x * s2 : x);
+            }
+            m = m2;
+            M = M2;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) write_row(p, b, h, row, V * lane + j, D, sum[j], l, m, M);
+    }
+}
+
+template <int D, bool E4M3>
+cudaError_t launch(const AttnParams& p, cudaStream_t st) {
+    static std::atomic<unsigned long long> ready{0};
+    constexpr int smem = Smem<D>::bytes;
+    if (cudaError_t e = set_smem_once(cache_attn_tc_kernel<D, E4M3>, smem, ready); e != cudaSuccess) return e;
+    static const int resident = resident_blocks(cache_attn_tc_kernel<D, E4M3>, kTcThreads, smem);
+    if (resident <= 0) return cudaErrorUnknown;
+    const int blocks = resident < kMaxTcBlocks ? resident : kMaxTcBlocks;
+    {
+        TraceScope ts("cache_attn_tc", st);
+        cache_attn_tc_kernel<D, E4M3><<<blocks, kTcThreads, smem, st>>>(p);
+        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    }
+    const int max_tiles = (p.c.T * p.G + kRows - 1) / kRows;
+    TraceScope ts("cache_attn_tc_join", st);
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.c.B * p.c.H * max_tiles, kRows / 32);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, cache_attn_tc_join_kernel<D>, p, blocks, max_tiles);
+}
+
+}  // namespace
+
+size_t cache_attn_tc_bytes(int d) { return (size_t)kMaxTcBlocks * 2 * tile_floats(d, kRows) * sizeof(float); }
+
+cudaError_t cache_attn_tc(const AttnParams& p, cudaStream_t st) {
+    if (p.c.code == DR_CODE_E4M3) return p.c.d == 128 ? launch<128, true>(p, st) : launch<64, true>(p, st);
+    return p.c.d == 128 ? launch<128, false>(p, st) : launch<64, false>(p, st);
+}
+
+}  // namespace dr

@@ -97,8 +97,13 @@ template <> struct Vec8<float> {
 
 // Block x: sequence and its i-th touched page; y: head; z: keys or values.  A page is 128 to 2048
 // pieces of 8 values, NV of them a thread.  The new values are read once, into registers: 8 prompts of up to 4096 tokens (4 heads of 128, bf16) take 75 MB of traffic.
+// Blocks of a page's threads on an SM: as many as hold the new values and 32 registers more.
+constexpr int write_blocks(int threads, int value_regs) {
+    const int n = 65536 / (threads * (32 + value_regs));
+    return n < 2048 / threads ? n : 2048 / threads;
+}
 template <typename IN, bool E4M3, int THREADS, int NV>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, write_blocks(THREADS, NV * (int)sizeof(IN) * 2))
     cache_write_kernel(const CacheParams c, const IN* __restrict__ k, long long ld_k,
                        const IN* __restrict__ v, long long ld_v, int pages_per_seq) {
     __shared__ uint32_t red[THREADS / 32];
