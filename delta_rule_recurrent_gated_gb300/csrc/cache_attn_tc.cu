@@ -200,43 +200,59 @@ __device__ __forceinline__ void convert16(const uint4& u, uint4& x, uint4& y) {
 }
 
 // ------------------------------------------------------------------ warps 4-7: codes to operand tiles
-// Thread: row t % 64 of the stage, half t / 64 of its channels.
+// Thread t takes the 16-byte piece t % (d/16) of rows t / (d/16) + (2048/d) j, so that a warp reads
+// whole rows; with d = 128 row j of a thread lies in part j of the stage's four parts of 16 positions,
+// with d = 64 rows j = 0, 1 in parts 0 or 1 and 2 or 3.  Page numbers are read three stages ahead,
+// codes one stage ahead.
 template <int D, bool E4M3>
 __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
-    constexpr int V = D / 32;  // 16-byte pieces of a thread's half row
-    const int t = threadIdx.x - 128, row = t & 63, half = t >> 6;
+    constexpr int C = D / 16, V = kStage * C / 128, R = 128 / C;  // pieces of a row, of a thread; rows between them
+    const int t = threadIdx.x - 128, row0 = t / C, piece = t % C;
     uint32_t n = 0;  // stages so far
     Stretch s;
     while (walk.next(p, s)) {
-        struct Src { int id; float ks, vs; bool value; };
-        const int end = s.len + s.n, stages = s.upto - s.from;
+        const int end = s.len + s.n, stages = s.upto - s.from, base = (s.t.s0 + s.from) * kStage;
+        struct Ids { int id[V]; };
         auto lookup = [&](int i) {
-            const int pos = (s.t.s0 + s.from + i) * kStage + row, part = pos & ~15;
-            return i < stages && part < s.t.hi && part + 16 > s.t.lo ? cache_page(p.c, s.b, pos / p.c.page) : -2;
-        };
-        auto fetch = [&](uint4 (&x)[V], const uint8_t* pool, int i, int id) {
-            const int pos = (s.t.s0 + s.from + i) * kStage + row;
-            const bool on = id >= 0 && pos < end;  // behind the last position: zeros
-            const uint4* at = reinterpret_cast<const uint4*>(
-                pool + (((size_t)(on ? id : 0) * p.c.H + s.h) * p.c.page + pos % p.c.page) * D + half * (D / 2));
-#pragma unroll
-            for (int j = 0; j < V; ++j) x[j] = on ? __ldg(at + j) : make_uint4(0, 0, 0, 0);
-        };
-        auto write = [&](uint8_t* tile, const uint4 (&x)[V]) {
-            uint8_t* at = tile + (D == 128 ? half * kStage * 128 : 0) + row * 128;
-            const int c0 = D == 128 ? 0 : 4 * half;
+            Ids x;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                uint4 a, b;
-                convert16<E4M3>(x[j], a, b);
-                *reinterpret_cast<uint4*>(at + (((c0 + 2 * j) ^ (row & 7)) << 4)) = a;
-                *reinterpret_cast<uint4*>(at + (((c0 + 2 * j + 1) ^ (row & 7)) << 4)) = b;
+                const int part = (base + i * kStage + row0 + R * j) & ~15;
+                x.id[j] = i < stages && part < s.t.hi && part + 16 > s.t.lo ? cache_page(p.c, s.b, part / p.c.page) : -2;
+            }
+            return x;
+        };
+        auto fetch = [&](uint4 (&x)[V], const uint8_t* pool, int i, const Ids& ids) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int pos = base + i * kStage + row0 + R * j;
+                x[j] = make_uint4(0, 0, 0, 0);  // behind the last position, and where no row sees it: zeros
+                if (ids.id[j] >= 0 && pos < end)
+                    x[j] = __ldg(reinterpret_cast<const uint4*>(
+                        pool + (((size_t)ids.id[j] * p.c.H + s.h) * p.c.page + (pos & (p.c.page - 1))) * D + 16 * piece));
             }
         };
-        const bool tells = half == 0 && (row & 15) == 0;  // notes its part's scales
+        auto write = [&](uint8_t* tile, const uint4 (&x)[V]) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int row = row0 + R * j;
+                uint8_t* at = tile + (piece >> 2) * kStage * 128 + row * 128;
+                uint4 a, b;
+                convert16<E4M3>(x[j], a, b);
+                // the second 64 channels in the other order: the banks of a row's two blocks are the same
+                const int c0 = 2 * (piece & 3), swap = piece >> 2;
+                *reinterpret_cast<uint4*>(at + (((c0 + swap) ^ (row & 7)) << 4)) = swap ? b : a;
+                *reinterpret_cast<uint4*>(at + (((c0 + 1 - swap) ^ (row & 7)) << 4)) = swap ? a : b;
+            }
+        };
+        // threads 0 .. 3 note the scales of the stage's parts
+        auto part_page = [&](int i) {
+            const int part = base + i * kStage + 16 * t;
+            return t < 4 && i < stages && part < s.t.hi && part + 16 > s.t.lo ? cache_page(p.c, s.b, part / p.c.page) : -2;
+        };
         auto scales = [&](int id, float& ks, float& vs) {
             ks = vs = id == -1 ? __uint_as_float(0x7fc00000u) : 0.f;
-            if (tells && id >= 0) {
+            if (id >= 0) {
                 const size_t ph = (size_t)id * p.c.H + s.h;
                 ks = p.c.k_scale[ph];
                 vs = p.c.v_scale[ph];
@@ -244,32 +260,36 @@ __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem
         };
         uint4 k[V], v[V];
         float ks, vs;
-        int id = lookup(0), ahead = lookup(1);
-        fetch(k, p.c.k, 0, id);
-        fetch(v, p.c.v, 0, id);
-        scales(id, ks, vs);
+        Ids ids = lookup(0), one = lookup(1), two = lookup(2);
+        int mid = part_page(0), mid1 = part_page(1), mid2 = part_page(2);
+        fetch(k, p.c.k, 0, ids);
+        fetch(v, p.c.v, 0, ids);
+        scales(mid, ks, vs);
         for (int i = 0; i < stages; ++i, ++n) {
             const uint32_t buf = n & 1, parity = (n >> 1) & 1;
             if (!wait(ct, &ct.kempty[buf], parity ^ 1)) return;
-            if (tells) {
+            if (t < 4) {
                 StageMeta& m = ct.meta[n % kMetas];
-                m.ks[row >> 4] = ks;
-                m.vs[row >> 4] = vs;
-                m.ve[row >> 4] = id >= 0 ? scale_exponent(vs) : id == -1 ? 0.f : kNegInf;
-                if (id == -1) flag_index_error(p.c);
+                m.ks[t] = ks;
+                m.vs[t] = vs;
+                m.ve[t] = mid >= 0 ? scale_exponent(vs) : mid == -1 ? 0.f : kNegInf;
+                if (mid == -1) flag_index_error(p.c);
             }
             write(smem + Smem<D>::k + buf * kStage * D * 2, k);
             fence_async_smem();
             mbar_arrive(&ct.kfull[buf]);
-            fetch(k, p.c.k, i + 1, ahead);
+            fetch(k, p.c.k, i + 1, one);
             if (!wait(ct, &ct.vempty[buf], parity ^ 1)) return;
             write(smem + Smem<D>::v + buf * kStage * D * 2, v);
             fence_async_smem();
             mbar_arrive(&ct.vfull[buf]);
-            fetch(v, p.c.v, i + 1, ahead);
-            scales(ahead, ks, vs);
-            id = ahead;
-            ahead = lookup(i + 2);
+            fetch(v, p.c.v, i + 1, one);
+            scales(mid1, ks, vs);
+            mid = mid1;
+            mid1 = mid2;
+            mid2 = part_page(i + 3);
+            one = two;
+            two = lookup(i + 3);
         }
     }
 }
@@ -384,12 +404,6 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
             const int first = (s.t.s0 + s.from + i) * kStage;
             if (!wait(ct, &ct.sfull[buf], (n >> 1) & 1)) return;
             tc_fence_after();
-            float x[4][16];
-#pragma unroll
-            for (int g = 0; g < 4; ++g) tmem_ld16(tm + buf * kStage + 16 * g, x[g]);
-            tmem_ld_wait();
-            tc_fence_before();
-            mbar_arrive(&ct.sempty[buf]);
             const StageMeta& mt = ct.meta[n % kMetas];
             const float4 ks4 = *reinterpret_cast<const float4*>(mt.ks), vs4 = *reinterpret_cast<const float4*>(mt.vs);
             const float4 ve4 = *reinterpret_cast<const float4*>(mt.ve);
@@ -397,24 +411,38 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
             const float ve[4] = {ve4.x, ve4.y, ve4.z, ve4.w};
             const bool edge = first + kStage > all_hi || first < all_lo || ks[0] != ks[0] || ks[1] != ks[1] ||
                               ks[2] != ks[2] || ks[3] != ks[3];
-            float mx = kNegInf, need = kNegInf;
+            // S is read twice, for its maxima and for the weights, a part of 32 columns at a time
+            auto scores = [&](int half, float (&x)[2][16]) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float kf = qs * ks[g];
-                float gm = kNegInf;
+                for (int g = 0; g < 2; ++g) tmem_ld16(tm + buf * kStage + 32 * half + 16 * g, x[g]);
+                tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) x[g][j] *= kf;
-                if (edge) {
+                for (int g = 0; g < 2; ++g) {
+                    const float kf = qs * ks[2 * half + g];
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int back = pos - (first + 16 * g + j);
-                        if (back < 0 || (p.window > 0 && back >= p.window)) x[g][j] = kNegInf;
+                    for (int j = 0; j < 16; ++j) x[g][j] *= kf;
+                    if (edge) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const int back = pos - (first + 32 * half + 16 * g + j);
+                            if (back < 0 || (p.window > 0 && back >= p.window)) x[g][j] = kNegInf;
+                        }
                     }
                 }
+            };
+            float mx = kNegInf, need = kNegInf;
 #pragma unroll
-                for (int j = 0; j < 16; ++j) gm = fmaxf(gm, x[g][j]);
-                mx = fmaxf(mx, gm);
-                need = fmaxf(need, ceilf(gm) + ve[g]);
+            for (int half = 0; half < 2; ++half) {
+                float x[2][16];
+                scores(half, x);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    float gm = x[g][0];
+#pragma unroll
+                    for (int j = 1; j < 16; ++j) gm = fmaxf(gm, x[g][j]);
+                    mx = fmaxf(mx, gm);
+                    need = fmaxf(need, ceilf(gm) + ve[2 * half + g]);
+                }
             }
             const float m2 = fmaxf(m, ceilf(mx));
             l *= pow2i(m - m2);
@@ -444,22 +472,33 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
             const float mref = m == kNegInf ? 0.f : m, fm = pow2i(fminf(m - M + kBias, 126.f));
             uint8_t* prow = smem + Smem<D>::pw + r * 128;
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float f = fm * vs[g];
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float e0 = ex2(x[g][2 * j] - mref), e1 = ex2(x[g][2 * j + 1] - mref);
-                    l += e0 + e1;
-                    float w0 = e0 * f, w1 = e1 * f;
-                    if (edge) {  // a hidden position weighs nothing even where the value scale is NaN
-                        if (x[g][2 * j] == kNegInf) w0 = 0.f;
-                        if (x[g][2 * j + 1] == kNegInf) w1 = 0.f;
-                    }
-                    w[j] = pack_half(w0, w1);
+            for (int half = 0; half < 2; ++half) {
+                float x[2][16];
+                __syncwarp();
+                scores(half, x);
+                if (half == 1) {
+                    tc_fence_before();
+                    mbar_arrive(&ct.sempty[buf]);
                 }
-                *reinterpret_cast<uint4*>(prow + (((2 * g) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4*>(prow + (((2 * g + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    const float f = fm * vs[2 * half + g];
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float e0 = ex2(x[g][2 * j] - mref), e1 = ex2(x[g][2 * j + 1] - mref);
+                        l += e0 + e1;
+                        float w0 = e0 * f, w1 = e1 * f;
+                        if (edge) {  // a hidden position weighs nothing even where the value scale is NaN
+                            if (x[g][2 * j] == kNegInf) w0 = 0.f;
+                            if (x[g][2 * j + 1] == kNegInf) w1 = 0.f;
+                        }
+                        w[j] = pack_half(w0, w1);
+                    }
+                    const int c = 4 * half + 2 * g;
+                    *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(prow + (((c + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
             }
             fence_async_smem();
             tc_fence_before();
@@ -636,9 +675,12 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
     constexpr int smem = Smem<D>::bytes;
     if (cudaError_t e = set_smem_once(cache_attn_tc_kernel<D, E4M3>, smem, ready); e != cudaSuccess) return e;
-    static const int resident = resident_blocks(cache_attn_tc_kernel<D, E4M3>, kTcThreads, smem);
-    if (resident <= 0) return cudaErrorUnknown;
-    const int blocks = resident < kMaxTcBlocks ? resident : kMaxTcBlocks;
+    // all of an SM's shared memory for two blocks (they would run as well one after the other)
+    if (cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<D, E4M3>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                             cudaSharedmemCarveoutMaxShared);
+        e != cudaSuccess)
+        return e;
+    const int blocks = kMaxTcBlocks;
     {
         TraceScope ts("cache_attn_tc", st);
         cache_attn_tc_kernel<D, E4M3><<<blocks, kTcThreads, smem, st>>>(p);
