@@ -1,22 +1,25 @@
 // cache_attn_tc.cu -- attention of many query tokens of each sequence over the paged 8-bit cache
 // (dr.h, dr_cache_attn; bf16 queries and outputs): the products on the fifth-generation tensor cores.
 //
-// A block works on a tile of 128 rows (query tokens times the G query heads that share a cache head,
-// row = t * G + g) over a stretch of positions, in stages of 64:
-//   S = Q K^T   128 x 64, contraction d; two accumulators in tensor memory, used in turn
-//   O += P V    128 x d, contraction 64; one accumulator, which stays in tensor memory
-// Warps 4-7 read the codes and write them as 16-bit floats (exact) into the operand tiles of K and V,
-// two of each; warp 8 issues the products; warps 0-3 hold a row per thread: they read S, keep the
-// softmax statistics and write the weights P as operand tile.  Two blocks share an SM, so that the
-// products of one run while the other's warps convert.
+// A block works on a tile of 256 rows (query tokens times the G query heads that share a cache head,
+// row = t * G + g), two halves of 128, over a stretch of positions, in stages of 64:
+//   S = Q K^T   128 x 64 for each half, contraction d
+//   O += P V    128 x d for each half, contraction 64
+// Q, P, S and O live in tensor memory, all 512 columns of it: P takes the columns of its S. Shared
+// memory holds K and V alone, as 16-bit floats (exact), three stages of them, so the products read
+// 32 KB a stage and half from it (with Q and P there as well: 80 KB, 640 cycles for 540 of products).
+// Warps 8-11 read the codes and write the operand tiles; warp 12 issues the products, the halves in
+// turn, so that one half's weights are formed while the other's products run; warps 0-3 and 4-7 hold
+// a row per thread: they read S, keep the softmax statistics and write P.
 //
 // Softmax in base 2 with whole-number references, as in cache_attn.cu: p = 2^(s - m), l = sum p,
 // operand w = p vs 2^(m - M + 14).  The accumulator is rescaled (exactly, by a power of two) only when
 // a row's largest s + log2 vs passes M by more than 1, so an operand reaches 2^15 at most.
 //
-// The stages of all tiles form one line that is divided evenly among the blocks (two per SM); a tile
+// The stages of all tiles form one line that is divided evenly among the blocks (one per SM); a tile
 // that several blocks worked on is joined by a second kernel from their rows in the workspace.
 #include "attn_util.cuh"
+#include "f32x2.cuh"
 #include "tc.cuh"
 #include "trace.cuh"
 
@@ -25,11 +28,17 @@ namespace {
 
 using namespace tc;
 
-constexpr int kRows = 128, kStage = 64;
-constexpr int kTcThreads = 288;  // four warps of rows, four of codes, one that issues
+constexpr int kHalf = 128, kRows = 2 * kHalf, kStage = 64;
+constexpr int kTcThreads = 416;  // eight warps of rows, four of codes, one that issues
+constexpr int kCodeThread0 = 256;
+constexpr int kBuffers = 3;      // stages of K and V
 constexpr int kTcOver = 4;       // what a tile costs beside its stages, in stages
 constexpr int kMetas = 8;        // stages whose scales are kept: more than the warps can be apart
-constexpr int kMaxTcBlocks = 152 * 2;
+constexpr int kMaxTcBlocks = 152;
+// columns of tensor memory of half i
+__device__ __forceinline__ uint32_t s_col(int i) { return 64 * i; }        // S, and P over it
+__device__ __forceinline__ uint32_t o_col(int i) { return 128 + 128 * i; }
+__device__ __forceinline__ uint32_t q_col(int i) { return 384 + 64 * i; }
 
 // ------------------------------------------------------------------ the line of stages
 struct TcTile {
@@ -154,14 +163,15 @@ struct __align__(16) StageMeta {  // read as 16-byte words
     int pad[3];
 };
 struct Control {
-    uint64_t kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], sempty[2], pfull, pvdone, qfull, drain;
+    uint64_t kfull[kBuffers], kempty[kBuffers], vfull[kBuffers], vempty[kBuffers];
+    uint64_t sfull[2], pfull[2], ofull[2], qfull[2], drain;
     uint32_t tmem;
     volatile int dead;
     StageMeta meta[kMetas];
 };
 template <int D> struct Smem {
-    static constexpr int q = 0, k = kRows * D * 2, v = k + 2 * kStage * D * 2, pw = v + 2 * kStage * D * 2,
-                         control = pw + kRows * kStage * 2, bytes = control + 1024;
+    static constexpr int tile = kStage * D * 2, k = 0, v = kBuffers * tile, control = 2 * kBuffers * tile,
+                         bytes = control + 1024;
     static_assert(sizeof(Control) <= 1024, "control block");
 };
 
@@ -184,7 +194,14 @@ __device__ __forceinline__ bool wait(Control& ct, uint64_t* bar, uint32_t parity
     }
     return __all_sync(0xffffffffu, done);
 }
-// D[tmem] (+)= A B, 16-bit floats, fp32 accumulator.
+// D[tmem] (+)= A[tmem] B[smem], 16-bit floats (A: a row per lane, two values a column), fp32 accumulator.
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
     return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
@@ -199,7 +216,7 @@ __device__ __forceinline__ void convert16(const uint4& u, uint4& x, uint4& y) {
     codes_to_half<E4M3>(u.w, y.z, y.w);
 }
 
-// ------------------------------------------------------------------ warps 4-7: codes to operand tiles
+// ------------------------------------------------------------------ warps 8-11: codes to operand tiles
 // Thread t takes the 16-byte piece t % (d/16) of rows t / (d/16) + (2048/d) j, so that a warp reads
 // whole rows; with d = 128 row j of a thread lies in part j of the stage's four parts of 16 positions,
 // with d = 64 rows j = 0, 1 in parts 0 or 1 and 2 or 3.  Page numbers are read three stages ahead,
@@ -207,8 +224,8 @@ __device__ __forceinline__ void convert16(const uint4& u, uint4& x, uint4& y) {
 template <int D, bool E4M3>
 __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
     constexpr int C = D / 16, V = kStage * C / 128, R = 128 / C;  // pieces of a row, of a thread; rows between them
-    const int t = threadIdx.x - 128, row0 = t / C, piece = t % C;
-    uint32_t n = 0;  // stages so far
+    const int t = threadIdx.x - kCodeThread0, row0 = t / C, piece = t % C;
+    uint32_t n = 0, buf = 0, parity = 0;  // stages so far, n % kBuffers, n / kBuffers % 2
     Stretch s;
     while (walk.next(p, s)) {
         const int end = s.len + s.n, stages = s.upto - s.from, base = (s.t.s0 + s.from) * kStage;
@@ -266,7 +283,6 @@ __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem
         fetch(v, p.c.v, 0, ids);
         scales(mid, ks, vs);
         for (int i = 0; i < stages; ++i, ++n) {
-            const uint32_t buf = n & 1, parity = (n >> 1) & 1;
             if (!wait(ct, &ct.kempty[buf], parity ^ 1)) return;
             if (t < 4) {
                 StageMeta& m = ct.meta[n % kMetas];
@@ -275,12 +291,12 @@ __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem
                 m.ve[t] = mid >= 0 ? scale_exponent(vs) : mid == -1 ? 0.f : kNegInf;
                 if (mid == -1) flag_index_error(p.c);
             }
-            write(smem + Smem<D>::k + buf * kStage * D * 2, k);
+            write(smem + Smem<D>::k + buf * Smem<D>::tile, k);
             fence_async_smem();
             mbar_arrive(&ct.kfull[buf]);
             fetch(k, p.c.k, i + 1, one);
             if (!wait(ct, &ct.vempty[buf], parity ^ 1)) return;
-            write(smem + Smem<D>::v + buf * kStage * D * 2, v);
+            write(smem + Smem<D>::v + buf * Smem<D>::tile, v);
             fence_async_smem();
             mbar_arrive(&ct.vfull[buf]);
             fetch(v, p.c.v, i + 1, one);
@@ -290,62 +306,68 @@ __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem
             mid2 = part_page(i + 3);
             one = two;
             two = lookup(i + 3);
+            if (++buf == kBuffers) { buf = 0; parity ^= 1; }
         }
     }
 }
 
-// ------------------------------------------------------------------ warp 8: the products
+// ------------------------------------------------------------------ warp 12: the products
+// Products of one thread run in the order of their issue, so S of a stage, over the columns of the
+// stage before's P, follows that P's product, and its completion says that O has that product too.
 template <int D>
 __device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
     const int lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem), tm = ct.tmem;
-    const Tile q{base + Smem<D>::q, kRows}, pw{base + Smem<D>::pw, kRows};
-    uint32_t n = 0, tiles = 0;
-    auto scores = [&](uint32_t i) {
-        const uint32_t buf = i & 1, parity = (i >> 1) & 1;
-        if (!wait(ct, &ct.kfull[buf], parity) || !wait(ct, &ct.sempty[buf], parity ^ 1)) return false;
-        tc_fence_after();
-        if (lane == 0) {
-            const Tile k{base + Smem<D>::k + buf * kStage * D * 2, kStage};
-#pragma unroll
-            for (int kk = 0; kk < D; kk += 16)
-                mma_bf16(tm + buf * kStage, desc_kmajor(q, kk), desc_kmajor(k, kk), idesc_f16(kRows, kStage, false),
-                         kk > 0);
-            mma_commit(&ct.kempty[buf]);
-            mbar_arrive(&ct.sfull[buf]);  // hands on the scales, which came with kfull
-            mma_commit(&ct.sfull[buf]);
-        }
-        __syncwarp();
-        return true;
-    };
-    auto values = [&](uint32_t i, bool accumulate) {
-        const uint32_t buf = i & 1, parity = (i >> 1) & 1;
-        if (!wait(ct, &ct.vfull[buf], parity) || !wait(ct, &ct.pfull, i & 1)) return false;
-        tc_fence_after();
-        if (lane == 0) {
-            const Tile v{base + Smem<D>::v + buf * kStage * D * 2, kStage};
-#pragma unroll
-            for (int kk = 0; kk < kStage; kk += 16)
-                mma_bf16(tm + 2 * kStage, desc_kmajor(pw, kk), desc_mnmajor(v, kk), idesc_f16(kRows, D, true),
-                         accumulate || kk > 0);
-            mma_commit(&ct.vempty[buf]);
-            mma_commit(&ct.pvdone);
-        }
-        __syncwarp();
-        return true;
-    };
+    uint32_t buf = 0, parity = 0, vbuf = 0, vparity = 0;
+    uint32_t n0 = 0, n1 = 0, tiles0 = 0, tiles1 = 0;  // stages and tiles of each half so far
     Stretch s;
     bool ok = true;
     while (ok && walk.next(p, s)) {
         const int stages = s.upto - s.from;
-        ok = wait(ct, &ct.qfull, tiles & 1);
-        ++tiles;
-        for (int i = 0; ok && i < stages; ++i) {
-            ok = scores(n + i);
-            if (ok && i > 0) ok = values(n + i - 1, i > 1);
+        const int halves = s.t.row0 + kHalf < s.n * p.G ? 2 : 1;
+        for (int i = 0; ok && i <= stages; ++i) {
+            for (int hf = 0; ok && hf < halves; ++hf) {
+                if (i > 0) {  // O += P V of stage i - 1
+                    ok = (hf > 0 || wait(ct, &ct.vfull[vbuf], vparity)) && wait(ct, &ct.pfull[hf], ((hf ? n1 : n0) + i - 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const Tile v{base + Smem<D>::v + vbuf * Smem<D>::tile, kStage};
+#pragma unroll
+                        for (int kk = 0; kk < kStage; kk += 16)
+                            mma_ts(tm + o_col(hf), tm + s_col(hf) + kk / 2, desc_mnmajor(v, kk),
+                                   idesc_f16(kHalf, D, true), i > 1 || kk > 0);
+                        if (hf == halves - 1) mma_commit(&ct.vempty[vbuf]);
+                        if (i == stages) mma_commit(&ct.ofull[hf]);
+                    }
+                    __syncwarp();
+                }
+                if (i < stages) {  // S = Q K^T of stage i
+                    ok = (hf > 0 || wait(ct, &ct.kfull[buf], parity)) && (i > 0 || wait(ct, &ct.qfull[hf], (hf ? tiles1 : tiles0) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const Tile k{base + Smem<D>::k + buf * Smem<D>::tile, kStage};
+#pragma unroll
+                        for (int kk = 0; kk < D; kk += 16)
+                            mma_ts(tm + s_col(hf), tm + q_col(hf) + kk / 2, desc_kmajor(k, kk),
+                                   idesc_f16(kHalf, kStage, false), kk > 0);
+                        mbar_arrive(&ct.sfull[hf]);  // hands on the scales, which came with kfull
+                        mma_commit(&ct.sfull[hf]);
+                        if (hf == halves - 1) mma_commit(&ct.kempty[buf]);
+                    }
+                    __syncwarp();
+                }
+            }
+            if (i > 0 && ++vbuf == kBuffers) { vbuf = 0; vparity ^= 1; }
+            if (i < stages && ++buf == kBuffers) { buf = 0; parity ^= 1; }
         }
-        if (ok) ok = values(n + stages - 1, stages > 1);
-        n += stages;
+        n0 += stages;
+        ++tiles0;
+        if (halves == 2) {
+            n1 += stages;
+            ++tiles1;
+        }
     }
     if (!ok) {  // let what is in flight end before the tensor memory goes
         if (lane == 0) mma_commit(&ct.drain);
@@ -353,19 +375,24 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* sme
     }
 }
 
-// ------------------------------------------------------------------ warps 0-3: a row per thread
+// ------------------------------------------------------------------ warps 0-7: a row per thread
 template <int D, bool E4M3>
-__device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
-    const int r = threadIdx.x;
-    const uint32_t tm = warp_lane_base(ct.tmem);
-    const uint32_t so = tm + 2 * kStage;  // this row of O
-    uint32_t n = 0;
+__device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Walk walk) {
+    const int hf = threadIdx.x / kHalf, r = threadIdx.x % kHalf;
+    const uint32_t tm = warp_lane_base(ct.tmem), ts = tm + s_col(hf), to = tm + o_col(hf);
+    uint32_t n = 0;  // stages that this half has seen
+    uint32_t all = 0;  // and that the block has
+    uint32_t tiles = 0;
     Stretch s;
     while (walk.next(p, s)) {
-        const int stages = s.upto - s.from, row = s.t.row0 + r;
+        const int stages = s.upto - s.from, row = s.t.row0 + hf * kHalf + r;
+        if (s.t.row0 + hf * kHalf >= s.n * p.G) {  // no rows in this half
+            all += stages;
+            continue;
+        }
         const bool on = row < s.n * p.G;
         const int tok = on ? row / p.G : 0, head = s.h * p.G + (on ? row % p.G : 0), pos = on ? s.len + tok : -1;
-        // the row's queries, scaled, as operand
+        // the row's queries, scaled, as operand (with the sign of the scale, so that factors are positive)
         const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
                                                          ((long long)s.b * p.c.T + tok) * p.ld_q + (long long)head * D);
         float top = 0.f;
@@ -379,134 +406,139 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
         int e;
         float up, rest;
         query_scale(top, e, up, rest);
-#pragma unroll 4
-        for (int j = 0; j < D / 8; ++j) {
-            float x[8];
-            unpack8(on ? __ldg(qp + j) : make_uint4(0, 0, 0, 0), x);
+        if (p.scale < 0.f) up = -up;
+#pragma unroll 2
+        for (int j = 0; j < D / 8; j += 2) {
+            float u[8];  // 16 queries, two a column
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * up * rest;
-            uint4 u;
-            if (E4M3) {
-                u = make_uint4(pack_half(x[0], x[1]), pack_half(x[2], x[3]), pack_half(x[4], x[5]), pack_half(x[6], x[7]));
-            } else {
-                u = make_uint4(pack_half(x[0], x[2]), pack_half(x[1], x[3]), pack_half(x[4], x[6]), pack_half(x[5], x[7]));
+            for (int i = 0; i < 2; ++i) {
+                float x[8];
+                unpack8(on ? __ldg(qp + j + i) : make_uint4(0, 0, 0, 0), x);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) x[q] = x[q] * up * rest;
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    u[4 * i + 2 * q] = __uint_as_float(pack_half(x[4 * q], x[4 * q + (E4M3 ? 1 : 2)]));
+                    u[4 * i + 2 * q + 1] = __uint_as_float(pack_half(x[4 * q + (E4M3 ? 2 : 1)], x[4 * q + 3]));
+                }
             }
-            *reinterpret_cast<uint4*>(smem + Smem<D>::q + (j >> 3) * kRows * 128 + r * 128 + (((j & 7) ^ (r & 7)) << 4)) = u;
+            __syncwarp();
+            tmem_st8(tm + q_col(hf) + 4 * j, u);
         }
-        fence_async_smem();
-        mbar_arrive(&ct.qfull);
-        const float qs = ldexpf(p.scale * kLog2e, e);
-        // positions that every row sees need no mask
-        const int all_hi = s.len + s.t.t0 + 1, all_lo = p.window > 0 ? max(0, s.len + s.t.t1 - p.window + 1) : 0;
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&ct.qfull[hf]);
+        const float qs = ldexpf(fabsf(p.scale) * kLog2e, e);
+        // positions that every row of the half sees need no mask
+        const int t0 = (s.t.row0 + hf * kHalf) / p.G, t1 = min(s.n - 1, (s.t.row0 + hf * kHalf + kHalf - 1) / p.G);
+        const int all_hi = s.len + t0 + 1, all_lo = p.window > 0 ? max(0, s.len + t1 - p.window + 1) : 0;
         float l = 0.f, m = kNegInf, M = kNegInf;
-        for (int i = 0; i < stages; ++i, ++n) {
-            const uint32_t buf = n & 1;
+        for (int i = 0; i < stages; ++i, ++n, ++all) {
             const int first = (s.t.s0 + s.from + i) * kStage;
-            if (!wait(ct, &ct.sfull[buf], (n >> 1) & 1)) return;
+            if (!wait(ct, &ct.sfull[hf], n & 1)) return;
             tc_fence_after();
-            const StageMeta& mt = ct.meta[n % kMetas];
+            const StageMeta& mt = ct.meta[all % kMetas];
             const float4 ks4 = *reinterpret_cast<const float4*>(mt.ks), vs4 = *reinterpret_cast<const float4*>(mt.vs);
             const float4 ve4 = *reinterpret_cast<const float4*>(mt.ve);
-            const float ks[4] = {ks4.x, ks4.y, ks4.z, ks4.w}, vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
+            float kf[4] = {qs * ks4.x, qs * ks4.y, qs * ks4.z, qs * ks4.w}, vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
             const float ve[4] = {ve4.x, ve4.y, ve4.z, ve4.w};
-            const bool edge = first + kStage > all_hi || first < all_lo || ks[0] != ks[0] || ks[1] != ks[1] ||
-                              ks[2] != ks[2] || ks[3] != ks[3];
-            // S is read twice, for its maxima and for the weights, a part of 32 columns at a time
-            auto scores = [&](int half, float (&x)[2][16]) {
+            const float sum = (ks4.x + ks4.y) + (ks4.z + ks4.w);
+            if (first + kStage > all_hi || first < all_lo || sum != sum) {
+                // Hidden positions become -inf in tensor memory, so that the code below knows no mask.  A part
+                // whose key scale is NaN makes what it shows NaN; a part that shows nothing weighs nothing, even
+                // where its value scale is NaN (in a row that sees some of it everything is NaN anyway).
 #pragma unroll
-                for (int g = 0; g < 2; ++g) tmem_ld16(tm + buf * kStage + 32 * half + 16 * g, x[g]);
-                tmem_ld_wait();
+                for (int g = 0; g < 4; ++g) {
+                    float x[16];
+                    __syncwarp();
+                    tmem_ld16(ts + 16 * g, x);
+                    tmem_ld_wait();
+                    const bool bad = kf[g] != kf[g];
+                    bool any = false;
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float kf = qs * ks[2 * half + g];
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) x[g][j] *= kf;
-                    if (edge) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const int back = pos - (first + 32 * half + 16 * g + j);
-                            if (back < 0 || (p.window > 0 && back >= p.window)) x[g][j] = kNegInf;
-                        }
+                    for (int j = 0; j < 16; ++j) {
+                        const int back = pos - (first + 16 * g + j);
+                        const bool see = back >= 0 && (p.window == 0 || back < p.window);
+                        any |= see;
+                        x[j] = see ? (bad ? kf[g] : x[j]) : kNegInf;
                     }
+                    if (bad) kf[g] = 1.f;
+                    if (!any) vs[g] = 0.f;
+                    float a[8], b[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) { a[q] = x[q]; b[q] = x[8 + q]; }
+                    tmem_st8(ts + 16 * g, a);
+                    tmem_st8(ts + 16 * g + 8, b);
                 }
-            };
+                tmem_st_wait();
+            }
+            __syncwarp();
+            float x[4][16];
+#pragma unroll
+            for (int g = 0; g < 4; ++g) tmem_ld16(ts + 16 * g, x[g]);
+            tmem_ld_wait();
             float mx = kNegInf, need = kNegInf;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float x[2][16];
-                scores(half, x);
+            for (int g = 0; g < 4; ++g) {
+                float gm = fmaxf(x[g][0], x[g][1]);
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    float gm = x[g][0];
-#pragma unroll
-                    for (int j = 1; j < 16; ++j) gm = fmaxf(gm, x[g][j]);
-                    mx = fmaxf(mx, gm);
-                    need = fmaxf(need, ceilf(gm) + ve[2 * half + g]);
-                }
+                for (int j = 2; j < 16; j += 2) gm = fmaxf(gm, fmaxf(x[g][j], x[g][j + 1]));
+                kf[g] = fmaxf(kf[g], 1e-37f);  // a zero factor and -inf make no NaN
+                gm *= kf[g];
+                mx = fmaxf(mx, gm);
+                need = fmaxf(need, ceilf(gm) + ve[g]);
             }
             const float m2 = fmaxf(m, ceilf(mx));
             l *= pow2i(m - m2);
             m = m2;
-            // the products of the stage before have read P and written O
-            if (n > 0 && !wait(ct, &ct.pvdone, (n - 1) & 1)) return;
-            tc_fence_after();
             const bool grow = need > M + 1.f;
             if (__any_sync(0xffffffffu, grow)) {
                 const float f = grow ? pow2i(M - need) : 1.f;
                 if (grow) M = need;
                 if (i > 0) {
-#pragma unroll 2
+#pragma unroll 1
                     for (int j = 0; j < D; j += 16) {
                         float y[16];
-                        tmem_ld16(so + j, y);
+                        __syncwarp();
+                        tmem_ld16(to + j, y);
                         tmem_ld_wait();
                         float a[8], b[8];
 #pragma unroll
                         for (int q = 0; q < 8; ++q) { a[q] = y[q] * f; b[q] = y[8 + q] * f; }
-                        tmem_st8(so + j, a);
-                        tmem_st8(so + j + 8, b);
+                        tmem_st8(to + j, a);
+                        tmem_st8(to + j + 8, b);
                     }
-                    tmem_st_wait();
                 }
             }
             const float mref = m == kNegInf ? 0.f : m, fm = pow2i(fminf(m - M + kBias, 126.f));
-            uint8_t* prow = smem + Smem<D>::pw + r * 128;
+            float2 l2 = make_float2(0.f, 0.f);
+            const float2 nm = make_float2(-mref, -mref);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float x[2][16];
+            for (int g = 0; g < 4; ++g) {
+                const float2 f = make_float2(fm * vs[g], fm * vs[g]), k2 = make_float2(kf[g], kf[g]);
+                float w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float2 z = fma2(make_float2(x[g][2 * j], x[g][2 * j + 1]), k2, nm);
+                    z.x = ex2(z.x);
+                    z.y = ex2(z.y);
+                    l2 = add2(l2, z);
+                    z = mul2(z, f);
+                    w[j] = __uint_as_float(pack_half(z.x, z.y));
+                }
                 __syncwarp();
-                scores(half, x);
-                if (half == 1) {
-                    tc_fence_before();
-                    mbar_arrive(&ct.sempty[buf]);
-                }
-#pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    const float f = fm * vs[2 * half + g];
-                    uint32_t w[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float e0 = ex2(x[g][2 * j] - mref), e1 = ex2(x[g][2 * j + 1] - mref);
-                        l += e0 + e1;
-                        float w0 = e0 * f, w1 = e1 * f;
-                        if (edge) {  // a hidden position weighs nothing even where the value scale is NaN
-                            if (x[g][2 * j] == kNegInf) w0 = 0.f;
-                            if (x[g][2 * j + 1] == kNegInf) w1 = 0.f;
-                        }
-                        w[j] = pack_half(w0, w1);
-                    }
-                    const int c = 4 * half + 2 * g;
-                    *reinterpret_cast<uint4*>(prow + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4*>(prow + (((c + 1) ^ (r & 7)) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
-                }
+                tmem_st8(ts + 8 * g, w);
             }
-            fence_async_smem();
+            l += l2.x + l2.y;
+            tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&ct.pfull);
+            mbar_arrive(&ct.pfull[hf]);
         }
         // the row leaves
-        if (!wait(ct, &ct.pvdone, (n - 1) & 1)) return;
+        if (!wait(ct, &ct.ofull[hf], tiles & 1)) return;
+        ++tiles;
         tc_fence_after();
+        const int rr = hf * kHalf + r;
         float* part = p.part + ((size_t)blockIdx.x * 2 + (s.first ? 0 : 1)) * tile_floats(D, kRows);
         const size_t at = ((size_t)s.b * p.c.T + tok) * p.Hq + head;
         const float f = M - m - kBias;  // sums are in units of 2^(M - 14), l in units of 2^m
@@ -515,7 +547,7 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
         for (int j = 0; j < D; j += 16) {
             float y[16];
             __syncwarp();
-            tmem_ld16(so + j, y);
+            tmem_ld16(to + j, y);
             tmem_ld_wait();
             if (!E4M3) {  // back to the order of the channels
 #pragma unroll
@@ -535,7 +567,7 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
                 o[0] = u[0];
                 o[1] = u[1];
             } else if (on) {
-                float4* o = reinterpret_cast<float4*>(part + (size_t)r * D + j);
+                float4* o = reinterpret_cast<float4*>(part + (size_t)rr * D + j);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) o[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
             }
@@ -543,9 +575,9 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
         tc_fence_before();
         if (on) {
             if (!s.whole) {
-                part[kRows * D + r] = l;
-                part[kRows * D + kRows + r] = m;
-                part[kRows * D + 2 * kRows + r] = M;
+                part[kRows * D + rr] = l;
+                part[kRows * D + kRows + rr] = m;
+                part[kRows * D + 2 * kRows + rr] = M;
             } else if (p.lse) {
                 p.lse[at] = (m + log2f(l)) * kLn2;
             }
@@ -554,27 +586,28 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
 }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const AttnParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Control& ct = *reinterpret_cast<Control*>(smem + Smem<D>::control);
     const int warp = threadIdx.x >> 5;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) {
-        tmem_alloc(&ct.tmem, 256);
+        tmem_alloc(&ct.tmem, 512);
         tmem_relinquish();
     }
     if (threadIdx.x == 32) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kBuffers; ++i) {
             mbar_init(&ct.kfull[i], 128);
             mbar_init(&ct.kempty[i], 1);
             mbar_init(&ct.vfull[i], 128);
             mbar_init(&ct.vempty[i], 1);
-            mbar_init(&ct.sfull[i], 2);
-            mbar_init(&ct.sempty[i], 128);
         }
-        mbar_init(&ct.pfull, 128);
-        mbar_init(&ct.pvdone, 1);
-        mbar_init(&ct.qfull, 128);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ct.sfull[i], 2);
+            mbar_init(&ct.pfull[i], kHalf);
+            mbar_init(&ct.ofull[i], 1);
+            mbar_init(&ct.qfull[i], kHalf);
+        }
         mbar_init(&ct.drain, 1);
         ct.dead = 0;
         fence_barrier_init();
@@ -584,14 +617,14 @@ __global__ void __launch_bounds__(kTcThreads, 2) cache_attn_tc_kernel(const Attn
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp < 4) soften_rows<D, E4M3>(p, smem, ct, walk);
-    else if (warp < 8) convert_codes<D, E4M3>(p, smem, ct, walk);
+    if (warp < 8) soften_rows<D, E4M3>(p, ct, walk);
+    else if (warp < 12) convert_codes<D, E4M3>(p, smem, ct, walk);
     else issue_products<D>(p, smem, ct, walk);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (ct.dead && threadIdx.x == 0 && p.c.status) *reinterpret_cast<volatile int32_t*>(p.c.status) = kErrTimeout;
-    if (warp == 0) tmem_dealloc(ct.tmem, 256);
+    if (warp == 0) tmem_dealloc(ct.tmem, 512);
 }
 
 // Joins the parts of a tile that several blocks worked on.  Block x: the tile, y: 32 of its rows, four
@@ -675,11 +708,6 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
     constexpr int smem = Smem<D>::bytes;
     if (cudaError_t e = set_smem_once(cache_attn_tc_kernel<D, E4M3>, smem, ready); e != cudaSuccess) return e;
-    // all of an SM's shared memory for two blocks (they would run as well one after the other)
-    if (cudaError_t e = cudaFuncSetAttribute(cache_attn_tc_kernel<D, E4M3>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                             cudaSharedmemCarveoutMaxShared);
-        e != cudaSuccess)
-        return e;
     const int blocks = kMaxTcBlocks;
     {
         TraceScope ts("cache_attn_tc", st);

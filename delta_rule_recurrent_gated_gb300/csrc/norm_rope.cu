@@ -14,6 +14,7 @@
 // pairs of fp32 values (fma.rn.f32x2).  Both kernels are bound by HBM at the sizes of training:
 // each value is read and written once.
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "rope.cuh"
 #include "trace.cuh"
 
@@ -24,25 +25,6 @@ constexpr int kRopeThreads = 256;
 constexpr int kRun = 4;                           // heads of a run, at most; bf16: all loaded at once
 constexpr int kBwdResident = 2;                   // blocks of the backward kernel on an SM
 constexpr int kBwdBlocks = 152 * kBwdResident;    // over all runs of heads
-
-// Pairs of fp32 values.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-        " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // A thread's 8 channels as loaded: two pieces of 4.
 template <typename T>
