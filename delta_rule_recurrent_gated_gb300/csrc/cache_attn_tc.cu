@@ -8,9 +8,10 @@
 // Q, P, S and O live in tensor memory, all 512 columns of it: P takes the columns of its S. Shared
 // memory holds K and V alone, as 16-bit floats (exact), three stages of them, so the products read
 // 32 KB a stage and half from it (with Q and P there as well: 80 KB, 640 cycles for 540 of products).
-// Warps 8-11 read the codes and write the operand tiles; warp 12 issues the products, the halves in
-// turn, so that one half's weights are formed while the other's products run; warps 0-3 and 4-7 hold
-// a row per thread: they read S, keep the softmax statistics and write P.
+// Warp 13 has the codes copied to a ring in shared memory; warps 8-11 turn them into the operand
+// tiles; warp 12 issues the products, the halves in turn, so that one half's weights are formed while
+// the other's products run; warps 0-3 and 4-7 hold a row per thread: they read S, keep the softmax
+// statistics and write P.
 //
 // Softmax in base 2 with whole-number references, as in cache_attn.cu: p = 2^(s - m), l = sum p,
 // operand w = p vs 2^(m - M + 14).  The accumulator is rescaled (exactly, by a power of two) only when
@@ -29,9 +30,10 @@ namespace {
 using namespace tc;
 
 constexpr int kHalf = 128, kRows = 2 * kHalf, kStage = 64;
-constexpr int kTcThreads = 416;  // eight warps of rows, four of codes, one that issues
+constexpr int kTcThreads = 448;  // eight warps of rows, four of codes, one that issues, one that copies
 constexpr int kCodeThread0 = 256;
-constexpr int kBuffers = 3;      // stages of K and V
+constexpr int kBuffers = 3;      // stages of K and V as operands
+constexpr int kRaw = 4;          // as codes
 constexpr int kTcOver = 4;       // what a tile costs beside its stages, in stages
 constexpr int kMetas = 8;        // stages whose scales are kept: more than the warps can be apart
 constexpr int kMaxTcBlocks = 152;
@@ -159,24 +161,35 @@ struct Walk {
 // ------------------------------------------------------------------ shared memory
 struct __align__(16) StageMeta {  // read as 16-byte words
     float ks[4], vs[4], ve[4];  // of the four 16-position parts
-    int bad;                    // a part whose page number is out of range
-    int pad[3];
+    int id[4];                  // their pages: -1 out of range, -2 seen by no row
 };
 struct Control {
-    uint64_t kfull[kBuffers], kempty[kBuffers], vfull[kBuffers], vempty[kBuffers];
+    uint64_t rfull[kRaw], rempty[kRaw], kfull[kBuffers], kempty[kBuffers], vfull[kBuffers], vempty[kBuffers];
     uint64_t sfull[2], pfull[2], ofull[2], qfull[2], drain;
     uint32_t tmem;
     volatile int dead;
     StageMeta meta[kMetas];
 };
 template <int D> struct Smem {
-    static constexpr int tile = kStage * D * 2, k = 0, v = kBuffers * tile, control = 2 * kBuffers * tile,
-                         bytes = control + 1024;
+    static constexpr int tile = kStage * D * 2, codes = kStage * D, k = 0, v = kBuffers * tile,
+                         raw = 2 * kBuffers * tile, control = raw + 2 * kRaw * codes, bytes = control + 1024;
     static_assert(sizeof(Control) <= 1024, "control block");
 };
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// As mbar_try_wait, asleep for up to about 10 us instead of polling.
+__device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
+        : "memory");
+    return ok != 0;
 }
 // Bounded wait of a whole warp; false once it or any other of the block's waits has run out.
 __device__ __forceinline__ bool wait(Control& ct, uint64_t* bar, uint32_t parity) {
@@ -184,7 +197,7 @@ __device__ __forceinline__ bool wait(Control& ct, uint64_t* bar, uint32_t parity
     if (!done) {
         const uint64_t t0 = globaltimer_ns();
         while (true) {
-            for (int i = 0; i < 64 && !done; ++i) done = mbar_try_wait(bar, parity);
+            for (int i = 0; i < 16 && !done; ++i) done = mbar_try_wait_long(bar, parity);
             if (done || ct.dead) break;
             if (globaltimer_ns() - t0 > kWaitLimitNs) {
                 ct.dead = 1;
@@ -216,96 +229,116 @@ __device__ __forceinline__ void convert16(const uint4& u, uint4& x, uint4& y) {
     codes_to_half<E4M3>(u.w, y.z, y.w);
 }
 
+// ------------------------------------------------------------------ warp 13: copies
+// Lane 4 j + g holds page and scales of part g of the j-th of eight stages; the next eight stages'
+// are read while these are in use.
+template <int D>
+__device__ __forceinline__ void copy_pages(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
+    const int lane = threadIdx.x & 31, g = lane & 3;
+    const int rows = min(p.c.page, kStage), copies = kStage / rows;  // of a stage
+    uint32_t n = 0;
+    Stretch s;
+    bool ok = true;
+    while (ok && walk.next(p, s)) {
+        const int stages = s.upto - s.from, base = (s.t.s0 + s.from) * kStage;
+        struct Part { int id; float ks, vs; };
+        auto lookup = [&](int i) {
+            Part x;
+            const int part = base + i * kStage + 16 * g;
+            x.id = i < stages && part < s.t.hi && part + 16 > s.t.lo ? cache_page(p.c, s.b, part / p.c.page) : -2;
+            x.ks = x.vs = x.id == -1 ? __uint_as_float(0x7fc00000u) : 0.f;
+            if (x.id >= 0) {
+                const size_t ph = (size_t)x.id * p.c.H + s.h;
+                x.ks = p.c.k_scale[ph];
+                x.vs = p.c.v_scale[ph];
+            }
+            return x;
+        };
+        Part now, next = lookup(lane >> 2);
+        for (int i = 0; i < stages; ++i, ++n) {
+            if ((i & 7) == 0) {
+                now = next;
+                next = lookup(i + 8 + (lane >> 2));
+            }
+            const uint32_t buf = n % kRaw, parity = (n / kRaw) & 1;
+            ok = wait(ct, &ct.rempty[buf], parity ^ 1);
+            if (!ok) break;
+            if ((lane >> 2) == (i & 7)) {
+                StageMeta& m = ct.meta[n % kMetas];
+                m.ks[g] = now.ks;
+                m.vs[g] = now.vs;
+                m.ve[g] = now.id >= 0 ? scale_exponent(now.vs) : now.id == -1 ? 0.f : kNegInf;
+                m.id[g] = now.id;
+                if (now.id == -1) flag_index_error(p.c);
+            }
+            // copy c takes the page of its first part that is seen
+            int id = __shfl_sync(0xffffffffu, now.id, 4 * (i & 7) + g);
+            if (rows > 16) id = max(id, __shfl_xor_sync(0xffffffffu, id, 1));
+            if (rows > 32) id = max(id, __shfl_xor_sync(0xffffffffu, id, 2));
+            const int c = lane;  // lane c < copies issues copy c, of parts c * rows / 16 ..
+            id = __shfl_sync(0xffffffffu, id, min(c * (rows / 16), 3));
+            const bool mine = c < copies && id >= 0;
+            const int total = __popc(__ballot_sync(0xffffffffu, mine)) * 2 * rows * D;
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&ct.rfull[buf], total);
+            __syncwarp();
+            if (mine) {
+                const int first = base + i * kStage + c * rows;
+                const size_t off = (((size_t)id * p.c.H + s.h) * p.c.page + (first & (p.c.page - 1))) * D;
+                uint8_t* to = smem + Smem<D>::raw + buf * 2 * Smem<D>::codes + c * rows * D;
+                bulk_g2s(to, p.c.k + off, rows * D, &ct.rfull[buf]);
+                bulk_g2s(to + Smem<D>::codes, p.c.v + off, rows * D, &ct.rfull[buf]);
+            }
+        }
+    }
+    // no copy outlives the block, whatever became of the other warps
+    for (uint32_t m = n > kRaw ? n - kRaw : 0; m < n; ++m) mbar_wait(&ct.rfull[m % kRaw], (m / kRaw) & 1, kWaitLimitNs);
+}
+
 // ------------------------------------------------------------------ warps 8-11: codes to operand tiles
-// Thread t takes the 16-byte piece t % (d/16) of rows t / (d/16) + (2048/d) j, so that a warp reads
-// whole rows; with d = 128 row j of a thread lies in part j of the stage's four parts of 16 positions,
-// with d = 64 rows j = 0, 1 in parts 0 or 1 and 2 or 3.  Page numbers are read three stages ahead,
-// codes one stage ahead.
+// Warp w takes the 16 positions of part w, 8 rows and a 64-byte half row of each at a time; even and
+// odd rows take the other half (d = 128), which keeps reads and writes off each other's banks.
 template <int D, bool E4M3>
 __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
-    constexpr int C = D / 16, V = kStage * C / 128, R = 128 / C;  // pieces of a row, of a thread; rows between them
-    const int t = threadIdx.x - kCodeThread0, row0 = t / C, piece = t % C;
+    constexpr int IT = D / 64;  // half rows of a row
+    const int lane = threadIdx.x & 31, w = (threadIdx.x - kCodeThread0) >> 5;
+    const int r8 = lane >> 2, q = lane & 3;
     uint32_t n = 0, buf = 0, parity = 0;  // stages so far, n % kBuffers, n / kBuffers % 2
     Stretch s;
     while (walk.next(p, s)) {
         const int end = s.len + s.n, stages = s.upto - s.from, base = (s.t.s0 + s.from) * kStage;
-        struct Ids { int id[V]; };
-        auto lookup = [&](int i) {
-            Ids x;
+        // `keep`: rows of the part that hold a position; the others become zeros
+        auto convert = [&](const uint8_t* raw, uint8_t* tile, int keep) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int part = (base + i * kStage + row0 + R * j) & ~15;
-                x.id[j] = i < stages && part < s.t.hi && part + 16 > s.t.lo ? cache_page(p.c, s.b, part / p.c.page) : -2;
-            }
-            return x;
-        };
-        auto fetch = [&](uint4 (&x)[V], const uint8_t* pool, int i, const Ids& ids) {
+            for (int o = 0; o < 2; ++o)
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int pos = base + i * kStage + row0 + R * j;
-                x[j] = make_uint4(0, 0, 0, 0);  // behind the last position, and where no row sees it: zeros
-                if (ids.id[j] >= 0 && pos < end)
-                    x[j] = __ldg(reinterpret_cast<const uint4*>(
-                        pool + (((size_t)ids.id[j] * p.c.H + s.h) * p.c.page + (pos & (p.c.page - 1))) * D + 16 * piece));
-            }
+                for (int it = 0; it < IT; ++it) {
+                    const int row = 16 * w + 8 * o + r8, half = IT == 2 ? (row ^ it) & 1 : 0;
+                    uint4 u = *reinterpret_cast<const uint4*>(raw + row * D + half * 64 + q * 16);
+                    if (8 * o + r8 >= keep) u = make_uint4(0, 0, 0, 0);
+                    uint4 a, b;
+                    convert16<E4M3>(u, a, b);
+                    uint8_t* at = tile + half * kStage * 128 + row * 128;
+                    *reinterpret_cast<uint4*>(at + (((2 * q) ^ (row & 7)) << 4)) = a;
+                    *reinterpret_cast<uint4*>(at + (((2 * q + 1) ^ (row & 7)) << 4)) = b;
+                }
         };
-        auto write = [&](uint8_t* tile, const uint4 (&x)[V]) {
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int row = row0 + R * j;
-                uint8_t* at = tile + (piece >> 2) * kStage * 128 + row * 128;
-                uint4 a, b;
-                convert16<E4M3>(x[j], a, b);
-                // the second 64 channels in the other order: the banks of a row's two blocks are the same
-                const int c0 = 2 * (piece & 3), swap = piece >> 2;
-                *reinterpret_cast<uint4*>(at + (((c0 + swap) ^ (row & 7)) << 4)) = swap ? b : a;
-                *reinterpret_cast<uint4*>(at + (((c0 + 1 - swap) ^ (row & 7)) << 4)) = swap ? a : b;
-            }
-        };
-        // threads 0 .. 3 note the scales of the stage's parts
-        auto part_page = [&](int i) {
-            const int part = base + i * kStage + 16 * t;
-            return t < 4 && i < stages && part < s.t.hi && part + 16 > s.t.lo ? cache_page(p.c, s.b, part / p.c.page) : -2;
-        };
-        auto scales = [&](int id, float& ks, float& vs) {
-            ks = vs = id == -1 ? __uint_as_float(0x7fc00000u) : 0.f;
-            if (id >= 0) {
-                const size_t ph = (size_t)id * p.c.H + s.h;
-                ks = p.c.k_scale[ph];
-                vs = p.c.v_scale[ph];
-            }
-        };
-        uint4 k[V], v[V];
-        float ks, vs;
-        Ids ids = lookup(0), one = lookup(1), two = lookup(2);
-        int mid = part_page(0), mid1 = part_page(1), mid2 = part_page(2);
-        fetch(k, p.c.k, 0, ids);
-        fetch(v, p.c.v, 0, ids);
-        scales(mid, ks, vs);
         for (int i = 0; i < stages; ++i, ++n) {
+            const uint32_t rb = n % kRaw;
+            if (!wait(ct, &ct.rfull[rb], (n / kRaw) & 1)) return;
+            const uint8_t* raw = smem + Smem<D>::raw + rb * 2 * Smem<D>::codes;
+            // what hides behind the last position, or was not copied, may be anything: zeros for values
+            // (as keys it makes scores that are hidden)
+            const int keep = ct.meta[n % kMetas].id[w] < 0 ? 0 : end - (base + i * kStage + 16 * w);
             if (!wait(ct, &ct.kempty[buf], parity ^ 1)) return;
-            if (t < 4) {
-                StageMeta& m = ct.meta[n % kMetas];
-                m.ks[t] = ks;
-                m.vs[t] = vs;
-                m.ve[t] = mid >= 0 ? scale_exponent(vs) : mid == -1 ? 0.f : kNegInf;
-                if (mid == -1) flag_index_error(p.c);
-            }
-            write(smem + Smem<D>::k + buf * Smem<D>::tile, k);
+            convert(raw, smem + Smem<D>::k + buf * Smem<D>::tile, 16);
             fence_async_smem();
             mbar_arrive(&ct.kfull[buf]);
-            fetch(k, p.c.k, i + 1, one);
             if (!wait(ct, &ct.vempty[buf], parity ^ 1)) return;
-            write(smem + Smem<D>::v + buf * Smem<D>::tile, v);
+            convert(raw + Smem<D>::codes, smem + Smem<D>::v + buf * Smem<D>::tile, keep);
             fence_async_smem();
             mbar_arrive(&ct.vfull[buf]);
-            fetch(v, p.c.v, i + 1, one);
-            scales(mid1, ks, vs);
-            mid = mid1;
-            mid1 = mid2;
-            mid2 = part_page(i + 3);
-            one = two;
-            two = lookup(i + 3);
+            mbar_arrive(&ct.rempty[rb]);
             if (++buf == kBuffers) { buf = 0; parity ^= 1; }
         }
     }
@@ -596,6 +629,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
         tmem_relinquish();
     }
     if (threadIdx.x == 32) {
+        for (int i = 0; i < kRaw; ++i) {
+            mbar_init(&ct.rfull[i], 1);
+            mbar_init(&ct.rempty[i], 128);
+        }
         for (int i = 0; i < kBuffers; ++i) {
             mbar_init(&ct.kfull[i], 128);
             mbar_init(&ct.kempty[i], 1);
@@ -619,7 +656,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     tc_fence_after();
     if (warp < 8) soften_rows<D, E4M3>(p, ct, walk);
     else if (warp < 12) convert_codes<D, E4M3>(p, smem, ct, walk);
-    else issue_products<D>(p, smem, ct, walk);
+    else if (warp == 12) issue_products<D>(p, smem, ct, walk);
+    else copy_pages<D>(p, smem, ct, walk);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
