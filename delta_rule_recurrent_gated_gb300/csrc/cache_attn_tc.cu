@@ -14,8 +14,10 @@
 // statistics and write P.
 //
 // Softmax in base 2 with whole-number references, as in cache_attn.cu: p = 2^(s - m), l = sum p,
-// operand w = p vs 2^(m - M + 14).  The accumulator is rescaled (exactly, by a power of two) only when
-// a row's largest s + log2 vs passes M by more than 1, so an operand reaches 2^15 at most.
+// operand w = p vs 2^(m - M + 13).  The accumulator is rescaled (exactly, by a power of two) only when
+// a row's largest s + log2 vs passes M by more than 2.9: a row's largest operand is never below 2^12
+// nor above 2^15.9, and with scores of unit size few stages rescale (8 % of them, 63 % where M
+// follows by whole numbers).
 //
 // The stages of all tiles form one line that is divided evenly among the blocks (one per SM); a tile
 // that several blocks worked on is joined by a second kernel from their rows in the workspace.
@@ -34,6 +36,8 @@ constexpr int kTcThreads = 448;  // eight warps of rows, four of codes, one that
 constexpr int kCodeThread0 = 256;
 constexpr int kBuffers = 3;      // stages of K and V as operands
 constexpr int kRaw = 4;          // as codes
+constexpr int kTcBias = 13;       // weights as 16-bit operands: 2^12 .. 2^15.9 for a row's largest
+constexpr float kSlack = 2.9f;
 constexpr int kTcOver = 4;       // what a tile costs beside its stages, in stages
 constexpr int kMetas = 8;        // stages whose scales are kept: more than the warps can be apart
 constexpr int kMaxTcBlocks = 152;
@@ -160,7 +164,7 @@ struct Walk {
 
 // ------------------------------------------------------------------ shared memory
 struct __align__(16) StageMeta {  // read as 16-byte words
-    float ks[4], vs[4], ve[4];  // of the four 16-position parts
+    float ks[4], vs[4], lv[4];  // of the four 16-position parts: scales, log2 vs
     int id[4];                  // their pages: -1 out of range, -2 seen by no row
 };
 struct Control {
@@ -179,30 +183,25 @@ template <int D> struct Smem {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// As mbar_try_wait, asleep for up to about 10 us instead of polling.
-__device__ __forceinline__ bool mbar_try_wait_long(uint64_t* bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(10000u)
-        : "memory");
-    return ok != 0;
+// Once for a whole warp, after what its lanes did.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
-// Bounded wait of a whole warp; false once it or any other of the block's waits has run out.
+// Bounded wait of a whole warp; false once it or any other of the block's waits has run out.  The
+// timer is read now and then only: its latency is that of a stage's whole exchange.
 __device__ __forceinline__ bool wait(Control& ct, uint64_t* bar, uint32_t parity) {
     bool done = mbar_try_wait(bar, parity);
-    if (!done) {
-        const uint64_t t0 = globaltimer_ns();
-        while (true) {
-            for (int i = 0; i < 16 && !done; ++i) done = mbar_try_wait_long(bar, parity);
-            if (done || ct.dead) break;
-            if (globaltimer_ns() - t0 > kWaitLimitNs) {
-                ct.dead = 1;
-                break;
-            }
+    uint64_t t0 = 0;
+    for (uint32_t k = 1; !done; ++k) {
+        done = mbar_try_wait(bar, parity);
+        if (done || (k & 63)) continue;
+        if (ct.dead) break;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > kWaitLimitNs) {
+            ct.dead = 1;
+            break;
         }
     }
     return __all_sync(0xffffffffu, done);
@@ -267,7 +266,7 @@ __device__ __forceinline__ void copy_pages(const AttnParams& p, uint8_t* smem, C
                 StageMeta& m = ct.meta[n % kMetas];
                 m.ks[g] = now.ks;
                 m.vs[g] = now.vs;
-                m.ve[g] = now.id >= 0 ? scale_exponent(now.vs) : now.id == -1 ? 0.f : kNegInf;
+                m.lv[g] = now.vs == now.vs ? log2f(now.vs) : 0.f;
                 m.id[g] = now.id;
                 if (now.id == -1) flag_index_error(p.c);
             }
@@ -333,12 +332,12 @@ __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem
             if (!wait(ct, &ct.kempty[buf], parity ^ 1)) return;
             convert(raw, smem + Smem<D>::k + buf * Smem<D>::tile, 16);
             fence_async_smem();
-            mbar_arrive(&ct.kfull[buf]);
+            warp_arrive(&ct.kfull[buf]);
             if (!wait(ct, &ct.vempty[buf], parity ^ 1)) return;
             convert(raw + Smem<D>::codes, smem + Smem<D>::v + buf * Smem<D>::tile, keep);
             fence_async_smem();
-            mbar_arrive(&ct.vfull[buf]);
-            mbar_arrive(&ct.rempty[rb]);
+            warp_arrive(&ct.vfull[buf]);
+            if (lane == 0) mbar_arrive(&ct.rempty[rb]);
             if (++buf == kBuffers) { buf = 0; parity ^= 1; }
         }
     }
@@ -428,11 +427,14 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
         // the row's queries, scaled, as operand (with the sign of the scale, so that factors are positive)
         const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
                                                          ((long long)s.b * p.c.T + tok) * p.ld_q + (long long)head * D);
+        uint4 raw[D / 8];
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) raw[j] = on ? __ldg(qp + j) : make_uint4(0, 0, 0, 0);
         float top = 0.f;
-#pragma unroll 4
+#pragma unroll
         for (int j = 0; j < D / 8; ++j) {
             float x[8];
-            unpack8(on ? __ldg(qp + j) : make_uint4(0, 0, 0, 0), x);
+            unpack8(raw[j], x);
 #pragma unroll
             for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
         }
@@ -440,13 +442,13 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
         float up, rest;
         query_scale(top, e, up, rest);
         if (p.scale < 0.f) up = -up;
-#pragma unroll 2
+#pragma unroll
         for (int j = 0; j < D / 8; j += 2) {
             float u[8];  // 16 queries, two a column
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float x[8];
-                unpack8(on ? __ldg(qp + j + i) : make_uint4(0, 0, 0, 0), x);
+                unpack8(raw[j + i], x);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) x[q] = x[q] * up * rest;
 #pragma unroll
@@ -460,7 +462,7 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&ct.qfull[hf]);
+        warp_arrive(&ct.qfull[hf]);
         const float qs = ldexpf(fabsf(p.scale) * kLog2e, e);
         // positions that every row of the half sees need no mask
         const int t0 = (s.t.row0 + hf * kHalf) / p.G, t1 = min(s.n - 1, (s.t.row0 + hf * kHalf + kHalf - 1) / p.G);
@@ -472,9 +474,9 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
             tc_fence_after();
             const StageMeta& mt = ct.meta[all % kMetas];
             const float4 ks4 = *reinterpret_cast<const float4*>(mt.ks), vs4 = *reinterpret_cast<const float4*>(mt.vs);
-            const float4 ve4 = *reinterpret_cast<const float4*>(mt.ve);
+            const float4 lv4 = *reinterpret_cast<const float4*>(mt.lv);
             float kf[4] = {qs * ks4.x, qs * ks4.y, qs * ks4.z, qs * ks4.w}, vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
-            const float ve[4] = {ve4.x, ve4.y, ve4.z, ve4.w};
+            const float lv[4] = {lv4.x, lv4.y, lv4.z, lv4.w};
             const float sum = (ks4.x + ks4.y) + (ks4.z + ks4.w);
             if (first + kStage > all_hi || first < all_lo || sum != sum) {
                 // Hidden positions become -inf in tensor memory, so that the code below knows no mask.  A part
@@ -519,31 +521,34 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
                 kf[g] = fmaxf(kf[g], 1e-37f);  // a zero factor and -inf make no NaN
                 gm *= kf[g];
                 mx = fmaxf(mx, gm);
-                need = fmaxf(need, ceilf(gm) + ve[g]);
+                need = fmaxf(need, gm + lv[g]);
             }
             const float m2 = fmaxf(m, ceilf(mx));
             l *= pow2i(m - m2);
             m = m2;
-            const bool grow = need > M + 1.f;
+            const bool grow = need > M + kSlack;
             if (__any_sync(0xffffffffu, grow)) {
-                const float f = grow ? pow2i(M - need) : 1.f;
-                if (grow) M = need;
+                const float up2 = ceilf(need), f = grow ? pow2i(M - up2) : 1.f;
+                if (grow) M = up2;
                 if (i > 0) {
 #pragma unroll 1
-                    for (int j = 0; j < D; j += 16) {
-                        float y[16];
+                    for (int j = 0; j < D; j += 32) {
+                        float y[2][16];
                         __syncwarp();
-                        tmem_ld16(to + j, y);
+                        tmem_ld16(to + j, y[0]);
+                        tmem_ld16(to + j + 16, y[1]);
                         tmem_ld_wait();
-                        float a[8], b[8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) { a[q] = y[q] * f; b[q] = y[8 + q] * f; }
-                        tmem_st8(to + j, a);
-                        tmem_st8(to + j + 8, b);
+                        for (int h = 0; h < 4; ++h) {
+                            float a[8];
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) a[q] = y[h >> 1][8 * (h & 1) + q] * f;
+                            tmem_st8(to + j + 8 * h, a);
+                        }
                     }
                 }
             }
-            const float mref = m == kNegInf ? 0.f : m, fm = pow2i(fminf(m - M + kBias, 126.f));
+            const float mref = m == kNegInf ? 0.f : m, fm = pow2i(fminf(m - M + kTcBias, 126.f));
             float2 l2 = make_float2(0.f, 0.f);
             const float2 nm = make_float2(-mref, -mref);
 #pragma unroll
@@ -565,7 +570,7 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
             l += l2.x + l2.y;
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive(&ct.pfull[hf]);
+            warp_arrive(&ct.pfull[hf]);
         }
         // the row leaves
         if (!wait(ct, &ct.ofull[hf], tiles & 1)) return;
@@ -574,7 +579,7 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
         const int rr = hf * kHalf + r;
         float* part = p.part + ((size_t)blockIdx.x * 2 + (s.first ? 0 : 1)) * tile_floats(D, kRows);
         const size_t at = ((size_t)s.b * p.c.T + tok) * p.Hq + head;
-        const float f = M - m - kBias;  // sums are in units of 2^(M - 14), l in units of 2^m
+        const float f = M - m - kTcBias;  // sums are in units of 2^(M - 13), l in units of 2^m
         const float inv = M == kNegInf ? (l == l ? 0.f : l) : ldexpf(1.f / l, (int)fminf(fmaxf(f, -140.f), 120.f));
 #pragma unroll 2
         for (int j = 0; j < D; j += 16) {
@@ -600,9 +605,10 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
                 o[0] = u[0];
                 o[1] = u[1];
             } else if (on) {
-                float4* o = reinterpret_cast<float4*>(part + (size_t)rr * D + j);
+                // four channels of all rows side by side, then the next four
+                float4* o = reinterpret_cast<float4*>(part) + (j / 4) * kRows + rr;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) o[q] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+                for (int q = 0; q < 4; ++q) o[q * kRows] = make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
             }
         }
         tc_fence_before();
@@ -610,7 +616,7 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
             if (!s.whole) {
                 part[kRows * D + rr] = l;
                 part[kRows * D + kRows + rr] = m;
-                part[kRows * D + 2 * kRows + rr] = M;
+                part[kRows * D + 2 * kRows + rr] = M + (kBias - kTcBias);
             } else if (p.lse) {
                 p.lse[at] = (m + log2f(l)) * kLn2;
             }
@@ -631,19 +637,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     if (threadIdx.x == 32) {
         for (int i = 0; i < kRaw; ++i) {
             mbar_init(&ct.rfull[i], 1);
-            mbar_init(&ct.rempty[i], 128);
+            mbar_init(&ct.rempty[i], 4);
         }
         for (int i = 0; i < kBuffers; ++i) {
-            mbar_init(&ct.kfull[i], 128);
+            mbar_init(&ct.kfull[i], 4);
             mbar_init(&ct.kempty[i], 1);
-            mbar_init(&ct.vfull[i], 128);
+            mbar_init(&ct.vfull[i], 4);
             mbar_init(&ct.vempty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ct.sfull[i], 2);
-            mbar_init(&ct.pfull[i], kHalf);
+            mbar_init(&ct.pfull[i], 4);
             mbar_init(&ct.ofull[i], 1);
-            mbar_init(&ct.qfull[i], kHalf);
+            mbar_init(&ct.qfull[i], 4);
         }
         mbar_init(&ct.drain, 1);
         ct.dead = 0;
@@ -665,31 +671,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     if (warp == 0) tmem_dealloc(ct.tmem, 512);
 }
 
-// Joins the parts of a tile that several blocks worked on.  Block x: the tile, y: 32 of its rows, four
-// a warp.  Rows of no query get zeros (behind a sequence's tokens) or NaN (a sequence out of range).
+// Joins the parts of a tile that several blocks worked on.  Block x: the tile, y: 32 of its rows, a
+// lane each; warp w takes channels w d/8 .. + d/8 - 1.  Rows of no query get zeros (behind a
+// sequence's tokens) or NaN (a sequence out of range).
 template <int D>
 __global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParams p, int blocks, int max_tiles) {
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int V = D / 32;  // float4s of a lane
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch0 = warp * (D / 8);
     const int b = blockIdx.x / (p.c.H * max_tiles), other = blockIdx.x % (p.c.H * max_tiles);
     const int h = other / max_tiles, tile = other % max_tiles;
-    const int r0 = blockIdx.y * 32 + warp * 4;
+    const int r = blockIdx.y * 32 + lane, row = tile * kRows + r;
     int len, n;
     const bool ok = cache_seq(p.c, b, len, n);
     if (!ok) {
         if (threadIdx.x == 0) flag_index_error(p.c);
         n = 0;
     }
-    for (int r = r0; r < r0 + 4; ++r) {
-        const int row = tile * kRows + r;
-        if (row < n * p.G || row >= p.c.T * p.G) continue;
+    if (row >= n * p.G && row < p.c.T * p.G) {
         const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
         const float bad = __uint_as_float(0x7fc00000u);
-#pragma unroll
-        for (int j = 0; j < V; ++j) st_any(p.o, at * D + V * lane + j, p.out, ok ? 0.f : bad);
-        if (lane == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
+        for (int j = ch0; j < ch0 + D / 8; ++j) st_any(p.o, at * D + j, p.out, ok ? 0.f : bad);
+        if (warp == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
     }
-    if (tile * kRows >= n * p.G) {
+    if (tile * kRows + blockIdx.y * 32 >= n * p.G) {
         wait_for_parts();
         return;
     }
@@ -715,30 +719,47 @@ __global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParam
     const long long a = before + h * mine + upto + kTcOver;  // the tile's first stage on the line
     const int stages = make_tile(p, len, n, tile).stages, used = blocks_used(total, blocks);
     const int first = holder(total, a, used), last = holder(total, a + stages - 1, used);
-    wait_for_parts();
-    if (first == last) return;  // finished by its block
     const float* head = p.part + ((size_t)first * 2 + (share(total, first, used) >= a - kTcOver ? 0 : 1)) * tile_floats(D, kRows);
-    for (int r = r0; r < r0 + 4; ++r) {
-        const int row = tile * kRows + r;
-        if (row >= n * p.G) return;
-        float m = kNegInf, M = kNegInf, l = 0.f, sum[V] = {};
-        for (int i = first; i <= last; ++i) {
-            const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, kRows);
-            const float pl = in[kRows * D + r], pm = in[kRows * D + kRows + r], pM = in[kRows * D + 2 * kRows + r];
-            const float m2 = fmaxf(m, pm), M2 = fmaxf(M, pM);
-            const float l1 = pow2i(m - m2), l2 = pow2i(pm - m2), s1 = pow2i(M - M2), s2 = pow2i(pM - M2);
-            l = (l == l ? l * l1 : l) + (pl == pl ? pl * l2 : pl);
+    wait_for_parts();
+    if (first == last || row >= n * p.G) return;  // finished by its block
+    float m = kNegInf, M = kNegInf, l = 0.f;
+    float4 sum[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const float x = in[(size_t)r * D + V * lane + j];
-                sum[j] = (sum[j] == sum[j] ? sum[j] * s1 : sum[j]) + (x == x ? x * s2 : x);
-            }
-            m = m2;
-            M = M2;
+    for (int j = 0; j < V; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // a part without weight adds nothing, one that met a NaN hands it on
+    auto add = [](float& x, float fx, float y, float fy) { x = (x == x ? x * fx : x) + (y == y ? y * fy : y); };
+#pragma unroll 2
+    for (int i = first; i <= last; ++i) {
+        const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, kRows);
+        float4 y[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) y[j] = reinterpret_cast<const float4*>(in)[(ch0 / 4 + j) * kRows + r];
+        const float pl = in[kRows * D + r], pm = in[kRows * D + kRows + r], pM = in[kRows * D + 2 * kRows + r];
+        const float m2 = fmaxf(m, pm), M2 = fmaxf(M, pM);
+        const float s1 = pow2i(M - M2), s2 = pow2i(pM - M2);
+        add(l, pow2i(m - m2), pl, pow2i(pm - m2));
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            add(sum[j].x, s1, y[j].x, s2);
+            add(sum[j].y, s1, y[j].y, s2);
+            add(sum[j].z, s1, y[j].z, s2);
+            add(sum[j].w, s1, y[j].w, s2);
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j) write_row(p, b, h, row, V * lane + j, D, sum[j], l, m, M);
+        m = m2;
+        M = M2;
     }
+    const float f = M - m - kBias;
+    const float inv = M == kNegInf ? (l == l ? 0.f : l) : ldexpf(1.f / l, (int)fminf(fmaxf(f, -140.f), 120.f));
+    const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
+    uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + ch0);
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+        const uint4 u = make_uint4(pack_bf16(sum[j].x * inv, sum[j].y * inv), pack_bf16(sum[j].z * inv, sum[j].w * inv),
+                                   pack_bf16(sum[j + 1].x * inv, sum[j + 1].y * inv),
+                                   pack_bf16(sum[j + 1].z * inv, sum[j + 1].w * inv));
+        *reinterpret_cast<uint4*>(o + j) = u;
+    }
+    if (warp == 0 && p.lse) p.lse[at] = (m + log2f(l)) * kLn2;
 }
 
 template <int D, bool E4M3>
