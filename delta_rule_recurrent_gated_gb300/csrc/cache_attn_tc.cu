@@ -188,23 +188,25 @@ __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
-// Bounded wait of a whole warp; false once it or any other of the block's waits has run out.  The
-// timer is read now and then only: its latency is that of a stage's whole exchange.
-__device__ __forceinline__ bool wait(Control& ct, uint64_t* bar, uint32_t parity) {
-    bool done = mbar_try_wait(bar, parity);
+// Bounded wait of a thread; false once it or any other of the block's waits has run out.
+__device__ __forceinline__ bool wait_one(Control& ct, uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
     uint64_t t0 = 0;
-    for (uint32_t k = 1; !done; ++k) {
-        done = mbar_try_wait(bar, parity);
-        if (done || (k & 63)) continue;
-        if (ct.dead) break;
+    for (uint32_t k = 1;; ++k) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (k & 63) continue;
+        if (ct.dead) return false;
         const uint64_t now = globaltimer_ns();
         if (t0 == 0) t0 = now;
         else if (now - t0 > kWaitLimitNs) {
             ct.dead = 1;
-            break;
+            return false;
         }
     }
-    return __all_sync(0xffffffffu, done);
+}
+// Of a whole warp.
+__device__ __forceinline__ bool wait(Control& ct, uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_one(ct, bar, parity));
 }
 // D[tmem] (+)= A[tmem] B[smem], 16-bit floats (A: a row per lane, two values a column), fp32 accumulator.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -344,12 +346,16 @@ __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem
 }
 
 // ------------------------------------------------------------------ warp 12: the products
-// Products of one thread run in the order of their issue, so S of a stage, over the columns of the
-// stage before's P, follows that P's product, and its completion says that O has that product too.
+// One thread.  Products of one thread run in the order of their issue, so S of a stage, over the
+// columns of the stage before's P, follows that P's product, and its completion says that O has that
+// product too.  A commit holds the thread up for some 200 cycles, so there is one for each S: the rows'
+// threads free the buffers of K and V once they see S of the last half.
 template <int D>
 __device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
-    const int lane = threadIdx.x & 31;
     const uint32_t base = smem_u32(smem), tm = ct.tmem;
+    // descriptors of the first buffers; an address step of 16 bytes is 1 in their lowest field
+    const uint64_t k0 = desc_kmajor(Tile{base + Smem<D>::k, kStage}, 0);
+    const uint64_t v0 = desc_mnmajor(Tile{base + Smem<D>::v, kStage}, 0);
     uint32_t buf = 0, parity = 0, vbuf = 0, vparity = 0;
     uint32_t n0 = 0, n1 = 0, tiles0 = 0, tiles1 = 0;  // stages and tiles of each half so far
     Stretch s;
@@ -358,37 +364,32 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* sme
         const int stages = s.upto - s.from;
         const int halves = s.t.row0 + kHalf < s.n * p.G ? 2 : 1;
         for (int i = 0; ok && i <= stages; ++i) {
+            const uint64_t kd = k0 + buf * (Smem<D>::tile >> 4), vd = v0 + vbuf * (Smem<D>::tile >> 4);
+            if (i > 0) ok = wait_one(ct, &ct.vfull[vbuf], vparity);
+            if (i < stages) ok = ok && wait_one(ct, &ct.kfull[buf], parity);
             for (int hf = 0; ok && hf < halves; ++hf) {
                 if (i > 0) {  // O += P V of stage i - 1
-                    ok = (hf > 0 || wait(ct, &ct.vfull[vbuf], vparity)) && wait(ct, &ct.pfull[hf], ((hf ? n1 : n0) + i - 1) & 1);
+                    ok = wait_one(ct, &ct.pfull[hf], ((hf ? n1 : n0) + i - 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    if (lane == 0) {
-                        const Tile v{base + Smem<D>::v + vbuf * Smem<D>::tile, kStage};
 #pragma unroll
-                        for (int kk = 0; kk < kStage; kk += 16)
-                            mma_ts(tm + o_col(hf), tm + s_col(hf) + kk / 2, desc_mnmajor(v, kk),
-                                   idesc_f16(kHalf, D, true), i > 1 || kk > 0);
-                        if (hf == halves - 1) mma_commit(&ct.vempty[vbuf]);
-                        if (i == stages) mma_commit(&ct.ofull[hf]);
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < kStage; kk += 16)  // 16 positions: 16 rows of 128 bytes
+                        mma_ts(tm + o_col(hf), tm + s_col(hf) + kk / 2, vd + kk * 8, idesc_f16(kHalf, D, true),
+                               i > 1 || kk > 0);
+                    if (i == stages) mma_commit(&ct.ofull[hf]);
+                } else {
+                    ok = wait_one(ct, &ct.qfull[hf], (hf ? tiles1 : tiles0) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
                 }
                 if (i < stages) {  // S = Q K^T of stage i
-                    ok = (hf > 0 || wait(ct, &ct.kfull[buf], parity)) && (i > 0 || wait(ct, &ct.qfull[hf], (hf ? tiles1 : tiles0) & 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    if (lane == 0) {
-                        const Tile k{base + Smem<D>::k + buf * Smem<D>::tile, kStage};
 #pragma unroll
-                        for (int kk = 0; kk < D; kk += 16)
-                            mma_ts(tm + s_col(hf), tm + q_col(hf) + kk / 2, desc_kmajor(k, kk),
-                                   idesc_f16(kHalf, kStage, false), kk > 0);
-                        mbar_arrive(&ct.sfull[hf]);  // hands on the scales, which came with kfull
-                        mma_commit(&ct.sfull[hf]);
-                        if (hf == halves - 1) mma_commit(&ct.kempty[buf]);
-                    }
-                    __syncwarp();
+                    for (int kk = 0; kk < D; kk += 16)  // 16 channels: 32 bytes of a 128-byte row
+                        mma_ts(tm + s_col(hf), tm + q_col(hf) + kk / 2,
+                               kd + (kk >> 6) * (kStage * 128 / 16) + (kk & 63) / 8, idesc_f16(kHalf, kStage, false),
+                               kk > 0);
+                    mma_commit(&ct.sfull[hf]);
+                    mbar_arrive(&ct.sfull[hf]);  // hands on the scales, which came with kfull
                 }
             }
             if (i > 0 && ++vbuf == kBuffers) { vbuf = 0; vparity ^= 1; }
@@ -402,7 +403,7 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* sme
         }
     }
     if (!ok) {  // let what is in flight end before the tensor memory goes
-        if (lane == 0) mma_commit(&ct.drain);
+        mma_commit(&ct.drain);
         mbar_wait(&ct.drain, 0, kWaitLimitNs);
     }
 }
@@ -410,7 +411,7 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* sme
 // ------------------------------------------------------------------ warps 0-7: a row per thread
 template <int D, bool E4M3>
 __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Walk walk) {
-    const int hf = threadIdx.x / kHalf, r = threadIdx.x % kHalf;
+    const int hf = threadIdx.x / kHalf, r = threadIdx.x % kHalf, lane = threadIdx.x & 31;
     const uint32_t tm = warp_lane_base(ct.tmem), ts = tm + s_col(hf), to = tm + o_col(hf);
     uint32_t n = 0;  // stages that this half has seen
     uint32_t all = 0;  // and that the block has
@@ -423,6 +424,7 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
             continue;
         }
         const bool on = row < s.n * p.G;
+        const bool last = hf == 1 || s.t.row0 + kHalf >= s.n * p.G;  // the last half with rows
         const int tok = on ? row / p.G : 0, head = s.h * p.G + (on ? row % p.G : 0), pos = on ? s.len + tok : -1;
         // the row's queries, scaled, as operand (with the sign of the scale, so that factors are positive)
         const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
@@ -471,6 +473,10 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
         for (int i = 0; i < stages; ++i, ++n, ++all) {
             const int first = (s.t.s0 + s.from + i) * kStage;
             if (!wait(ct, &ct.sfull[hf], n & 1)) return;
+            if (last && lane == 0) {  // S of this stage is there, and with it the products with V of the one before
+                mbar_arrive(&ct.kempty[all % kBuffers]);
+                if (i > 0) mbar_arrive(&ct.vempty[(all - 1) % kBuffers]);
+            }
             tc_fence_after();
             const StageMeta& mt = ct.meta[all % kMetas];
             const float4 ks4 = *reinterpret_cast<const float4*>(mt.ks), vs4 = *reinterpret_cast<const float4*>(mt.vs);
@@ -574,6 +580,7 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
         }
         // the row leaves
         if (!wait(ct, &ct.ofull[hf], tiles & 1)) return;
+        if (last && lane == 0) mbar_arrive(&ct.vempty[(all - 1) % kBuffers]);
         ++tiles;
         tc_fence_after();
         const int rr = hf * kHalf + r;
@@ -641,9 +648,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
         }
         for (int i = 0; i < kBuffers; ++i) {
             mbar_init(&ct.kfull[i], 4);
-            mbar_init(&ct.kempty[i], 1);
+            mbar_init(&ct.kempty[i], 4);
             mbar_init(&ct.vfull[i], 4);
-            mbar_init(&ct.vempty[i], 1);
+            mbar_init(&ct.vempty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ct.sfull[i], 2);
@@ -662,8 +669,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     tc_fence_after();
     if (warp < 8) soften_rows<D, E4M3>(p, ct, walk);
     else if (warp < 12) convert_codes<D, E4M3>(p, smem, ct, walk);
-    else if (warp == 12) issue_products<D>(p, smem, ct, walk);
-    else copy_pages<D>(p, smem, ct, walk);
+    else if (warp == 13) copy_pages<D>(p, smem, ct, walk);
+    else if ((threadIdx.x & 31) == 0) issue_products<D>(p, smem, ct, walk);
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
