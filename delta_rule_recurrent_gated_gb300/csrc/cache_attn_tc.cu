@@ -5,9 +5,11 @@
 // row = t * G + g), two halves of 128, over a stretch of positions, in stages of 64:
 //   S = Q K^T   128 x 64 for each half, contraction d
 //   O += P V    128 x d for each half, contraction 64
-// Q, P, S and O live in tensor memory, all 512 columns of it: P takes the columns of its S. Shared
-// memory holds K and V alone, as 16-bit floats (exact), three stages of them, so the products read
-// 32 KB a stage and half from it (with Q and P there as well: 80 KB, 640 cycles for 540 of products).
+// Tensor memory, all 512 columns of it, holds O and two S of each half, used in turn; P takes the
+// columns of its S.  So S of the next stage is formed before the weights of this one are there, and a
+// half waits for nobody (with one S it waited for the exchange with the issuing thread and for two
+// products every stage: 2950 cycles for both halves, where the products take 1140).  Shared memory
+// holds Q, and K and V as 16-bit floats (exact), three stages of them.
 // Warp 13 has the codes copied to a ring in shared memory; warps 8-11 turn them into the operand
 // tiles; warp 12 issues the products, the halves in turn, so that one half's weights are formed while
 // the other's products run; warps 0-3 and 4-7 hold a row per thread: they read S, keep the softmax
@@ -34,17 +36,16 @@ using namespace tc;
 constexpr int kHalf = 128, kRows = 2 * kHalf, kStage = 64;
 constexpr int kTcThreads = 448;  // eight warps of rows, four of codes, one that issues, one that copies
 constexpr int kCodeThread0 = 256;
-constexpr int kBuffers = 3;      // stages of K and V as operands
-constexpr int kRaw = 4;          // as codes
+constexpr int kKBuffers = 3, kVBuffers = 4;  // stages of K and V as operands: V is needed for longer
+constexpr int kRaw = 3;                      // as codes
 constexpr int kTcBias = 13;       // weights as 16-bit operands: 2^12 .. 2^15.9 for a row's largest
 constexpr float kSlack = 2.9f;
 constexpr int kTcOver = 4;       // what a tile costs beside its stages, in stages
 constexpr int kMetas = 8;        // stages whose scales are kept: more than the warps can be apart
 constexpr int kMaxTcBlocks = 152;
 // columns of tensor memory of half i
-__device__ __forceinline__ uint32_t s_col(int i) { return 64 * i; }        // S, and P over it
-__device__ __forceinline__ uint32_t o_col(int i) { return 128 + 128 * i; }
-__device__ __forceinline__ uint32_t q_col(int i) { return 384 + 64 * i; }
+__device__ __forceinline__ uint32_t s_col(int i, uint32_t b) { return 128 * i + 64 * b; }  // S, and P over it
+__device__ __forceinline__ uint32_t o_col(int i) { return 256 + 128 * i; }
 
 // ------------------------------------------------------------------ the line of stages
 struct TcTile {
@@ -168,15 +169,17 @@ struct __align__(16) StageMeta {  // read as 16-byte words
     int id[4];                  // their pages: -1 out of range, -2 seen by no row
 };
 struct Control {
-    uint64_t rfull[kRaw], rempty[kRaw], kfull[kBuffers], kempty[kBuffers], vfull[kBuffers], vempty[kBuffers];
-    uint64_t sfull[2], pfull[2], ofull[2], qfull[2], drain;
+    uint64_t rfull[kRaw], rempty[kRaw], kfull[kKBuffers], kempty[kKBuffers], vfull[kVBuffers], vempty[kVBuffers];
+    uint64_t sfull[2][2], pfull[2][2];  // of each half, by the stage's S
+    uint64_t lastv[2], ofull[2], qfull[2], drain;
     uint32_t tmem;
     volatile int dead;
     StageMeta meta[kMetas];
 };
 template <int D> struct Smem {
-    static constexpr int tile = kStage * D * 2, codes = kStage * D, k = 0, v = kBuffers * tile,
-                         raw = 2 * kBuffers * tile, control = raw + 2 * kRaw * codes, bytes = control + 1024;
+    static constexpr int tile = kStage * D * 2, codes = kStage * D, k = 0, v = kKBuffers * tile,
+                         raw = v + kVBuffers * tile, q = raw + 2 * kRaw * codes,
+                         qtile = kHalf * D * 2, control = q + 2 * qtile, bytes = control + 1024;
     static_assert(sizeof(Control) <= 1024, "control block");
 };
 
@@ -297,103 +300,117 @@ __device__ __forceinline__ void copy_pages(const AttnParams& p, uint8_t* smem, C
 }
 
 // ------------------------------------------------------------------ warps 8-11: codes to operand tiles
-// Warp w takes the 16 positions of part w, 8 rows and a 64-byte half row of each at a time; even and
-// odd rows take the other half (d = 128), which keeps reads and writes off each other's banks.
+// Warps 8 and 9 convert keys, 10 and 11 values, each two parts of 16 positions: 8 rows and a 64-byte
+// half row of each at a time; even and odd rows take the other half (d = 128), which keeps reads and
+// writes off each other's banks.
 template <int D, bool E4M3>
 __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
     constexpr int IT = D / 64;  // half rows of a row
     const int lane = threadIdx.x & 31, w = (threadIdx.x - kCodeThread0) >> 5;
-    const int r8 = lane >> 2, q = lane & 3;
-    uint32_t n = 0, buf = 0, parity = 0;  // stages so far, n % kBuffers, n / kBuffers % 2
+    const int r8 = lane >> 2, q = lane & 3, part0 = 2 * (w & 1);
+    const bool keys = w < 2;
+    uint64_t* full = keys ? ct.kfull : ct.vfull;
+    uint64_t* empty = keys ? ct.kempty : ct.vempty;
+    const uint32_t buffers = keys ? kKBuffers : kVBuffers;
+    uint8_t* tiles = smem + (keys ? Smem<D>::k : Smem<D>::v);
+    const uint8_t* raws = smem + Smem<D>::raw + (keys ? 0 : Smem<D>::codes);
+    uint32_t n = 0, buf = 0, parity = 0, rb = 0, rparity = 0;  // stages so far; buffers and their phases
     Stretch s;
     while (walk.next(p, s)) {
         const int end = s.len + s.n, stages = s.upto - s.from, base = (s.t.s0 + s.from) * kStage;
-        // `keep`: rows of the part that hold a position; the others become zeros
-        auto convert = [&](const uint8_t* raw, uint8_t* tile, int keep) {
-#pragma unroll
-            for (int o = 0; o < 2; ++o)
-#pragma unroll
-                for (int it = 0; it < IT; ++it) {
-                    const int row = 16 * w + 8 * o + r8, half = IT == 2 ? (row ^ it) & 1 : 0;
-                    uint4 u = *reinterpret_cast<const uint4*>(raw + row * D + half * 64 + q * 16);
-                    if (8 * o + r8 >= keep) u = make_uint4(0, 0, 0, 0);
-                    uint4 a, b;
-                    convert16<E4M3>(u, a, b);
-                    uint8_t* at = tile + half * kStage * 128 + row * 128;
-                    *reinterpret_cast<uint4*>(at + (((2 * q) ^ (row & 7)) << 4)) = a;
-                    *reinterpret_cast<uint4*>(at + (((2 * q + 1) ^ (row & 7)) << 4)) = b;
-                }
-        };
         for (int i = 0; i < stages; ++i, ++n) {
-            const uint32_t rb = n % kRaw;
-            if (!wait(ct, &ct.rfull[rb], (n / kRaw) & 1)) return;
-            const uint8_t* raw = smem + Smem<D>::raw + rb * 2 * Smem<D>::codes;
-            // what hides behind the last position, or was not copied, may be anything: zeros for values
-            // (as keys it makes scores that are hidden)
-            const int keep = ct.meta[n % kMetas].id[w] < 0 ? 0 : end - (base + i * kStage + 16 * w);
-            if (!wait(ct, &ct.kempty[buf], parity ^ 1)) return;
-            convert(raw, smem + Smem<D>::k + buf * Smem<D>::tile, 16);
+            if (!wait(ct, &ct.rfull[rb], rparity)) return;
+            if (!wait(ct, &empty[buf], parity ^ 1)) return;
+            const uint8_t* raw = raws + rb * 2 * Smem<D>::codes;
+            uint8_t* tile = tiles + buf * Smem<D>::tile;
+#pragma unroll
+            for (int a = 0; a < 2; ++a) {
+                const int part = part0 + a;
+                // values that hide behind the last position, or were not copied, may be anything: zeros
+                // (as keys they make scores that are hidden)
+                const int keep = keys ? 16 : ct.meta[n % kMetas].id[part] < 0 ? 0 : end - (base + i * kStage + 16 * part);
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+#pragma unroll
+                    for (int it = 0; it < IT; ++it) {
+                        const int row = 16 * part + 8 * o + r8, half = IT == 2 ? (row ^ it) & 1 : 0;
+                        uint4 u = *reinterpret_cast<const uint4*>(raw + row * D + half * 64 + q * 16);
+                        if (8 * o + r8 >= keep) u = make_uint4(0, 0, 0, 0);
+                        uint4 x, y;
+                        convert16<E4M3>(u, x, y);
+                        uint8_t* at = tile + half * kStage * 128 + row * 128;
+                        *reinterpret_cast<uint4*>(at + (((2 * q) ^ (row & 7)) << 4)) = x;
+                        *reinterpret_cast<uint4*>(at + (((2 * q + 1) ^ (row & 7)) << 4)) = y;
+                    }
+            }
             fence_async_smem();
-            warp_arrive(&ct.kfull[buf]);
-            if (!wait(ct, &ct.vempty[buf], parity ^ 1)) return;
-            convert(raw + Smem<D>::codes, smem + Smem<D>::v + buf * Smem<D>::tile, keep);
-            fence_async_smem();
-            warp_arrive(&ct.vfull[buf]);
+            warp_arrive(&full[buf]);
             if (lane == 0) mbar_arrive(&ct.rempty[rb]);
-            if (++buf == kBuffers) { buf = 0; parity ^= 1; }
+            if (++buf == buffers) { buf = 0; parity ^= 1; }
+            if (++rb == kRaw) { rb = 0; rparity ^= 1; }
         }
     }
 }
 
 // ------------------------------------------------------------------ warp 12: the products
-// One thread.  Products of one thread run in the order of their issue, so S of a stage, over the
-// columns of the stage before's P, follows that P's product, and its completion says that O has that
-// product too.  A commit holds the thread up for some 200 cycles, so there is one for each S: the rows'
-// threads free the buffers of K and V once they see S of the last half.
+// One thread.  Products of one thread run in the order of their issue: S of stage i + 1, over the
+// columns of P of stage i - 1, follows that P's product, and its completion says that O has it.  A
+// commit holds the thread up for some 200 cycles, so there is one for each S: the rows' threads free
+// the buffers of K and V once they see S of the last half.
 template <int D>
 __device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
     const uint32_t base = smem_u32(smem), tm = ct.tmem;
     // descriptors of the first buffers; an address step of 16 bytes is 1 in their lowest field
     const uint64_t k0 = desc_kmajor(Tile{base + Smem<D>::k, kStage}, 0);
     const uint64_t v0 = desc_mnmajor(Tile{base + Smem<D>::v, kStage}, 0);
+    const uint64_t q0 = desc_kmajor(Tile{base + Smem<D>::q, kHalf}, 0);
     uint32_t buf = 0, parity = 0, vbuf = 0, vparity = 0;
     uint32_t n0 = 0, n1 = 0, tiles0 = 0, tiles1 = 0;  // stages and tiles of each half so far
+    // S = Q K^T of a half, its n-th stage
+    auto scores = [&](int hf, uint32_t n) {
+        const uint64_t kd = k0 + buf * (Smem<D>::tile >> 4), qd = q0 + hf * (Smem<D>::qtile >> 4);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < D; kk += 16)  // 16 channels: 32 bytes of a 128-byte row
+            mma_bf16(tm + s_col(hf, n & 1), qd + (kk >> 6) * (kHalf * 128 / 16) + (kk & 63) / 8,
+                     kd + (kk >> 6) * (kStage * 128 / 16) + (kk & 63) / 8, idesc_f16(kHalf, kStage, false), kk > 0);
+        mma_commit(&ct.sfull[hf][n & 1]);
+        mbar_arrive(&ct.sfull[hf][n & 1]);  // hands on the scales, which came with kfull
+    };
+    // O += P V of a half, its n-th stage
+    auto values = [&](int hf, uint32_t n, bool more) {
+        const uint64_t vd = v0 + vbuf * (Smem<D>::tile >> 4);
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kStage; kk += 16)  // 16 positions: 16 rows of 128 bytes
+            mma_ts(tm + o_col(hf), tm + s_col(hf, n & 1) + kk / 2, vd + kk * 8, idesc_f16(kHalf, D, true), more || kk > 0);
+    };
     Stretch s;
     bool ok = true;
     while (ok && walk.next(p, s)) {
         const int stages = s.upto - s.from;
         const int halves = s.t.row0 + kHalf < s.n * p.G ? 2 : 1;
-        for (int i = 0; ok && i <= stages; ++i) {
-            const uint64_t kd = k0 + buf * (Smem<D>::tile >> 4), vd = v0 + vbuf * (Smem<D>::tile >> 4);
-            if (i > 0) ok = wait_one(ct, &ct.vfull[vbuf], vparity);
-            if (i < stages) ok = ok && wait_one(ct, &ct.kfull[buf], parity);
-            for (int hf = 0; ok && hf < halves; ++hf) {
-                if (i > 0) {  // O += P V of stage i - 1
-                    ok = wait_one(ct, &ct.pfull[hf], ((hf ? n1 : n0) + i - 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < kStage; kk += 16)  // 16 positions: 16 rows of 128 bytes
-                        mma_ts(tm + o_col(hf), tm + s_col(hf) + kk / 2, vd + kk * 8, idesc_f16(kHalf, D, true),
-                               i > 1 || kk > 0);
-                    if (i == stages) mma_commit(&ct.ofull[hf]);
-                } else {
-                    ok = wait_one(ct, &ct.qfull[hf], (hf ? tiles1 : tiles0) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
+        for (int i = -1; ok && i < stages; ++i) {
+            if (i + 1 < stages) {
+                ok = wait_one(ct, &ct.kfull[buf], parity);
+                for (int hf = 0; ok && hf < halves; ++hf) {
+                    if (i < 0) ok = wait_one(ct, &ct.qfull[hf], (hf ? tiles1 : tiles0) & 1);
+                    if (ok) scores(hf, (hf ? n1 : n0) + i + 1);
                 }
-                if (i < stages) {  // S = Q K^T of stage i
-#pragma unroll
-                    for (int kk = 0; kk < D; kk += 16)  // 16 channels: 32 bytes of a 128-byte row
-                        mma_ts(tm + s_col(hf), tm + q_col(hf) + kk / 2,
-                               kd + (kk >> 6) * (kStage * 128 / 16) + (kk & 63) / 8, idesc_f16(kHalf, kStage, false),
-                               kk > 0);
-                    mma_commit(&ct.sfull[hf]);
-                    mbar_arrive(&ct.sfull[hf]);  // hands on the scales, which came with kfull
-                }
+                if (++buf == kKBuffers) { buf = 0; parity ^= 1; }
+            } else {  // no S follows: the rows' threads ask here for the product of the stage before
+                for (int hf = 0; hf < halves; ++hf) mma_commit(&ct.lastv[hf]);
             }
-            if (i > 0 && ++vbuf == kBuffers) { vbuf = 0; vparity ^= 1; }
-            if (i < stages && ++buf == kBuffers) { buf = 0; parity ^= 1; }
+            if (i < 0) continue;
+            ok = ok && wait_one(ct, &ct.vfull[vbuf], vparity);
+            for (int hf = 0; ok && hf < halves; ++hf) {
+                const uint32_t n = (hf ? n1 : n0) + i;
+                ok = wait_one(ct, &ct.pfull[hf][n & 1], (n >> 1) & 1);
+                if (!ok) break;
+                values(hf, n, i > 0);
+                if (i == stages - 1) mma_commit(&ct.ofull[hf]);
+            }
+            if (++vbuf == kVBuffers) { vbuf = 0; vparity ^= 1; }
         }
         n0 += stages;
         ++tiles0;
@@ -410,9 +427,10 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* sme
 
 // ------------------------------------------------------------------ warps 0-7: a row per thread
 template <int D, bool E4M3>
-__device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Walk walk) {
+__device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
     const int hf = threadIdx.x / kHalf, r = threadIdx.x % kHalf, lane = threadIdx.x & 31;
-    const uint32_t tm = warp_lane_base(ct.tmem), ts = tm + s_col(hf), to = tm + o_col(hf);
+    const uint32_t tm = warp_lane_base(ct.tmem), to = tm + o_col(hf);
+    uint8_t* qrow = smem + Smem<D>::q + hf * Smem<D>::qtile + r * 128;
     uint32_t n = 0;  // stages that this half has seen
     uint32_t all = 0;  // and that the block has
     uint32_t tiles = 0;
@@ -445,25 +463,16 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
         query_scale(top, e, up, rest);
         if (p.scale < 0.f) up = -up;
 #pragma unroll
-        for (int j = 0; j < D / 8; j += 2) {
-            float u[8];  // 16 queries, two a column
+        for (int j = 0; j < D / 8; ++j) {
+            float x[8];
+            unpack8(raw[j], x);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float x[8];
-                unpack8(raw[j + i], x);
-#pragma unroll
-                for (int q = 0; q < 8; ++q) x[q] = x[q] * up * rest;
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    u[4 * i + 2 * q] = __uint_as_float(pack_half(x[4 * q], x[4 * q + (E4M3 ? 1 : 2)]));
-                    u[4 * i + 2 * q + 1] = __uint_as_float(pack_half(x[4 * q + (E4M3 ? 2 : 1)], x[4 * q + 3]));
-                }
-            }
-            __syncwarp();
-            tmem_st8(tm + q_col(hf) + 4 * j, u);
+            for (int q = 0; q < 8; ++q) x[q] = x[q] * up * rest;
+            constexpr int a = E4M3 ? 1 : 2, b = 3 - a;  // the order of convert16
+            *reinterpret_cast<uint4*>(qrow + (j >> 3) * kHalf * 128 + (((j & 7) ^ (r & 7)) << 4)) =
+                make_uint4(pack_half(x[0], x[a]), pack_half(x[b], x[3]), pack_half(x[4], x[4 + a]), pack_half(x[4 + b], x[7]));
         }
-        tmem_st_wait();
-        tc_fence_before();
+        fence_async_smem();
         warp_arrive(&ct.qfull[hf]);
         const float qs = ldexpf(fabsf(p.scale) * kLog2e, e);
         // positions that every row of the half sees need no mask
@@ -472,10 +481,11 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
         float l = 0.f, m = kNegInf, M = kNegInf;
         for (int i = 0; i < stages; ++i, ++n, ++all) {
             const int first = (s.t.s0 + s.from + i) * kStage;
-            if (!wait(ct, &ct.sfull[hf], n & 1)) return;
-            if (last && lane == 0) {  // S of this stage is there, and with it the products with V of the one before
-                mbar_arrive(&ct.kempty[all % kBuffers]);
-                if (i > 0) mbar_arrive(&ct.vempty[(all - 1) % kBuffers]);
+            const uint32_t ts = tm + s_col(hf, n & 1);
+            if (!wait(ct, &ct.sfull[hf][n & 1], (n >> 1) & 1)) return;
+            if (last && lane == 0) {  // S of this stage is there, and the products with V of the last but one
+                mbar_arrive(&ct.kempty[all % kKBuffers]);
+                if (i > 1) mbar_arrive(&ct.vempty[(all - 2) % kVBuffers]);
             }
             tc_fence_after();
             const StageMeta& mt = ct.meta[all % kMetas];
@@ -537,6 +547,11 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
                 const float up2 = ceilf(need), f = grow ? pow2i(M - up2) : 1.f;
                 if (grow) M = up2;
                 if (i > 0) {
+                    // O has the product of the stage before
+                    if (!(i + 1 < stages ? wait(ct, &ct.sfull[hf][(n + 1) & 1], ((n + 1) >> 1) & 1)
+                                         : wait(ct, &ct.lastv[hf], tiles & 1)))
+                        return;
+                    tc_fence_after();
 #pragma unroll 1
                     for (int j = 0; j < D; j += 32) {
                         float y[2][16];
@@ -576,11 +591,14 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, Control& ct, Wa
             l += l2.x + l2.y;
             tmem_st_wait();
             tc_fence_before();
-            warp_arrive(&ct.pfull[hf]);
+            warp_arrive(&ct.pfull[hf][n & 1]);
         }
         // the row leaves
         if (!wait(ct, &ct.ofull[hf], tiles & 1)) return;
-        if (last && lane == 0) mbar_arrive(&ct.vempty[(all - 1) % kBuffers]);
+        if (last && lane == 0) {
+            if (stages > 1) mbar_arrive(&ct.vempty[(all - 2) % kVBuffers]);
+            mbar_arrive(&ct.vempty[(all - 1) % kVBuffers]);
+        }
         ++tiles;
         tc_fence_after();
         const int rr = hf * kHalf + r;
@@ -646,15 +664,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
             mbar_init(&ct.rfull[i], 1);
             mbar_init(&ct.rempty[i], 4);
         }
-        for (int i = 0; i < kBuffers; ++i) {
-            mbar_init(&ct.kfull[i], 4);
+        for (int i = 0; i < kKBuffers; ++i) {
+            mbar_init(&ct.kfull[i], 2);
             mbar_init(&ct.kempty[i], 4);
-            mbar_init(&ct.vfull[i], 4);
+        }
+        for (int i = 0; i < kVBuffers; ++i) {
+            mbar_init(&ct.vfull[i], 2);
             mbar_init(&ct.vempty[i], 4);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&ct.sfull[i], 2);
-            mbar_init(&ct.pfull[i], 4);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&ct.sfull[i][j], 2);
+                mbar_init(&ct.pfull[i][j], 4);
+            }
+            mbar_init(&ct.lastv[i], 1);
             mbar_init(&ct.ofull[i], 1);
             mbar_init(&ct.qfull[i], 4);
         }
@@ -667,7 +690,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp < 8) soften_rows<D, E4M3>(p, ct, walk);
+    if (warp < 8) soften_rows<D, E4M3>(p, smem, ct, walk);
     else if (warp < 12) convert_codes<D, E4M3>(p, smem, ct, walk);
     else if (warp == 13) copy_pages<D>(p, smem, ct, walk);
     else if ((threadIdx.x & 31) == 0) issue_products<D>(p, smem, ct, walk);
