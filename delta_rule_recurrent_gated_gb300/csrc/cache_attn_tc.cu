@@ -170,8 +170,7 @@ struct __align__(16) StageMeta {  // read as 16-byte words
 };
 struct Control {
     uint64_t rfull[kRaw], rempty[kRaw], kfull[kKBuffers], kempty[kKBuffers], vfull[kVBuffers], vempty[kVBuffers];
-    uint64_t sfull[2][2], pfull[2][2];  // of each half, by the stage's S
-    uint64_t lastv[2], ofull[2], qfull[2], drain;
+    uint64_t sfull[2], pfull[2], lastv, ofull, qfull, drain;
     uint32_t tmem;
     volatile int dead;
     StageMeta meta[kMetas];
@@ -210,6 +209,12 @@ __device__ __forceinline__ bool wait_one(Control& ct, uint64_t* bar, uint32_t pa
 // Of a whole warp.
 __device__ __forceinline__ bool wait(Control& ct, uint64_t* bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_one(ct, bar, parity));
+}
+// One lane of a converged warp: the compiler then keeps descriptors in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
 }
 // D[tmem] (+)= A[tmem] B[smem], 16-bit floats (A: a row per lane, two values a column), fp32 accumulator.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
@@ -353,10 +358,10 @@ __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem
 }
 
 // ------------------------------------------------------------------ warp 12: the products
-// One thread.  Products of one thread run in the order of their issue: S of stage i + 1, over the
-// columns of P of stage i - 1, follows that P's product, and its completion says that O has it.  A
-// commit holds the thread up for some 200 cycles, so there is one for each S: the rows' threads free
-// the buffers of K and V once they see S of the last half.
+// Products of one thread run in the order of their issue: S of stage n + 1, over the columns of P of
+// stage n - 1, follows that P's products, and its completion says that O has them.  Every wait, every
+// commit and every switch between the products costs this warp 100 to 250 cycles, so both halves go
+// together: one S commit and two groups of products a stage.
 template <int D>
 __device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
     const uint32_t base = smem_u32(smem), tm = ct.tmem;
@@ -364,63 +369,66 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* sme
     const uint64_t k0 = desc_kmajor(Tile{base + Smem<D>::k, kStage}, 0);
     const uint64_t v0 = desc_mnmajor(Tile{base + Smem<D>::v, kStage}, 0);
     const uint64_t q0 = desc_kmajor(Tile{base + Smem<D>::q, kHalf}, 0);
-    uint32_t buf = 0, parity = 0, vbuf = 0, vparity = 0;
-    uint32_t n0 = 0, n1 = 0, tiles0 = 0, tiles1 = 0;  // stages and tiles of each half so far
-    // S = Q K^T of a half, its n-th stage
-    auto scores = [&](int hf, uint32_t n) {
-        const uint64_t kd = k0 + buf * (Smem<D>::tile >> 4), qd = q0 + hf * (Smem<D>::qtile >> 4);
+    uint32_t buf = 0, parity = 0, vbuf = 0, vparity = 0, n = 0, tiles = 0;
+    // S = Q K^T of both halves
+    auto scores = [&](uint32_t at) {
+        const uint64_t kd = k0 + buf * (Smem<D>::tile >> 4);
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < D; kk += 16)  // 16 channels: 32 bytes of a 128-byte row
-            mma_bf16(tm + s_col(hf, n & 1), qd + (kk >> 6) * (kHalf * 128 / 16) + (kk & 63) / 8,
-                     kd + (kk >> 6) * (kStage * 128 / 16) + (kk & 63) / 8, idesc_f16(kHalf, kStage, false), kk > 0);
-        mma_commit(&ct.sfull[hf][n & 1]);
-        mbar_arrive(&ct.sfull[hf][n & 1]);  // hands on the scales, which came with kfull
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int kk = 0; kk < D; kk += 16)  // 16 channels: 32 bytes of a 128-byte row
+                    mma_bf16(tm + s_col(hf, at & 1),
+                             q0 + hf * (Smem<D>::qtile >> 4) + (kk >> 6) * (kHalf * 128 / 16) + (kk & 63) / 8,
+                             kd + (kk >> 6) * (kStage * 128 / 16) + (kk & 63) / 8, idesc_f16(kHalf, kStage, false), kk > 0);
+            mma_commit(&ct.sfull[at & 1]);
+            mbar_arrive(&ct.sfull[at & 1]);  // hands on the scales, which came with kfull
+        }
+        __syncwarp();
     };
-    // O += P V of a half, its n-th stage
-    auto values = [&](int hf, uint32_t n, bool more) {
+    // O += P V of both halves
+    auto values = [&](uint32_t at, bool more, uint64_t* done) {
         const uint64_t vd = v0 + vbuf * (Smem<D>::tile >> 4);
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kStage; kk += 16)  // 16 positions: 16 rows of 128 bytes
-            mma_ts(tm + o_col(hf), tm + s_col(hf, n & 1) + kk / 2, vd + kk * 8, idesc_f16(kHalf, D, true), more || kk > 0);
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int kk = 0; kk < kStage; kk += 16)  // 16 positions: 16 rows of 128 bytes
+                    mma_ts(tm + o_col(hf), tm + s_col(hf, at & 1) + kk / 2, vd + kk * 8, idesc_f16(kHalf, D, true),
+                           more || kk > 0);
+            if (done) mma_commit(done);
+        }
+        __syncwarp();
     };
     Stretch s;
     bool ok = true;
     while (ok && walk.next(p, s)) {
         const int stages = s.upto - s.from;
-        const int halves = s.t.row0 + kHalf < s.n * p.G ? 2 : 1;
+        ok = wait(ct, &ct.qfull, tiles & 1);
         for (int i = -1; ok && i < stages; ++i) {
             if (i + 1 < stages) {
-                ok = wait_one(ct, &ct.kfull[buf], parity);
-                for (int hf = 0; ok && hf < halves; ++hf) {
-                    if (i < 0) ok = wait_one(ct, &ct.qfull[hf], (hf ? tiles1 : tiles0) & 1);
-                    if (ok) scores(hf, (hf ? n1 : n0) + i + 1);
-                }
+                ok = wait(ct, &ct.kfull[buf], parity);
+                if (!ok) break;
+                scores(n + 1 + i);
                 if (++buf == kKBuffers) { buf = 0; parity ^= 1; }
-            } else {  // no S follows: the rows' threads ask here for the product of the stage before
-                for (int hf = 0; hf < halves; ++hf) mma_commit(&ct.lastv[hf]);
+            } else {  // no S follows: the rows' threads ask here for the products of the stage before
+                if (elect_one()) mma_commit(&ct.lastv);
+                __syncwarp();
             }
             if (i < 0) continue;
-            ok = ok && wait_one(ct, &ct.vfull[vbuf], vparity);
-            for (int hf = 0; ok && hf < halves; ++hf) {
-                const uint32_t n = (hf ? n1 : n0) + i;
-                ok = wait_one(ct, &ct.pfull[hf][n & 1], (n >> 1) & 1);
-                if (!ok) break;
-                values(hf, n, i > 0);
-                if (i == stages - 1) mma_commit(&ct.ofull[hf]);
-            }
+            ok = wait(ct, &ct.vfull[vbuf], vparity) && wait(ct, &ct.pfull[(n + i) & 1], ((n + i) >> 1) & 1);
+            if (!ok) break;
+            values(n + i, i > 0, i == stages - 1 ? &ct.ofull : nullptr);
             if (++vbuf == kVBuffers) { vbuf = 0; vparity ^= 1; }
         }
-        n0 += stages;
-        ++tiles0;
-        if (halves == 2) {
-            n1 += stages;
-            ++tiles1;
-        }
+        n += stages;
+        ++tiles;
     }
     if (!ok) {  // let what is in flight end before the tensor memory goes
-        mma_commit(&ct.drain);
+        if (elect_one()) mma_commit(&ct.drain);
+        __syncwarp();
         mbar_wait(&ct.drain, 0, kWaitLimitNs);
     }
 }
@@ -428,21 +436,15 @@ __device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* sme
 // ------------------------------------------------------------------ warps 0-7: a row per thread
 template <int D, bool E4M3>
 __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
-    const int hf = threadIdx.x / kHalf, r = threadIdx.x % kHalf, lane = threadIdx.x & 31;
+    const int hf = threadIdx.x / kHalf, r = threadIdx.x % kHalf;
     const uint32_t tm = warp_lane_base(ct.tmem), to = tm + o_col(hf);
     uint8_t* qrow = smem + Smem<D>::q + hf * Smem<D>::qtile + r * 128;
-    uint32_t n = 0;  // stages that this half has seen
-    uint32_t all = 0;  // and that the block has
-    uint32_t tiles = 0;
+    uint32_t n = 0, tiles = 0;  // stages and tiles so far
     Stretch s;
     while (walk.next(p, s)) {
         const int stages = s.upto - s.from, row = s.t.row0 + hf * kHalf + r;
-        if (s.t.row0 + hf * kHalf >= s.n * p.G) {  // no rows in this half
-            all += stages;
-            continue;
-        }
         const bool on = row < s.n * p.G;
-        const bool last = hf == 1 || s.t.row0 + kHalf >= s.n * p.G;  // the last half with rows
+        const bool some = s.t.row0 + hf * kHalf < s.n * p.G;  // the half has rows
         const int tok = on ? row / p.G : 0, head = s.h * p.G + (on ? row % p.G : 0), pos = on ? s.len + tok : -1;
         // the row's queries, scaled, as operand (with the sign of the scale, so that factors are positive)
         const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
@@ -473,22 +475,26 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
                 make_uint4(pack_half(x[0], x[a]), pack_half(x[b], x[3]), pack_half(x[4], x[4 + a]), pack_half(x[4 + b], x[7]));
         }
         fence_async_smem();
-        warp_arrive(&ct.qfull[hf]);
+        warp_arrive(&ct.qfull);
         const float qs = ldexpf(fabsf(p.scale) * kLog2e, e);
         // positions that every row of the half sees need no mask
         const int t0 = (s.t.row0 + hf * kHalf) / p.G, t1 = min(s.n - 1, (s.t.row0 + hf * kHalf + kHalf - 1) / p.G);
         const int all_hi = s.len + t0 + 1, all_lo = p.window > 0 ? max(0, s.len + t1 - p.window + 1) : 0;
         float l = 0.f, m = kNegInf, M = kNegInf;
-        for (int i = 0; i < stages; ++i, ++n, ++all) {
+        for (int i = 0; i < stages; ++i, ++n) {
             const int first = (s.t.s0 + s.from + i) * kStage;
             const uint32_t ts = tm + s_col(hf, n & 1);
-            if (!wait(ct, &ct.sfull[hf][n & 1], (n >> 1) & 1)) return;
-            if (last && lane == 0) {  // S of this stage is there, and the products with V of the last but one
-                mbar_arrive(&ct.kempty[all % kKBuffers]);
-                if (i > 1) mbar_arrive(&ct.vempty[(all - 2) % kVBuffers]);
+            if (!wait(ct, &ct.sfull[n & 1], (n >> 1) & 1)) return;
+            if (threadIdx.x == 0) {  // S of this stage is there, and the products with V of the last but one
+                mbar_arrive(&ct.kempty[n % kKBuffers]);
+                if (i > 1) mbar_arrive(&ct.vempty[(n - 2) % kVBuffers]);
+            }
+            if (!some) {
+                warp_arrive(&ct.pfull[n & 1]);
+                continue;
             }
             tc_fence_after();
-            const StageMeta& mt = ct.meta[all % kMetas];
+            const StageMeta& mt = ct.meta[n % kMetas];
             const float4 ks4 = *reinterpret_cast<const float4*>(mt.ks), vs4 = *reinterpret_cast<const float4*>(mt.vs);
             const float4 lv4 = *reinterpret_cast<const float4*>(mt.lv);
             float kf[4] = {qs * ks4.x, qs * ks4.y, qs * ks4.z, qs * ks4.w}, vs[4] = {vs4.x, vs4.y, vs4.z, vs4.w};
@@ -548,8 +554,8 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
                 if (grow) M = up2;
                 if (i > 0) {
                     // O has the product of the stage before
-                    if (!(i + 1 < stages ? wait(ct, &ct.sfull[hf][(n + 1) & 1], ((n + 1) >> 1) & 1)
-                                         : wait(ct, &ct.lastv[hf], tiles & 1)))
+                    if (!(i + 1 < stages ? wait(ct, &ct.sfull[(n + 1) & 1], ((n + 1) >> 1) & 1)
+                                         : wait(ct, &ct.lastv, tiles & 1)))
                         return;
                     tc_fence_after();
 #pragma unroll 1
@@ -591,13 +597,13 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
             l += l2.x + l2.y;
             tmem_st_wait();
             tc_fence_before();
-            warp_arrive(&ct.pfull[hf][n & 1]);
+            warp_arrive(&ct.pfull[n & 1]);
         }
         // the row leaves
-        if (!wait(ct, &ct.ofull[hf], tiles & 1)) return;
-        if (last && lane == 0) {
-            if (stages > 1) mbar_arrive(&ct.vempty[(all - 2) % kVBuffers]);
-            mbar_arrive(&ct.vempty[(all - 1) % kVBuffers]);
+        if (!wait(ct, &ct.ofull, tiles & 1)) return;
+        if (threadIdx.x == 0) {
+            if (stages > 1) mbar_arrive(&ct.vempty[(n - 2) % kVBuffers]);
+            mbar_arrive(&ct.vempty[(n - 1) % kVBuffers]);
         }
         ++tiles;
         tc_fence_after();
@@ -666,21 +672,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
         }
         for (int i = 0; i < kKBuffers; ++i) {
             mbar_init(&ct.kfull[i], 2);
-            mbar_init(&ct.kempty[i], 4);
+            mbar_init(&ct.kempty[i], 1);
         }
         for (int i = 0; i < kVBuffers; ++i) {
             mbar_init(&ct.vfull[i], 2);
-            mbar_init(&ct.vempty[i], 4);
+            mbar_init(&ct.vempty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            for (int j = 0; j < 2; ++j) {
-                mbar_init(&ct.sfull[i][j], 2);
-                mbar_init(&ct.pfull[i][j], 4);
-            }
-            mbar_init(&ct.lastv[i], 1);
-            mbar_init(&ct.ofull[i], 1);
-            mbar_init(&ct.qfull[i], 4);
+            mbar_init(&ct.sfull[i], 2);
+            mbar_init(&ct.pfull[i], 8);
         }
+        mbar_init(&ct.lastv, 1);
+        mbar_init(&ct.ofull, 1);
+        mbar_init(&ct.qfull, 8);
         mbar_init(&ct.drain, 1);
         ct.dead = 0;
         fence_barrier_init();
@@ -693,7 +697,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     if (warp < 8) soften_rows<D, E4M3>(p, smem, ct, walk);
     else if (warp < 12) convert_codes<D, E4M3>(p, smem, ct, walk);
     else if (warp == 13) copy_pages<D>(p, smem, ct, walk);
-    else if ((threadIdx.x & 31) == 0) issue_products<D>(p, smem, ct, walk);
+    else issue_products<D>(p, smem, ct, walk);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
