@@ -11,9 +11,8 @@
 // products every stage: 2950 cycles for both halves, where the products take 1140).  Shared memory
 // holds Q, and K and V as 16-bit floats (exact), three stages of them.
 // Warp 13 has the codes copied to a ring in shared memory; warps 8-11 turn them into the operand
-// tiles; warp 12 issues the products, the halves in turn, so that one half's weights are formed while
-// the other's products run; warps 0-3 and 4-7 hold a row per thread: they read S, keep the softmax
-// statistics and write P.
+// tiles; warps 12 and 14 issue the products; warps 0-3 and 4-7 hold a row of their half per thread:
+// they read S, keep the softmax statistics and write P.
 //
 // Softmax in base 2 with whole-number references, as in cache_attn.cu: p = 2^(s - m), l = sum p,
 // operand w = p vs 2^(m - M + 13).  The accumulator is rescaled (exactly, by a power of two) only when
@@ -34,7 +33,7 @@ namespace {
 using namespace tc;
 
 constexpr int kHalf = 128, kRows = 2 * kHalf, kStage = 64;
-constexpr int kTcThreads = 448;  // eight warps of rows, four of codes, one that issues, one that copies
+constexpr int kTcThreads = 480;  // eight warps of rows, four of codes, two that issue products, one that copies
 constexpr int kCodeThread0 = 256;
 constexpr int kKBuffers = 3, kVBuffers = 4;  // stages of K and V as operands: V is needed for longer
 constexpr int kRaw = 3;                      // as codes
@@ -170,7 +169,7 @@ struct __align__(16) StageMeta {  // read as 16-byte words
 };
 struct Control {
     uint64_t rfull[kRaw], rempty[kRaw], kfull[kKBuffers], kempty[kKBuffers], vfull[kVBuffers], vempty[kVBuffers];
-    uint64_t sfull[2], pfull[2], lastv, ofull, qfull, drain;
+    uint64_t sfull[2], pfull[2], odone[2], qfull, drain[2];
     uint32_t tmem;
     volatile int dead;
     StageMeta meta[kMetas];
@@ -357,80 +356,79 @@ __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem
     }
 }
 
-// ------------------------------------------------------------------ warp 12: the products
-// Products of one thread run in the order of their issue: S of stage n + 1, over the columns of P of
-// stage n - 1, follows that P's products, and its completion says that O has them.  Every wait, every
-// commit and every switch between the products costs this warp 100 to 250 cycles, so both halves go
-// together: one S commit and two groups of products a stage.
+// ------------------------------------------------------------------ warps 12 and 14: the products
+// A wait, a commit and a switch from one product to the other cost the issuing warp 100 to 250 cycles
+// each, so S and O have a warp each, which issues both halves together.
+// S = Q K^T of stage n, over the columns of P of stage n - 2: after that P's products.
 template <int D>
-__device__ __forceinline__ void issue_products(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
+__device__ __forceinline__ void issue_scores(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
     const uint32_t base = smem_u32(smem), tm = ct.tmem;
     // descriptors of the first buffers; an address step of 16 bytes is 1 in their lowest field
     const uint64_t k0 = desc_kmajor(Tile{base + Smem<D>::k, kStage}, 0);
-    const uint64_t v0 = desc_mnmajor(Tile{base + Smem<D>::v, kStage}, 0);
     const uint64_t q0 = desc_kmajor(Tile{base + Smem<D>::q, kHalf}, 0);
-    uint32_t buf = 0, parity = 0, vbuf = 0, vparity = 0, n = 0, tiles = 0;
-    // S = Q K^T of both halves
-    auto scores = [&](uint32_t at) {
-        const uint64_t kd = k0 + buf * (Smem<D>::tile >> 4);
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int kk = 0; kk < D; kk += 16)  // 16 channels: 32 bytes of a 128-byte row
-                    mma_bf16(tm + s_col(hf, at & 1),
-                             q0 + hf * (Smem<D>::qtile >> 4) + (kk >> 6) * (kHalf * 128 / 16) + (kk & 63) / 8,
-                             kd + (kk >> 6) * (kStage * 128 / 16) + (kk & 63) / 8, idesc_f16(kHalf, kStage, false), kk > 0);
-            mma_commit(&ct.sfull[at & 1]);
-            mbar_arrive(&ct.sfull[at & 1]);  // hands on the scales, which came with kfull
-        }
-        __syncwarp();
-    };
-    // O += P V of both halves
-    auto values = [&](uint32_t at, bool more, uint64_t* done) {
-        const uint64_t vd = v0 + vbuf * (Smem<D>::tile >> 4);
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                for (int kk = 0; kk < kStage; kk += 16)  // 16 positions: 16 rows of 128 bytes
-                    mma_ts(tm + o_col(hf), tm + s_col(hf, at & 1) + kk / 2, vd + kk * 8, idesc_f16(kHalf, D, true),
-                           more || kk > 0);
-            if (done) mma_commit(done);
-        }
-        __syncwarp();
-    };
+    uint32_t buf = 0, parity = 0, n = 0, tiles = 0;
     Stretch s;
-    bool ok = true;
-    while (ok && walk.next(p, s)) {
+    while (walk.next(p, s)) {
         const int stages = s.upto - s.from;
-        ok = wait(ct, &ct.qfull, tiles & 1);
-        for (int i = -1; ok && i < stages; ++i) {
-            if (i + 1 < stages) {
-                ok = wait(ct, &ct.kfull[buf], parity);
-                if (!ok) break;
-                scores(n + 1 + i);
-                if (++buf == kKBuffers) { buf = 0; parity ^= 1; }
-            } else {  // no S follows: the rows' threads ask here for the products of the stage before
-                if (elect_one()) mma_commit(&ct.lastv);
-                __syncwarp();
-            }
-            if (i < 0) continue;
-            ok = wait(ct, &ct.vfull[vbuf], vparity) && wait(ct, &ct.pfull[(n + i) & 1], ((n + i) >> 1) & 1);
-            if (!ok) break;
-            values(n + i, i > 0, i == stages - 1 ? &ct.ofull : nullptr);
-            if (++vbuf == kVBuffers) { vbuf = 0; vparity ^= 1; }
-        }
-        n += stages;
+        if (!wait(ct, &ct.qfull, tiles & 1)) return;
         ++tiles;
+        for (int i = 0; i < stages; ++i, ++n) {
+            if (!wait(ct, &ct.kfull[buf], parity)) return;
+            if (n >= 2 && !wait(ct, &ct.odone[n & 1], ((n - 2) >> 1) & 1)) return;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t kd = k0 + buf * (Smem<D>::tile >> 4);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int kk = 0; kk < D; kk += 16)  // 16 channels: 32 bytes of a 128-byte row
+                        mma_bf16(tm + s_col(hf, n & 1),
+                                 q0 + hf * (Smem<D>::qtile >> 4) + (kk >> 6) * (kHalf * 128 / 16) + (kk & 63) / 8,
+                                 kd + (kk >> 6) * (kStage * 128 / 16) + (kk & 63) / 8, idesc_f16(kHalf, kStage, false),
+                                 kk > 0);
+                mma_commit(&ct.sfull[n & 1]);
+                mbar_arrive(&ct.sfull[n & 1]);  // hands on the scales, which came with kfull
+                mma_commit(&ct.kempty[buf]);
+            }
+            __syncwarp();
+            if (++buf == kKBuffers) { buf = 0; parity ^= 1; }
+        }
     }
-    if (!ok) {  // let what is in flight end before the tensor memory goes
-        if (elect_one()) mma_commit(&ct.drain);
-        __syncwarp();
-        mbar_wait(&ct.drain, 0, kWaitLimitNs);
+}
+// O += P V.
+template <int D>
+__device__ __forceinline__ void issue_values(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
+    const uint32_t tm = ct.tmem;
+    const uint64_t v0 = desc_mnmajor(Tile{smem_u32(smem) + Smem<D>::v, kStage}, 0);
+    uint32_t buf = 0, parity = 0, n = 0;
+    Stretch s;
+    while (walk.next(p, s)) {
+        const int stages = s.upto - s.from;
+        for (int i = 0; i < stages; ++i, ++n) {
+            if (!wait(ct, &ct.vfull[buf], parity) || !wait(ct, &ct.pfull[n & 1], (n >> 1) & 1)) return;
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t vd = v0 + buf * (Smem<D>::tile >> 4);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                    for (int kk = 0; kk < kStage; kk += 16)  // 16 positions: 16 rows of 128 bytes
+                        mma_ts(tm + o_col(hf), tm + s_col(hf, n & 1) + kk / 2, vd + kk * 8, idesc_f16(kHalf, D, true),
+                               i > 0 || kk > 0);
+                mma_commit(&ct.odone[n & 1]);
+                mma_commit(&ct.vempty[buf]);
+            }
+            __syncwarp();
+            if (++buf == kVBuffers) { buf = 0; parity ^= 1; }
+        }
     }
+}
+// Lets what a warp has in flight end before the tensor memory goes.
+__device__ __forceinline__ void drain(Control& ct, uint64_t* bar) {
+    __syncwarp();
+    if (elect_one()) mma_commit(bar);
+    __syncwarp();
+    mbar_wait(bar, 0, kWaitLimitNs);
 }
 
 // ------------------------------------------------------------------ warps 0-7: a row per thread
@@ -439,7 +437,7 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
     const int hf = threadIdx.x / kHalf, r = threadIdx.x % kHalf;
     const uint32_t tm = warp_lane_base(ct.tmem), to = tm + o_col(hf);
     uint8_t* qrow = smem + Smem<D>::q + hf * Smem<D>::qtile + r * 128;
-    uint32_t n = 0, tiles = 0;  // stages and tiles so far
+    uint32_t n = 0;  // stages so far
     Stretch s;
     while (walk.next(p, s)) {
         const int stages = s.upto - s.from, row = s.t.row0 + hf * kHalf + r;
@@ -485,10 +483,6 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
             const int first = (s.t.s0 + s.from + i) * kStage;
             const uint32_t ts = tm + s_col(hf, n & 1);
             if (!wait(ct, &ct.sfull[n & 1], (n >> 1) & 1)) return;
-            if (threadIdx.x == 0) {  // S of this stage is there, and the products with V of the last but one
-                mbar_arrive(&ct.kempty[n % kKBuffers]);
-                if (i > 1) mbar_arrive(&ct.vempty[(n - 2) % kVBuffers]);
-            }
             if (!some) {
                 warp_arrive(&ct.pfull[n & 1]);
                 continue;
@@ -554,9 +548,7 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
                 if (grow) M = up2;
                 if (i > 0) {
                     // O has the product of the stage before
-                    if (!(i + 1 < stages ? wait(ct, &ct.sfull[(n + 1) & 1], ((n + 1) >> 1) & 1)
-                                         : wait(ct, &ct.lastv, tiles & 1)))
-                        return;
+                    if (!wait(ct, &ct.odone[(n - 1) & 1], ((n - 1) >> 1) & 1)) return;
                     tc_fence_after();
 #pragma unroll 1
                     for (int j = 0; j < D; j += 32) {
@@ -600,12 +592,7 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
             warp_arrive(&ct.pfull[n & 1]);
         }
         // the row leaves
-        if (!wait(ct, &ct.ofull, tiles & 1)) return;
-        if (threadIdx.x == 0) {
-            if (stages > 1) mbar_arrive(&ct.vempty[(n - 2) % kVBuffers]);
-            mbar_arrive(&ct.vempty[(n - 1) % kVBuffers]);
-        }
-        ++tiles;
+        if (!wait(ct, &ct.odone[(n - 1) & 1], ((n - 1) >> 1) & 1)) return;
         tc_fence_after();
         const int rr = hf * kHalf + r;
         float* part = p.part + ((size_t)blockIdx.x * 2 + (s.first ? 0 : 1)) * tile_floats(D, kRows);
@@ -681,11 +668,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
         for (int i = 0; i < 2; ++i) {
             mbar_init(&ct.sfull[i], 2);
             mbar_init(&ct.pfull[i], 8);
+            mbar_init(&ct.odone[i], 1);
+            mbar_init(&ct.drain[i], 1);
         }
-        mbar_init(&ct.lastv, 1);
-        mbar_init(&ct.ofull, 1);
         mbar_init(&ct.qfull, 8);
-        mbar_init(&ct.drain, 1);
         ct.dead = 0;
         fence_barrier_init();
     }
@@ -696,8 +682,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     tc_fence_after();
     if (warp < 8) soften_rows<D, E4M3>(p, smem, ct, walk);
     else if (warp < 12) convert_codes<D, E4M3>(p, smem, ct, walk);
+    else if (warp == 12) issue_scores<D>(p, smem, ct, walk), drain(ct, &ct.drain[0]);
     else if (warp == 13) copy_pages<D>(p, smem, ct, walk);
-    else issue_products<D>(p, smem, ct, walk);
+    else issue_values<D>(p, smem, ct, walk), drain(ct, &ct.drain[1]);
     __syncwarp();
     tc_fence_before();
     __syncthreads();
