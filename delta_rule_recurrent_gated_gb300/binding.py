@@ -437,7 +437,7 @@ class Gdn2Problem(Problem):
 def _rows(t, shape, what):
     """Elements between the token rows of t, a tensor of the given shape [B, T, heads, d]:
     contiguous, or a range of heads of a wider contiguous tensor."""
-    if t.shape == shape:
+    if t.shape == shape and t.is_cuda:
         B, T, H, D = shape
         if t.is_contiguous():
             return H * D
@@ -445,14 +445,18 @@ def _rows(t, shape, what):
         ld = s[1] if T > 1 else s[0]
         if (D == 1 or s[3] == 1) and (H == 1 or s[2] == D) and (T == 1 or B == 1 or s[0] == T * ld):
             return ld if B * T > 1 else H * D
-    raise ValueError(f"{what}: shape {tuple(t.shape)} strides {t.stride()} is no {tuple(shape)} with whole "
-                     "token rows at one distance")
+    raise ValueError(f"{what}: shape {tuple(t.shape)} strides {t.stride()} on {t.device} is no {tuple(shape)} "
+                     "in device memory with whole token rows at one distance")
 
 
-def _expect(t, dtype, shape, what):
-    if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, got "
-                         f"{t.dtype} {tuple(t.shape)}")
+def _address(t, dtype, shape, what):
+    """Address of a contiguous tensor of the given type and shape, or None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)} in device "
+                         f"memory, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 _TORCH_TYPES = {"bf16": "bfloat16", "f32": "float32"}
@@ -472,16 +476,16 @@ class _Calls:
         self.device = torch.device(device)
         if self.device.type == "cuda" and self.device.index is None and torch.cuda.is_available():
             self.device = torch.device("cuda", torch.cuda.current_device())
-        self._torch = torch
+        self._torch, self._f32, self._i32 = torch, torch.float32, torch.int32
         self._lib = load()
+        self._index = self.device.index
         # the handle alone where torch offers it: building a Stream object costs more than a launch
         self._raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if self._raw is None or self._index is None:
+            self._raw = lambda _: torch.cuda.current_stream(self.device).cuda_stream
 
     def _stream(self):
-        index = self.device.index
-        if self._raw is None or index is None:
-            return self._torch.cuda.current_stream(self.device).cuda_stream
-        return self._raw(index)
+        return self._raw(self._index)
 
     def _empty(self, shape, dtype):
         return self._torch.empty(shape, dtype=dtype, device=self.device)
@@ -509,67 +513,72 @@ class HeadNormRope(_Calls):
         e.table_rows = 0
         self.desc, self._ref = e, ctypes.byref(e)
         self.io_dtype, self.out_dtype, self.grad_dtype = map(_torch_type, (io, out, grad))
-        self._q, self._k, self._rot = (B, T, Hq, d), (B, T, Hk, d), e.rot
+        self._q, self._k, self._w, self._rot = (B, T, Hq, d), (B, T, Hk, d), (d,), e.rot
+        self._fwd, self._bwd = self._lib.dr_norm_rope_fwd, self._lib.dr_norm_rope_bwd
         self.ws = None
         if int(self._lib.dr_norm_rope_workspace_bytes(self._ref)) == 0:
             raise DrError(DR_ERR_UNSUPPORTED, "dr_norm_rope_workspace_bytes")
 
-    def _fill(self, q, k, wq, wk, cos, sin, positions, start, oq, ok, out_dtype):
-        """Checks the tensors of a call and notes their row distances in the descriptor."""
-        torch, e = self._torch, self.desc
-        f32, i32 = torch.float32, torch.int32
-        for t, o, shape, what in ((q, oq, self._q, "q"), (k, ok, self._k, "k")):
-            if shape[2] == 0:
-                continue
-            if t.dtype is not self.io_dtype or o.dtype is not out_dtype:
-                raise ValueError(f"{what}: expected {self.io_dtype} and an output of {out_dtype}, got {t.dtype} "
-                                 f"and {o.dtype}")
-            ld, ldo = _rows(t, shape, what), _rows(o, shape, "output of " + what)
-            if what == "q":
-                e.ld_q, e.ld_oq = ld, ldo
-            else:
-                e.ld_k, e.ld_ok = ld, ldo
-        w = (e.d,)
-        _expect(wq, f32, w, "wq")
-        _expect(wk, f32, w, "wk")
+    def _inputs(self, q, k, wq, wk, cos, sin, positions, start):
+        """Checks the inputs of a call, notes what the descriptor has of them, and returns their addresses."""
+        e, f32, i32, w = self.desc, self._f32, self._i32, self._w
+        qp = kp = None
+        if self._q[2]:
+            if q.dtype is not self.io_dtype:
+                raise ValueError(f"q: expected {self.io_dtype}, got {q.dtype}")
+            e.ld_q, qp = _rows(q, self._q, "q"), q.data_ptr()
+        if self._k[2]:
+            if k.dtype is not self.io_dtype:
+                raise ValueError(f"k: expected {self.io_dtype}, got {k.dtype}")
+            e.ld_k, kp = _rows(k, self._k, "k"), k.data_ptr()
+        wqp, wkp = _address(wq, f32, w, "wq"), _address(wk, f32, w, "wk")
+        cp = sp = None
         if self._rot:
-            e.table_rows = rows = cos.shape[0]
-            table = (rows, self._rot // 2)
-            _expect(cos, f32, table, "cos")
-            _expect(sin, f32, table, "sin")
-        _expect(positions, i32, self._q[:2], "positions")
-        _expect(start, i32, self._q[:1], "start")
+            table = (cos.shape[0], self._rot // 2)
+            cp, sp = _address(cos, f32, table, "cos"), _address(sin, f32, table, "sin")
+            e.table_rows = table[0]
+        return (qp, kp, wqp, wkp, cp, sp, _address(positions, i32, self._q[:2], "positions"),
+                _address(start, i32, self._q[:1], "start"))
+
+    def _output(self, t, shape, dtype, what):
+        """A given output, or a new one, and its row distance."""
+        if t is None:
+            return self._torch.empty(shape, dtype=dtype, device=self.device), shape[2] * shape[3]
+        if t.dtype is not dtype:
+            raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+        return t, _rows(t, shape, what)
 
     def forward(self, q, k, wq, wk, cos, sin, positions=None, start=None, yq=None, yk=None):
         """yq, yk in the output type (given: written there, in place where it is q or k itself)."""
-        yq = self._empty(self._q, self.out_dtype) if yq is None else yq
-        yk = self._empty(self._k, self.out_dtype) if yk is None else yk
-        self._fill(q, k, wq, wk, cos, sin, positions, start, yq, yk, self.out_dtype)
-        _check(self._lib.dr_norm_rope_fwd(self._ref, _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin),
-                                          _ptr(positions), _ptr(start), _ptr(yq), _ptr(yk), self._stream()),
-               "dr_norm_rope_fwd")
+        e = self.desc
+        yq, e.ld_oq = self._output(yq, self._q, self.out_dtype, "yq")
+        yk, e.ld_ok = self._output(yk, self._k, self.out_dtype, "yk")
+        rc = self._fwd(self._ref, *self._inputs(q, k, wq, wk, cos, sin, positions, start), yq.data_ptr(),
+                       yk.data_ptr(), self._stream())
+        if rc:
+            raise DrError(rc, "dr_norm_rope_fwd")
         return yq, yk
 
     def backward(self, q, k, wq, wk, cos, sin, dyq, dyk, positions=None, start=None, out=None):
         """{dq, dk, dwq, dwk} for the incoming gradients dyq, dyk (contiguous, of the input type)."""
-        w = (self.desc.d,)
+        e, w, f32 = self.desc, self._w, self._f32
+        given = out or {}
+        dq, e.ld_oq = self._output(given.get("dq"), self._q, self.grad_dtype, "dq")
+        dk, e.ld_ok = self._output(given.get("dk"), self._k, self.grad_dtype, "dk")
+        dwq, dwk = given.get("dwq"), given.get("dwk")
         if out is None:
-            f32 = self._torch.float32
-            out = {"dq": self._empty(self._q, self.grad_dtype), "dk": self._empty(self._k, self.grad_dtype),
-                   "dwq": None if wq is None else self._empty(w, f32),
-                   "dwk": None if wk is None else self._empty(w, f32)}
-        self._fill(q, k, wq, wk, cos, sin, positions, start, out["dq"], out["dk"], self.grad_dtype)
-        _expect(dyq, self.io_dtype, self._q, "dyq")
-        _expect(dyk, self.io_dtype, self._k, "dyk")
-        _expect(out["dwq"], self._torch.float32, w, "dwq")
-        _expect(out["dwk"], self._torch.float32, w, "dwk")
+            empty, device = self._torch.empty, self.device
+            dwq = None if wq is None else empty(w, dtype=f32, device=device)
+            dwk = None if wk is None else empty(w, dtype=f32, device=device)
         if self.ws is None:
             self.ws = self._empty(int(self._lib.dr_norm_rope_workspace_bytes(self._ref)), self._torch.uint8)
-        _check(self._lib.dr_norm_rope_bwd(self._ref, _ptr(q), _ptr(k), _ptr(wq), _ptr(wk), _ptr(cos), _ptr(sin),
-                                          _ptr(positions), _ptr(start), _ptr(dyq), _ptr(dyk), _ptr(out["dq"]),
-                                          _ptr(out["dk"]), _ptr(out["dwq"]), _ptr(out["dwk"]), _ptr(self.ws),
-                                          self.ws.numel(), self._stream()), "dr_norm_rope_bwd")
-        return out
+        rc = self._bwd(self._ref, *self._inputs(q, k, wq, wk, cos, sin, positions, start),
+                       _address(dyq, self.io_dtype, self._q, "dyq"), _address(dyk, self.io_dtype, self._k, "dyk"),
+                       dq.data_ptr(), dk.data_ptr(), _address(dwq, f32, w, "dwq"), _address(dwk, f32, w, "dwk"),
+                       self.ws.data_ptr(), self.ws.numel(), self._stream())
+        if rc:
+            raise DrError(rc, "dr_norm_rope_bwd")
+        return {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
 
 
 class KvCache(_Calls):
@@ -588,9 +597,9 @@ class KvCache(_Calls):
             buffers += [torch.zeros(num_pages, H, dtype=torch.float32, device=self.device) for _ in range(2)]
         self.k, self.v, self.k_scale, self.v_scale = buffers
         for t, what in ((self.k, "k codes"), (self.v, "v codes")):
-            _expect(t, kind, (num_pages, H, page, d), what)
+            _address(t, kind, (num_pages, H, page, d), what)
         for t, what in ((self.k_scale, "k scales"), (self.v_scale, "v scales")):
-            _expect(t, torch.float32, (num_pages, H), what)
+            _address(t, torch.float32, (num_pages, H), what)
         self.word = torch.zeros(4, dtype=torch.int32, device=self.device)
         c = DrCache()
         c.num_pages, c.H, c.d, c.page, c.code = num_pages, H, d, page, CACHE_CODES[code]
@@ -599,39 +608,44 @@ class KvCache(_Calls):
         c.status = self.word.data_ptr()
         self.desc, self._ref = c, ctypes.byref(c)
         self._heads = (H, d)
+        self._io = {torch.bfloat16: DR_BF16, torch.float32: DR_F32}
+        self._out = {"bf16": (torch.bfloat16, DR_BF16), "f32": (torch.float32, DR_F32)}
+        self._write, self._read = self._lib.dr_cache_write, self._lib.dr_cache_read
 
     def seqs(self, B, table, lens, counts, T):
         """The call's positions: T tokens (or counts[b] <= T) after lens[b], in the pages of table
         [B, pages]."""
-        i32 = self._torch.int32
-        pages = table.shape[-1]
-        _expect(table, i32, (B, pages), "table")
-        _expect(lens, i32, (B,), "lens")
-        _expect(counts, i32, (B,), "counts")
-        return DrCacheSeqs(B, T, table.data_ptr(), pages, lens.data_ptr(), _ptr(counts))
+        i32, pages = self._i32, table.shape[-1]
+        return DrCacheSeqs(B, T, _address(table, i32, (B, pages), "table"), pages,
+                           _address(lens, i32, (B,), "lens"), _address(counts, i32, (B,), "counts"))
 
     def write(self, k, v, table, lens, counts=None):
         """Append k, v [B, T, H, d] (bf16 or fp32, or head ranges of a packed projection) after the
         first lens[b] positions of every sequence."""
-        torch = self._torch
-        if k.dtype is not v.dtype or k.dtype not in (torch.bfloat16, torch.float32):
+        code = self._io.get(k.dtype)
+        if code is None or v.dtype is not k.dtype:
             raise ValueError("k, v: expected two bf16 or two fp32 tensors")
-        shape = (*k.shape[:2], *self._heads)
-        s = self.seqs(shape[0], table, lens, counts, shape[1])
-        _check(self._lib.dr_cache_write(self._ref, ctypes.byref(s), _ptr(k), _rows(k, shape, "k"), _ptr(v),
-                                        _rows(v, shape, "v"), _dt(k), self._stream()), "dr_cache_write")
+        B, T = k.shape[:2]
+        shape = (B, T, *self._heads)
+        s = self.seqs(B, table, lens, counts, T)
+        rc = self._write(self._ref, ctypes.byref(s), k.data_ptr(), _rows(k, shape, "k"), v.data_ptr(),
+                         _rows(v, shape, "v"), code, self._stream())
+        if rc:
+            raise DrError(rc, "dr_cache_write")
 
     def read(self, table, lens, counts, T, out="bf16", k=None, v=None):
         """k, v [B, T, H, d]: the values at positions lens[b] .. lens[b] + counts[b] - 1, zeros after."""
-        B, dtype = lens.shape[0], _torch_type(out)
+        dtype, code = self._out[out]
+        B = lens.shape[0]
         s = self.seqs(B, table, lens, counts, T)
         shape = (B, T, *self._heads)
-        k = self._empty(shape, dtype) if k is None else k
-        v = self._empty(shape, dtype) if v is None else v
-        _expect(k, dtype, shape, "k")
-        _expect(v, dtype, shape, "v")
-        _check(self._lib.dr_cache_read(self._ref, ctypes.byref(s), _ptr(k), _ptr(v), _TYPE_CODES[out],
-                                       self._stream()), "dr_cache_read")
+        empty, device = self._torch.empty, self.device
+        k = empty(shape, dtype=dtype, device=device) if k is None else k
+        v = empty(shape, dtype=dtype, device=device) if v is None else v
+        rc = self._read(self._ref, ctypes.byref(s), _address(k, dtype, shape, "k"), _address(v, dtype, shape, "v"),
+                        code, self._stream())
+        if rc:
+            raise DrError(rc, "dr_cache_read")
         return k, v
 
     def status(self) -> int:
@@ -658,19 +672,22 @@ class CacheAttention(_Calls):
         if n == 0:
             raise DrError(DR_ERR_UNSUPPORTED, "dr_cache_attn_workspace_bytes")
         self.ws = self._empty(n, self._torch.uint8)
+        self._ws, self._ws_bytes, self._attn = self.ws.data_ptr(), n, self._lib.dr_cache_attn
 
     def forward(self, q, table, lens, counts=None, o=None, lse=None, want_lse=False):
         """o [B, T, Hq, d] and lse [B, T, Hq] (or None): query t of sequence b is the position
         lens[b] + t, which the cache already holds."""
-        shape, f32 = self._shape, self._torch.float32
+        shape, cache = self._shape, self.cache
         if q.dtype is not self.io_dtype:
             raise ValueError(f"q: expected {self.io_dtype}, got {q.dtype}")
         self.desc.ld_q = _rows(q, shape, "q")
-        s = self.cache.seqs(self.B, table, lens, counts, self.T)
-        o = self._empty(shape, self.out_dtype) if o is None else o
-        lse = self._empty(shape[:3], f32) if lse is None and want_lse else lse
-        _expect(o, self.out_dtype, shape, "o")
-        _expect(lse, f32, shape[:3], "lse")
-        _check(self._lib.dr_cache_attn(self.cache._ref, ctypes.byref(s), self._ref, _ptr(q), _ptr(o), _ptr(lse),
-                                       _ptr(self.ws), self.ws.numel(), self._stream()), "dr_cache_attn")
+        s = cache.seqs(self.B, table, lens, counts, self.T)
+        empty, device = self._torch.empty, self.device
+        o = empty(shape, dtype=self.out_dtype, device=device) if o is None else o
+        lse = empty(shape[:3], dtype=self._f32, device=device) if lse is None and want_lse else lse
+        rc = self._attn(cache._ref, ctypes.byref(s), self._ref, q.data_ptr(),
+                        _address(o, self.out_dtype, shape, "o"), _address(lse, self._f32, shape[:3], "lse"),
+                        self._ws, self._ws_bytes, self._stream())
+        if rc:
+            raise DrError(rc, "dr_cache_attn")
         return o, lse
