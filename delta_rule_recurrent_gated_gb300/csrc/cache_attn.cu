@@ -251,27 +251,36 @@ __device__ __forceinline__ void load_tile(Tile<D, NT, PREC>& t, RawQ<D, NT>& raw
 }
 
 // One step: 32 positions from `first` on, as two halves of 16 with their pages' scales.
-// Positions from `end` on hold no value (edge).  `same`: both halves lie in one page.
-template <int D, int NT, bool E4M3, bool PREC>
+// Positions from `end` on hold no value (EDGE: some are hidden from some row).  `same`: both halves
+// lie in one page.
+template <int D, int NT, bool E4M3, bool PREC, bool EDGE>
 __device__ __forceinline__ void step(Tile<D, NT, PREC>& t, const uint8_t* slot, const AttnParams& p, int first,
-                                     int end, const Meta& m0, const Meta& m1, bool same, bool edge, int lane) {
+                                     int end, const Meta& m0, const Meta& m1, bool same, int lane) {
     const int g = lane >> 2, c = lane & 3;
     float sc[NT][2][4];
+    {
+        uint32_t k0[2][D / 16], k1[2][D / 16];
+        load_keys<D>(k0, slot, lane);
+        load_keys<D>(k1, slot + 16 * D, lane);
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-        uint32_t k[2][D / 16];
-        load_keys<D>(k, slot + hf * 16 * D, lane);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) sc[n][hf][0] = sc[n][hf][1] = sc[n][hf][2] = sc[n][hf][3] = 0.f;
+            for (int i = 0; i < 4; ++i) sc[n][0][i] = sc[n][1][i] = 0.f;
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-            uint32_t a0, a1, a2, a3;
-            codes_to_half<E4M3>(k[0][j], a0, a2);
-            codes_to_half<E4M3>(k[1][j], a1, a3);
+        for (int j = 0; j < D / 16; ++j) {  // the two halves' sums side by side
+            uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+            codes_to_half<E4M3>(k0[0][j], a0, a2);
+            codes_to_half<E4M3>(k0[1][j], a1, a3);
+            codes_to_half<E4M3>(k1[0][j], b0, b2);
+            codes_to_half<E4M3>(k1[1][j], b1, b3);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                mma(sc[n][hf], a0, a1, a2, a3, t.q[n][j][0], t.q[n][j][1]);
-                if constexpr (PREC) mma(sc[n][hf], a0, a1, a2, a3, t.ql[n][j][0], t.ql[n][j][1]);
+                mma(sc[n][0], a0, a1, a2, a3, t.q[n][j][0], t.q[n][j][1]);
+                mma(sc[n][1], b0, b1, b2, b3, t.q[n][j][0], t.q[n][j][1]);
+                if constexpr (PREC) {
+                    mma(sc[n][0], a0, a1, a2, a3, t.ql[n][j][0], t.ql[n][j][1]);
+                    mma(sc[n][1], b0, b1, b2, b3, t.ql[n][j][0], t.ql[n][j][1]);
+                }
             }
         }
     }
@@ -286,7 +295,7 @@ __device__ __forceinline__ void step(Tile<D, NT, PREC>& t, const uint8_t* slot, 
             sc[n][0][2 + j] *= k0;
             sc[n][1][j] *= k1;
             sc[n][1][2 + j] *= k1;
-            if (edge) {
+            if constexpr (EDGE) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {  // positions first + g + 8 i
                     const int back = t.pos[n][j] - (first + g + 8 * i);
@@ -347,7 +356,7 @@ __device__ __forceinline__ void step(Tile<D, NT, PREC>& t, const uint8_t* slot, 
                 w[1][2 * i + j] = e1 * f1;
             }
         }
-        if (edge) {  // a hidden position weighs nothing even where the page's value scale is NaN
+        if constexpr (EDGE) {  // a hidden position weighs nothing even where the page's value scale is NaN
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (sc[n][0][i] == kNegInf) w[0][i] = 0.f;
@@ -370,7 +379,7 @@ __device__ __forceinline__ void step(Tile<D, NT, PREC>& t, const uint8_t* slot, 
     for (int hf = 0; hf < 2; ++hf) {
         uint32_t v[4][D / 32];
         load_values<D>(v, slot + (2 + hf) * 16 * D, lane);
-        if (edge) {
+        if constexpr (EDGE) {
             // what lies in the ring there may be anything: as values it counts as zero
             const bool none = (hf ? m1.id : m0.id) < 0;
 #pragma unroll
@@ -518,8 +527,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 6 : 4) cache_attn
             if (m0.id != -2 || m1.id != -2) {
                 const int first = base + k * kStage;
                 const bool edge = first + kStep > all_hi || first < all_lo || m0.id < 0 || m1.id < 0;
-                step<D, NT, E4M3, PREC>(t, ring + (k % kRing) * 2 * kStep * D, p, first, s.len + s.n, m0, m1, same,
-                                        edge, lane);
+                const uint8_t* slot = ring + (k % kRing) * 2 * kStep * D;
+                if (edge) step<D, NT, E4M3, PREC, true>(t, slot, p, first, s.len + s.n, m0, m1, same, lane);
+                else step<D, NT, E4M3, PREC, false>(t, slot, p, first, s.len + s.n, m0, m1, same, lane);
             }
             if ((k & 15) == 15) {  // entries 2k - 30 .. 2k + 1 are used up
                 __syncwarp();
