@@ -4,6 +4,7 @@
 #include <cuda_fp16.h>
 
 #include "cache_attn.cuh"
+#include "chain.cuh"
 
 namespace dr {
 namespace {
@@ -108,10 +109,6 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int b, int h, int
     st_any(p.o, at * d + ch, p.out, y);
     if (ch == 0 && p.lse) p.lse[at] = (m + log2f(l)) * kLn2;
 }
-
-// Until the first kernel has ended and its writes are there.  Every thread of the second one comes
-// here, so that its end also means the end of the first.
-__device__ __forceinline__ void wait_for_parts() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename K>
 int resident_blocks(K kernel, int threads, int smem) {

@@ -438,7 +438,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 6 : 4) cache_attn
     Meta* metas = reinterpret_cast<Meta*>(smem + rows_or_rings<D, NT>()) + warp * kMetas;
     const bool same = p.c.page > 16;
 
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    chain_wait();
+    chain_release();
     const long long total = line_length<ROWS>(p, lane);
     const int used = blocks_used(total, gridDim.x);
     if ((int)blockIdx.x >= used) return;
@@ -604,6 +605,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_attn_join_kernel(const 
     const int b = blockIdx.x / (p.c.H * max_tiles), rest = blockIdx.x % (p.c.H * max_tiles);
     const int h = rest / max_tiles, tile = rest % max_tiles;
     const int r = blockIdx.y, row = tile * ROWS + r;
+    // The first kernel's blocks released this one after their own wait: what they read may be read.  Its
+    // parts are there after chain_wait(), which every thread comes to, so that the end of this kernel is
+    // also the end of the first.
     const Seq s = make_seq<ROWS>(p, b);
     if (row >= s.n * p.G) {
         int len, n;
@@ -615,7 +619,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_attn_join_kernel(const 
             if (threadIdx.x < D) st_any(p.o, at * D + threadIdx.x, p.out, ok ? 0.f : bad);
             if (threadIdx.x == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
         }
-        wait_for_parts();
+        chain_wait();
+        chain_release();
         return;
     }
     long long total = 0, before = 0;  // the line, and up to this sequence
@@ -633,7 +638,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_attn_join_kernel(const 
     const long long a = before + ((long long)h * s.tiles + tile) * (s.stages + kOver) + kOver;
     const int used = blocks_used(total, blocks);
     const int first = holder(total, a, used), last = holder(total, a + s.stages - 1, used);
-    wait_for_parts();
+    chain_wait();
+    chain_release();
     if (first == last) return;  // finished by its block
     // the tile is the first part of a block with stages of it that begins in it or in its start
     const float* head = p.part + ((size_t)first * 2 + (share(total, first, used) >= a - kOver ? 0 : 1)) * tile_floats(D, ROWS);
@@ -654,7 +660,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_attn_join_kernel(const 
 #pragma unroll
     for (int i = 0; i < kJoinWarps; ++i) { m = fmaxf(m, ms[i]); M = fmaxf(M, Ms[i]); }
     float l = 0.f, sum[V] = {};
-#pragma unroll 4
+#pragma unroll 8
     for (int i = first + warp; i <= last; i += kJoinWarps) {
         const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, ROWS);
         const float pl = in[ROWS * D + r], fl = pow2i(in[ROWS * D + ROWS + r] - m);
@@ -690,21 +696,13 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
     const int blocks = resident < kMaxBlocks ? resident : kMaxBlocks;
     {
         TraceScope ts("cache_attn", st);
-        cache_attn_kernel<D, NT, E4M3, PREC><<<blocks, kThreads, smem, st>>>(p);
-        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+        if (cudaError_t e = launch_chained(cache_attn_kernel<D, NT, E4M3, PREC>, dim3(blocks), kThreads, smem, st, p);
+            e != cudaSuccess)
+            return e;
     }
     const int max_tiles = (p.c.T * p.G + 8 * NT - 1) / (8 * NT);
     TraceScope ts("cache_attn_join", st);
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.c.B * p.c.H * max_tiles, 8 * NT);
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.stream = st;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_attn_join_kernel<D, NT>, p, blocks, max_tiles);
+    return launch_chained(cache_attn_join_kernel<D, NT>, dim3((unsigned)p.c.B * p.c.H * max_tiles, 8 * NT), 32 * kJoinWarps, 0, st, p, blocks, max_tiles);
 }
 
 // Rows of a tile: 16 halve the reads of the cache where a sequence and head have more than 8.  The

@@ -647,7 +647,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     extern __shared__ __align__(1024) uint8_t smem[];
     Control& ct = *reinterpret_cast<Control*>(smem + Smem<D>::control);
     const int warp = threadIdx.x >> 5;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) {
         tmem_alloc(&ct.tmem, 512);
         tmem_relinquish();
@@ -675,6 +674,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
         ct.dead = 0;
         fence_barrier_init();
     }
+    chain_wait();
+    chain_release();
     Walk walk;
     walk.start(p, threadIdx.x & 31);
     tc_fence_before();
@@ -703,6 +704,9 @@ __global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParam
     const int b = blockIdx.x / (p.c.H * max_tiles), other = blockIdx.x % (p.c.H * max_tiles);
     const int h = other / max_tiles, tile = other % max_tiles;
     const int r = blockIdx.y * 32 + lane, row = tile * kRows + r;
+    // The first kernel's blocks released this one after their own wait: what they read may be read.  Its
+    // parts are there after chain_wait(), which every thread comes to, so that the end of this kernel is
+    // also the end of the first.
     int len, n;
     const bool ok = cache_seq(p.c, b, len, n);
     if (!ok) {
@@ -716,7 +720,8 @@ __global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParam
         if (warp == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
     }
     if (tile * kRows + blockIdx.y * 32 >= n * p.G) {
-        wait_for_parts();
+        chain_wait();
+        chain_release();
         return;
     }
     long long total = 0, before = 0;
@@ -742,7 +747,8 @@ __global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParam
     const int stages = make_tile(p, len, n, tile).stages, used = blocks_used(total, blocks);
     const int first = holder(total, a, used), last = holder(total, a + stages - 1, used);
     const float* head = p.part + ((size_t)first * 2 + (share(total, first, used) >= a - kTcOver ? 0 : 1)) * tile_floats(D, kRows);
-    wait_for_parts();
+    chain_wait();
+    chain_release();
     if (first == last || row >= n * p.G) return;  // finished by its block
     float m = kNegInf, M = kNegInf, l = 0.f;
     float4 sum[V];
@@ -792,21 +798,13 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
     const int blocks = kMaxTcBlocks;
     {
         TraceScope ts("cache_attn_tc", st);
-        cache_attn_tc_kernel<D, E4M3><<<blocks, kTcThreads, smem, st>>>(p);
-        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+        if (cudaError_t e = launch_chained(cache_attn_tc_kernel<D, E4M3>, dim3(blocks), kTcThreads, smem, st, p);
+            e != cudaSuccess)
+            return e;
     }
     const int max_tiles = (p.c.T * p.G + kRows - 1) / kRows;
     TraceScope ts("cache_attn_tc_join", st);
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.c.B * p.c.H * max_tiles, kRows / 32);
-    cfg.blockDim = dim3(256);
-    cfg.stream = st;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_attn_tc_join_kernel<D>, p, blocks, max_tiles);
+    return launch_chained(cache_attn_tc_join_kernel<D>, dim3((unsigned)p.c.B * p.c.H * max_tiles, kRows / 32), 256, 0, st, p, blocks, max_tiles);
 }
 
 }  // namespace

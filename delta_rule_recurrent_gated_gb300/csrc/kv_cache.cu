@@ -9,6 +9,7 @@
 
 #include <cuda_fp8.h>
 
+#include "chain.cuh"
 #include "kv_cache.cuh"
 #include "trace.cuh"
 
@@ -107,6 +108,8 @@ __global__ void __launch_bounds__(THREADS, write_blocks(THREADS, NV * (int)sizeo
     cache_write_kernel(const CacheParams c, const IN* __restrict__ k, long long ld_k,
                        const IN* __restrict__ v, long long ld_v, int pages_per_seq) {
     __shared__ uint32_t red[THREADS / 32];
+    chain_wait();
+    chain_release();
     const int b = blockIdx.x / pages_per_seq, i = blockIdx.x % pages_per_seq, h = blockIdx.y;
     const bool keys = blockIdx.z == 0;
     int len, n;
@@ -197,6 +200,8 @@ __global__ void __launch_bounds__(THREADS, write_blocks(THREADS, NV * (int)sizeo
 template <typename OUT, bool E4M3, int THREADS, int NV>
 __global__ void __launch_bounds__(THREADS)
     cache_read_kernel(const CacheParams c, OUT* __restrict__ k, OUT* __restrict__ v, int pages_per_seq) {
+    chain_wait();
+    chain_release();
     const int b = blockIdx.x / pages_per_seq, i = blockIdx.x % pages_per_seq, h = blockIdx.y;
     const bool keys = blockIdx.z == 0;
     OUT* out = keys ? k : v;
@@ -255,17 +260,15 @@ cudaError_t write_page(const CacheParams& c, const void* k, long long ld_k, cons
                        cudaStream_t st) {
     const int pages = pages_of(c);
     TraceScope ts("cache_write", st);
-    cache_write_kernel<IN, E4M3, THREADS, NV><<<dim3((unsigned)c.B * pages, c.H, 2), THREADS, 0, st>>>(
-        c, static_cast<const IN*>(k), ld_k, static_cast<const IN*>(v), ld_v, pages);
-    return cudaGetLastError();
+    return launch_chained(cache_write_kernel<IN, E4M3, THREADS, NV>, dim3((unsigned)c.B * pages, c.H, 2), THREADS, 0, st,
+                          c, static_cast<const IN*>(k), ld_k, static_cast<const IN*>(v), ld_v, pages);
 }
 template <typename OUT, bool E4M3, int THREADS, int NV>
 cudaError_t read_page(const CacheParams& c, void* k, void* v, cudaStream_t st) {
     const int pages = pages_of(c);
     TraceScope ts("cache_read", st);
-    cache_read_kernel<OUT, E4M3, THREADS, NV><<<dim3((unsigned)c.B * pages, c.H, 2), THREADS, 0, st>>>(
-        c, static_cast<OUT*>(k), static_cast<OUT*>(v), pages);
-    return cudaGetLastError();
+    return launch_chained(cache_read_kernel<OUT, E4M3, THREADS, NV>, dim3((unsigned)c.B * pages, c.H, 2), THREADS, 0, st,
+                          c, static_cast<OUT*>(k), static_cast<OUT*>(v), pages);
 }
 
 // f(threads, pieces of each) for the page's size, as compile-time values

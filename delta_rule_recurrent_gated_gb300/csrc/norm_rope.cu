@@ -13,6 +13,7 @@
 // pairs, so nothing but the sums of a row passes between threads.  Products and sums run on
 // pairs of fp32 values (fma.rn.f32x2).  Both kernels are bound by HBM at the sizes of training:
 // each value is read and written once.
+#include "chain.cuh"
 #include "common.cuh"
 #include "f32x2.cuh"
 #include "rope.cuh"
@@ -174,6 +175,8 @@ __device__ __forceinline__ void load_heads(Vec8<T> (&v)[U], const T* row, const 
 template <typename IN, typename OUT, int LANES>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(IN) == 2 ? 4 : 3) norm_rope_fwd_kernel(const RopeParams p) {
     constexpr int kGroups = kRopeThreads / LANES, U = 4;
+    chain_wait();
+    chain_release();
     const Lane a = make_lane<LANES>(p);
     const Run run = make_run(p);
     const bool pairs = p.style == DR_ROPE_PAIRS;
@@ -222,7 +225,8 @@ template <typename IN, typename OUT, int LANES>
 __global__ void __launch_bounds__(kRopeThreads, kBwdResident) norm_rope_bwd_kernel(const RopeParams p) {
     constexpr int kGroups = kRopeThreads / LANES, U = sizeof(IN) == 2 ? kRun : kRun / 2;
     __shared__ float sums[kGroups][LANES * 8 + 1];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    chain_wait();
+    chain_release();
     const Lane a = make_lane<LANES>(p);
     const Run run = make_run(p);
     const bool pairs = p.style == DR_ROPE_PAIRS;
@@ -307,9 +311,8 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_dw_kernel(const RopePa
     __shared__ float sums[32][9];
     const bool is_q = blockIdx.y == 0;
     float* dw = is_q ? p.dwq : p.dwk;
-    // launched early: until the parts are there (all threads wait, so that the end of this kernel is
-    // also the end of the one before)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    chain_wait();  // until the parts are there
+    chain_release();
     if (!dw) return;
     const int c = threadIdx.x & 7, j = threadIdx.x >> 3, ch = blockIdx.x * 8 + c;
     const long long lo = is_q ? 0 : (long long)p.nq * blocks;
@@ -353,27 +356,19 @@ cudaError_t launch(const RopeParams& p, bool bwd, cudaStream_t st) {
         const long long tiles = (p.tokens + kGroups - 1) / kGroups;
         const dim3 grid((unsigned)(tiles < 0x7fffffff ? tiles : 0x7fffffff), p.nq + p.nk);
         TraceScope ts("norm_rope_fwd", st);
-        norm_rope_fwd_kernel<IN, OUT, LANES><<<grid, kRopeThreads, 0, st>>>(p);
-        return cudaGetLastError();
+        return launch_chained(norm_rope_fwd_kernel<IN, OUT, LANES>, grid, kRopeThreads, 0, st, p);
     }
     const int blocks = bwd_blocks(p, LANES);
     {
         TraceScope ts("norm_rope_bwd", st);
-        norm_rope_bwd_kernel<IN, OUT, LANES><<<dim3(blocks, p.nq + p.nk), kRopeThreads, 0, st>>>(p);
-        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+        if (cudaError_t e = launch_chained(norm_rope_bwd_kernel<IN, OUT, LANES>, dim3(blocks, p.nq + p.nk), kRopeThreads,
+                                           0, st, p);
+            e != cudaSuccess)
+            return e;
     }
     if (!p.dwq && !p.dwk) return cudaSuccess;
     TraceScope ts("norm_rope_dw", st);
-    cudaLaunchAttribute early;
-    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    early.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.d / 8, 2);
-    cfg.blockDim = dim3(kRopeThreads);
-    cfg.stream = st;
-    cfg.attrs = &early;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, norm_rope_dw_kernel, p, blocks);
+    return launch_chained(norm_rope_dw_kernel, dim3(p.d / 8, 2), kRopeThreads, 0, st, p, blocks);
 }
 
 template <typename IN, typename OUT>
