@@ -593,18 +593,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 6 : 4) cache_attn
     }
 }
 
-// Joins the parts of a tile that several blocks worked on.  Block x: the tile, y: its row.  Rows of
-// no query get zeros (behind a sequence's tokens) or NaN (a sequence out of range).
+// Joins the parts of a tile that several blocks worked on.  Block x: the tile.  A row is a block's
+// (DEEP: many parts; y: the row) or a warp's (y: 8 rows).  Rows of no query get zeros (behind a
+// sequence's tokens) or NaN (a sequence out of range).
 constexpr int kJoinWarps = 8;
-template <int D, int NT>
+template <int D, int NT, bool DEEP>
 __global__ void __launch_bounds__(32 * kJoinWarps) cache_attn_join_kernel(const AttnParams p, int blocks,
                                                                           int max_tiles) {
     constexpr int ROWS = 8 * NT, V = D / 32;
-    __shared__ float sums[kJoinWarps][D], ls[kJoinWarps], ms[kJoinWarps], Ms[kJoinWarps];
+    __shared__ float sums[DEEP ? kJoinWarps : 1][D], ls[kJoinWarps], ms[kJoinWarps], Ms[kJoinWarps];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int b = blockIdx.x / (p.c.H * max_tiles), rest = blockIdx.x % (p.c.H * max_tiles);
     const int h = rest / max_tiles, tile = rest % max_tiles;
-    const int r = blockIdx.y, row = tile * ROWS + r;
+    const int r = DEEP ? blockIdx.y : blockIdx.y * kJoinWarps + warp, row = tile * ROWS + r;
     // The first kernel's blocks released this one after their own wait: what they read may be read.  Its
     // parts are there after chain_wait(), which every thread comes to, so that the end of this kernel is
     // also the end of the first.
@@ -612,12 +613,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_attn_join_kernel(const 
     if (row >= s.n * p.G) {
         int len, n;
         const bool ok = cache_seq(p.c, b, len, n);
-        if (!ok && threadIdx.x == 0) flag_index_error(p.c);
+        if (!ok && lane == 0) flag_index_error(p.c);
         if (row < p.c.T * p.G) {
             const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
             const float bad = __uint_as_float(0x7fc00000u);
-            if (threadIdx.x < D) st_any(p.o, at * D + threadIdx.x, p.out, ok ? 0.f : bad);
-            if (threadIdx.x == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
+            for (int ch = DEEP ? threadIdx.x : lane; ch < D; ch += DEEP ? 32 * kJoinWarps : 32)
+                st_any(p.o, at * D + ch, p.out, ok ? 0.f : bad);
+            if (lane == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
         }
         chain_wait();
         chain_release();
@@ -638,49 +640,65 @@ __global__ void __launch_bounds__(32 * kJoinWarps) cache_attn_join_kernel(const 
     const long long a = before + ((long long)h * s.tiles + tile) * (s.stages + kOver) + kOver;
     const int used = blocks_used(total, blocks);
     const int first = holder(total, a, used), last = holder(total, a + s.stages - 1, used);
+    // the tile is the first part of a block with stages of it that begins in it or in its start
+    const float* head = p.part + ((size_t)first * 2 + (share(total, first, used) >= a - kOver ? 0 : 1)) * tile_floats(D, ROWS);
     chain_wait();
     chain_release();
     if (first == last) return;  // finished by its block
-    // the tile is the first part of a block with stages of it that begins in it or in its start
-    const float* head = p.part + ((size_t)first * 2 + (share(total, first, used) >= a - kOver ? 0 : 1)) * tile_floats(D, ROWS);
-    // warp w takes parts w, w + 8, ..: the references first, then the sums in the order of the parts
-    float m = kNegInf, M = kNegInf;
-    for (int i = first + threadIdx.x; i <= last; i += 32 * kJoinWarps) {
-        const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, ROWS);
-        m = fmaxf(m, in[ROWS * D + ROWS + r]);
-        M = fmaxf(M, in[ROWS * D + 2 * ROWS + r]);
-    }
+    // A warp takes parts i0, i0 + step, .., kAtOnce of them in flight.  A part without weight adds nothing,
+    // one that met a NaN hands it on.
+    constexpr int kAtOnce = DEEP ? 8 : 4, step = DEEP ? kJoinWarps : 1;
+    float m = kNegInf, M = kNegInf, l = 0.f, sum[V] = {};
+    for (int i0 = first + (DEEP ? warp : 0); i0 <= last; i0 += kAtOnce * step) {
+        float pl[kAtOnce], pm[kAtOnce], pM[kAtOnce], x[kAtOnce][V];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    }
-    if (lane == 0) { ms[warp] = m; Ms[warp] = M; }
-    __syncthreads();
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int i = i0 + k * step;
+            const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, ROWS);
+            const bool on = i <= last;
+            pl[k] = on ? in[ROWS * D + r] : 0.f;
+            pm[k] = on ? in[ROWS * D + ROWS + r] : kNegInf;
+            pM[k] = on ? in[ROWS * D + 2 * ROWS + r] : kNegInf;
 #pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) { m = fmaxf(m, ms[i]); M = fmaxf(M, Ms[i]); }
-    float l = 0.f, sum[V] = {};
-#pragma unroll 8
-    for (int i = first + warp; i <= last; i += kJoinWarps) {
-        const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, ROWS);
-        const float pl = in[ROWS * D + r], fl = pow2i(in[ROWS * D + ROWS + r] - m);
-        const float fs = pow2i(in[ROWS * D + 2 * ROWS + r] - M);
-        l += pl == pl ? pl * fl : pl;
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float x = in[(size_t)r * D + 32 * j + lane];
-            sum[j] += x == x ? x * fs : x;
+            for (int j = 0; j < V; ++j) x[k][j] = on ? in[(size_t)r * D + 32 * j + lane] : 0.f;
         }
+        float m2 = m, M2 = M;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) { m2 = fmaxf(m2, pm[k]); M2 = fmaxf(M2, pM[k]); }
+        l = l == l ? l * pow2i(m - m2) : l;
+        const float fs = pow2i(M - M2);
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum[j] = sum[j] == sum[j] ? sum[j] * fs : sum[j];
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (i0 + k * step > last) break;  // uniform
+            const float f = pow2i(pM[k] - M2);
+            l += pl[k] == pl[k] ? pl[k] * pow2i(pm[k] - m2) : pl[k];
+#pragma unroll
+            for (int j = 0; j < V; ++j) sum[j] += x[k][j] == x[k][j] ? x[k][j] * f : x[k][j];
+        }
+        m = m2;
+        M = M2;
     }
+    if constexpr (!DEEP) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) sums[warp][32 * j + lane] = sum[j];
-    if (lane == 0) ls[warp] = l;
-    __syncthreads();
-    if (threadIdx.x < D) {
-        float x = 0.f, tot = 0.f;
+        for (int j = 0; j < V; ++j) write_row(p, b, h, row, 32 * j + lane, D, sum[j], l, m, M);
+    } else {
 #pragma unroll
-        for (int i = 0; i < kJoinWarps; ++i) { x += sums[i][threadIdx.x]; tot += ls[i]; }
-        write_row(p, b, h, row, threadIdx.x, D, x, tot, m, M);
+        for (int j = 0; j < V; ++j) sums[warp][32 * j + lane] = sum[j];
+        if (lane == 0) { ls[warp] = l; ms[warp] = m; Ms[warp] = M; }
+        __syncthreads();
+        if (threadIdx.x >= D) return;
+        float x = 0.f, tot = 0.f, mm = kNegInf, MM = kNegInf;
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) { mm = fmaxf(mm, ms[i]); MM = fmaxf(MM, Ms[i]); }
+#pragma unroll
+        for (int i = 0; i < kJoinWarps; ++i) {
+            const float y = sums[i][threadIdx.x];
+            x += y == y ? y * pow2i(Ms[i] - MM) : y;
+            tot += ls[i] == ls[i] ? ls[i] * pow2i(ms[i] - mm) : ls[i];
+        }
+        write_row(p, b, h, row, threadIdx.x, D, x, tot, mm, MM);
     }
 }
 
@@ -702,7 +720,14 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
     }
     const int max_tiles = (p.c.T * p.G + 8 * NT - 1) / (8 * NT);
     TraceScope ts("cache_attn_join", st);
-    return launch_chained(cache_attn_join_kernel<D, NT>, dim3((unsigned)p.c.B * p.c.H * max_tiles, 8 * NT), 32 * kJoinWarps, 0, st, p, blocks, max_tiles);
+    // a block for each row where a tile has 8 parts or more on average: 114 parts take 5 us (a warp: 12 us);
+    // a warp where it has fewer: 1024 rows of one or two parts take 7 us (a block: 11 us)
+    const unsigned tiles = (unsigned)p.c.B * p.c.H * max_tiles;
+    const int rows = max_tiles > 1 ? 8 * NT : p.c.T * p.G;
+    return tiles * 8 <= (unsigned)blocks
+               ? launch_chained(cache_attn_join_kernel<D, NT, true>, dim3(tiles, rows), 32 * kJoinWarps, 0, st, p, blocks, max_tiles)
+               : launch_chained(cache_attn_join_kernel<D, NT, false>, dim3(tiles, (rows + kJoinWarps - 1) / kJoinWarps),
+                                32 * kJoinWarps, 0, st, p, blocks, max_tiles);
 }
 
 // Rows of a tile: 16 halve the reads of the cache where a sequence and head have more than 8.  The

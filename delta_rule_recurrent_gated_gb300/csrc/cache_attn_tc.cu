@@ -184,6 +184,10 @@ template <int D> struct Smem {
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
+// Bytes that the phase waits for, beside its arrivals.
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
 // Once for a whole warp, after what its lanes did.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar) {
     __syncwarp();
@@ -271,14 +275,6 @@ __device__ __forceinline__ void copy_pages(const AttnParams& p, uint8_t* smem, C
             const uint32_t buf = n % kRaw, parity = (n / kRaw) & 1;
             ok = wait(ct, &ct.rempty[buf], parity ^ 1);
             if (!ok) break;
-            if ((lane >> 2) == (i & 7)) {
-                StageMeta& m = ct.meta[n % kMetas];
-                m.ks[g] = now.ks;
-                m.vs[g] = now.vs;
-                m.lv[g] = now.vs == now.vs ? log2f(now.vs) : 0.f;
-                m.id[g] = now.id;
-                if (now.id == -1) flag_index_error(p.c);
-            }
             // copy c takes the page of its first part that is seen
             int id = __shfl_sync(0xffffffffu, now.id, 4 * (i & 7) + g);
             if (rows > 16) id = max(id, __shfl_xor_sync(0xffffffffu, id, 1));
@@ -287,8 +283,7 @@ __device__ __forceinline__ void copy_pages(const AttnParams& p, uint8_t* smem, C
             id = __shfl_sync(0xffffffffu, id, min(c * (rows / 16), 3));
             const bool mine = c < copies && id >= 0;
             const int total = __popc(__ballot_sync(0xffffffffu, mine)) * 2 * rows * D;
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&ct.rfull[buf], total);
+            if (lane == 0) mbar_expect_tx(&ct.rfull[buf], total);
             __syncwarp();
             if (mine) {
                 const int first = base + i * kStage + c * rows;
@@ -297,6 +292,16 @@ __device__ __forceinline__ void copy_pages(const AttnParams& p, uint8_t* smem, C
                 bulk_g2s(to, p.c.k + off, rows * D, &ct.rfull[buf]);
                 bulk_g2s(to + Smem<D>::codes, p.c.v + off, rows * D, &ct.rfull[buf]);
             }
+            // the copies are on their way: now the scales
+            if ((lane >> 2) == (i & 7)) {
+                StageMeta& m = ct.meta[n % kMetas];
+                m.ks[g] = now.ks;
+                m.vs[g] = now.vs;
+                m.lv[g] = now.vs == now.vs ? log2f(now.vs) : 0.f;
+                m.id[g] = now.id;
+                if (now.id == -1) flag_index_error(p.c);
+            }
+            warp_arrive(&ct.rfull[buf]);
         }
     }
     // no copy outlives the block, whatever became of the other warps
@@ -434,9 +439,8 @@ __device__ __forceinline__ void drain(Control& ct, uint64_t* bar) {
 // ------------------------------------------------------------------ warps 0-7: a row per thread
 template <int D, bool E4M3>
 __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
-    const int hf = threadIdx.x / kHalf, r = threadIdx.x % kHalf;
+    const int hf = threadIdx.x / kHalf, r = threadIdx.x % kHalf, lane = threadIdx.x & 31;
     const uint32_t tm = warp_lane_base(ct.tmem), to = tm + o_col(hf);
-    uint8_t* qrow = smem + Smem<D>::q + hf * Smem<D>::qtile + r * 128;
     uint32_t n = 0;  // stages so far
     Stretch s;
     while (walk.next(p, s)) {
@@ -444,33 +448,50 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
         const bool on = row < s.n * p.G;
         const bool some = s.t.row0 + hf * kHalf < s.n * p.G;  // the half has rows
         const int tok = on ? row / p.G : 0, head = s.h * p.G + (on ? row % p.G : 0), pos = on ? s.len + tok : -1;
-        // the row's queries, scaled, as operand (with the sign of the scale, so that factors are positive)
-        const uint4* qp = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                         ((long long)s.b * p.c.T + tok) * p.ld_q + (long long)head * D);
-        uint4 raw[D / 8];
+        // The warp's queries as operand: whole rows at a time, 16 bytes a lane, each row scaled (with the sign
+        // of the softmax scale, so that the factors of S are positive).
+        const long long at0 = on ? ((long long)s.b * p.c.T + tok) * p.ld_q + (long long)head * D : -1;
+        int e = 0;
+        {
+            constexpr int L = D / 8, R = 32 / L;  // lanes of a row, rows at a time
+            const int lr = lane / L, chunk = lane % L;
+            uint4 raw[L];
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) raw[j] = on ? __ldg(qp + j) : make_uint4(0, 0, 0, 0);
-        float top = 0.f;
+            for (int i = 0; i < L; ++i) {
+                const long long from = __shfl_sync(0xffffffffu, at0, R * i + lr);
+                raw[i] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + from) + chunk)
+                                   : make_uint4(0, 0, 0, 0);
+            }
+            float mine = 0.f;  // the largest magnitude of this lane's own row
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-            float x[8];
-            unpack8(raw[j], x);
+            for (int i = 0; i < L; ++i) {
+                float x[8], top = 0.f;
+                unpack8(raw[i], x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
-        }
-        int e;
-        float up, rest;
-        query_scale(top, e, up, rest);
-        if (p.scale < 0.f) up = -up;
+                for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(x[q]));
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-            float x[8];
-            unpack8(raw[j], x);
+                for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                top = __shfl_sync(0xffffffffu, top, (lane % R) * L);
+                if (lane / R == i) mine = top;
+            }
+            float up, rest;
+            query_scale(mine, e, up, rest);
+            e = max(e, -126);  // one factor is enough for bf16
+            const float f = p.scale < 0.f ? -pow2i(-(float)e) : pow2i(-(float)e);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) x[q] = x[q] * up * rest;
-            constexpr int a = E4M3 ? 1 : 2, b = 3 - a;  // the order of convert16
-            *reinterpret_cast<uint4*>(qrow + (j >> 3) * kHalf * 128 + (((j & 7) ^ (r & 7)) << 4)) =
-                make_uint4(pack_half(x[0], x[a]), pack_half(x[b], x[3]), pack_half(x[4], x[4 + a]), pack_half(x[4 + b], x[7]));
+            for (int i = 0; i < L; ++i) {
+                float x[8];
+                const float fi = __shfl_sync(0xffffffffu, f, R * i + lr);
+                unpack8(raw[i], x);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) x[q] *= fi;
+                constexpr int a = E4M3 ? 1 : 2, b = 3 - a;  // the order of convert16
+                const int rr = (threadIdx.x & 96) + R * i + lr;
+                *reinterpret_cast<uint4*>(smem + Smem<D>::q + hf * Smem<D>::qtile + (chunk >> 3) * kHalf * 128 + rr * 128 +
+                                          (((chunk & 7) ^ (rr & 7)) << 4)) =
+                    make_uint4(pack_half(x[0], x[a]), pack_half(x[b], x[3]), pack_half(x[4], x[4 + a]),
+                               pack_half(x[4 + b], x[7]));
+            }
         }
         fence_async_smem();
         warp_arrive(&ct.qfull);
