@@ -10,6 +10,7 @@
 #include <cuda_fp8.h>
 
 #include "chain.cuh"
+#include "f32x2.cuh"
 #include "kv_cache.cuh"
 #include "trace.cuh"
 
@@ -19,16 +20,19 @@ namespace {
 template <bool E4M3> __device__ __forceinline__ float inv_code_max() {
     return E4M3 ? 1.f / 448.f : 1.f / 127.f;
 }
-// The nearest codes of four values, ties to even, the first in the lowest byte.
-template <bool E4M3> __device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d) {
+// The nearest codes of four values of magnitude below 128 (448), ties to even, the first in the lowest byte.
+template <bool E4M3> __device__ __forceinline__ uint32_t to_codes(float2 a, float2 b) {
     if (E4M3) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
         return lo | hi << 16;
     }
     // 1.5 * 2^23 + x has spacing 1: rounded to nearest even, its low byte is the whole number
-    auto whole = [](float x) { return __float_as_uint(fminf(fmaxf(x, -127.f), 127.f) + 12582912.f); };
-    return __byte_perm(__byte_perm(whole(a), whole(b), 0x0040), __byte_perm(whole(c), whole(d), 0x0040), 0x5410);
+    const float2 big = make_float2(12582912.f, 12582912.f);
+    a = add2(a, big);
+    b = add2(b, big);
+    return __byte_perm(__byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040),
+                       __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040), 0x5410);
 }
 template <bool E4M3> __device__ __forceinline__ float from_code(uint32_t byte) {
     if (E4M3) {
@@ -53,21 +57,41 @@ __device__ __forceinline__ void store8(float* p, const float (&y)[8]) {
     reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
 }
 
-// x / s, correctly rounded, for many x and one s: with y the correctly rounded 1 / s and q within a
-// unit of the quotient, q + (x - q s) y is the rounded quotient (P. Markstein, IBM J. Res. Dev. 34,
-// 1990); a first such step brings x y to within a unit.  A remainder that underflows belongs to a
-// quotient below 2^-20, whose code is zero whatever its last bits are; scales outside
-// 1e-18 .. 1e18 take the division itself.  A zero keeps its sign.
-struct Divisor {
+// Codes of x / s for many x and one s.  The quotient is correctly rounded: with y the correctly
+// rounded 1 / s and q within a unit of the quotient, q + (x - q s) y is the rounded quotient
+// (P. Markstein, IBM J. Res. Dev. 34, 1990); a first such step brings x y to within a unit.  A
+// remainder that underflows belongs to a quotient below 2^-20, whose code is zero whatever its last
+// bits are; a zero keeps the sign of x.  Scales outside 1e-18 .. 1e18 take the division itself, and
+// the bound on the magnitude that a scale among the smallest numbers does not keep.
+template <bool E4M3> struct Coder {
     float s, y;
-    bool plain;
-    __device__ __forceinline__ explicit Divisor(float d) : s(d), y(1.f / d), plain(!(d > 1e-18f && d < 1e18f)) {}
-    __device__ __forceinline__ float operator()(float x) const {
-        if (plain) return x / s;
-        float q = x * y;
-        if (q == 0.f) return q;
-        q = fmaf(fmaf(-q, s, x), y, q);
-        return fmaf(fmaf(-q, s, x), y, q);
+    __device__ __forceinline__ explicit Coder(float d) : s(d), y(1.f / d) {}
+    __device__ __forceinline__ bool plain() const { return !(s > 1e-18f && s < 1e18f); }
+    __device__ __forceinline__ float2 fast(float2 x) const {
+        const float2 y2 = make_float2(y, y), s2 = make_float2(-s, -s);
+        float2 q = mul2(x, y2);
+        q = fma2(fma2(q, s2, x), y2, q);
+        q = fma2(fma2(q, s2, x), y2, q);
+        if (E4M3) {
+            q.x = __uint_as_float((__float_as_uint(q.x) & 0x7fffffffu) | (__float_as_uint(x.x) & 0x80000000u));
+            q.y = __uint_as_float((__float_as_uint(q.y) & 0x7fffffffu) | (__float_as_uint(x.y) & 0x80000000u));
+        }
+        return q;
+    }
+    __device__ __forceinline__ float slow(float x) const {
+        constexpr float top = E4M3 ? 448.f : 127.f;
+        return fminf(fmaxf(x / s, -top), top);
+    }
+    __device__ __forceinline__ uint2 operator()(const float (&x)[8]) const {
+        float2 q[4];
+        if (plain()) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[j] = make_float2(slow(x[2 * j]), slow(x[2 * j + 1]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[j] = fast(make_float2(x[2 * j], x[2 * j + 1]));
+        }
+        return make_uint2(to_codes<E4M3>(q[0], q[1]), to_codes<E4M3>(q[2], q[3]));
     }
 };
 
@@ -75,6 +99,12 @@ template <typename T> struct Vec8;  // 8 values as loaded
 template <> struct Vec8<__nv_bfloat16> {
     uint4 u;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
+    // the larger of `top` and the magnitudes, as bits of fp32 (which order as the magnitudes do)
+    __device__ __forceinline__ uint32_t magnitude(uint32_t top) const {
+        const uint32_t a = __vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu);
+        const uint32_t b = __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu), c = __vmaxu2(a, b);
+        return max(top, max(c & 0xffff0000u, c << 16));
+    }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -89,6 +119,12 @@ template <> struct Vec8<float> {
     __device__ __forceinline__ void load(const float* p) {
         a = reinterpret_cast<const float4*>(p)[0];
         b = reinterpret_cast<const float4*>(p)[1];
+    }
+    __device__ __forceinline__ uint32_t magnitude(uint32_t top) const {
+        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
+        return top;
     }
     __device__ __forceinline__ void get(float (&x)[8]) const {
         x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
@@ -148,12 +184,7 @@ __global__ void __launch_bounds__(THREADS, write_blocks(THREADS, NV * (int)sizeo
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
         const int j = e * THREADS + threadIdx.x;
-        if (j >= from && j < to) {
-            float y[8];
-            x[e].get(y);
-#pragma unroll
-            for (int m = 0; m < 8; ++m) top = max(top, __float_as_uint(y[m]) & 0x7fffffffu);
-        }
+        if (j >= from && j < to) top = x[e].magnitude(top);
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
@@ -165,21 +196,14 @@ __global__ void __launch_bounds__(THREADS, write_blocks(THREADS, NV * (int)sizeo
                            : __uint_as_float(0x7fc00000u);
     if (threadIdx.x == 0) *scale = s;
 
-    const Divisor over(s);
+    const Coder<E4M3> code(s);
 #pragma unroll
     for (int e = 0; e < NV; ++e) {
         const int j = e * THREADS + threadIdx.x;
         if (j >= from && j < to) {
             float y[8];
             x[e].get(y);
-            uint32_t w[2] = {0, 0};
-            if (s > 0.f) {
-#pragma unroll
-                for (int m = 0; m < 8; ++m) y[m] = over(y[m]);
-                w[0] = to_codes<E4M3>(y[0], y[1], y[2], y[3]);
-                w[1] = to_codes<E4M3>(y[4], y[5], y[6], y[7]);
-            }
-            *reinterpret_cast<uint2*>(codes + (size_t)j * 8) = make_uint2(w[0], w[1]);
+            *reinterpret_cast<uint2*>(codes + (size_t)j * 8) = s > 0.f ? code(y) : make_uint2(0, 0);
         }
     }
     if (s > s_old && s_old > 0.f) {  // false for NaN
@@ -189,9 +213,8 @@ __global__ void __launch_bounds__(THREADS, write_blocks(THREADS, NV * (int)sizeo
             float y[8];
 #pragma unroll
             for (int m = 0; m < 8; ++m)
-                y[m] = over(__fmul_rn(from_code<E4M3>((in[m >> 2] >> (8 * (m & 3))) & 0xffu), s_old));
-            *reinterpret_cast<uint2*>(codes + (size_t)j * 8) =
-                make_uint2(to_codes<E4M3>(y[0], y[1], y[2], y[3]), to_codes<E4M3>(y[4], y[5], y[6], y[7]));
+                y[m] = __fmul_rn(from_code<E4M3>((in[m >> 2] >> (8 * (m & 3))) & 0xffu), s_old);
+            *reinterpret_cast<uint2*>(codes + (size_t)j * 8) = code(y);
         }
     }
 }
