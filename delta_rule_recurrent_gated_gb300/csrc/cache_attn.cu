@@ -3,7 +3,7 @@
 //
 // The rows of a sequence and cache head are its query tokens times the G query heads that share
 // the cache head, row = t * G + g.  A block works on a tile of 8 NT rows of one (sequence, cache
-// head) over a stretch of its positions, in stages of 64; warp w takes positions 32 w .. 32 w + 31
+// head) over a stretch of its positions, in stages of 128; warp w takes positions 32 w .. 32 w + 31
 // of each stage on its own, through a ring in shared memory that it fills with asynchronous copies
 // a stage ahead, so that warps never wait for one another before the rows are joined.
 //
@@ -30,7 +30,7 @@
 namespace dr {
 namespace {
 
-constexpr int kWarps = 2, kThreads = 32 * kWarps;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStep = 32, kStage = kStep * kWarps;  // positions of a warp's step, of a stage
 constexpr int kOver = 4;  // what a tile costs beside its stages, in stages
 
@@ -428,7 +428,7 @@ template <int D, int NT> __host__ __device__ constexpr int smem_bytes() {
 }
 
 template <int D, int NT, bool E4M3, bool PREC>
-__global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 6 : 4) cache_attn_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 3 : 2) cache_attn_kernel(const AttnParams p) {
     constexpr int ROWS = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem[];
     Joined<D, NT>& joined = *reinterpret_cast<Joined<D, NT>*>(smem);
@@ -474,24 +474,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 6 : 4) cache_attn
         // Step k = 0 .. n - 1 of the stretch is its stage from + k; the meta of its halves are entries 2k
         // and 2k + 1 modulo kMetas.  A batch of 32 entries is written while the one before is in use.
         const int n = upto - from, base = (s.s0 + from) * kStage + kStep * warp;
-        auto fill_metas = [&](int entry) {
+        auto page_of = [&](int entry) {
+            const int first = base + (entry >> 1) * kStage + (entry & 1) * 16;
+            const bool seen = entry < 2 * n && first < hi && first + 16 > lo;
+            return seen ? cache_page(p.c, b, first / p.c.page) : -2;
+        };
+        auto note = [&](int entry, int id) {
             Meta x;
-            x.id = -2;
+            x.id = id;
             x.ks = x.vs = 0.f;
             x.ve = kNegInf;
-            const int first = base + (entry >> 1) * kStage + (entry & 1) * 16;
-            if (entry < 2 * n && first < hi && first + 16 > lo) {
-                x.id = cache_page(p.c, b, first / p.c.page);
-                if (x.id >= 0) {
-                    const size_t ph = (size_t)x.id * p.c.H + h;
-                    x.ks = p.c.k_scale[ph];
-                    x.vs = p.c.v_scale[ph];
-                    x.ve = scale_exponent(x.vs);
-                } else {
-                    flag_index_error(p.c);
-                    x.ks = x.vs = __uint_as_float(0x7fc00000u);
-                    x.ve = 0.f;
-                }
+            if (id >= 0) {
+                const size_t ph = (size_t)id * p.c.H + h;
+                x.ks = p.c.k_scale[ph];
+                x.vs = p.c.v_scale[ph];
+                x.ve = scale_exponent(x.vs);
+            } else if (id == -1) {
+                flag_index_error(p.c);
+                x.ks = x.vs = __uint_as_float(0x7fc00000u);
+                x.ve = 0.f;
             }
             metas[entry & (kMetas - 1)] = x;
         };
@@ -512,11 +513,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 6 : 4) cache_attn
         };
         RawQ<D, NT> raw;
         fetch_q<D, NT>(raw, p, b, h, row0, s, lane);
-        fill_metas(lane);
+        // the first pages are on their way before their scales are asked for
+        const int id0 = page_of(lane), id1 = page_of(32 + lane);
+        metas[lane].id = id0;
         __syncwarp();
 #pragma unroll
         for (int k = 0; k < kRing - 1; ++k) fetch(k);
-        fill_metas(32 + lane);
+        __syncwarp();
+        note(lane, id0);
+        note(32 + lane, id1);
         Tile<D, NT, PREC> t;
         load_tile<D, NT, E4M3, PREC>(t, raw, p, b, h, row0, s, lane);
         for (int k = 0; k < n; ++k) {
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && !PREC ? 6 : 4) cache_attn
             }
             if ((k & 15) == 15) {  // entries 2k - 30 .. 2k + 1 are used up
                 __syncwarp();
-                fill_metas(2 * k + 34 + lane);
+                note(2 * k + 34 + lane, page_of(2 * k + 34 + lane));
             }
         }
 
