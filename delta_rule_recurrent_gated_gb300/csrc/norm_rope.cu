@@ -126,7 +126,7 @@ __device__ __forceinline__ void coefficients(const RopeParams& p, const Lane& a,
 }
 
 // The partners of a thread's channels: beside them (pairs) or in the other piece (halves).
-__device__ __forceinline__ void partners(const float2 (&x)[4], bool pairs, float2 (&q)[4]) {
+__device__ __forceinline__ void partners(const float2 (&x)[4], const bool pairs, float2 (&q)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         q[i].x = pairs ? x[i].y : x[i ^ 2].x;
@@ -147,16 +147,16 @@ template <int LANES> __device__ __forceinline__ float row_sum(float2 a, float2 b
     return lane_group_sum<LANES>((a.x + a.y) + (b.x + b.y));
 }
 
-// blockIdx.y: a run of `hp` heads of q (the first nq of them) or of k
+// A run of `hp` heads of q (the first nq runs) or of k, the i-th of them.
 struct Run {
     bool is_q;
     int h0, h1, H;
 };
-__device__ __forceinline__ Run make_run(const RopeParams& p) {
+__device__ __forceinline__ Run make_run(const RopeParams& p, int i) {
     Run r;
-    r.is_q = (int)blockIdx.y < p.nq;
+    r.is_q = i < p.nq;
     r.H = r.is_q ? p.Hq : p.Hk;
-    r.h0 = (r.is_q ? (int)blockIdx.y : (int)blockIdx.y - p.nq) * p.hp;
+    r.h0 = (r.is_q ? i : i - p.nq) * p.hp;
     r.h1 = min(r.h0 + p.hp, r.H);
     return r;
 }
@@ -172,14 +172,14 @@ __device__ __forceinline__ void load_heads(Vec8<T> (&v)[U], const T* row, const 
     }
 }
 
-template <typename IN, typename OUT, int LANES>
+template <typename IN, typename OUT, int LANES, bool PAIRS>
 __global__ void __launch_bounds__(kRopeThreads, sizeof(IN) == 2 ? 4 : 3) norm_rope_fwd_kernel(const RopeParams p) {
     constexpr int kGroups = kRopeThreads / LANES, U = 4;
     chain_wait();
     chain_release();
     const Lane a = make_lane<LANES>(p);
-    const Run run = make_run(p);
-    const bool pairs = p.style == DR_ROPE_PAIRS;
+    const Run run = make_run(p, blockIdx.y);
+    constexpr bool pairs = PAIRS;
     const long long ld = run.is_q ? p.ld_q : p.ld_k, ldo = run.is_q ? p.ld_oq : p.ld_ok;
     const IN* x0 = static_cast<const IN*>(run.is_q ? p.q : p.k);
     OUT* y0 = static_cast<OUT*>(run.is_q ? p.oq : p.ok);
@@ -221,15 +221,22 @@ __global__ void __launch_bounds__(kRopeThreads, sizeof(IN) == 2 ? 4 : 3) norm_ro
     }
 }
 
-template <typename IN, typename OUT, int LANES>
+template <typename IN, typename OUT, int LANES, bool PAIRS>
 __global__ void __launch_bounds__(kRopeThreads, kBwdResident) norm_rope_bwd_kernel(const RopeParams p) {
     constexpr int kGroups = kRopeThreads / LANES, U = sizeof(IN) == 2 ? kRun : kRun / 2;
     __shared__ float sums[kGroups][LANES * 8 + 1];
     chain_wait();
     chain_release();
     const Lane a = make_lane<LANES>(p);
-    const Run run = make_run(p);
-    const bool pairs = p.style == DR_ROPE_PAIRS;
+    // the block's run, its place among the run's blocks, and their number
+    const bool of_k = (int)blockIdx.x >= p.bq;
+    const int runs = of_k ? p.nk : p.nq;
+    int place = of_k ? blockIdx.x - p.bq : blockIdx.x;
+    const int i = min(place / p.nb, runs - 1);
+    place -= i * p.nb;
+    const int of = i < runs - 1 ? p.nb : of_k ? p.nbk : p.nbq;
+    const Run run = make_run(p, (of_k ? p.nq : 0) + i);
+    constexpr bool pairs = PAIRS;
     const long long ld = run.is_q ? p.ld_q : p.ld_k, ldo = run.is_q ? p.ld_oq : p.ld_ok;
     const IN* x0 = static_cast<const IN*>(run.is_q ? p.q : p.k);
     const IN* g0 = static_cast<const IN*>(run.is_q ? p.dyq : p.dyk);
@@ -239,8 +246,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdResident) norm_rope_bwd_kern
 #pragma unroll
     for (int i = 0; i < 4; ++i) dw[i] = both(0.f);
     const float inv_d = 1.f / p.d;
-    for (long long base = (long long)blockIdx.x * kGroups; base < p.tokens;
-         base += (long long)gridDim.x * kGroups) {
+    for (long long base = (long long)place * kGroups; base < p.tokens; base += (long long)of * kGroups) {
         const long long tok = base + threadIdx.x / LANES;
         const bool on = tok < p.tokens && a.active;
         const IN* xt = x0 + tok * ld + a.ch;
@@ -302,12 +308,12 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdResident) norm_rope_bwd_kern
         float s = 0.f;
 #pragma unroll 4
         for (int g = 0; g < kGroups; ++g) s += sums[g][c];
-        p.part[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * p.d + c] = s;
+        p.part[(size_t)blockIdx.x * p.d + c] = s;
     }
 }
 
 // Sums the blocks' parts of dw: block (i, 0) takes 8 channels of dwq, block (i, 1) of dwk.
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_dw_kernel(const RopeParams p, int blocks) {
+__global__ void __launch_bounds__(kRopeThreads) norm_rope_dw_kernel(const RopeParams p) {
     __shared__ float sums[32][9];
     const bool is_q = blockIdx.y == 0;
     float* dw = is_q ? p.dwq : p.dwk;
@@ -315,10 +321,9 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_dw_kernel(const RopePa
     chain_release();
     if (!dw) return;
     const int c = threadIdx.x & 7, j = threadIdx.x >> 3, ch = blockIdx.x * 8 + c;
-    const long long lo = is_q ? 0 : (long long)p.nq * blocks;
-    const long long hi = is_q ? (long long)p.nq * blocks : (long long)(p.nq + p.nk) * blocks;
+    const int lo = is_q ? 0 : p.bq, hi = is_q ? p.bq : p.bq + p.bk;
     float s = 0.f;
-    for (long long i = lo + j; i < hi; i += 32) s += p.part[i * p.d + ch];
+    for (int i = lo + j; i < hi; i += 32) s += p.part[(size_t)i * p.d + ch];
     sums[j][c] = s;
     __syncthreads();
     if (j == 0) {
@@ -332,65 +337,69 @@ __global__ void __launch_bounds__(kRopeThreads) norm_rope_dw_kernel(const RopePa
 int lanes_of(int d) { return d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : 32; }
 
 // Heads that a group of threads takes: all threads of the GPU get work before a group gets a
-// second head; from then on a run shares one token's coefficients: up to 16 heads forward (against 4:
-// 62 and 78 us for 8 x 4096 tokens, 20 heads of 128), 4 backward, where runs of equal length keep
-// the blocks, whose number is fixed, equally long.
-void split_heads(RopeParams& p, int lanes, bool bwd) {
+// second head; from then on a run of up to 16 heads shares one token's coefficients and reads 4 KB at
+// a time.  8 x 4096 tokens, 20 heads of 128, runs of 16 against runs of 4: forward 54 us (62), gradient
+// @@BWD@@.
+// The backward's blocks, all of them resident at once, are shared out by the heads of the runs.
+void split(RopeParams& p, int lanes, bool bwd) {
     const long long rows = p.tokens * (p.Hq + p.Hk), groups = 152ll * 2048 / lanes;
-    p.hp = rows < 2 * groups ? 1 : rows < 4 * groups ? 2 : bwd || rows < 16 * groups ? kRun : 16;
+    p.hp = rows < 2 * groups ? 1 : rows < 4 * groups ? 2 : rows < 16 * groups ? kRun : 16;
     p.nq = (p.Hq + p.hp - 1) / p.hp;
     p.nk = (p.Hk + p.hp - 1) / p.hp;
+    if (!bwd) return;
+    const int per = kRopeThreads / lanes;
+    const long long tiles = (p.tokens + per - 1) / per;
+    auto blocks = [&](int heads) {
+        long long n = (long long)kBwdBlocks * heads / (p.Hq + p.Hk);
+        n = n < 1 ? 1 : n;
+        return (int)(n < tiles ? n : tiles);
+    };
+    p.nb = blocks(p.hp);
+    p.nbq = p.nq ? blocks(p.Hq - (p.nq - 1) * p.hp) : 0;
+    p.nbk = p.nk ? blocks(p.Hk - (p.nk - 1) * p.hp) : 0;
+    p.bq = p.nq ? (p.nq - 1) * p.nb + p.nbq : 0;
+    p.bk = p.nk ? (p.nk - 1) * p.nb + p.nbk : 0;
 }
 
-// Blocks of each run in the backward: all of them resident at once.
-int bwd_blocks(const RopeParams& p, int lanes) {
-    const long long tiles = (p.tokens + kRopeThreads / lanes - 1) / (kRopeThreads / lanes);
-    const int runs = p.nq + p.nk, per = runs < kBwdBlocks ? kBwdBlocks / runs : 1;
-    return (int)(tiles < per ? tiles : per);
-}
-
-template <typename IN, typename OUT, int LANES>
+template <typename IN, typename OUT, int LANES, bool PAIRS>
 cudaError_t launch(const RopeParams& p, bool bwd, cudaStream_t st) {
     constexpr int kGroups = kRopeThreads / LANES;
     if (!bwd) {
         const long long tiles = (p.tokens + kGroups - 1) / kGroups;
         const dim3 grid((unsigned)(tiles < 0x7fffffff ? tiles : 0x7fffffff), p.nq + p.nk);
         TraceScope ts("norm_rope_fwd", st);
-        return launch_chained(norm_rope_fwd_kernel<IN, OUT, LANES>, grid, kRopeThreads, 0, st, p);
+        return launch_chained(norm_rope_fwd_kernel<IN, OUT, LANES, PAIRS>, grid, kRopeThreads, 0, st, p);
     }
-    const int blocks = bwd_blocks(p, LANES);
     {
         TraceScope ts("norm_rope_bwd", st);
-        if (cudaError_t e = launch_chained(norm_rope_bwd_kernel<IN, OUT, LANES>, dim3(blocks, p.nq + p.nk), kRopeThreads,
-                                           0, st, p);
+        if (cudaError_t e = launch_chained(norm_rope_bwd_kernel<IN, OUT, LANES, PAIRS>, dim3(p.bq + p.bk), kRopeThreads, 0, st, p);
             e != cudaSuccess)
             return e;
     }
     if (!p.dwq && !p.dwk) return cudaSuccess;
     TraceScope ts("norm_rope_dw", st);
-    return launch_chained(norm_rope_dw_kernel, dim3(p.d / 8, 2), kRopeThreads, 0, st, p, blocks);
+    return launch_chained(norm_rope_dw_kernel, dim3(p.d / 8, 2), kRopeThreads, 0, st, p);
 }
 
 template <typename IN, typename OUT>
 cudaError_t by_lanes(const RopeParams& p, bool bwd, cudaStream_t st) {
     switch (lanes_of(p.d)) {
-        case 4: return launch<IN, OUT, 4>(p, bwd, st);
-        case 8: return launch<IN, OUT, 8>(p, bwd, st);
-        case 16: return launch<IN, OUT, 16>(p, bwd, st);
-        default: return launch<IN, OUT, 32>(p, bwd, st);
+        case 4: return p.style == DR_ROPE_PAIRS ? launch<IN, OUT, 4, true>(p, bwd, st) : launch<IN, OUT, 4, false>(p, bwd, st);
+        case 8: return p.style == DR_ROPE_PAIRS ? launch<IN, OUT, 8, true>(p, bwd, st) : launch<IN, OUT, 8, false>(p, bwd, st);
+        case 16: return p.style == DR_ROPE_PAIRS ? launch<IN, OUT, 16, true>(p, bwd, st) : launch<IN, OUT, 16, false>(p, bwd, st);
+        default: return p.style == DR_ROPE_PAIRS ? launch<IN, OUT, 32, true>(p, bwd, st) : launch<IN, OUT, 32, false>(p, bwd, st);
     }
 }
 
 }  // namespace
 
 size_t norm_rope_part_bytes(RopeParams p) {
-    const int lanes = lanes_of(p.d);
-    split_heads(p, lanes, true);
-    return (size_t)(p.nq + p.nk) * bwd_blocks(p, lanes) * p.d * sizeof(float);
+    split(p, lanes_of(p.d), true);
+    return (size_t)(p.bq + p.bk) * p.d * sizeof(float);
 }
 
 cudaError_t norm_rope(RopeParams p, bool bwd, int io, int out, cudaStream_t st) {
-    split_heads(p, lanes_of(p.d), bwd);
+    split(p, lanes_of(p.d), bwd);
     if (io == DR_BF16)
         return out == DR_BF16 ? by_lanes<__nv_bfloat16, __nv_bfloat16>(p, bwd, st)
                               : by_lanes<__nv_bfloat16, float>(p, bwd, st);

@@ -16,7 +16,9 @@ struct RopeParams {
     void *oq, *ok;              // yq, yk (forward) or dq, dk (backward)
     float *dwq, *dwk;
     float* part;                // backward: the blocks' parts of dwq, dwk
-    int hp, nq, nk;             // heads of a run, runs of q and of k (set by the launcher)
+    // set by the launcher: heads of a run, runs of q and of k; backward: blocks of a run, of the last run
+    // of q and of k, of all runs of q and of k
+    int hp, nq, nk, nb, nbq, nbk, bq, bk;
 };
 
 size_t norm_rope_part_bytes(RopeParams p);
