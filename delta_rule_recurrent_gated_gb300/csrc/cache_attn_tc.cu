@@ -9,10 +9,11 @@
 // columns of its S.  So S of the next stage is formed before the weights of this one are there, and a
 // half waits for nobody (with one S it waited for the exchange with the issuing thread and for two
 // products every stage: 2950 cycles for both halves, where the products take 1140).  Shared memory
-// holds Q, and K and V as 16-bit floats (exact), three stages of them.
-// Warp 13 has the codes copied to a ring in shared memory; warps 8-11 turn them into the operand
-// tiles; warps 12 and 14 issue the products; warps 0-3 and 4-7 hold a row of their half per thread:
-// they read S, keep the softmax statistics and write P.
+// holds Q, and K and V as 16-bit floats (exact), three stages of K and four of V.
+// Warps 0-3 and 4-7 hold a row of their half per thread: they read S, keep the softmax statistics and
+// write P.  Warps 8-15 turn codes into the operand tiles (four of them were slower than the rows: a
+// stage took 2400 cycles instead of 2100); warps 16 and 18 issue the products; warp 17 has the codes
+// copied to a ring in shared memory.
 //
 // Softmax in base 2 with whole-number references, as in cache_attn.cu: p = 2^(s - m), l = sum p,
 // operand w = p vs 2^(m - M + 13).  The accumulator is rescaled (exactly, by a power of two) only when
@@ -33,7 +34,10 @@ namespace {
 using namespace tc;
 
 constexpr int kHalf = 128, kRows = 2 * kHalf, kStage = 64;
-constexpr int kTcThreads = 480;  // eight warps of rows, four of codes, two that issue products, one that copies
+constexpr int kTcThreads = 640;  // warps 0-7 rows, 8-15 codes, 16-18 products and copies (19: none)
+// Registers of a thread: as launched, then of the rows' threads and of the others, which give theirs up.
+constexpr int kRegs = 96, kRowRegs = 152, kOtherRegs = 56;
+static_assert(256 * kRowRegs + (kTcThreads - 256) * kOtherRegs <= kTcThreads * kRegs, "more than the block has");
 constexpr int kCodeThread0 = 256;
 constexpr int kKBuffers = 3, kVBuffers = 4;  // stages of K and V as operands: V is needed for longer
 constexpr int kRaw = 3;                      // as codes
@@ -42,6 +46,7 @@ constexpr float kSlack = 2.9f;
 constexpr int kTcOver = 4;       // what a tile costs beside its stages, in stages
 constexpr int kMetas = 8;        // stages whose scales are kept: more than the warps can be apart
 constexpr int kMaxTcBlocks = 152;
+constexpr int kJoinRows = 64;    // of a block of the second kernel: 6 us less on 256 tiles than with 128, 2 less than with 32
 // columns of tensor memory of half i
 __device__ __forceinline__ uint32_t s_col(int i, uint32_t b) { return 128 * i + 64 * b; }  // S, and P over it
 __device__ __forceinline__ uint32_t o_col(int i) { return 256 + 128 * i; }
@@ -241,7 +246,7 @@ __device__ __forceinline__ void convert16(const uint4& u, uint4& x, uint4& y) {
     codes_to_half<E4M3>(u.w, y.z, y.w);
 }
 
-// ------------------------------------------------------------------ warp 13: copies
+// ------------------------------------------------------------------ warp 17: copies
 // Lane 4 j + g holds page and scales of part g of the j-th of eight stages; the next eight stages'
 // are read while these are in use.
 template <int D>
@@ -308,16 +313,16 @@ __device__ __forceinline__ void copy_pages(const AttnParams& p, uint8_t* smem, C
     for (uint32_t m = n > kRaw ? n - kRaw : 0; m < n; ++m) mbar_wait(&ct.rfull[m % kRaw], (m / kRaw) & 1, kWaitLimitNs);
 }
 
-// ------------------------------------------------------------------ warps 8-11: codes to operand tiles
-// Warps 8 and 9 convert keys, 10 and 11 values, each two parts of 16 positions: 8 rows and a 64-byte
+// ------------------------------------------------------------------ warps 8-15: codes to operand tiles
+// Warps 8-11 convert keys, 12-15 values, each a part of 16 positions: 8 rows and a 64-byte
 // half row of each at a time; even and odd rows take the other half (d = 128), which keeps reads and
 // writes off each other's banks.
 template <int D, bool E4M3>
 __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
     constexpr int IT = D / 64;  // half rows of a row
     const int lane = threadIdx.x & 31, w = (threadIdx.x - kCodeThread0) >> 5;
-    const int r8 = lane >> 2, q = lane & 3, part0 = 2 * (w & 1);
-    const bool keys = w < 2;
+    const int r8 = lane >> 2, q = lane & 3, part = w & 3;
+    const bool keys = w < 4;
     uint64_t* full = keys ? ct.kfull : ct.vfull;
     uint64_t* empty = keys ? ct.kempty : ct.vempty;
     const uint32_t buffers = keys ? kKBuffers : kVBuffers;
@@ -332,26 +337,22 @@ __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem
             if (!wait(ct, &empty[buf], parity ^ 1)) return;
             const uint8_t* raw = raws + rb * 2 * Smem<D>::codes;
             uint8_t* tile = tiles + buf * Smem<D>::tile;
+            // values that hide behind the last position, or were not copied, may be anything: zeros
+            // (as keys they make scores that are hidden)
+            const int keep = keys ? 16 : ct.meta[n % kMetas].id[part] < 0 ? 0 : end - (base + i * kStage + 16 * part);
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                const int part = part0 + a;
-                // values that hide behind the last position, or were not copied, may be anything: zeros
-                // (as keys they make scores that are hidden)
-                const int keep = keys ? 16 : ct.meta[n % kMetas].id[part] < 0 ? 0 : end - (base + i * kStage + 16 * part);
+            for (int o = 0; o < 2; ++o)
 #pragma unroll
-                for (int o = 0; o < 2; ++o)
-#pragma unroll
-                    for (int it = 0; it < IT; ++it) {
-                        const int row = 16 * part + 8 * o + r8, half = IT == 2 ? (row ^ it) & 1 : 0;
-                        uint4 u = *reinterpret_cast<const uint4*>(raw + row * D + half * 64 + q * 16);
-                        if (8 * o + r8 >= keep) u = make_uint4(0, 0, 0, 0);
-                        uint4 x, y;
-                        convert16<E4M3>(u, x, y);
-                        uint8_t* at = tile + half * kStage * 128 + row * 128;
-                        *reinterpret_cast<uint4*>(at + (((2 * q) ^ (row & 7)) << 4)) = x;
-                        *reinterpret_cast<uint4*>(at + (((2 * q + 1) ^ (row & 7)) << 4)) = y;
-                    }
-            }
+                for (int it = 0; it < IT; ++it) {
+                    const int row = 16 * part + 8 * o + r8, half = IT == 2 ? (row ^ it) & 1 : 0;
+                    uint4 u = *reinterpret_cast<const uint4*>(raw + row * D + half * 64 + q * 16);
+                    if (8 * o + r8 >= keep) u = make_uint4(0, 0, 0, 0);
+                    uint4 x, y;
+                    convert16<E4M3>(u, x, y);
+                    uint8_t* at = tile + half * kStage * 128 + row * 128;
+                    *reinterpret_cast<uint4*>(at + (((2 * q) ^ (row & 7)) << 4)) = x;
+                    *reinterpret_cast<uint4*>(at + (((2 * q + 1) ^ (row & 7)) << 4)) = y;
+                }
             fence_async_smem();
             warp_arrive(&full[buf]);
             if (lane == 0) mbar_arrive(&ct.rempty[rb]);
@@ -361,7 +362,7 @@ __device__ __forceinline__ void convert_codes(const AttnParams& p, uint8_t* smem
     }
 }
 
-// ------------------------------------------------------------------ warps 12 and 14: the products
+// ------------------------------------------------------------------ warps 16 and 18: the products
 // A wait, a commit and a switch from one product to the other cost the issuing warp 100 to 250 cycles
 // each, so S and O have a warp each, which issues both halves together.
 // S = Q K^T of stage n, over the columns of P of stage n - 2: after that P's products.
@@ -437,6 +438,13 @@ __device__ __forceinline__ void drain(Control& ct, uint64_t* bar) {
 }
 
 // ------------------------------------------------------------------ warps 0-7: a row per thread
+// Keeps the instructions before and after it apart: a pair's chain of product, powers, sum and conversion is
+// long, and two warps a scheduler hide it only where eight pairs take each of its steps together (17 cycles a
+// pair and scheduler otherwise, 10 so).
+__device__ __forceinline__ void in_order(float2 (&z)[8]) {
+    asm volatile("" : "+f"(z[0].x), "+f"(z[0].y), "+f"(z[1].x), "+f"(z[1].y), "+f"(z[2].x), "+f"(z[2].y), "+f"(z[3].x), "+f"(z[3].y),
+                 "+f"(z[4].x), "+f"(z[4].y), "+f"(z[5].x), "+f"(z[5].y), "+f"(z[6].x), "+f"(z[6].y), "+f"(z[7].x), "+f"(z[7].y));
+}
 template <int D, bool E4M3>
 __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
     const int hf = threadIdx.x / kHalf, r = threadIdx.x % kHalf, lane = threadIdx.x & 31;
@@ -589,24 +597,33 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
                 }
             }
             const float mref = m == kNegInf ? 0.f : m, fm = pow2i(fminf(m - M + kTcBias, 126.f));
-            float2 l2 = make_float2(0.f, 0.f);
+            float2 l2 = make_float2(0.f, 0.f), l3 = l2;
             const float2 nm = make_float2(-mref, -mref);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const float2 f = make_float2(fm * vs[g], fm * vs[g]), k2 = make_float2(kf[g], kf[g]);
+                float2 z[8];
                 float w[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float2 z = fma2(make_float2(x[g][2 * j], x[g][2 * j + 1]), k2, nm);
-                    z.x = ex2(z.x);
-                    z.y = ex2(z.y);
-                    l2 = add2(l2, z);
-                    z = mul2(z, f);
-                    w[j] = __uint_as_float(pack_half(z.x, z.y));
+                for (int j = 0; j < 8; ++j) z[j] = fma2(make_float2(x[g][2 * j], x[g][2 * j + 1]), k2, nm);
+                in_order(z);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) z[j] = make_float2(ex2(z[j].x), ex2(z[j].y));
+                in_order(z);
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) {
+                    l2 = add2(l2, z[j]);
+                    z[j] = mul2(z[j], f);
+                    l3 = add2(l3, z[j + 1]);
+                    z[j + 1] = mul2(z[j + 1], f);
                 }
+                in_order(z);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = __uint_as_float(pack_half(z[j].x, z[j].y));
                 __syncwarp();
                 tmem_st8(ts + 8 * g, w);
             }
+            l2 = add2(l2, l3);
             l += l2.x + l2.y;
             tmem_st_wait();
             tc_fence_before();
@@ -675,14 +692,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     if (threadIdx.x == 32) {
         for (int i = 0; i < kRaw; ++i) {
             mbar_init(&ct.rfull[i], 1);
-            mbar_init(&ct.rempty[i], 4);
+            mbar_init(&ct.rempty[i], 8);
         }
         for (int i = 0; i < kKBuffers; ++i) {
-            mbar_init(&ct.kfull[i], 2);
+            mbar_init(&ct.kfull[i], 4);
             mbar_init(&ct.kempty[i], 1);
         }
         for (int i = 0; i < kVBuffers; ++i) {
-            mbar_init(&ct.vfull[i], 2);
+            mbar_init(&ct.vfull[i], 4);
             mbar_init(&ct.vempty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -702,11 +719,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp < 8) soften_rows<D, E4M3>(p, smem, ct, walk);
-    else if (warp < 12) convert_codes<D, E4M3>(p, smem, ct, walk);
-    else if (warp == 12) issue_scores<D>(p, smem, ct, walk), drain(ct, &ct.drain[0]);
-    else if (warp == 13) copy_pages<D>(p, smem, ct, walk);
-    else issue_values<D>(p, smem, ct, walk), drain(ct, &ct.drain[1]);
+    if (warp < 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRowRegs));
+        soften_rows<D, E4M3>(p, smem, ct, walk);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp < 16) convert_codes<D, E4M3>(p, smem, ct, walk);
+        else if (warp == 16) issue_scores<D>(p, smem, ct, walk), drain(ct, &ct.drain[0]);
+        else if (warp == 17) copy_pages<D>(p, smem, ct, walk);
+        else if (warp == 18) issue_values<D>(p, smem, ct, walk), drain(ct, &ct.drain[1]);
+    }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -715,8 +737,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     if (warp == 0) tmem_dealloc(ct.tmem, 512);
 }
 
-// Joins the parts of a tile that several blocks worked on.  Block x: the tile, y: 32 of its rows, a
-// lane each; warp w takes channels w d/8 .. + d/8 - 1.  Rows of no query get zeros (behind a
+// Joins the parts of a tile that several blocks worked on.  Block x: the tile, y: 64 of its rows, two
+// a lane; warp w takes channels w d/8 .. + d/8 - 1.  Rows of no query get zeros (behind a
 // sequence's tokens) or NaN (a sequence out of range).
 template <int D>
 __global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParams p, int blocks, int max_tiles) {
@@ -724,7 +746,7 @@ __global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParam
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch0 = warp * (D / 8);
     const int b = blockIdx.x / (p.c.H * max_tiles), other = blockIdx.x % (p.c.H * max_tiles);
     const int h = other / max_tiles, tile = other % max_tiles;
-    const int r = blockIdx.y * 32 + lane, row = tile * kRows + r;
+    const int r0 = blockIdx.y * kJoinRows + lane, r1 = r0 + kJoinRows;
     // The first kernel's blocks released this one after their own wait: what they read may be read.  Its
     // parts are there after chain_wait(), which every thread comes to, so that the end of this kernel is
     // also the end of the first.
@@ -734,13 +756,14 @@ __global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParam
         if (threadIdx.x == 0) flag_index_error(p.c);
         n = 0;
     }
-    if (row >= n * p.G && row < p.c.T * p.G) {
+    for (int row = tile * kRows + r0; row < min(tile * kRows + r1, p.c.T * p.G); row += 32) {
+        if (row < n * p.G) continue;
         const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
         const float bad = __uint_as_float(0x7fc00000u);
         for (int j = ch0; j < ch0 + D / 8; ++j) st_any(p.o, at * D + j, p.out, ok ? 0.f : bad);
         if (warp == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
     }
-    if (tile * kRows + blockIdx.y * 32 >= n * p.G) {
+    if (tile * kRows + blockIdx.y * kJoinRows >= n * p.G) {
         chain_wait();
         chain_release();
         return;
@@ -770,51 +793,61 @@ __global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParam
     const float* head = p.part + ((size_t)first * 2 + (share(total, first, used) >= a - kTcOver ? 0 : 1)) * tile_floats(D, kRows);
     chain_wait();
     chain_release();
-    if (first == last || row >= n * p.G) return;  // finished by its block
-    float m = kNegInf, M = kNegInf, l = 0.f;
-    float4 sum[V];
+    if (first == last) return;  // finished by its block
+    for (int r = r0; r < r1; r += 32) {
+        const int row = tile * kRows + r;
+        if (row >= n * p.G) return;
+        float m = kNegInf, M = kNegInf, l = 0.f;
+        float4 sum[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-    // a part without weight adds nothing, one that met a NaN hands it on
-    auto add = [](float& x, float fx, float y, float fy) { x = (x == x ? x * fx : x) + (y == y ? y * fy : y); };
+        for (int j = 0; j < V; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+        // a part without weight adds nothing, one that met a NaN hands it on
+        auto add = [](float& x, float fx, float y, float fy) { x = (x == x ? x * fx : x) + (y == y ? y * fy : y); };
 #pragma unroll 2
-    for (int i = first; i <= last; ++i) {
-        const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, kRows);
-        float4 y[V];
+        for (int i = first; i <= last; ++i) {
+            const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, kRows);
+            float4 y[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) y[j] = reinterpret_cast<const float4*>(in)[(ch0 / 4 + j) * kRows + r];
-        const float pl = in[kRows * D + r], pm = in[kRows * D + kRows + r], pM = in[kRows * D + 2 * kRows + r];
-        const float m2 = fmaxf(m, pm), M2 = fmaxf(M, pM);
-        const float s1 = pow2i(M - M2), s2 = pow2i(pM - M2);
-        add(l, pow2i(m - m2), pl, pow2i(pm - m2));
+            for (int j = 0; j < V; ++j) y[j] = reinterpret_cast<const float4*>(in)[(ch0 / 4 + j) * kRows + r];
+            const float pl = in[kRows * D + r], pm = in[kRows * D + kRows + r], pM = in[kRows * D + 2 * kRows + r];
+            const float m2 = fmaxf(m, pm), M2 = fmaxf(M, pM);
+            const float s1 = pow2i(M - M2), s2 = pow2i(pM - M2);
+            add(l, pow2i(m - m2), pl, pow2i(pm - m2));
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            add(sum[j].x, s1, y[j].x, s2);
-            add(sum[j].y, s1, y[j].y, s2);
-            add(sum[j].z, s1, y[j].z, s2);
-            add(sum[j].w, s1, y[j].w, s2);
+            for (int j = 0; j < V; ++j) {
+                add(sum[j].x, s1, y[j].x, s2);
+                add(sum[j].y, s1, y[j].y, s2);
+                add(sum[j].z, s1, y[j].z, s2);
+                add(sum[j].w, s1, y[j].w, s2);
+            }
+            m = m2;
+            M = M2;
         }
-        m = m2;
-        M = M2;
-    }
-    const float f = M - m - kBias;
-    const float inv = M == kNegInf ? (l == l ? 0.f : l) : ldexpf(1.f / l, (int)fminf(fmaxf(f, -140.f), 120.f));
-    const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
-    uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + ch0);
+        const float f = M - m - kBias;
+        const float inv = M == kNegInf ? (l == l ? 0.f : l) : ldexpf(1.f / l, (int)fminf(fmaxf(f, -140.f), 120.f));
+        const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
+        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + ch0);
 #pragma unroll
-    for (int j = 0; j < V; j += 2) {
-        const uint4 u = make_uint4(pack_bf16(sum[j].x * inv, sum[j].y * inv), pack_bf16(sum[j].z * inv, sum[j].w * inv),
-                                   pack_bf16(sum[j + 1].x * inv, sum[j + 1].y * inv),
-                                   pack_bf16(sum[j + 1].z * inv, sum[j + 1].w * inv));
-        *reinterpret_cast<uint4*>(o + j) = u;
+        for (int j = 0; j < V; j += 2) {
+            const uint4 u = make_uint4(pack_bf16(sum[j].x * inv, sum[j].y * inv), pack_bf16(sum[j].z * inv, sum[j].w * inv),
+                                       pack_bf16(sum[j + 1].x * inv, sum[j + 1].y * inv),
+                                       pack_bf16(sum[j + 1].z * inv, sum[j + 1].w * inv));
+            *reinterpret_cast<uint4*>(o + j) = u;
+        }
+        if (warp == 0 && p.lse) p.lse[at] = (m + log2f(l)) * kLn2;
     }
-    if (warp == 0 && p.lse) p.lse[at] = (m + log2f(l)) * kLn2;
 }
 
 template <int D, bool E4M3>
 cudaError_t launch(const AttnParams& p, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
     constexpr int smem = Smem<D>::bytes;
+    // the split of the registers must not ask for more than the block is launched with: it would wait for them
+    static const bool fits = [] {
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, cache_attn_tc_kernel<D, E4M3>) == cudaSuccess && a.numRegs == kRegs;
+    }();
+    if (!fits) return cudaErrorInvalidConfiguration;
     if (cudaError_t e = set_smem_once(cache_attn_tc_kernel<D, E4M3>, smem, ready); e != cudaSuccess) return e;
     const int blocks = kMaxTcBlocks;
     {
@@ -825,7 +858,7 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
     }
     const int max_tiles = (p.c.T * p.G + kRows - 1) / kRows;
     TraceScope ts("cache_attn_tc_join", st);
-    return launch_chained(cache_attn_tc_join_kernel<D>, dim3((unsigned)p.c.B * p.c.H * max_tiles, kRows / 32), 256, 0, st, p, blocks, max_tiles);
+    return launch_chained(cache_attn_tc_join_kernel<D>, dim3((unsigned)p.c.B * p.c.H * max_tiles, kRows / kJoinRows), 256, 0, st, p, blocks, max_tiles);
 }
 
 }  // namespace
