@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kStep = 32, kStage = kStep * kWarps;  // positions of a warp's step, of a stage
-constexpr int kOver = 4;  // what a tile costs beside its stages, in stages
+constexpr int kOver = 4;  // what a tile costs beside its stages, in stages (64 ragged sequences: 57.6 us; 61.1 with 2, 59.0 with 6)
 
 // ------------------------------------------------------------------ the line of stages
 // Stages of sequence b that its tokens see, tiles of rows, and their product with the heads.

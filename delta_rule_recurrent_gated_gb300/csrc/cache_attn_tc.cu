@@ -43,7 +43,7 @@ constexpr int kKBuffers = 3, kVBuffers = 4;  // stages of K and V as operands: V
 constexpr int kRaw = 3;                      // as codes
 constexpr int kTcBias = 13;       // weights as 16-bit operands: 2^12 .. 2^15.9 for a row's largest
 constexpr float kSlack = 2.9f;
-constexpr int kTcOver = 4;       // what a tile costs beside its stages, in stages
+constexpr int kTcOver = 8;       // what a tile costs beside its stages, in stages (126 us with 8, 127 with 6 and 12, 130 with 4)
 constexpr int kMetas = 8;        // stages whose scales are kept: more than the warps can be apart
 constexpr int kMaxTcBlocks = 152;
 constexpr int kJoinRows = 64;    // of a block of the second kernel: 6 us less on 256 tiles than with 128, 2 less than with 32
@@ -470,21 +470,28 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
                 raw[i] = from >= 0 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + from) + chunk)
                                    : make_uint4(0, 0, 0, 0);
             }
-            float mine = 0.f;  // the largest magnitude of this lane's own row
+            // Magnitudes of bf16 values order as their bits: the largest of two rows at once, and of this lane's own.
+            uint32_t mine = 0;
 #pragma unroll
-            for (int i = 0; i < L; ++i) {
-                float x[8], top = 0.f;
-                unpack8(raw[i], x);
+            for (int i = 0; i < L; i += 2) {
+                uint32_t top[2];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) top = fmaxf(top, fabsf(x[q]));
+                for (int j = 0; j < 2; ++j) {
+                    const uint4 u = raw[i + j];
+                    const uint32_t t = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu),
+                                                __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+                    top[j] = __vmaxu2(t, t >> 16);
+                }
+                uint32_t two = __byte_perm(top[0], top[1], 0x5410);
 #pragma unroll
-                for (int o = L / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-                top = __shfl_sync(0xffffffffu, top, (lane % R) * L);
-                if (lane / R == i) mine = top;
+                for (int o = L / 2; o > 0; o >>= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, o));
+                two = __shfl_sync(0xffffffffu, two, (lane % R) * L);
+                if (lane / R == i) mine = two & 0xffffu;
+                if (lane / R == i + 1) mine = two >> 16;
             }
-            float up, rest;
-            query_scale(mine, e, up, rest);
-            e = max(e, -126);  // one factor is enough for bf16
+            // a power of two to a largest magnitude of 2^9 .. 2^10: a bf16 value stays exact unless it is below
+            // 2^-24 of the row's largest
+            e = mine > 0 && mine < 0x7f80u ? max((int)(mine >> 7) - 136, -126) : 0;
             const float f = p.scale < 0.f ? -pow2i(-(float)e) : pow2i(-(float)e);
 #pragma unroll
             for (int i = 0; i < L; ++i) {
