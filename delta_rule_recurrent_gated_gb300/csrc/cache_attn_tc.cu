@@ -46,7 +46,6 @@ constexpr float kSlack = 2.9f;
 constexpr int kTcOver = 8;       // what a tile costs beside its stages, in stages (126 us with 8, 127 with 6 and 12, 130 with 4)
 constexpr int kMetas = 8;        // stages whose scales are kept: more than the warps can be apart
 constexpr int kMaxTcBlocks = 152;
-constexpr int kJoinRows = 64;    // of a block of the second kernel: 6 us less on 256 tiles than with 128, 2 less than with 32
 // columns of tensor memory of half i
 __device__ __forceinline__ uint32_t s_col(int i, uint32_t b) { return 128 * i + 64 * b; }  // S, and P over it
 __device__ __forceinline__ uint32_t o_col(int i) { return 256 + 128 * i; }
@@ -84,6 +83,14 @@ struct Stretch {
     bool whole, first;   // the whole tile; the block's first stretch
     TcTile t;
 };
+// The whole line (every lane gets it).
+__device__ __forceinline__ long long line_length(const AttnParams& p, int lane) {
+    long long total = 0;
+    for (int i = lane; i < p.c.B; i += 32) total += head_work(p, i) * p.c.H;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    return total;
+}
 // Walks through a block's part of the line; every warp does so for itself, with the same result.
 struct Walk {
     long long at, end;
@@ -91,16 +98,17 @@ struct Walk {
     bool first;
 
     __device__ __forceinline__ void start(const AttnParams& p, int lane) {
-        long long total = 0;
-        for (int i = lane; i < p.c.B; i += 32) total += head_work(p, i) * p.c.H;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        const long long total = line_length(p, lane);
         const int used = blocks_used(total, gridDim.x);
         at = end = 0;
         first = true;
         if ((int)blockIdx.x >= used) return;
         at = share(total, blockIdx.x, used);
         end = share(total, blockIdx.x + 1, used);
+        find(p, lane);
+    }
+    // The tile that holds place `at`, and the place within it; b < 0 where there is none.
+    __device__ __forceinline__ void find(const AttnParams& p, int lane) {
         long long before = 0, mine = 0;
         b = -1;
         for (int b0 = 0; b0 < p.c.B && b < 0; b0 += 32) {
@@ -166,6 +174,15 @@ struct Walk {
         return false;
     }
 };
+
+// A tile that several blocks worked on, as its first block leaves it for the second kernel: its rows, the last of the
+// blocks (none: -1) and which of the first block's two parts it is.
+struct __align__(16) Joint {
+    int b, h, n, row0, last, slot, unused[2];
+};
+__device__ __forceinline__ Joint* joints(const AttnParams& p, int d) {
+    return reinterpret_cast<Joint*>(p.part + (size_t)kMaxTcBlocks * 2 * tile_floats(d, kRows));
+}
 
 // ------------------------------------------------------------------ shared memory
 struct __align__(16) StageMeta {  // read as 16-byte words
@@ -255,6 +272,8 @@ __device__ __forceinline__ void copy_pages(const AttnParams& p, uint8_t* smem, C
     const int rows = min(p.c.page, kStage), copies = kStage / rows;  // of a stage
     uint32_t n = 0;
     Stretch s;
+    s.from = s.upto = s.t.stages = 0;
+    if (lane == 0) joints(p, D)[blockIdx.x].last = -1;
     bool ok = true;
     while (ok && walk.next(p, s)) {
         const int stages = s.upto - s.from, base = (s.t.s0 + s.from) * kStage;
@@ -308,6 +327,14 @@ __device__ __forceinline__ void copy_pages(const AttnParams& p, uint8_t* smem, C
             }
             warp_arrive(&ct.rfull[buf]);
         }
+    }
+    // the block's last tile goes on in the next ones
+    if (s.from == 0 && s.upto > 0 && s.upto < s.t.stages) {
+        const long long total = line_length(p, lane);
+        const int used = blocks_used(total, gridDim.x), i = blockIdx.x;
+        const long long after = share(total, i + 1, used) - s.upto + s.t.stages;  // the tile's last place + 1
+        if (lane == 0 && after <= total)  // (the lengths may have changed under the call)
+            joints(p, D)[i] = {s.b, s.h, s.n, s.t.row0, min(holder(total, after - 1, used), used - 1), s.first ? 0 : 1};
     }
     // no copy outlives the block, whatever became of the other warps
     for (uint32_t m = n > kRaw ? n - kRaw : 0; m < n; ++m) mbar_wait(&ct.rfull[m % kRaw], (m / kRaw) & 1, kWaitLimitNs);
@@ -744,105 +771,75 @@ __global__ void __launch_bounds__(kTcThreads, 1) cache_attn_tc_kernel(const Attn
     if (warp == 0) tmem_dealloc(ct.tmem, 512);
 }
 
-// Joins the parts of a tile that several blocks worked on.  Block x: the tile, y: 64 of its rows, two
-// a lane; warp w takes channels w d/8 .. + d/8 - 1.  Rows of no query get zeros (behind a
-// sequence's tokens) or NaN (a sequence out of range).
+// Joins the parts of the tiles that several blocks worked on.  Block x: the tile that the first kernel's block x
+// began and others went on with, if any, so that the number of tiles does not matter (a search for it on the
+// line took 10 us); y: 32 of its rows, a lane each; warp w takes channels w d/8 .. + d/8 - 1.  Rows of no
+// query get zeros (behind a sequence's tokens) or NaN (a sequence out of range).
 template <int D>
-__global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParams p, int blocks, int max_tiles) {
+__global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParams p) {
     constexpr int V = D / 32;  // float4s of a lane
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ch0 = warp * (D / 8);
-    const int b = blockIdx.x / (p.c.H * max_tiles), other = blockIdx.x % (p.c.H * max_tiles);
-    const int h = other / max_tiles, tile = other % max_tiles;
-    const int r0 = blockIdx.y * kJoinRows + lane, r1 = r0 + kJoinRows;
     // The first kernel's blocks released this one after their own wait: what they read may be read.  Its
     // parts are there after chain_wait(), which every thread comes to, so that the end of this kernel is
     // also the end of the first.
-    int len, n;
-    const bool ok = cache_seq(p.c, b, len, n);
-    if (!ok) {
-        if (threadIdx.x == 0) flag_index_error(p.c);
-        n = 0;
+    const long long tokens = (long long)p.c.B * p.c.T;
+    for (long long t = (blockIdx.y * gridDim.x + blockIdx.x) * 8 + warp; t < tokens; t += gridDim.x * gridDim.y * 8) {
+        int len, n;
+        const bool ok = cache_seq(p.c, (int)(t / p.c.T), len, n);
+        if (!ok && lane == 0) flag_index_error(p.c);
+        if (ok && t % p.c.T < n) continue;
+        const uint32_t bad = ok ? 0u : 0x7fc07fc0u;
+        uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + t * p.Hq * D);
+        for (int j = lane; j < p.Hq * D / 8; j += 32) o[j] = make_uint4(bad, bad, bad, bad);
+        if (p.lse)
+            for (int j = lane; j < p.Hq; j += 32) p.lse[t * p.Hq + j] = ok ? kNegInf : __uint_as_float(0x7fc00000u);
     }
-    for (int row = tile * kRows + r0; row < min(tile * kRows + r1, p.c.T * p.G); row += 32) {
-        if (row < n * p.G) continue;
-        const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
-        const float bad = __uint_as_float(0x7fc00000u);
-        for (int j = ch0; j < ch0 + D / 8; ++j) st_any(p.o, at * D + j, p.out, ok ? 0.f : bad);
-        if (warp == 0 && p.lse) p.lse[at] = ok ? kNegInf : bad;
-    }
-    if (tile * kRows + blockIdx.y * kJoinRows >= n * p.G) {
-        chain_wait();
-        chain_release();
-        return;
-    }
-    long long total = 0, before = 0;
-    for (int i = lane; i < p.c.B; i += 32) {
-        const long long w = head_work(p, i) * p.c.H;
-        total += w;
-        if (i < b) before += w;
-    }
-    long long mine = 0, upto = 0;  // a head of this sequence; its tiles before this one
-    for (int i = lane; i < tiles_of(p, n); i += 32) {
-        const int cost = make_tile(p, len, n, i).stages + kTcOver;
-        mine += cost;
-        if (i < tile) upto += cost;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-        before += __shfl_xor_sync(0xffffffffu, before, o);
-        mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        upto += __shfl_xor_sync(0xffffffffu, upto, o);
-    }
-    const long long a = before + h * mine + upto + kTcOver;  // the tile's first stage on the line
-    const int stages = make_tile(p, len, n, tile).stages, used = blocks_used(total, blocks);
-    const int first = holder(total, a, used), last = holder(total, a + stages - 1, used);
-    const float* head = p.part + ((size_t)first * 2 + (share(total, first, used) >= a - kTcOver ? 0 : 1)) * tile_floats(D, kRows);
     chain_wait();
     chain_release();
-    if (first == last) return;  // finished by its block
-    for (int r = r0; r < r1; r += 32) {
-        const int row = tile * kRows + r;
-        if (row >= n * p.G) return;
-        float m = kNegInf, M = kNegInf, l = 0.f;
-        float4 sum[V];
+    const int first = blockIdx.x;
+    const Joint j0 = joints(p, D)[first];
+    if (j0.last <= first) return;  // its last tile was finished by it, or is another's to join
+    const int b = j0.b, h = j0.h, n = j0.n, last = j0.last, slot = j0.slot;
+    const int r = blockIdx.y * 32 + lane, row = j0.row0 + r;
+    if (row >= n * p.G) return;
+    float m = kNegInf, M = kNegInf, l = 0.f;
+    float4 sum[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-        // a part without weight adds nothing, one that met a NaN hands it on
-        auto add = [](float& x, float fx, float y, float fy) { x = (x == x ? x * fx : x) + (y == y ? y * fy : y); };
+    for (int j = 0; j < V; ++j) sum[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+    // a part without weight adds nothing, one that met a NaN hands it on
+    auto add = [](float& x, float fx, float y, float fy) { x = (x == x ? x * fx : x) + (y == y ? y * fy : y); };
 #pragma unroll 2
-        for (int i = first; i <= last; ++i) {
-            const float* in = i == first ? head : p.part + (size_t)i * 2 * tile_floats(D, kRows);
-            float4 y[V];
+    for (int i = first; i <= last; ++i) {
+        const float* in = p.part + ((size_t)i * 2 + (i == first ? slot : 0)) * tile_floats(D, kRows);
+        float4 y[V];
 #pragma unroll
-            for (int j = 0; j < V; ++j) y[j] = reinterpret_cast<const float4*>(in)[(ch0 / 4 + j) * kRows + r];
-            const float pl = in[kRows * D + r], pm = in[kRows * D + kRows + r], pM = in[kRows * D + 2 * kRows + r];
-            const float m2 = fmaxf(m, pm), M2 = fmaxf(M, pM);
-            const float s1 = pow2i(M - M2), s2 = pow2i(pM - M2);
-            add(l, pow2i(m - m2), pl, pow2i(pm - m2));
+        for (int j = 0; j < V; ++j) y[j] = reinterpret_cast<const float4*>(in)[(ch0 / 4 + j) * kRows + r];
+        const float pl = in[kRows * D + r], pm = in[kRows * D + kRows + r], pM = in[kRows * D + 2 * kRows + r];
+        const float m2 = fmaxf(m, pm), M2 = fmaxf(M, pM);
+        const float s1 = pow2i(M - M2), s2 = pow2i(pM - M2);
+        add(l, pow2i(m - m2), pl, pow2i(pm - m2));
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                add(sum[j].x, s1, y[j].x, s2);
-                add(sum[j].y, s1, y[j].y, s2);
-                add(sum[j].z, s1, y[j].z, s2);
-                add(sum[j].w, s1, y[j].w, s2);
-            }
-            m = m2;
-            M = M2;
+        for (int j = 0; j < V; ++j) {
+            add(sum[j].x, s1, y[j].x, s2);
+            add(sum[j].y, s1, y[j].y, s2);
+            add(sum[j].z, s1, y[j].z, s2);
+            add(sum[j].w, s1, y[j].w, s2);
         }
-        const float f = M - m - kBias;
-        const float inv = M == kNegInf ? (l == l ? 0.f : l) : ldexpf(1.f / l, (int)fminf(fmaxf(f, -140.f), 120.f));
-        const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
-        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + ch0);
-#pragma unroll
-        for (int j = 0; j < V; j += 2) {
-            const uint4 u = make_uint4(pack_bf16(sum[j].x * inv, sum[j].y * inv), pack_bf16(sum[j].z * inv, sum[j].w * inv),
-                                       pack_bf16(sum[j + 1].x * inv, sum[j + 1].y * inv),
-                                       pack_bf16(sum[j + 1].z * inv, sum[j + 1].w * inv));
-            *reinterpret_cast<uint4*>(o + j) = u;
-        }
-        if (warp == 0 && p.lse) p.lse[at] = (m + log2f(l)) * kLn2;
+        m = m2;
+        M = M2;
     }
+    const float f = M - m - kBias;
+    const float inv = M == kNegInf ? (l == l ? 0.f : l) : ldexpf(1.f / l, (int)fminf(fmaxf(f, -140.f), 120.f));
+    const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
+    uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + ch0);
+#pragma unroll
+    for (int j = 0; j < V; j += 2) {
+        const uint4 u = make_uint4(pack_bf16(sum[j].x * inv, sum[j].y * inv), pack_bf16(sum[j].z * inv, sum[j].w * inv),
+                                   pack_bf16(sum[j + 1].x * inv, sum[j + 1].y * inv),
+                                   pack_bf16(sum[j + 1].z * inv, sum[j + 1].w * inv));
+        *reinterpret_cast<uint4*>(o + j) = u;
+    }
+    if (warp == 0 && p.lse) p.lse[at] = (m + log2f(l)) * kLn2;
 }
 
 template <int D, bool E4M3>
@@ -863,14 +860,13 @@ cudaError_t launch(const AttnParams& p, cudaStream_t st) {
             e != cudaSuccess)
             return e;
     }
-    const int max_tiles = (p.c.T * p.G + kRows - 1) / kRows;
     TraceScope ts("cache_attn_tc_join", st);
-    return launch_chained(cache_attn_tc_join_kernel<D>, dim3((unsigned)p.c.B * p.c.H * max_tiles, kRows / kJoinRows), 256, 0, st, p, blocks, max_tiles);
+    return launch_chained(cache_attn_tc_join_kernel<D>, dim3(blocks, kRows / 32), 256, 0, st, p);
 }
 
 }  // namespace
 
-size_t cache_attn_tc_bytes(int d) { return (size_t)kMaxTcBlocks * 2 * tile_floats(d, kRows) * sizeof(float); }
+size_t cache_attn_tc_bytes(int d) { return (size_t)kMaxTcBlocks * (2 * tile_floats(d, kRows) * sizeof(float) + sizeof(Joint)); }
 
 cudaError_t cache_attn_tc(const AttnParams& p, cudaStream_t st) {
     if (p.c.code == DR_CODE_E4M3) return p.c.d == 128 ? launch<128, true>(p, st) : launch<64, true>(p, st);

