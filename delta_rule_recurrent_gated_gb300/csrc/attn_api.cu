@@ -94,11 +94,11 @@ int check_attn(const dr_cache* c, const dr_attn_desc* d, int B, int T) {
 }
 
 // Which kernel, by the rows of a sequence and cache head (query tokens times the query heads that share
-// it): from 48 on a tile of the tensor cores is the faster even partly filled.  Four sequences of 8000
-// positions, four cache heads of 128: 32 rows 33.8 us (41.0 on the tensor cores), 48 rows 47.0 (41.7),
-// 256 rows 122 (46); heads of 64: 32 rows 22.8 (30.4), 48 rows 31.6 (30.3).  fp32 types need the split
-// operands of the other kernel.
-constexpr int kTcRows = 48;
+// it): up to 32 rows are one tile of the kernel for few rows; from 33 on a tile of the tensor cores is the
+// faster even partly filled.  Four sequences of 8000 positions, four cache heads of 128: 32 rows 34.0 us (35.6
+// on the tensor cores), 40 rows 41.9 (36.0), 256 rows 122.7 (40.0); heads of 64: 32 rows 23.1 (28.7), 40 rows
+// 29.1 (28.9), 256 rows 84.4 (32.5).  fp32 types need the split operands of the other kernel.
+constexpr int kTcRows = 33;
 bool on_tensor_cores(const dr_cache* c, const dr_attn_desc* d, int T) {
     return d->io_dtype == DR_BF16 && d->out_dtype == DR_BF16 && (long long)T * (d->Hq / c->H) >= kTcRows;
 }
