@@ -24,7 +24,7 @@
 // The stages of all tiles form one line that is divided evenly among the blocks (one per SM); a tile
 // that several blocks worked on is joined by a second kernel from their rows in the workspace.
 //
-// Chunks of 512 tokens of four sequences of 4000 to 8191 positions, 16 query heads on 4 of 128: 122 us for
+// Chunks of 512 tokens of four sequences of 4000 to 8191 positions, 16 query heads on 4 of 128: 122 to 125 us for
 // 107 GFLOP (0.87 PFLOP/s; tensor pipe 40 % active).  The rows' threads bound it: they work 1650 of a stage's
 // 2100 cycles (350 instructions a warp, two warps a scheduler), and the products take 1140.
 #include "attn_util.cuh"
