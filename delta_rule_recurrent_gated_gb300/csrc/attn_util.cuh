@@ -11,6 +11,11 @@ namespace {
 
 constexpr float kNegInf = -INFINITY;
 constexpr int kBias = 14;  // weights as 16-bit operands reach 2^14
+// A weight w = p vs 2^(m - M + bias) is formed as p f with one factor f for a page as long as f is at most 2^100: then
+// a p below 2^-126, which ex2 gives as zero, has w below the smallest 16-bit operand.  Where the factor is larger or its
+// power of two past fp32 (value scales that are all tiny, or scores far below one whose value scale is small or zero),
+// w is taken as one power of two, 2^(s - M + bias + log2 vs).
+constexpr float kMaxFactor = 100.f;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 
 // ------------------------------------------------------------------ shares of the work

@@ -18,6 +18,8 @@
 // vs multiplies the weights.  Both references are whole numbers, so that every rescaling is exact:
 //   m >= max s, weights p = 2^(s - m), l = sum p;
 //   M >= max (s + log2 vs), w = p vs 2^(m - M + 14) <= 2^14 is the 16-bit operand.
+// Where vs 2^(m - M + 14) passes 2^100 w is taken as one power of two, 2^(s - M + 14 + log2 vs): the test for it takes
+// 1 us of 58 (64 ragged sequences of 17 to 8191 positions), in a branch for each of the two rows 2 us.
 // With PREC (fp32 queries or outputs) queries and weights are split into two 16-bit terms.
 //
 // Work is divided evenly: the stages of all tiles, each tile with a few more for its start and end,
@@ -27,7 +29,7 @@
 //
 // Bound by HBM where the cache is long: two sequences of 200001 to 262143 positions, four cache heads of 128,
 // 83 us for 474 MB (84 % of the copy rate, join and launches within it); 64 ragged sequences of 17 to 8191
-// positions 57 us for 270 MB (70 %: a tile's start and end cost as much as four stages).
+// positions 58 us for 270 MB (69 %: a tile's start and end cost as much as four stages).
 #include "attn_util.cuh"
 #include "trace.cuh"
 
@@ -254,6 +256,13 @@ __device__ __forceinline__ void load_tile(Tile<D, NT, PREC>& t, RawQ<D, NT>& raw
     }
 }
 
+// A page's weights as 2^(s - x) y: w = 2^(s - M + 14 + ve) (vs 2^-ve), where s - M + ve <= 0.
+__device__ __forceinline__ float2 weight_parts(float M, const Meta& page) {
+    int e;
+    const float y = frexpf(page.vs, &e);  // ve = e; -inf where vs = 0
+    return make_float2((M == kNegInf ? 0.f : M) - kBias - page.ve, y);
+}
+
 // One step: 32 positions from `first` on, as two halves of 16 with their pages' scales.
 // Positions from `end` on hold no value (EDGE: some are hidden from some row).  `same`: both halves
 // lie in one page.
@@ -336,8 +345,7 @@ __device__ __forceinline__ void step(Tile<D, NT, PREC>& t, const uint8_t* slot, 
                 oscale[j] = pow2i(t.M[n][j] - M);
                 t.m[n][j] = m;
                 t.M[n][j] = M;
-                // held inside the range of fp32 where a far larger value scale is past
-                t.f[n][j] = pow2i(fminf(m - M + kBias, 126.f));
+                t.f[n][j] = m - M + kBias < 128.f ? pow2i(m - M + kBias) : INFINITY;
             }
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -348,6 +356,7 @@ __device__ __forceinline__ void step(Tile<D, NT, PREC>& t, const uint8_t* slot, 
             }
         }
         float w[2][4];
+        bool apart = false;  // (an infinite factor and a scale of zero make a NaN)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float mref = t.m[n][j] == kNegInf ? 0.f : t.m[n][j];
@@ -358,6 +367,19 @@ __device__ __forceinline__ void step(Tile<D, NT, PREC>& t, const uint8_t* slot, 
                 t.l[n][j] += e0 + e1;
                 w[0][2 * i + j] = e0 * f0;
                 w[1][2 * i + j] = e1 * f1;
+            }
+            apart |= !(fmaxf(f0, f1) <= pow2i(kMaxFactor));
+        }
+        if (apart) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if (fmaxf(t.f[n][j] * m0.vs, t.f[n][j] * m1.vs) <= pow2i(kMaxFactor)) continue;
+                const float2 v0 = weight_parts(t.M[n][j], m0), v1 = weight_parts(t.M[n][j], m1);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    w[0][2 * i + j] = ex2(sc[n][0][2 * i + j] - v0.x) * v0.y;
+                    w[1][2 * i + j] = ex2(sc[n][1][2 * i + j] - v1.x) * v1.y;
+                }
             }
         }
         if constexpr (EDGE) {  // a hidden position weighs nothing even where the page's value scale is NaN

@@ -19,13 +19,14 @@
 // operand w = p vs 2^(m - M + 13).  The accumulator is rescaled (exactly, by a power of two) only when
 // a row's largest s + log2 vs passes M by more than 2.9: a row's largest operand is never below 2^12
 // nor above 2^15.9, and with scores of unit size few stages rescale (8 % of them, 63 % where M
-// follows by whole numbers).
+// follows by whole numbers).  Where vs 2^(m - M + 13) could pass 2^100, w is a power of two
+// of its own, in a copy of the loop: without the test for it 124 us instead of 126.5.
 //
 // The stages of all tiles form one line that is divided evenly among the blocks (one per SM); a tile
 // that several blocks worked on is joined by a second kernel from their rows in the workspace.
 //
-// Chunks of 512 tokens of four sequences of 4000 to 8191 positions, 16 query heads on 4 of 128: 122 to 125 us for
-// 107 GFLOP (0.87 PFLOP/s; tensor pipe 40 % active).  The rows' threads bound it: they work 1650 of a stage's
+// Chunks of 512 tokens of four sequences of 4000 to 8191 positions, 16 query heads on 4 of 128: 126 to 127 us for
+// 107 GFLOP (0.85 PFLOP/s; tensor pipe 40 % active).  The rows' threads bound it: they work 1650 of a stage's
 // 2100 cycles (350 instructions a warp, two warps a scheduler), and the products take 1140.
 #include "attn_util.cuh"
 #include "f32x2.cuh"
@@ -192,6 +193,7 @@ __device__ __forceinline__ Joint* joints(const AttnParams& p, int d) {
 struct __align__(16) StageMeta {  // read as 16-byte words
     float ks[4], vs[4], lv[4];  // of the four 16-position parts: scales, log2 vs
     int id[4];                  // their pages: -1 out of range, -2 seen by no row
+    float top;                  // largest of lv and 0
 };
 struct Control {
     uint64_t rfull[kRaw], rempty[kRaw], kfull[kKBuffers], kempty[kKBuffers], vfull[kVBuffers], vempty[kVBuffers];
@@ -327,6 +329,10 @@ __device__ __forceinline__ void copy_pages(const AttnParams& p, uint8_t* smem, C
                 m.vs[g] = now.vs;
                 m.lv[g] = now.vs == now.vs ? log2f(now.vs) : 0.f;
                 m.id[g] = now.id;
+                float top = fmaxf(m.lv[g], 0.f);
+                const unsigned four = 15u << (lane & 28);
+                top = fmaxf(top, __shfl_xor_sync(four, top, 1));
+                m.top = fmaxf(top, __shfl_xor_sync(four, top, 2));
                 if (now.id == -1) flag_index_error(p.c);
             }
             warp_arrive(&ct.rfull[buf]);
@@ -476,6 +482,53 @@ __device__ __forceinline__ void in_order(float2 (&z)[8]) {
     asm volatile("" : "+f"(z[0].x), "+f"(z[0].y), "+f"(z[1].x), "+f"(z[1].y), "+f"(z[2].x), "+f"(z[2].y), "+f"(z[3].x), "+f"(z[3].y),
                  "+f"(z[4].x), "+f"(z[4].y), "+f"(z[5].x), "+f"(z[5].y), "+f"(z[6].x), "+f"(z[6].y), "+f"(z[7].x), "+f"(z[7].y));
 }
+// The weights of the 64 positions of a stage, to tensor memory as 16-bit operands, and their sum:
+// p = 2^(x kf - mref), w = p (2^(m - M + 13) vs).  APART: the rows that
+// are `mine` take w as a power of two of its own, 2^(x kf - M + 13 + log2 vs).
+template <bool APART>
+__device__ __forceinline__ void weigh(uint32_t ts, const float (&x)[4][16], const float (&kf)[4], const float (&vs)[4],
+                                      const StageMeta& mt, float mref, float m, float M, bool mine, float2& l2, float2& l3) {
+    const float fm = pow2i(m - M + kTcBias), up = M == kNegInf ? 0.f : kTcBias - M;
+    const float2 nm = make_float2(-mref, -mref);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+        const float2 f = make_float2(fm * vs[g], fm * vs[g]), k2 = make_float2(kf[g], kf[g]);
+        float2 z[8];
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = fma2(make_float2(x[g][2 * j], x[g][2 * j + 1]), k2, nm);
+        in_order(z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = make_float2(ex2(z[j].x), ex2(z[j].y));
+        in_order(z);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            l2 = add2(l2, z[j]);
+            z[j] = mul2(z[j], f);
+            l3 = add2(l3, z[j + 1]);
+            z[j + 1] = mul2(z[j + 1], f);
+        }
+        in_order(z);
+        if (APART && mine) {
+            const float one = vs[g] == vs[g] ? 1.f : vs[g];  // a NaN marks the page
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                z[j] = make_float2(ex2(fmaf(x[g][2 * j], kf[g], up + mt.lv[g])) * one,
+                                   ex2(fmaf(x[g][2 * j + 1], kf[g], up + mt.lv[g])) * one);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __uint_as_float(pack_half(z[j].x, z[j].y));
+        __syncwarp();
+        tmem_st8(ts + 8 * g, w);
+    }
+}
+// A row's result is its sum times 2^f / l: as two factors, which stay normal numbers where the result is not.
+__device__ __forceinline__ float2 row_factors(float f, float l, float M) {
+    if (M == kNegInf) return make_float2(l == l ? 0.f : l, 1.f);
+    f = fminf(fmaxf(f, -250.f), 250.f);
+    const float half = truncf(0.5f * f);
+    return make_float2(pow2i(half) / l, pow2i(f - half));
+}
 template <int D, bool E4M3>
 __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, Control& ct, Walk walk) {
     const int hf = threadIdx.x / kHalf, r = threadIdx.x % kHalf, lane = threadIdx.x & 31;
@@ -610,9 +663,13 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
             l *= pow2i(m - m2);
             m = m2;
             const bool grow = need > M + kSlack;
-            if (__any_sync(0xffffffffu, grow)) {
+            // 2^(m - M + 13) vs of the stage's largest vs (or of 1): too large before M grows, and after it?
+            const float most = kMaxFactor - kTcBias - mt.top;
+            bool apart = false;
+            if (__any_sync(0xffffffffu, grow || m - M > most)) {
                 const float up2 = ceilf(need), f = grow ? pow2i(M - up2) : 1.f;
                 if (grow) M = up2;
+                apart = __any_sync(0xffffffffu, m - M > most);
                 if (i > 0) {
                     // O has the product of the stage before
                     if (!wait(ct, &ct.odone[(n - 1) & 1], ((n - 1) >> 1) & 1)) return;
@@ -634,33 +691,10 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
                     }
                 }
             }
-            const float mref = m == kNegInf ? 0.f : m, fm = pow2i(fminf(m - M + kTcBias, 126.f));
+            const float mref = m == kNegInf ? 0.f : m;
             float2 l2 = make_float2(0.f, 0.f), l3 = l2;
-            const float2 nm = make_float2(-mref, -mref);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const float2 f = make_float2(fm * vs[g], fm * vs[g]), k2 = make_float2(kf[g], kf[g]);
-                float2 z[8];
-                float w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = fma2(make_float2(x[g][2 * j], x[g][2 * j + 1]), k2, nm);
-                in_order(z);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) z[j] = make_float2(ex2(z[j].x), ex2(z[j].y));
-                in_order(z);
-#pragma unroll
-                for (int j = 0; j < 8; j += 2) {
-                    l2 = add2(l2, z[j]);
-                    z[j] = mul2(z[j], f);
-                    l3 = add2(l3, z[j + 1]);
-                    z[j + 1] = mul2(z[j + 1], f);
-                }
-                in_order(z);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = __uint_as_float(pack_half(z[j].x, z[j].y));
-                __syncwarp();
-                tmem_st8(ts + 8 * g, w);
-            }
+            if (!apart) weigh<false>(ts, x, kf, vs, mt, mref, m, M, false, l2, l3);
+            else weigh<true>(ts, x, kf, vs, mt, mref, m, M, m - M > most, l2, l3);
             l2 = add2(l2, l3);
             l += l2.x + l2.y;
             tmem_st_wait();
@@ -673,8 +707,8 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
         const int rr = hf * kHalf + r;
         float* part = p.part + ((size_t)blockIdx.x * 2 + (s.first ? 0 : 1)) * tile_floats(D, kRows);
         const size_t at = ((size_t)s.b * p.c.T + tok) * p.Hq + head;
-        const float f = M - m - kTcBias;  // sums are in units of 2^(M - 13), l in units of 2^m
-        const float inv = M == kNegInf ? (l == l ? 0.f : l) : ldexpf(1.f / l, (int)fminf(fmaxf(f, -140.f), 120.f));
+        // sums are in units of 2^(M - 13), l in units of 2^m
+        const float2 inv = row_factors(M - m - kTcBias, l, M);
 #pragma unroll 2
         for (int j = 0; j < D; j += 16) {
             float y[16];
@@ -690,11 +724,13 @@ __device__ __forceinline__ void soften_rows(const AttnParams& p, uint8_t* smem, 
                 }
             }
             if (on && s.whole) {
+#pragma unroll
+                for (int q = 0; q < 16; ++q) y[q] = y[q] * inv.x * inv.y;
                 uint4 u[2];
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
-                    u[q] = make_uint4(pack_bf16(y[8 * q] * inv, y[8 * q + 1] * inv), pack_bf16(y[8 * q + 2] * inv, y[8 * q + 3] * inv),
-                                      pack_bf16(y[8 * q + 4] * inv, y[8 * q + 5] * inv), pack_bf16(y[8 * q + 6] * inv, y[8 * q + 7] * inv));
+                    u[q] = make_uint4(pack_bf16(y[8 * q], y[8 * q + 1]), pack_bf16(y[8 * q + 2], y[8 * q + 3]),
+                                      pack_bf16(y[8 * q + 4], y[8 * q + 5]), pack_bf16(y[8 * q + 6], y[8 * q + 7]));
                 uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + j);
                 o[0] = u[0];
                 o[1] = u[1];
@@ -832,15 +868,17 @@ __global__ void __launch_bounds__(256) cache_attn_tc_join_kernel(const AttnParam
         m = m2;
         M = M2;
     }
-    const float f = M - m - kBias;
-    const float inv = M == kNegInf ? (l == l ? 0.f : l) : ldexpf(1.f / l, (int)fminf(fmaxf(f, -140.f), 120.f));
+    const float2 inv = row_factors(M - m - kBias, l, M);
     const size_t at = ((size_t)b * p.c.T + row / p.G) * p.Hq + h * p.G + row % p.G;
     uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D + ch0);
 #pragma unroll
+    for (int j = 0; j < V; ++j)
+        sum[j] = make_float4(sum[j].x * inv.x * inv.y, sum[j].y * inv.x * inv.y, sum[j].z * inv.x * inv.y, sum[j].w * inv.x * inv.y);
+#pragma unroll
     for (int j = 0; j < V; j += 2) {
-        const uint4 u = make_uint4(pack_bf16(sum[j].x * inv, sum[j].y * inv), pack_bf16(sum[j].z * inv, sum[j].w * inv),
-                                   pack_bf16(sum[j + 1].x * inv, sum[j + 1].y * inv),
-                                   pack_bf16(sum[j + 1].z * inv, sum[j + 1].w * inv));
+        const uint4 u = make_uint4(pack_bf16(sum[j].x, sum[j].y), pack_bf16(sum[j].z, sum[j].w),
+                                   pack_bf16(sum[j + 1].x, sum[j + 1].y),
+                                   pack_bf16(sum[j + 1].z, sum[j + 1].w));
         *reinterpret_cast<uint4*>(o + j) = u;
     }
     if (warp == 0 && p.lse) p.lse[at] = (m + log2f(l)) * kLn2;
