@@ -110,7 +110,8 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int b, int h, int
     float y = sum / l;
     if (f > 100.f || f < -100.f) { y = ldexpf(y, (int)fminf(fmaxf(f, -400.f), 400.f)); }
     else y *= pow2i(f);
-    if (M == kNegInf && sum == 0.f) y = l == l ? 0.f : sum / l;  // every value scale is zero
+    // every value scale is zero; without weights (every score is -inf: a row sees at least its own position) 0 / 0
+    if (M == kNegInf && sum == 0.f && l > 0.f) y = 0.f;
     st_any(p.o, at * d + ch, p.out, y);
     if (ch == 0 && p.lse) p.lse[at] = (m + log2f(l)) * kLn2;
 }

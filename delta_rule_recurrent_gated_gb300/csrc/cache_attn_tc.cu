@@ -524,7 +524,7 @@ __device__ __forceinline__ void weigh(uint32_t ts, const float (&x)[4][16], cons
 }
 // A row's result is its sum times 2^f / l: as two factors, which stay normal numbers where the result is not.
 __device__ __forceinline__ float2 row_factors(float f, float l, float M) {
-    if (M == kNegInf) return make_float2(l == l ? 0.f : l, 1.f);
+    if (M == kNegInf) return make_float2(l > 0.f ? 0.f : 0.f / l, 1.f);  // no value scale but zeros; no weights
     f = fminf(fmaxf(f, -250.f), 250.f);
     const float half = truncf(0.5f * f);
     return make_float2(pow2i(half) / l, pow2i(f - half));

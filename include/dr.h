@@ -398,7 +398,8 @@ int dr_cache_read(const dr_cache* cache, const dr_cache_seqs* seqs, void* k, voi
  *   s_j = scale * sum_c q_c k_jc;  o = sum_j e^{s_j} v_j / sum_j e^{s_j};
  *   lse = ln sum_j e^{s_j}
  * Tokens t >= n_b: o = 0, lse = -inf.  Where a sequence's length, count or a page number that
- * a token needs is out of range, its o and lse are NaN.
+ * a token needs is out of range, its o and lse are NaN.  A query that is not finite makes its
+ * own o NaN (also where all its scores are -inf, then with lse = -inf).
  * q: [B*T] rows of Hq*d, ld_q elements apart (io dtype); o [B, T, Hq, d] (out dtype); lse
  *   [B, T, Hq] fp32 or NULL.
  * Arithmetic: 16-bit floating-point operands that hold the codes and bf16 queries exactly and

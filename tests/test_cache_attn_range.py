@@ -83,3 +83,19 @@ def test_pages_without_values_that_hold_the_top_score(kind, gap, order):
     c.cache.k.view(torch.int8).copy_(torch.from_numpy(codes.view(np.int8)))
     assert c.cache.k.dtype == kind_of
     check(c, *c.run())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_row_whose_every_score_is_minus_infinity_is_not_a_number(kind):
+    """e^-inf / e^-inf: an infinite query is no row without positions, and must not come out as zeros."""
+    c = Case(*kind, seed=43)
+    codes = c.codes[0]
+    codes[..., 0] = 0xff if c.code == "i8" else 0xb8  # -1
+    c.cache.k.view(torch.int8).copy_(torch.from_numpy(codes.view(np.int8)))
+    good, lse = c.run()
+    q = c.q.clone()
+    q[0, 0, 1, 0] = float("inf")
+    o, b = c.run(q)
+    assert o[0, 0, 1].isnan().all() and b[0, 0, 1].isneginf()
+    o[0, 0, 1], b[0, 0, 1] = good[0, 0, 1], lse[0, 0, 1]
+    assert torch.equal(o, good) and torch.equal(b, lse)
