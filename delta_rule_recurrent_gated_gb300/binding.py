@@ -512,6 +512,7 @@ class HeadNormRope(_Calls):
         e.ld_k = e.ld_ok = Hk * d
         e.table_rows = 0
         self.desc, self._ref = e, ctypes.byref(e)
+        self._layouts = {}
         self.io_dtype, self.out_dtype, self.grad_dtype = map(_torch_type, (io, out, grad))
         self._q, self._k, self._w, self._rot = (B, T, Hq, d), (B, T, Hk, d), (d,), e.rot
         self._fwd, self._bwd = self._lib.dr_norm_rope_fwd, self._lib.dr_norm_rope_bwd
@@ -519,26 +520,38 @@ class HeadNormRope(_Calls):
         if int(self._lib.dr_norm_rope_workspace_bytes(self._ref)) == 0:
             raise DrError(DR_ERR_UNSUPPORTED, "dr_norm_rope_workspace_bytes")
 
-    def _inputs(self, q, k, wq, wk, cos, sin, positions, start):
-        """Checks the inputs of a call, notes what the descriptor has of them, and returns their addresses."""
+    def _layout(self, ld_q, ld_k, ld_oq, ld_ok, table_rows):
+        """The descriptor of calls with these row distances and rows of the tables.  It is not changed
+        afterwards: the library reads it while other threads call."""
+        key = (ld_q, ld_k, ld_oq, ld_ok, table_rows)
+        ref = self._layouts.get(key)
+        if ref is None:
+            e = DrRopeDesc.from_buffer_copy(self.desc)
+            e.ld_q, e.ld_k, e.ld_oq, e.ld_ok, e.table_rows = key
+            ref = self._layouts[key] = ctypes.byref(e)
+        return ref
+
+    def _inputs(self, q, k, wq, wk, cos, sin, positions, start, ld_oq, ld_ok):
+        """Checks the inputs of a call, and returns its descriptor and their addresses."""
         e, f32, i32, w = self.desc, self._f32, self._i32, self._w
         qp = kp = None
+        ld_q, ld_k, rows = e.ld_q, e.ld_k, 0
         if self._q[2]:
             if q.dtype is not self.io_dtype:
                 raise ValueError(f"q: expected {self.io_dtype}, got {q.dtype}")
-            e.ld_q, qp = _rows(q, self._q, "q"), q.data_ptr()
+            ld_q, qp = _rows(q, self._q, "q"), q.data_ptr()
         if self._k[2]:
             if k.dtype is not self.io_dtype:
                 raise ValueError(f"k: expected {self.io_dtype}, got {k.dtype}")
-            e.ld_k, kp = _rows(k, self._k, "k"), k.data_ptr()
+            ld_k, kp = _rows(k, self._k, "k"), k.data_ptr()
         wqp, wkp = _address(wq, f32, w, "wq"), _address(wk, f32, w, "wk")
         cp = sp = None
         if self._rot:
-            table = (cos.shape[0], self._rot // 2)
+            rows = cos.shape[0]
+            table = (rows, self._rot // 2)
             cp, sp = _address(cos, f32, table, "cos"), _address(sin, f32, table, "sin")
-            e.table_rows = table[0]
-        return (qp, kp, wqp, wkp, cp, sp, _address(positions, i32, self._q[:2], "positions"),
-                _address(start, i32, self._q[:1], "start"))
+        return (self._layout(ld_q, ld_k, ld_oq, ld_ok, rows), qp, kp, wqp, wkp, cp, sp,
+                _address(positions, i32, self._q[:2], "positions"), _address(start, i32, self._q[:1], "start"))
 
     def _output(self, t, shape, dtype, what):
         """A given output, or a new one, and its row distance."""
@@ -550,10 +563,9 @@ class HeadNormRope(_Calls):
 
     def forward(self, q, k, wq, wk, cos, sin, positions=None, start=None, yq=None, yk=None):
         """yq, yk in the output type (given: written there, in place where it is q or k itself)."""
-        e = self.desc
-        yq, e.ld_oq = self._output(yq, self._q, self.out_dtype, "yq")
-        yk, e.ld_ok = self._output(yk, self._k, self.out_dtype, "yk")
-        rc = self._fwd(self._ref, *self._inputs(q, k, wq, wk, cos, sin, positions, start), yq.data_ptr(),
+        yq, ld_oq = self._output(yq, self._q, self.out_dtype, "yq")
+        yk, ld_ok = self._output(yk, self._k, self.out_dtype, "yk")
+        rc = self._fwd(*self._inputs(q, k, wq, wk, cos, sin, positions, start, ld_oq, ld_ok), yq.data_ptr(),
                        yk.data_ptr(), self._stream())
         if rc:
             raise DrError(rc, "dr_norm_rope_fwd")
@@ -561,10 +573,10 @@ class HeadNormRope(_Calls):
 
     def backward(self, q, k, wq, wk, cos, sin, dyq, dyk, positions=None, start=None, out=None):
         """{dq, dk, dwq, dwk} for the incoming gradients dyq, dyk (contiguous, of the input type)."""
-        e, w, f32 = self.desc, self._w, self._f32
+        w, f32 = self._w, self._f32
         given = out or {}
-        dq, e.ld_oq = self._output(given.get("dq"), self._q, self.grad_dtype, "dq")
-        dk, e.ld_ok = self._output(given.get("dk"), self._k, self.grad_dtype, "dk")
+        dq, ld_oq = self._output(given.get("dq"), self._q, self.grad_dtype, "dq")
+        dk, ld_ok = self._output(given.get("dk"), self._k, self.grad_dtype, "dk")
         dwq, dwk = given.get("dwq"), given.get("dwk")
         if out is None:
             empty, device = self._torch.empty, self.device
@@ -572,7 +584,7 @@ class HeadNormRope(_Calls):
             dwk = None if wk is None else empty(w, dtype=f32, device=device)
         if self.ws is None:
             self.ws = self._empty(int(self._lib.dr_norm_rope_workspace_bytes(self._ref)), self._torch.uint8)
-        rc = self._bwd(self._ref, *self._inputs(q, k, wq, wk, cos, sin, positions, start),
+        rc = self._bwd(*self._inputs(q, k, wq, wk, cos, sin, positions, start, ld_oq, ld_ok),
                        _address(dyq, self.io_dtype, self._q, "dyq"), _address(dyk, self.io_dtype, self._k, "dyk"),
                        dq.data_ptr(), dk.data_ptr(), _address(dwq, f32, w, "dwq"), _address(dwk, f32, w, "dwk"),
                        self.ws.data_ptr(), self.ws.numel(), self._stream())
@@ -666,6 +678,7 @@ class CacheAttention(_Calls):
         a = DrAttnDesc(Hq, _TYPE_CODES[io], _TYPE_CODES[out], window,
                        d ** -0.5 if scale is None else float(scale), Hq * d)
         self.desc, self._ref = a, ctypes.byref(a)
+        self._layouts = {a.ld_q: self._ref}  # descriptors by row distance, not changed afterwards
         self.io_dtype, self.out_dtype = _torch_type(io), _torch_type(out)
         self._shape = (B, T, Hq, d)
         n = int(self._lib.dr_cache_attn_workspace_bytes(cache._ref, self._ref, B, T))
@@ -680,12 +693,17 @@ class CacheAttention(_Calls):
         shape, cache = self._shape, self.cache
         if q.dtype is not self.io_dtype:
             raise ValueError(f"q: expected {self.io_dtype}, got {q.dtype}")
-        self.desc.ld_q = _rows(q, shape, "q")
+        ld_q = _rows(q, shape, "q")
+        ref = self._layouts.get(ld_q)
+        if ref is None:
+            a = DrAttnDesc.from_buffer_copy(self.desc)
+            a.ld_q = ld_q
+            ref = self._layouts[ld_q] = ctypes.byref(a)
         s = cache.seqs(self.B, table, lens, counts, self.T)
         empty, device = self._torch.empty, self.device
         o = empty(shape, dtype=self.out_dtype, device=device) if o is None else o
         lse = empty(shape[:3], dtype=self._f32, device=device) if lse is None and want_lse else lse
-        rc = self._attn(cache._ref, ctypes.byref(s), self._ref, q.data_ptr(),
+        rc = self._attn(cache._ref, ctypes.byref(s), ref, q.data_ptr(),
                         _address(o, self.out_dtype, shape, "o"), _address(lse, self._f32, shape[:3], "lse"),
                         self._ws, self._ws_bytes, self._stream())
         if rc:

@@ -1,0 +1,115 @@
+"""Plans of the attention layer on the host: what a call hands to the library, with the library's entry points
+replaced by recorders and CPU tensors that stand for device memory (no GPU: nothing is launched)."""
+import threading
+
+import pytest
+import torch
+
+from delta_rule_recurrent_gated_gb300 import binding as B
+
+
+class OnDevice(torch.Tensor):
+    """A CPU tensor that says it lies in the memory of device `index`."""
+    index = 0
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.index
+
+
+def dev(t, index=0):
+    t = t.as_subclass(OnDevice)
+    t.index = index
+    return t
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    from delta_rule_recurrent_gated_gb300 import build
+    build.build()
+    return B.load()
+
+
+def here(plan, stream=7):
+    """A plan of the CPU as one of device 0, on a stream of the test's."""
+    plan._index, plan._stream = 0, lambda: stream
+    return plan
+
+
+def norm(T=3, Hq=4, Hk=2, d=64):
+    return here(B.HeadNormRope(2, T, Hq, Hk, d, device="cpu"))
+
+
+def packed(heads, T=3, d=64, width=8):
+    return dev(torch.zeros(2, T, width, d, dtype=torch.bfloat16)[:, :, :heads])
+
+
+def plain(heads, T=3, d=64):
+    return dev(torch.zeros(2, T, heads, d, dtype=torch.bfloat16))
+
+
+def tables(rows, d=64):
+    return [dev(torch.zeros(rows, d // 2)) for _ in range(2)]
+
+
+def cache():
+    kinds = [torch.zeros(8, 2, 16, 64, dtype=torch.int8) for _ in range(2)] + [torch.zeros(8, 2) for _ in range(2)]
+    return here(B.KvCache(8, 2, 64, page=16, buffers=[dev(t) for t in kinds], device="cpu"))
+
+
+def places():
+    return dev(torch.zeros(2, 4, dtype=torch.int32)), dev(torch.zeros(2, dtype=torch.int32))
+
+
+def in_a_thread(f):
+    out = []
+    t = threading.Thread(target=lambda: out.append(f()))
+    t.start()
+    t.join(30)
+    assert out, "the other thread's call did not return"
+
+
+def test_two_threads_hand_over_their_own_layouts():
+    """A call that another thread's comes between (the library is called without the interpreter's lock)."""
+    p, seen = norm(), []
+
+    def entry(ref, *rest):
+        d = ref._obj
+        if not seen:
+            seen.append(None)
+            in_a_thread(lambda: p.forward(packed(4), packed(2, width=6), None, None, *tables(9)))
+        seen.append((d.ld_q, d.ld_k, d.ld_oq, d.ld_ok, d.table_rows))
+        return 0
+
+    p._fwd = entry
+    p.forward(plain(4), plain(2), None, None, *tables(5), yq=packed(4, width=5))
+    assert seen[1:] == [(512, 384, 256, 128, 9), (256, 128, 320, 128, 5)]
+
+    p, seen = norm(), []
+
+    def entry(ref, *rest):  # noqa: F811
+        d = ref._obj
+        if not seen:
+            seen.append(None)
+            in_a_thread(lambda: p.forward(packed(4), packed(2, width=6), None, None, *tables(9)))
+        seen.append((d.ld_q, d.ld_k, d.ld_oq, d.ld_ok, d.table_rows))
+        return 0
+
+    p._bwd = p._fwd = entry
+    p.backward(plain(4), plain(2), None, None, *tables(5), plain(4), plain(2))
+    assert seen[1:] == [(512, 384, 256, 128, 9), (256, 128, 256, 128, 5)]
+
+
+def test_two_threads_hand_over_their_own_queries():
+    a, seen = here(B.CacheAttention(cache(), 2, 3, 4)), []
+
+    def entry(c, s, ref, *rest):
+        if not seen:
+            seen.append(None)
+            in_a_thread(lambda: a.forward(packed(4), *places(), o=plain(4)))
+        seen.append(ref._obj.ld_q)
+        return 0
+
+    a._attn = entry
+    a.forward(plain(4), *places(), o=plain(4))
+    assert seen[1:] == [512, 256]
