@@ -113,3 +113,17 @@ def test_two_threads_hand_over_their_own_queries():
     a._attn = entry
     a.forward(plain(4), *places(), o=plain(4))
     assert seen[1:] == [512, 256]
+
+
+def test_a_refused_call_leaves_the_gradient_its_workspace():
+    """A row distance that the library refuses is that call's alone."""
+    p, got = norm(), []
+    wide = dev(torch.zeros(2 * 3 * 258 + 8, dtype=torch.bfloat16).as_strided((2, 3, 4, 64), (3 * 258, 258, 64, 1)))
+    with pytest.raises(B.DrError) as e:
+        p.forward(wide, plain(2), None, None, *tables(5))
+    assert e.value.code == B.DR_ERR_ALIGNMENT
+    need = int(B.load().dr_norm_rope_workspace_bytes(norm()._ref))
+    p._bwd = lambda *a: got.append(a[-3:-1]) or 0
+    p.backward(plain(4), plain(2), None, None, *tables(5), plain(4), plain(2))
+    (address, size), = got
+    assert need > 0 and size == need and address
