@@ -434,10 +434,10 @@ class Gdn2Problem(Problem):
 # ------------------------------------------------------------------ softmax-attention layer
 # A step of a serving loop makes these calls for a few microseconds of work on the device, so the
 # argument checks compare whole shapes and ask for strides only where a tensor is not contiguous.
-def _rows(t, shape, what):
-    """Elements between the token rows of t, a tensor of the given shape [B, T, heads, d]:
+def _rows(t, shape, what, index):
+    """Elements between the token rows of t, a tensor of the given shape [B, T, heads, d] on device `index`:
     contiguous, or a range of heads of a wider contiguous tensor."""
-    if t.shape == shape and t.is_cuda:
+    if t.shape == shape and t.get_device() == index:
         B, T, H, D = shape
         if t.is_contiguous():
             return H * D
@@ -446,16 +446,16 @@ def _rows(t, shape, what):
         if (D == 1 or s[3] == 1) and (H == 1 or s[2] == D) and (T == 1 or B == 1 or s[0] == T * ld):
             return ld if B * T > 1 else H * D
     raise ValueError(f"{what}: shape {tuple(t.shape)} strides {t.stride()} on {t.device} is no {tuple(shape)} "
-                     "in device memory with whole token rows at one distance")
+                     f"in the memory of device {index} with whole token rows at one distance")
 
 
-def _address(t, dtype, shape, what):
-    """Address of a contiguous tensor of the given type and shape, or None."""
+def _address(t, dtype, shape, what, index):
+    """Address of a contiguous tensor of the given type and shape on device `index`, or None."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)} in device "
-                         f"memory, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{what}: expected a contiguous {dtype} tensor of shape {tuple(shape)} in the memory of "
+                         f"device {index}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
@@ -483,8 +483,13 @@ class _Calls:
         self._raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if self._raw is None or self._index is None:
             self._raw = lambda _: torch.cuda.current_stream(self.device).cuda_stream
+        self._current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
     def _stream(self):
+        """The current stream of the plan's device, which has to be the current one: a launch goes to the current
+        device, and the default stream has the same handle on each."""
+        if self._current() != self._index:
+            raise ValueError(f"a plan of device {self._index} was called while device {self._current()} is the current one")
         return self._raw(self._index)
 
     def _empty(self, shape, dtype):
@@ -533,25 +538,26 @@ class HeadNormRope(_Calls):
 
     def _inputs(self, q, k, wq, wk, cos, sin, positions, start, ld_oq, ld_ok):
         """Checks the inputs of a call, and returns its descriptor and their addresses."""
-        e, f32, i32, w = self.desc, self._f32, self._i32, self._w
+        e, f32, i32, w, index = self.desc, self._f32, self._i32, self._w, self._index
         qp = kp = None
         ld_q, ld_k, rows = e.ld_q, e.ld_k, 0
         if self._q[2]:
             if q.dtype is not self.io_dtype:
                 raise ValueError(f"q: expected {self.io_dtype}, got {q.dtype}")
-            ld_q, qp = _rows(q, self._q, "q"), q.data_ptr()
+            ld_q, qp = _rows(q, self._q, "q", index), q.data_ptr()
         if self._k[2]:
             if k.dtype is not self.io_dtype:
                 raise ValueError(f"k: expected {self.io_dtype}, got {k.dtype}")
-            ld_k, kp = _rows(k, self._k, "k"), k.data_ptr()
-        wqp, wkp = _address(wq, f32, w, "wq"), _address(wk, f32, w, "wk")
+            ld_k, kp = _rows(k, self._k, "k", index), k.data_ptr()
+        wqp, wkp = _address(wq, f32, w, "wq", index), _address(wk, f32, w, "wk", index)
         cp = sp = None
         if self._rot:
             rows = cos.shape[0]
             table = (rows, self._rot // 2)
-            cp, sp = _address(cos, f32, table, "cos"), _address(sin, f32, table, "sin")
+            cp, sp = _address(cos, f32, table, "cos", index), _address(sin, f32, table, "sin", index)
         return (self._layout(ld_q, ld_k, ld_oq, ld_ok, rows), qp, kp, wqp, wkp, cp, sp,
-                _address(positions, i32, self._q[:2], "positions"), _address(start, i32, self._q[:1], "start"))
+                _address(positions, i32, self._q[:2], "positions", index),
+                _address(start, i32, self._q[:1], "start", index))
 
     def _output(self, t, shape, dtype, what):
         """A given output, or a new one, and its row distance."""
@@ -559,7 +565,7 @@ class HeadNormRope(_Calls):
             return self._torch.empty(shape, dtype=dtype, device=self.device), shape[2] * shape[3]
         if t.dtype is not dtype:
             raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-        return t, _rows(t, shape, what)
+        return t, _rows(t, shape, what, self._index)
 
     def forward(self, q, k, wq, wk, cos, sin, positions=None, start=None, yq=None, yk=None):
         """yq, yk in the output type (given: written there, in place where it is q or k itself)."""
@@ -573,7 +579,7 @@ class HeadNormRope(_Calls):
 
     def backward(self, q, k, wq, wk, cos, sin, dyq, dyk, positions=None, start=None, out=None):
         """{dq, dk, dwq, dwk} for the incoming gradients dyq, dyk (contiguous, of the input type)."""
-        w, f32 = self._w, self._f32
+        w, f32, index = self._w, self._f32, self._index
         given = out or {}
         dq, ld_oq = self._output(given.get("dq"), self._q, self.grad_dtype, "dq")
         dk, ld_ok = self._output(given.get("dk"), self._k, self.grad_dtype, "dk")
@@ -585,8 +591,9 @@ class HeadNormRope(_Calls):
         if self.ws is None:
             self.ws = self._empty(int(self._lib.dr_norm_rope_workspace_bytes(self._ref)), self._torch.uint8)
         rc = self._bwd(*self._inputs(q, k, wq, wk, cos, sin, positions, start, ld_oq, ld_ok),
-                       _address(dyq, self.io_dtype, self._q, "dyq"), _address(dyk, self.io_dtype, self._k, "dyk"),
-                       dq.data_ptr(), dk.data_ptr(), _address(dwq, f32, w, "dwq"), _address(dwk, f32, w, "dwk"),
+                       _address(dyq, self.io_dtype, self._q, "dyq", index),
+                       _address(dyk, self.io_dtype, self._k, "dyk", index), dq.data_ptr(), dk.data_ptr(),
+                       _address(dwq, f32, w, "dwq", index), _address(dwk, f32, w, "dwk", index),
                        self.ws.data_ptr(), self.ws.numel(), self._stream())
         if rc:
             raise DrError(rc, "dr_norm_rope_bwd")
@@ -609,9 +616,9 @@ class KvCache(_Calls):
             buffers += [torch.zeros(num_pages, H, dtype=torch.float32, device=self.device) for _ in range(2)]
         self.k, self.v, self.k_scale, self.v_scale = buffers
         for t, what in ((self.k, "k codes"), (self.v, "v codes")):
-            _address(t, kind, (num_pages, H, page, d), what)
+            _address(t, kind, (num_pages, H, page, d), what, self._index)
         for t, what in ((self.k_scale, "k scales"), (self.v_scale, "v scales")):
-            _address(t, torch.float32, (num_pages, H), what)
+            _address(t, torch.float32, (num_pages, H), what, self._index)
         self.word = torch.zeros(4, dtype=torch.int32, device=self.device)
         c = DrCache()
         c.num_pages, c.H, c.d, c.page, c.code = num_pages, H, d, page, CACHE_CODES[code]
@@ -627,9 +634,9 @@ class KvCache(_Calls):
     def seqs(self, B, table, lens, counts, T):
         """The call's positions: T tokens (or counts[b] <= T) after lens[b], in the pages of table
         [B, pages]."""
-        i32, pages = self._i32, table.shape[-1]
-        return DrCacheSeqs(B, T, _address(table, i32, (B, pages), "table"), pages,
-                           _address(lens, i32, (B,), "lens"), _address(counts, i32, (B,), "counts"))
+        i32, pages, index = self._i32, table.shape[-1], self._index
+        return DrCacheSeqs(B, T, _address(table, i32, (B, pages), "table", index), pages,
+                           _address(lens, i32, (B,), "lens", index), _address(counts, i32, (B,), "counts", index))
 
     def write(self, k, v, table, lens, counts=None):
         """Append k, v [B, T, H, d] (bf16 or fp32, or head ranges of a packed projection) after the
@@ -638,10 +645,10 @@ class KvCache(_Calls):
         if code is None or v.dtype is not k.dtype:
             raise ValueError("k, v: expected two bf16 or two fp32 tensors")
         B, T = k.shape[:2]
-        shape = (B, T, *self._heads)
+        shape, index = (B, T, *self._heads), self._index
         s = self.seqs(B, table, lens, counts, T)
-        rc = self._write(self._ref, ctypes.byref(s), k.data_ptr(), _rows(k, shape, "k"), v.data_ptr(),
-                         _rows(v, shape, "v"), code, self._stream())
+        rc = self._write(self._ref, ctypes.byref(s), k.data_ptr(), _rows(k, shape, "k", index), v.data_ptr(),
+                         _rows(v, shape, "v", index), code, self._stream())
         if rc:
             raise DrError(rc, "dr_cache_write")
 
@@ -650,12 +657,12 @@ class KvCache(_Calls):
         dtype, code = self._out[out]
         B = lens.shape[0]
         s = self.seqs(B, table, lens, counts, T)
-        shape = (B, T, *self._heads)
+        shape, index = (B, T, *self._heads), self._index
         empty, device = self._torch.empty, self.device
         k = empty(shape, dtype=dtype, device=device) if k is None else k
         v = empty(shape, dtype=dtype, device=device) if v is None else v
-        rc = self._read(self._ref, ctypes.byref(s), _address(k, dtype, shape, "k"), _address(v, dtype, shape, "v"),
-                        code, self._stream())
+        rc = self._read(self._ref, ctypes.byref(s), _address(k, dtype, shape, "k", index),
+                        _address(v, dtype, shape, "v", index), code, self._stream())
         if rc:
             raise DrError(rc, "dr_cache_read")
         return k, v
@@ -690,10 +697,10 @@ class CacheAttention(_Calls):
     def forward(self, q, table, lens, counts=None, o=None, lse=None, want_lse=False):
         """o [B, T, Hq, d] and lse [B, T, Hq] (or None): query t of sequence b is the position
         lens[b] + t, which the cache already holds."""
-        shape, cache = self._shape, self.cache
+        shape, cache, index = self._shape, self.cache, self._index
         if q.dtype is not self.io_dtype:
             raise ValueError(f"q: expected {self.io_dtype}, got {q.dtype}")
-        ld_q = _rows(q, shape, "q")
+        ld_q = _rows(q, shape, "q", index)
         ref = self._layouts.get(ld_q)
         if ref is None:
             a = DrAttnDesc.from_buffer_copy(self.desc)
@@ -704,7 +711,7 @@ class CacheAttention(_Calls):
         o = empty(shape, dtype=self.out_dtype, device=device) if o is None else o
         lse = empty(shape[:3], dtype=self._f32, device=device) if lse is None and want_lse else lse
         rc = self._attn(cache._ref, ctypes.byref(s), ref, q.data_ptr(),
-                        _address(o, self.out_dtype, shape, "o"), _address(lse, self._f32, shape[:3], "lse"),
+                        _address(o, self.out_dtype, shape, "o", index), _address(lse, self._f32, shape[:3], "lse", index),
                         self._ws, self._ws_bytes, self._stream())
         if rc:
             raise DrError(rc, "dr_cache_attn")

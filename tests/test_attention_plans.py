@@ -52,9 +52,18 @@ def tables(rows, d=64):
     return [dev(torch.zeros(rows, d // 2)) for _ in range(2)]
 
 
-def cache():
+class Cache(B.KvCache):
+    """A cache of the CPU as one of device 0."""
+
+    def _at(self, device):
+        super()._at(device)
+        here(self)
+
+
+def cache(other=None):
+    """`other`: the buffer that lies on another device."""
     kinds = [torch.zeros(8, 2, 16, 64, dtype=torch.int8) for _ in range(2)] + [torch.zeros(8, 2) for _ in range(2)]
-    return here(B.KvCache(8, 2, 64, page=16, buffers=[dev(t) for t in kinds], device="cpu"))
+    return Cache(8, 2, 64, page=16, buffers=[dev(t, int(i == other)) for i, t in enumerate(kinds)], device="cpu")
 
 
 def places():
@@ -127,3 +136,59 @@ def test_a_refused_call_leaves_the_gradient_its_workspace():
     p.backward(plain(4), plain(2), None, None, *tables(5), plain(4), plain(2))
     (address, size), = got
     assert need > 0 and size == need and address
+
+
+def test_tensors_of_another_device_are_refused():
+    p, c = norm(), cache()
+    a = here(B.CacheAttention(c, 2, 3, 4))
+    ran = []
+    p._fwd = p._bwd = a._attn = c._write = c._read = lambda *x: ran.append(x) or 0
+    good = [plain(4), plain(2), dev(torch.zeros(64)), dev(torch.zeros(64)), *tables(5)]
+    outs = dict(yq=plain(4), yk=plain(2), positions=dev(torch.zeros(2, 3, dtype=torch.int32)), start=places()[1])
+    p.forward(*good, **outs)
+    for i in range(6):
+        with pytest.raises(ValueError):
+            p.forward(*good[:i], dev(good[i].clone(), 1), *good[i + 1:])
+    for n, t in outs.items():
+        with pytest.raises(ValueError):
+            p.forward(*good, **{n: dev(t.clone(), 1)})
+    for i in (0, 1):
+        dy = [plain(4), plain(2)]
+        dy[i] = dev(dy[i].clone(), 1)
+        with pytest.raises(ValueError):
+            p.backward(*good, *dy)
+    table, lens = places()
+    for q, t, n, extra in ((plain(4), table, lens, {}), (plain(4), table, lens, dict(counts=lens))):
+        a.forward(q, t, n, o=plain(4), **extra)
+        args = [q, t, n]
+        for i in range(3):
+            with pytest.raises(ValueError):
+                a.forward(*args[:i], dev(args[i].clone(), 1), *args[i + 1:], o=plain(4), **extra)
+    with pytest.raises(ValueError):
+        a.forward(plain(4), table, lens, o=dev(plain(4).clone(), 1))
+    k = plain(2)
+    for args in ((dev(k.clone(), 1), k), (k, dev(k.clone(), 1))):
+        with pytest.raises(ValueError):
+            c.write(*args, table, lens)
+    with pytest.raises(ValueError):
+        c.read(table, lens, lens, 3, k=dev(k.clone(), 1), v=k)
+    assert len(ran) == 3
+    on_host = torch.zeros(2, 3, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        a.forward(on_host, table, lens, o=plain(4))
+
+
+def test_a_cache_of_another_device_is_refused():
+    for i in range(4):
+        with pytest.raises(ValueError):
+            cache(other=i)
+
+
+def test_a_plan_runs_on_its_own_device_only(monkeypatch):
+    """The default stream's handle names the stream of whichever device is current."""
+    p = B.HeadNormRope(2, 3, 4, 2, 64, device="cpu")
+    p._index, p._raw, p._current = 0, lambda i: 7, lambda: 0
+    assert p._stream() == 7
+    p._current = lambda: 1
+    with pytest.raises(ValueError):
+        p._stream()
