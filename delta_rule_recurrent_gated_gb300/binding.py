@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -469,7 +470,7 @@ def _torch_type(name):
 
 
 class _Calls:
-    """The device of a plan, its current stream and its allocations."""
+    """The device of a plan, its current stream, its allocations and workspaces."""
 
     def _at(self, device):
         import torch
@@ -495,6 +496,15 @@ class _Calls:
     def _empty(self, shape, dtype):
         return self._torch.empty(shape, dtype=dtype, device=self.device)
 
+    def _workspace(self, stream):
+        """A workspace for the calls of this thread on a stream: calls on another stream may run at the same
+        time, and another thread's may put its kernels between the two of a call."""
+        key = (stream, threading.get_ident())
+        ws = self._spaces.get(key)
+        if ws is None:
+            ws = self._spaces[key] = self._empty(self._ws_bytes, self._torch.uint8)
+        return ws
+
 
 class HeadNormRope(_Calls):
     """RMS norm of queries and keys for each head with the position rotation in the same pass
@@ -502,7 +512,10 @@ class HeadNormRope(_Calls):
 
     q [B, T, Hq, d] and k [B, T, Hk, d] may be head ranges of one packed projection.  The position
     of token (b, t) is ``positions[b, t]`` (default t) plus ``start[b]`` (default 0), a row of the
-    tables cos, sin [rows, rot / 2]."""
+    tables cos, sin [rows, rot / 2].
+
+    A plan may be used on any stream of its device and by several threads: the gradient's
+    workspace is one for each of both, kept with the plan."""
 
     def __init__(self, B, T, Hq, Hk, d, rot=None, style="halves", io="bf16", out="bf16", grad="bf16",
                  eps=1e-6, device="cuda"):
@@ -521,8 +534,8 @@ class HeadNormRope(_Calls):
         self.io_dtype, self.out_dtype, self.grad_dtype = map(_torch_type, (io, out, grad))
         self._q, self._k, self._w, self._rot = (B, T, Hq, d), (B, T, Hk, d), (d,), e.rot
         self._fwd, self._bwd = self._lib.dr_norm_rope_fwd, self._lib.dr_norm_rope_bwd
-        self.ws = None
-        if int(self._lib.dr_norm_rope_workspace_bytes(self._ref)) == 0:
+        self._spaces, self._ws_bytes = {}, int(self._lib.dr_norm_rope_workspace_bytes(self._ref))
+        if self._ws_bytes == 0:
             raise DrError(DR_ERR_UNSUPPORTED, "dr_norm_rope_workspace_bytes")
 
     def _layout(self, ld_q, ld_k, ld_oq, ld_ok, table_rows):
@@ -588,13 +601,12 @@ class HeadNormRope(_Calls):
             empty, device = self._torch.empty, self.device
             dwq = None if wq is None else empty(w, dtype=f32, device=device)
             dwk = None if wk is None else empty(w, dtype=f32, device=device)
-        if self.ws is None:
-            self.ws = self._empty(int(self._lib.dr_norm_rope_workspace_bytes(self._ref)), self._torch.uint8)
+        stream = self._stream()
         rc = self._bwd(*self._inputs(q, k, wq, wk, cos, sin, positions, start, ld_oq, ld_ok),
                        _address(dyq, self.io_dtype, self._q, "dyq", index),
                        _address(dyk, self.io_dtype, self._k, "dyk", index), dq.data_ptr(), dk.data_ptr(),
                        _address(dwq, f32, w, "dwq", index), _address(dwk, f32, w, "dwk", index),
-                       self.ws.data_ptr(), self.ws.numel(), self._stream())
+                       self._workspace(stream).data_ptr(), self._ws_bytes, stream)
         if rc:
             raise DrError(rc, "dr_norm_rope_bwd")
         return {"dq": dq, "dk": dk, "dwq": dwq, "dwk": dwk}
@@ -676,7 +688,11 @@ class KvCache(_Calls):
 
 
 class CacheAttention(_Calls):
-    """Attention of up to T query tokens of each of B sequences over a KvCache (dr_cache_attn)."""
+    """Attention of up to T query tokens of each of B sequences over a KvCache (dr_cache_attn).
+
+    A plan may be used on any stream of its device and by several threads: it keeps a workspace for
+    each of both.  Graphs that were captured on one stream share its workspace, so they are replayed one
+    after another."""
 
     def __init__(self, cache, B, T, Hq, io="bf16", out="bf16", scale=None, window=0):
         self._at(cache.device)
@@ -691,8 +707,12 @@ class CacheAttention(_Calls):
         n = int(self._lib.dr_cache_attn_workspace_bytes(cache._ref, self._ref, B, T))
         if n == 0:
             raise DrError(DR_ERR_UNSUPPORTED, "dr_cache_attn_workspace_bytes")
-        self.ws = self._empty(n, self._torch.uint8)
-        self._ws, self._ws_bytes, self._attn = self.ws.data_ptr(), n, self._lib.dr_cache_attn
+        self._spaces, self._ws_bytes, self._attn = {}, n, self._lib.dr_cache_attn
+
+    @property
+    def ws(self):
+        """The workspace of this thread's calls on the current stream."""
+        return self._workspace(self._stream())
 
     def forward(self, q, table, lens, counts=None, o=None, lse=None, want_lse=False):
         """o [B, T, Hq, d] and lse [B, T, Hq] (or None): query t of sequence b is the position
@@ -710,9 +730,11 @@ class CacheAttention(_Calls):
         empty, device = self._torch.empty, self.device
         o = empty(shape, dtype=self.out_dtype, device=device) if o is None else o
         lse = empty(shape[:3], dtype=self._f32, device=device) if lse is None and want_lse else lse
+        stream = self._stream()
         rc = self._attn(cache._ref, ctypes.byref(s), ref, q.data_ptr(),
-                        _address(o, self.out_dtype, shape, "o", index), _address(lse, self._f32, shape[:3], "lse", index),
-                        self._ws, self._ws_bytes, self._stream())
+                        _address(o, self.out_dtype, shape, "o", index),
+                        _address(lse, self._f32, shape[:3], "lse", index),
+                        self._workspace(stream).data_ptr(), self._ws_bytes, stream)
         if rc:
             raise DrError(rc, "dr_cache_attn")
         return o, lse

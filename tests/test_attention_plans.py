@@ -192,3 +192,33 @@ def test_a_plan_runs_on_its_own_device_only(monkeypatch):
     p._current = lambda: 1
     with pytest.raises(ValueError):
         p._stream()
+
+
+def test_streams_and_threads_have_workspaces_of_their_own():
+    """Calls that may run at the same time, or whose kernels may interleave, share no workspace."""
+    a, p, used = here(B.CacheAttention(cache(), 2, 3, 4)), norm(), []
+    a._attn = lambda *x: used.append(x[-3:-1]) or 0
+    p._bwd = lambda *x: used.append(x[-3:-1]) or 0
+
+    def attend():
+        a.forward(plain(4), *places(), o=plain(4))
+
+    def gradient():
+        p.backward(plain(4), plain(2), None, None, *tables(5), plain(4), plain(2))
+
+    for plan, call in ((a, attend), (p, gradient)):
+        used.clear()
+        call()
+        call()
+        here(plan, stream=8)
+        call()
+        threading.Thread(target=call).start()
+        while len(used) < 4:
+            pass
+        here(plan, stream=7)
+        call()
+        (first, size), second, other, thread, back = used
+        assert second == back == (first, size)
+        addresses = sorted({first, other[0], thread[0]})
+        assert len(addresses) == 3 and all(y - x >= size for x, y in zip(addresses, addresses[1:]))
+        assert other[1] == thread[1] == size
