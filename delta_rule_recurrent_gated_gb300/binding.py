@@ -499,7 +499,7 @@ class _Calls:
     def _workspace(self, stream):
         """A workspace for the calls of this thread on a stream: calls on another stream may run at the same
         time, and another thread's may put its kernels between the two of a call."""
-        key = (stream, threading.get_ident())
+        key = (self._ws_bytes, stream, threading.get_ident())
         ws = self._spaces.get(key)
         if ws is None:
             ws = self._spaces[key] = self._empty(self._ws_bytes, self._torch.uint8)
@@ -632,6 +632,7 @@ class KvCache(_Calls):
         for t, what in ((self.k_scale, "k scales"), (self.v_scale, "v scales")):
             _address(t, torch.float32, (num_pages, H), what, self._index)
         self.word = torch.zeros(4, dtype=torch.int32, device=self.device)
+        self._spaces = {}  # workspaces of the attention plans
         c = DrCache()
         c.num_pages, c.H, c.d, c.page, c.code = num_pages, H, d, page, CACHE_CODES[code]
         c.k, c.v = self.k.data_ptr(), self.v.data_ptr()
@@ -690,8 +691,9 @@ class KvCache(_Calls):
 class CacheAttention(_Calls):
     """Attention of up to T query tokens of each of B sequences over a KvCache (dr_cache_attn).
 
-    A plan may be used on any stream of its device and by several threads: it keeps a workspace for
-    each of both.  Graphs that were captured on one stream share its workspace, so they are replayed one
+    A plan may be used on any stream of its device and by several threads: there is a workspace for each of
+    both.  The workspaces are the cache's, for all plans over it, so that a plan itself is only a
+    descriptor.  Graphs that were captured on one stream share its workspace, so they are replayed one
     after another."""
 
     def __init__(self, cache, B, T, Hq, io="bf16", out="bf16", scale=None, window=0):
@@ -707,7 +709,7 @@ class CacheAttention(_Calls):
         n = int(self._lib.dr_cache_attn_workspace_bytes(cache._ref, self._ref, B, T))
         if n == 0:
             raise DrError(DR_ERR_UNSUPPORTED, "dr_cache_attn_workspace_bytes")
-        self._spaces, self._ws_bytes, self._attn = {}, n, self._lib.dr_cache_attn
+        self._spaces, self._ws_bytes, self._attn = cache._spaces, n, self._lib.dr_cache_attn
 
     @property
     def ws(self):

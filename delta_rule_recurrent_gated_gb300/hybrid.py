@@ -68,7 +68,7 @@ class AttentionLayer:
         self.plans = {}
 
     def _plan(self, T):
-        if T not in self.plans:  # descriptors and workspaces, once for each number of tokens
+        if T not in self.plans:  # descriptors, once for each number of tokens
             self.plans[T] = (binding.HeadNormRope(self.B, T, self.Hq, self.H, self.d, rot=self.rot),
                              binding.CacheAttention(self.cache, self.B, T, self.Hq, window=self.window))
         return self.plans[T]

@@ -222,3 +222,14 @@ def test_streams_and_threads_have_workspaces_of_their_own():
         addresses = sorted({first, other[0], thread[0]})
         assert len(addresses) == 3 and all(y - x >= size for x, y in zip(addresses, addresses[1:]))
         assert other[1] == thread[1] == size
+
+
+def test_plans_over_one_cache_share_its_workspaces():
+    """A program with prompts of any length makes a plan for each; their workspaces do not add up."""
+    c, used = cache(), []
+    for T in (1, 2, 40, 41, 80, 200):
+        a = here(B.CacheAttention(c, 2, T, 4))
+        a._attn = lambda *x: used.append(x[-3:-1]) or 0
+        a.forward(plain(4, T=T), *places(), o=plain(4, T=T))
+        assert used[-1][1] == int(B.load().dr_cache_attn_workspace_bytes(c._ref, a._ref, 2, T))
+    assert len(set(used)) == 2  # one for each of the two kernels
