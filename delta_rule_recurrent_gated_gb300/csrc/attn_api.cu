@@ -94,10 +94,13 @@ int check_attn(const dr_cache* c, const dr_attn_desc* d, int B, int T) {
 }
 
 // Which kernel, by the rows of a sequence and cache head (query tokens times the query heads that share
-// it): up to 32 rows are one tile of the kernel for few rows; from 33 on a tile of the tensor cores is the
-// faster even partly filled.  Four sequences of 8000 positions, four cache heads of 128: 32 rows 34.0 us (35.6
-// on the tensor cores), 40 rows 41.9 (36.0), 256 rows 122.7 (40.0); heads of 64: 32 rows 23.1 (28.7), 40 rows
-// 29.1 (28.9), 256 rows 84.4 (32.5).  fp32 types need the split operands of the other kernel.
+// it): the kernel for few rows reads the cache once for each 16 of them (8 where a type is fp32), and from 33
+// on a tile of 256 on the tensor cores is the faster even partly filled.  us, and in brackets on the tensor
+// cores, four cache heads; four sequences of 8000 positions, heads of 128: 16 rows 24.1 (34.8), 32 rows 34.8
+// (34.8), 36 rows 42.8 (35.0), 256 rows 129 (39.6); heads of 64: 32 rows 23.1 (29.6), 36 rows 29.4 (29.9), 64
+// rows 35.3 (30.0), 256 rows 89.2 (32.8).  64 sequences of 4000, heads of 128: 16 rows 82.6 (131), 32 rows 150
+// (132), 36 rows 205 (133); heads of 64: 16 rows 57.2 (129), 32 rows 102 (129), 36 rows 139 (129).  fp32 types
+// need the split operands of the other kernel.
 constexpr int kTcRows = 33;
 bool on_tensor_cores(const dr_cache* c, const dr_attn_desc* d, int T) {
     return d->io_dtype == DR_BF16 && d->out_dtype == DR_BF16 && (long long)T * (d->Hq / c->H) >= kTcRows;

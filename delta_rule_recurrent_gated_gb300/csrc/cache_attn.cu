@@ -28,7 +28,7 @@
 // kernel joins them, a block or a warp to a row.  It is launched early and waits on the device for the first.
 //
 // Bound by HBM where the cache is long: two sequences of 200001 to 262143 positions, four cache heads of 128,
-// 83 us for 474 MB (84 % of the copy rate, join and launches within it); 64 ragged sequences of 17 to 8191
+// 84.5 us for 474 MB (82 % of the copy rate, join and launches within it); 64 ragged sequences of 17 to 8191
 // positions 58 us for 270 MB (69 %: a tile's start and end cost as much as four stages).
 #include "attn_util.cuh"
 #include "trace.cuh"

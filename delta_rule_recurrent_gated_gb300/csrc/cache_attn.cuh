@@ -19,7 +19,7 @@ struct AttnParams {
 // A few rows of a sequence and cache head at a time, any type (cache_attn.cu).
 size_t cache_attn_rows_bytes(int d);
 cudaError_t cache_attn_rows(const AttnParams& p, cudaStream_t st);
-// 128 rows at a time on the tensor cores, bf16 queries and outputs (cache_attn_tc.cu).
+// 256 rows at a time on the tensor cores, bf16 queries and outputs (cache_attn_tc.cu).
 size_t cache_attn_tc_bytes(int d);
 cudaError_t cache_attn_tc(const AttnParams& p, cudaStream_t st);
 }  // namespace dr

@@ -26,7 +26,7 @@
 // that several blocks worked on is joined by a second kernel from their rows in the workspace.
 //
 // Chunks of 512 tokens of four sequences of 4000 to 8191 positions, 16 query heads on 4 of 128: 126 to 127 us for
-// 107 GFLOP (0.85 PFLOP/s; tensor pipe 40 % active).  The rows' threads bound it: they work 1650 of a stage's
+// 107 GFLOP (0.85 PFLOP/s; tensor pipe 38 % active).  The rows' threads bound it: they work 1650 of a stage's
 // 2100 cycles (350 instructions a warp, two warps a scheduler), and the products take 1140.
 #include "attn_util.cuh"
 #include "f32x2.cuh"

@@ -6,8 +6,8 @@
 // the new values to codes and, where the scale grew, the earlier codes again.  No other block
 // touches that page and head, so nothing is exchanged between blocks.  The read's blocks are the same.
 //
-// 8 prompts of 4096 tokens, four heads of 128, bf16 to e4m3 and back: append (101 MB) 20 us and read back
-// (101 MB) 17 us, 5.4 TB/s for the pair.  A block is a chain of length, values, maximum and codes of about
+// 8 prompts of 2048 to 4096 tokens, four heads of 128, bf16 to e4m3 and back: append (75 MB) 19 us and read back
+// (92 MB) 19 us, 4.5 TB/s for the pair.  A block is a chain of length, values, maximum and codes of about
 // 4 us, an SM holds five (append) or eight (read) of them, and a scheduler issues in 55 to 65 % of the cycles.
 #include <type_traits>
 

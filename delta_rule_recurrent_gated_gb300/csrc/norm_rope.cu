@@ -13,8 +13,8 @@
 // pairs, so nothing but the sums of a row passes between threads.  Products and sums run on
 // pairs of fp32 values (fma.rn.f32x2).  Each value is read and written once.
 //
-// 8 x 4096 tokens, 20 heads of 128, bf16: forward 53.5 us, 6.3 TB/s, bound by HBM; gradient 91.4 us,
-// 5.5 TB/s, bound by the loads that 512 threads of 116 registers keep in flight (in blocks of 256 92.2):
+// 8 x 4096 tokens, 20 heads of 128, bf16: forward 53.7 us, 6.3 TB/s, bound by HBM; gradient 89.5 us,
+// 5.6 TB/s, bound by the loads that 512 threads of 116 registers keep in flight (in blocks of 256 92.2):
 // 768 threads with two heads loaded at once take 98 us, a ring of asynchronous copies 113.
 #include "chain.cuh"
 #include "common.cuh"

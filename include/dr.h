@@ -354,7 +354,8 @@ int dr_norm_rope_bwd(const dr_rope_desc* desc, const void* q, const void* k, con
  *   page page_table[b * table_stride + p / page]; the call's tokens t < n_b of sequence b
  *   (n_b = counts ? counts[b] : T, at most T) are the positions lens[b] + t.  Only table
  *   entries of pages that hold such positions (attention: or earlier, visible ones) are read.
- * Supported: d 64 or 128; page 16, 32, 64 or 128; any H >= 1, B, T >= 0.
+ * Supported: d 64 or 128; page 16, 32, 64 or 128; any H >= 1, B, T >= 0.  Every array begins at a
+ *   multiple of 16 bytes, page_table, lens and counts too (DR_ERR_ALIGNMENT).
  *
  * dr_cache_write appends the tokens k, v ([B*T] rows of H*d, ld_k / ld_v elements apart, io
  * dtype).  For each page and head it touches, with s_old the page's scale if the page holds
