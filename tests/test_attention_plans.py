@@ -212,9 +212,9 @@ def test_streams_and_threads_have_workspaces_of_their_own():
         call()
         here(plan, stream=8)
         call()
-        threading.Thread(target=call).start()
-        while len(used) < 4:
-            pass
+        other_thread = threading.Thread(target=call)
+        other_thread.start()
+        other_thread.join(30)
         here(plan, stream=7)
         call()
         (first, size), second, other, thread, back = used
