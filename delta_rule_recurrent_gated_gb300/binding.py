@@ -62,6 +62,18 @@ class DrAttnDesc(ctypes.Structure):
                 ("window", ctypes.c_int), ("scale", ctypes.c_float), ("ld_q", ctypes.c_longlong)]
 
 
+class DrPromptDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "Hq", "H", "d", "num_seqs", "io_dtype", "window")]
+    _fields_ += [("scale", ctypes.c_float)]
+    _fields_ += [(n, ctypes.c_longlong) for n in ("ld_q", "ld_k", "ld_v", "ld_dq", "ld_dk", "ld_dv")]
+
+
+class DrLinearDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "H", "d_k", "d_v", "num_seqs", "io_dtype")]
+    _fields_ += [("scale", ctypes.c_float)]
+    _fields_ += [(n, ctypes.c_longlong) for n in ("ld_q", "ld_k", "ld_v", "ld_dq", "ld_dk", "ld_dv")]
+
+
 class DrError(RuntimeError):
     def __init__(self, code: int, where: str):
         self.code = code
@@ -125,6 +137,21 @@ def load(path: str = LIB_PATH):
     lib.dr_cache_attn_workspace_bytes.restype = S
     lib.dr_cache_attn.argtypes = [C, Q, A] + [P] * 4 + [S, P]
     lib.dr_cache_attn.restype = I
+    M, N = ctypes.POINTER(DrPromptDesc), ctypes.POINTER(DrLinearDesc)
+    lib.dr_prompt_attn_fwd.argtypes = [M] + [P] * 7
+    lib.dr_prompt_attn_fwd.restype = I
+    lib.dr_prompt_attn_workspace_bytes.argtypes = [M]
+    lib.dr_prompt_attn_workspace_bytes.restype = S
+    lib.dr_prompt_attn_bwd.argtypes = [M] + [P] * 11 + [S, P]
+    lib.dr_prompt_attn_bwd.restype = I
+    lib.dr_linear_attn_workspace_bytes.argtypes = [N]
+    lib.dr_linear_attn_workspace_bytes.restype = S
+    lib.dr_linear_attn_fwd.argtypes = [N] + [P] * 9 + [S, P]
+    lib.dr_linear_attn_fwd.restype = I
+    lib.dr_linear_attn_bwd.argtypes = [N] + [P] * 13 + [S, P]
+    lib.dr_linear_attn_bwd.restype = I
+    lib.dr_linear_attn_step.argtypes = [N] + [P] * 7
+    lib.dr_linear_attn_step.restype = I
     lib.dr_trace_enable.argtypes = [I]
     lib.dr_trace_enable.restype = I
     lib.dr_trace_count.argtypes = []
@@ -740,3 +767,193 @@ class CacheAttention(_Calls):
         if rc:
             raise DrError(rc, "dr_cache_attn")
         return o, lse
+
+
+# ------------------------------------------------------------------ token mixers over whole prompts
+class _Mixer(_Calls):
+    """What the plans of PromptAttention and LinearAttention share: tensors as rows of heads, sequences
+    dense [B, T] or packed into the rows of one (B = 1, ``seqs`` of them, offsets ``cu`` at each call)."""
+
+    def _plan(self, desc, seqs, io):
+        d = self.desc = desc
+        if seqs is not None and d.B != 1:
+            raise ValueError("packed sequences are the rows of one batch: B has to be 1")
+        d.num_seqs = d.B if seqs is None else seqs
+        d.io_dtype = _TYPE_CODES[io]
+        self.io_dtype, self._cu = _torch_type(io), None if seqs is None else (seqs + 1,)
+        self._refs, self._spaces = {}, {}
+
+    def _ref(self, lds):
+        """The descriptor of calls with these six row distances.  It is not changed afterwards: the library
+        reads it while other threads call."""
+        ref = self._refs.get(lds)
+        if ref is None:
+            d = type(self.desc).from_buffer_copy(self.desc)
+            d.ld_q, d.ld_k, d.ld_v, d.ld_dq, d.ld_dk, d.ld_dv = lds
+            ref = self._refs[lds] = ctypes.byref(d)
+        return ref
+
+    def _offsets(self, cu):
+        if (cu is None) != (self._cu is None):
+            raise ValueError("cu: the offsets of packed sequences go with a plan that was made with seqs")
+        return None if cu is None else _address(cu, self._i32, self._cu, "cu", self._index)
+
+    def _in(self, t, shape, what):
+        """Row distance and address of an input."""
+        if t.dtype is not self.io_dtype:
+            raise ValueError(f"{what}: expected {self.io_dtype}, got {t.dtype}")
+        return _rows(t, shape, what, self._index), t.data_ptr()
+
+    def _out(self, t, shape, what):
+        """A given gradient or a new one, its row distance and address."""
+        if t is None:
+            t = self._empty(shape, self.io_dtype)
+        return (t, *self._in(t, shape, what))
+
+
+class PromptAttention(_Mixer):
+    """Causal softmax attention over whole prompts and its gradient (dr_prompt_attn_fwd / dr_prompt_attn_bwd):
+    q [B, T, Hq, d], k and v [B, T, H, d], which may be head ranges of one packed projection; query head h
+    reads key head h // (Hq // H).
+
+    ``seqs``: packed sequences, at most that many; B is 1, T the rows in all, and each call takes the offsets
+    ``cu`` [seqs + 1] (int32, device).  Rows of no sequence are left as they were.
+
+    A plan may be used on any stream of its device and by several threads: the gradient's workspace is one for
+    each of both, kept with the plan; graphs that were captured on one stream share it, so they are replayed
+    one after another."""
+
+    def __init__(self, B, T, Hq, H, d, seqs=None, io="bf16", scale=None, window=0, device="cuda"):
+        self._at(device)
+        e = DrPromptDesc()
+        e.B, e.T, e.Hq, e.H, e.d, e.window = B, T, Hq, H, d, window
+        e.scale = d ** -0.5 if scale is None else float(scale)
+        e.ld_q = e.ld_dq = Hq * d
+        e.ld_k = e.ld_v = e.ld_dk = e.ld_dv = H * d
+        self._plan(e, seqs, io)
+        self._q, self._k, self._lse = (B, T, Hq, d), (B, T, H, d), (B, T, Hq)
+        self._fwd, self._bwd = self._lib.dr_prompt_attn_fwd, self._lib.dr_prompt_attn_bwd
+        self._ws_bytes = int(self._lib.dr_prompt_attn_workspace_bytes(ctypes.byref(e)))
+        if self._ws_bytes == 0:
+            raise DrError(DR_ERR_UNSUPPORTED, "dr_prompt_attn_workspace_bytes")
+
+    def forward(self, q, k, v, cu=None, o=None, lse=None, want_lse=False):
+        """o [B, T, Hq, d] and lse [B, T, Hq] fp32 (or None)."""
+        e, index = self.desc, self._index
+        (ld_q, qp), (ld_k, kp), (ld_v, vp) = self._in(q, self._q, "q"), self._in(k, self._k, "k"), self._in(v, self._k, "v")
+        o = self._empty(self._q, self.io_dtype) if o is None else o
+        lse = self._empty(self._lse, self._f32) if lse is None and want_lse else lse
+        rc = self._fwd(self._ref((ld_q, ld_k, ld_v, e.ld_dq, e.ld_dk, e.ld_dv)), qp, kp, vp, self._offsets(cu),
+                       _address(o, self.io_dtype, self._q, "o", index),
+                       _address(lse, self._f32, self._lse, "lse", index), self._stream())
+        if rc:
+            raise DrError(rc, "dr_prompt_attn_fwd")
+        return o, lse
+
+    def backward(self, q, k, v, o, lse, dO, cu=None, out=None):
+        """{dq, dk, dv} for the incoming gradient dO, with the forward's inputs and results.  ``out``: tensors to
+        write to, also head ranges of one packed gradient."""
+        index, given = self._index, out or {}
+        (ld_q, qp), (ld_k, kp), (ld_v, vp) = self._in(q, self._q, "q"), self._in(k, self._k, "k"), self._in(v, self._k, "v")
+        dq, ld_dq, dqp = self._out(given.get("dq"), self._q, "dq")
+        dk, ld_dk, dkp = self._out(given.get("dk"), self._k, "dk")
+        dv, ld_dv, dvp = self._out(given.get("dv"), self._k, "dv")
+        if lse is None:
+            raise ValueError("lse: the gradient needs the forward's")
+        stream = self._stream()
+        rc = self._bwd(self._ref((ld_q, ld_k, ld_v, ld_dq, ld_dk, ld_dv)), qp, kp, vp,
+                       _address(o, self.io_dtype, self._q, "o", index), _address(lse, self._f32, self._lse, "lse", index),
+                       _address(dO, self.io_dtype, self._q, "dO", index), self._offsets(cu), dqp, dkp, dvp,
+                       self._workspace(stream).data_ptr(), self._ws_bytes, stream)
+        if rc:
+            raise DrError(rc, "dr_prompt_attn_bwd")
+        return {"dq": dq, "dk": dk, "dv": dv}
+
+
+class LinearAttention(_Mixer):
+    """Linear attention with a decay for each head, S_t = e^g S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t: over
+    whole prompts in chunks, its gradient, and the recurrent step (dr_linear_attn_fwd / _bwd / _step).
+
+    q, k [B, T, H, dk] and v [B, T, H, dv] may be head ranges of one packed projection; g [H] fp32 is the
+    log-decay of a step, a constant of the layer; states are [sequences, H, dk, dv] fp32.  ``seqs`` and ``cu``:
+    packed sequences, as for PromptAttention, and so are streams, threads and graphs."""
+
+    def __init__(self, B, T, H, dk, dv, seqs=None, io="bf16", scale=1.0, device="cuda"):
+        self._at(device)
+        e = DrLinearDesc()
+        e.B, e.T, e.H, e.d_k, e.d_v = B, T, H, dk, dv
+        e.scale = float(scale)
+        e.ld_q = e.ld_k = e.ld_dq = e.ld_dk = H * dk
+        e.ld_v = e.ld_dv = H * dv
+        self._plan(e, seqs, io)
+        self._k, self._v, self._g = (B, T, H, dk), (B, T, H, dv), (H,)
+        self._h = (e.num_seqs, H, dk, dv)
+        self._fwd, self._bwd, self._step = (getattr(self._lib, "dr_linear_attn_" + n) for n in ("fwd", "bwd", "step"))
+        self._ws_bytes = int(self._lib.dr_linear_attn_workspace_bytes(ctypes.byref(e)))
+        # sizes that only the recurrent step takes: the library refuses the other calls itself
+        if self._ws_bytes == 0 and not (dk in (16, 32, 64, 128) and dv in (16, 32, 64, 128) and seqs is None):
+            raise DrError(DR_ERR_UNSUPPORTED, "dr_linear_attn_workspace_bytes")
+
+    def _inputs(self, q, k, v):
+        return (*self._in(q, self._k, "q"), *self._in(k, self._k, "k"), *self._in(v, self._v, "v"))
+
+    def _state(self, t, what):
+        return _address(t, self._f32, self._h, what, self._index)
+
+    def _decays(self, g):
+        if g is None:
+            raise ValueError("g: the log-decays of the heads are missing")
+        return _address(g, self._f32, self._g, "g", self._index)
+
+    def forward(self, q, k, v, g, h0=None, cu=None, o=None, hT=None, want_hT=True):
+        """o [B, T, H, dv] and the states after the last tokens (or None); h0 None: empty states before."""
+        e = self.desc
+        ld_q, qp, ld_k, kp, ld_v, vp = self._inputs(q, k, v)
+        o = self._empty(self._v, self.io_dtype) if o is None else o
+        hT = self._empty(self._h, self._f32) if hT is None and want_hT else hT
+        stream = self._stream()
+        rc = self._fwd(self._ref((ld_q, ld_k, ld_v, e.ld_dq, e.ld_dk, e.ld_dv)), qp, kp, vp, self._decays(g),
+                       self._state(h0, "h0"), self._offsets(cu), _address(o, self.io_dtype, self._v, "o", self._index),
+                       self._state(hT, "hT"), self._workspace(stream).data_ptr(), self._ws_bytes, stream)
+        if rc:
+            raise DrError(rc, "dr_linear_attn_fwd")
+        return o, hT
+
+    def backward(self, q, k, v, g, dO, h0=None, dhT=None, cu=None, out=None, want_dh0=None):
+        """{dq, dk, dv, dh0} for the incoming gradients dO and dhT (None: zero).  dh0 is None unless it is wanted
+        (default: where h0 or dhT is given).  ``out``: tensors to write to, also head ranges of one packed
+        gradient."""
+        given = out or {}
+        ld_q, qp, ld_k, kp, ld_v, vp = self._inputs(q, k, v)
+        dq, ld_dq, dqp = self._out(given.get("dq"), self._k, "dq")
+        dk, ld_dk, dkp = self._out(given.get("dk"), self._k, "dk")
+        dv, ld_dv, dvp = self._out(given.get("dv"), self._v, "dv")
+        dh0 = given.get("dh0")
+        if want_dh0 is None:
+            want_dh0 = h0 is not None or dhT is not None
+        if dh0 is None and want_dh0:
+            dh0 = self._empty(self._h, self._f32)
+        stream = self._stream()
+        rc = self._bwd(self._ref((ld_q, ld_k, ld_v, ld_dq, ld_dk, ld_dv)), qp, kp, vp, self._decays(g),
+                       self._state(h0, "h0"), _address(dO, self.io_dtype, self._v, "dO", self._index),
+                       self._state(dhT, "dhT"), self._offsets(cu), dqp, dkp, dvp, self._state(dh0, "dh0"),
+                       self._workspace(stream).data_ptr(), self._ws_bytes, stream)
+        if rc:
+            raise DrError(rc, "dr_linear_attn_bwd")
+        return {"dq": dq, "dk": dk, "dv": dv, "dh0": dh0}
+
+    def step(self, q, k, v, g, state, o=None):
+        """o [B, T, H, dv] of the T next tokens of every sequence; ``state`` [B, H, dk, dv] is updated in place."""
+        if self._cu is not None:
+            raise ValueError("the recurrent step takes dense batches")
+        if state is None:
+            raise ValueError("state: missing")
+        e = self.desc
+        ld_q, qp, ld_k, kp, ld_v, vp = self._inputs(q, k, v)
+        o = self._empty(self._v, self.io_dtype) if o is None else o
+        rc = self._step(self._ref((ld_q, ld_k, ld_v, e.ld_dq, e.ld_dk, e.ld_dv)), qp, kp, vp, self._decays(g),
+                        self._state(state, "state"), _address(o, self.io_dtype, self._v, "o", self._index),
+                        self._stream())
+        if rc:
+            raise DrError(rc, "dr_linear_attn_step")
+        return o

@@ -1,0 +1,292 @@
+// linear_attn.cu -- linear attention with a decay for each head on the CUDA cores, fp32 arithmetic: the
+// chunked scan of linear_attn.cuh (dr.h, dr_linear_attn_fwd / dr_linear_attn_bwd) and the recurrent step
+// (dr_linear_attn_step).
+//
+// The scan in chunks of C = 64 tokens, i and j within the chunk, X the state before it, a = e^g:
+//   out_i = sum_{j<=i} a^{i-j} (q_i.k_j) v_j + a^{i+1} X^T q_i;   X' = a^C X + sum_j a^{C-1-j} k_j v_j^T
+// (reverse: a^i X^T q_i and X' = a^C X + sum_j a^{C-j} k_j v_j^T).  Columns of v and of the state do not meet,
+// so a block has one sequence, one head and up to 32 columns; the products q_i.k_j are formed by each.
+#include "common.cuh"
+#include "linear_attn.cuh"
+#include "trace.cuh"
+#include "vec4.cuh"
+
+namespace dr {
+namespace {
+
+constexpr int kThreads = 256, kChunk = 64;
+
+template <int DK, int W> struct ScanSmem {  // pitches: 16-byte reads of eight rows meet all banks
+    static constexpr int pk = DK + 4, pw = W + 4, pa = kChunk + 4;
+    static constexpr int k = kChunk * pk, v = 2 * kChunk * pk, a = v + kChunk * pw, x = a + kChunk * pa,
+                         floats = x + DK * pw;
+};
+
+template <int DK, int W, typename IO> __global__ void __launch_bounds__(kThreads, 2) linear_scan_kernel(const ScanParams p) {
+    using L = ScanSmem<DK, W>;
+    extern __shared__ __align__(16) float sm[];
+    float *Q = sm, *K = sm + L::k, *V = sm + L::v, *A = sm + L::a, *X = sm + L::x;
+    __shared__ float pw[kChunk + 1];  // a^n
+    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, w0 = blockIdx.y * W;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    constexpr int WX = W / 16, RX = DK / 16;  // a thread's columns; its rows of the state
+    int row0, len;
+    seq_rows(p.s, s, row0, len);
+    const float g = p.g[h];
+    if (threadIdx.x <= kChunk) pw[threadIdx.x] = decay(g, (float)threadIdx.x);
+    const size_t unit = (size_t)s * p.H + h;
+    for (int i = threadIdx.x; i < DK * W; i += kThreads) {
+        const int r = i / W, c = w0 + i % W;
+        const size_t at = p.x0_transposed ? (unit * p.dv + c) * DK + r : (unit * DK + r) * p.dv + c;
+        X[r * L::pw + i % W] = p.x0 ? p.x0[at] : 0.f;
+    }
+    const float f_in = p.reverse ? p.scale : 1.f, f_out = p.reverse ? 1.f : p.scale;
+    const int late = p.reverse ? 1 : 0;
+    for (int t0 = 0; t0 < len; t0 += kChunk) {
+        const int n = min(kChunk, len - t0);
+        __syncthreads();
+        auto token = [&](int i) { return (long long)row0 + (p.reverse ? len - 1 - t0 - i : t0 + i); };
+        for (int i = threadIdx.x; i < kChunk * (DK / 4); i += kThreads) {
+            const int r = i / (DK / 4), c = (i % (DK / 4)) * 4;
+            float4 q = make_float4(0.f, 0.f, 0.f, 0.f), k = q;
+            if (r < n) {
+                q = load4(static_cast<const IO*>(p.q) + token(r) * p.ld_q + (long long)h * DK + c);
+                k = load4(static_cast<const IO*>(p.k) + token(r) * p.ld_k + (long long)h * DK + c);
+            }
+            *reinterpret_cast<float4*>(Q + r * L::pk + c) = q;
+            *reinterpret_cast<float4*>(K + r * L::pk + c) = k;
+        }
+        for (int i = threadIdx.x; i < kChunk * (W / 4); i += kThreads) {
+            const int r = i / (W / 4), c = (i % (W / 4)) * 4;
+            const float4 v = r < n ? load4(static_cast<const IO*>(p.v) + token(r) * p.ld_v + (long long)h * p.dv + w0 + c)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4*>(V + r * L::pw + c) = v;
+        }
+        __syncthreads();
+        {   // weights of the pairs: rows 4 ty + i, columns tx + 16 j
+            float acc[4][4] = {};
+#pragma unroll 4
+            for (int c = 0; c < DK; c += 4) {
+                float4 a[4], b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    a[i] = *reinterpret_cast<const float4*>(Q + (4 * ty + i) * L::pk + c);
+                    b[i] = *reinterpret_cast<const float4*>(K + (tx + 16 * i) * L::pk + c);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
+                        acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
+                        acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
+                        acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int back = 4 * ty + i - (tx + 16 * j);
+                    A[(4 * ty + i) * L::pa + tx + 16 * j] = back >= 0 ? acc[i][j] * pw[back] * f_in : 0.f;
+                }
+        }
+        __syncthreads();
+        {   // out: rows 4 ty + i, columns WX tx ..
+            float o[4][WX] = {}, r[4][WX] = {};
+#pragma unroll 2
+            for (int c = 0; c < kChunk; c += 4) {
+                float4 a[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * L::pa + c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int w = 0; w < WX; ++w) {
+                        const float v = V[(c + k) * L::pw + WX * tx + w];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[i][w] = fmaf(k == 0 ? a[i].x : k == 1 ? a[i].y : k == 2 ? a[i].z : a[i].w, v, o[i][w]);
+                    }
+            }
+#pragma unroll 2
+            for (int c = 0; c < DK; c += 4) {
+                float4 q[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(Q + (4 * ty + i) * L::pk + c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int w = 0; w < WX; ++w) {
+                        const float x = X[(c + k) * L::pw + WX * tx + w];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            r[i][w] = fmaf(k == 0 ? q[i].x : k == 1 ? q[i].y : k == 2 ? q[i].z : q[i].w, x, r[i][w]);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (4 * ty + i < n)
+#pragma unroll
+                    for (int w = 0; w < WX; ++w) {
+                        const float y = f_out * fmaf(pw[4 * ty + i + 1 - late], r[i][w], o[i][w]);
+                        static_cast<IO*>(p.out)[token(4 * ty + i) * p.ld_o + (long long)h * p.dv + w0 + WX * tx + w] = from_f<IO>(y);
+                    }
+        }
+        __syncthreads();
+        {   // the state: rows RX ty ..
+            float x[RX][WX];
+            const float a = pw[n];
+#pragma unroll
+            for (int i = 0; i < RX; ++i)
+#pragma unroll
+                for (int w = 0; w < WX; ++w) x[i][w] = a * X[(RX * ty + i) * L::pw + WX * tx + w];
+            for (int j = 0; j < n; ++j) {
+                const float f = pw[n - 1 - j + late] * f_in;
+                float v[WX];
+#pragma unroll
+                for (int w = 0; w < WX; ++w) v[w] = f * V[j * L::pw + WX * tx + w];
+#pragma unroll
+                for (int i = 0; i < RX; ++i) {
+                    const float k = K[j * L::pk + RX * ty + i];
+#pragma unroll
+                    for (int w = 0; w < WX; ++w) x[i][w] = fmaf(k, v[w], x[i][w]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < RX; ++i)
+#pragma unroll
+                for (int w = 0; w < WX; ++w) X[(RX * ty + i) * L::pw + WX * tx + w] = x[i][w];
+        }
+    }
+    __syncthreads();
+    if (p.xT)
+        for (int i = threadIdx.x; i < DK * W; i += kThreads)
+            p.xT[(unit * DK + i / W) * p.dv + w0 + i % W] = X[(i / W) * L::pw + i % W];
+}
+
+template <int DK, int W, typename IO> cudaError_t scan(const ScanParams& p, cudaStream_t st) {
+    static std::atomic<unsigned long long> ready{0};
+    constexpr int smem = ScanSmem<DK, W>::floats * 4;
+    if (cudaError_t e = set_smem_once(linear_scan_kernel<DK, W, IO>, smem, ready); e != cudaSuccess) return e;
+    TraceScope ts("linear_scan", st);
+    linear_scan_kernel<DK, W, IO><<<dim3(p.s.N * p.H, p.dv / W), kThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+template <int DK, typename IO> cudaError_t scan_width(const ScanParams& p, cudaStream_t st) {
+    return p.dv == 16 ? scan<DK, 16, IO>(p, st) : scan<DK, 32, IO>(p, st);
+}
+
+// ------------------------------------------------------------------ the recurrent step
+// A block has one sequence and head, each thread four columns of R rows of the state in registers:
+//   X = a X + k_t v_t^T;  o_t = scale X^T q_t
+// The state is read and written once, a row of it at a time by neighbouring lanes.  The tokens' parts of o
+// are summed in shared memory, eight tokens at a time, so that no token waits for another.
+constexpr int kTokens = 8;
+template <int DK, int DV, typename IO> __global__ void __launch_bounds__(kThreads) linear_step_kernel(const StepParams p) {
+    constexpr int L = DV / 4;                                       // lanes of a row
+    constexpr int G = kThreads / L < DK ? kThreads / L : DK;        // rows at a time
+    constexpr int R = DK / G, GW = 32 / L, PARTS = G / GW > 0 ? G / GW : 1;  // rows of a thread; groups in a warp; warps
+    __shared__ __align__(16) float q[kTokens][DK], k[kTokens][DK], v[kTokens][DV], part[kTokens][PARTS][DV];
+    const int b = blockIdx.x / p.H, h = blockIdx.x % p.H;
+    const int lane = threadIdx.x % L, grp = threadIdx.x / L;
+    const bool on = grp < G;
+    float* S = p.state + ((size_t)b * p.H + h) * DK * DV;
+    float4 x[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) x[i] = on ? load4(S + (size_t)(grp + i * G) * DV + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float a = expf(p.g[h]);
+    for (int t0 = 0; t0 < p.T; t0 += kTokens) {
+        const int n = min(kTokens, p.T - t0);
+        const long long tok = (long long)b * p.T + t0;
+        if (t0) __syncthreads();
+        for (int i = threadIdx.x; i < n * (DK / 4); i += kThreads) {
+            const int t = i / (DK / 4), c = (i % (DK / 4)) * 4;
+            *reinterpret_cast<float4*>(&q[t][c]) = load4(static_cast<const IO*>(p.q) + (tok + t) * p.ld_q + (long long)h * DK + c);
+            *reinterpret_cast<float4*>(&k[t][c]) = load4(static_cast<const IO*>(p.k) + (tok + t) * p.ld_k + (long long)h * DK + c);
+        }
+        for (int i = threadIdx.x; i < n * L; i += kThreads) {
+            const int t = i / L, c = (i % L) * 4;
+            *reinterpret_cast<float4*>(&v[t][c]) = load4(static_cast<const IO*>(p.v) + (tok + t) * p.ld_v + (long long)h * DV + c);
+        }
+        __syncthreads();
+        for (int t = 0; t < n; ++t) {
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (on) {
+                const float4 w = *reinterpret_cast<const float4*>(&v[t][4 * lane]);
+#pragma unroll
+                for (int i = 0; i < R; ++i) {
+                    const float kk = k[t][grp + i * G], qq = q[t][grp + i * G];
+                    x[i].x = fmaf(a, x[i].x, kk * w.x); o.x = fmaf(qq, x[i].x, o.x);
+                    x[i].y = fmaf(a, x[i].y, kk * w.y); o.y = fmaf(qq, x[i].y, o.y);
+                    x[i].z = fmaf(a, x[i].z, kk * w.z); o.z = fmaf(qq, x[i].z, o.z);
+                    x[i].w = fmaf(a, x[i].w, kk * w.w); o.w = fmaf(qq, x[i].w, o.w);
+                }
+            }
+#pragma unroll
+            for (int d = L; d < 32; d <<= 1) {
+                o.x += __shfl_xor_sync(0xffffffffu, o.x, d);
+                o.y += __shfl_xor_sync(0xffffffffu, o.y, d);
+                o.z += __shfl_xor_sync(0xffffffffu, o.z, d);
+                o.w += __shfl_xor_sync(0xffffffffu, o.w, d);
+            }
+            if (on && (threadIdx.x & 31) < L) *reinterpret_cast<float4*>(&part[t][threadIdx.x >> 5][4 * lane]) = o;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * L; i += kThreads) {
+            const int t = i / L, c = (i % L) * 4;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < PARTS; ++w) {
+                const float4 y = *reinterpret_cast<const float4*>(&part[t][w][c]);
+                o.x += y.x; o.y += y.y; o.z += y.z; o.w += y.w;
+            }
+            store4(static_cast<IO*>(p.o) + ((tok + t) * p.H + h) * DV + c,
+                   make_float4(p.scale * o.x, p.scale * o.y, p.scale * o.z, p.scale * o.w));
+        }
+    }
+    if (on)
+#pragma unroll
+        for (int i = 0; i < R; ++i) store4(S + (size_t)(grp + i * G) * DV + 4 * lane, x[i]);
+}
+
+template <int DK, int DV, typename IO> cudaError_t step(const StepParams& p, cudaStream_t st) {
+    TraceScope ts("linear_step", st);
+    linear_step_kernel<DK, DV, IO><<<p.B * p.H, kThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
+template <int DK, typename IO> cudaError_t step_width(const StepParams& p, cudaStream_t st) {
+    switch (p.dv) {
+        case 16: return step<DK, 16, IO>(p, st);
+        case 32: return step<DK, 32, IO>(p, st);
+        case 64: return step<DK, 64, IO>(p, st);
+        default: return step<DK, 128, IO>(p, st);
+    }
+}
+template <typename IO> cudaError_t scan_of(const ScanParams& p, cudaStream_t st) {
+    switch (p.dk) {
+        case 16: return scan_width<16, IO>(p, st);
+        case 32: return scan_width<32, IO>(p, st);
+        case 64: return scan_width<64, IO>(p, st);
+        default: return scan_width<128, IO>(p, st);
+    }
+}
+template <typename IO> cudaError_t step_of(const StepParams& p, cudaStream_t st) {
+    switch (p.dk) {
+        case 16: return step_width<16, IO>(p, st);
+        case 32: return step_width<32, IO>(p, st);
+        case 64: return step_width<64, IO>(p, st);
+        default: return step_width<128, IO>(p, st);
+    }
+}
+
+}  // namespace
+
+cudaError_t linear_scan_simt(const ScanParams& p, int io, cudaStream_t st) {
+    return io == DR_F32 ? scan_of<float>(p, st) : scan_of<__nv_bfloat16>(p, st);
+}
+cudaError_t linear_step(const StepParams& p, int io, cudaStream_t st) {
+    return io == DR_F32 ? step_of<float>(p, st) : step_of<__nv_bfloat16>(p, st);
+}
+
+}  // namespace dr

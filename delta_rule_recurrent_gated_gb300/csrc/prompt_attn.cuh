@@ -1,0 +1,25 @@
+// prompt_attn.cuh -- launch parameters of causal attention over whole prompts.
+#pragma once
+#include <cstddef>
+
+#include "seqs.cuh"
+
+namespace dr {
+struct PromptParams {
+    Seqs s;
+    long long rows;          // of every tensor
+    int Hq, H, G, d;         // query heads, key heads, query heads of each key head, channels
+    int window;
+    float scale;
+    long long ld_q, ld_k, ld_v, ld_dq, ld_dk, ld_dv;
+    const void *q, *k, *v, *dO;
+    void* o;                 // forward: written; backward: read
+    float* lse;              // the same (forward: may be null)
+    void *dq, *dk, *dv;
+    float* delta;            // workspace: sum of dO o for each row and query head
+};
+
+// CUDA cores, bf16 or fp32 (prompt_attn.cu).
+cudaError_t prompt_attn_fwd_simt(const PromptParams& p, int io, cudaStream_t st);
+cudaError_t prompt_attn_bwd_simt(const PromptParams& p, int io, cudaStream_t st);
+}  // namespace dr

@@ -1,0 +1,82 @@
+// seqs.cuh -- the sequences of a call, dense [N, T] or packed one behind the other, and the order in which
+// their tiles are worked on.
+#pragma once
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace dr {
+struct Seqs {
+    const int32_t* cu;  // packed: device [N + 1], the first row of each sequence; null: dense
+    int N, T;           // sequences; tokens of each (dense) or rows in all (packed)
+};
+
+// First row and length of sequence s.  Offsets outside 0 .. T are taken as the nearest of them and a
+// sequence that would end before it starts is empty, so that nothing outside the tensors is touched.
+__device__ __forceinline__ void seq_rows(const Seqs& q, int s, int& row0, int& len) {
+    if (!q.cu) {
+        row0 = s * q.T;
+        len = q.T;
+        return;
+    }
+    row0 = min(max(q.cu[s], 0), q.T);
+    len = max(min(max(q.cu[s + 1], 0), q.T) - row0, 0);
+}
+
+// Tiles of R rows that the sequences can have in all (offsets in order): a grid size.
+inline long long most_tiles(const Seqs& q, int R) {
+    return q.cu ? (long long)q.T / R + q.N : (long long)q.N * ((q.T + R - 1) / R);
+}
+
+__device__ __forceinline__ long long warp_sum(long long x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// Tile number `item` of all tiles of R rows, those with the largest index in their sequence first (under a
+// causal mask the longest rows of work start first and the short ones fill the gaps); called by a whole warp.
+// Returns false where there are fewer tiles.
+__device__ __forceinline__ bool find_tile(const Seqs& q, int R, long long item, int& seq, int& tile) {
+    if (!q.cu) {
+        const int n = (q.T + R - 1) / R;
+        if (item >= (long long)n * q.N) return false;
+        tile = n - 1 - (int)(item / q.N);
+        seq = (int)(item % q.N);
+        return true;
+    }
+    const int lane = threadIdx.x & 31;
+    auto tiles = [&](int s) {
+        if (s >= q.N) return 0;
+        int row0, len;
+        seq_rows(q, s, row0, len);
+        return (len + R - 1) / R;
+    };
+    auto count = [&](int v) {  // tiles with index v or more
+        long long c = 0;
+        for (int s = lane; s < q.N; s += 32) c += max(0, tiles(s) - v);
+        return warp_sum(c);
+    };
+    if (item >= count(0)) return false;
+    int lo = 0, hi = (q.T + R - 1) / R;  // count(lo) > item >= count(hi)
+    long long above = 0;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        const long long c = count(mid);
+        if (c > item) lo = mid;
+        else hi = mid, above = c;
+    }
+    tile = lo;
+    int rest = (int)(item - above);  // among the sequences that have tile lo
+    for (int s0 = 0; s0 < q.N; s0 += 32) {
+        const unsigned has = __ballot_sync(0xffffffffu, tiles(s0 + lane) > lo);
+        const int n = __popc(has);
+        if (rest < n) {
+            const bool mine = (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == rest;
+            seq = s0 + __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+            return true;
+        }
+        rest -= n;
+    }
+    return false;
+}
+}  // namespace dr

@@ -425,6 +425,90 @@ int dr_cache_attn(const dr_cache* cache, const dr_cache_seqs* seqs, const dr_att
                   void* stream);
 
 /*
+ * The two other token mixers of a hybrid stack, over whole prompts and for training (the same page:
+ * its stacks set softmax attention and linear attention with a decay beside the delta rule; it
+ * names them only, the equations are the standard ones, stated here).
+ *
+ * Sequences, for both: dense, cu_seqlens NULL, num_seqs == B sequences of T tokens; or packed,
+ * B == 1, T rows, sequence s in the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (device
+ * [num_seqs + 1], read when the kernels run: a captured call takes new lengths).  Lengths may be
+ * zero.  Rows of no sequence are left as they were.  An offset outside 0 .. T counts as the nearest
+ * of them and a sequence that would end before it starts as empty: nothing else is touched.
+ * Tensors are rows of heads: q [B*T] rows of Hq*d values (or H*d_k), ld_q elements from one row to
+ * the next, and k, v, dq, dk, dv likewise with their own distances (column ranges of one packed
+ * projection, or of its gradient, will do); o, dO contiguous.  Everything is of io dtype except
+ * statistics, decays and states, which are fp32.
+ * Arithmetic: fp32 for fp32 tensors.  For bf16 the products take bf16 operands and accumulate in
+ * fp32; softmax weights, decayed scores and the state that queries read are rounded to bf16 as
+ * operands, what is carried from chunk to chunk (the states) is not.
+ * Gradients of shared key heads are summed in a fixed order: the same inputs give the same bits.
+ * A token that is not finite leaves other sequences alone; in its own it may also reach the results
+ * of tokens that do not see it (a weight of zero times it).
+ * Errors as dr_fwd.
+ *
+ * Causal softmax attention: query i of a sequence sees its keys j <= i, and with window > 0 only
+ * j > i - window; query head h reads key head h / (Hq / H).
+ *   s_ij = scale q_i.k_j;  lse_i = ln sum_j e^{s_ij};  o_i = sum_j e^{s_ij - lse_i} v_j
+ * Forward: o [B, T, Hq, d], lse [B, T, Hq] (or NULL).  Backward: dq, dk, dv of L = sum(dO * o), from
+ * the forward's inputs, o and lse.  Workspace (backward): dr_prompt_attn_workspace_bytes (0 when desc
+ * is invalid or unsupported); results do not depend on what it held.
+ * Supported: d 64 or 128, H dividing Hq, any B, T >= 0, B*T < 2^30.
+ */
+typedef struct dr_prompt_desc {
+    int B, T, Hq, H, d;
+    int num_seqs;
+    int io_dtype;
+    int window;                   /* 0: none                                           */
+    float scale;
+    long long ld_q, ld_k, ld_v;
+    long long ld_dq, ld_dk, ld_dv; /* backward                                          */
+} dr_prompt_desc;
+
+int dr_prompt_attn_fwd(const dr_prompt_desc* desc, const void* q, const void* k, const void* v,
+                       const int32_t* cu_seqlens, void* o, float* lse, void* stream);
+size_t dr_prompt_attn_workspace_bytes(const dr_prompt_desc* desc);
+int dr_prompt_attn_bwd(const dr_prompt_desc* desc, const void* q, const void* k, const void* v,
+                       const void* o, const float* lse, const void* dO, const int32_t* cu_seqlens,
+                       void* dq, void* dk, void* dv, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
+ * Linear attention with a decay for each head (sequences, tensors and arithmetic as above):
+ *   S_t = e^{g_h} S_{t-1} + k_t v_t^T;  o_t = scale S_t^T q_t
+ * g: [H] fp32, the log-decay of a step, <= 0, a constant of the layer (no gradient).  States
+ * h0, hT, dhT, dh0 [num_seqs, H, d_k, d_v] fp32, NULL: zero (h0, dhT) or not wanted (hT, dh0).  A
+ * sequence without tokens hands its state on (hT = h0, dh0 = dhT).
+ * dr_linear_attn_fwd: o [B, T, H, d_v] and hT.  dr_linear_attn_bwd: dq, dk, dv and dh0 of
+ * L = sum(dO * o) + sum(dhT * hT).  Workspace for both: dr_linear_attn_workspace_bytes (0 when desc
+ * is invalid or unsupported; needs the device current that will run the call); results do not depend
+ * on what it held.
+ * dr_linear_attn_step: the recurrence token by token for T tokens of every sequence, on the caller's
+ * state [B, H, d_k, d_v] fp32, updated in place (fp32 arithmetic for both types; dense only; ld_dq,
+ * ld_dk, ld_dv are not looked at).
+ * Supported: bf16 d_k, d_v in {64, 128} (step: also 16, 32); fp32 d_k, d_v in {16, 32, 64, 128};
+ * any B, T >= 0, B*T < 2^30.
+ */
+typedef struct dr_linear_desc {
+    int B, T, H, d_k, d_v;
+    int num_seqs;
+    int io_dtype;
+    float scale;
+    long long ld_q, ld_k, ld_v;
+    long long ld_dq, ld_dk, ld_dv; /* backward                                          */
+} dr_linear_desc;
+
+size_t dr_linear_attn_workspace_bytes(const dr_linear_desc* desc);
+int dr_linear_attn_fwd(const dr_linear_desc* desc, const void* q, const void* k, const void* v,
+                       const float* g, const float* h0, const int32_t* cu_seqlens, void* o, float* hT,
+                       void* workspace, size_t workspace_bytes, void* stream);
+int dr_linear_attn_bwd(const dr_linear_desc* desc, const void* q, const void* k, const void* v,
+                       const float* g, const float* h0, const void* dO, const float* dhT,
+                       const int32_t* cu_seqlens, void* dq, void* dk, void* dv, float* dh0,
+                       void* workspace, size_t workspace_bytes, void* stream);
+int dr_linear_attn_step(const dr_linear_desc* desc, const void* q, const void* k, const void* v,
+                        const float* g, float* state, void* o, void* stream);
+
+/*
  * Self-test of the device failure path (no counterpart on the pages).  Launches one
  * warp that waits, with the bounded wait every tensor-core kernel uses, on an mbarrier
  * phase that only completes when `arrive` is non-zero (the warp completes it itself);
