@@ -66,12 +66,14 @@ class DrPromptDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "Hq", "H", "d", "num_seqs", "io_dtype", "window")]
     _fields_ += [("scale", ctypes.c_float)]
     _fields_ += [(n, ctypes.c_longlong) for n in ("ld_q", "ld_k", "ld_v", "ld_dq", "ld_dk", "ld_dv")]
+    _fields_ += [("status", ctypes.c_void_p)]
 
 
 class DrLinearDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("B", "T", "H", "d_k", "d_v", "num_seqs", "io_dtype")]
     _fields_ += [("scale", ctypes.c_float)]
     _fields_ += [(n, ctypes.c_longlong) for n in ("ld_q", "ld_k", "ld_v", "ld_dq", "ld_dk", "ld_dv")]
+    _fields_ += [("status", ctypes.c_void_p)]
 
 
 class DrError(RuntimeError):
@@ -782,6 +784,12 @@ class _Mixer(_Calls):
         d.io_dtype = _TYPE_CODES[io]
         self.io_dtype, self._cu = _torch_type(io), None if seqs is None else (seqs + 1,)
         self._refs, self._spaces = {}, {}
+        self.word = self._torch.zeros(4, dtype=self._i32, device=self.device)
+        d.status = self.word.data_ptr()
+
+    def status(self) -> int:
+        """DR_OK, or DR_ERR_TIMEOUT after a kernel's bounded wait ran out."""
+        return check_status(self.word.data_ptr(), self._stream())
 
     def _ref(self, lds):
         """The descriptor of calls with these six row distances.  It is not changed afterwards: the library

@@ -25,6 +25,7 @@ struct ScanParams {
     const float* x0;             // [N, H, dk, dv], transposed: [N, H, dv, dk]; null: zero
     float* xT;                   // [N, H, dk, dv]; null: not wanted
     bool x0_transposed, reverse;
+    int32_t* status;
     float scale;                 // of what is read (forward) or written (reverse)
 };
 

@@ -32,6 +32,7 @@ int check_layout(int B, int num_seqs, const int32_t* cu) {
     if (cu ? B != 1 : num_seqs != B) return DR_ERR_INVALID_ARG;
     return reinterpret_cast<uintptr_t>(cu) & 3 ? DR_ERR_ALIGNMENT : DR_OK;
 }
+int check_status_word(const int32_t* status) { return reinterpret_cast<uintptr_t>(status) & 3 ? DR_ERR_ALIGNMENT : DR_OK; }
 
 int check_prompt(const dr_prompt_desc* d, bool bwd) {
     if (!d) return DR_ERR_INVALID_ARG;
@@ -44,7 +45,7 @@ int check_prompt(const dr_prompt_desc* d, bool bwd) {
     const long long lds[][2] = {{d->ld_q, q}, {d->ld_k, k}, {d->ld_v, k}, {d->ld_dq, q}, {d->ld_dk, k}, {d->ld_dv, k}};
     for (int i = 0; i < (bwd ? 6 : 3); ++i)
         if (int rc = check_row(lds[i][0], lds[i][1], d->io_dtype); rc != DR_OK) return rc;
-    return DR_OK;
+    return check_status_word(d->status);
 }
 dr::PromptParams prompt_params(const dr_prompt_desc* d, const void* q, const void* k, const void* v, const int32_t* cu) {
     dr::PromptParams p = {};
@@ -55,6 +56,7 @@ dr::PromptParams prompt_params(const dr_prompt_desc* d, const void* q, const voi
     p.ld_q = d->ld_q; p.ld_k = d->ld_k; p.ld_v = d->ld_v;
     p.ld_dq = d->ld_dq; p.ld_dk = d->ld_dk; p.ld_dv = d->ld_dv;
     p.q = q; p.k = k; p.v = v;
+    p.status = d->status;
     return p;
 }
 
@@ -70,14 +72,14 @@ int check_linear(const dr_linear_desc* d, bool bwd, bool step) {
     const long long lds[][2] = {{d->ld_q, q}, {d->ld_k, q}, {d->ld_v, v}, {d->ld_dq, q}, {d->ld_dk, q}, {d->ld_dv, v}};
     for (int i = 0; i < (bwd ? 6 : 3); ++i)
         if (int rc = check_row(lds[i][0], lds[i][1], d->io_dtype); rc != DR_OK) return rc;
-    return DR_OK;
+    return check_status_word(d->status);
 }
 dr::ScanParams scan_params(const dr_linear_desc* d, const float* g, const int32_t* cu) {
     dr::ScanParams p = {};
     p.s = {cu, d->num_seqs, d->T};
     p.rows = (long long)d->B * d->T;
     p.H = d->H; p.dk = d->d_k; p.dv = d->d_v;
-    p.g = g; p.scale = d->scale;
+    p.g = g; p.scale = d->scale; p.status = d->status;
     return p;
 }
 size_t linear_bytes(const dr_linear_desc*) { return 16; }
@@ -96,7 +98,8 @@ int dr_prompt_attn_fwd(const dr_prompt_desc* desc, const void* q, const void* k,
     if (!q || !k || !v || !o) return DR_ERR_INVALID_ARG;
     if (any_misaligned({q, k, v, o, lse})) return DR_ERR_ALIGNMENT;
     p.o = o; p.lse = lse;
-    return cuda_status(dr::prompt_attn_fwd_simt(p, desc->io_dtype, static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(desc->io_dtype == DR_BF16 ? dr::prompt_attn_fwd_tc(p, st) : dr::prompt_attn_fwd_simt(p, desc->io_dtype, st));
 }
 
 size_t dr_prompt_attn_workspace_bytes(const dr_prompt_desc* desc) {

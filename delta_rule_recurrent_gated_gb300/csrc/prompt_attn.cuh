@@ -16,10 +16,13 @@ struct PromptParams {
     void* o;                 // forward: written; backward: read
     float* lse;              // the same (forward: may be null)
     void *dq, *dk, *dv;
+    int32_t* status;
     float* delta;            // workspace: sum of dO o for each row and query head
 };
 
 // CUDA cores, bf16 or fp32 (prompt_attn.cu).
 cudaError_t prompt_attn_fwd_simt(const PromptParams& p, int io, cudaStream_t st);
 cudaError_t prompt_attn_bwd_simt(const PromptParams& p, int io, cudaStream_t st);
+// Tensor cores, bf16 (prompt_attn_tc.cu).
+cudaError_t prompt_attn_fwd_tc(const PromptParams& p, cudaStream_t st);
 }  // namespace dr

@@ -444,7 +444,8 @@ int dr_cache_attn(const dr_cache* cache, const dr_cache_seqs* seqs, const dr_att
  * Gradients of shared key heads are summed in a fixed order: the same inputs give the same bits.
  * A token that is not finite leaves other sequences alone; in its own it may also reach the results
  * of tokens that do not see it (a weight of zero times it).
- * Errors as dr_fwd.
+ * Errors as dr_fwd.  status: one device int32 the caller sets to zero, or NULL; a kernel whose bounded
+ * wait ran out records it there (dr_check_status: DR_ERR_TIMEOUT).
  *
  * Causal softmax attention: query i of a sequence sees its keys j <= i, and with window > 0 only
  * j > i - window; query head h reads key head h / (Hq / H).
@@ -462,6 +463,7 @@ typedef struct dr_prompt_desc {
     float scale;
     long long ld_q, ld_k, ld_v;
     long long ld_dq, ld_dk, ld_dv; /* backward                                          */
+    int32_t* status;
 } dr_prompt_desc;
 
 int dr_prompt_attn_fwd(const dr_prompt_desc* desc, const void* q, const void* k, const void* v,
@@ -495,6 +497,7 @@ typedef struct dr_linear_desc {
     float scale;
     long long ld_q, ld_k, ld_v;
     long long ld_dq, ld_dk, ld_dv; /* backward                                          */
+    int32_t* status;
 } dr_linear_desc;
 
 size_t dr_linear_attn_workspace_bytes(const dr_linear_desc* desc);
