@@ -52,7 +52,8 @@ dr::PromptParams prompt_params(const dr_prompt_desc* d, const void* q, const voi
     p.s = {cu, d->num_seqs, d->T};
     p.rows = (long long)d->B * d->T;
     p.Hq = d->Hq; p.H = d->H; p.G = d->Hq / d->H; p.d = d->d;
-    p.window = d->window; p.scale = d->scale;
+    p.window = d->window < d->T ? d->window : 0;  // one that shows everything is none
+    p.scale = d->scale;
     p.ld_q = d->ld_q; p.ld_k = d->ld_k; p.ld_v = d->ld_v;
     p.ld_dq = d->ld_dq; p.ld_dk = d->ld_dk; p.ld_dv = d->ld_dv;
     p.q = q; p.k = k; p.v = v;
@@ -122,7 +123,8 @@ int dr_prompt_attn_bwd(const dr_prompt_desc* desc, const void* q, const void* k,
     if (!workspace || workspace_bytes < dr_prompt_attn_workspace_bytes(desc)) return DR_ERR_WORKSPACE;
     p.o = const_cast<void*>(o); p.lse = const_cast<float*>(lse); p.dO = dO;
     p.dq = dq; p.dk = dk; p.dv = dv; p.delta = static_cast<float*>(workspace);
-    return cuda_status(dr::prompt_attn_bwd_simt(p, desc->io_dtype, static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cuda_status(desc->io_dtype == DR_BF16 ? dr::prompt_attn_bwd_tc(p, st) : dr::prompt_attn_bwd_simt(p, desc->io_dtype, st));
 }
 
 size_t dr_linear_attn_workspace_bytes(const dr_linear_desc* desc) {

@@ -336,14 +336,15 @@ template <int D, typename IO> cudaError_t fwd(const PromptParams& p, cudaStream_
     static std::atomic<unsigned long long> ready{0};
     return run("prompt_fwd", prompt_fwd_kernel<D, IO>, dim3(tiles(p), p.Hq), fwd_smem<D>(), ready, p, st);
 }
+template <int D, typename IO> cudaError_t delta(const PromptParams& p, cudaStream_t st) {
+    TraceScope ts("prompt_delta", st);
+    const long long n = (p.rows * p.Hq + kThreads / 8 - 1) / (kThreads / 8);
+    prompt_delta_kernel<D, IO><<<(unsigned)(n < 16384 ? n : 16384), kThreads, 0, st>>>(p);
+    return cudaGetLastError();
+}
 template <int D, typename IO> cudaError_t bwd(const PromptParams& p, cudaStream_t st) {
     static std::atomic<unsigned long long> ready[2] = {};
-    {
-        TraceScope ts("prompt_delta", st);
-        const long long n = (p.rows * p.Hq + kThreads / 8 - 1) / (kThreads / 8);
-        prompt_delta_kernel<D, IO><<<(unsigned)(n < 16384 ? n : 16384), kThreads, 0, st>>>(p);
-        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
-    }
+    if (cudaError_t e = delta<D, IO>(p, st); e != cudaSuccess) return e;
     if (cudaError_t e = run("prompt_dq", prompt_dq_kernel<D, IO>, dim3(tiles(p), p.Hq), bwd_smem<D>(), ready[0], p, st);
         e != cudaSuccess)
         return e;
@@ -355,6 +356,10 @@ template <int D, typename IO> cudaError_t bwd(const PromptParams& p, cudaStream_
 cudaError_t prompt_attn_fwd_simt(const PromptParams& p, int io, cudaStream_t st) {
     if (io == DR_F32) return p.d == 128 ? fwd<128, float>(p, st) : fwd<64, float>(p, st);
     return p.d == 128 ? fwd<128, __nv_bfloat16>(p, st) : fwd<64, __nv_bfloat16>(p, st);
+}
+cudaError_t prompt_attn_delta(const PromptParams& p, int io, cudaStream_t st) {
+    if (io == DR_F32) return p.d == 128 ? delta<128, float>(p, st) : delta<64, float>(p, st);
+    return p.d == 128 ? delta<128, __nv_bfloat16>(p, st) : delta<64, __nv_bfloat16>(p, st);
 }
 cudaError_t prompt_attn_bwd_simt(const PromptParams& p, int io, cudaStream_t st) {
     if (io == DR_F32) return p.d == 128 ? bwd<128, float>(p, st) : bwd<64, float>(p, st);

@@ -23,6 +23,9 @@ struct PromptParams {
 // CUDA cores, bf16 or fp32 (prompt_attn.cu).
 cudaError_t prompt_attn_fwd_simt(const PromptParams& p, int io, cudaStream_t st);
 cudaError_t prompt_attn_bwd_simt(const PromptParams& p, int io, cudaStream_t st);
-// Tensor cores, bf16 (prompt_attn_tc.cu).
+// p.delta, the first step of both.
+cudaError_t prompt_attn_delta(const PromptParams& p, int io, cudaStream_t st);
+// Tensor cores, bf16 (prompt_attn_tc.cu, prompt_attn_tc_bwd.cu).
 cudaError_t prompt_attn_fwd_tc(const PromptParams& p, cudaStream_t st);
+cudaError_t prompt_attn_bwd_tc(const PromptParams& p, cudaStream_t st);
 }  // namespace dr

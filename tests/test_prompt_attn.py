@@ -24,6 +24,7 @@ CASES = [  # lengths, packed, Hq, H, d, window, inside a projection
     ([0, 0, 3], True, 2, 1, 64, 0, False),
     ([127, 128, 129, 255, 256, 1], True, 4, 1, 64, 0, False),
     ([300, 31, 511], True, 2, 2, 128, 129, False),
+    ([300, 200], True, 2, 1, 64, 2 ** 31 - 1, False),
     ([1] * 70, True, 8, 2, 64, 0, False),
     ([17, 40, 3] * 14, True, 2, 1, 128, 9, True),
 ]
