@@ -31,6 +31,8 @@ struct ScanParams {
 
 // CUDA cores, any supported size (linear_attn.cu).
 cudaError_t linear_scan_simt(const ScanParams& p, int io, cudaStream_t st);
+// Tensor cores, bf16 with dk and dv 64 or 128, p.rows > 0 (linear_attn_tc.cu).
+cudaError_t linear_scan_tc(const ScanParams& p, cudaStream_t st);
 // The recurrent step: T tokens of every sequence on the caller's state.
 struct StepParams {
     int B, T, H, dk, dv;

@@ -83,6 +83,9 @@ dr::ScanParams scan_params(const dr_linear_desc* d, const float* g, const int32_
     p.g = g; p.scale = d->scale; p.status = d->status;
     return p;
 }
+cudaError_t scan(const dr::ScanParams& p, int io, cudaStream_t st) {
+    return io == DR_BF16 && p.rows > 0 ? dr::linear_scan_tc(p, st) : dr::linear_scan_simt(p, io, st);
+}
 size_t linear_bytes(const dr_linear_desc*) { return 16; }
 
 }  // namespace
@@ -145,7 +148,7 @@ int dr_linear_attn_fwd(const dr_linear_desc* desc, const void* q, const void* k,
     p.q = q; p.k = k; p.v = v; p.out = o;
     p.ld_q = desc->ld_q; p.ld_k = desc->ld_k; p.ld_v = desc->ld_v; p.ld_o = (long long)desc->H * desc->d_v;
     p.x0 = h0; p.xT = hT;
-    return cuda_status(dr::linear_scan_simt(p, desc->io_dtype, static_cast<cudaStream_t>(stream)));
+    return cuda_status(scan(p, desc->io_dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int dr_linear_attn_bwd(const dr_linear_desc* desc, const void* q, const void* k, const void* v,
@@ -167,20 +170,20 @@ int dr_linear_attn_bwd(const dr_linear_desc* desc, const void* q, const void* k,
     x.q = dO; x.k = v; x.v = k; x.out = dq;
     x.ld_q = ld_g; x.ld_k = desc->ld_v; x.ld_v = desc->ld_k; x.ld_o = desc->ld_dq;
     x.x0 = h0; x.x0_transposed = true;
-    cudaError_t e = base.rows ? dr::linear_scan_simt(x, desc->io_dtype, st) : cudaSuccess;
+    cudaError_t e = base.rows ? scan(x, desc->io_dtype, st) : cudaSuccess;
     if (e != cudaSuccess) return DR_ERR_CUDA;
     x.reverse = true;         // dk: (v, dO, q) from the last token to the first
     x.q = v; x.k = dO; x.v = q; x.out = dk;
     x.ld_q = desc->ld_v; x.ld_k = ld_g; x.ld_v = desc->ld_q; x.ld_o = desc->ld_dk;
     x.x0 = dhT;
-    e = base.rows ? dr::linear_scan_simt(x, desc->io_dtype, st) : cudaSuccess;
+    e = base.rows ? scan(x, desc->io_dtype, st) : cudaSuccess;
     if (e != cudaSuccess) return DR_ERR_CUDA;
     x = base;                 // dv: (k, q, dO) likewise
     x.reverse = true;
     x.q = k; x.k = q; x.v = dO; x.out = dv;
     x.ld_q = desc->ld_k; x.ld_k = desc->ld_q; x.ld_v = ld_g; x.ld_o = desc->ld_dv;
     x.x0 = dhT; x.xT = dh0;
-    return cuda_status(dr::linear_scan_simt(x, desc->io_dtype, st));
+    return cuda_status(scan(x, desc->io_dtype, st));
 }
 
 int dr_linear_attn_step(const dr_linear_desc* desc, const void* q, const void* k, const void* v,
