@@ -11,8 +11,9 @@
 // chunk's queries.  K' is a sum of two bf16 parts (2^-16 of it is lost), so that what the states add up over a
 // sequence is not bf16; P, and the state as an operand, are rounded once (2^-8 at most).
 // Tensor memory: A with P over it, Q X, P V, K'^T V: 4 x 128 columns.
-// Warps 0-3: P, then the output rows.  4-7: K' (its high part over K, once A is there).  8-11: state.  12: products,
+// Warps 0-3: K' (its high part over K, once A is there), then P.  4-7: output rows.  8-11: state.  12: products,
 // 13: copies, through a ring of five tiles in the order K, Q, V.
+#include "f32x2.cuh"
 #include "linear_attn.cuh"
 #include "tc_block.cuh"
 #include "trace.cuh"
@@ -23,15 +24,16 @@ namespace {
 
 constexpr int kC = 128, kThreads = 512, kSlots = 5;
 // Registers of a thread: as launched, then of the four groups of four warps.
-constexpr int kRegs = 128, kOutRegs = 128, kKeyRegs = 96, kStateRegs = 208, kOtherRegs = 80;
-static_assert(kOutRegs + kKeyRegs + kStateRegs + kOtherRegs <= 4 * kRegs, "more than the block has");
+constexpr int kRegs = 128, kWeightRegs = 112, kOutRegs = 112, kStateRegs = 208, kOtherRegs = 80;
+static_assert(kWeightRegs + kOutRegs + kStateRegs + kOtherRegs <= 4 * kRegs, "more than the block has");
 constexpr uint32_t kA = 0, kQX = 128, kPV = 256, kKV = 384;  // columns of tensor memory
 
 struct Control {
     uint64_t full[kSlots], empty[kSlots], landed, afull, pfull, kfull, dfull, xfull, ofull, oempty, drained;
     uint32_t tmem;
     volatile int dead;
-    float power[kC];  // beta a^n
+    __align__(16) float power[kC];  // beta a^n
+    __align__(16) float column[32];  // a^{31 - j}, reverse a^j
 };
 template <int DK, int DV> struct Smem {
     static constexpr int slot = kC * (DK > DV ? DK : DV) * 2, low = kSlots * slot, x = low + kC * DK * 2,
@@ -109,7 +111,6 @@ __device__ __forceinline__ void issue(const Work& w, uint8_t* smem, Control& ct)
             for (int kk = 0; kk < DK; kk += 16)
                 mma_bf16(tm + kQX, row0 + q + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8, x0 + kk * 8,
                          idesc_bf16(kC, DV, false, true), kk > 0);
-            mma_commit(&ct.empty[slot[1]]);
         }
         __syncwarp();
         if (!wait(ct.dead, &ct.full[slot[2]], ((u - 1) / kSlots) & 1) || !wait(ct.dead, &ct.kfull, n & 1)) return;
@@ -138,40 +139,91 @@ __device__ __forceinline__ void issue(const Work& w, uint8_t* smem, Control& ct)
     }
 }
 
-// Warps 0-3: a token per thread.
-template <int DV> __device__ __forceinline__ void outputs(const ScanParams& p, const Work& w, int head, Control& ct) {
+// The parts hi + lo of f times two bf16 values: what hi, rounded, leaves of a value is rounded to lo.
+__device__ __forceinline__ void split2(uint32_t u, float f, uint32_t& hi, uint32_t& lo) {
+    const float2 x = mul2(make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u)), both(f));
+    hi = pack_bf16(x.x, x.y);
+    lo = pack_bf16(x.x - __uint_as_float(hi << 16), x.y - __uint_as_float(hi & 0xffff0000u));
+}
+// Warps 0-3, a token per thread: K', which the state waits for, then P.
+template <int DK, int DV> __device__ __forceinline__ void weights(const ScanParams& p, const Work& w, int head, uint8_t* smem, Control& ct) {
     const int i = threadIdx.x, warp = i >> 5;
     const uint32_t tm = warp_lane_base(ct.tmem);
-    const float g = p.g[head], f_out = p.reverse ? 1.f : p.scale;
+    const float g = p.g[head], f_in = p.reverse ? p.scale : 1.f;
     for (int n = 0; n < w.chunks; ++n) {
-        const int first = w.at(p, n), tokens = w.tokens(first);
-        if (!wait(ct.dead, &ct.afull, n & 1)) return;
+        const uint32_t u = 3 * n;
+        const int tokens = w.tokens(w.at(p, n));
+        const float f = i < tokens ? f_in * decay(g, (float)(p.reverse ? i + 1 : tokens - 1 - i)) : 0.f;
+        uint8_t* tile = smem + u % kSlots * Smem<DK, DV>::slot;
+        if (!wait(ct.dead, &ct.full[u % kSlots], (u / kSlots) & 1) || !wait(ct.dead, &ct.afull, n & 1)) return;
+        if (n && !wait(ct.dead, &ct.dfull, (n - 1) & 1)) return;  // the low parts of the chunk before are in use
         tc_fence_after();
+#pragma unroll 4
+        for (int c = 0; c < DK; c += 8) {
+            const uint32_t off = sw128_offset(i, c, kC);
+            uint4 u = *reinterpret_cast<const uint4*>(tile + off), hi, lo;
+            if (tokens < kC && i >= tokens) u = make_uint4(0, 0, 0, 0);  // behind the sequence: may be no numbers
+            split2(u.x, f, hi.x, lo.x);
+            split2(u.y, f, hi.y, lo.y);
+            split2(u.z, f, hi.z, lo.z);
+            split2(u.w, f, hi.w, lo.w);
+            *reinterpret_cast<uint4*>(tile + off) = hi;
+            *reinterpret_cast<uint4*>(smem + Smem<DK, DV>::low + off) = lo;
+        }
+        fence_async_smem();
+        warp_arrive(&ct.kfull);
+        // 32 columns at a time: those that all the warp's rows see take a^{|i-j|} as a row's and a column's factor,
+        // both at most one; those on the diagonal one of the powers each; the others are zero
 #pragma unroll
-        for (int c = 0; c < kC; c += 64) {
-            float s[64];
-            uint32_t z[32];
-            if (p.reverse ? c + 63 >= 32 * warp : c <= 32 * warp + 31) {  // the warp's rows meet these columns
-                tmem_ld32(tm + kA + c, s);
-                tmem_ld32(tm + kA + c + 32, s + 32);
-                tmem_ld_wait();
+        for (int b = 0; b < 4; ++b) {
+            float s[32];
+            uint32_t z[16];
+            const int c = 32 * b;
+            if (p.reverse ? b < warp : b > warp) {
 #pragma unroll
-                for (int j = 0; j < 64; ++j) {
-                    const int back = p.reverse ? c + j - i : i - c - j;
-                    s[j] = back >= 0 && c + j < tokens ? s[j] * ct.power[max(back, 0)] : 0.f;
-                }
+                for (int j = 0; j < 16; ++j) z[j] = 0;
             } else {
+                tmem_ld32(tm + kA + c, s);
+                tmem_ld_wait();
+                if (b == warp || (p.reverse && tokens < kC)) {
 #pragma unroll
-                for (int j = 0; j < 64; ++j) s[j] = 0.f;
+                    for (int j = 0; j < 32; ++j) {
+                        const int back = p.reverse ? c + j - i : i - c - j;
+                        s[j] = back >= 0 && c + j < tokens ? s[j] * ct.power[max(back, 0)] : 0.f;
+                    }
+                } else {
+                    const float2 fr = both(p.reverse ? ct.power[c - i] : ct.power[i - c - 31]);
+                    const float4* fc = reinterpret_cast<const float4*>(ct.column);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        const float4 y = fc[j / 4];
+                        const float2 t0 = mul2(make_float2(s[j], s[j + 1]), mul2(fr, make_float2(y.x, y.y)));
+                        const float2 t1 = mul2(make_float2(s[j + 2], s[j + 3]), mul2(fr, make_float2(y.z, y.w)));
+                        s[j] = t0.x; s[j + 1] = t0.y; s[j + 2] = t1.x; s[j + 3] = t1.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j) z[j] = pack_bf16(s[2 * j], s[2 * j + 1]);
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) z[j] = pack_bf16(s[2 * j], s[2 * j + 1]);
-            tmem_st32(tm + kA + c / 2, z);
+            tmem_st16(tm + kA + c / 2, z);
         }
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(&ct.pfull);
-        const float f = decay(g, (float)(p.reverse ? tokens - 1 - i : i + 1));
+    }
+}
+
+// Warps 4-7, a token per thread.  A whole chunk's rows leave as tensor stores, from the place of its queries.
+template <int DK, int DV>
+__device__ __forceinline__ void outputs(const ScanParams& p, const Work& w, int head, const CUtensorMap* mo, uint8_t* smem, Control& ct) {
+    const int i = threadIdx.x & (kC - 1);
+    const uint32_t tm = warp_lane_base(ct.tmem);
+    const float g = p.g[head], f_out = p.reverse ? 1.f : p.scale;
+    for (int n = 0; n < w.chunks; ++n) {
+        const int first = w.at(p, n), tokens = w.tokens(first);
+        const uint32_t slot = (3 * n + 1) % kSlots;
+        uint8_t* tile = smem + slot * Smem<DK, DV>::slot;
+        const float2 fx = both(f_out * decay(g, (float)(p.reverse ? tokens - 1 - i : i + 1))), fy = both(f_out);
         if (!wait(ct.dead, &ct.ofull, n & 1)) return;
         tc_fence_after();
         __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + (w.row0 + first + i) * p.ld_o + (long long)head * DV;
@@ -185,45 +237,33 @@ template <int DV> __device__ __forceinline__ void outputs(const ScanParams& p, c
                 tc_fence_before();
                 warp_arrive(&ct.oempty);
             }
+            uint32_t z[16];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) y[j] = f_out * fmaf(f, x[j], y[j]);
-            if (i < tokens)
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    reinterpret_cast<uint4*>(to + c)[j] = make_uint4(pack_bf16(y[8 * j], y[8 * j + 1]), pack_bf16(y[8 * j + 2], y[8 * j + 3]),
-                                                                     pack_bf16(y[8 * j + 4], y[8 * j + 5]), pack_bf16(y[8 * j + 6], y[8 * j + 7]));
-        }
-    }
-}
-
-// Warps 4-7: a token per thread.
-template <int DK, int DV> __device__ __forceinline__ void keys(const ScanParams& p, const Work& w, int head, uint8_t* smem, Control& ct) {
-    const int j = threadIdx.x & (kC - 1);
-    const float g = p.g[head], f_in = p.reverse ? p.scale : 1.f;
-    for (int n = 0; n < w.chunks; ++n) {
-        const uint32_t u = 3 * n;
-        const int tokens = w.tokens(w.at(p, n));
-        const float f = j < tokens ? f_in * decay(g, (float)(p.reverse ? j + 1 : tokens - 1 - j)) : 0.f;
-        uint8_t* tile = smem + u % kSlots * Smem<DK, DV>::slot;
-        if (!wait(ct.dead, &ct.full[u % kSlots], (u / kSlots) & 1) || !wait(ct.dead, &ct.afull, n & 1)) return;
-        if (n && !wait(ct.dead, &ct.dfull, (n - 1) & 1)) return;  // the low parts of the chunk before are in use
-#pragma unroll 4
-        for (int c = 0; c < DK; c += 8) {
-            uint8_t* at = tile + sw128_offset(j, c, kC);
-            float x[8], hi[8], lo[8];
-            unpack8(*reinterpret_cast<const uint4*>(at), x);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                x[q] = j < tokens ? x[q] * f : 0.f;  // what is behind the sequence may be no number
-                hi[q] = __bfloat162float(__float2bfloat16_rn(x[q]));
-                lo[q] = x[q] - hi[q];
+            for (int j = 0; j < 16; ++j) {
+                const float2 o = fma2(fx, make_float2(x[2 * j], x[2 * j + 1]), mul2(fy, make_float2(y[2 * j], y[2 * j + 1])));
+                z[j] = pack_bf16(o.x, o.y);
             }
-            tile_store8(tile, j, c, kC, hi);
-            tile_store8(smem + Smem<DK, DV>::low, j, c, kC, lo);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 u = make_uint4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
+                if (tokens == kC) *reinterpret_cast<uint4*>(tile + sw128_offset(i, c + 8 * j, kC)) = u;
+                else if (i < tokens) reinterpret_cast<uint4*>(to + c)[j] = u;
+            }
         }
-        fence_async_smem();
-        warp_arrive(&ct.kfull);
+        if (tokens == kC) fence_async_smem();
+        asm volatile("bar.sync 1, 128;" ::: "memory");
+        if (i == 0) {
+            if (tokens == kC) {
+#pragma unroll
+                for (int c = 0; c < DV; c += 64) tma_store_3d(mo, tile + (c / 64) * kC * 128, c, head, w.row0 + first);
+                bulk_commit();
+                bulk_wait_read();
+            }
+            mbar_arrive(&ct.empty[slot]);
+        }
+        __syncwarp();
     }
+    if (i == 0) bulk_wait_all();
 }
 
 // Warps 8-11: a row of the state per thread (of the first DK).
@@ -285,7 +325,7 @@ __device__ __forceinline__ void states(const ScanParams& p, const Work& w, int s
 template <int DK, int DV>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_scan_tc_kernel(const ScanParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                          const __grid_constant__ CUtensorMap mv) {
+                          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Control& ct = *reinterpret_cast<Control*>(smem + Smem<DK, DV>::control);
     const int warp = threadIdx.x >> 5, seq = blockIdx.x / p.H, head = blockIdx.x % p.H;
@@ -304,6 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_barrier_init();
     }
     if (threadIdx.x < kC) ct.power[threadIdx.x] = (p.reverse ? p.scale : 1.f) * decay(p.g[head], (float)threadIdx.x);
+    if (threadIdx.x < 32) ct.column[threadIdx.x] = decay(p.g[head], (float)(p.reverse ? threadIdx.x : 31 - threadIdx.x));
     Work w;
     seq_rows(p.s, seq, w.row0, w.len);
     w.chunks = (w.len + kC - 1) / kC;
@@ -311,10 +352,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     if (warp < 4) {
-        outputs<DV>(p, w, head, ct);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWeightRegs));
+        weights<DK, DV>(p, w, head, smem, ct);
     } else if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kKeyRegs));
-        keys<DK, DV>(p, w, head, smem, ct);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
+        outputs<DK, DV>(p, w, head, &mo, smem, ct);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
         states<DK, DV>(p, w, seq, head, smem, ct);
@@ -340,12 +382,12 @@ template <int DK, int DV> cudaError_t launch(const ScanParams& p, cudaStream_t s
     }();
     if (!fits) return cudaErrorInvalidConfiguration;
     if (cudaError_t e = set_smem_once(linear_scan_tc_kernel<DK, DV>, Smem<DK, DV>::bytes, ready); e != cudaSuccess) return e;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mo;
     if (!head_rows_map(&mq, p.q, DK, p.H, p.rows, p.ld_q, kC) || !head_rows_map(&mk, p.k, DK, p.H, p.rows, p.ld_k, kC) ||
-        !head_rows_map(&mv, p.v, DV, p.H, p.rows, p.ld_v, kC))
+        !head_rows_map(&mv, p.v, DV, p.H, p.rows, p.ld_v, kC) || !head_rows_map(&mo, p.out, DV, p.H, p.rows, p.ld_o, kC))
         return cudaErrorInvalidValue;
     TraceScope ts("linear_scan_tc", st);
-    linear_scan_tc_kernel<DK, DV><<<p.s.N * p.H, kThreads, Smem<DK, DV>::bytes, st>>>(p, mq, mk, mv);
+    linear_scan_tc_kernel<DK, DV><<<p.s.N * p.H, kThreads, Smem<DK, DV>::bytes, st>>>(p, mq, mk, mv, mo);
     return cudaGetLastError();
 }
 
