@@ -27,7 +27,18 @@ struct ScanParams {
     bool x0_transposed, reverse;
     int32_t* status;
     float scale;                 // of what is read (forward) or written (reverse)
+    int span;                    // chunks of a segment; 0: sequences are not split
+    long long slots;             // segments that the workspace has room for
+    float* part;                 // their states, [slots, H, dk, dv]
+    bool wide_out;               // set by the launcher: rows of out begin at multiples of 32 bytes
 };
+
+// Long sequences are split where a block for each sequence and head would leave most of the GPU idle: first every
+// segment's own state is formed from nothing, then the states that they begin with are the running sums of
+// these, and then all segments are scanned at once.  The first step reads k and v once more.
+constexpr int kScanChunk = 128;
+int scan_span(long long rows, int N, int T, bool packed, int H);       // p.span
+long long scan_slots(long long rows, int span);                        // p.slots
 
 // CUDA cores, any supported size (linear_attn.cu).
 cudaError_t linear_scan_simt(const ScanParams& p, int io, cudaStream_t st);

@@ -6,13 +6,16 @@
 //   forward: out(i) = i + 1, in(j) = n - 1 - j;  reverse: out(i) = n - 1 - i, in(j) = j + 1
 // so no power of a is ever above one, however strong the decay.
 //
-// A block has a sequence and a head.  The state stays in fp32 registers, a row of it in each thread of four warps;
-// what a chunk adds comes from tensor memory, and a bf16 image of the state goes to shared memory for the next
-// chunk's queries.  K' is a sum of two bf16 parts (2^-16 of it is lost), so that what the states add up over a
-// sequence is not bf16; P, and the state as an operand, are rounded once (2^-8 at most).
+// A block has a sequence, or a segment of one, and a head.  The state stays in fp32 registers, a row of it in each
+// thread of four warps; what a chunk adds comes from tensor memory, and a bf16 image of the state goes to shared memory
+// for the next chunk's queries.  K' is a sum of two bf16 parts (2^-16 of it is lost), so that what the states add up over
+// a sequence is not bf16; P, and the state as an operand, are rounded once (2^-8 at most).
 // Tensor memory: A with P over it, Q X, P V, K'^T V: 4 x 128 columns.
-// Warps 0-3: K' (its high part over K, once A is there), then P.  4-7: output rows.  8-11: state.  12: products,
-// 13: copies, through a ring of five tiles in the order K, Q, V.
+// Warps 0-3: P.  4-7: K' (its high part over K, once A is there).  8-11: output rows.  12-15: state.  16: products,
+// 17: copies, through a ring of five tiles in the order K, Q, V.
+//
+// The products of a chunk are issued as P V (n), A (n + 1), K'V (n), Q X (n), each when what it needs is there: P and K'
+// of the next chunk are formed while the last two run.
 #include "f32x2.cuh"
 #include "linear_attn.cuh"
 #include "tc_block.cuh"
@@ -22,14 +25,16 @@
 namespace dr {
 namespace {
 
-constexpr int kC = 128, kThreads = 512, kSlots = 5;
-// Registers of a thread: as launched, then of the four groups of four warps.
-constexpr int kRegs = 128, kWeightRegs = 112, kOutRegs = 112, kStateRegs = 208, kOtherRegs = 80;
-static_assert(kWeightRegs + kOutRegs + kStateRegs + kOtherRegs <= 4 * kRegs, "more than the block has");
+constexpr int kC = kScanChunk, kThreads = 640, kSlots = 5;
+// Registers of a thread: as launched, then of the five groups of four warps.
+constexpr int kRegs = 96, kWeightRegs = 88, kKeyRegs = 72, kOutRegs = 96, kStateRegs = 176, kOtherRegs = 48;
+static_assert(kWeightRegs + kKeyRegs + kOutRegs + kStateRegs + kOtherRegs <= 5 * kRegs, "more than the block has");
+// Segments: blocks for all SMs; what is split at all; chunks of a segment.
+constexpr int kSms = 152, kSplitFrom = 12, kLeastSpan = 4;
 constexpr uint32_t kA = 0, kQX = 128, kPV = 256, kKV = 384;  // columns of tensor memory
 
 struct Control {
-    uint64_t full[kSlots], empty[kSlots], landed, afull, pfull, kfull, dfull, xfull, ofull, oempty, drained;
+    uint64_t full[kSlots], empty[kSlots], landed, afull, akeys, pfull, kfull, dfull, dread, xfull, ofull, oempty, drained;
     uint32_t tmem;
     volatile int dead;
     __align__(16) float power[kC];  // beta a^n
@@ -43,13 +48,39 @@ template <int DK, int DV> struct Smem {
     static_assert(sizeof(Control) <= 1024, "control block");
 };
 
+// A block's chunks: all of a sequence or a segment of them.
 struct Work {
-    int row0, len, chunks;
-    __device__ __forceinline__ int at(const ScanParams& p, int n) const { return (p.reverse ? chunks - 1 - n : n) * kC; }
-    __device__ __forceinline__ int tokens(int first) const { return min(kC, len - first); }
+    int seq, row0, len, c0, chunks;
+    bool first, last;       // of the sequence's segments in the order of the scan
+    const float* before;    // the state before a segment that is not the only one (first step: where its own goes)
+    __device__ __forceinline__ int at(const ScanParams& p, int n) const { return (c0 + (p.reverse ? chunks - 1 - n : n)) * kC; }
+    __device__ __forceinline__ int tokens(int at) const { return min(kC, len - at); }
 };
+__device__ __forceinline__ bool make_work(const ScanParams& p, int item, int head, Work& w) {
+    const int span = p.span ? p.span : (1 << 30) / kC;
+    int tile, tiles;
+    long long slot;
+    if (!find_tile_in_order(p.s, span * kC, item, w.seq, tile, tiles, slot)) return false;
+    seq_rows(p.s, w.seq, w.row0, w.len);
+    w.c0 = tile * span;
+    w.chunks = min(span, (w.len + kC - 1) / kC - w.c0);
+    w.first = p.reverse ? tile == tiles - 1 : tile == 0;
+    w.last = p.reverse ? tile == 0 : tile == tiles - 1;
+    if (tiles > 1 && slot + tiles > p.slots) return false;  // offsets out of order: sequences that overlap
+    w.before = tiles > 1 ? p.part + ((slot + tile) * p.H + head) * p.dk * p.dv : nullptr;
+    return true;
+}
 
-template <int DK, int DV>
+// Items of a launch: segments of the sequences, a sequence without tokens as one.
+long long scan_items(const ScanParams& p) {
+    const long long R = (p.span ? p.span : (1 << 30) / kC) * (long long)kC;
+    return p.s.cu ? p.s.T / R + p.s.N : p.s.N * ((p.s.T + R - 1) / R);
+}
+
+// What goes through the ring for a chunk: K, Q, V, or K, V where only states are formed.
+template <bool ONLY> constexpr int kTiles = ONLY ? 2 : 3;
+
+template <int DK, int DV, bool ONLY>
 __device__ __forceinline__ void copy_tiles(const ScanParams& p, const Work& w, int head, const CUtensorMap* mq,
                                            const CUtensorMap* mk, const CUtensorMap* mv, uint8_t* smem, Control& ct) {
     const int lane = threadIdx.x & 31;
@@ -57,15 +88,16 @@ __device__ __forceinline__ void copy_tiles(const ScanParams& p, const Work& w, i
     for (int n = 0; n < w.chunks; ++n) {
         const int first = w.at(p, n), row = w.row0 + first, rows = w.tokens(first);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < kTiles<ONLY>; ++i) {
+            constexpr int V = kTiles<ONLY> - 1;
             if (!wait(ct.dead, &ct.empty[slot], parity)) return;
             uint8_t* tile = smem + slot * Smem<DK, DV>::slot;
             // values behind the sequence are summed with weights of zero: they have to be numbers
-            const bool cut = i == 2 && rows < kC;
+            const bool cut = i == V && rows < kC;
             uint64_t* bar = cut ? &ct.landed : &ct.full[slot];
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar, kC * (i == 2 ? DV : DK) * 2);
-                if (i == 2) load_rows<kC, DV>(tile, mv, bar, head, row);
+                mbar_arrive_expect_tx(bar, kC * (i == V ? DV : DK) * 2);
+                if (i == V) load_rows<kC, DV>(tile, mv, bar, head, row);
                 else load_rows<kC, DK>(tile, i == 0 ? mk : mq, bar, head, row);
             }
             __syncwarp();
@@ -80,64 +112,94 @@ __device__ __forceinline__ void copy_tiles(const ScanParams& p, const Work& w, i
     }
 }
 
-template <int DK, int DV>
-__device__ __forceinline__ void issue(const Work& w, uint8_t* smem, Control& ct) {
+template <int DK, int DV, bool ONLY> struct Issuer {
     using S = Smem<DK, DV>;
-    const uint32_t base = smem_u32(smem), tm = ct.tmem;
-    const uint64_t row0 = desc_kmajor(Tile{base, kC}, 0), col0 = desc_mnmajor(Tile{base, kC}, 0);  // of slot 0
-    const uint64_t low0 = desc_mnmajor(Tile{base + S::low, kC}, 0), x0 = desc_mnmajor(Tile{base + S::x, DK}, 0);
-    uint32_t u = 0;
-    for (int n = 0; n < w.chunks; ++n) {
-        uint32_t slot[3];
-#pragma unroll
-        for (int i = 0; i < 3; ++i, ++u) {
-            slot[i] = u % kSlots;
-            if (i < 2 && !wait(ct.dead, &ct.full[slot[i]], (u / kSlots) & 1)) return;
-        }
-        const uint64_t k = slot[0] * (S::slot >> 4), q = slot[1] * (S::slot >> 4), v = slot[2] * (S::slot >> 4);
+    static constexpr int N = kTiles<ONLY>;
+    Control& ct;
+    uint32_t tm;
+    uint64_t row0, col0, low0, x0;  // descriptors: of slot 0, by rows and by columns; of the low parts; of the state
+    __device__ __forceinline__ Issuer(uint8_t* smem, Control& c) : ct(c), tm(c.tmem) {
+        const uint32_t base = smem_u32(smem);
+        row0 = desc_kmajor(Tile{base, kC}, 0);
+        col0 = desc_mnmajor(Tile{base, kC}, 0);
+        low0 = desc_mnmajor(Tile{base + S::low, kC}, 0);
+        x0 = desc_mnmajor(Tile{base + S::x, DK}, 0);
+    }
+    static __device__ __forceinline__ uint32_t slot(int n, int i) { return (uint32_t)(N * n + i) % kSlots; }
+    static __device__ __forceinline__ uint64_t at(int n, int i) { return slot(n, i) * (uint64_t)(S::slot >> 4); }
+    __device__ __forceinline__ bool arrived(int n, int i) {
+        return wait(ct.dead, &ct.full[slot(n, i)], ((uint32_t)(N * n + i) / kSlots) & 1);
+    }
+    __device__ __forceinline__ bool scores(int n) {  // A
+        if (!arrived(n, 0) || !arrived(n, 1)) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < DK; kk += 16)  // 16 channels: 32 bytes of a 128-byte row
-                mma_bf16(tm + kA, row0 + q + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8,
-                         row0 + k + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8, idesc_bf16(kC, kC), kk > 0);
+                mma_bf16(tm + kA, row0 + at(n, 1) + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8,
+                         row0 + at(n, 0) + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8, idesc_bf16(kC, kC), kk > 0);
             mma_commit(&ct.afull);
+            mma_commit(&ct.akeys);
         }
         __syncwarp();
-        if (!wait(ct.dead, &ct.xfull, n & 1) || !wait(ct.dead, &ct.oempty, (n & 1) ^ 1)) return;
+        return true;
+    }
+    __device__ __forceinline__ bool values(int n) {  // P V
+        if (!wait(ct.dead, &ct.pfull, n & 1) || !wait(ct.dead, &ct.oempty, (n & 1) ^ 1)) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < DK; kk += 16)
-                mma_bf16(tm + kQX, row0 + q + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8, x0 + kk * 8,
-                         idesc_bf16(kC, DV, false, true), kk > 0);
+            for (int kk = 0; kk < kC; kk += 16)  // 16 tokens: 16 rows of 128 bytes
+                mma_ts(tm + kPV, tm + kA + kk / 2, col0 + at(n, N - 1) + kk * 8, idesc_bf16(kC, DV, false, true), kk > 0);
         }
         __syncwarp();
-        if (!wait(ct.dead, &ct.full[slot[2]], ((u - 1) / kSlots) & 1) || !wait(ct.dead, &ct.kfull, n & 1)) return;
+        return true;
+    }
+    __device__ __forceinline__ bool added(int n) {  // K'V
+        if (!wait(ct.dead, &ct.kfull, n & 1) || !wait(ct.dead, &ct.dread, (n & 1) ^ 1)) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
             for (int part = 0; part < 2; ++part)
 #pragma unroll
-                for (int kk = 0; kk < kC; kk += 16)  // 16 tokens: 16 rows of 128 bytes
-                    mma_bf16(tm + kKV, (part ? low0 : col0 + k) + kk * 8, col0 + v + kk * 8, idesc_bf16(128, DV, true, true),
-                             part + kk > 0);
+                for (int kk = 0; kk < kC; kk += 16)
+                    mma_bf16(tm + kKV, (part ? low0 : col0 + at(n, 0)) + kk * 8, col0 + at(n, N - 1) + kk * 8,
+                             idesc_bf16(128, DV, true, true), part + kk > 0);
             mma_commit(&ct.dfull);
-            mma_commit(&ct.empty[slot[0]]);
+            mma_commit(&ct.empty[slot(n, 0)]);
+            mma_commit(&ct.empty[slot(n, N - 1)]);  // after P V too
         }
         __syncwarp();
-        if (!wait(ct.dead, &ct.pfull, n & 1)) return;
+        return true;
+    }
+    __device__ __forceinline__ bool reads(int n) {  // Q X
+        if (!wait(ct.dead, &ct.xfull, n & 1)) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < kC; kk += 16)
-                mma_ts(tm + kPV, tm + kA + kk / 2, col0 + v + kk * 8, idesc_bf16(kC, DV, false, true), kk > 0);
+            for (int kk = 0; kk < DK; kk += 16)
+                mma_bf16(tm + kQX, row0 + at(n, 1) + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8, x0 + kk * 8,
+                         idesc_bf16(kC, DV, false, true), kk > 0);
             mma_commit(&ct.ofull);
-            mma_commit(&ct.empty[slot[2]]);
+            mma_commit(&ct.empty[slot(n, 1)]);
         }
         __syncwarp();
+        return true;
     }
-}
+    __device__ __forceinline__ void run(int chunks) {
+        if (ONLY) {
+            for (int n = 0; n < chunks; ++n)
+                if (!arrived(n, 1) || !added(n)) return;
+            return;
+        }
+        if (chunks > 0 && !scores(0)) return;
+        for (int n = 0; n < chunks; ++n) {
+            if (!arrived(n, 2) || !values(n)) return;
+            if (n + 1 < chunks && !scores(n + 1)) return;
+            if (!added(n) || !reads(n)) return;
+        }
+    }
+};
 
 // The parts hi + lo of f times two bf16 values: what hi, rounded, leaves of a value is rounded to lo.
 __device__ __forceinline__ void split2(uint32_t u, float f, uint32_t& hi, uint32_t& lo) {
@@ -145,35 +207,54 @@ __device__ __forceinline__ void split2(uint32_t u, float f, uint32_t& hi, uint32
     hi = pack_bf16(x.x, x.y);
     lo = pack_bf16(x.x - __uint_as_float(hi << 16), x.y - __uint_as_float(hi & 0xffff0000u));
 }
-// Warps 0-3, a token per thread: K', which the state waits for, then P.
-template <int DK, int DV> __device__ __forceinline__ void weights(const ScanParams& p, const Work& w, int head, uint8_t* smem, Control& ct) {
-    const int i = threadIdx.x, warp = i >> 5;
-    const uint32_t tm = warp_lane_base(ct.tmem);
+// Warps 4-7, a token per thread: K'.
+template <int DK, int DV, bool ONLY>
+__device__ __forceinline__ void keys(const ScanParams& p, const Work& w, int head, uint8_t* smem, Control& ct) {
+    const int j = threadIdx.x & (kC - 1);
     const float g = p.g[head], f_in = p.reverse ? p.scale : 1.f;
     for (int n = 0; n < w.chunks; ++n) {
-        const uint32_t u = 3 * n;
+        const uint32_t u = kTiles<ONLY> * n;
         const int tokens = w.tokens(w.at(p, n));
-        const float f = i < tokens ? f_in * decay(g, (float)(p.reverse ? i + 1 : tokens - 1 - i)) : 0.f;
+        const float f = j < tokens ? f_in * decay(g, (float)(p.reverse ? j + 1 : tokens - 1 - j)) : 0.f;
         uint8_t* tile = smem + u % kSlots * Smem<DK, DV>::slot;
-        if (!wait(ct.dead, &ct.full[u % kSlots], (u / kSlots) & 1) || !wait(ct.dead, &ct.afull, n & 1)) return;
-        if (n && !wait(ct.dead, &ct.dfull, (n - 1) & 1)) return;  // the low parts of the chunk before are in use
-        tc_fence_after();
-#pragma unroll 4
-        for (int c = 0; c < DK; c += 8) {
-            const uint32_t off = sw128_offset(i, c, kC);
-            uint4 u = *reinterpret_cast<const uint4*>(tile + off), hi, lo;
-            if (tokens < kC && i >= tokens) u = make_uint4(0, 0, 0, 0);  // behind the sequence: may be no numbers
-            split2(u.x, f, hi.x, lo.x);
-            split2(u.y, f, hi.y, lo.y);
-            split2(u.z, f, hi.z, lo.z);
-            split2(u.w, f, hi.w, lo.w);
-            *reinterpret_cast<uint4*>(tile + off) = hi;
-            *reinterpret_cast<uint4*>(smem + Smem<DK, DV>::low + off) = lo;
+        if (!wait(ct.dead, &ct.full[u % kSlots], (u / kSlots) & 1)) return;
+        if (!ONLY) {  // A needs the keys as they came; it is formed up to a chunk ahead of this, so its phases count both
+            warp_arrive(&ct.akeys);
+            if (!wait(ct.dead, &ct.akeys, n & 1)) return;
+        }
+        if (n && !wait(ct.dead, &ct.dfull, (n - 1) & 1)) return;       // low parts of the chunk before are in use
+#pragma unroll 1
+        for (int c = 0; c < DK; c += 64) {  // eight pieces are read before the first is written
+            uint4 u4[8];
+            uint8_t *at = tile + c / 64 * kC * 128 + j * 128, *low = smem + Smem<DK, DV>::low + c / 64 * kC * 128 + j * 128;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) u4[q] = *reinterpret_cast<const uint4*>(at + ((q ^ (j & 7)) << 4));
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                uint4 hi, lo;
+                if (tokens < kC && j >= tokens) u4[q] = make_uint4(0, 0, 0, 0);  // behind the sequence: may be no numbers
+                split2(u4[q].x, f, hi.x, lo.x);
+                split2(u4[q].y, f, hi.y, lo.y);
+                split2(u4[q].z, f, hi.z, lo.z);
+                split2(u4[q].w, f, hi.w, lo.w);
+                *reinterpret_cast<uint4*>(at + ((q ^ (j & 7)) << 4)) = hi;
+                *reinterpret_cast<uint4*>(low + ((q ^ (j & 7)) << 4)) = lo;
+            }
         }
         fence_async_smem();
         warp_arrive(&ct.kfull);
-        // 32 columns at a time: those that all the warp's rows see take a^{|i-j|} as a row's and a column's factor,
-        // both at most one; those on the diagonal one of the powers each; the others are zero
+    }
+}
+
+// Warps 0-3, a token per thread: P, 32 columns at a time.  Those that all the warp's rows see take a^{|i-j|} as a row's
+// and a column's factor, both at most one; those on the diagonal one of the powers each; the others are zero.
+__device__ __forceinline__ void weights(const ScanParams& p, const Work& w, Control& ct) {
+    const int i = threadIdx.x, warp = i >> 5;
+    const uint32_t tm = warp_lane_base(ct.tmem);
+    for (int n = 0; n < w.chunks; ++n) {
+        const int tokens = w.tokens(w.at(p, n));
+        if (!wait(ct.dead, &ct.afull, n & 1)) return;
+        tc_fence_after();
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             float s[32];
@@ -213,16 +294,13 @@ template <int DK, int DV> __device__ __forceinline__ void weights(const ScanPara
     }
 }
 
-// Warps 4-7, a token per thread.  A whole chunk's rows leave as tensor stores, from the place of its queries.
-template <int DK, int DV>
-__device__ __forceinline__ void outputs(const ScanParams& p, const Work& w, int head, const CUtensorMap* mo, uint8_t* smem, Control& ct) {
+// Warps 8-11, a token per thread.
+template <int DV> __device__ __forceinline__ void outputs(const ScanParams& p, const Work& w, int head, Control& ct) {
     const int i = threadIdx.x & (kC - 1);
     const uint32_t tm = warp_lane_base(ct.tmem);
     const float g = p.g[head], f_out = p.reverse ? 1.f : p.scale;
     for (int n = 0; n < w.chunks; ++n) {
         const int first = w.at(p, n), tokens = w.tokens(first);
-        const uint32_t slot = (3 * n + 1) % kSlots;
-        uint8_t* tile = smem + slot * Smem<DK, DV>::slot;
         const float2 fx = both(f_out * decay(g, (float)(p.reverse ? tokens - 1 - i : i + 1))), fy = both(f_out);
         if (!wait(ct.dead, &ct.ofull, n & 1)) return;
         tc_fence_after();
@@ -243,55 +321,38 @@ __device__ __forceinline__ void outputs(const ScanParams& p, const Work& w, int 
                 const float2 o = fma2(fx, make_float2(x[2 * j], x[2 * j + 1]), mul2(fy, make_float2(y[2 * j], y[2 * j + 1])));
                 z[j] = pack_bf16(o.x, o.y);
             }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint4 u = make_uint4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
-                if (tokens == kC) *reinterpret_cast<uint4*>(tile + sw128_offset(i, c + 8 * j, kC)) = u;
-                else if (i < tokens) reinterpret_cast<uint4*>(to + c)[j] = u;
-            }
+            if (i < tokens) store_bf16x32(to + c, z, p.wide_out);
         }
-        if (tokens == kC) fence_async_smem();
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (i == 0) {
-            if (tokens == kC) {
-#pragma unroll
-                for (int c = 0; c < DV; c += 64) tma_store_3d(mo, tile + (c / 64) * kC * 128, c, head, w.row0 + first);
-                bulk_commit();
-                bulk_wait_read();
-            }
-            mbar_arrive(&ct.empty[slot]);
-        }
-        __syncwarp();
     }
-    if (i == 0) bulk_wait_all();
 }
 
-// Warps 8-11: a row of the state per thread (of the first DK).
-template <int DK, int DV>
-__device__ __forceinline__ void states(const ScanParams& p, const Work& w, int seq, int head, uint8_t* smem, Control& ct) {
+// Warps 12-15: a row of the state per thread (of the first DK).
+template <int DK, int DV, bool ONLY>
+__device__ __forceinline__ void states(const ScanParams& p, const Work& w, int head, uint8_t* smem, Control& ct) {
     const int r = threadIdx.x & 127;
     const bool on = r < DK;
     const uint32_t tm = warp_lane_base(ct.tmem);
     const float g = p.g[head];
-    const size_t unit = (size_t)seq * p.H + head;
+    const size_t unit = (size_t)w.seq * p.H + head;
     float x[DV];
 #pragma unroll
     for (int c = 0; c < DV; ++c) x[c] = 0.f;
-    if (p.x0 && on) {
-        if (p.x0_transposed) {
+    const float* from = w.before ? w.before : p.x0 ? p.x0 + unit * DK * DV : nullptr;
+    if (!ONLY && from && on) {
+        if (!w.before && p.x0_transposed) {
 #pragma unroll
-            for (int c = 0; c < DV; ++c) x[c] = p.x0[(unit * DV + c) * DK + r];
+            for (int c = 0; c < DV; ++c) x[c] = from[c * DK + r];
         } else {
 #pragma unroll
             for (int c = 0; c < DV; c += 4) {
-                const float4 y = load4(p.x0 + (unit * DK + r) * DV + c);
+                const float4 y = load4(from + r * DV + c);
                 x[c] = y.x; x[c + 1] = y.y; x[c + 2] = y.z; x[c + 3] = y.w;
             }
         }
     }
     for (int n = 0; n <= w.chunks; ++n) {
         if (n > 0) {
-            if (!wait(ct.dead, &ct.dfull, (n - 1) & 1)) return;  // and the image of the state has been read
+            if (!wait(ct.dead, &ct.dfull, (n - 1) & 1)) return;
             tc_fence_after();
             const float a = decay(g, (float)w.tokens(w.at(p, n - 1)));
 #pragma unroll
@@ -300,11 +361,17 @@ __device__ __forceinline__ void states(const ScanParams& p, const Work& w, int s
                 tmem_ld32(tm + kKV + c, y);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) x[c + j] = fmaf(a, x[c + j], y[j]);
+                for (int j = 0; j < 32; j += 2) {
+                    const float2 z = fma2(both(a), make_float2(x[c + j], x[c + j + 1]), make_float2(y[j], y[j + 1]));
+                    x[c + j] = z.x;
+                    x[c + j + 1] = z.y;
+                }
             }
             tc_fence_before();
+            warp_arrive(&ct.dread);
+            if (!ONLY && !wait(ct.dead, &ct.ofull, (n - 1) & 1)) return;  // the image of the state has been read
         }
-        if (n < w.chunks) {
+        if (!ONLY && n < w.chunks) {
             if (on)
 #pragma unroll
                 for (int c = 0; c < DV; c += 16) {
@@ -317,18 +384,22 @@ __device__ __forceinline__ void states(const ScanParams& p, const Work& w, int s
             warp_arrive(&ct.xfull);
         }
     }
-    if (p.xT && on)
+    float* to = ONLY ? const_cast<float*>(w.before) : w.last && p.xT ? p.xT + unit * DK * DV : nullptr;
+    if (to && on)
 #pragma unroll
-        for (int c = 0; c < DV; c += 4) store4(p.xT + (unit * DK + r) * DV + c, make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]));
+        for (int c = 0; c < DV; c += 4) store4(to + r * DV + c, make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]));
 }
 
-template <int DK, int DV>
+// ONLY: the segments' own states, from nothing.
+template <int DK, int DV, bool ONLY>
 __global__ void __launch_bounds__(kThreads, 1)
     linear_scan_tc_kernel(const ScanParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                          const __grid_constant__ CUtensorMap mv, const __grid_constant__ CUtensorMap mo) {
+                          const __grid_constant__ CUtensorMap mv) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Control& ct = *reinterpret_cast<Control*>(smem + Smem<DK, DV>::control);
-    const int warp = threadIdx.x >> 5, seq = blockIdx.x / p.H, head = blockIdx.x % p.H;
+    const int warp = threadIdx.x >> 5, head = blockIdx.x % p.H;
+    Work w;
+    if (!make_work(p, blockIdx.x / p.H, head, w) || (ONLY && (!w.before || w.last))) return;
     if (warp == 0) {
         tmem_alloc(&ct.tmem, 512);
         tmem_relinquish();
@@ -339,31 +410,31 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ct.empty[i], 1);
         }
         for (uint64_t* one : {&ct.landed, &ct.afull, &ct.dfull, &ct.ofull, &ct.drained}) mbar_init(one, 1);
-        for (uint64_t* four : {&ct.pfull, &ct.kfull, &ct.xfull, &ct.oempty}) mbar_init(four, 4);
+        mbar_init(&ct.akeys, 1 + 4);
+        for (uint64_t* four : {&ct.pfull, &ct.kfull, &ct.dread, &ct.xfull, &ct.oempty}) mbar_init(four, 4);
         ct.dead = 0;
         fence_barrier_init();
     }
     if (threadIdx.x < kC) ct.power[threadIdx.x] = (p.reverse ? p.scale : 1.f) * decay(p.g[head], (float)threadIdx.x);
     if (threadIdx.x < 32) ct.column[threadIdx.x] = decay(p.g[head], (float)(p.reverse ? threadIdx.x : 31 - threadIdx.x));
-    Work w;
-    seq_rows(p.s, seq, w.row0, w.len);
-    w.chunks = (w.len + kC - 1) / kC;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWeightRegs));
-        weights<DK, DV>(p, w, head, smem, ct);
+        if (!ONLY) weights(p, w, ct);
     } else if (warp < 8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOutRegs));
-        outputs<DK, DV>(p, w, head, &mo, smem, ct);
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kKeyRegs));
+        keys<DK, DV, ONLY>(p, w, head, smem, ct);
     } else if (warp < 12) {
+        if (!ONLY) outputs<DV>(p, w, head, ct);
+    } else if (warp < 16) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
-        states<DK, DV>(p, w, seq, head, smem, ct);
+        states<DK, DV, ONLY>(p, w, head, smem, ct);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 12) issue<DK, DV>(w, smem, ct), drain(&ct.drained);
-        else if (warp == 13) copy_tiles<DK, DV>(p, w, head, &mq, &mk, &mv, smem, ct);
+        if (warp == 16) Issuer<DK, DV, ONLY>(smem, ct).run(w.chunks), drain(&ct.drained);
+        else if (warp == 17) copy_tiles<DK, DV, ONLY>(p, w, head, &mq, &mk, &mv, smem, ct);
     }
     __syncwarp();
     tc_fence_before();
@@ -373,29 +444,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) tmem_dealloc(ct.tmem, 512);
 }
 
-template <int DK, int DV> cudaError_t launch(const ScanParams& p, cudaStream_t st) {
+// The states that the segments begin with, over the segments' own: four values per thread.
+__global__ void __launch_bounds__(256) linear_join_kernel(const ScanParams p) {
+    const int head = blockIdx.x % p.H, R = p.span * kC, size = p.dk * p.dv;
+    Work w;
+    if (!make_work(p, blockIdx.x / p.H, head, w) || !w.before || !w.first) return;
+    const int i = 4 * (blockIdx.y * 256 + threadIdx.x);
+    if (i >= size) return;
+    const float g = p.g[head];
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.x0) {
+        const float* from = p.x0 + ((size_t)w.seq * p.H + head) * size;
+        if (p.x0_transposed) {
+            const int r = i / p.dv, c = i % p.dv;
+            x = make_float4(from[c * p.dk + r], from[(c + 1) * p.dk + r], from[(c + 2) * p.dk + r], from[(c + 3) * p.dk + r]);
+        } else {
+            x = load4(from + i);
+        }
+    }
+    const int tiles = (w.len + R - 1) / R, step = p.reverse ? -1 : 1;
+    float* at = const_cast<float*>(w.before) + i;
+    for (int n = 0, t = p.reverse ? tiles - 1 : 0; n < tiles; ++n, t += step, at += (long long)step * p.H * size) {
+        const float4 own = n + 1 < tiles ? load4(at) : x;  // the last segment's own state was not formed
+        store4(at, x);
+        const float a = decay(g, (float)min(R, w.len - t * R));
+        x = make_float4(fmaf(a, x.x, own.x), fmaf(a, x.y, own.y), fmaf(a, x.z, own.z), fmaf(a, x.w, own.w));
+    }
+}
+
+template <int DK, int DV, bool ONLY> cudaError_t launch(const ScanParams& p, const CUtensorMap (&m)[3], int blocks, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
     // the split of the registers must not ask for more than the block is launched with: it would wait for them
     static const bool fits = [] {
         cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, linear_scan_tc_kernel<DK, DV>) == cudaSuccess && a.numRegs == kRegs;
+        return cudaFuncGetAttributes(&a, linear_scan_tc_kernel<DK, DV, ONLY>) == cudaSuccess && a.numRegs == kRegs;
     }();
     if (!fits) return cudaErrorInvalidConfiguration;
-    if (cudaError_t e = set_smem_once(linear_scan_tc_kernel<DK, DV>, Smem<DK, DV>::bytes, ready); e != cudaSuccess) return e;
-    CUtensorMap mq, mk, mv, mo;
-    if (!head_rows_map(&mq, p.q, DK, p.H, p.rows, p.ld_q, kC) || !head_rows_map(&mk, p.k, DK, p.H, p.rows, p.ld_k, kC) ||
-        !head_rows_map(&mv, p.v, DV, p.H, p.rows, p.ld_v, kC) || !head_rows_map(&mo, p.out, DV, p.H, p.rows, p.ld_o, kC))
-        return cudaErrorInvalidValue;
-    TraceScope ts("linear_scan_tc", st);
-    linear_scan_tc_kernel<DK, DV><<<p.s.N * p.H, kThreads, Smem<DK, DV>::bytes, st>>>(p, mq, mk, mv, mo);
+    if (cudaError_t e = set_smem_once(linear_scan_tc_kernel<DK, DV, ONLY>, Smem<DK, DV>::bytes, ready); e != cudaSuccess) return e;
+    TraceScope ts(ONLY ? "linear_segments_tc" : "linear_scan_tc", st);
+    linear_scan_tc_kernel<DK, DV, ONLY><<<blocks, kThreads, Smem<DK, DV>::bytes, st>>>(p, m[0], m[1], m[2]);
     return cudaGetLastError();
+}
+template <int DK, int DV> cudaError_t scan(const ScanParams& p, cudaStream_t st) {
+    CUtensorMap m[3];
+    if (!head_rows_map(&m[0], p.q, DK, p.H, p.rows, p.ld_q, kC) || !head_rows_map(&m[1], p.k, DK, p.H, p.rows, p.ld_k, kC) ||
+        !head_rows_map(&m[2], p.v, DV, p.H, p.rows, p.ld_v, kC))
+        return cudaErrorInvalidValue;
+    const long long blocks = scan_items(p) * p.H;
+    if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
+    if (p.span) {
+        if (cudaError_t e = launch<DK, DV, true>(p, m, (int)blocks, st); e != cudaSuccess) return e;
+        TraceScope ts("linear_join", st);
+        linear_join_kernel<<<dim3((unsigned)blocks, (DK * DV + 1023) / 1024), 256, 0, st>>>(p);
+        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    }
+    return launch<DK, DV, false>(p, m, (int)blocks, st);
 }
 
 }  // namespace
 
-cudaError_t linear_scan_tc(const ScanParams& p, cudaStream_t st) {
-    if (p.dk == 128) return p.dv == 128 ? launch<128, 128>(p, st) : launch<128, 64>(p, st);
-    return p.dv == 128 ? launch<64, 128>(p, st) : launch<64, 64>(p, st);
+int scan_span(long long rows, int N, int T, bool packed, int H) {
+    if (rows == 0 || N == 0) return 0;
+    const long long units = (long long)N * H;
+    if (!packed) {
+        // as many segments as there are blocks for in one go
+        const long long chunks = (T + kC - 1) / kC, segments = kSms / units;
+        if (segments < 2 || chunks < kSplitFrom) return 0;
+        const long long span = (chunks + segments - 1) / segments;
+        return (int)(span < kLeastSpan ? kLeastSpan : span);
+    }
+    // lengths are known on the device only: a block's share of all chunks
+    const long long chunks = rows / kC + N, span = (chunks * H + kSms - 1) / kSms;
+    if (rows / kC < kSplitFrom) return 0;
+    return (int)(span < kLeastSpan ? kLeastSpan : span);
+}
+long long scan_slots(long long rows, int span) {
+    // sequences of several segments: no more than twice as many as whole segments
+    return span ? 2 * (rows / ((long long)span * kC) + 1) : 0;
+}
+
+cudaError_t linear_scan_tc(const ScanParams& params, cudaStream_t st) {
+    ScanParams p = params;
+    p.wide_out = wide_rows(p.out, p.ld_o);
+    if (p.dk == 128) return p.dv == 128 ? scan<128, 128>(p, st) : scan<128, 64>(p, st);
+    return p.dv == 128 ? scan<64, 128>(p, st) : scan<64, 64>(p, st);
 }
 
 }  // namespace dr

@@ -1,5 +1,6 @@
 // mixer_api.cu -- the C ABI of causal attention over whole prompts and of linear attention with a decay for
 // each head (declared in dr.h): argument validation and dispatch to prompt_attn*.cu and linear_attn*.cu.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -75,18 +76,31 @@ int check_linear(const dr_linear_desc* d, bool bwd, bool step) {
         if (int rc = check_row(lds[i][0], lds[i][1], d->io_dtype); rc != DR_OK) return rc;
     return check_status_word(d->status);
 }
-dr::ScanParams scan_params(const dr_linear_desc* d, const float* g, const int32_t* cu) {
+int span_of(const dr_linear_desc* d, bool packed) {
+    return d->io_dtype == DR_BF16 ? dr::scan_span((long long)d->B * d->T, d->num_seqs, d->T, packed, d->H) : 0;
+}
+dr::ScanParams scan_params(const dr_linear_desc* d, const float* g, const int32_t* cu, void* ws) {
     dr::ScanParams p = {};
     p.s = {cu, d->num_seqs, d->T};
     p.rows = (long long)d->B * d->T;
     p.H = d->H; p.dk = d->d_k; p.dv = d->d_v;
     p.g = g; p.scale = d->scale; p.status = d->status;
+    p.part = static_cast<float*>(ws);
+    p.span = span_of(d, cu != nullptr);
+    p.slots = dr::scan_slots(p.rows, p.span);
     return p;
 }
 cudaError_t scan(const dr::ScanParams& p, int io, cudaStream_t st) {
     return io == DR_BF16 && p.rows > 0 ? dr::linear_scan_tc(p, st) : dr::linear_scan_simt(p, io, st);
 }
-size_t linear_bytes(const dr_linear_desc*) { return 16; }
+// Room for the segments' states, whether the sequences come dense or packed.
+size_t linear_bytes(const dr_linear_desc* d) {
+    const long long rows = (long long)d->B * d->T;
+    long long slots = 0;
+    if (d->num_seqs == d->B) slots = std::max(slots, dr::scan_slots(rows, span_of(d, false)));
+    if (d->B == 1) slots = std::max(slots, dr::scan_slots(rows, span_of(d, true)));
+    return std::max<size_t>(16, (size_t)slots * d->H * d->d_k * d->d_v * sizeof(float));
+}
 
 }  // namespace
 
@@ -140,7 +154,7 @@ int dr_linear_attn_fwd(const dr_linear_desc* desc, const void* q, const void* k,
     int rc = check_linear(desc, false, false);
     if (rc != DR_OK) return rc;
     if ((rc = check_layout(desc->B, desc->num_seqs, cu_seqlens)) != DR_OK) return rc;
-    dr::ScanParams p = scan_params(desc, g, cu_seqlens);
+    dr::ScanParams p = scan_params(desc, g, cu_seqlens, workspace);
     if (p.s.N == 0) return DR_OK;
     if (!g || (p.rows > 0 && (!q || !k || !v || !o))) return DR_ERR_INVALID_ARG;
     if (any_misaligned({q, k, v, g, h0, o, hT, workspace})) return DR_ERR_ALIGNMENT;
@@ -158,7 +172,7 @@ int dr_linear_attn_bwd(const dr_linear_desc* desc, const void* q, const void* k,
     int rc = check_linear(desc, true, false);
     if (rc != DR_OK) return rc;
     if ((rc = check_layout(desc->B, desc->num_seqs, cu_seqlens)) != DR_OK) return rc;
-    const dr::ScanParams base = scan_params(desc, g, cu_seqlens);
+    const dr::ScanParams base = scan_params(desc, g, cu_seqlens, workspace);
     if (base.s.N == 0) return DR_OK;
     if (!g || (base.rows > 0 && (!q || !k || !v || !dO || !dq || !dk || !dv))) return DR_ERR_INVALID_ARG;
     if (any_misaligned({q, k, v, g, h0, dO, dhT, dq, dk, dv, dh0, workspace})) return DR_ERR_ALIGNMENT;

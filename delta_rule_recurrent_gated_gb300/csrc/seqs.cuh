@@ -79,4 +79,43 @@ __device__ __forceinline__ bool find_tile(const Seqs& q, int R, long long item, 
     }
     return false;
 }
+
+// The same tiles in the order of the sequences: number `item`, and for a sequence of several tiles how many tiles
+// such sequences have before it (`slot`: a place for each of them); called by a whole warp.
+__device__ __forceinline__ bool find_tile_in_order(const Seqs& q, int R, long long item, int& seq, int& tile, int& tiles,
+                                                   long long& slot) {
+    const int lane = threadIdx.x & 31;
+    if (!q.cu) {
+        tiles = (q.T + R - 1) / R;
+        if (item >= (long long)tiles * q.N) return false;
+        seq = (int)(item / tiles);
+        tile = (int)(item % tiles);
+        slot = (long long)seq * tiles;
+        return true;
+    }
+    long long all = 0, split = 0;  // tiles before these 32 sequences; of those that are split
+    for (int s0 = 0; s0 < q.N; s0 += 32) {
+        int row0, len = 0;
+        if (s0 + lane < q.N) seq_rows(q, s0 + lane, row0, len);
+        const int n = max((len + R - 1) / R, 1), m = s0 + lane >= q.N ? 0 : n;  // one without tokens counts as one
+        int a = m, b = m > 1 ? m : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+            if (lane >= o) a += x, b += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, all + a > item);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            seq = s0 + l;
+            tiles = __shfl_sync(0xffffffffu, m, l);
+            tile = (int)(item - all) - (__shfl_sync(0xffffffffu, a, l) - tiles);
+            slot = split + __shfl_sync(0xffffffffu, b, l) - (tiles > 1 ? tiles : 0);
+            return true;
+        }
+        all += __shfl_sync(0xffffffffu, a, 31);
+        split += __shfl_sync(0xffffffffu, b, 31);
+    }
+    return false;
+}
 }  // namespace dr

@@ -433,7 +433,8 @@ int dr_cache_attn(const dr_cache* cache, const dr_cache_seqs* seqs, const dr_att
  * B == 1, T rows, sequence s in the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (device
  * [num_seqs + 1], read when the kernels run: a captured call takes new lengths).  Lengths may be
  * zero.  Rows of no sequence are left as they were.  An offset outside 0 .. T counts as the nearest
- * of them and a sequence that would end before it starts as empty: nothing else is touched.
+ * of them and a sequence that would end before it starts as empty: nothing else is touched (where
+ * sequences then overlap, their results are undefined).
  * Tensors are rows of heads: q [B*T] rows of Hq*d values (or H*d_k), ld_q elements from one row to
  * the next, and k, v, dq, dk, dv likewise with their own distances (column ranges of one packed
  * projection, or of its gradient, will do); o, dO contiguous.  Everything is of io dtype except
