@@ -37,7 +37,7 @@ struct Control {
     uint64_t full[kSlots], empty[kSlots], landed, afull, akeys, pfull, kfull, dfull, dread, xfull, ofull, oempty, drained;
     uint32_t tmem;
     volatile int dead;
-    __align__(16) float power[kC];  // beta a^n
+    __align__(16) float power[32 + kC];  // beta a^n from place 32 on, zeros before
     __align__(16) float column[32];  // a^{31 - j}, reverse a^j
 };
 template <int DK, int DV> struct Smem {
@@ -223,22 +223,24 @@ __device__ __forceinline__ void keys(const ScanParams& p, const Work& w, int hea
             if (!wait(ct.dead, &ct.akeys, n & 1)) return;
         }
         if (n && !wait(ct.dead, &ct.dfull, (n - 1) & 1)) return;       // low parts of the chunk before are in use
+        const bool none = tokens < kC && j >= tokens;  // behind the sequence: may be no numbers
 #pragma unroll 1
-        for (int c = 0; c < DK; c += 64) {  // eight pieces are read before the first is written
-            uint4 u4[8];
-            uint8_t *at = tile + c / 64 * kC * 128 + j * 128, *low = smem + Smem<DK, DV>::low + c / 64 * kC * 128 + j * 128;
+        for (int c = 0; c < DK; c += 32) {  // four pieces are read before the first is written
+            const uint32_t row = c / 64 * kC * 128 + j * 128;
+            uint4 x[4];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) u4[q] = *reinterpret_cast<const uint4*>(at + ((q ^ (j & 7)) << 4));
+            for (int q = 0; q < 4; ++q) x[q] = *reinterpret_cast<const uint4*>(tile + row + (((c / 8 + q) & 7 ^ (j & 7)) << 4));
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
+            for (int q = 0; q < 4; ++q) {
+                const uint32_t off = row + (((c / 8 + q) & 7 ^ (j & 7)) << 4);
                 uint4 hi, lo;
-                if (tokens < kC && j >= tokens) u4[q] = make_uint4(0, 0, 0, 0);  // behind the sequence: may be no numbers
-                split2(u4[q].x, f, hi.x, lo.x);
-                split2(u4[q].y, f, hi.y, lo.y);
-                split2(u4[q].z, f, hi.z, lo.z);
-                split2(u4[q].w, f, hi.w, lo.w);
-                *reinterpret_cast<uint4*>(at + ((q ^ (j & 7)) << 4)) = hi;
-                *reinterpret_cast<uint4*>(low + ((q ^ (j & 7)) << 4)) = lo;
+                if (none) x[q] = make_uint4(0, 0, 0, 0);
+                split2(x[q].x, f, hi.x, lo.x);
+                split2(x[q].y, f, hi.y, lo.y);
+                split2(x[q].z, f, hi.z, lo.z);
+                split2(x[q].w, f, hi.w, lo.w);
+                *reinterpret_cast<uint4*>(tile + off) = hi;
+                *reinterpret_cast<uint4*>(smem + Smem<DK, DV>::low + off) = lo;
             }
         }
         fence_async_smem();
@@ -255,7 +257,7 @@ __device__ __forceinline__ void weights(const ScanParams& p, const Work& w, Cont
         const int tokens = w.tokens(w.at(p, n));
         if (!wait(ct.dead, &ct.afull, n & 1)) return;
         tc_fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < 4; ++b) {
             float s[32];
             uint32_t z[16];
@@ -266,14 +268,19 @@ __device__ __forceinline__ void weights(const ScanParams& p, const Work& w, Cont
             } else {
                 tmem_ld32(tm + kA + c, s);
                 tmem_ld_wait();
-                if (b == warp || (p.reverse && tokens < kC)) {
+                if (tokens < kC) {  // scores behind the sequence may be no numbers
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int back = p.reverse ? c + j - i : i - c - j;
-                        s[j] = back >= 0 && c + j < tokens ? s[j] * ct.power[max(back, 0)] : 0.f;
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        if (c + j >= tokens) s[j] = 0.f;
+                }
+                if (b == warp) {
+                    // power[n] is zero for n < 0
+                    const float* f = ct.power + 32 + (p.reverse ? c - i : i - c);
+                    const int step = p.reverse ? 1 : -1;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) s[j] *= f[step * j];
                 } else {
-                    const float2 fr = both(p.reverse ? ct.power[c - i] : ct.power[i - c - 31]);
+                    const float2 fr = both(ct.power[32 + (p.reverse ? c - i : i - c - 31)]);
                     const float4* fc = reinterpret_cast<const float4*>(ct.column);
 #pragma unroll
                     for (int j = 0; j < 32; j += 4) {
@@ -305,7 +312,7 @@ template <int DV> __device__ __forceinline__ void outputs(const ScanParams& p, c
         if (!wait(ct.dead, &ct.ofull, n & 1)) return;
         tc_fence_after();
         __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + (w.row0 + first + i) * p.ld_o + (long long)head * DV;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < DV; c += 32) {
             float x[32], y[32];
             tmem_ld32(tm + kQX + c, x);
@@ -415,7 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ct.dead = 0;
         fence_barrier_init();
     }
-    if (threadIdx.x < kC) ct.power[threadIdx.x] = (p.reverse ? p.scale : 1.f) * decay(p.g[head], (float)threadIdx.x);
+    if (threadIdx.x < 32 + kC)
+        ct.power[threadIdx.x] = threadIdx.x < 32 ? 0.f : (p.reverse ? p.scale : 1.f) * decay(p.g[head], (float)threadIdx.x - 32.f);
     if (threadIdx.x < 32) ct.column[threadIdx.x] = decay(p.g[head], (float)(p.reverse ? threadIdx.x : 31 - threadIdx.x));
     tc_fence_before();
     __syncthreads();
@@ -506,15 +514,15 @@ template <int DK, int DV> cudaError_t scan(const ScanParams& p, cudaStream_t st)
 int scan_span(long long rows, int N, int T, bool packed, int H) {
     if (rows == 0 || N == 0) return 0;
     const long long units = (long long)N * H;
-    if (!packed) {
+    if (!packed || N == 1) {
         // as many segments as there are blocks for in one go
         const long long chunks = (T + kC - 1) / kC, segments = kSms / units;
         if (segments < 2 || chunks < kSplitFrom) return 0;
         const long long span = (chunks + segments - 1) / segments;
         return (int)(span < kLeastSpan ? kLeastSpan : span);
     }
-    // lengths are known on the device only: a block's share of all chunks
-    const long long chunks = rows / kC + N, span = (chunks * H + kSms - 1) / kSms;
+    // lengths are known on the device only: what is far longer than a block's share of all chunks
+    const long long span = (5 * (rows / kC + N) * H / 2 + kSms - 1) / kSms;
     if (rows / kC < kSplitFrom) return 0;
     return (int)(span < kLeastSpan ? kLeastSpan : span);
 }
