@@ -6,10 +6,11 @@
 //   out_i = sum_{j<=i} a^{i-j} (q_i.k_j) v_j + a^{i+1} X^T q_i;   X' = a^C X + sum_j a^{C-1-j} k_j v_j^T
 // (reverse: a^i X^T q_i and X' = a^C X + sum_j a^{C-j} k_j v_j^T).  Columns of v and of the state do not meet,
 // so a block has one sequence, one head and up to 32 columns; the products q_i.k_j are formed by each.
+#include <algorithm>
+
 #include "common.cuh"
-#include "linear_attn.cuh"
+#include "linear_work.cuh"
 #include "trace.cuh"
-#include "vec4.cuh"
 
 namespace dr {
 namespace {
@@ -22,48 +23,51 @@ template <int DK, int W> struct ScanSmem {  // pitches: 16-byte reads of eight r
                          floats = x + DK * pw;
 };
 
-template <int DK, int W, typename IO> __global__ void __launch_bounds__(kThreads, 2) linear_scan_kernel(const ScanParams p) {
+// ONLY: the segments' own states, from nothing.
+template <int DK, int W, bool ONLY> __global__ void __launch_bounds__(kThreads, 2) linear_scan_kernel(const ScanParams p) {
     using L = ScanSmem<DK, W>;
     extern __shared__ __align__(16) float sm[];
     float *Q = sm, *K = sm + L::k, *V = sm + L::v, *A = sm + L::a, *X = sm + L::x;
     __shared__ float pw[kChunk + 1];  // a^n
-    const int s = blockIdx.x / p.H, h = blockIdx.x % p.H, w0 = blockIdx.y * W;
+    const int h = blockIdx.x % p.H, w0 = blockIdx.y * W;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
     constexpr int WX = W / 16, RX = DK / 16;  // a thread's columns; its rows of the state
-    int row0, len;
-    seq_rows(p.s, s, row0, len);
+    Work w;
+    if (!make_work(p, blockIdx.x / p.H, h, w) || (ONLY && (!w.before || w.last))) return;
+    const int begin = w.c0 * kScanChunk, end = min(w.len, begin + w.chunks * kScanChunk), len = end - begin;
     const float g = p.g[h];
     if (threadIdx.x <= kChunk) pw[threadIdx.x] = decay(g, (float)threadIdx.x);
-    const size_t unit = (size_t)s * p.H + h;
+    const size_t unit = ((size_t)w.seq * p.H + h) * DK * p.dv;
+    const float* from = ONLY ? nullptr : w.before ? w.before : p.x0 ? p.x0 + unit : nullptr;
+    const bool turned = p.x0_transposed && !w.before;
     for (int i = threadIdx.x; i < DK * W; i += kThreads) {
         const int r = i / W, c = w0 + i % W;
-        const size_t at = p.x0_transposed ? (unit * p.dv + c) * DK + r : (unit * DK + r) * p.dv + c;
-        X[r * L::pw + i % W] = p.x0 ? p.x0[at] : 0.f;
+        X[r * L::pw + i % W] = from ? from[turned ? c * DK + r : r * p.dv + c] : 0.f;
     }
     const float f_in = p.reverse ? p.scale : 1.f, f_out = p.reverse ? 1.f : p.scale;
     const int late = p.reverse ? 1 : 0;
     for (int t0 = 0; t0 < len; t0 += kChunk) {
         const int n = min(kChunk, len - t0);
         __syncthreads();
-        auto token = [&](int i) { return (long long)row0 + (p.reverse ? len - 1 - t0 - i : t0 + i); };
+        auto token = [&](int i) { return (long long)w.row0 + (p.reverse ? end - 1 - t0 - i : begin + t0 + i); };
         for (int i = threadIdx.x; i < kChunk * (DK / 4); i += kThreads) {
             const int r = i / (DK / 4), c = (i % (DK / 4)) * 4;
             float4 q = make_float4(0.f, 0.f, 0.f, 0.f), k = q;
             if (r < n) {
-                q = load4(static_cast<const IO*>(p.q) + token(r) * p.ld_q + (long long)h * DK + c);
-                k = load4(static_cast<const IO*>(p.k) + token(r) * p.ld_k + (long long)h * DK + c);
+                if (!ONLY) q = load4(static_cast<const float*>(p.q) + token(r) * p.ld_q + (long long)h * DK + c);
+                k = load4(static_cast<const float*>(p.k) + token(r) * p.ld_k + (long long)h * DK + c);
             }
             *reinterpret_cast<float4*>(Q + r * L::pk + c) = q;
             *reinterpret_cast<float4*>(K + r * L::pk + c) = k;
         }
         for (int i = threadIdx.x; i < kChunk * (W / 4); i += kThreads) {
             const int r = i / (W / 4), c = (i % (W / 4)) * 4;
-            const float4 v = r < n ? load4(static_cast<const IO*>(p.v) + token(r) * p.ld_v + (long long)h * p.dv + w0 + c)
+            const float4 v = r < n ? load4(static_cast<const float*>(p.v) + token(r) * p.ld_v + (long long)h * p.dv + w0 + c)
                                    : make_float4(0.f, 0.f, 0.f, 0.f);
             *reinterpret_cast<float4*>(V + r * L::pw + c) = v;
         }
         __syncthreads();
-        {   // weights of the pairs: rows 4 ty + i, columns tx + 16 j
+        if (!ONLY) {  // weights of the pairs: rows 4 ty + i, columns tx + 16 j
             float acc[4][4] = {};
 #pragma unroll 4
             for (int c = 0; c < DK; c += 4) {
@@ -92,7 +96,7 @@ template <int DK, int W, typename IO> __global__ void __launch_bounds__(kThreads
                 }
         }
         __syncthreads();
-        {   // out: rows 4 ty + i, columns WX tx ..
+        if (!ONLY) {  // out: rows 4 ty + i, columns WX tx ..
             float o[4][WX] = {}, r[4][WX] = {};
 #pragma unroll 2
             for (int c = 0; c < kChunk; c += 4) {
@@ -130,9 +134,11 @@ template <int DK, int W, typename IO> __global__ void __launch_bounds__(kThreads
 #pragma unroll
                     for (int w = 0; w < WX; ++w) {
                         const float y = f_out * fmaf(pw[4 * ty + i + 1 - late], r[i][w], o[i][w]);
-                        static_cast<IO*>(p.out)[token(4 * ty + i) * p.ld_o + (long long)h * p.dv + w0 + WX * tx + w] = from_f<IO>(y);
+                        static_cast<float*>(p.out)[token(4 * ty + i) * p.ld_o + (long long)h * p.dv + w0 + WX * tx + w] = y;
                     }
         }
+        __syncthreads();
+        for (int i = threadIdx.x; i < n * W; i += kThreads) V[i / W * L::pw + i % W] *= pw[n - 1 - i / W + late] * f_in;
         __syncthreads();
         {   // the state: rows RX ty ..
             float x[RX][WX];
@@ -141,17 +147,17 @@ template <int DK, int W, typename IO> __global__ void __launch_bounds__(kThreads
             for (int i = 0; i < RX; ++i)
 #pragma unroll
                 for (int w = 0; w < WX; ++w) x[i][w] = a * X[(RX * ty + i) * L::pw + WX * tx + w];
+#pragma unroll 4
             for (int j = 0; j < n; ++j) {
-                const float f = pw[n - 1 - j + late] * f_in;
-                float v[WX];
+                float v[WX], k[RX];
 #pragma unroll
-                for (int w = 0; w < WX; ++w) v[w] = f * V[j * L::pw + WX * tx + w];
+                for (int w = 0; w < WX; ++w) v[w] = V[j * L::pw + WX * tx + w];
 #pragma unroll
-                for (int i = 0; i < RX; ++i) {
-                    const float k = K[j * L::pk + RX * ty + i];
+                for (int i = 0; i < RX; ++i) k[i] = K[j * L::pk + RX * ty + i];
 #pragma unroll
-                    for (int w = 0; w < WX; ++w) x[i][w] = fmaf(k, v[w], x[i][w]);
-                }
+                for (int i = 0; i < RX; ++i)
+#pragma unroll
+                    for (int w = 0; w < WX; ++w) x[i][w] = fmaf(k[i], v[w], x[i][w]);
             }
 #pragma unroll
             for (int i = 0; i < RX; ++i)
@@ -160,22 +166,65 @@ template <int DK, int W, typename IO> __global__ void __launch_bounds__(kThreads
         }
     }
     __syncthreads();
-    if (p.xT)
-        for (int i = threadIdx.x; i < DK * W; i += kThreads)
-            p.xT[(unit * DK + i / W) * p.dv + w0 + i % W] = X[(i / W) * L::pw + i % W];
+    float* to = ONLY ? const_cast<float*>(w.before) : w.last && p.xT ? p.xT + unit : nullptr;
+    if (to)
+        for (int i = threadIdx.x; i < DK * W; i += kThreads) to[(i / W) * p.dv + w0 + i % W] = X[(i / W) * L::pw + i % W];
 }
 
-template <int DK, int W, typename IO> cudaError_t scan(const ScanParams& p, cudaStream_t st) {
+template <int DK, int W, bool ONLY> cudaError_t scan(const ScanParams& p, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
     constexpr int smem = ScanSmem<DK, W>::floats * 4;
-    if (cudaError_t e = set_smem_once(linear_scan_kernel<DK, W, IO>, smem, ready); e != cudaSuccess) return e;
-    TraceScope ts("linear_scan", st);
-    linear_scan_kernel<DK, W, IO><<<dim3(p.s.N * p.H, p.dv / W), kThreads, smem, st>>>(p);
+    if (cudaError_t e = set_smem_once(linear_scan_kernel<DK, W, ONLY>, smem, ready); e != cudaSuccess) return e;
+    const long long blocks = scan_items(p) * p.H;
+    if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
+    TraceScope ts(ONLY ? "linear_segments" : "linear_scan", st);
+    linear_scan_kernel<DK, W, ONLY><<<dim3((unsigned)blocks, p.dv / W), kThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
-template <int DK, typename IO> cudaError_t scan_width(const ScanParams& p, cudaStream_t st) {
-    return p.dv == 16 ? scan<DK, 16, IO>(p, st) : scan<DK, 32, IO>(p, st);
+template <int DK> cudaError_t scan_width(const ScanParams& p, bool only, cudaStream_t st) {
+    if (p.dv == 16) return only ? scan<DK, 16, true>(p, st) : scan<DK, 16, false>(p, st);
+    return only ? scan<DK, 32, true>(p, st) : scan<DK, 32, false>(p, st);
 }
+cudaError_t scan_simt(const ScanParams& p, bool only, cudaStream_t st) {
+    switch (p.dk) {
+        case 16: return scan_width<16>(p, only, st);
+        case 32: return scan_width<32>(p, only, st);
+        case 64: return scan_width<64>(p, only, st);
+        default: return scan_width<128>(p, only, st);
+    }
+}
+
+// ------------------------------------------------------------------ segments
+// The states that the segments begin with, over the segments' own: four values per thread.
+struct JoinSet { ScanParams p[kMostScans]; };
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ JoinSet set) {
+    const ScanParams& p = set.p[blockIdx.z];
+    const int head = blockIdx.x % p.H, R = p.span * kScanChunk, size = p.dk * p.dv;
+    Work w;
+    if (!make_work(p, blockIdx.x / p.H, head, w) || !w.before || !w.first) return;
+    const int i = 4 * (blockIdx.y * 256 + threadIdx.x);
+    if (i >= size) return;
+    const float g = p.g[head];
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.x0) {
+        const float* from = p.x0 + ((size_t)w.seq * p.H + head) * size;
+        if (p.x0_transposed) {
+            const int r = i / p.dv, c = i % p.dv;
+            x = make_float4(from[c * p.dk + r], from[(c + 1) * p.dk + r], from[(c + 2) * p.dk + r], from[(c + 3) * p.dk + r]);
+        } else {
+            x = load4(from + i);
+        }
+    }
+    const int tiles = (w.len + R - 1) / R, step = p.reverse ? -1 : 1;
+    float* at = const_cast<float*>(w.before) + i;
+    for (int n = 0, t = p.reverse ? tiles - 1 : 0; n < tiles; ++n, t += step, at += (long long)step * p.H * size) {
+        const float4 own = n + 1 < tiles ? load4(at) : x;  // the last segment's own state was not formed
+        store4(at, x);
+        const float a = decay(g, (float)min(R, w.len - t * R));
+        x = make_float4(fmaf(a, x.x, own.x), fmaf(a, x.y, own.y), fmaf(a, x.z, own.z), fmaf(a, x.w, own.w));
+    }
+}
+
 
 // ------------------------------------------------------------------ the recurrent step
 // A block has one sequence and head, each thread four columns of R rows of the state in registers:
@@ -263,14 +312,6 @@ template <int DK, typename IO> cudaError_t step_width(const StepParams& p, cudaS
         default: return step<DK, 128, IO>(p, st);
     }
 }
-template <typename IO> cudaError_t scan_of(const ScanParams& p, cudaStream_t st) {
-    switch (p.dk) {
-        case 16: return scan_width<16, IO>(p, st);
-        case 32: return scan_width<32, IO>(p, st);
-        case 64: return scan_width<64, IO>(p, st);
-        default: return scan_width<128, IO>(p, st);
-    }
-}
 template <typename IO> cudaError_t step_of(const StepParams& p, cudaStream_t st) {
     switch (p.dk) {
         case 16: return step_width<16, IO>(p, st);
@@ -282,8 +323,51 @@ template <typename IO> cudaError_t step_of(const StepParams& p, cudaStream_t st)
 
 }  // namespace
 
-cudaError_t linear_scan_simt(const ScanParams& p, int io, cudaStream_t st) {
-    return io == DR_F32 ? scan_of<float>(p, st) : scan_of<__nv_bfloat16>(p, st);
+// Blocks that run at once; from how many chunks on, and into how few, sequences are split.  On the tensor cores a block
+// has an SM to itself and its start costs about two chunks; on the CUDA cores two share one.
+int scan_span(int io, long long rows, int N, int T, bool packed, int H, int dk, int dv, int scans) {
+    if (rows == 0 || N == 0) return 0;
+    const bool tc = io == DR_BF16;
+    const int room = tc ? 152 : 304, least = tc ? 4 : 1;
+    const long long units = (long long)N * H * scans * (tc ? 1 : std::max(std::min(dk, dv) / 32, 1));
+    const long long chunks = packed ? rows / kScanChunk + N : (long long)N * ((T + kScanChunk - 1) / kScanChunk);  // of all sequences
+    if (chunks < (tc ? 12 : 2)) return 0;
+    long long span;
+    if (!packed || N == 1) {
+        const long long segments = room / units;  // as many as there are blocks for in one go
+        if (segments < 2 || chunks / N < (tc ? 12 : 2)) return 0;
+        span = (chunks / N + segments - 1) / segments;
+    } else {
+        // lengths are known on the device only: what is far longer than a block's share of all chunks
+        span = (5 * chunks * (units / N) / 2 + room - 1) / room;
+    }
+    return (int)std::min<long long>(std::max<long long>(span, least), 1 << 22);
+}
+long long scan_slots(long long rows, int span) {
+    // sequences of several segments: no more than twice as many as whole segments
+    return span ? 2 * (rows / ((long long)span * kScanChunk) + 1) : 0;
+}
+
+cudaError_t linear_scans(const ScanParams* p, int n, int io, cudaStream_t st) {
+    const bool tc = io == DR_BF16 && p->rows > 0;
+    // scans of the same sizes follow one another
+    auto all = [&](bool only) {
+        for (int i = 0, j; i < n; i = j) {
+            for (j = i + 1; tc && j < n && p[j].dk == p[i].dk && p[j].dv == p[i].dv;) ++j;
+            if (cudaError_t e = tc ? linear_scans_tc(p + i, j - i, only, st) : scan_simt(p[i], only, st); e != cudaSuccess) return e;
+        }
+        return cudaSuccess;
+    };
+    if (p->rows > 0 && p->span) {
+        if (cudaError_t e = all(true); e != cudaSuccess) return e;
+        JoinSet set;
+        for (int i = 0; i < n; ++i) set.p[i] = p[i];
+        TraceScope ts("linear_join", st);
+        const dim3 grid((unsigned)(scan_items(*p) * p->H), (p->dk * p->dv + 1023) / 1024, n);
+        linear_join_kernel<<<grid, 256, 0, st>>>(set);
+        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    }
+    return all(false);
 }
 cudaError_t linear_step(const StepParams& p, int io, cudaStream_t st) {
     return io == DR_F32 ? step_of<float>(p, st) : step_of<__nv_bfloat16>(p, st);

@@ -36,14 +36,17 @@ struct ScanParams {
 // Long sequences are split where a block for each sequence and head would leave most of the GPU idle: first every
 // segment's own state is formed from nothing, then the states that they begin with are the running sums of
 // these, and then all segments are scanned at once.  The first step reads k and v once more.
-constexpr int kScanChunk = 128;
-int scan_span(long long rows, int N, int T, bool packed, int H);       // p.span
-long long scan_slots(long long rows, int span);                        // p.slots
+constexpr int kScanChunk = 128, kMostScans = 3;
+// Chunks of a segment (0: not split) for `scans` scans that run together, and how many segments of split sequences
+// there can be.
+int scan_span(int io, long long rows, int N, int T, bool packed, int H, int dk, int dv, int scans);
+long long scan_slots(long long rows, int span);
 
-// CUDA cores, any supported size (linear_attn.cu).
-cudaError_t linear_scan_simt(const ScanParams& p, int io, cudaStream_t st);
-// Tensor cores, bf16 with dk and dv 64 or 128, p.rows > 0 (linear_attn_tc.cu).
-cudaError_t linear_scan_tc(const ScanParams& p, cudaStream_t st);
+// n scans (of the same sequences and heads) together.
+cudaError_t linear_scans(const ScanParams* p, int n, int io, cudaStream_t st);
+// Their kernels on the tensor cores, bf16 with dk and dv 64 or 128, rows > 0 (linear_attn_tc.cu); `only`: the
+// segments' own states.
+cudaError_t linear_scans_tc(const ScanParams* p, int n, bool only, cudaStream_t st);
 // The recurrent step: T tokens of every sequence on the caller's state.
 struct StepParams {
     int B, T, H, dk, dv;

@@ -17,10 +17,9 @@
 // The products of a chunk are issued as P V (n), A (n + 1), K'V (n), Q X (n), each when what it needs is there: P and K'
 // of the next chunk are formed while the last two run.
 #include "f32x2.cuh"
-#include "linear_attn.cuh"
+#include "linear_work.cuh"
 #include "tc_block.cuh"
 #include "trace.cuh"
-#include "vec4.cuh"
 
 namespace dr {
 namespace {
@@ -29,8 +28,6 @@ constexpr int kC = kScanChunk, kThreads = 640, kSlots = 5;
 // Registers of a thread: as launched, then of the five groups of four warps.
 constexpr int kRegs = 96, kWeightRegs = 88, kKeyRegs = 72, kOutRegs = 96, kStateRegs = 176, kOtherRegs = 48;
 static_assert(kWeightRegs + kKeyRegs + kOutRegs + kStateRegs + kOtherRegs <= 5 * kRegs, "more than the block has");
-// Segments: blocks for all SMs; what is split at all; chunks of a segment.
-constexpr int kSms = 152, kSplitFrom = 12, kLeastSpan = 4;
 constexpr uint32_t kA = 0, kQX = 128, kPV = 256, kKV = 384;  // columns of tensor memory
 
 struct Control {
@@ -47,35 +44,6 @@ template <int DK, int DV> struct Smem {
                          control = end > low + kC * 128 * 2 ? end : low + kC * 128 * 2, bytes = control + 1024;
     static_assert(sizeof(Control) <= 1024, "control block");
 };
-
-// A block's chunks: all of a sequence or a segment of them.
-struct Work {
-    int seq, row0, len, c0, chunks;
-    bool first, last;       // of the sequence's segments in the order of the scan
-    const float* before;    // the state before a segment that is not the only one (first step: where its own goes)
-    __device__ __forceinline__ int at(const ScanParams& p, int n) const { return (c0 + (p.reverse ? chunks - 1 - n : n)) * kC; }
-    __device__ __forceinline__ int tokens(int at) const { return min(kC, len - at); }
-};
-__device__ __forceinline__ bool make_work(const ScanParams& p, int item, int head, Work& w) {
-    const int span = p.span ? p.span : (1 << 30) / kC;
-    int tile, tiles;
-    long long slot;
-    if (!find_tile_in_order(p.s, span * kC, item, w.seq, tile, tiles, slot)) return false;
-    seq_rows(p.s, w.seq, w.row0, w.len);
-    w.c0 = tile * span;
-    w.chunks = min(span, (w.len + kC - 1) / kC - w.c0);
-    w.first = p.reverse ? tile == tiles - 1 : tile == 0;
-    w.last = p.reverse ? tile == 0 : tile == tiles - 1;
-    if (tiles > 1 && slot + tiles > p.slots) return false;  // offsets out of order: sequences that overlap
-    w.before = tiles > 1 ? p.part + ((slot + tile) * p.H + head) * p.dk * p.dv : nullptr;
-    return true;
-}
-
-// Items of a launch: segments of the sequences, a sequence without tokens as one.
-long long scan_items(const ScanParams& p) {
-    const long long R = (p.span ? p.span : (1 << 30) / kC) * (long long)kC;
-    return p.s.cu ? p.s.T / R + p.s.N : p.s.N * ((p.s.T + R - 1) / R);
-}
 
 // What goes through the ring for a chunk: K, Q, V, or K, V where only states are formed.
 template <bool ONLY> constexpr int kTiles = ONLY ? 2 : 3;
@@ -397,16 +365,21 @@ __device__ __forceinline__ void states(const ScanParams& p, const Work& w, int h
         for (int c = 0; c < DV; c += 4) store4(to + r * DV + c, make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]));
 }
 
+// n scans of the same sequences side by side: what they share is read at about the same time.
+struct ScanSet {
+    CUtensorMap m[kMostScans][3];  // of q, k, v
+    ScanParams p[kMostScans];
+};
 // ONLY: the segments' own states, from nothing.
 template <int DK, int DV, bool ONLY>
-__global__ void __launch_bounds__(kThreads, 1)
-    linear_scan_tc_kernel(const ScanParams p, const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                          const __grid_constant__ CUtensorMap mv) {
+__global__ void __launch_bounds__(kThreads, 1) linear_scan_tc_kernel(const __grid_constant__ ScanSet set, int n) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Control& ct = *reinterpret_cast<Control*>(smem + Smem<DK, DV>::control);
-    const int warp = threadIdx.x >> 5, head = blockIdx.x % p.H;
+    const ScanParams& p = set.p[blockIdx.x % n];
+    const CUtensorMap* m = set.m[blockIdx.x % n];
+    const int warp = threadIdx.x >> 5, item = blockIdx.x / n, head = item % p.H;
     Work w;
-    if (!make_work(p, blockIdx.x / p.H, head, w) || (ONLY && (!w.before || w.last))) return;
+    if (!make_work(p, item / p.H, head, w) || (ONLY && (!w.before || w.last))) return;
     if (warp == 0) {
         tmem_alloc(&ct.tmem, 512);
         tmem_relinquish();
@@ -442,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 16) Issuer<DK, DV, ONLY>(smem, ct).run(w.chunks), drain(&ct.drained);
-        else if (warp == 17) copy_tiles<DK, DV, ONLY>(p, w, head, &mq, &mk, &mv, smem, ct);
+        else if (warp == 17) copy_tiles<DK, DV, ONLY>(p, w, head, m, m + 1, m + 2, smem, ct);
     }
     __syncwarp();
     tc_fence_before();
@@ -452,35 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 0) tmem_dealloc(ct.tmem, 512);
 }
 
-// The states that the segments begin with, over the segments' own: four values per thread.
-__global__ void __launch_bounds__(256) linear_join_kernel(const ScanParams p) {
-    const int head = blockIdx.x % p.H, R = p.span * kC, size = p.dk * p.dv;
-    Work w;
-    if (!make_work(p, blockIdx.x / p.H, head, w) || !w.before || !w.first) return;
-    const int i = 4 * (blockIdx.y * 256 + threadIdx.x);
-    if (i >= size) return;
-    const float g = p.g[head];
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.x0) {
-        const float* from = p.x0 + ((size_t)w.seq * p.H + head) * size;
-        if (p.x0_transposed) {
-            const int r = i / p.dv, c = i % p.dv;
-            x = make_float4(from[c * p.dk + r], from[(c + 1) * p.dk + r], from[(c + 2) * p.dk + r], from[(c + 3) * p.dk + r]);
-        } else {
-            x = load4(from + i);
-        }
-    }
-    const int tiles = (w.len + R - 1) / R, step = p.reverse ? -1 : 1;
-    float* at = const_cast<float*>(w.before) + i;
-    for (int n = 0, t = p.reverse ? tiles - 1 : 0; n < tiles; ++n, t += step, at += (long long)step * p.H * size) {
-        const float4 own = n + 1 < tiles ? load4(at) : x;  // the last segment's own state was not formed
-        store4(at, x);
-        const float a = decay(g, (float)min(R, w.len - t * R));
-        x = make_float4(fmaf(a, x.x, own.x), fmaf(a, x.y, own.y), fmaf(a, x.z, own.z), fmaf(a, x.w, own.w));
-    }
-}
-
-template <int DK, int DV, bool ONLY> cudaError_t launch(const ScanParams& p, const CUtensorMap (&m)[3], int blocks, cudaStream_t st) {
+template <int DK, int DV, bool ONLY> cudaError_t launch(const ScanSet& set, int n, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
     // the split of the registers must not ask for more than the block is launched with: it would wait for them
     static const bool fits = [] {
@@ -490,52 +435,30 @@ template <int DK, int DV, bool ONLY> cudaError_t launch(const ScanParams& p, con
     if (!fits) return cudaErrorInvalidConfiguration;
     if (cudaError_t e = set_smem_once(linear_scan_tc_kernel<DK, DV, ONLY>, Smem<DK, DV>::bytes, ready); e != cudaSuccess) return e;
     TraceScope ts(ONLY ? "linear_segments_tc" : "linear_scan_tc", st);
-    linear_scan_tc_kernel<DK, DV, ONLY><<<blocks, kThreads, Smem<DK, DV>::bytes, st>>>(p, m[0], m[1], m[2]);
+    const long long blocks = scan_items(set.p[0]) * set.p[0].H * n;
+    if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
+    linear_scan_tc_kernel<DK, DV, ONLY><<<(unsigned)blocks, kThreads, Smem<DK, DV>::bytes, st>>>(set, n);
     return cudaGetLastError();
 }
-template <int DK, int DV> cudaError_t scan(const ScanParams& p, cudaStream_t st) {
-    CUtensorMap m[3];
-    if (!head_rows_map(&m[0], p.q, DK, p.H, p.rows, p.ld_q, kC) || !head_rows_map(&m[1], p.k, DK, p.H, p.rows, p.ld_k, kC) ||
-        !head_rows_map(&m[2], p.v, DV, p.H, p.rows, p.ld_v, kC))
-        return cudaErrorInvalidValue;
-    const long long blocks = scan_items(p) * p.H;
-    if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
-    if (p.span) {
-        if (cudaError_t e = launch<DK, DV, true>(p, m, (int)blocks, st); e != cudaSuccess) return e;
-        TraceScope ts("linear_join", st);
-        linear_join_kernel<<<dim3((unsigned)blocks, (DK * DV + 1023) / 1024), 256, 0, st>>>(p);
-        if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+template <int DK, int DV> cudaError_t scans(const ScanParams* p, int n, bool only, cudaStream_t st) {
+    ScanSet set;
+    for (int i = 0; i < n; ++i) {
+        set.p[i] = p[i];
+        set.p[i].wide_out = wide_rows(p[i].out, p[i].ld_o);
+        if (!head_rows_map(&set.m[i][0], p[i].q, DK, p[i].H, p[i].rows, p[i].ld_q, kC) ||
+            !head_rows_map(&set.m[i][1], p[i].k, DK, p[i].H, p[i].rows, p[i].ld_k, kC) ||
+            !head_rows_map(&set.m[i][2], p[i].v, DV, p[i].H, p[i].rows, p[i].ld_v, kC))
+            return cudaErrorInvalidValue;
     }
-    return launch<DK, DV, false>(p, m, (int)blocks, st);
+    return only ? launch<DK, DV, true>(set, n, st) : launch<DK, DV, false>(set, n, st);
 }
 
 }  // namespace
 
-int scan_span(long long rows, int N, int T, bool packed, int H) {
-    if (rows == 0 || N == 0) return 0;
-    const long long units = (long long)N * H;
-    if (!packed || N == 1) {
-        // as many segments as there are blocks for in one go
-        const long long chunks = (T + kC - 1) / kC, segments = kSms / units;
-        if (segments < 2 || chunks < kSplitFrom) return 0;
-        const long long span = (chunks + segments - 1) / segments;
-        return (int)(span < kLeastSpan ? kLeastSpan : span);
-    }
-    // lengths are known on the device only: what is far longer than a block's share of all chunks
-    const long long span = (5 * (rows / kC + N) * H / 2 + kSms - 1) / kSms;
-    if (rows / kC < kSplitFrom) return 0;
-    return (int)(span < kLeastSpan ? kLeastSpan : span);
-}
-long long scan_slots(long long rows, int span) {
-    // sequences of several segments: no more than twice as many as whole segments
-    return span ? 2 * (rows / ((long long)span * kC) + 1) : 0;
-}
-
-cudaError_t linear_scan_tc(const ScanParams& params, cudaStream_t st) {
-    ScanParams p = params;
-    p.wide_out = wide_rows(p.out, p.ld_o);
-    if (p.dk == 128) return p.dv == 128 ? scan<128, 128>(p, st) : scan<128, 64>(p, st);
-    return p.dv == 128 ? scan<64, 128>(p, st) : scan<64, 64>(p, st);
+cudaError_t linear_scans_tc(const ScanParams* p, int n, bool only, cudaStream_t st) {
+    if (n == 0) return cudaSuccess;
+    if (p->dk == 128) return p->dv == 128 ? scans<128, 128>(p, n, only, st) : scans<128, 64>(p, n, only, st);
+    return p->dv == 128 ? scans<64, 128>(p, n, only, st) : scans<64, 64>(p, n, only, st);
 }
 
 }  // namespace dr

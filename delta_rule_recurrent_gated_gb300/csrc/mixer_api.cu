@@ -76,29 +76,28 @@ int check_linear(const dr_linear_desc* d, bool bwd, bool step) {
         if (int rc = check_row(lds[i][0], lds[i][1], d->io_dtype); rc != DR_OK) return rc;
     return check_status_word(d->status);
 }
-int span_of(const dr_linear_desc* d, bool packed) {
-    return d->io_dtype == DR_BF16 ? dr::scan_span((long long)d->B * d->T, d->num_seqs, d->T, packed, d->H) : 0;
+int span_of(const dr_linear_desc* d, bool packed, int scans) {
+    return dr::scan_span(d->io_dtype, (long long)d->B * d->T, d->num_seqs, d->T, packed, d->H, d->d_k, d->d_v, scans);
 }
-dr::ScanParams scan_params(const dr_linear_desc* d, const float* g, const int32_t* cu, void* ws) {
+dr::ScanParams scan_params(const dr_linear_desc* d, const float* g, const int32_t* cu, void* ws, int scans) {
     dr::ScanParams p = {};
     p.s = {cu, d->num_seqs, d->T};
     p.rows = (long long)d->B * d->T;
     p.H = d->H; p.dk = d->d_k; p.dv = d->d_v;
     p.g = g; p.scale = d->scale; p.status = d->status;
     p.part = static_cast<float*>(ws);
-    p.span = span_of(d, cu != nullptr);
+    p.span = span_of(d, cu != nullptr, scans);
     p.slots = dr::scan_slots(p.rows, p.span);
     return p;
 }
-cudaError_t scan(const dr::ScanParams& p, int io, cudaStream_t st) {
-    return io == DR_BF16 && p.rows > 0 ? dr::linear_scan_tc(p, st) : dr::linear_scan_simt(p, io, st);
-}
-// Room for the segments' states, whether the sequences come dense or packed.
+// Room for the segments' states, whether the sequences come dense or packed, of one scan or of three together.
 size_t linear_bytes(const dr_linear_desc* d) {
     const long long rows = (long long)d->B * d->T;
     long long slots = 0;
-    if (d->num_seqs == d->B) slots = std::max(slots, dr::scan_slots(rows, span_of(d, false)));
-    if (d->B == 1) slots = std::max(slots, dr::scan_slots(rows, span_of(d, true)));
+    for (int scans : {1, 3})
+        for (bool packed : {false, true})
+            if (packed ? d->B == 1 : d->num_seqs == d->B)
+                slots = std::max(slots, scans * dr::scan_slots(rows, span_of(d, packed, scans)));
     return std::max<size_t>(16, (size_t)slots * d->H * d->d_k * d->d_v * sizeof(float));
 }
 
@@ -154,7 +153,7 @@ int dr_linear_attn_fwd(const dr_linear_desc* desc, const void* q, const void* k,
     int rc = check_linear(desc, false, false);
     if (rc != DR_OK) return rc;
     if ((rc = check_layout(desc->B, desc->num_seqs, cu_seqlens)) != DR_OK) return rc;
-    dr::ScanParams p = scan_params(desc, g, cu_seqlens, workspace);
+    dr::ScanParams p = scan_params(desc, g, cu_seqlens, workspace, 1);
     if (p.s.N == 0) return DR_OK;
     if (!g || (p.rows > 0 && (!q || !k || !v || !o))) return DR_ERR_INVALID_ARG;
     if (any_misaligned({q, k, v, g, h0, o, hT, workspace})) return DR_ERR_ALIGNMENT;
@@ -162,7 +161,7 @@ int dr_linear_attn_fwd(const dr_linear_desc* desc, const void* q, const void* k,
     p.q = q; p.k = k; p.v = v; p.out = o;
     p.ld_q = desc->ld_q; p.ld_k = desc->ld_k; p.ld_v = desc->ld_v; p.ld_o = (long long)desc->H * desc->d_v;
     p.x0 = h0; p.xT = hT;
-    return cuda_status(scan(p, desc->io_dtype, static_cast<cudaStream_t>(stream)));
+    return cuda_status(dr::linear_scans(&p, 1, desc->io_dtype, static_cast<cudaStream_t>(stream)));
 }
 
 int dr_linear_attn_bwd(const dr_linear_desc* desc, const void* q, const void* k, const void* v,
@@ -172,32 +171,31 @@ int dr_linear_attn_bwd(const dr_linear_desc* desc, const void* q, const void* k,
     int rc = check_linear(desc, true, false);
     if (rc != DR_OK) return rc;
     if ((rc = check_layout(desc->B, desc->num_seqs, cu_seqlens)) != DR_OK) return rc;
-    const dr::ScanParams base = scan_params(desc, g, cu_seqlens, workspace);
+    const dr::ScanParams base = scan_params(desc, g, cu_seqlens, workspace, 3);
     if (base.s.N == 0) return DR_OK;
     if (!g || (base.rows > 0 && (!q || !k || !v || !dO || !dq || !dk || !dv))) return DR_ERR_INVALID_ARG;
     if (any_misaligned({q, k, v, g, h0, dO, dhT, dq, dk, dv, dh0, workspace})) return DR_ERR_ALIGNMENT;
     if (!workspace || workspace_bytes < linear_bytes(desc)) return DR_ERR_WORKSPACE;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const long long ld_g = (long long)desc->H * desc->d_v;
-    dr::ScanParams x = base;  // dq: (dO, v, k), the state transposed
-    x.dk = desc->d_v; x.dv = desc->d_k;
-    x.q = dO; x.k = v; x.v = k; x.out = dq;
-    x.ld_q = ld_g; x.ld_k = desc->ld_v; x.ld_v = desc->ld_k; x.ld_o = desc->ld_dq;
-    x.x0 = h0; x.x0_transposed = true;
-    cudaError_t e = base.rows ? scan(x, desc->io_dtype, st) : cudaSuccess;
-    if (e != cudaSuccess) return DR_ERR_CUDA;
-    x.reverse = true;         // dk: (v, dO, q) from the last token to the first
-    x.q = v; x.k = dO; x.v = q; x.out = dk;
-    x.ld_q = desc->ld_v; x.ld_k = ld_g; x.ld_v = desc->ld_q; x.ld_o = desc->ld_dk;
-    x.x0 = dhT;
-    e = base.rows ? scan(x, desc->io_dtype, st) : cudaSuccess;
-    if (e != cudaSuccess) return DR_ERR_CUDA;
-    x = base;                 // dv: (k, q, dO) likewise
-    x.reverse = true;
-    x.q = k; x.k = q; x.v = dO; x.out = dv;
-    x.ld_q = desc->ld_k; x.ld_k = desc->ld_q; x.ld_v = ld_g; x.ld_o = desc->ld_dv;
-    x.x0 = dhT; x.xT = dh0;
-    return cuda_status(scan(x, desc->io_dtype, st));
+    const long long ld_g = (long long)desc->H * desc->d_v, part = base.slots * desc->H * desc->d_k * desc->d_v;
+    dr::ScanParams x[3] = {base, base, base};
+    x[0].dk = x[1].dk = desc->d_v;  // dq: (dO, v, k), the state transposed
+    x[0].dv = x[1].dv = desc->d_k;
+    x[0].q = dO; x[0].k = v; x[0].v = k; x[0].out = dq;
+    x[0].ld_q = ld_g; x[0].ld_k = desc->ld_v; x[0].ld_v = desc->ld_k; x[0].ld_o = desc->ld_dq;
+    x[0].x0 = h0;
+    x[1].reverse = x[2].reverse = true;  // dk: (v, dO, q) from the last token to the first, likewise
+    x[1].q = v; x[1].k = dO; x[1].v = q; x[1].out = dk;
+    x[1].ld_q = desc->ld_v; x[1].ld_k = ld_g; x[1].ld_v = desc->ld_q; x[1].ld_o = desc->ld_dk;
+    x[1].x0 = x[2].x0 = dhT;
+    x[0].x0_transposed = x[1].x0_transposed = true;
+    x[2].q = k; x[2].k = q; x[2].v = dO; x[2].out = dv;  // dv: (k, q, dO)
+    x[2].ld_q = desc->ld_k; x[2].ld_k = desc->ld_q; x[2].ld_v = ld_g; x[2].ld_o = desc->ld_dv;
+    x[2].xT = dh0;
+    x[1].part += part;
+    x[2].part += 2 * part;
+    if (base.rows == 0) return cuda_status(dr::linear_scans(x + 2, 1, desc->io_dtype, st));
+    return cuda_status(dr::linear_scans(x, 3, desc->io_dtype, st));
 }
 
 int dr_linear_attn_step(const dr_linear_desc* desc, const void* q, const void* k, const void* v,

@@ -86,7 +86,7 @@ __device__ __forceinline__ bool find_tile_in_order(const Seqs& q, int R, long lo
                                                    long long& slot) {
     const int lane = threadIdx.x & 31;
     if (!q.cu) {
-        tiles = (q.T + R - 1) / R;
+        tiles = max((q.T + R - 1) / R, 1);  // a sequence without tokens counts as one
         if (item >= (long long)tiles * q.N) return false;
         seq = (int)(item / tiles);
         tile = (int)(item % tiles);
@@ -97,7 +97,7 @@ __device__ __forceinline__ bool find_tile_in_order(const Seqs& q, int R, long lo
     for (int s0 = 0; s0 < q.N; s0 += 32) {
         int row0, len = 0;
         if (s0 + lane < q.N) seq_rows(q, s0 + lane, row0, len);
-        const int n = max((len + R - 1) / R, 1), m = s0 + lane >= q.N ? 0 : n;  // one without tokens counts as one
+        const int m = s0 + lane >= q.N ? 0 : max((len + R - 1) / R, 1);
         int a = m, b = m > 1 ? m : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
