@@ -18,7 +18,7 @@ __device__ __forceinline__ bool make_work(const ScanParams& p, int item, int hea
     const int span = p.span ? p.span : (1 << 30) / kScanChunk;
     int tile, tiles;
     long long slot;
-    if (!find_tile_in_order(p.s, span * kScanChunk, item, w.seq, tile, tiles, slot)) return false;
+    if (!find_tile_in_order(p.s, span * kScanChunk, 1, item, w.seq, tile, tiles, slot)) return false;
     seq_rows(p.s, w.seq, w.row0, w.len);
     w.c0 = tile * span;
     w.chunks = min(span, (w.len + kScanChunk - 1) / kScanChunk - w.c0);

@@ -81,12 +81,13 @@ __device__ __forceinline__ bool find_tile(const Seqs& q, int R, long long item, 
 }
 
 // The same tiles in the order of the sequences: number `item`, and for a sequence of several tiles how many tiles
-// such sequences have before it (`slot`: a place for each of them); called by a whole warp.
-__device__ __forceinline__ bool find_tile_in_order(const Seqs& q, int R, long long item, int& seq, int& tile, int& tiles,
-                                                   long long& slot) {
+// such sequences have before it (`slot`: a place for each of them); called by a whole warp.  A sequence without tokens
+// counts as `least` tiles, 0 or 1.
+__device__ __forceinline__ bool find_tile_in_order(const Seqs& q, int R, int least, long long item, int& seq, int& tile,
+                                                   int& tiles, long long& slot) {
     const int lane = threadIdx.x & 31;
     if (!q.cu) {
-        tiles = max((q.T + R - 1) / R, 1);  // a sequence without tokens counts as one
+        tiles = max((q.T + R - 1) / R, least);
         if (item >= (long long)tiles * q.N) return false;
         seq = (int)(item / tiles);
         tile = (int)(item % tiles);
@@ -97,7 +98,7 @@ __device__ __forceinline__ bool find_tile_in_order(const Seqs& q, int R, long lo
     for (int s0 = 0; s0 < q.N; s0 += 32) {
         int row0, len = 0;
         if (s0 + lane < q.N) seq_rows(q, s0 + lane, row0, len);
-        const int m = s0 + lane >= q.N ? 0 : max((len + R - 1) / R, 1);
+        const int m = s0 + lane >= q.N ? 0 : max((len + R - 1) / R, least);
         int a = m, b = m > 1 ? m : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
