@@ -6,12 +6,16 @@
 //
 // Two kernels, so that every sum has one owner: no atomics, no fp32 image of a gradient in memory, the same
 // bits every time.  They form S and dP = dO V^T twice, 7 products where 5 would do.
-//   dq:     256 queries of a head, two halves of 128, against 64 keys a stage:
-//           S = Q K^T, dP = dO V^T, dQ += dS K.  The halves take turns, as in the forward kernel.
-//   dk, dv: 128 keys of a key head, against 64 queries a stage of all query heads that read it, one after another:
-//           S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.  S^T and dP^T have two buffers, used in turn by
-//           the two groups of four warps.
-// P and dS go over the columns of their scores as bf16 operands in tensor memory; they never are in shared memory.
+//   dq:     128 queries of a head, against 128 keys a stage: S = Q K^T, dP = dO V^T, dQ += dS K, issued as
+//           S(n + 1), dP(n + 1), dQ(n).  dP has two buffers in tensor memory, and dS takes the place of its dP.
+//   dk, dv: 128 keys of a key head, against 128 queries a stage of all query heads that read it, one after another:
+//           S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q, issued as dK(n - 1), dP(n), dV(n), S(n + 1), with P
+//           and dS in the places of S and dP.
+// While the tensor cores are at one product, the row threads prepare the operand of the next.  (Stages of 64 with two
+// buffers for everything were slower: a product of 128 x 64 from shared memory takes 61 cycles where 128 x 128
+// takes 66.)  P and dS are bf16 operands in tensor memory; they never are in shared memory.
+// Warps 0-3 and 4-7: a row per thread, the first and the second 64 columns of a stage.  Warp 8: products, 9: copies,
+// 10: the queries' statistics (dk, dv).
 #include "f32x2.cuh"
 #include "prompt_attn.cuh"
 #include "tc_block.cuh"
@@ -20,39 +24,35 @@
 namespace dr {
 namespace {
 
-constexpr int kRows = 128, kStage = 64, kThreads = 384, kInfos = 4;
+constexpr int kRows = 128, kThreads = 384, kInfos = 4, kFirst = 3, kSecond = 2;  // buffers of what a stage needs first and last, and of the rest
 constexpr int kRegs = 168, kRowRegs = 208, kOtherRegs = 88;  // of a thread: as launched, of the rows' threads, of the others
 static_assert(256 * kRowRegs + (kThreads - 256) * kOtherRegs <= kThreads * kRegs, "more than the block has");
 constexpr float kLog2e = 1.44269504088896340736f;
-__device__ __forceinline__ uint32_t s_col(int b) { return 64 * b; }        // of half or buffer b
-__device__ __forceinline__ uint32_t dp_col(int b) { return 128 + 64 * b; }
-__device__ __forceinline__ uint32_t acc_col(int b) { return 256 + 128 * b; }  // dQ of half b; dV, dK
 
 // Rounds run through the blocks forwards and backwards in turn: who gets a round's longer items gets the next one's shorter.
 __device__ __forceinline__ long long place(long long k) {
     return k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
 }
+template <int D> constexpr int kTileBytes = kRows * D * 2;  // 128 rows of a head
 
-// 128 rows of a head: four 64-channel column blocks at most.
-template <int D> constexpr int kRowTile = kRows * D * 2;
-template <int D> constexpr int kStageTile = kStage * D * 2;
-
-// D[128 x 64] = A[128 x d] B[64 x d]^T, both in shared memory.
+// D[128 x 128] = A[128 x d] B[128 x d]^T, both in shared memory.
 template <int D> __device__ __forceinline__ void scores(uint32_t d, uint64_t a, uint64_t b) {
 #pragma unroll
-    for (int kk = 0; kk < D; kk += 16)
-        mma_bf16(d, a + (kk >> 6) * (kRows * 128 / 16) + (kk & 63) / 8, b + (kk >> 6) * (kStage * 128 / 16) + (kk & 63) / 8,
-                 idesc_bf16(kRows, kStage), kk > 0);
+    for (int kk = 0; kk < D; kk += 16) {  // 16 channels: 32 bytes of a 128-byte row
+        const uint32_t off = (kk >> 6) * (kRows * 128 / 16) + (kk & 63) / 8;
+        mma_bf16(d, a + off, b + off, idesc_bf16(kRows, kRows), kk > 0);
+    }
 }
-// D[128 x d] (+)= A[128 x 64] (tensor memory) B[64 x d].
+// D[128 x d] (+)= A[128 x 128] B[128 x d], A in tensor memory as the two groups of warps leave it: 64 columns in 32, twice.
 template <int D> __device__ __forceinline__ void gather(uint32_t d, uint32_t a, uint64_t b, bool add) {
 #pragma unroll
-    for (int kk = 0; kk < kStage; kk += 16) mma_ts(d, a + kk / 2, b + kk * 8, idesc_bf16(kRows, D, false, true), add || kk > 0);
+    for (int kk = 0; kk < kRows; kk += 16)
+        mma_ts(d, a + (kk >> 6) * 64 + (kk & 63) / 2, b + kk * 8, idesc_bf16(kRows, D, false, true), add || kk > 0);
 }
-// One accumulator row, times f, as bf16.
-template <int D> __device__ __forceinline__ void store_row(uint32_t from, __nv_bfloat16* to, float f, bool on) {
+// Columns c0 .. c0 + N - 1 of an accumulator row, times f, as bf16.
+template <int N> __device__ __forceinline__ void store_row(uint32_t from, __nv_bfloat16* to, float f, bool on) {
 #pragma unroll
-    for (int c = 0; c < D; c += 32) {
+    for (int c = 0; c < N; c += 32) {
         float y[32];
         tmem_ld32(from + c, y);
         tmem_ld_wait();
@@ -65,81 +65,93 @@ template <int D> __device__ __forceinline__ void store_row(uint32_t from, __nv_b
     }
     tc_fence_before();
 }
-// A tile of 64 rows whose first `rows` belong to the sequence: zeros behind them.
+// A tile of which the first `rows` rows belong to the sequence; zeros behind them where `clean`.
 template <int D>
-__device__ __forceinline__ bool load_stage(volatile int& dead, uint8_t* tile, const CUtensorMap* map, uint64_t* full,
-                                           uint64_t* landed, uint32_t& landings, int head, int row, int rows) {
+__device__ __forceinline__ bool load_tile(volatile int& dead, uint8_t* tile, const CUtensorMap* map, uint64_t* full,
+                                          uint64_t* landed, uint32_t& landings, int head, int row, int rows, bool clean) {
     const int lane = threadIdx.x & 31;
-    uint64_t* bar = rows < kStage ? landed : full;
+    const bool cut = clean && rows < kRows;
+    uint64_t* bar = cut ? landed : full;
     if (lane == 0) {
-        mbar_arrive_expect_tx(bar, kStageTile<D>);
-        load_rows<kStage, D>(tile, map, bar, head, row);
+        mbar_arrive_expect_tx(bar, kTileBytes<D>);
+        load_rows<kRows, D>(tile, map, bar, head, row);
     }
     __syncwarp();
-    if (rows < kStage) {
+    if (cut) {
         if (!wait(dead, landed, landings++ & 1)) return false;
-        clear_rows<kStage, D>(tile, rows);
+        clear_rows<kRows, D>(tile, rows);
         if (lane == 0) mbar_arrive(full);
         __syncwarp();
     }
     return true;
 }
+// Counts through the phases of a ring of buffers.
+template <int N> struct Ring {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void step() {
+        if (++at == N) { at = 0; phase ^= 1; }
+    }
+};
+// 64 fp32 values as bf16 pairs to 32 columns.
+__device__ __forceinline__ void store_operand(uint32_t to, const float (&x)[64]) {
+    uint32_t z[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) z[j] = pack_bf16(x[2 * j], x[2 * j + 1]);
+    tmem_st32(to, z);
+    tmem_st_wait();
+    tc_fence_before();
+}
 
 // ================================================================== dq
 namespace dq {
-constexpr int kTile = 2 * kRows, kBuffers = 3;
+constexpr uint32_t kS = 0, kDP = 128, kDQ = 384;  // columns of tensor memory
 struct Item {
-    int any, row0, len, head, i0;
-    int lo[2], hi[2];  // stages of each half (none: lo >= hi)
+    int any, row0, len, head, i0, lo, hi;  // lo, hi: stages of keys
 };
 struct Control {
-    uint64_t qfull, qempty, kfull[kBuffers], kempty[kBuffers], vfull[kBuffers], vempty[kBuffers], landed;
-    uint64_t sfull[2], pfull[2], done[2], drained;
+    uint64_t qfull, qempty, kfull[kFirst], kempty[kFirst], vfull[kSecond], vempty[kSecond], landed;
+    uint64_t sfull, sread, dpfull[2], dsfull[2], done, drained;  // [2]: with the buffers of dP
     uint32_t tmem;
     volatile int dead;
     Item item[kInfos];
 };
 template <int D> struct Smem {
-    static constexpr int q = 0, g = 2 * kRowTile<D>, k = 2 * g, v = k + kBuffers * kStageTile<D>,
-                         control = v + kBuffers * kStageTile<D>, bytes = control + 1024;
+    static constexpr int q = 0, g = kTileBytes<D>, k = 2 * g, v = k + kFirst * kTileBytes<D>, control = v + kSecond * kTileBytes<D>,
+                         bytes = control + 1024;
     static_assert(sizeof(Control) <= 1024, "control block");
 };
 __device__ __forceinline__ Item make_item(const PromptParams& p, long long k) {
     const long long at = place(k);
     Item x = {};
     int seq = 0, tile = 0;
-    x.any = find_tile(p.s, kTile, at / p.Hq, seq, tile);
+    x.any = find_tile(p.s, kRows, at / p.Hq, seq, tile);
     if (!x.any) return x;
     x.head = (int)(at % p.Hq);
     seq_rows(p.s, seq, x.row0, x.len);
-    x.i0 = tile * kTile;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int first = x.i0 + h * kRows, end = min(first + kRows, x.len);
-        x.lo[h] = p.window ? max(0, first - p.window + 1) / kStage : 0;
-        x.hi[h] = first < x.len ? (end + kStage - 1) / kStage : x.lo[h];
-    }
+    x.i0 = tile * kRows;
+    x.lo = p.window ? max(0, x.i0 - p.window + 1) / kRows : 0;
+    x.hi = tile + 1;
     return x;
 }
-__device__ __forceinline__ int last_stage(const Item& x) { return max(x.hi[0], x.hi[1]); }  // one behind
 
 template <int D>
 __device__ __forceinline__ void copy_tiles(const PromptParams& p, const CUtensorMap* mq, const CUtensorMap* mg,
                                            const CUtensorMap* mk, const CUtensorMap* mv, uint8_t* smem, Control& ct) {
     const int lane = threadIdx.x & 31;
-    uint32_t n = 0, landings = 0;
+    uint32_t landings = 0;
+    Ring<kFirst> rk;
+    Ring<kSecond> rv;
     for (long long k = 0;; ++k) {
         const Item x = make_item(p, k);
+        // queries and the item's data: after the last item's products with its queries, and after the row threads
+        // have begun with it (so they are never two items behind)
         if (!wait(ct.dead, &ct.qempty, (k & 1) ^ 1)) return;
         if (lane == 0) {
             ct.item[k % kInfos] = x;
             if (x.any) {
-                mbar_arrive_expect_tx(&ct.qfull, 4 * kRowTile<D>);
-                for (int h = 0; h < 2; ++h) {
-                    const int row = x.row0 + x.i0 + h * kRows;
-                    load_rows<kRows, D>(smem + Smem<D>::q + h * kRowTile<D>, mq, &ct.qfull, x.head, row);
-                    load_rows<kRows, D>(smem + Smem<D>::g + h * kRowTile<D>, mg, &ct.qfull, x.head, row);
-                }
+                mbar_arrive_expect_tx(&ct.qfull, 2 * kTileBytes<D>);
+                load_rows<kRows, D>(smem + Smem<D>::q, mq, &ct.qfull, x.head, x.row0 + x.i0);
+                load_rows<kRows, D>(smem + Smem<D>::g, mg, &ct.qfull, x.head, x.row0 + x.i0);
             } else {
                 mbar_arrive(&ct.qfull);
             }
@@ -147,20 +159,19 @@ __device__ __forceinline__ void copy_tiles(const PromptParams& p, const CUtensor
         __syncwarp();
         if (!x.any) return;
         const int hk = x.head / p.G;
-        for (int t = x.lo[0]; t < last_stage(x); ++t, ++n) {
-            const uint32_t buf = n % kBuffers, parity = (n / kBuffers) & 1;
-            const int row = x.row0 + t * kStage;
-            if (!wait(ct.dead, &ct.kempty[buf], parity ^ 1)) return;
+        for (int t = x.lo; t < x.hi; ++t) {
+            const int row = x.row0 + t * kRows, rows = x.len - t * kRows;
             // keys behind the sequence are summed with a weight of zero: they have to be numbers
-            if (!load_stage<D>(ct.dead, smem + Smem<D>::k + buf * kStageTile<D>, mk, &ct.kfull[buf], &ct.landed, landings, hk,
-                               row, x.len - t * kStage))
+            if (!wait(ct.dead, &ct.kempty[rk.at], rk.phase ^ 1) ||
+                !load_tile<D>(ct.dead, smem + Smem<D>::k + rk.at * kTileBytes<D>, mk, &ct.kfull[rk.at], &ct.landed, landings, hk,
+                              row, rows, true))
                 return;
-            if (!wait(ct.dead, &ct.vempty[buf], parity ^ 1)) return;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&ct.vfull[buf], kStageTile<D>);
-                load_rows<kStage, D>(smem + Smem<D>::v + buf * kStageTile<D>, mv, &ct.vfull[buf], hk, row);
-            }
-            __syncwarp();
+            rk.step();
+            if (!wait(ct.dead, &ct.vempty[rv.at], rv.phase ^ 1) ||
+                !load_tile<D>(ct.dead, smem + Smem<D>::v + rv.at * kTileBytes<D>, mv, &ct.vfull[rv.at], &ct.landed, landings, hk,
+                              row, rows, false))
+                return;
+            rv.step();
         }
     }
 }
@@ -168,101 +179,110 @@ __device__ __forceinline__ void copy_tiles(const PromptParams& p, const CUtensor
 template <int D> __device__ __forceinline__ void issue(uint8_t* smem, Control& ct) {
     const uint32_t base = smem_u32(smem), tm = ct.tmem;
     const uint64_t q0 = desc_kmajor(Tile{base + Smem<D>::q, kRows}, 0), g0 = desc_kmajor(Tile{base + Smem<D>::g, kRows}, 0);
-    const uint64_t k0 = desc_kmajor(Tile{base + Smem<D>::k, kStage}, 0), v0 = desc_kmajor(Tile{base + Smem<D>::v, kStage}, 0);
-    const uint64_t kt0 = desc_mnmajor(Tile{base + Smem<D>::k, kStage}, 0);
-    uint32_t n = 0, np[2] = {0, 0};  // stages whose dQ was issued
+    const uint64_t k0 = desc_kmajor(Tile{base + Smem<D>::k, kRows}, 0), v0 = desc_kmajor(Tile{base + Smem<D>::v, kRows}, 0);
+    const uint64_t kt0 = desc_mnmajor(Tile{base + Smem<D>::k, kRows}, 0);
+    Ring<kFirst> ahead, behind;  // of K: of S and of dQ
+    Ring<kSecond> rv;
+    uint32_t ns = 0, nq = 0;  // stages whose S, whose dQ was issued
     for (long long k = 0;; ++k) {
         if (!wait(ct.dead, &ct.qfull, k & 1)) return;
         const Item x = ct.item[k % kInfos];
         if (!x.any) return;
-        const int first = x.lo[0], last = last_stage(x);
-        for (int t = first - 1; t < last; ++t) {
-            const uint32_t next = t < first ? n : n + 1, nb = next % kBuffers, b = n % kBuffers;
-            if (t + 1 < last) {
-                if (!wait(ct.dead, &ct.kfull[nb], (next / kBuffers) & 1) || !wait(ct.dead, &ct.vfull[nb], (next / kBuffers) & 1))
-                    return;
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bool sum = t >= x.lo[h] && t < x.hi[h], qk = t + 1 >= x.lo[h] && t + 1 < x.hi[h];
-                if (sum) {
-                    if (!wait(ct.dead, &ct.pfull[h], np[h]++ & 1)) return;
-                    tc_fence_after();
-                }
+        for (int t = x.lo; t <= x.hi; ++t) {
+            if (t < x.hi) {
+                if (!wait(ct.dead, &ct.kfull[ahead.at], ahead.phase) || !wait(ct.dead, &ct.sread, (ns & 1) ^ 1)) return;
+                tc_fence_after();
                 if (elect_one()) {
-                    if (sum) {
-                        gather<D>(tm + acc_col(h), tm + s_col(h), kt0 + b * (kStageTile<D> >> 4), t > x.lo[h]);
-                        if (t + 1 == x.hi[h]) mma_commit(&ct.done[h]);
-                    }
-                    if (qk) {
-                        scores<D>(tm + s_col(h), q0 + h * (kRowTile<D> >> 4), k0 + nb * (kStageTile<D> >> 4));
-                        scores<D>(tm + dp_col(h), g0 + h * (kRowTile<D> >> 4), v0 + nb * (kStageTile<D> >> 4));
-                        mma_commit(&ct.sfull[h]);
-                    }
+                    scores<D>(tm + kS, q0, k0 + ahead.at * (kTileBytes<D> >> 4));
+                    mma_commit(&ct.sfull);
                 }
                 __syncwarp();
+                if (!wait(ct.dead, &ct.vfull[rv.at], rv.phase)) return;
+                if (elect_one()) {  // over the dS of two stages before, whose dQ was issued
+                    scores<D>(tm + kDP + 128 * (ns & 1), g0, v0 + rv.at * (kTileBytes<D> >> 4));
+                    mma_commit(&ct.dpfull[ns & 1]);
+                    mma_commit(&ct.vempty[rv.at]);
+                    if (t + 1 == x.hi) mma_commit(&ct.qempty);
+                }
+                __syncwarp();
+                ahead.step();
+                rv.step();
+                ++ns;
             }
-            if (elect_one()) {
-                if (t >= first) mma_commit(&ct.kempty[b]);
-                if (t + 1 < last) mma_commit(&ct.vempty[nb]);
-                if (t + 2 == last) mma_commit(&ct.qempty);
+            if (t > x.lo) {
+                if (!wait(ct.dead, &ct.dsfull[nq & 1], (nq >> 1) & 1)) return;
+                tc_fence_after();
+                if (elect_one()) {
+                    gather<D>(tm + kDQ, tm + kDP + 128 * (nq & 1), kt0 + behind.at * (kTileBytes<D> >> 4), t > x.lo + 1);
+                    mma_commit(&ct.kempty[behind.at]);
+                    if (t == x.hi) mma_commit(&ct.done);
+                }
+                __syncwarp();
+                behind.step();
+                ++nq;
             }
-            __syncwarp();
-            if (t >= first) ++n;
         }
     }
 }
 
 template <int D> __device__ __forceinline__ void rows(const PromptParams& p, Control& ct) {
-    const int h = threadIdx.x / kRows, r = threadIdx.x % kRows;
-    const uint32_t tm = warp_lane_base(ct.tmem), ts = tm + s_col(h), td = tm + dp_col(h);
+    const int grp = threadIdx.x / kRows, r = threadIdx.x % kRows, c0 = 64 * grp;
+    const uint32_t tm = warp_lane_base(ct.tmem);
     const float c2 = p.scale * kLog2e;
-    uint32_t n = 0, done = 0;
+    uint32_t n = 0;
     for (long long k = 0;; ++k) {
         if (!wait(ct.dead, &ct.qfull, k & 1)) return;
         const Item x = ct.item[k % kInfos];
         warp_arrive(&ct.qempty);
         if (!x.any) return;
-        const int lo = h ? x.lo[1] : x.lo[0], hi = h ? x.hi[1] : x.hi[0];
-        if (lo >= hi) continue;
-        const int pos = x.i0 + h * kRows + r, w0 = pos & ~31;
+        const int pos = x.i0 + r, w0 = pos & ~31;
         const bool on = pos < x.len;
         const size_t at = (size_t)(x.row0 + pos) * p.Hq + x.head;
         const float lse = on ? p.lse[at] * -kLog2e : 0.f, delta = on ? -p.delta[at] : 0.f;
-        for (int t = lo; t < hi; ++t, ++n) {
-            const int j0 = t * kStage;
-            if (!wait(ct.dead, &ct.sfull[h], n & 1)) return;
+        for (int t = x.lo; t < x.hi; ++t, ++n) {
+            const int j0 = t * kRows + c0;
+            if (!wait(ct.dead, &ct.sfull, n & 1)) return;
             tc_fence_after();
-            float s[kStage], d[kStage];
-            tmem_ld32(ts, s);
-            tmem_ld32(ts + 32, s + 32);
-            tmem_ld32(td, d);
-            tmem_ld32(td + 32, d + 32);
+            float s[64];
+            tmem_ld32(tm + kS + c0, s);
+            tmem_ld32(tm + kS + c0 + 32, s + 32);
             tmem_ld_wait();
+            tc_fence_before();
+            warp_arrive(&ct.sread);
 #pragma unroll
-            for (int j = 0; j < kStage; j += 2) {
-                float2 z = fma2(make_float2(s[j], s[j + 1]), both(c2), both(lse));
-                z = make_float2(ex2(z.x), ex2(z.y));
-                z = mul2(z, add2(make_float2(d[j], d[j + 1]), both(delta)));
-                s[j] = z.x;
-                s[j + 1] = z.y;
+            for (int j = 0; j < 64; j += 2) {
+                const float2 z = fma2(make_float2(s[j], s[j + 1]), both(c2), both(lse));
+                s[j] = ex2(z.x);
+                s[j + 1] = ex2(z.y);
             }
-            if (j0 + kStage - 1 > w0 || (p.window && j0 <= w0 + 31 - p.window)) {
+            if (!wait(ct.dead, &ct.dpfull[n & 1], (n >> 1) & 1)) return;
+            tc_fence_after();
+            const uint32_t td = tm + kDP + 128 * (n & 1) + c0;
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+                float d[32];
+                tmem_ld32(td + c, d);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float2 z = mul2(make_float2(s[c + j], s[c + j + 1]), add2(make_float2(d[j], d[j + 1]), both(delta)));
+                    s[c + j] = z.x;
+                    s[c + j + 1] = z.y;
+                }
+            }
+            if (j0 + 63 > w0 || (p.window && j0 <= w0 + 31 - p.window)) {
                 const int up = pos - j0, down = p.window ? up - p.window : -1;
 #pragma unroll
-                for (int j = 0; j < kStage; ++j) s[j] = j <= up && j > down ? s[j] : 0.f;
+                for (int j = 0; j < 64; ++j) s[j] = j <= up && j > down ? s[j] : 0.f;
             }
-            uint32_t z[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) z[j] = pack_bf16(s[2 * j], s[2 * j + 1]);
-            tmem_st32(ts, z);
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&ct.pfull[h]);
+            store_operand(td, s);
+            warp_arrive(&ct.dsfull[n & 1]);
         }
-        if (!wait(ct.dead, &ct.done[h], done++ & 1)) return;
+        if (!wait(ct.dead, &ct.done, k & 1)) return;
         tc_fence_after();
-        store_row<D>(tm + acc_col(h), static_cast<__nv_bfloat16*>(p.dq) + (x.row0 + pos) * p.ld_dq + (long long)x.head * D, p.scale, on);
+        constexpr int N = D / 2;  // the groups' shares of the channels
+        store_row<N>(tm + kDQ + N * grp, static_cast<__nv_bfloat16*>(p.dq) + (x.row0 + pos) * p.ld_dq + (long long)x.head * D + N * grp,
+                     p.scale, on);
     }
 }
 
@@ -278,21 +298,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     if (threadIdx.x == 32) {
-        mbar_init(&ct.qfull, 1);
+        for (uint64_t* one : {&ct.qfull, &ct.landed, &ct.sfull, &ct.dpfull[0], &ct.dpfull[1], &ct.done, &ct.drained}) mbar_init(one, 1);
+        for (uint64_t* eight : {&ct.sread, &ct.dsfull[0], &ct.dsfull[1]}) mbar_init(eight, 8);
         mbar_init(&ct.qempty, 1 + 8);
-        mbar_init(&ct.landed, 1);
-        mbar_init(&ct.drained, 1);
-        for (int i = 0; i < kBuffers; ++i) {
-            mbar_init(&ct.kfull[i], 1);
-            mbar_init(&ct.kempty[i], 1);
-            mbar_init(&ct.vfull[i], 1);
-            mbar_init(&ct.vempty[i], 1);
-        }
-        for (int h = 0; h < 2; ++h) {
-            mbar_init(&ct.sfull[h], 1);
-            mbar_init(&ct.pfull[h], 4);
-            mbar_init(&ct.done[h], 1);
-        }
+        for (int i = 0; i < kFirst; ++i) mbar_init(&ct.kfull[i], 1), mbar_init(&ct.kempty[i], 1);
+        for (int i = 0; i < kSecond; ++i) mbar_init(&ct.vfull[i], 1), mbar_init(&ct.vempty[i], 1);
         ct.dead = 0;
         fence_barrier_init();
     }
@@ -318,22 +328,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ================================================================== dk, dv
 namespace dkv {
-constexpr int kBuffers = 4;
+constexpr uint32_t kS = 0, kDP = 128, kDV = 256, kDK = 384;  // columns of tensor memory
 struct Item {
     int any, row0, len, head, j0;  // head: of the keys
     int lo, hi;                    // query stages of each query head
 };
 struct Control {
-    uint64_t kvfull, kvempty, full[kBuffers], empty[kBuffers], landed;
-    uint64_t sfull[2], pfull[2], done, left, drained;
+    uint64_t kvfull, kvempty, qfull[kFirst], qempty[kFirst], gfull[kSecond], gempty[kSecond], stfull[2], stempty[2], landed;
+    uint64_t sfull, pfull, dpfull, dsfull, done, drained;
     uint32_t tmem;
     volatile int dead;
     Item item[kInfos];
-    __align__(16) float lse[kBuffers][kStage], delta[kBuffers][kStage];  // negative, lse in base 2
+    __align__(16) float lse[2][kRows], delta[2][kRows];  // negative, lse in base 2
 };
 template <int D> struct Smem {
-    static constexpr int k = 0, v = kRowTile<D>, q = 2 * v, g = q + kBuffers * kStageTile<D>,
-                         control = g + kBuffers * kStageTile<D>, bytes = control + 3072;
+    static constexpr int k = 0, v = kTileBytes<D>, q = 2 * v, g = q + kFirst * kTileBytes<D>, control = g + kSecond * kTileBytes<D>,
+                         bytes = control + 3072;
     static_assert(sizeof(Control) <= 3072, "control block");
 };
 // Items in the order of the sequences, the first keys first, which have the most queries: the blocks that run at the same
@@ -349,25 +359,26 @@ __device__ __forceinline__ Item make_item(const PromptParams& p, long long k) {
     x.head = (int)(at % p.H);
     seq_rows(p.s, seq, x.row0, x.len);
     x.j0 = tile * kRows;
-    x.lo = x.j0 / kStage;
+    x.lo = tile;
     const int end = p.window ? (int)min((long long)x.len, (long long)min(x.j0 + kRows, x.len) - 1 + p.window) : x.len;
-    x.hi = (end + kStage - 1) / kStage;
+    x.hi = (end + kRows - 1) / kRows;
     return x;
 }
 
-// Warp 9: tiles.  Warp 10: the rows' lse and D, the next stage's already on their way.
 template <int D>
 __device__ __forceinline__ void copy_tiles(const PromptParams& p, const CUtensorMap* mq, const CUtensorMap* mg,
                                            const CUtensorMap* mk, const CUtensorMap* mv, uint8_t* smem, Control& ct) {
     const int lane = threadIdx.x & 31;
-    uint32_t n = 0, landings = 0;
+    uint32_t landings = 0;
+    Ring<kFirst> rq;
+    Ring<kSecond> rg;
     for (long long k = 0;; ++k) {
         const Item x = make_item(p, k);
         if (!wait(ct.dead, &ct.kvempty, (k & 1) ^ 1)) return;
         if (lane == 0) {
             ct.item[k % kInfos] = x;
             if (x.any) {  // rows of no key get no result, so that they may be anything
-                mbar_arrive_expect_tx(&ct.kvfull, 2 * kRowTile<D>);
+                mbar_arrive_expect_tx(&ct.kvfull, 2 * kTileBytes<D>);
                 load_rows<kRows, D>(smem + Smem<D>::k, mk, &ct.kvfull, x.head, x.row0 + x.j0);
                 load_rows<kRows, D>(smem + Smem<D>::v, mv, &ct.kvfull, x.head, x.row0 + x.j0);
             } else {
@@ -377,49 +388,54 @@ __device__ __forceinline__ void copy_tiles(const PromptParams& p, const CUtensor
         __syncwarp();
         if (!x.any) return;
         for (int h = x.head * p.G; h < (x.head + 1) * p.G; ++h)
-            for (int t = x.lo; t < x.hi; ++t, ++n) {
-                const uint32_t buf = n % kBuffers;
-                if (!wait(ct.dead, &ct.empty[buf], ((n / kBuffers) & 1) ^ 1)) return;
-                if (!load_stage<D>(ct.dead, smem + Smem<D>::q + buf * kStageTile<D>, mq, &ct.full[buf], &ct.landed, landings, h,
-                                   x.row0 + t * kStage, x.len - t * kStage) ||
-                    !load_stage<D>(ct.dead, smem + Smem<D>::g + buf * kStageTile<D>, mg, &ct.full[buf], &ct.landed, landings, h,
-                                   x.row0 + t * kStage, x.len - t * kStage))
+            for (int t = x.lo; t < x.hi; ++t) {
+                // queries behind the sequence are summed with weights of zero: they have to be numbers
+                const int row = x.row0 + t * kRows, rows = x.len - t * kRows;
+                if (!wait(ct.dead, &ct.qempty[rq.at], rq.phase ^ 1) ||
+                    !load_tile<D>(ct.dead, smem + Smem<D>::q + rq.at * kTileBytes<D>, mq, &ct.qfull[rq.at], &ct.landed, landings, h,
+                                  row, rows, true))
                     return;
+                rq.step();
+                if (!wait(ct.dead, &ct.gempty[rg.at], rg.phase ^ 1) ||
+                    !load_tile<D>(ct.dead, smem + Smem<D>::g + rg.at * kTileBytes<D>, mg, &ct.gfull[rg.at], &ct.landed, landings, h,
+                                  row, rows, true))
+                    return;
+                rg.step();
             }
     }
 }
+// The queries' lse and D, the next stage's already on their way.
 __device__ __forceinline__ void copy_stats(const PromptParams& p, Control& ct) {
     const int lane = threadIdx.x & 31;
     uint32_t n = 0;
     for (long long k = 0;; ++k) {
         const Item x = make_item(p, k);
         if (!x.any) return;
-        const int stages = x.hi - x.lo, total = stages * p.G;
-        auto read = [&](int i, float (&l)[2], float (&d)[2]) {
+        int t = x.lo, h = x.head * p.G;  // of what is read next
+        float l[4], d[4], l2[4], d2[4];
+        auto read = [&] {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int pos = (x.lo + i % stages) * kStage + lane + 32 * j;
-                const bool on = i < total && pos < x.len;
-                const size_t at = on ? (size_t)(x.row0 + pos) * p.Hq + x.head * p.G + i / stages : 0;
-                l[j] = on ? p.lse[at] * -kLog2e : -INFINITY;  // no query: no weight
-                d[j] = on ? -p.delta[at] : 0.f;
+            for (int j = 0; j < 4; ++j) {
+                const int pos = t * kRows + lane + 32 * j;
+                const bool on = h < (x.head + 1) * p.G && pos < x.len;
+                const size_t at = on ? (size_t)(x.row0 + pos) * p.Hq + h : 0;
+                l2[j] = on ? p.lse[at] * -kLog2e : -INFINITY;  // no query: no weight
+                d2[j] = on ? -p.delta[at] : 0.f;
             }
+            if (++t == x.hi) t = x.lo, ++h;
         };
-        float l[2], d[2];
-        read(0, l, d);
-        for (int i = 0; i < total; ++i, ++n) {
-            const uint32_t buf = n % kBuffers;
-            float l2[2], d2[2];
-            read(i + 1, l2, d2);
-            if (!wait(ct.dead, &ct.empty[buf], ((n / kBuffers) & 1) ^ 1)) return;
+        read();
+        for (int i = 0; i < (x.hi - x.lo) * p.G; ++i, ++n) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                ct.lse[buf][lane + 32 * j] = l[j];
-                ct.delta[buf][lane + 32 * j] = d[j];
-                l[j] = l2[j];
-                d[j] = d2[j];
+            for (int j = 0; j < 4; ++j) l[j] = l2[j], d[j] = d2[j];
+            read();
+            if (!wait(ct.dead, &ct.stempty[n & 1], ((n >> 1) & 1) ^ 1)) return;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                ct.lse[n & 1][lane + 32 * j] = l[j];
+                ct.delta[n & 1][lane + 32 * j] = d[j];
             }
-            warp_arrive(&ct.full[buf]);
+            warp_arrive(&ct.stfull[n & 1]);
         }
     }
 }
@@ -427,49 +443,62 @@ __device__ __forceinline__ void copy_stats(const PromptParams& p, Control& ct) {
 template <int D> __device__ __forceinline__ void issue(const PromptParams& p, uint8_t* smem, Control& ct) {
     const uint32_t base = smem_u32(smem), tm = ct.tmem;
     const uint64_t k0 = desc_kmajor(Tile{base + Smem<D>::k, kRows}, 0), v0 = desc_kmajor(Tile{base + Smem<D>::v, kRows}, 0);
-    const uint64_t q0 = desc_kmajor(Tile{base + Smem<D>::q, kStage}, 0), g0 = desc_kmajor(Tile{base + Smem<D>::g, kStage}, 0);
-    const uint64_t qt0 = desc_mnmajor(Tile{base + Smem<D>::q, kStage}, 0), gt0 = desc_mnmajor(Tile{base + Smem<D>::g, kStage}, 0);
-    uint32_t n = 0;
+    const uint64_t q0 = desc_kmajor(Tile{base + Smem<D>::q, kRows}, 0), g0 = desc_kmajor(Tile{base + Smem<D>::g, kRows}, 0);
+    const uint64_t qt0 = desc_mnmajor(Tile{base + Smem<D>::q, kRows}, 0), gt0 = desc_mnmajor(Tile{base + Smem<D>::g, kRows}, 0);
+    Ring<kFirst> ahead, behind;  // of Q: of S and of dK
+    Ring<kSecond> rg;
+    uint32_t n = 0;  // stages before
     for (long long k = 0;; ++k) {
         if (!wait(ct.dead, &ct.kvfull, k & 1)) return;
         const Item x = ct.item[k % kInfos];
         if (!x.any) return;
         const int total = (x.hi - x.lo) * p.G;
-        for (int i = -1; i < total; ++i) {
-            const uint32_t next = i < 0 ? n : n + 1, nb = next % kBuffers, b = n % kBuffers;
-            if (i + 1 < total) {
-                if (!wait(ct.dead, &ct.full[nb], (next / kBuffers) & 1)) return;
+        for (int i = -1; i <= total; ++i) {
+            if (i > 0) {  // dK of the stage before
+                if (!wait(ct.dead, &ct.dsfull, (n - 1) & 1)) return;
                 tc_fence_after();
-                if (elect_one()) {  // over the operands of stage next - 2, whose products were issued before
-                    scores<D>(tm + s_col(next & 1), k0, q0 + nb * (kStageTile<D> >> 4));
-                    scores<D>(tm + dp_col(next & 1), v0, g0 + nb * (kStageTile<D> >> 4));
-                    mma_commit(&ct.sfull[next & 1]);
-                    mbar_arrive(&ct.sfull[next & 1]);  // hands on the rows' lse and D, which came with `full`
-                    if (i + 2 == total) mma_commit(&ct.kvempty);
+                if (elect_one()) {
+                    gather<D>(tm + kDK, tm + kDP, qt0 + behind.at * (kTileBytes<D> >> 4), i > 1);
+                    mma_commit(&ct.qempty[behind.at]);
+                    if (i == total) mma_commit(&ct.done);
                 }
                 __syncwarp();
+                behind.step();
             }
-            if (i < 0) {
-                if (!wait(ct.dead, &ct.left, (k & 1) ^ 1)) return;  // the sums of the item before have been read
-                continue;
+            if (i >= 0 && i < total) {
+                if (!wait(ct.dead, &ct.gfull[rg.at], rg.phase)) return;
+                if (elect_one()) {
+                    scores<D>(tm + kDP, v0, g0 + rg.at * (kTileBytes<D> >> 4));
+                    mma_commit(&ct.dpfull);
+                    if (i + 1 == total) mma_commit(&ct.kvempty);
+                }
+                __syncwarp();
+                if (!wait(ct.dead, &ct.pfull, n & 1)) return;
+                tc_fence_after();
+                if (elect_one()) {
+                    gather<D>(tm + kDV, tm + kS, gt0 + rg.at * (kTileBytes<D> >> 4), i > 0);
+                    mma_commit(&ct.gempty[rg.at]);
+                }
+                __syncwarp();
+                rg.step();
+                ++n;
             }
-            if (!wait(ct.dead, &ct.pfull[n & 1], (n >> 1) & 1)) return;
-            tc_fence_after();
-            if (elect_one()) {
-                gather<D>(tm + acc_col(0), tm + s_col(n & 1), gt0 + b * (kStageTile<D> >> 4), i > 0);
-                gather<D>(tm + acc_col(1), tm + dp_col(n & 1), qt0 + b * (kStageTile<D> >> 4), i > 0);
-                mma_commit(&ct.empty[b]);
-                if (i + 1 == total) mma_commit(&ct.done);
+            if (i + 1 < total) {
+                if (!wait(ct.dead, &ct.qfull[ahead.at], ahead.phase)) return;
+                if (elect_one()) {  // over P, whose dV was issued
+                    scores<D>(tm + kS, k0, q0 + ahead.at * (kTileBytes<D> >> 4));
+                    mma_commit(&ct.sfull);
+                }
+                __syncwarp();
+                ahead.step();
             }
-            __syncwarp();
-            ++n;
         }
     }
 }
 
 template <int D> __device__ __forceinline__ void rows(const PromptParams& p, Control& ct) {
-    const int grp = threadIdx.x / kRows, r = threadIdx.x % kRows;
-    const uint32_t tm = warp_lane_base(ct.tmem), ts = tm + s_col(grp), td = tm + dp_col(grp);
+    const int grp = threadIdx.x / kRows, r = threadIdx.x % kRows, c0 = 64 * grp;
+    const uint32_t tm = warp_lane_base(ct.tmem), ts = tm + kS + c0, td = tm + kDP + c0;
     const float c2 = p.scale * kLog2e;
     uint32_t n = 0;
     for (long long k = 0;; ++k) {
@@ -477,64 +506,65 @@ template <int D> __device__ __forceinline__ void rows(const PromptParams& p, Con
         const Item x = ct.item[k % kInfos];
         warp_arrive(&ct.kvempty);
         if (!x.any) return;
-        const int stages = x.hi - x.lo, total = stages * p.G, pos = x.j0 + r, w0 = pos & ~31;
+        const int total = (x.hi - x.lo) * p.G, pos = x.j0 + r, w0 = pos & ~31;
+        int t = x.lo;
         for (int i = 0; i < total; ++i, ++n) {
-            if ((n & 1) != (uint32_t)grp) continue;
-            const int i0 = (x.lo + i % stages) * kStage;
-            if (!wait(ct.dead, &ct.sfull[grp], (n >> 1) & 1)) return;
+            const int i0 = t * kRows + c0;
+            if (++t == x.hi) t = x.lo;
+            const float4* lse = reinterpret_cast<const float4*>(ct.lse[n & 1] + c0);
+            const float4* delta = reinterpret_cast<const float4*>(ct.delta[n & 1] + c0);
+            if (!wait(ct.dead, &ct.stfull[n & 1], (n >> 1) & 1) || !wait(ct.dead, &ct.sfull, n & 1)) return;
             tc_fence_after();
-            const float4* lse = reinterpret_cast<const float4*>(ct.lse[n % kBuffers]);
-            const float4* delta = reinterpret_cast<const float4*>(ct.delta[n % kBuffers]);
-            float s[kStage], d[kStage];
+            float s[64];
             tmem_ld32(ts, s);
             tmem_ld32(ts + 32, s + 32);
-            tmem_ld32(td, d);
-            tmem_ld32(td + 32, d + 32);
             tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < kStage; j += 4) {
+            for (int j = 0; j < 64; j += 4) {
                 const float4 l = lse[j / 4];
-                float2 z = fma2(make_float2(s[j], s[j + 1]), both(c2), make_float2(l.x, l.y));
-                float2 y = fma2(make_float2(s[j + 2], s[j + 3]), both(c2), make_float2(l.z, l.w));
+                const float2 z = fma2(make_float2(s[j], s[j + 1]), both(c2), make_float2(l.x, l.y));
+                const float2 y = fma2(make_float2(s[j + 2], s[j + 3]), both(c2), make_float2(l.z, l.w));
                 s[j] = ex2(z.x);
                 s[j + 1] = ex2(z.y);
                 s[j + 2] = ex2(y.x);
                 s[j + 3] = ex2(y.y);
             }
-            const bool masked = i0 < w0 + 31 || (p.window && i0 + kStage - 1 >= w0 + p.window);
-            const int from = pos - i0, upto = p.window ? from + p.window : kStage;  // queries that see this key
+            const bool masked = i0 < w0 + 31 || (p.window && i0 + 63 >= w0 + p.window);
+            const int from = pos - i0, upto = p.window ? from + p.window : 64;  // queries that see this key
             if (masked)
 #pragma unroll
-                for (int j = 0; j < kStage; ++j) s[j] = j >= from && j < upto ? s[j] : 0.f;
-            uint32_t z[32];
+                for (int j = 0; j < 64; ++j) s[j] = j >= from && j < upto ? s[j] : 0.f;
+            store_operand(ts, s);
+            warp_arrive(&ct.pfull);
+            if (!wait(ct.dead, &ct.dpfull, n & 1)) return;
+            tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) z[j] = pack_bf16(s[2 * j], s[2 * j + 1]);
-            tmem_st32(ts, z);
+            for (int c = 0; c < 64; c += 32) {
+                float d[32];
+                tmem_ld32(td + c, d);
+                tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < kStage; j += 4) {
-                const float4 e = delta[j / 4];
-                const float2 a = mul2(make_float2(s[j], s[j + 1]), add2(make_float2(d[j], d[j + 1]), make_float2(e.x, e.y)));
-                const float2 b = mul2(make_float2(s[j + 2], s[j + 3]), add2(make_float2(d[j + 2], d[j + 3]), make_float2(e.z, e.w)));
-                d[j] = a.x; d[j + 1] = a.y; d[j + 2] = b.x; d[j + 3] = b.y;
+                for (int j = 0; j < 32; j += 4) {
+                    const float4 e = delta[(c + j) / 4];
+                    const float2 a = mul2(make_float2(s[c + j], s[c + j + 1]), add2(make_float2(d[j], d[j + 1]), make_float2(e.x, e.y)));
+                    const float2 b = mul2(make_float2(s[c + j + 2], s[c + j + 3]), add2(make_float2(d[j + 2], d[j + 3]), make_float2(e.z, e.w)));
+                    s[c + j] = a.x; s[c + j + 1] = a.y; s[c + j + 2] = b.x; s[c + j + 3] = b.y;
+                }
             }
             if (masked)  // a weight of zero times what is not finite is no zero
 #pragma unroll
-                for (int j = 0; j < kStage; ++j) d[j] = j >= from && j < upto ? d[j] : 0.f;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) z[j] = pack_bf16(d[2 * j], d[2 * j + 1]);
-            tmem_st32(td, z);
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&ct.pfull[grp]);
+                for (int j = 0; j < 64; ++j) s[j] = j >= from && j < upto ? s[j] : 0.f;
+            store_operand(td, s);
+            warp_arrive(&ct.stempty[n & 1]);
+            warp_arrive(&ct.dsfull);
         }
         if (!wait(ct.dead, &ct.done, k & 1)) return;
         tc_fence_after();
         const bool on = pos < x.len;
         if (grp == 0)
-            store_row<D>(tm + acc_col(0), static_cast<__nv_bfloat16*>(p.dv) + (x.row0 + pos) * p.ld_dv + (long long)x.head * D, 1.f, on);
+            store_row<D>(tm + kDV, static_cast<__nv_bfloat16*>(p.dv) + (x.row0 + pos) * p.ld_dv + (long long)x.head * D, 1.f, on);
         else
-            store_row<D>(tm + acc_col(1), static_cast<__nv_bfloat16*>(p.dk) + (x.row0 + pos) * p.ld_dk + (long long)x.head * D, p.scale, on);
-        warp_arrive(&ct.left);
+            store_row<D>(tm + kDK, static_cast<__nv_bfloat16*>(p.dk) + (x.row0 + pos) * p.ld_dk + (long long)x.head * D, p.scale, on);
     }
 }
 
@@ -550,20 +580,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_relinquish();
     }
     if (threadIdx.x == 32) {
-        mbar_init(&ct.kvfull, 1);
+        for (uint64_t* one : {&ct.kvfull, &ct.landed, &ct.sfull, &ct.dpfull, &ct.done, &ct.drained}) mbar_init(one, 1);
+        for (uint64_t* eight : {&ct.pfull, &ct.dsfull}) mbar_init(eight, 8);
         mbar_init(&ct.kvempty, 1 + 8);
-        mbar_init(&ct.landed, 1);
-        mbar_init(&ct.drained, 1);
-        mbar_init(&ct.done, 1);
-        mbar_init(&ct.left, 8);
-        for (int i = 0; i < kBuffers; ++i) {
-            mbar_init(&ct.full[i], 3);  // queries, gradients, statistics
-            mbar_init(&ct.empty[i], 1);
-        }
-        for (int h = 0; h < 2; ++h) {
-            mbar_init(&ct.sfull[h], 2);
-            mbar_init(&ct.pfull[h], 4);
-        }
+        for (int i = 0; i < kFirst; ++i) mbar_init(&ct.qfull[i], 1), mbar_init(&ct.qempty[i], 1);
+        for (int i = 0; i < kSecond; ++i) mbar_init(&ct.gfull[i], 1), mbar_init(&ct.gempty[i], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&ct.stfull[i], 1), mbar_init(&ct.stempty[i], 8);
         ct.dead = 0;
         fence_barrier_init();
     }
@@ -604,18 +626,15 @@ template <int D> cudaError_t launch(const PromptParams& p, cudaStream_t st) {
     if (sms < 1) return cudaErrorInvalidDevice;
     auto blocks = [&](long long items) { return (int)(items < sms ? items : sms); };
     const long long ld_g = (long long)p.Hq * D;
-    auto maps = [&](CUtensorMap (&m)[4], int own, int other) {  // boxes of `own` query rows and `other` key rows
-        return head_rows_map(&m[0], p.q, D, p.Hq, p.rows, p.ld_q, own) && head_rows_map(&m[1], p.dO, D, p.Hq, p.rows, ld_g, own) &&
-               head_rows_map(&m[2], p.k, D, p.H, p.rows, p.ld_k, other) && head_rows_map(&m[3], p.v, D, p.H, p.rows, p.ld_v, other);
-    };
     CUtensorMap m[4];
-    if (!maps(m, kRows, kStage)) return cudaErrorInvalidValue;
+    if (!head_rows_map(&m[0], p.q, D, p.Hq, p.rows, p.ld_q, kRows) || !head_rows_map(&m[1], p.dO, D, p.Hq, p.rows, ld_g, kRows) ||
+        !head_rows_map(&m[2], p.k, D, p.H, p.rows, p.ld_k, kRows) || !head_rows_map(&m[3], p.v, D, p.H, p.rows, p.ld_v, kRows))
+        return cudaErrorInvalidValue;
     {
         TraceScope ts("prompt_dq_tc", st);
-        dq::prompt_dq_tc_kernel<D><<<blocks(most_tiles(p.s, dq::kTile) * p.Hq), kThreads, dq::Smem<D>::bytes, st>>>(p, m[0], m[1], m[2], m[3]);
+        dq::prompt_dq_tc_kernel<D><<<blocks(most_tiles(p.s, kRows) * p.Hq), kThreads, dq::Smem<D>::bytes, st>>>(p, m[0], m[1], m[2], m[3]);
         if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     }
-    if (!maps(m, kStage, kRows)) return cudaErrorInvalidValue;
     // A block for each item, so that one that is through takes the next in order: 1066 us instead of 1425 with a block for
     // each SM and its items dealt out beforehand (b8 t4096, 16 heads of 128, four of keys).
     const long long keys = most_tiles(p.s, kRows) * p.H;
