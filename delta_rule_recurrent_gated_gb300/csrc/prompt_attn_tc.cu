@@ -13,6 +13,7 @@
 // Softmax in base 2 against a reference m that follows the row's maximum only when that has passed it by more
 // than 8: weights stay below 2^8, which bf16 and the fp32 sums hold as well, and O is rarely rescaled.  P is
 // rounded to bf16 as an operand (2^-8 of a weight at most); the sum of the weights takes them unrounded.
+#include "f32x2.cuh"
 #include "prompt_attn.cuh"
 #include "tc_block.cuh"
 #include "trace.cuh"
@@ -232,20 +233,21 @@ template <int D> __device__ __forceinline__ void soften(const PromptParams& p, C
                 }
             }
             const float ref = m == kNegInf ? 0.f : -m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float2 sum[2] = {both(0.f), both(0.f)};
 #pragma unroll
             for (int c = 0; c < kStage; c += 64) {
                 uint32_t z[32];
 #pragma unroll
                 for (int j = 0; j < 64; j += 2) {
-                    const float a = ex2(fmaf(s[c + j], c2, ref)), b = ex2(fmaf(s[c + j + 1], c2, ref));
-                    sum[j & 2] += a;
-                    sum[(j & 2) + 1] += b;
-                    z[j / 2] = pack_bf16(a, b);
+                    float2 e = fma2(make_float2(s[c + j], s[c + j + 1]), both(c2), both(ref));
+                    e = make_float2(ex2(e.x), ex2(e.y));
+                    sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], e);
+                    z[j / 2] = pack_bf16(e.x, e.y);
                 }
                 tmem_st32(ts + c / 2, z);
             }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            sum[0] = add2(sum[0], sum[1]);
+            l += sum[0].x + sum[0].y;
             tmem_st_wait();
             tc_fence_before();
             warp_arrive(&ct.pfull[h]);
