@@ -36,7 +36,7 @@ struct Item {
 };
 struct Control {
     uint64_t qfull, qempty, kfull[kBuffers], kempty[kBuffers], vfull[kBuffers], vempty[kBuffers], landed;
-    uint64_t sfull[2], pfull[2], odone[2], drained;
+    uint64_t sfull[2], pfull[2][2], odone[2], drained;  // pfull: of each half the first and the last 64 columns
     uint32_t tmem;
     volatile int dead;
     Item item[kInfos];
@@ -141,18 +141,23 @@ __device__ __forceinline__ void issue(const PromptParams& p, uint8_t* smem, Cont
             for (int h = 0; h < 2; ++h) {
                 const bool pv = t >= x.lo[h] && t < x.hi[h], qk = t + 1 >= x.lo[h] && t + 1 < x.hi[h];
                 if (pv) {
-                    if (!wait(ct.dead, &ct.pfull[h], np[h]++ & 1)) return;
-                    tc_fence_after();
+                    const uint64_t vd = v0 + (nv % kBuffers) * (Smem<D>::tile >> 4);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part) {
+                        if (!wait(ct.dead, &ct.pfull[h][part], np[h] & 1)) return;
+                        tc_fence_after();
+                        if (elect_one()) {
+#pragma unroll
+                            for (int kk = 64 * part; kk < 64 * part + 64; kk += 16)  // 16 positions: 16 rows of 128 bytes
+                                mma_ts(tm + o_col(h), tm + s_col(h) + kk / 2, vd + kk * 8, idesc_bf16(kHalf, D, false, true),
+                                       t > x.lo[h] || kk > 0);
+                            if (part && t + 1 == x.hi[h]) mma_commit(&ct.odone[h]);
+                        }
+                        __syncwarp();
+                    }
+                    ++np[h];
                 }
                 if (elect_one()) {
-                    if (pv) {
-                        const uint64_t vd = v0 + (nv % kBuffers) * (Smem<D>::tile >> 4);
-#pragma unroll
-                        for (int kk = 0; kk < kStage; kk += 16)  // 16 positions: 16 rows of 128 bytes
-                            mma_ts(tm + o_col(h), tm + s_col(h) + kk / 2, vd + kk * 8, idesc_bf16(kHalf, D, false, true),
-                                   t > x.lo[h] || kk > 0);
-                        if (t + 1 == x.hi[h]) mma_commit(&ct.odone[h]);
-                    }
                     if (qk) {
                         const uint64_t kd = k0 + (nk % kBuffers) * (Smem<D>::tile >> 4), qd = q0 + h * (Smem<D>::tile >> 4);
 #pragma unroll
@@ -245,12 +250,12 @@ template <int D> __device__ __forceinline__ void soften(const PromptParams& p, C
                     z[j / 2] = pack_bf16(e.x, e.y);
                 }
                 tmem_st32(ts + c / 2, z);
+                tmem_st_wait();
+                tc_fence_before();
+                warp_arrive(&ct.pfull[h][c / 64]);
             }
             sum[0] = add2(sum[0], sum[1]);
             l += sum[0].x + sum[0].y;
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&ct.pfull[h]);
         }
         if (!wait(ct.dead, &ct.odone[h], done++ & 1)) return;
         tc_fence_after();
@@ -298,7 +303,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(&ct.sfull[h], 1);
-            mbar_init(&ct.pfull[h], 4);
+            mbar_init(&ct.pfull[h][0], 4);
+            mbar_init(&ct.pfull[h][1], 4);
             mbar_init(&ct.odone[h], 1);
         }
         ct.dead = 0;
