@@ -215,13 +215,23 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
             x = load4(from + i);
         }
     }
-    const int tiles = (w.len + R - 1) / R, step = p.reverse ? -1 : 1;
+    const int tiles = (w.len + R - 1) / R;
+    const long long step = (p.reverse ? -1ll : 1ll) * p.H * size;
     float* at = const_cast<float*>(w.before) + i;
-    for (int n = 0, t = p.reverse ? tiles - 1 : 0; n < tiles; ++n, t += step, at += (long long)step * p.H * size) {
-        const float4 own = n + 1 < tiles ? load4(at) : x;  // the last segment's own state was not formed
-        store4(at, x);
-        const float a = decay(g, (float)min(R, w.len - t * R));
-        x = make_float4(fmaf(a, x.x, own.x), fmaf(a, x.y, own.y), fmaf(a, x.z, own.z), fmaf(a, x.w, own.w));
+    // four segments' own states are read at once (the last segment's was not formed, nothing comes after it)
+    for (int n = 0; n < tiles; n += 4) {
+        float4 own[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) own[k] = n + k + 1 < tiles ? load4(at + k * step) : x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (n + k >= tiles) break;
+            store4(at + k * step, x);
+            const int t = p.reverse ? tiles - 1 - n - k : n + k;
+            const float a = decay(g, (float)min(R, w.len - t * R));
+            x = make_float4(fmaf(a, x.x, own[k].x), fmaf(a, x.y, own[k].y), fmaf(a, x.z, own[k].z), fmaf(a, x.w, own[k].w));
+        }
+        at += 4 * step;
     }
 }
 

@@ -62,6 +62,11 @@ dr::PromptParams prompt_params(const dr_prompt_desc* d, const void* q, const voi
     return p;
 }
 
+size_t delta_bytes(const dr_prompt_desc* d) { return ((size_t)d->B * d->T * d->Hq * sizeof(float) + 15) / 16 * 16; }
+size_t heads_bytes(const dr_prompt_desc* d) {
+    return d->io_dtype == DR_F32 ? dr::prompt_attn_heads_bytes((long long)d->B * d->T, d->num_seqs, d->Hq, d->H, d->d) : 0;
+}
+
 bool linear_size(int d, int io, bool step) { return d == 64 || d == 128 || ((io == DR_F32 || step) && (d == 16 || d == 32)); }
 int check_linear(const dr_linear_desc* d, bool bwd, bool step) {
     if (!d) return DR_ERR_INVALID_ARG;
@@ -116,13 +121,13 @@ int dr_prompt_attn_fwd(const dr_prompt_desc* desc, const void* q, const void* k,
     if (any_misaligned({q, k, v, o, lse})) return DR_ERR_ALIGNMENT;
     p.o = o; p.lse = lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return cuda_status(desc->io_dtype == DR_BF16 ? dr::prompt_attn_fwd_tc(p, st) : dr::prompt_attn_fwd_simt(p, desc->io_dtype, st));
+    return cuda_status(desc->io_dtype == DR_BF16 ? dr::prompt_attn_fwd_tc(p, st) : dr::prompt_attn_fwd_simt(p, st));
 }
 
 size_t dr_prompt_attn_workspace_bytes(const dr_prompt_desc* desc) {
     if (check_prompt(desc, true) != DR_OK) return 0;
-    const size_t n = (size_t)desc->B * desc->T * desc->Hq * sizeof(float);
-    return n < 16 ? 16 : (n + 15) / 16 * 16;
+    const size_t n = delta_bytes(desc) + heads_bytes(desc);
+    return n < 16 ? 16 : n;
 }
 
 int dr_prompt_attn_bwd(const dr_prompt_desc* desc, const void* q, const void* k, const void* v,
@@ -139,8 +144,9 @@ int dr_prompt_attn_bwd(const dr_prompt_desc* desc, const void* q, const void* k,
     if (!workspace || workspace_bytes < dr_prompt_attn_workspace_bytes(desc)) return DR_ERR_WORKSPACE;
     p.o = const_cast<void*>(o); p.lse = const_cast<float*>(lse); p.dO = dO;
     p.dq = dq; p.dk = dk; p.dv = dv; p.delta = static_cast<float*>(workspace);
+    if (heads_bytes(desc)) p.heads = p.delta + delta_bytes(desc) / sizeof(float);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return cuda_status(desc->io_dtype == DR_BF16 ? dr::prompt_attn_bwd_tc(p, st) : dr::prompt_attn_bwd_simt(p, desc->io_dtype, st));
+    return cuda_status(desc->io_dtype == DR_BF16 ? dr::prompt_attn_bwd_tc(p, st) : dr::prompt_attn_bwd_simt(p, st));
 }
 
 size_t dr_linear_attn_workspace_bytes(const dr_linear_desc* desc) {

@@ -1,5 +1,5 @@
-// prompt_attn.cu -- causal attention over whole prompts on the CUDA cores, fp32 arithmetic (dr.h,
-// dr_prompt_attn_fwd / dr_prompt_attn_bwd).
+// prompt_attn.cu -- causal attention over whole prompts in fp32, on the CUDA cores (dr.h, dr_prompt_attn_fwd /
+// dr_prompt_attn_bwd), and the first step of the gradient for both types.
 //
 //   s_ij = scale q_i.k_j for the keys j <= i that the window shows;  p_ij = e^{s_ij - lse_i};
 //   o_i = sum_j p_ij v_j;  D_i = dO_i.o_i;  ds_ij = p_ij (dO_i.v_j - D_i)
@@ -7,8 +7,7 @@
 //
 // A block holds 64 rows (queries, or keys for dk and dv) and streams the other side in tiles.  Every thread of
 // a 16 x 16 arrangement has four rows: its part of the scores, and of the sums a sixteenth of the channels.  dk
-// and dv are summed over the query heads of a group inside the block, in order: no atomics, the same bits every
-// time.
+// and dv are summed over the query heads of a group in order: no atomics, the same bits every time.
 #include "common.cuh"
 #include "prompt_attn.cuh"
 #include "trace.cuh"
@@ -25,8 +24,8 @@ constexpr float kNegInf = -INFINITY;
 template <int D> constexpr int kPitch = D + 4;
 
 // R rows of a tensor from src on, zeros from row n on.
-template <int R, int D, typename IO>
-__device__ __forceinline__ void load_tile(float* dst, const IO* src, long long ld, int n) {
+template <int R, int D>
+__device__ __forceinline__ void load_tile(float* dst, const float* src, long long ld, int n) {
     for (int i = threadIdx.x; i < R * (D / 4); i += kThreads) {
         const int r = i / (D / 4), c = (i % (D / 4)) * 4;
         const float4 x = r < n ? load4(src + r * ld + c) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -89,8 +88,8 @@ template <int D> __device__ __forceinline__ void clear(float4 (&acc)[4][D / 64])
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) acc[i][h] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
-template <int D, typename IO>
-__device__ __forceinline__ void store_rows(IO* dst, long long ld, int n, const float4 (&acc)[4][D / 64], const float (&f)[4],
+template <int D>
+__device__ __forceinline__ void store_rows(float* dst, long long ld, int n, const float4 (&acc)[4][D / 64], const float (&f)[4],
                                            int ty, int tx) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -122,7 +121,7 @@ __device__ __forceinline__ Place place_of(const PromptParams& p, long long item,
     return x;
 }
 
-template <int D, typename IO> __global__ void __launch_bounds__(kThreads, 2) prompt_fwd_kernel(const PromptParams p) {
+template <int D> __global__ void __launch_bounds__(kThreads, 2) prompt_fwd_kernel(const PromptParams p) {
     extern __shared__ __align__(16) float sm[];
     float *Q = sm, *KV = Q + kRows * kPitch<D>, *P = KV + kRows * kPitch<D>;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, h = blockIdx.y, hk = h / p.G;
@@ -131,7 +130,7 @@ template <int D, typename IO> __global__ void __launch_bounds__(kThreads, 2) pro
         const Place at = place_of(p, item, false);
         if (!at.any) return;
         const int i0 = at.tile * kRows, ni = min(kRows, at.len - i0);
-        load_tile<kRows, D>(Q, static_cast<const IO*>(p.q) + (at.row0 + i0) * p.ld_q + (long long)h * D, p.ld_q, ni);
+        load_tile<kRows, D>(Q, static_cast<const float*>(p.q) + (at.row0 + i0) * p.ld_q + (long long)h * D, p.ld_q, ni);
         float4 acc[4][D / 64];
         clear<D>(acc);
         float m[4], l[4];
@@ -141,7 +140,7 @@ template <int D, typename IO> __global__ void __launch_bounds__(kThreads, 2) pro
         for (int t = first; t * kRows < i0 + ni; ++t) {
             const int j0 = t * kRows, nj = min(kRows, at.len - j0);
             __syncthreads();
-            load_tile<kRows, D>(KV, static_cast<const IO*>(p.k) + (at.row0 + j0) * p.ld_k + (long long)hk * D, p.ld_k, nj);
+            load_tile<kRows, D>(KV, static_cast<const float*>(p.k) + (at.row0 + j0) * p.ld_k + (long long)hk * D, p.ld_k, nj);
             __syncthreads();
             float s[4][4];
             dot_rows<4, D>(s, Q, KV, ty, tx);
@@ -172,7 +171,7 @@ template <int D, typename IO> __global__ void __launch_bounds__(kThreads, 2) pro
                 }
             }
             __syncthreads();
-            load_tile<kRows, D>(KV, static_cast<const IO*>(p.v) + (at.row0 + j0) * p.ld_v + (long long)hk * D, p.ld_v, nj);
+            load_tile<kRows, D>(KV, static_cast<const float*>(p.v) + (at.row0 + j0) * p.ld_v + (long long)hk * D, p.ld_v, nj);
             __syncthreads();
             add_rows<kRows, D>(acc, P, KV, ty, tx);
         }
@@ -180,7 +179,7 @@ template <int D, typename IO> __global__ void __launch_bounds__(kThreads, 2) pro
 #pragma unroll
         for (int i = 0; i < 4; ++i) f[i] = 1.f / l[i];
         const long long out = ((long long)(at.row0 + i0) * p.Hq + h);
-        store_rows<D>(static_cast<IO*>(p.o) + out * D, (long long)p.Hq * D, ni, acc, f, ty, tx);
+        store_rows<D>(static_cast<float*>(p.o) + out * D, (long long)p.Hq * D, ni, acc, f, ty, tx);
         if (p.lse && tx == 0)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -209,7 +208,7 @@ template <int D, typename IO> __global__ void __launch_bounds__(kThreads) prompt
 
 constexpr int kCols = 32;  // rows of a streamed tile of the backward kernels
 
-template <int D, typename IO> __global__ void __launch_bounds__(kThreads, 2) prompt_dq_kernel(const PromptParams p) {
+template <int D> __global__ void __launch_bounds__(kThreads, 2) prompt_dq_kernel(const PromptParams p) {
     extern __shared__ __align__(16) float sm[];
     float *Q = sm, *G = Q + kRows * kPitch<D>, *K = G + kRows * kPitch<D>, *V = K + kCols * kPitch<D>, *W = V + kCols * kPitch<D>;
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, h = blockIdx.y, hk = h / p.G;
@@ -219,8 +218,8 @@ template <int D, typename IO> __global__ void __launch_bounds__(kThreads, 2) pro
         if (!at.any) return;
         const int i0 = at.tile * kRows, ni = min(kRows, at.len - i0);
         const long long out = ((long long)(at.row0 + i0) * p.Hq + h);
-        load_tile<kRows, D>(Q, static_cast<const IO*>(p.q) + (at.row0 + i0) * p.ld_q + (long long)h * D, p.ld_q, ni);
-        load_tile<kRows, D>(G, static_cast<const IO*>(p.dO) + out * D, (long long)p.Hq * D, ni);
+        load_tile<kRows, D>(Q, static_cast<const float*>(p.q) + (at.row0 + i0) * p.ld_q + (long long)h * D, p.ld_q, ni);
+        load_tile<kRows, D>(G, static_cast<const float*>(p.dO) + out * D, (long long)p.Hq * D, ni);
         float lse[4], delta[4], f[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -235,8 +234,8 @@ template <int D, typename IO> __global__ void __launch_bounds__(kThreads, 2) pro
         for (int t = first; t * kCols < i0 + ni; ++t) {
             const int j0 = t * kCols, nj = min(kCols, at.len - j0);
             __syncthreads();
-            load_tile<kCols, D>(K, static_cast<const IO*>(p.k) + (at.row0 + j0) * p.ld_k + (long long)hk * D, p.ld_k, nj);
-            load_tile<kCols, D>(V, static_cast<const IO*>(p.v) + (at.row0 + j0) * p.ld_v + (long long)hk * D, p.ld_v, nj);
+            load_tile<kCols, D>(K, static_cast<const float*>(p.k) + (at.row0 + j0) * p.ld_k + (long long)hk * D, p.ld_k, nj);
+            load_tile<kCols, D>(V, static_cast<const float*>(p.v) + (at.row0 + j0) * p.ld_v + (long long)hk * D, p.ld_v, nj);
             __syncthreads();
             float s[4][2], dp[4][2];
             dot_rows<2, D>(s, Q, K, ty, tx);
@@ -251,33 +250,37 @@ template <int D, typename IO> __global__ void __launch_bounds__(kThreads, 2) pro
             __syncthreads();
             add_rows<kCols, D>(acc, W, K, ty, tx);
         }
-        store_rows<D>(static_cast<IO*>(p.dq) + (at.row0 + i0) * p.ld_dq + (long long)h * D, p.ld_dq, ni, acc, f, ty, tx);
+        store_rows<D>(static_cast<float*>(p.dq) + (at.row0 + i0) * p.ld_dq + (long long)h * D, p.ld_dq, ni, acc, f, ty, tx);
         __syncthreads();
     }
 }
 
-template <int D, typename IO> __global__ void __launch_bounds__(kThreads, 2) prompt_dkv_kernel(const PromptParams p) {
+template <int D> __global__ void __launch_bounds__(kThreads, 2) prompt_dkv_kernel(const PromptParams p) {
     extern __shared__ __align__(16) float sm[];
     float *K = sm, *V = K + kRows * kPitch<D>, *Q = V + kRows * kPitch<D>, *G = Q + kCols * kPitch<D>, *W = G + kCols * kPitch<D>;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, hk = blockIdx.y;
+    // a block for each key head, or for each query head where that would be too few: then dk and dv of the query heads
+    // go to the workspace, to be summed after
+    const bool split = p.heads != nullptr;
+    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, hk = split ? blockIdx.y / p.G : blockIdx.y;
+    const int h0 = split ? blockIdx.y : hk * p.G, h1 = split ? h0 + 1 : h0 + p.G;
     const float c2 = p.scale * kLog2e;
     for (long long item = blockIdx.x;; item += gridDim.x) {
         const Place at = place_of(p, item, true);
         if (!at.any) return;
         const int j0 = at.tile * kRows, nj = min(kRows, at.len - j0);
-        load_tile<kRows, D>(K, static_cast<const IO*>(p.k) + (at.row0 + j0) * p.ld_k + (long long)hk * D, p.ld_k, nj);
-        load_tile<kRows, D>(V, static_cast<const IO*>(p.v) + (at.row0 + j0) * p.ld_v + (long long)hk * D, p.ld_v, nj);
+        load_tile<kRows, D>(K, static_cast<const float*>(p.k) + (at.row0 + j0) * p.ld_k + (long long)hk * D, p.ld_k, nj);
+        load_tile<kRows, D>(V, static_cast<const float*>(p.v) + (at.row0 + j0) * p.ld_v + (long long)hk * D, p.ld_v, nj);
         float4 dk[4][D / 64], dv[4][D / 64];
         clear<D>(dk);
         clear<D>(dv);
         const int end = p.window ? (int)min((long long)at.len, (long long)j0 + nj - 1 + p.window) : at.len;
-        for (int h = hk * p.G; h < (hk + 1) * p.G; ++h)
+        for (int h = h0; h < h1; ++h)
             for (int i0 = j0; i0 < end; i0 += kCols) {
                 const int ni = min(kCols, at.len - i0);
                 const long long row = ((long long)(at.row0 + i0) * p.Hq + h);
                 __syncthreads();
-                load_tile<kCols, D>(Q, static_cast<const IO*>(p.q) + (at.row0 + i0) * p.ld_q + (long long)h * D, p.ld_q, ni);
-                load_tile<kCols, D>(G, static_cast<const IO*>(p.dO) + row * D, (long long)p.Hq * D, ni);
+                load_tile<kCols, D>(Q, static_cast<const float*>(p.q) + (at.row0 + i0) * p.ld_q + (long long)h * D, p.ld_q, ni);
+                load_tile<kCols, D>(G, static_cast<const float*>(p.dO) + row * D, (long long)p.Hq * D, ni);
                 float lse[2], delta[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -310,8 +313,40 @@ template <int D, typename IO> __global__ void __launch_bounds__(kThreads, 2) pro
                 add_rows<kCols, D>(dk, W, Q, ty, tx);
             }
         const float one[4] = {1.f, 1.f, 1.f, 1.f}, f[4] = {p.scale, p.scale, p.scale, p.scale};
-        store_rows<D>(static_cast<IO*>(p.dk) + (at.row0 + j0) * p.ld_dk + (long long)hk * D, p.ld_dk, nj, dk, f, ty, tx);
-        store_rows<D>(static_cast<IO*>(p.dv) + (at.row0 + j0) * p.ld_dv + (long long)hk * D, p.ld_dv, nj, dv, one, ty, tx);
+        if (split) {
+            float* to = p.heads + ((at.row0 + j0) * (long long)p.Hq + h0) * D;
+            store_rows<D>(to, (long long)p.Hq * D, nj, dk, f, ty, tx);
+            store_rows<D>(to + p.rows * p.Hq * D, (long long)p.Hq * D, nj, dv, one, ty, tx);
+            __syncthreads();
+            continue;
+        }
+        store_rows<D>(static_cast<float*>(p.dk) + (at.row0 + j0) * p.ld_dk + (long long)hk * D, p.ld_dk, nj, dk, f, ty, tx);
+        store_rows<D>(static_cast<float*>(p.dv) + (at.row0 + j0) * p.ld_dv + (long long)hk * D, p.ld_dv, nj, dv, one, ty, tx);
+        __syncthreads();
+    }
+}
+
+// dk and dv of a key head: the sums over its query heads, in order, for the rows of the sequences.
+template <int D> __global__ void __launch_bounds__(kThreads) prompt_heads_kernel(const PromptParams p) {
+    for (long long item = blockIdx.x;; item += gridDim.x) {
+        const Place at = place_of(p, item, false);
+        if (!at.any) return;
+        const int j0 = at.tile * kRows, nj = min(kRows, at.len - j0), hk = blockIdx.y;
+        for (int i = threadIdx.x; i < nj * (D / 4); i += kThreads) {
+            const long long row = at.row0 + j0 + i / (D / 4);
+            const int c = i % (D / 4) * 4;
+#pragma unroll
+            for (int which = 0; which < 2; ++which) {
+                const float* from = p.heads + which * p.rows * p.Hq * D + (row * p.Hq + hk * p.G) * D + c;
+                float4 sum = load4(from);
+                for (int h = 1; h < p.G; ++h) {
+                    const float4 x = load4(from + h * D);
+                    sum = make_float4(sum.x + x.x, sum.y + x.y, sum.z + x.z, sum.w + x.w);
+                }
+                store4(which ? static_cast<float*>(p.dv) + row * p.ld_dv + (long long)hk * D + c
+                             : static_cast<float*>(p.dk) + row * p.ld_dk + (long long)hk * D + c, sum);
+            }
+        }
         __syncthreads();
     }
 }
@@ -332,9 +367,9 @@ unsigned tiles(const PromptParams& p) {
     return (unsigned)(n < (1 << 30) ? n : 1 << 30);
 }
 
-template <int D, typename IO> cudaError_t fwd(const PromptParams& p, cudaStream_t st) {
+template <int D> cudaError_t fwd(const PromptParams& p, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
-    return run("prompt_fwd", prompt_fwd_kernel<D, IO>, dim3(tiles(p), p.Hq), fwd_smem<D>(), ready, p, st);
+    return run("prompt_fwd", prompt_fwd_kernel<D>, dim3(tiles(p), p.Hq), fwd_smem<D>(), ready, p, st);
 }
 template <int D, typename IO> cudaError_t delta(const PromptParams& p, cudaStream_t st) {
     TraceScope ts("prompt_delta", st);
@@ -342,28 +377,30 @@ template <int D, typename IO> cudaError_t delta(const PromptParams& p, cudaStrea
     prompt_delta_kernel<D, IO><<<(unsigned)(n < 16384 ? n : 16384), kThreads, 0, st>>>(p);
     return cudaGetLastError();
 }
-template <int D, typename IO> cudaError_t bwd(const PromptParams& p, cudaStream_t st) {
+template <int D> cudaError_t bwd(const PromptParams& p, cudaStream_t st) {
     static std::atomic<unsigned long long> ready[2] = {};
-    if (cudaError_t e = delta<D, IO>(p, st); e != cudaSuccess) return e;
-    if (cudaError_t e = run("prompt_dq", prompt_dq_kernel<D, IO>, dim3(tiles(p), p.Hq), bwd_smem<D>(), ready[0], p, st);
-        e != cudaSuccess)
+    if (cudaError_t e = delta<D, float>(p, st); e != cudaSuccess) return e;
+    if (cudaError_t e = run("prompt_dq", prompt_dq_kernel<D>, dim3(tiles(p), p.Hq), bwd_smem<D>(), ready[0], p, st); e != cudaSuccess)
         return e;
-    return run("prompt_dkv", prompt_dkv_kernel<D, IO>, dim3(tiles(p), p.H), bwd_smem<D>(), ready[1], p, st);
+    if (cudaError_t e = run("prompt_dkv", prompt_dkv_kernel<D>, dim3(tiles(p), p.heads ? p.Hq : p.H), bwd_smem<D>(), ready[1], p, st);
+        e != cudaSuccess || !p.heads)
+        return e;
+    TraceScope ts("prompt_heads", st);
+    prompt_heads_kernel<D><<<dim3(tiles(p), p.H), kThreads, 0, st>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t prompt_attn_fwd_simt(const PromptParams& p, int io, cudaStream_t st) {
-    if (io == DR_F32) return p.d == 128 ? fwd<128, float>(p, st) : fwd<64, float>(p, st);
-    return p.d == 128 ? fwd<128, __nv_bfloat16>(p, st) : fwd<64, __nv_bfloat16>(p, st);
+// Two blocks share an SM, 304 run at once: with fewer than twice as many, shared key heads are taken apart.
+size_t prompt_attn_heads_bytes(long long rows, int N, int Hq, int H, int d) {
+    const long long blocks = (rows / kRows + N) * H;
+    return Hq > H && blocks < 608 ? (size_t)(2 * rows) * Hq * d * sizeof(float) : 0;
 }
-cudaError_t prompt_attn_delta(const PromptParams& p, int io, cudaStream_t st) {
-    if (io == DR_F32) return p.d == 128 ? delta<128, float>(p, st) : delta<64, float>(p, st);
+cudaError_t prompt_attn_fwd_simt(const PromptParams& p, cudaStream_t st) { return p.d == 128 ? fwd<128>(p, st) : fwd<64>(p, st); }
+cudaError_t prompt_attn_delta_bf16(const PromptParams& p, cudaStream_t st) {
     return p.d == 128 ? delta<128, __nv_bfloat16>(p, st) : delta<64, __nv_bfloat16>(p, st);
 }
-cudaError_t prompt_attn_bwd_simt(const PromptParams& p, int io, cudaStream_t st) {
-    if (io == DR_F32) return p.d == 128 ? bwd<128, float>(p, st) : bwd<64, float>(p, st);
-    return p.d == 128 ? bwd<128, __nv_bfloat16>(p, st) : bwd<64, __nv_bfloat16>(p, st);
-}
+cudaError_t prompt_attn_bwd_simt(const PromptParams& p, cudaStream_t st) { return p.d == 128 ? bwd<128>(p, st) : bwd<64>(p, st); }
 
 }  // namespace dr

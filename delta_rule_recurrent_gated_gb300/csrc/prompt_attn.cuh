@@ -18,13 +18,15 @@ struct PromptParams {
     void *dq, *dk, *dv;
     int32_t* status;
     float* delta;            // workspace: sum of dO o for each row and query head
+    float* heads;            // workspace: dk, then dv, of each query head [rows, Hq, d]; null: not taken apart
 };
 
-// CUDA cores, bf16 or fp32 (prompt_attn.cu).
-cudaError_t prompt_attn_fwd_simt(const PromptParams& p, int io, cudaStream_t st);
-cudaError_t prompt_attn_bwd_simt(const PromptParams& p, int io, cudaStream_t st);
-// p.delta, the first step of both.
-cudaError_t prompt_attn_delta(const PromptParams& p, int io, cudaStream_t st);
+// CUDA cores, fp32 (prompt_attn.cu).
+cudaError_t prompt_attn_fwd_simt(const PromptParams& p, cudaStream_t st);
+cudaError_t prompt_attn_bwd_simt(const PromptParams& p, cudaStream_t st);
+size_t prompt_attn_heads_bytes(long long rows, int N, int Hq, int H, int d);  // p.heads (0: null)
+// p.delta for bf16, the first step of the gradient.
+cudaError_t prompt_attn_delta_bf16(const PromptParams& p, cudaStream_t st);
 // Tensor cores, bf16 (prompt_attn_tc.cu, prompt_attn_tc_bwd.cu).
 cudaError_t prompt_attn_fwd_tc(const PromptParams& p, cudaStream_t st);
 cudaError_t prompt_attn_bwd_tc(const PromptParams& p, cudaStream_t st);

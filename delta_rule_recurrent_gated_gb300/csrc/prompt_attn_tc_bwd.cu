@@ -647,7 +647,7 @@ template <int D> cudaError_t launch(const PromptParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t prompt_attn_bwd_tc(const PromptParams& p, cudaStream_t st) {
-    if (cudaError_t e = prompt_attn_delta(p, DR_BF16, st); e != cudaSuccess) return e;
+    if (cudaError_t e = prompt_attn_delta_bf16(p, st); e != cudaSuccess) return e;
     return p.d == 128 ? launch<128>(p, st) : launch<64>(p, st);
 }
 
