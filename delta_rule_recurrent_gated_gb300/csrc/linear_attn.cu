@@ -339,7 +339,7 @@ int scan_span(int io, long long rows, int N, int T, bool packed, int H, int dk, 
     if (rows == 0 || N == 0) return 0;
     const bool tc = io == DR_BF16;
     const int room = tc ? 152 : 304, least = tc ? 4 : 1;
-    const long long units = (long long)N * H * scans * (tc ? 1 : std::max(std::min(dk, dv) / 32, 1));
+    const long long units = (long long)N * H * (tc ? scans : std::max(std::min(dk, dv) / 32, 1));  // on the CUDA cores one by one
     const long long chunks = packed ? rows / kScanChunk + N : (long long)N * ((T + kScanChunk - 1) / kScanChunk);  // of all sequences
     if (chunks < (tc ? 12 : 2)) return 0;
     long long span;
@@ -348,8 +348,9 @@ int scan_span(int io, long long rows, int N, int T, bool packed, int H, int dk, 
         if (segments < 2 || chunks / N < (tc ? 12 : 2)) return 0;
         span = (chunks / N + segments - 1) / segments;
     } else {
-        // lengths are known on the device only: what is far longer than a block's share of all chunks
-        span = (5 * chunks * (units / N) / 2 + room - 1) / room;
+        // Lengths are known on the device only.  On the tensor cores, where a split costs more, only what is far longer than
+        // a block's share of all chunks.
+        span = ((tc ? 5 : 2) * chunks * (units / N) / 2 + room - 1) / room;
     }
     return (int)std::min<long long>(std::max<long long>(span, least), 1 << 22);
 }
