@@ -52,32 +52,37 @@ template <int DK, int DV, bool ONLY>
 __device__ __forceinline__ void copy_tiles(const ScanParams& p, const Work& w, int head, const CUtensorMap* mq,
                                            const CUtensorMap* mk, const CUtensorMap* mv, uint8_t* smem, Control& ct) {
     const int lane = threadIdx.x & 31;
-    uint32_t landings = 0, slot = 0, parity = 1;
-    for (int n = 0; n < w.chunks; ++n) {
-        const int first = w.at(p, n), row = w.row0 + first, rows = w.tokens(first);
+    uint32_t landings = 0;
+    Ring<kSlots> ring;
+    [&] {
+        for (int n = 0; n < w.chunks; ++n) {
+            const int first = w.at(p, n), row = w.row0 + first, rows = w.tokens(first);
 #pragma unroll
-        for (int i = 0; i < kTiles<ONLY>; ++i) {
-            constexpr int V = kTiles<ONLY> - 1;
-            if (!wait(ct.dead, &ct.empty[slot], parity)) return;
-            uint8_t* tile = smem + slot * Smem<DK, DV>::slot;
-            // values behind the sequence are summed with weights of zero: they have to be numbers
-            const bool cut = i == V && rows < kC;
-            uint64_t* bar = cut ? &ct.landed : &ct.full[slot];
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, kC * (i == V ? DV : DK) * 2);
-                if (i == V) load_rows<kC, DV>(tile, mv, bar, head, row);
-                else load_rows<kC, DK>(tile, i == 0 ? mk : mq, bar, head, row);
-            }
-            __syncwarp();
-            if (cut) {
-                if (!wait(ct.dead, &ct.landed, landings++ & 1)) return;
-                clear_rows<kC, DV>(tile, rows);
-                if (lane == 0) mbar_arrive(&ct.full[slot]);
+            for (int i = 0; i < kTiles<ONLY>; ++i) {
+                constexpr int V = kTiles<ONLY> - 1;
+                if (!wait(ct.dead, &ct.empty[ring.at], ring.phase ^ 1)) return;
+                uint8_t* tile = smem + ring.at * Smem<DK, DV>::slot;
+                // values behind the sequence are summed with weights of zero: they have to be numbers
+                const bool cut = i == V && rows < kC;
+                uint64_t* bar = cut ? &ct.landed : &ct.full[ring.at];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, kC * (i == V ? DV : DK) * 2);
+                    if (i == V) load_rows<kC, DV>(tile, mv, bar, head, row);
+                    else load_rows<kC, DK>(tile, i == 0 ? mk : mq, bar, head, row);
+                }
                 __syncwarp();
+                if (cut) {
+                    if (!wait(ct.dead, &ct.landed, landings++ & 1)) return;
+                    clear_rows<kC, DV>(tile, rows);
+                    if (lane == 0) mbar_arrive(&ct.full[ring.at]);
+                    __syncwarp();
+                }
+                ring.step();
             }
-            if (++slot == kSlots) { slot = 0; parity ^= 1; }
         }
-    }
+    }();
+    settle(&ct.landed, landings);
+    settle(ring, ct.full);
 }
 
 template <int DK, int DV, bool ONLY> struct Issuer {

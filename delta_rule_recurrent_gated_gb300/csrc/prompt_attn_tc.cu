@@ -74,51 +74,60 @@ template <int D>
 __device__ __forceinline__ void copy_tiles(const PromptParams& p, const CUtensorMap* mq, const CUtensorMap* mk,
                                            const CUtensorMap* mv, uint8_t* smem, Control& ct) {
     const int lane = threadIdx.x & 31;
-    uint32_t n = 0, landings = 0;
-    for (long long k = 0;; ++k) {
-        const Item x = make_item(p, k);
-        // queries and the item's data: after the last item's products with its queries, and after the row threads
-        // have begun with it (so they are never two items behind)
-        if (!wait(ct.dead, &ct.qempty, (k & 1) ^ 1)) return;
-        if (lane == 0) {
-            ct.item[k % kInfos] = x;
-            if (x.any) {
-                mbar_arrive_expect_tx(&ct.qfull, 2 * Smem<D>::tile);
-                for (int h = 0; h < 2; ++h)
-                    load_rows<kHalf, D>(smem + Smem<D>::q + h * Smem<D>::tile, mq, &ct.qfull, x.head, x.row0 + x.i0 + h * kHalf);
-            } else {
-                mbar_arrive(&ct.qfull);
-            }
-        }
-        __syncwarp();
-        if (!x.any) return;
-        const int hk = x.head / p.G;
-        for (int t = first_stage(x); t < last_stage(x); ++t, ++n) {
-            const uint32_t buf = n % kBuffers, parity = (n / kBuffers) & 1;
-            const int row = x.row0 + t * kStage;
-            if (!wait(ct.dead, &ct.kempty[buf], parity ^ 1)) return;
-            if (lane == 0) {  // keys behind the sequence make scores that are hidden
-                mbar_arrive_expect_tx(&ct.kfull[buf], Smem<D>::tile);
-                load_rows<kStage, D>(smem + Smem<D>::k + buf * Smem<D>::tile, mk, &ct.kfull[buf], hk, row);
-            }
-            __syncwarp();
-            if (!wait(ct.dead, &ct.vempty[buf], parity ^ 1)) return;
-            uint8_t* v = smem + Smem<D>::v + buf * Smem<D>::tile;
-            const int rows = x.len - t * kStage;
-            uint64_t* bar = rows < kStage ? &ct.landed : &ct.vfull[buf];
+    uint32_t landings = 0;
+    Ring<kBuffers> rk, rv;
+    long long items = 0;
+    [&] {
+        for (long long k = 0;; ++k) {
+            const Item x = make_item(p, k);
+            // queries and the item's data: after the last item's products with its queries, and after the row threads
+            // have begun with it (so they are never two items behind)
+            if (!wait(ct.dead, &ct.qempty, (k & 1) ^ 1)) return;
             if (lane == 0) {
-                mbar_arrive_expect_tx(bar, Smem<D>::tile);
-                load_rows<kStage, D>(v, mv, bar, hk, row);
+                ct.item[k % kInfos] = x;
+                if (x.any) {
+                    mbar_arrive_expect_tx(&ct.qfull, 2 * Smem<D>::tile);
+                    for (int h = 0; h < 2; ++h)
+                        load_rows<kHalf, D>(smem + Smem<D>::q + h * Smem<D>::tile, mq, &ct.qfull, x.head, x.row0 + x.i0 + h * kHalf);
+                } else {
+                    mbar_arrive(&ct.qfull);
+                }
             }
             __syncwarp();
-            if (rows < kStage) {  // values behind the sequence may be anything, and zero times that is not zero
-                if (!wait(ct.dead, &ct.landed, landings++ & 1)) return;
-                clear_rows<kStage, D>(v, rows);
-                if (lane == 0) mbar_arrive(&ct.vfull[buf]);
+            ++items;
+            if (!x.any) return;
+            const int hk = x.head / p.G;
+            for (int t = first_stage(x); t < last_stage(x); ++t) {
+                const int row = x.row0 + t * kStage, rows = x.len - t * kStage;
+                if (!wait(ct.dead, &ct.kempty[rk.at], rk.phase ^ 1)) return;
+                if (lane == 0) {  // keys behind the sequence make scores that are hidden
+                    mbar_arrive_expect_tx(&ct.kfull[rk.at], Smem<D>::tile);
+                    load_rows<kStage, D>(smem + Smem<D>::k + rk.at * Smem<D>::tile, mk, &ct.kfull[rk.at], hk, row);
+                }
                 __syncwarp();
+                rk.step();
+                if (!wait(ct.dead, &ct.vempty[rv.at], rv.phase ^ 1)) return;
+                uint8_t* v = smem + Smem<D>::v + rv.at * Smem<D>::tile;
+                uint64_t* bar = rows < kStage ? &ct.landed : &ct.vfull[rv.at];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, Smem<D>::tile);
+                    load_rows<kStage, D>(v, mv, bar, hk, row);
+                }
+                __syncwarp();
+                if (rows < kStage) {  // values behind the sequence may be anything, and zero times that is not zero
+                    if (!wait(ct.dead, &ct.landed, landings++ & 1)) return;
+                    clear_rows<kStage, D>(v, rows);
+                    if (lane == 0) mbar_arrive(&ct.vfull[rv.at]);
+                    __syncwarp();
+                }
+                rv.step();
             }
         }
-    }
+    }();
+    settle(&ct.qfull, items);
+    settle(&ct.landed, landings);
+    settle(rk, ct.kfull);
+    settle(rv, ct.vfull);
 }
 
 // ------------------------------------------------------------------ warp 8: products

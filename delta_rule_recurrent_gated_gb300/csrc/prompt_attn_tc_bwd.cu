@@ -85,13 +85,6 @@ __device__ __forceinline__ bool load_tile(volatile int& dead, uint8_t* tile, con
     }
     return true;
 }
-// Counts through the phases of a ring of buffers.
-template <int N> struct Ring {
-    uint32_t at = 0, phase = 0;
-    __device__ __forceinline__ void step() {
-        if (++at == N) { at = 0; phase ^= 1; }
-    }
-};
 // 64 fp32 values as bf16 pairs to 32 columns.
 __device__ __forceinline__ void store_operand(uint32_t to, const float (&x)[64]) {
     uint32_t z[32];
@@ -141,39 +134,47 @@ __device__ __forceinline__ void copy_tiles(const PromptParams& p, const CUtensor
     uint32_t landings = 0;
     Ring<kFirst> rk;
     Ring<kSecond> rv;
-    for (long long k = 0;; ++k) {
-        const Item x = make_item(p, k);
-        // queries and the item's data: after the last item's products with its queries, and after the row threads
-        // have begun with it (so they are never two items behind)
-        if (!wait(ct.dead, &ct.qempty, (k & 1) ^ 1)) return;
-        if (lane == 0) {
-            ct.item[k % kInfos] = x;
-            if (x.any) {
-                mbar_arrive_expect_tx(&ct.qfull, 2 * kTileBytes<D>);
-                load_rows<kRows, D>(smem + Smem<D>::q, mq, &ct.qfull, x.head, x.row0 + x.i0);
-                load_rows<kRows, D>(smem + Smem<D>::g, mg, &ct.qfull, x.head, x.row0 + x.i0);
-            } else {
-                mbar_arrive(&ct.qfull);
+    long long items = 0;
+    [&] {
+        for (long long k = 0;; ++k) {
+            const Item x = make_item(p, k);
+            // queries and the item's data: after the last item's products with its queries, and after the row threads
+            // have begun with it (so they are never two items behind)
+            if (!wait(ct.dead, &ct.qempty, (k & 1) ^ 1)) return;
+            if (lane == 0) {
+                ct.item[k % kInfos] = x;
+                if (x.any) {
+                    mbar_arrive_expect_tx(&ct.qfull, 2 * kTileBytes<D>);
+                    load_rows<kRows, D>(smem + Smem<D>::q, mq, &ct.qfull, x.head, x.row0 + x.i0);
+                    load_rows<kRows, D>(smem + Smem<D>::g, mg, &ct.qfull, x.head, x.row0 + x.i0);
+                } else {
+                    mbar_arrive(&ct.qfull);
+                }
+            }
+            __syncwarp();
+            ++items;
+            if (!x.any) return;
+            const int hk = x.head / p.G;
+            for (int t = x.lo; t < x.hi; ++t) {
+                const int row = x.row0 + t * kRows, rows = x.len - t * kRows;
+                // keys behind the sequence are summed with a weight of zero: they have to be numbers
+                if (!wait(ct.dead, &ct.kempty[rk.at], rk.phase ^ 1) ||
+                    !load_tile<D>(ct.dead, smem + Smem<D>::k + rk.at * kTileBytes<D>, mk, &ct.kfull[rk.at], &ct.landed, landings, hk,
+                                  row, rows, true))
+                    return;
+                rk.step();
+                if (!wait(ct.dead, &ct.vempty[rv.at], rv.phase ^ 1) ||
+                    !load_tile<D>(ct.dead, smem + Smem<D>::v + rv.at * kTileBytes<D>, mv, &ct.vfull[rv.at], &ct.landed, landings, hk,
+                                  row, rows, false))
+                    return;
+                rv.step();
             }
         }
-        __syncwarp();
-        if (!x.any) return;
-        const int hk = x.head / p.G;
-        for (int t = x.lo; t < x.hi; ++t) {
-            const int row = x.row0 + t * kRows, rows = x.len - t * kRows;
-            // keys behind the sequence are summed with a weight of zero: they have to be numbers
-            if (!wait(ct.dead, &ct.kempty[rk.at], rk.phase ^ 1) ||
-                !load_tile<D>(ct.dead, smem + Smem<D>::k + rk.at * kTileBytes<D>, mk, &ct.kfull[rk.at], &ct.landed, landings, hk,
-                              row, rows, true))
-                return;
-            rk.step();
-            if (!wait(ct.dead, &ct.vempty[rv.at], rv.phase ^ 1) ||
-                !load_tile<D>(ct.dead, smem + Smem<D>::v + rv.at * kTileBytes<D>, mv, &ct.vfull[rv.at], &ct.landed, landings, hk,
-                              row, rows, false))
-                return;
-            rv.step();
-        }
-    }
+    }();
+    settle(&ct.qfull, items);
+    settle(&ct.landed, landings);
+    settle(rk, ct.kfull);
+    settle(rv, ct.vfull);
 }
 
 template <int D> __device__ __forceinline__ void issue(uint8_t* smem, Control& ct) {
@@ -372,37 +373,45 @@ __device__ __forceinline__ void copy_tiles(const PromptParams& p, const CUtensor
     uint32_t landings = 0;
     Ring<kFirst> rq;
     Ring<kSecond> rg;
-    for (long long k = 0;; ++k) {
-        const Item x = make_item(p, k);
-        if (!wait(ct.dead, &ct.kvempty, (k & 1) ^ 1)) return;
-        if (lane == 0) {
-            ct.item[k % kInfos] = x;
-            if (x.any) {  // rows of no key get no result, so that they may be anything
-                mbar_arrive_expect_tx(&ct.kvfull, 2 * kTileBytes<D>);
-                load_rows<kRows, D>(smem + Smem<D>::k, mk, &ct.kvfull, x.head, x.row0 + x.j0);
-                load_rows<kRows, D>(smem + Smem<D>::v, mv, &ct.kvfull, x.head, x.row0 + x.j0);
-            } else {
-                mbar_arrive(&ct.kvfull);
+    long long items = 0;
+    [&] {
+        for (long long k = 0;; ++k) {
+            const Item x = make_item(p, k);
+            if (!wait(ct.dead, &ct.kvempty, (k & 1) ^ 1)) return;
+            if (lane == 0) {
+                ct.item[k % kInfos] = x;
+                if (x.any) {  // rows of no key get no result, so that they may be anything
+                    mbar_arrive_expect_tx(&ct.kvfull, 2 * kTileBytes<D>);
+                    load_rows<kRows, D>(smem + Smem<D>::k, mk, &ct.kvfull, x.head, x.row0 + x.j0);
+                    load_rows<kRows, D>(smem + Smem<D>::v, mv, &ct.kvfull, x.head, x.row0 + x.j0);
+                } else {
+                    mbar_arrive(&ct.kvfull);
+                }
             }
+            __syncwarp();
+            ++items;
+            if (!x.any) return;
+            for (int h = x.head * p.G; h < (x.head + 1) * p.G; ++h)
+                for (int t = x.lo; t < x.hi; ++t) {
+                    // queries behind the sequence are summed with weights of zero: they have to be numbers
+                    const int row = x.row0 + t * kRows, rows = x.len - t * kRows;
+                    if (!wait(ct.dead, &ct.qempty[rq.at], rq.phase ^ 1) ||
+                        !load_tile<D>(ct.dead, smem + Smem<D>::q + rq.at * kTileBytes<D>, mq, &ct.qfull[rq.at], &ct.landed, landings, h,
+                                      row, rows, true))
+                        return;
+                    rq.step();
+                    if (!wait(ct.dead, &ct.gempty[rg.at], rg.phase ^ 1) ||
+                        !load_tile<D>(ct.dead, smem + Smem<D>::g + rg.at * kTileBytes<D>, mg, &ct.gfull[rg.at], &ct.landed, landings, h,
+                                      row, rows, true))
+                        return;
+                    rg.step();
+                }
         }
-        __syncwarp();
-        if (!x.any) return;
-        for (int h = x.head * p.G; h < (x.head + 1) * p.G; ++h)
-            for (int t = x.lo; t < x.hi; ++t) {
-                // queries behind the sequence are summed with weights of zero: they have to be numbers
-                const int row = x.row0 + t * kRows, rows = x.len - t * kRows;
-                if (!wait(ct.dead, &ct.qempty[rq.at], rq.phase ^ 1) ||
-                    !load_tile<D>(ct.dead, smem + Smem<D>::q + rq.at * kTileBytes<D>, mq, &ct.qfull[rq.at], &ct.landed, landings, h,
-                                  row, rows, true))
-                    return;
-                rq.step();
-                if (!wait(ct.dead, &ct.gempty[rg.at], rg.phase ^ 1) ||
-                    !load_tile<D>(ct.dead, smem + Smem<D>::g + rg.at * kTileBytes<D>, mg, &ct.gfull[rg.at], &ct.landed, landings, h,
-                                  row, rows, true))
-                    return;
-                rg.step();
-            }
-    }
+    }();
+    settle(&ct.kvfull, items);
+    settle(&ct.landed, landings);
+    settle(rq, ct.qfull);
+    settle(rg, ct.gfull);
 }
 // The queries' lse and D, the next stage's already on their way.
 __device__ __forceinline__ void copy_stats(const PromptParams& p, Control& ct) {

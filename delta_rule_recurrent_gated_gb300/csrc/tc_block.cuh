@@ -137,6 +137,21 @@ template <int R, int D> __device__ __forceinline__ void clear_rows(uint8_t* tile
     __syncwarp();
 }
 
+// Counts through the phases of a ring of buffers.
+template <int N> struct Ring {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void step() {
+        if (++at == N) { at = 0; phase ^= 1; }
+    }
+};
+// Before a block ends no copy of it may be on its way, whatever became of its warps: waits, with a limit, for the last
+// phase of each buffer that was filled (what was never filled is not waited for).
+template <int N> __device__ __forceinline__ void settle(const Ring<N>& ring, uint64_t (&full)[N]) {
+    for (uint32_t b = 0; b < N; ++b) mbar_wait(&full[b], b < ring.at ? ring.phase : ring.phase ^ 1, kWaitLimitNs);
+}
+// The same for a barrier that `n` copies went through one after another.
+__device__ __forceinline__ void settle(uint64_t* full, long long n) { mbar_wait(full, (uint32_t)(n & 1) ^ 1, kWaitLimitNs); }
+
 // ------------------------------------------------------------------ host
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {

@@ -443,6 +443,7 @@ int dr_cache_attn(const dr_cache* cache, const dr_cache_seqs* seqs, const dr_att
  * fp32; softmax weights, decayed scores and the state that queries read are rounded to bf16 as
  * operands, what is carried from chunk to chunk (the states) is not.
  * Gradients of shared key heads are summed in a fixed order: the same inputs give the same bits.
+ * Outputs do not overlap inputs.
  * A token that is not finite leaves other sequences alone; in its own it may also reach the results
  * of tokens that do not see it (a weight of zero times it).
  * Errors as dr_fwd.  status: one device int32 the caller sets to zero, or NULL; a kernel whose bounded
