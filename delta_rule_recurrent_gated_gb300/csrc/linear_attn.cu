@@ -361,12 +361,10 @@ long long scan_slots(long long rows, int span) {
 
 cudaError_t linear_scans(const ScanParams* p, int n, int io, cudaStream_t st) {
     const bool tc = io == DR_BF16 && p->rows > 0;
-    // scans of the same sizes follow one another
     auto all = [&](bool only) {
-        for (int i = 0, j; i < n; i = j) {
-            for (j = i + 1; tc && j < n && p[j].dk == p[i].dk && p[j].dv == p[i].dv;) ++j;
-            if (cudaError_t e = tc ? linear_scans_tc(p + i, j - i, only, st) : scan_simt(p[i], only, st); e != cudaSuccess) return e;
-        }
+        if (tc) return linear_scans_tc(p, n, only, st);
+        for (int i = 0; i < n; ++i)
+            if (cudaError_t e = scan_simt(p[i], only, st); e != cudaSuccess) return e;
         return cudaSuccess;
     };
     if (p->rows > 0 && p->span) {

@@ -370,21 +370,16 @@ __device__ __forceinline__ void states(const ScanParams& p, const Work& w, int h
         for (int c = 0; c < DV; c += 4) store4(to + r * DV + c, make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]));
 }
 
-// n scans of the same sequences side by side: what they share is read at about the same time.
+// n scans of the same sequences side by side: what they share is read at about the same time, and a block that is
+// through with one takes what comes next of all.
 struct ScanSet {
     CUtensorMap m[kMostScans][3];  // of q, k, v
     ScanParams p[kMostScans];
 };
-// ONLY: the segments' own states, from nothing.
 template <int DK, int DV, bool ONLY>
-__global__ void __launch_bounds__(kThreads, 1) linear_scan_tc_kernel(const __grid_constant__ ScanSet set, int n) {
-    extern __shared__ __align__(1024) uint8_t smem[];
+__device__ __forceinline__ void scan_block(const ScanParams& p, const CUtensorMap* m, const Work& w, int head, uint8_t* smem) {
     Control& ct = *reinterpret_cast<Control*>(smem + Smem<DK, DV>::control);
-    const ScanParams& p = set.p[blockIdx.x % n];
-    const CUtensorMap* m = set.m[blockIdx.x % n];
-    const int warp = threadIdx.x >> 5, item = blockIdx.x / n, head = item % p.H;
-    Work w;
-    if (!make_work(p, item / p.H, head, w) || (ONLY && (!w.before || w.last))) return;
+    const int warp = threadIdx.x >> 5;
     if (warp == 0) {
         tmem_alloc(&ct.tmem, 512);
         tmem_relinquish();
@@ -429,41 +424,51 @@ __global__ void __launch_bounds__(kThreads, 1) linear_scan_tc_kernel(const __gri
     if (ct.dead && threadIdx.x == 0 && p.status) *reinterpret_cast<volatile int32_t*>(p.status) = kErrTimeout;
     if (warp == 0) tmem_dealloc(ct.tmem, 512);
 }
+// Scans with DA channels of queries and DB of values, or the other way round.  ONLY: the segments' own states, from nothing.
+template <int DA, int DB, bool ONLY>
+__global__ void __launch_bounds__(kThreads, 1) linear_scan_tc_kernel(const __grid_constant__ ScanSet set, int n) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const ScanParams& p = set.p[blockIdx.x % n];
+    const CUtensorMap* m = set.m[blockIdx.x % n];
+    const int item = blockIdx.x / n, head = item % p.H;
+    Work w;
+    if (!make_work(p, item / p.H, head, w) || (ONLY && (!w.before || w.last))) return;
+    if (DA == DB || p.dk == DA) scan_block<DA, DB, ONLY>(p, m, w, head, smem);
+    else scan_block<DB, DA, ONLY>(p, m, w, head, smem);
+}
 
-template <int DK, int DV, bool ONLY> cudaError_t launch(const ScanSet& set, int n, cudaStream_t st) {
+template <int DA, int DB, bool ONLY> cudaError_t launch(const ScanSet& set, int n, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
+    constexpr int smem = Smem<DA, DB>::bytes > Smem<DB, DA>::bytes ? Smem<DA, DB>::bytes : Smem<DB, DA>::bytes;
     // the split of the registers must not ask for more than the block is launched with: it would wait for them
     static const bool fits = [] {
         cudaFuncAttributes a;
-        return cudaFuncGetAttributes(&a, linear_scan_tc_kernel<DK, DV, ONLY>) == cudaSuccess && a.numRegs == kRegs;
+        return cudaFuncGetAttributes(&a, linear_scan_tc_kernel<DA, DB, ONLY>) == cudaSuccess && a.numRegs == kRegs;
     }();
     if (!fits) return cudaErrorInvalidConfiguration;
-    if (cudaError_t e = set_smem_once(linear_scan_tc_kernel<DK, DV, ONLY>, Smem<DK, DV>::bytes, ready); e != cudaSuccess) return e;
+    if (cudaError_t e = set_smem_once(linear_scan_tc_kernel<DA, DB, ONLY>, smem, ready); e != cudaSuccess) return e;
     TraceScope ts(ONLY ? "linear_segments_tc" : "linear_scan_tc", st);
     const long long blocks = scan_items(set.p[0]) * set.p[0].H * n;
     if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
-    linear_scan_tc_kernel<DK, DV, ONLY><<<(unsigned)blocks, kThreads, Smem<DK, DV>::bytes, st>>>(set, n);
+    linear_scan_tc_kernel<DA, DB, ONLY><<<(unsigned)blocks, kThreads, smem, st>>>(set, n);
     return cudaGetLastError();
-}
-template <int DK, int DV> cudaError_t scans(const ScanParams* p, int n, bool only, cudaStream_t st) {
-    ScanSet set;
-    for (int i = 0; i < n; ++i) {
-        set.p[i] = p[i];
-        set.p[i].wide_out = wide_rows(p[i].out, p[i].ld_o);
-        if (!head_rows_map(&set.m[i][0], p[i].q, DK, p[i].H, p[i].rows, p[i].ld_q, kC) ||
-            !head_rows_map(&set.m[i][1], p[i].k, DK, p[i].H, p[i].rows, p[i].ld_k, kC) ||
-            !head_rows_map(&set.m[i][2], p[i].v, DV, p[i].H, p[i].rows, p[i].ld_v, kC))
-            return cudaErrorInvalidValue;
-    }
-    return only ? launch<DK, DV, true>(set, n, st) : launch<DK, DV, false>(set, n, st);
 }
 
 }  // namespace
 
 cudaError_t linear_scans_tc(const ScanParams* p, int n, bool only, cudaStream_t st) {
-    if (n == 0) return cudaSuccess;
-    if (p->dk == 128) return p->dv == 128 ? scans<128, 128>(p, n, only, st) : scans<128, 64>(p, n, only, st);
-    return p->dv == 128 ? scans<64, 128>(p, n, only, st) : scans<64, 64>(p, n, only, st);
+    ScanSet set;
+    for (int i = 0; i < n; ++i) {
+        set.p[i] = p[i];
+        set.p[i].wide_out = wide_rows(p[i].out, p[i].ld_o);
+        if (!head_rows_map(&set.m[i][0], p[i].q, p[i].dk, p[i].H, p[i].rows, p[i].ld_q, kC) ||
+            !head_rows_map(&set.m[i][1], p[i].k, p[i].dk, p[i].H, p[i].rows, p[i].ld_k, kC) ||
+            !head_rows_map(&set.m[i][2], p[i].v, p[i].dv, p[i].H, p[i].rows, p[i].ld_v, kC))
+            return cudaErrorInvalidValue;
+    }
+    if (p->dk != p->dv) return only ? launch<64, 128, true>(set, n, st) : launch<64, 128, false>(set, n, st);
+    if (p->dk == 128) return only ? launch<128, 128, true>(set, n, st) : launch<128, 128, false>(set, n, st);
+    return only ? launch<64, 64, true>(set, n, st) : launch<64, 64, false>(set, n, st);
 }
 
 }  // namespace dr
