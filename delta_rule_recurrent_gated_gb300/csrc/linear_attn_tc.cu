@@ -7,15 +7,16 @@
 // so no power of a is ever above one, however strong the decay.
 //
 // A block has a sequence, or a segment of one, and a head.  The state stays in fp32 registers, a row of it in each
-// thread of four warps; what a chunk adds comes from tensor memory, and a bf16 image of the state goes to shared memory
+// thread of eight warps, half each; what a chunk adds comes from tensor memory, and a bf16 image of the state goes to shared memory
 // for the next chunk's queries.  K' is a sum of two bf16 parts (2^-16 of it is lost), so that what the states add up over
 // a sequence is not bf16; P, and the state as an operand, are rounded once (2^-8 at most).
 // Tensor memory: A with P over it, Q X, P V, K'^T V: 4 x 128 columns.
-// Warps 0-3: P.  4-7: K' (its high part over K, once A is there).  8-11: output rows.  12-15: state.  16: products,
-// 17: copies, through a ring of five tiles in the order K, Q, V.
+// Warps 0-3: P.  4-7: K' (its high part over K, once A is there).  8-11: output rows.  12-19: state.  20: products,
+// 21: copies, through a ring of five tiles in the order Q, K, V.
 //
-// The products of a chunk are issued as P V (n), A (n + 1), K'V (n), Q X (n), each when what it needs is there: P and K'
-// of the next chunk are formed while the last two run.
+// The products of a chunk are issued as P V (n), Q X (n), A (n + 1), K'V (n), each when what it needs is there.  So the
+// tile of a chunk's queries is the first to be free, for the values of the next chunk, which are on their way while A
+// and K'V run (with Q X last the loop waited for them: 133 us for b8 t4096 h16 d128 instead of 119).
 #include "f32x2.cuh"
 #include "linear_work.cuh"
 #include "tc_block.cuh"
@@ -24,10 +25,12 @@
 namespace dr {
 namespace {
 
-constexpr int kC = kScanChunk, kThreads = 640, kSlots = 5;
-// Registers of a thread: as launched, then of the five groups of four warps.
-constexpr int kRegs = 96, kWeightRegs = 88, kKeyRegs = 72, kOutRegs = 96, kStateRegs = 176, kOtherRegs = 48;
-static_assert(kWeightRegs + kKeyRegs + kOutRegs + kStateRegs + kOtherRegs <= 5 * kRegs, "more than the block has");
+constexpr int kC = kScanChunk, kThreads = 768, kSlots = 5;
+// Registers of a thread: as launched, then of the six groups of four warps (two of them the state's).
+constexpr int kRegs = 80, kWeightRegs = 88, kKeyRegs = 72, kOutRegs = 96, kStateRegs = 88, kOtherRegs = 48;
+static_assert(kWeightRegs >= kRegs && kOutRegs >= kRegs && kStateRegs >= kRegs && kKeyRegs <= kRegs && kOtherRegs <= kRegs,
+              "each takes or gives, as its instruction says");
+static_assert(kWeightRegs + kKeyRegs + kOutRegs + 2 * kStateRegs + kOtherRegs <= 6 * kRegs, "more than the block has");
 constexpr uint32_t kA = 0, kQX = 128, kPV = 256, kKV = 384;  // columns of tensor memory
 
 struct Control {
@@ -45,8 +48,9 @@ template <int DK, int DV> struct Smem {
     static_assert(sizeof(Control) <= 1024, "control block");
 };
 
-// What goes through the ring for a chunk: K, Q, V, or K, V where only states are formed.
+// What goes through the ring for a chunk: Q, K, V, or K, V where only states are formed.
 template <bool ONLY> constexpr int kTiles = ONLY ? 2 : 3;
+template <bool ONLY> constexpr int kKeyTile = ONLY ? 0 : 1;
 
 template <int DK, int DV, bool ONLY>
 __device__ __forceinline__ void copy_tiles(const ScanParams& p, const Work& w, int head, const CUtensorMap* mq,
@@ -68,7 +72,7 @@ __device__ __forceinline__ void copy_tiles(const ScanParams& p, const Work& w, i
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar, kC * (i == V ? DV : DK) * 2);
                     if (i == V) load_rows<kC, DV>(tile, mv, bar, head, row);
-                    else load_rows<kC, DK>(tile, i == 0 ? mk : mq, bar, head, row);
+                    else load_rows<kC, DK>(tile, i == kKeyTile<ONLY> ? mk : mq, bar, head, row);
                 }
                 __syncwarp();
                 if (cut) {
@@ -87,7 +91,7 @@ __device__ __forceinline__ void copy_tiles(const ScanParams& p, const Work& w, i
 
 template <int DK, int DV, bool ONLY> struct Issuer {
     using S = Smem<DK, DV>;
-    static constexpr int N = kTiles<ONLY>;
+    static constexpr int N = kTiles<ONLY>, K = kKeyTile<ONLY>, Q = 0, V = N - 1;
     Control& ct;
     uint32_t tm;
     uint64_t row0, col0, low0, x0;  // descriptors: of slot 0, by rows and by columns; of the low parts; of the state
@@ -104,13 +108,13 @@ template <int DK, int DV, bool ONLY> struct Issuer {
         return wait(ct.dead, &ct.full[slot(n, i)], ((uint32_t)(N * n + i) / kSlots) & 1);
     }
     __device__ __forceinline__ bool scores(int n) {  // A
-        if (!arrived(n, 0) || !arrived(n, 1)) return false;
+        if (!arrived(n, Q) || !arrived(n, K)) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < DK; kk += 16)  // 16 channels: 32 bytes of a 128-byte row
-                mma_bf16(tm + kA, row0 + at(n, 1) + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8,
-                         row0 + at(n, 0) + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8, idesc_bf16(kC, kC), kk > 0);
+                mma_bf16(tm + kA, row0 + at(n, Q) + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8,
+                         row0 + at(n, K) + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8, idesc_bf16(kC, kC), kk > 0);
             mma_commit(&ct.afull);
             mma_commit(&ct.akeys);
         }
@@ -123,7 +127,7 @@ template <int DK, int DV, bool ONLY> struct Issuer {
         if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < kC; kk += 16)  // 16 tokens: 16 rows of 128 bytes
-                mma_ts(tm + kPV, tm + kA + kk / 2, col0 + at(n, N - 1) + kk * 8, idesc_bf16(kC, DV, false, true), kk > 0);
+                mma_ts(tm + kPV, tm + kA + kk / 2, col0 + at(n, V) + kk * 8, idesc_bf16(kC, DV, false, true), kk > 0);
         }
         __syncwarp();
         return true;
@@ -136,11 +140,11 @@ template <int DK, int DV, bool ONLY> struct Issuer {
             for (int part = 0; part < 2; ++part)
 #pragma unroll
                 for (int kk = 0; kk < kC; kk += 16)
-                    mma_bf16(tm + kKV, (part ? low0 : col0 + at(n, 0)) + kk * 8, col0 + at(n, N - 1) + kk * 8,
+                    mma_bf16(tm + kKV, (part ? low0 : col0 + at(n, K)) + kk * 8, col0 + at(n, V) + kk * 8,
                              idesc_bf16(128, DV, true, true), part + kk > 0);
             mma_commit(&ct.dfull);
-            mma_commit(&ct.empty[slot(n, 0)]);
-            mma_commit(&ct.empty[slot(n, N - 1)]);  // after P V too
+            mma_commit(&ct.empty[slot(n, K)]);
+            mma_commit(&ct.empty[slot(n, V)]);  // after P V too
         }
         __syncwarp();
         return true;
@@ -151,10 +155,10 @@ template <int DK, int DV, bool ONLY> struct Issuer {
         if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < DK; kk += 16)
-                mma_bf16(tm + kQX, row0 + at(n, 1) + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8, x0 + kk * 8,
+                mma_bf16(tm + kQX, row0 + at(n, Q) + (kk >> 6) * (kC * 128 / 16) + (kk & 63) / 8, x0 + kk * 8,
                          idesc_bf16(kC, DV, false, true), kk > 0);
             mma_commit(&ct.ofull);
-            mma_commit(&ct.empty[slot(n, 1)]);
+            mma_commit(&ct.empty[slot(n, Q)]);
         }
         __syncwarp();
         return true;
@@ -162,14 +166,14 @@ template <int DK, int DV, bool ONLY> struct Issuer {
     __device__ __forceinline__ void run(int chunks) {
         if (ONLY) {
             for (int n = 0; n < chunks; ++n)
-                if (!arrived(n, 1) || !added(n)) return;
+                if (!arrived(n, V) || !added(n)) return;
             return;
         }
         if (chunks > 0 && !scores(0)) return;
         for (int n = 0; n < chunks; ++n) {
-            if (!arrived(n, 2) || !values(n)) return;
+            if (!arrived(n, V) || !values(n) || !reads(n)) return;
             if (n + 1 < chunks && !scores(n + 1)) return;
-            if (!added(n) || !reads(n)) return;
+            if (!added(n)) return;
         }
     }
 };
@@ -186,7 +190,7 @@ __device__ __forceinline__ void keys(const ScanParams& p, const Work& w, int hea
     const int j = threadIdx.x & (kC - 1);
     const float g = p.g[head], f_in = p.reverse ? p.scale : 1.f;
     for (int n = 0; n < w.chunks; ++n) {
-        const uint32_t u = kTiles<ONLY> * n;
+        const uint32_t u = kTiles<ONLY> * n + kKeyTile<ONLY>;
         const int tokens = w.tokens(w.at(p, n));
         const float f = j < tokens ? f_in * decay(g, (float)(p.reverse ? j + 1 : tokens - 1 - j)) : 0.f;
         uint8_t* tile = smem + u % kSlots * Smem<DK, DV>::slot;
@@ -306,26 +310,27 @@ template <int DV> __device__ __forceinline__ void outputs(const ScanParams& p, c
     }
 }
 
-// Warps 12-15: a row of the state per thread (of the first DK).
+// Warps 12-19: half a row of the state per thread (of the first DK rows; warps 12-15 the first half of the columns).
 template <int DK, int DV, bool ONLY>
 __device__ __forceinline__ void states(const ScanParams& p, const Work& w, int head, uint8_t* smem, Control& ct) {
-    const int r = threadIdx.x & 127;
+    constexpr int N = DV / 2;  // columns of a thread
+    const int r = threadIdx.x & 127, c0 = threadIdx.x >= 16 * 32 ? N : 0;
     const bool on = r < DK;
-    const uint32_t tm = warp_lane_base(ct.tmem);
+    const uint32_t td = warp_lane_base(ct.tmem) + kKV + c0;
     const float g = p.g[head];
     const size_t unit = (size_t)w.seq * p.H + head;
-    float x[DV];
+    float x[N];
 #pragma unroll
-    for (int c = 0; c < DV; ++c) x[c] = 0.f;
+    for (int c = 0; c < N; ++c) x[c] = 0.f;
     const float* from = w.before ? w.before : p.x0 ? p.x0 + unit * DK * DV : nullptr;
     if (!ONLY && from && on) {
         if (!w.before && p.x0_transposed) {
 #pragma unroll
-            for (int c = 0; c < DV; ++c) x[c] = from[c * DK + r];
+            for (int c = 0; c < N; ++c) x[c] = from[(c0 + c) * DK + r];
         } else {
 #pragma unroll
-            for (int c = 0; c < DV; c += 4) {
-                const float4 y = load4(from + r * DV + c);
+            for (int c = 0; c < N; c += 4) {
+                const float4 y = load4(from + r * DV + c0 + c);
                 x[c] = y.x; x[c + 1] = y.y; x[c + 2] = y.z; x[c + 3] = y.w;
             }
         }
@@ -336,12 +341,12 @@ __device__ __forceinline__ void states(const ScanParams& p, const Work& w, int h
             tc_fence_after();
             const float a = decay(g, (float)w.tokens(w.at(p, n - 1)));
 #pragma unroll
-            for (int c = 0; c < DV; c += 32) {
-                float y[32];
-                tmem_ld32(tm + kKV + c, y);
+            for (int c = 0; c < N; c += 16) {
+                float y[16];
+                tmem_ld16(td + c, y);
                 tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
+                for (int j = 0; j < 16; j += 2) {
                     const float2 z = fma2(both(a), make_float2(x[c + j], x[c + j + 1]), make_float2(y[j], y[j + 1]));
                     x[c + j] = z.x;
                     x[c + j + 1] = z.y;
@@ -354,11 +359,11 @@ __device__ __forceinline__ void states(const ScanParams& p, const Work& w, int h
         if (!ONLY && n < w.chunks) {
             if (on)
 #pragma unroll
-                for (int c = 0; c < DV; c += 16) {
+                for (int c = 0; c < N; c += 16) {
                     float y[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) y[j] = x[c + j];
-                    tile_store16(smem + Smem<DK, DV>::x, r, c, DK, y);
+                    tile_store16(smem + Smem<DK, DV>::x, r, c0 + c, DK, y);
                 }
             fence_async_smem();
             warp_arrive(&ct.xfull);
@@ -367,7 +372,7 @@ __device__ __forceinline__ void states(const ScanParams& p, const Work& w, int h
     float* to = ONLY ? const_cast<float*>(w.before) : w.last && p.xT ? p.xT + unit * DK * DV : nullptr;
     if (to && on)
 #pragma unroll
-        for (int c = 0; c < DV; c += 4) store4(to + r * DV + c, make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]));
+        for (int c = 0; c < N; c += 4) store4(to + r * DV + c0 + c, make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]));
 }
 
 // n scans of the same sequences side by side: what they share is read at about the same time, and a block that is
@@ -391,7 +396,8 @@ __device__ __forceinline__ void scan_block(const ScanParams& p, const CUtensorMa
         }
         for (uint64_t* one : {&ct.landed, &ct.afull, &ct.dfull, &ct.ofull, &ct.drained}) mbar_init(one, 1);
         mbar_init(&ct.akeys, 1 + 4);
-        for (uint64_t* four : {&ct.pfull, &ct.kfull, &ct.dread, &ct.xfull, &ct.oempty}) mbar_init(four, 4);
+        for (uint64_t* four : {&ct.pfull, &ct.kfull, &ct.oempty}) mbar_init(four, 4);
+        for (uint64_t* eight : {&ct.dread, &ct.xfull}) mbar_init(eight, 8);
         ct.dead = 0;
         fence_barrier_init();
     }
@@ -402,20 +408,21 @@ __device__ __forceinline__ void scan_block(const ScanParams& p, const CUtensorMa
     __syncthreads();
     tc_fence_after();
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWeightRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWeightRegs));
         if (!ONLY) weights(p, w, ct);
     } else if (warp < 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kKeyRegs));
         keys<DK, DV, ONLY>(p, w, head, smem, ct);
     } else if (warp < 12) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOutRegs));
         if (!ONLY) outputs<DV>(p, w, head, ct);
-    } else if (warp < 16) {
+    } else if (warp < 20) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
         states<DK, DV, ONLY>(p, w, head, smem, ct);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-        if (warp == 16) Issuer<DK, DV, ONLY>(smem, ct).run(w.chunks), drain(&ct.drained);
-        else if (warp == 17) copy_tiles<DK, DV, ONLY>(p, w, head, m, m + 1, m + 2, smem, ct);
+        if (warp == 20) Issuer<DK, DV, ONLY>(smem, ct).run(w.chunks), drain(&ct.drained);
+        else if (warp == 21) copy_tiles<DK, DV, ONLY>(p, w, head, m, m + 1, m + 2, smem, ct);
     }
     __syncwarp();
     tc_fence_before();
