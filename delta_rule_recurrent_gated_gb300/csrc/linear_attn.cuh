@@ -30,7 +30,6 @@ struct ScanParams {
     int span;                    // chunks of a segment; 0: sequences are not split
     long long slots;             // segments that the workspace has room for
     float* part;                 // their states, [slots, H, dk, dv]
-    bool wide_out;               // set by the launcher: rows of out begin at multiples of 32 bytes
 };
 
 // Long sequences are split where a block for each sequence and head would leave most of the GPU idle: first every

@@ -34,17 +34,17 @@ static_assert(kWeightRegs + kKeyRegs + kOutRegs + 2 * kStateRegs + kOtherRegs <=
 constexpr uint32_t kA = 0, kQX = 128, kPV = 256, kKV = 384;  // columns of tensor memory
 
 struct Control {
-    uint64_t full[kSlots], empty[kSlots], landed, afull, akeys, pfull, kfull, dfull, dread, xfull, ofull, oempty, drained;
+    uint64_t full[kSlots], empty[kSlots], landed, afull, akeys, pfull, kfull, dfull, dread, xfull, xempty, ofull, oempty, drained;
     uint32_t tmem;
     volatile int dead;
     __align__(16) float power[32 + kC];  // beta a^n from place 32 on, zeros before
     __align__(16) float column[32];  // a^{31 - j}, reverse a^j
 };
 template <int DK, int DV> struct Smem {
+    // K'^T is read as 128 rows, for 64 channels 64 rows past them (at most of x) that nobody looks at; x: the image of the
+    // state, and 128 output rows
     static constexpr int slot = kC * (DK > DV ? DK : DV) * 2, low = kSlots * slot, x = low + kC * DK * 2,
-                         end = x + DK * DV * 2,
-                         // K'^T is read as 128 rows, for 64 channels 64 rows past them that nobody looks at
-                         control = end > low + kC * 128 * 2 ? end : low + kC * 128 * 2, bytes = control + 1024;
+                         control = x + kC * DV * 2, bytes = control + 1024;
     static_assert(sizeof(Control) <= 1024, "control block");
 };
 
@@ -278,15 +278,19 @@ __device__ __forceinline__ void weights(const ScanParams& p, const Work& w, Cont
     }
 }
 
-// Warps 8-11, a token per thread.
-template <int DV> __device__ __forceinline__ void outputs(const ScanParams& p, const Work& w, int head, Control& ct) {
-    const int i = threadIdx.x & (kC - 1);
+// Warps 8-11, a token per thread.  The rows of a whole chunk leave as tensor stores, 32 by each warp, from the place of the
+// state's image, which nobody needs between Q X and the next state: a lane has a row of its own, and its pieces in
+// memory would be a transaction each (122 us for b8 t4096 h16 d128 that way, 97 without stores).
+template <int DK, int DV>
+__device__ __forceinline__ void outputs(const ScanParams& p, const Work& w, int head, const CUtensorMap* mo, uint8_t* smem, Control& ct) {
+    const int i = threadIdx.x & (kC - 1), lane = threadIdx.x & 31;
     const uint32_t tm = warp_lane_base(ct.tmem);
     const float g = p.g[head], f_out = p.reverse ? 1.f : p.scale;
+    uint8_t* tile = smem + Smem<DK, DV>::x;
     for (int n = 0; n < w.chunks; ++n) {
         const int first = w.at(p, n), tokens = w.tokens(first);
         const float2 fx = both(f_out * decay(g, (float)(p.reverse ? tokens - 1 - i : i + 1))), fy = both(f_out);
-        if (!wait(ct.dead, &ct.ofull, n & 1)) return;
+        if (!wait(ct.dead, &ct.ofull, n & 1)) break;
         tc_fence_after();
         __nv_bfloat16* to = static_cast<__nv_bfloat16*>(p.out) + (w.row0 + first + i) * p.ld_o + (long long)head * DV;
 #pragma unroll 1
@@ -295,19 +299,35 @@ template <int DV> __device__ __forceinline__ void outputs(const ScanParams& p, c
             tmem_ld32(tm + kQX + c, x);
             tmem_ld32(tm + kPV + c, y);
             tmem_ld_wait();
-            if (c + 32 == DV) {
-                tc_fence_before();
-                warp_arrive(&ct.oempty);
-            }
             uint32_t z[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 const float2 o = fma2(fx, make_float2(x[2 * j], x[2 * j + 1]), mul2(fy, make_float2(y[2 * j], y[2 * j + 1])));
                 z[j] = pack_bf16(o.x, o.y);
             }
-            if (i < tokens) store_bf16x32(to + c, z, p.wide_out);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint4 u = make_uint4(z[4 * j], z[4 * j + 1], z[4 * j + 2], z[4 * j + 3]);
+                if (tokens == kC) *reinterpret_cast<uint4*>(tile + sw128_offset(i, c + 8 * j, kC)) = u;
+                else if (i < tokens) reinterpret_cast<uint4*>(to + c)[j] = u;
+            }
         }
+        tc_fence_before();
+        warp_arrive(&ct.oempty);
+        if (tokens == kC) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+#pragma unroll
+                for (int c = 0; c < DV; c += 64)
+                    tma_store_3d(mo, tile + (c / 64) * kC * 128 + i * 128, c, head, w.row0 + first + i);
+                bulk_commit();
+                bulk_wait_read();
+            }
+        }
+        warp_arrive(&ct.xempty);
     }
+    if (lane == 0) bulk_wait_all();
 }
 
 // Warps 12-19: half a row of the state per thread (of the first DK rows; warps 12-15 the first half of the columns).
@@ -354,7 +374,7 @@ __device__ __forceinline__ void states(const ScanParams& p, const Work& w, int h
             }
             tc_fence_before();
             warp_arrive(&ct.dread);
-            if (!ONLY && !wait(ct.dead, &ct.ofull, (n - 1) & 1)) return;  // the image of the state has been read
+            if (!ONLY && !wait(ct.dead, &ct.xempty, (n - 1) & 1)) return;  // its image, and then the rows there, have been read
         }
         if (!ONLY && n < w.chunks) {
             if (on)
@@ -378,7 +398,7 @@ __device__ __forceinline__ void states(const ScanParams& p, const Work& w, int h
 // n scans of the same sequences side by side: what they share is read at about the same time, and a block that is
 // through with one takes what comes next of all.
 struct ScanSet {
-    CUtensorMap m[kMostScans][3];  // of q, k, v
+    CUtensorMap m[kMostScans][4];  // of q, k, v, out
     ScanParams p[kMostScans];
 };
 template <int DK, int DV, bool ONLY>
@@ -396,7 +416,7 @@ __device__ __forceinline__ void scan_block(const ScanParams& p, const CUtensorMa
         }
         for (uint64_t* one : {&ct.landed, &ct.afull, &ct.dfull, &ct.ofull, &ct.drained}) mbar_init(one, 1);
         mbar_init(&ct.akeys, 1 + 4);
-        for (uint64_t* four : {&ct.pfull, &ct.kfull, &ct.oempty}) mbar_init(four, 4);
+        for (uint64_t* four : {&ct.pfull, &ct.kfull, &ct.xempty, &ct.oempty}) mbar_init(four, 4);
         for (uint64_t* eight : {&ct.dread, &ct.xfull}) mbar_init(eight, 8);
         ct.dead = 0;
         fence_barrier_init();
@@ -415,7 +435,7 @@ __device__ __forceinline__ void scan_block(const ScanParams& p, const CUtensorMa
         keys<DK, DV, ONLY>(p, w, head, smem, ct);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOutRegs));
-        if (!ONLY) outputs<DV>(p, w, head, ct);
+        if (!ONLY) outputs<DK, DV>(p, w, head, m + 3, smem, ct);
     } else if (warp < 20) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegs));
         states<DK, DV, ONLY>(p, w, head, smem, ct);
@@ -467,10 +487,10 @@ cudaError_t linear_scans_tc(const ScanParams* p, int n, bool only, cudaStream_t 
     ScanSet set;
     for (int i = 0; i < n; ++i) {
         set.p[i] = p[i];
-        set.p[i].wide_out = wide_rows(p[i].out, p[i].ld_o);
         if (!head_rows_map(&set.m[i][0], p[i].q, p[i].dk, p[i].H, p[i].rows, p[i].ld_q, kC) ||
             !head_rows_map(&set.m[i][1], p[i].k, p[i].dk, p[i].H, p[i].rows, p[i].ld_k, kC) ||
-            !head_rows_map(&set.m[i][2], p[i].v, p[i].dv, p[i].H, p[i].rows, p[i].ld_v, kC))
+            !head_rows_map(&set.m[i][2], p[i].v, p[i].dv, p[i].H, p[i].rows, p[i].ld_v, kC) ||
+            !head_rows_map(&set.m[i][3], p[i].out, p[i].dv, p[i].H, p[i].rows, p[i].ld_o, 32))
             return cudaErrorInvalidValue;
     }
     if (p->dk != p->dv) return only ? launch<64, 128, true>(set, n, st) : launch<64, 128, false>(set, n, st);

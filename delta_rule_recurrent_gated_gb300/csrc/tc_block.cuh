@@ -105,21 +105,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         : "memory");
 }
 
-// 32 bf16 values, 16-byte aligned, as two pairs of words z; `wide`: 32-byte aligned, whole sectors at a time (a lane
-// has a row of its own, so that every 16-byte piece would be a transaction of its own).
-__device__ __forceinline__ void store_bf16x32(__nv_bfloat16* to, const uint32_t (&z)[16], bool wide) {
-    if (wide) {
-#pragma unroll
-        for (int i = 0; i < 16; i += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(to + 2 * i), "r"(z[i]), "r"(z[i + 1]),
-                         "r"(z[i + 2]), "r"(z[i + 3]), "r"(z[i + 4]), "r"(z[i + 5]), "r"(z[i + 6]), "r"(z[i + 7])
-                         : "memory");
-    } else {
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) *reinterpret_cast<uint4*>(to + 2 * i) = make_uint4(z[i], z[i + 1], z[i + 2], z[i + 3]);
-    }
-}
-
 // ------------------------------------------------------------------ tiles
 // R rows of a head as an SW128 tile: a box for each 64 channels.
 template <int R, int D>
@@ -176,8 +161,6 @@ inline bool head_rows_map(CUtensorMap* m, const void* ptr, int D, int H, long lo
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// Whether rows of bf16 values, ld apart, begin at multiples of 32 bytes.
-inline bool wide_rows(const void* p, long long ld) { return reinterpret_cast<uintptr_t>(p) % 32 == 0 && ld % 16 == 0; }
 inline int sm_count() {
     int dev = 0, n = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
