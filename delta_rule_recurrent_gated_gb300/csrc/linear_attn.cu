@@ -199,15 +199,19 @@ cudaError_t scan_simt(const ScanParams& p, bool only, cudaStream_t st) {
 struct JoinSet { ScanParams p[kMostScans]; };
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ JoinSet set) {
     const ScanParams& p = set.p[blockIdx.z];
-    const int head = blockIdx.x % p.H, R = p.span * kScanChunk, size = p.dk * p.dv;
-    Work w;
-    if (!make_work(p, blockIdx.x / p.H, head, w) || !w.before || !w.first) return;
+    const int seq = blockIdx.x / p.H, head = blockIdx.x % p.H, R = p.span * kScanChunk, size = p.dk * p.dv;
+    int row0, len;
+    seq_rows(p.s, seq, row0, len);
+    const int tiles = (len + R - 1) / R;
+    if (tiles < 2) return;
+    const long long slot = slots_before(p.s, R, seq);
+    if (slot + tiles > p.slots) return;  // offsets out of order, as in make_work
     const int i = 4 * (blockIdx.y * 256 + threadIdx.x);
     if (i >= size) return;
     const float g = p.g[head];
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (p.x0) {
-        const float* from = p.x0 + ((size_t)w.seq * p.H + head) * size;
+        const float* from = p.x0 + ((size_t)seq * p.H + head) * size;
         if (p.x0_transposed) {
             const int r = i / p.dv, c = i % p.dv;
             x = make_float4(from[c * p.dk + r], from[(c + 1) * p.dk + r], from[(c + 2) * p.dk + r], from[(c + 3) * p.dk + r]);
@@ -215,9 +219,8 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
             x = load4(from + i);
         }
     }
-    const int tiles = (w.len + R - 1) / R;
     const long long step = (p.reverse ? -1ll : 1ll) * p.H * size;
-    float* at = const_cast<float*>(w.before) + i;
+    float* at = p.part + ((slot + (p.reverse ? tiles - 1 : 0)) * p.H + head) * size + i;
     // four segments' own states are read at once (the last segment's was not formed, nothing comes after it)
     for (int n = 0; n < tiles; n += 4) {
         float4 own[4];
@@ -228,7 +231,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
             if (n + k >= tiles) break;
             store4(at + k * step, x);
             const int t = p.reverse ? tiles - 1 - n - k : n + k;
-            const float a = decay(g, (float)min(R, w.len - t * R));
+            const float a = decay(g, (float)min(R, len - t * R));
             x = make_float4(fmaf(a, x.x, own[k].x), fmaf(a, x.y, own[k].y), fmaf(a, x.z, own[k].z), fmaf(a, x.w, own[k].w));
         }
         at += 4 * step;
@@ -372,7 +375,7 @@ cudaError_t linear_scans(const ScanParams* p, int n, int io, cudaStream_t st) {
         JoinSet set;
         for (int i = 0; i < n; ++i) set.p[i] = p[i];
         TraceScope ts("linear_join", st);
-        const dim3 grid((unsigned)(scan_items(*p) * p->H), (p->dk * p->dv + 1023) / 1024, n);
+        const dim3 grid((unsigned)(p->s.N * p->H), (p->dk * p->dv + 1023) / 1024, n);
         linear_join_kernel<<<grid, 256, 0, st>>>(set);
         if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     }

@@ -184,9 +184,9 @@ __device__ __forceinline__ void split2(uint32_t u, float f, uint32_t& hi, uint32
     hi = pack_bf16(x.x, x.y);
     lo = pack_bf16(x.x - __uint_as_float(hi << 16), x.y - __uint_as_float(hi & 0xffff0000u));
 }
-// Warps 4-7, a token per thread: K'.
+// Warps 4-7, a token per thread: K', channels c0 .. c1 - 1 (all; where there is no P to form warps 0-3 have half of them).
 template <int DK, int DV, bool ONLY>
-__device__ __forceinline__ void keys(const ScanParams& p, const Work& w, int head, uint8_t* smem, Control& ct) {
+__device__ __forceinline__ void keys(const ScanParams& p, const Work& w, int head, int c0, int c1, uint8_t* smem, Control& ct) {
     const int j = threadIdx.x & (kC - 1);
     const float g = p.g[head], f_in = p.reverse ? p.scale : 1.f;
     for (int n = 0; n < w.chunks; ++n) {
@@ -202,7 +202,7 @@ __device__ __forceinline__ void keys(const ScanParams& p, const Work& w, int hea
         if (n && !wait(ct.dead, &ct.dfull, (n - 1) & 1)) return;       // low parts of the chunk before are in use
         const bool none = tokens < kC && j >= tokens;  // behind the sequence: may be no numbers
 #pragma unroll 1
-        for (int c = 0; c < DK; c += 32) {  // four pieces are read before the first is written
+        for (int c = c0; c < c1; c += 32) {  // four pieces are read before the first is written
             const uint32_t row = c / 64 * kC * 128 + j * 128;
             uint4 x[4];
 #pragma unroll
@@ -416,7 +416,8 @@ __device__ __forceinline__ void scan_block(const ScanParams& p, const CUtensorMa
         }
         for (uint64_t* one : {&ct.landed, &ct.afull, &ct.dfull, &ct.ofull, &ct.drained}) mbar_init(one, 1);
         mbar_init(&ct.akeys, 1 + 4);
-        for (uint64_t* four : {&ct.pfull, &ct.kfull, &ct.xempty, &ct.oempty}) mbar_init(four, 4);
+        for (uint64_t* four : {&ct.pfull, &ct.xempty, &ct.oempty}) mbar_init(four, 4);
+        mbar_init(&ct.kfull, ONLY ? 8 : 4);
         for (uint64_t* eight : {&ct.dread, &ct.xfull}) mbar_init(eight, 8);
         ct.dead = 0;
         fence_barrier_init();
@@ -429,10 +430,11 @@ __device__ __forceinline__ void scan_block(const ScanParams& p, const CUtensorMa
     tc_fence_after();
     if (warp < 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWeightRegs));
-        if (!ONLY) weights(p, w, ct);
+        if (ONLY) keys<DK, DV, ONLY>(p, w, head, DK / 2, DK, smem, ct);
+        else weights(p, w, ct);
     } else if (warp < 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kKeyRegs));
-        keys<DK, DV, ONLY>(p, w, head, smem, ct);
+        keys<DK, DV, ONLY>(p, w, head, 0, ONLY ? DK / 2 : DK, smem, ct);
     } else if (warp < 12) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kOutRegs));
         if (!ONLY) outputs<DK, DV>(p, w, head, m + 3, smem, ct);

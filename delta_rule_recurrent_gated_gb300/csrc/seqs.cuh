@@ -119,4 +119,15 @@ __device__ __forceinline__ bool find_tile_in_order(const Seqs& q, int R, int lea
     }
     return false;
 }
+// find_tile_in_order's `slot` of a sequence that has several tiles; called by a whole warp.
+__device__ __forceinline__ long long slots_before(const Seqs& q, int R, int seq) {
+    if (!q.cu) return (long long)seq * ((q.T + R - 1) / R);
+    long long c = 0;
+    for (int s = threadIdx.x & 31; s < seq; s += 32) {
+        int row0, len;
+        seq_rows(q, s, row0, len);
+        if (len > R) c += (len + R - 1) / R;
+    }
+    return warp_sum(c);
+}
 }  // namespace dr
