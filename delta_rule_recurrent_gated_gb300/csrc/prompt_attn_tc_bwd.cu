@@ -5,7 +5,9 @@
 //   dq_i = scale sum_j ds_ij k_j;   dk_j = scale sum_i ds_ij q_i;   dv_j = sum_i p_ij dO_i
 //
 // Two kernels, so that every sum has one owner: no atomics, no fp32 image of a gradient in memory, the same
-// bits every time.  They form S and dP = dO V^T twice, 7 products where 5 would do.
+// bits every time.  They form S and dP = dO V^T twice, 7 products where 5 would do.  8 x 4096 tokens, 16 query heads of
+// 128, 4 key heads: dq 565 us (1460 TFLOP/s of its own three products), dk and dv 672 us (1640 TFLOP/s of their four),
+// bound by the tensor cores and the operands they read from shared memory; D = dO.o before them 49 us.
 //   dq:     128 queries of a head, against 128 keys a stage: S = Q K^T, dP = dO V^T, dQ += dS K, issued as
 //           S(n + 1), dP(n + 1), dQ(n).  dP has two buffers in tensor memory, and dS takes the place of its dP.
 //   dk, dv: 128 keys of a key head, against 128 queries a stage of all query heads that read it, one after another:

@@ -149,10 +149,20 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     }();
     return fn;
 }
+// The encoder is a call of the driver and wants a current context, which a host thread has from its first call of the
+// runtime that needs one: once for each thread and device.
+inline bool thread_context() {
+    static thread_local int bound = -1;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev != bound && cudaSetDevice(dev) != cudaSuccess) return false;
+    bound = dev;
+    return true;
+}
 // `rows` token rows of H heads of D bf16 values, ld elements apart; boxes of 64 channels of one head of R rows.
 inline bool head_rows_map(CUtensorMap* m, const void* ptr, int D, int H, long long rows, long long ld, int R) {
     auto enc = tensor_map_encoder();
-    if (!enc) return false;
+    if (!enc || !thread_context()) return false;
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)rows};
     cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)ld * 2};
     cuuint32_t box[3] = {64, 1, (cuuint32_t)R};
