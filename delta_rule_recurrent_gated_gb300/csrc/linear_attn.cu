@@ -26,8 +26,14 @@ template <int DK, int W> struct ScanSmem {  // pitches: 16-byte reads of eight r
                          floats = x + DK * pw;
 };
 
+// Scans of the same sizes, side by side (blockIdx.z).
+struct ScanSet {
+    ScanParams p[kMostScans];
+};
 // ONLY: the segments' own states, from nothing.
-template <int DK, int W, bool ONLY> __global__ void __launch_bounds__(kThreads, 2) linear_scan_kernel(const ScanParams p) {
+template <int DK, int W, bool ONLY>
+__global__ void __launch_bounds__(kThreads, 2) linear_scan_kernel(const __grid_constant__ ScanSet set) {
+    const ScanParams& p = set.p[blockIdx.z];
     using L = ScanSmem<DK, W>;
     extern __shared__ __align__(16) float sm[];
     float *Q = sm, *K = sm + L::k, *V = sm + L::v, *A = sm + L::a, *X = sm + L::x;
@@ -174,33 +180,32 @@ template <int DK, int W, bool ONLY> __global__ void __launch_bounds__(kThreads, 
         for (int i = threadIdx.x; i < DK * W; i += kThreads) to[(i / W) * p.dv + w0 + i % W] = X[(i / W) * L::pw + i % W];
 }
 
-template <int DK, int W, bool ONLY> cudaError_t scan(const ScanParams& p, cudaStream_t st) {
+template <int DK, int W, bool ONLY> cudaError_t scan(const ScanSet& set, int n, cudaStream_t st) {
     static std::atomic<unsigned long long> ready{0};
     constexpr int smem = ScanSmem<DK, W>::floats * 4;
     if (cudaError_t e = set_smem_once(linear_scan_kernel<DK, W, ONLY>, smem, ready); e != cudaSuccess) return e;
-    const long long blocks = scan_items(p) * p.H;
+    const long long blocks = scan_items(set.p[0]) * set.p[0].H;
     if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
     TraceScope ts(ONLY ? "linear_segments" : "linear_scan", st);
-    linear_scan_kernel<DK, W, ONLY><<<dim3((unsigned)blocks, p.dv / W), kThreads, smem, st>>>(p);
+    linear_scan_kernel<DK, W, ONLY><<<dim3((unsigned)blocks, set.p[0].dv / W, n), kThreads, smem, st>>>(set);
     return cudaGetLastError();
 }
-template <int DK> cudaError_t scan_width(const ScanParams& p, bool only, cudaStream_t st) {
-    if (p.dv == 16) return only ? scan<DK, 16, true>(p, st) : scan<DK, 16, false>(p, st);
-    return only ? scan<DK, 32, true>(p, st) : scan<DK, 32, false>(p, st);
+template <int DK> cudaError_t scan_width(const ScanSet& set, int n, bool only, cudaStream_t st) {
+    if (set.p[0].dv == 16) return only ? scan<DK, 16, true>(set, n, st) : scan<DK, 16, false>(set, n, st);
+    return only ? scan<DK, 32, true>(set, n, st) : scan<DK, 32, false>(set, n, st);
 }
-cudaError_t scan_simt(const ScanParams& p, bool only, cudaStream_t st) {
-    switch (p.dk) {
-        case 16: return scan_width<16>(p, only, st);
-        case 32: return scan_width<32>(p, only, st);
-        case 64: return scan_width<64>(p, only, st);
-        default: return scan_width<128>(p, only, st);
+cudaError_t scan_simt(const ScanSet& set, int n, bool only, cudaStream_t st) {
+    switch (set.p[0].dk) {
+        case 16: return scan_width<16>(set, n, only, st);
+        case 32: return scan_width<32>(set, n, only, st);
+        case 64: return scan_width<64>(set, n, only, st);
+        default: return scan_width<128>(set, n, only, st);
     }
 }
 
 // ------------------------------------------------------------------ segments
 // The states that the segments begin with, over the segments' own: four values per thread.
-struct JoinSet { ScanParams p[kMostScans]; };
-__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ JoinSet set) {
+__global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ ScanSet set) {
     const ScanParams& p = set.p[blockIdx.z];
     const int seq = blockIdx.x / p.H, head = blockIdx.x % p.H, R = p.span * kScanChunk, size = p.dk * p.dv;
     int row0, len;
@@ -346,7 +351,7 @@ int scan_span(int io, long long rows, int N, int T, bool packed, int H, int dk, 
     if (rows == 0 || N == 0) return 0;
     const bool tc = io == DR_BF16;
     const int room = tc ? 152 : 304, least = tc ? 4 : 1;
-    const long long units = (long long)N * H * (tc ? scans : std::max(std::min(dk, dv) / 32, 1));  // on the CUDA cores one by one
+    const long long units = (long long)N * H * (tc ? scans : std::max(std::min(dk, dv) / 32, 1));  // on the CUDA cores not all together
     const long long chunks = packed ? rows / kScanChunk + N : (long long)N * ((T + kScanChunk - 1) / kScanChunk);  // of all sequences
     if (chunks < (tc ? 12 : 2)) return 0;
     long long span;
@@ -370,13 +375,16 @@ cudaError_t linear_scans(const ScanParams* p, int n, int io, cudaStream_t st) {
     const bool tc = io == DR_BF16 && p->rows > 0;
     auto all = [&](bool only) {
         if (tc) return linear_scans_tc(p, n, only, st);
-        for (int i = 0; i < n; ++i)
-            if (cudaError_t e = scan_simt(p[i], only, st); e != cudaSuccess) return e;
+        for (int i = 0, m; i < n; i += m) {  // scans of the same sizes follow one another
+            ScanSet set;
+            for (m = 0; i + m < n && p[i + m].dk == p[i].dk && p[i + m].dv == p[i].dv; ++m) set.p[m] = p[i + m];
+            if (cudaError_t e = scan_simt(set, m, only, st); e != cudaSuccess) return e;
+        }
         return cudaSuccess;
     };
     if (p->rows > 0 && p->span) {
         if (cudaError_t e = all(true); e != cudaSuccess) return e;
-        JoinSet set;
+        ScanSet set;
         for (int i = 0; i < n; ++i) set.p[i] = p[i];
         TraceScope ts("linear_join", st);
         const dim3 grid((unsigned)(p->s.N * p->H), (p->dk * p->dv + 1023) / 1024, n);

@@ -18,7 +18,14 @@ __device__ __forceinline__ bool make_work(const ScanParams& p, int item, int hea
     const int span = p.span ? p.span : (1 << 30) / kScanChunk;
     int tile, tiles;
     long long slot;
-    if (!find_tile_in_order(p.s, span * kScanChunk, 1, item, w.seq, tile, tiles, slot)) return false;
+    if (p.span) {
+        if (!find_tile_in_order(p.s, span * kScanChunk, 1, item, w.seq, tile, tiles, slot)) return false;
+    } else {  // an item for each sequence
+        w.seq = item;
+        tile = 0;
+        tiles = 1;
+        slot = 0;
+    }
     seq_rows(p.s, w.seq, w.row0, w.len);
     w.c0 = tile * span;
     w.chunks = min(span, (w.len + kScanChunk - 1) / kScanChunk - w.c0);
@@ -32,6 +39,7 @@ __device__ __forceinline__ bool make_work(const ScanParams& p, int item, int hea
 // Items of a launch: segments of the sequences, a sequence without tokens as one.
 long long scan_items(const ScanParams& p) {
     const long long R = (p.span ? p.span : (1 << 30) / kScanChunk) * (long long)kScanChunk;
+    if (!p.span) return p.s.N;
     return p.s.cu ? p.s.T / R + p.s.N : p.s.N * (p.s.T > R ? (p.s.T + R - 1) / R : 1);
 }
 

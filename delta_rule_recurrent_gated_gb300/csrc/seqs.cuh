@@ -33,55 +33,8 @@ __device__ __forceinline__ long long warp_sum(long long x) {
     return x;
 }
 
-// Tile number `item` of all tiles of R rows, those with the largest index in their sequence first (under a
-// causal mask the longest rows of work start first and the short ones fill the gaps); called by a whole warp.
-// Returns false where there are fewer tiles.
-__device__ __forceinline__ bool find_tile(const Seqs& q, int R, long long item, int& seq, int& tile) {
-    if (!q.cu) {
-        const int n = (q.T + R - 1) / R;
-        if (item >= (long long)n * q.N) return false;
-        tile = n - 1 - (int)(item / q.N);
-        seq = (int)(item % q.N);
-        return true;
-    }
-    const int lane = threadIdx.x & 31;
-    auto tiles = [&](int s) {
-        if (s >= q.N) return 0;
-        int row0, len;
-        seq_rows(q, s, row0, len);
-        return (len + R - 1) / R;
-    };
-    auto count = [&](int v) {  // tiles with index v or more
-        long long c = 0;
-        for (int s = lane; s < q.N; s += 32) c += max(0, tiles(s) - v);
-        return warp_sum(c);
-    };
-    if (item >= count(0)) return false;
-    int lo = 0, hi = (q.T + R - 1) / R;  // count(lo) > item >= count(hi)
-    long long above = 0;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        const long long c = count(mid);
-        if (c > item) lo = mid;
-        else hi = mid, above = c;
-    }
-    tile = lo;
-    int rest = (int)(item - above);  // among the sequences that have tile lo
-    for (int s0 = 0; s0 < q.N; s0 += 32) {
-        const unsigned has = __ballot_sync(0xffffffffu, tiles(s0 + lane) > lo);
-        const int n = __popc(has);
-        if (rest < n) {
-            const bool mine = (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == rest;
-            seq = s0 + __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
-            return true;
-        }
-        rest -= n;
-    }
-    return false;
-}
-
-// The same tiles in the order of the sequences: number `item`, and for a sequence of several tiles how many tiles
-// such sequences have before it (`slot`: a place for each of them); called by a whole warp.  A sequence without tokens
+// Tile number `item` of all tiles of R rows in the order of the sequences, and for a sequence of several tiles how many
+// tiles such sequences have before it (`slot`: a place for each of them); called by a whole warp.  A sequence without tokens
 // counts as `least` tiles, 0 or 1.
 __device__ __forceinline__ bool find_tile_in_order(const Seqs& q, int R, int least, long long item, int& seq, int& tile,
                                                    int& tiles, long long& slot) {
@@ -119,6 +72,59 @@ __device__ __forceinline__ bool find_tile_in_order(const Seqs& q, int R, int lea
     }
     return false;
 }
+// Tile number `item` of all tiles of R rows, those with the largest index in their sequence first (under a
+// causal mask the longest rows of work start first and the short ones fill the gaps); called by a whole warp.
+// Returns false where there are fewer tiles.  With many sequences, whose tiles are few, in their order: a search is
+// a pass over the offsets instead of one for each power of two of the tiles.
+__device__ __forceinline__ bool find_tile(const Seqs& q, int R, long long item, int& seq, int& tile) {
+    if (!q.cu) {
+        const int n = (q.T + R - 1) / R;
+        if (item >= (long long)n * q.N) return false;
+        tile = n - 1 - (int)(item / q.N);
+        seq = (int)(item % q.N);
+        return true;
+    }
+    if (q.cu && q.N > 256) {
+        int tiles;
+        long long slot;
+        return find_tile_in_order(q, R, 0, item, seq, tile, tiles, slot);
+    }
+    const int lane = threadIdx.x & 31;
+    auto tiles = [&](int s) {
+        if (s >= q.N) return 0;
+        int row0, len;
+        seq_rows(q, s, row0, len);
+        return (len + R - 1) / R;
+    };
+    auto count = [&](int v) {  // tiles with index v or more
+        long long c = 0;
+        for (int s = lane; s < q.N; s += 32) c += max(0, tiles(s) - v);
+        return warp_sum(c);
+    };
+    if (item >= count(0)) return false;
+    int lo = 0, hi = (q.T + R - 1) / R;  // count(lo) > item >= count(hi)
+    long long above = 0;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        const long long c = count(mid);
+        if (c > item) lo = mid;
+        else hi = mid, above = c;
+    }
+    tile = lo;
+    int rest = (int)(item - above);  // among the sequences that have tile lo
+    for (int s0 = 0; s0 < q.N; s0 += 32) {
+        const unsigned has = __ballot_sync(0xffffffffu, tiles(s0 + lane) > lo);
+        const int n = __popc(has);
+        if (rest < n) {
+            const bool mine = (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == rest;
+            seq = s0 + __ffs(__ballot_sync(0xffffffffu, mine)) - 1;
+            return true;
+        }
+        rest -= n;
+    }
+    return false;
+}
+
 // find_tile_in_order's `slot` of a sequence that has several tiles; called by a whole warp.
 __device__ __forceinline__ long long slots_before(const Seqs& q, int R, int seq) {
     if (!q.cu) return (long long)seq * ((q.T + R - 1) / R);

@@ -25,6 +25,8 @@ CASES = [  # lengths, packed, H, dk, dv, states, inside a projection
     ([127, 128, 129, 255, 256, 1], True, 1, 64, 128, True, False),
     ([1] * 70, True, 2, 64, 64, True, False),
     ([17, 40, 3] * 14, True, 1, 128, 64, False, True),
+    ([1, 0, 3, 2] * 90, True, 1, 64, 64, True, False),  # many sequences
+    ([1, 0, 2] * 100 + [2500], True, 1, 64, 64, True, False),  # and a long one, in segments
 ]
 SMALL = [([70, 3, 0, 129], True, 2, 16, 32, True, True), ([33, 33], False, 3, 32, 16, False, False),
          ([65], False, 2, 16, 16, True, False), ([100], False, 1, 32, 128, True, True), ([90, 1], True, 2, 128, 16, True, False)]

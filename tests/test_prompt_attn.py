@@ -27,6 +27,7 @@ CASES = [  # lengths, packed, Hq, H, d, window, inside a projection
     ([300, 200], True, 2, 1, 64, 2 ** 31 - 1, False),
     ([1] * 70, True, 8, 2, 64, 0, False),
     ([17, 40, 3] * 14, True, 2, 1, 128, 9, True),
+    ([1, 0, 3, 2] * 90, True, 1, 1, 64, 0, False),  # many sequences
 ]
 
 
