@@ -26,6 +26,21 @@ template <int DK, int W> struct ScanSmem {  // pitches: 16-byte reads of eight r
                          floats = x + DK * pw;
 };
 
+// N neighbouring values, N = 1, 2, or a multiple of 4.
+template <int N> __device__ __forceinline__ void load_row(float (&x)[N], const float* p) {
+    if constexpr (N == 1) {
+        x[0] = *p;
+    } else if constexpr (N == 2) {
+        const float2 y = *reinterpret_cast<const float2*>(p);
+        x[0] = y.x; x[1] = y.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 y = *reinterpret_cast<const float4*>(p + i);
+            x[i] = y.x; x[i + 1] = y.y; x[i + 2] = y.z; x[i + 3] = y.w;
+        }
+    }
+}
 // Scans of the same sizes, side by side (blockIdx.z).
 struct ScanSet {
     ScanParams p[kMostScans];
@@ -59,21 +74,33 @@ __global__ void __launch_bounds__(kThreads, 2) linear_scan_kernel(const __grid_c
         const int n = min(kChunk, len - t0);
         __syncthreads();
         auto token = [&](int i) { return (long long)w.row0 + (p.reverse ? end - 1 - t0 - i : begin + t0 + i); };
-        for (int i = threadIdx.x; i < kChunk * (DK / 4); i += kThreads) {
-            const int r = i / (DK / 4), c = (i % (DK / 4)) * 4;
-            float4 q = make_float4(0.f, 0.f, 0.f, 0.f), k = q;
-            if (r < n) {
-                if (!ONLY) q = load4(static_cast<const float*>(p.q) + token(r) * p.ld_q + (long long)h * DK + c);
-                k = load4(static_cast<const float*>(p.k) + token(r) * p.ld_k + (long long)h * DK + c);
+        {   // everything is on its way before the first of it is stored
+            constexpr int NK = kChunk * DK / 4 / kThreads, NV = kChunk * W / 4 / kThreads > 0 ? kChunk * W / 4 / kThreads : 1;
+            static_assert(NK * kThreads == kChunk * DK / 4 && NV * kThreads >= kChunk * W / 4, "pieces of the threads");
+            const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+            float4 q[NK], k[NK], v[NV];
+#pragma unroll
+            for (int m = 0; m < NK; ++m) {
+                const int i = threadIdx.x + m * kThreads, r = i / (DK / 4), c = (i % (DK / 4)) * 4;
+                q[m] = !ONLY && r < n ? load4(static_cast<const float*>(p.q) + token(r) * p.ld_q + (long long)h * DK + c) : zero;
+                k[m] = r < n ? load4(static_cast<const float*>(p.k) + token(r) * p.ld_k + (long long)h * DK + c) : zero;
             }
-            *reinterpret_cast<float4*>(Q + r * L::pk + c) = q;
-            *reinterpret_cast<float4*>(K + r * L::pk + c) = k;
-        }
-        for (int i = threadIdx.x; i < kChunk * (W / 4); i += kThreads) {
-            const int r = i / (W / 4), c = (i % (W / 4)) * 4;
-            const float4 v = r < n ? load4(static_cast<const float*>(p.v) + token(r) * p.ld_v + (long long)h * p.dv + w0 + c)
-                                   : make_float4(0.f, 0.f, 0.f, 0.f);
-            *reinterpret_cast<float4*>(V + r * L::pw + c) = v;
+#pragma unroll
+            for (int m = 0; m < NV; ++m) {
+                const int i = threadIdx.x + m * kThreads, r = i / (W / 4), c = (i % (W / 4)) * 4;
+                v[m] = r < n ? load4(static_cast<const float*>(p.v) + token(r) * p.ld_v + (long long)h * p.dv + w0 + c) : zero;
+            }
+#pragma unroll
+            for (int m = 0; m < NK; ++m) {
+                const int i = threadIdx.x + m * kThreads, at = i / (DK / 4) * L::pk + (i % (DK / 4)) * 4;
+                if (!ONLY) *reinterpret_cast<float4*>(Q + at) = q[m];
+                *reinterpret_cast<float4*>(K + at) = k[m];
+            }
+#pragma unroll
+            for (int m = 0; m < NV; ++m) {
+                const int i = threadIdx.x + m * kThreads;
+                if (i < kChunk * W / 4) *reinterpret_cast<float4*>(V + i / (W / 4) * L::pw + (i % (W / 4)) * 4) = v[m];
+            }
         }
         __syncthreads();
         if (!ONLY) {  // weights of the pairs: rows 4 ty + i, columns tx + 16 j
@@ -113,14 +140,15 @@ __global__ void __launch_bounds__(kThreads, 2) linear_scan_kernel(const __grid_c
 #pragma unroll
                 for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * L::pa + c);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 4; ++k) {
+                    float v[WX];
+                    load_row(v, V + (c + k) * L::pw + WX * tx);
 #pragma unroll
-                    for (int w = 0; w < WX; ++w) {
-                        const float v = V[(c + k) * L::pw + WX * tx + w];
+                    for (int w = 0; w < WX; ++w)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            o[i][w] = fmaf(k == 0 ? a[i].x : k == 1 ? a[i].y : k == 2 ? a[i].z : a[i].w, v, o[i][w]);
-                    }
+                            o[i][w] = fmaf(k == 0 ? a[i].x : k == 1 ? a[i].y : k == 2 ? a[i].z : a[i].w, v[w], o[i][w]);
+                }
             }
 #pragma unroll 2
             for (int c = 0; c < DK; c += 4) {
@@ -128,14 +156,15 @@ __global__ void __launch_bounds__(kThreads, 2) linear_scan_kernel(const __grid_c
 #pragma unroll
                 for (int i = 0; i < 4; ++i) q[i] = *reinterpret_cast<const float4*>(Q + (4 * ty + i) * L::pk + c);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
+                for (int k = 0; k < 4; ++k) {
+                    float x[WX];
+                    load_row(x, X + (c + k) * L::pw + WX * tx);
 #pragma unroll
-                    for (int w = 0; w < WX; ++w) {
-                        const float x = X[(c + k) * L::pw + WX * tx + w];
+                    for (int w = 0; w < WX; ++w)
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            r[i][w] = fmaf(k == 0 ? q[i].x : k == 1 ? q[i].y : k == 2 ? q[i].z : q[i].w, x, r[i][w]);
-                    }
+                            r[i][w] = fmaf(k == 0 ? q[i].x : k == 1 ? q[i].y : k == 2 ? q[i].z : q[i].w, x[w], r[i][w]);
+                }
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -159,10 +188,8 @@ __global__ void __launch_bounds__(kThreads, 2) linear_scan_kernel(const __grid_c
 #pragma unroll 4
             for (int j = 0; j < n; ++j) {
                 float v[WX], k[RX];
-#pragma unroll
-                for (int w = 0; w < WX; ++w) v[w] = V[j * L::pw + WX * tx + w];
-#pragma unroll
-                for (int i = 0; i < RX; ++i) k[i] = K[j * L::pk + RX * ty + i];
+                load_row(v, V + j * L::pw + WX * tx);
+                load_row(k, K + j * L::pk + RX * ty);
 #pragma unroll
                 for (int i = 0; i < RX; ++i)
 #pragma unroll
