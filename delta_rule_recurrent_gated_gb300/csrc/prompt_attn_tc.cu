@@ -7,8 +7,8 @@
 // take turns: while the threads of one form P from its S, the tensor cores work for the other.  Products are
 // issued by one warp in the order PV(n), S(n + 1) for each half, so that S(n + 1) being there means that PV(n)
 // is done, and the same barrier says both.
-// Warps 0-3 and 4-7 hold a row of their half per thread, warp 8 issues products, warp 9 has tiles copied
-// (10 and 11: none; registers are handed out by groups of four warps).
+// Warps 0-3 and 4-7 hold a row of their half per thread, warp 8 issues products, warps 9 and 10 have tiles copied
+// (11: none; registers are handed out by groups of four warps).
 //
 // 385 us for 8 x 4096 tokens, 16 query heads of 128, 4 key heads: 1430 TFLOP/s.  The two products of a half and stage
 // take 1140 cycles of the tensor cores, the chain from one S to the weights being back about 1600 (barriers, tensor
@@ -27,7 +27,10 @@
 namespace dr {
 namespace {
 
-constexpr int kHalf = 128, kTile = 2 * kHalf, kStage = 128, kThreads = 384, kBuffers = 2, kInfos = 4;
+constexpr int kHalf = 128, kTile = 2 * kHalf, kStage = 128, kThreads = 384, kInfos = 4;
+// Keys are needed a stage earlier.  16 documents of 1 to 2500 tokens: 153 us, with two buffers each and one warp for all
+// copies 166.
+constexpr int kKBuffers = 3, kVBuffers = 2;
 // Registers of a thread: as launched, then of the rows' threads and of the others, which give theirs up.
 constexpr int kRegs = 168, kRowRegs = 208, kOtherRegs = 88;
 static_assert(256 * kRowRegs + (kThreads - 256) * kOtherRegs <= kThreads * kRegs, "more than the block has");
@@ -41,14 +44,14 @@ struct Item {
     int lo[2], hi[2];              // stages of each half (none: lo >= hi)
 };
 struct Control {
-    uint64_t qfull, qempty, kfull[kBuffers], kempty[kBuffers], vfull[kBuffers], vempty[kBuffers], landed;
+    uint64_t qfull, qempty, kfull[kKBuffers], kempty[kKBuffers], vfull[kVBuffers], vempty[kVBuffers], landed;
     uint64_t sfull[2], pfull[2][2], odone[2], drained;  // pfull: of each half the first and the last 64 columns
     uint32_t tmem;
     volatile int dead;
     Item item[kInfos];
 };
 template <int D> struct Smem {
-    static constexpr int tile = 128 * D * 2, q = 0, k = 2 * tile, v = k + kBuffers * tile, control = v + kBuffers * tile,
+    static constexpr int tile = 128 * D * 2, q = 0, k = 2 * tile, v = k + kKBuffers * tile, control = v + kVBuffers * tile,
                          bytes = control + 1024;
     static_assert(sizeof(Control) <= 1024, "control block");
 };
@@ -75,19 +78,18 @@ __device__ __forceinline__ Item make_item(const PromptParams& p, long long k) {
 __device__ __forceinline__ int first_stage(const Item& x) { return x.lo[0]; }
 __device__ __forceinline__ int last_stage(const Item& x) { return max(x.hi[0], x.hi[1]); }  // one behind
 
-// ------------------------------------------------------------------ warp 9: copies
+// ------------------------------------------------------------------ warps 9 and 10: copies
+// Queries and keys, and the items' data.
 template <int D>
-__device__ __forceinline__ void copy_tiles(const PromptParams& p, const CUtensorMap* mq, const CUtensorMap* mk,
-                                           const CUtensorMap* mv, uint8_t* smem, Control& ct) {
+__device__ __forceinline__ void copy_keys(const PromptParams& p, const CUtensorMap* mq, const CUtensorMap* mk, uint8_t* smem, Control& ct) {
     const int lane = threadIdx.x & 31;
-    uint32_t landings = 0;
-    Ring<kBuffers> rk, rv;
+    Ring<kKBuffers> ring;
     long long items = 0;
     [&] {
         for (long long k = 0;; ++k) {
             const Item x = make_item(p, k);
-            // queries and the item's data: after the last item's products with its queries, and after the row threads
-            // have begun with it (so they are never two items behind)
+            // after the last item's products with its queries, and after the row threads and the values' copies have begun
+            // with it (so they are never two items behind)
             if (!wait(ct.dead, &ct.qempty, (k & 1) ^ 1)) return;
             if (lane == 0) {
                 ct.item[k % kInfos] = x;
@@ -102,38 +104,53 @@ __device__ __forceinline__ void copy_tiles(const PromptParams& p, const CUtensor
             __syncwarp();
             ++items;
             if (!x.any) return;
-            const int hk = x.head / p.G;
             for (int t = first_stage(x); t < last_stage(x); ++t) {
-                const int row = x.row0 + t * kStage, rows = x.len - t * kStage;
-                if (!wait(ct.dead, &ct.kempty[rk.at], rk.phase ^ 1)) return;
+                if (!wait(ct.dead, &ct.kempty[ring.at], ring.phase ^ 1)) return;
                 if (lane == 0) {  // keys behind the sequence make scores that are hidden
-                    mbar_arrive_expect_tx(&ct.kfull[rk.at], Smem<D>::tile);
-                    load_rows<kStage, D>(smem + Smem<D>::k + rk.at * Smem<D>::tile, mk, &ct.kfull[rk.at], hk, row);
+                    mbar_arrive_expect_tx(&ct.kfull[ring.at], Smem<D>::tile);
+                    load_rows<kStage, D>(smem + Smem<D>::k + ring.at * Smem<D>::tile, mk, &ct.kfull[ring.at], x.head / p.G,
+                                         x.row0 + t * kStage);
                 }
                 __syncwarp();
-                rk.step();
-                if (!wait(ct.dead, &ct.vempty[rv.at], rv.phase ^ 1)) return;
-                uint8_t* v = smem + Smem<D>::v + rv.at * Smem<D>::tile;
-                uint64_t* bar = rows < kStage ? &ct.landed : &ct.vfull[rv.at];
+                ring.step();
+            }
+        }
+    }();
+    settle(&ct.qfull, items);
+    settle(ring, ct.kfull);
+}
+template <int D> __device__ __forceinline__ void copy_values(const PromptParams& p, const CUtensorMap* mv, uint8_t* smem, Control& ct) {
+    const int lane = threadIdx.x & 31;
+    uint32_t landings = 0;
+    Ring<kVBuffers> ring;
+    [&] {
+        for (long long k = 0;; ++k) {
+            if (!wait(ct.dead, &ct.qfull, k & 1)) return;
+            const Item x = ct.item[k % kInfos];
+            warp_arrive(&ct.qempty);
+            if (!x.any) return;
+            for (int t = first_stage(x); t < last_stage(x); ++t) {
+                if (!wait(ct.dead, &ct.vempty[ring.at], ring.phase ^ 1)) return;
+                uint8_t* v = smem + Smem<D>::v + ring.at * Smem<D>::tile;
+                const int rows = x.len - t * kStage;
+                uint64_t* bar = rows < kStage ? &ct.landed : &ct.vfull[ring.at];
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bar, Smem<D>::tile);
-                    load_rows<kStage, D>(v, mv, bar, hk, row);
+                    load_rows<kStage, D>(v, mv, bar, x.head / p.G, x.row0 + t * kStage);
                 }
                 __syncwarp();
                 if (rows < kStage) {  // values behind the sequence may be anything, and zero times that is not zero
                     if (!wait(ct.dead, &ct.landed, landings++ & 1)) return;
                     clear_rows<kStage, D>(v, rows);
-                    if (lane == 0) mbar_arrive(&ct.vfull[rv.at]);
+                    if (lane == 0) mbar_arrive(&ct.vfull[ring.at]);
                     __syncwarp();
                 }
-                rv.step();
+                ring.step();
             }
         }
     }();
-    settle(&ct.qfull, items);
     settle(&ct.landed, landings);
-    settle(rk, ct.kfull);
-    settle(rv, ct.vfull);
+    settle(ring, ct.vfull);
 }
 
 // ------------------------------------------------------------------ warp 8: products
@@ -143,20 +160,22 @@ __device__ __forceinline__ void issue(const PromptParams& p, uint8_t* smem, Cont
     // descriptors of the first buffers; an address step of 16 bytes is 1 in their lowest field
     const uint64_t q0 = desc_kmajor(Tile{base + Smem<D>::q, kHalf}, 0), k0 = desc_kmajor(Tile{base + Smem<D>::k, kStage}, 0);
     const uint64_t v0 = desc_mnmajor(Tile{base + Smem<D>::v, kStage}, 0);
-    uint32_t nk = 0, nv = 0, np[2] = {0, 0};
+    Ring<kKBuffers> rk;
+    Ring<kVBuffers> rv;
+    uint32_t np[2] = {0, 0};
     for (long long k = 0;; ++k) {
         if (!wait(ct.dead, &ct.qfull, k & 1)) return;
         const Item x = ct.item[k % kInfos];
         if (!x.any) return;
         const int first = first_stage(x), last = last_stage(x);
         for (int t = first - 1; t < last; ++t) {
-            if (t >= first && !wait(ct.dead, &ct.vfull[nv % kBuffers], (nv / kBuffers) & 1)) return;
-            if (t + 1 < last && !wait(ct.dead, &ct.kfull[nk % kBuffers], (nk / kBuffers) & 1)) return;
+            if (t >= first && !wait(ct.dead, &ct.vfull[rv.at], rv.phase)) return;
+            if (t + 1 < last && !wait(ct.dead, &ct.kfull[rk.at], rk.phase)) return;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const bool pv = t >= x.lo[h] && t < x.hi[h], qk = t + 1 >= x.lo[h] && t + 1 < x.hi[h];
                 if (pv) {
-                    const uint64_t vd = v0 + (nv % kBuffers) * (Smem<D>::tile >> 4);
+                    const uint64_t vd = v0 + rv.at * (Smem<D>::tile >> 4);
 #pragma unroll
                     for (int part = 0; part < 2; ++part) {
                         if (!wait(ct.dead, &ct.pfull[h][part], np[h] & 1)) return;
@@ -174,7 +193,7 @@ __device__ __forceinline__ void issue(const PromptParams& p, uint8_t* smem, Cont
                 }
                 if (elect_one()) {
                     if (qk) {
-                        const uint64_t kd = k0 + (nk % kBuffers) * (Smem<D>::tile >> 4), qd = q0 + h * (Smem<D>::tile >> 4);
+                        const uint64_t kd = k0 + rk.at * (Smem<D>::tile >> 4), qd = q0 + h * (Smem<D>::tile >> 4);
 #pragma unroll
                         for (int kk = 0; kk < D; kk += 16)  // 16 channels: 32 bytes of a 128-byte row
                             mma_bf16(tm + s_col(h), qd + (kk >> 6) * (kHalf * 128 / 16) + (kk & 63) / 8,
@@ -185,13 +204,13 @@ __device__ __forceinline__ void issue(const PromptParams& p, uint8_t* smem, Cont
                 __syncwarp();
             }
             if (elect_one()) {
-                if (t >= first) mma_commit(&ct.vempty[nv % kBuffers]);
-                if (t + 1 < last) mma_commit(&ct.kempty[nk % kBuffers]);
+                if (t >= first) mma_commit(&ct.vempty[rv.at]);
+                if (t + 1 < last) mma_commit(&ct.kempty[rk.at]);
                 if (t + 2 == last) mma_commit(&ct.qempty);
             }
             __syncwarp();
-            if (t >= first) ++nv;
-            if (t + 1 < last) ++nk;
+            if (t >= first) rv.step();
+            if (t + 1 < last) rk.step();
         }
     }
 }
@@ -307,15 +326,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x == 32) {
         mbar_init(&ct.qfull, 1);
-        mbar_init(&ct.qempty, 1 + 8);
+        mbar_init(&ct.qempty, 1 + 8 + 1);
         mbar_init(&ct.landed, 1);
         mbar_init(&ct.drained, 1);
-        for (int i = 0; i < kBuffers; ++i) {
-            mbar_init(&ct.kfull[i], 1);
-            mbar_init(&ct.kempty[i], 1);
-            mbar_init(&ct.vfull[i], 1);
-            mbar_init(&ct.vempty[i], 1);
-        }
+        for (int i = 0; i < kKBuffers; ++i) mbar_init(&ct.kfull[i], 1), mbar_init(&ct.kempty[i], 1);
+        for (int i = 0; i < kVBuffers; ++i) mbar_init(&ct.vfull[i], 1), mbar_init(&ct.vempty[i], 1);
         for (int h = 0; h < 2; ++h) {
             mbar_init(&ct.sfull[h], 1);
             mbar_init(&ct.pfull[h][0], 4);
@@ -334,7 +349,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == 8) issue<D>(p, smem, ct), drain(&ct.drained);
-        else if (warp == 9) copy_tiles<D>(p, &mq, &mk, &mv, smem, ct);
+        else if (warp == 9) copy_keys<D>(p, &mq, &mk, smem, ct);
+        else if (warp == 10) copy_values<D>(p, &mv, smem, ct);
     }
     __syncwarp();
     tc_fence_before();
