@@ -3,7 +3,8 @@
 // (dr_linear_attn_step).
 //
 // fp32 prompts only (bf16 ones are scanned on the tensor cores); 2635 packed tokens in 5 sequences, 8 heads of 32 and 64:
-// forward 64 us in three kernels, gradient 157 us in seven, bound by the chain of a chunk (loads, three products, 8 us).
+// forward 63 us in three kernels, gradient 128 us in five, bound by issue slots and the chain of a chunk (loads, three
+// products, 8 us).
 //
 // The scan in chunks of C = 64 tokens, i and j within the chunk, X the state before it, a = e^g:
 //   out_i = sum_{j<=i} a^{i-j} (q_i.k_j) v_j + a^{i+1} X^T q_i;   X' = a^C X + sum_j a^{C-1-j} k_j v_j^T

@@ -7,8 +7,8 @@
 // so no power of a is ever above one, however strong the decay.
 //
 // A block has a sequence, or a segment of one, and a head.  The state stays in fp32 registers, a row of it in each
-// thread of eight warps, half each; what a chunk adds comes from tensor memory, and a bf16 image of the state goes to shared memory
-// for the next chunk's queries.  K' is a sum of two bf16 parts (2^-16 of it is lost), so that what the states add up over
+// thread of eight warps, half each; what a chunk adds comes from tensor memory, and a bf16 image of the state goes to
+// shared memory for the next chunk's queries.  K' is a sum of two bf16 parts (2^-16 of it is lost), so that what the states add up over
 // a sequence is not bf16; P, and the state as an operand, are rounded once (2^-8 at most).
 // Tensor memory: A with P over it, Q X, P V, K'^T V: 4 x 128 columns.
 // Warps 0-3: P.  4-7: K' (its high part over K, once A is there).  8-11: output rows.  12-19: state.  20: products,
@@ -17,7 +17,7 @@
 // The products of a chunk are issued as P V (n), Q X (n), A (n + 1), K'V (n), each when what it needs is there.  So the
 // tile of a chunk's queries is the first to be free, for the values of the next chunk, which are on their way while A
 // and K'V run (with Q X last the loop waited for them: 133 us for b8 t4096 h16 d128 instead of 119).
-// 8 x 4096 tokens, 16 heads of 128: 110 us (537 MB, 4.9 TB/s), the gradient's three scans 300 us.  Bound by how little is
+// 8 x 4096 tokens, 16 heads of 128: 110 us (537 MB, 4.9 TB/s), the gradient's three scans 295 us.  Bound by how little is
 // in flight: of 227 KB, low parts and state hold 64 KB and a chunk's own tiles most of the ring (with nothing but the
 // copies the same kernel takes 61 us).  What moved it: short code for each task (unrolled to the end, five instruction
 // streams missed the instruction cache: 170 us), K' and P by warps of their own, the order of the products, rows by tensor

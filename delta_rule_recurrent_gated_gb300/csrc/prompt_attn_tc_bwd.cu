@@ -6,7 +6,7 @@
 //
 // Two kernels, so that every sum has one owner: no atomics, no fp32 image of a gradient in memory, the same
 // bits every time.  They form S and dP = dO V^T twice, 7 products where 5 would do.  8 x 4096 tokens, 16 query heads of
-// 128, 4 key heads: dq 565 us (1460 TFLOP/s of its own three products), dk and dv 672 us (1640 TFLOP/s of their four),
+// 128, 4 key heads: dq 563 us (1460 TFLOP/s of its own three products), dk and dv 678 us (1620 TFLOP/s of their four),
 // bound by the tensor cores and the operands they read from shared memory; D = dO.o before them 49 us.
 //   dq:     128 queries of a head, against 128 keys a stage: S = Q K^T, dP = dO V^T, dQ += dS K, issued as
 //           S(n + 1), dP(n + 1), dQ(n).  dP has two buffers in tensor memory, and dS takes the place of its dP.

@@ -440,8 +440,9 @@ int dr_cache_attn(const dr_cache* cache, const dr_cache_seqs* seqs, const dr_att
  * projection, or of its gradient, will do); o, dO contiguous.  Everything is of io dtype except
  * statistics, decays and states, which are fp32.
  * Arithmetic: fp32 for fp32 tensors.  For bf16 the products take bf16 operands and accumulate in
- * fp32; softmax weights, decayed scores and the state that queries read are rounded to bf16 as
- * operands, what is carried from chunk to chunk (the states) is not.
+ * fp32; softmax weights and their gradients, decayed scores and the state that queries read are rounded
+ * to bf16 as operands, what is carried from chunk to chunk (the states) is not: states that come back
+ * are good to 2^-16 of their terms.  The gradient takes dO.o from o as it was rounded.
  * Gradients of shared key heads are summed in a fixed order: the same inputs give the same bits.
  * Outputs do not overlap inputs.
  * A token that is not finite leaves other sequences alone; in its own it may also reach the results
