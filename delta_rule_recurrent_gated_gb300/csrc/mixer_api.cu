@@ -150,7 +150,7 @@ int dr_prompt_attn_bwd(const dr_prompt_desc* desc, const void* q, const void* k,
 }
 
 size_t dr_linear_attn_workspace_bytes(const dr_linear_desc* desc) {
-    return check_linear(desc, true, false) == DR_OK ? linear_bytes(desc) : 0;
+    return check_linear(desc, false, false) == DR_OK ? linear_bytes(desc) : 0;  // of a forward call alone too
 }
 
 int dr_linear_attn_fwd(const dr_linear_desc* desc, const void* q, const void* k, const void* v,
