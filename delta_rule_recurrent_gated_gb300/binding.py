@@ -776,7 +776,7 @@ class _Mixer(_Calls):
     """What the plans of PromptAttention and LinearAttention share: tensors as rows of heads, sequences
     dense [B, T] or packed into the rows of one (B = 1, ``seqs`` of them, offsets ``cu`` at each call)."""
 
-    def _plan(self, desc, seqs, io):
+    def _plan(self, desc, seqs, io, word):
         d = self.desc = desc
         if seqs is not None and d.B != 1:
             raise ValueError("packed sequences are the rows of one batch: B has to be 1")
@@ -784,11 +784,15 @@ class _Mixer(_Calls):
         d.io_dtype = _TYPE_CODES[io]
         self.io_dtype, self._cu = _torch_type(io), None if seqs is None else (seqs + 1,)
         self._refs, self._spaces = {}, {}
-        self.word = self._torch.zeros(4, dtype=self._i32, device=self.device)
-        d.status = self.word.data_ptr()
+        if word is None:
+            word = self._torch.zeros(4, dtype=self._i32, device=self.device)
+        else:
+            _address(word, self._i32, (4,), "word", self._index if self.device.type == "cuda" else -1)
+        self.word = word
+        d.status = word.data_ptr()
 
     def status(self) -> int:
-        """DR_OK, or DR_ERR_TIMEOUT after a kernel's bounded wait ran out."""
+        """DR_OK, or DR_ERR_TIMEOUT after a kernel's bounded wait ran out (of any plan with the same word)."""
         return check_status(self.word.data_ptr(), self._stream())
 
     def _ref(self, lds):
@@ -827,18 +831,20 @@ class PromptAttention(_Mixer):
     ``seqs``: packed sequences, at most that many; B is 1, T the rows in all, and each call takes the offsets
     ``cu`` [seqs + 1] (int32, device).  Rows of no sequence are left as they were.
 
+    ``word``: another plan's, so that its status() tells of this one's calls too, also when this one is gone.
+
     A plan may be used on any stream of its device and by several threads: the gradient's workspace is one for
     each of both, kept with the plan; graphs that were captured on one stream share it, so they are replayed
     one after another."""
 
-    def __init__(self, B, T, Hq, H, d, seqs=None, io="bf16", scale=None, window=0, device="cuda"):
+    def __init__(self, B, T, Hq, H, d, seqs=None, io="bf16", scale=None, window=0, device="cuda", word=None):
         self._at(device)
         e = DrPromptDesc()
         e.B, e.T, e.Hq, e.H, e.d, e.window = B, T, Hq, H, d, window
         e.scale = d ** -0.5 if scale is None else float(scale)
         e.ld_q = e.ld_dq = Hq * d
         e.ld_k = e.ld_v = e.ld_dk = e.ld_dv = H * d
-        self._plan(e, seqs, io)
+        self._plan(e, seqs, io, word)
         self._q, self._k, self._lse = (B, T, Hq, d), (B, T, H, d), (B, T, Hq)
         self._fwd, self._bwd = self._lib.dr_prompt_attn_fwd, self._lib.dr_prompt_attn_bwd
         self._ws_bytes = int(self._lib.dr_prompt_attn_workspace_bytes(ctypes.byref(e)))
@@ -884,16 +890,16 @@ class LinearAttention(_Mixer):
 
     q, k [B, T, H, dk] and v [B, T, H, dv] may be head ranges of one packed projection; g [H] fp32 is the
     log-decay of a step, a constant of the layer; states are [sequences, H, dk, dv] fp32.  ``seqs`` and ``cu``:
-    packed sequences, as for PromptAttention, and so are streams, threads and graphs."""
+    packed sequences, as for PromptAttention, and so are ``word``, streams, threads and graphs."""
 
-    def __init__(self, B, T, H, dk, dv, seqs=None, io="bf16", scale=1.0, device="cuda"):
+    def __init__(self, B, T, H, dk, dv, seqs=None, io="bf16", scale=1.0, device="cuda", word=None):
         self._at(device)
         e = DrLinearDesc()
         e.B, e.T, e.H, e.d_k, e.d_v = B, T, H, dk, dv
         e.scale = float(scale)
         e.ld_q = e.ld_k = e.ld_dq = e.ld_dk = H * dk
         e.ld_v = e.ld_dv = H * dv
-        self._plan(e, seqs, io)
+        self._plan(e, seqs, io, word)
         self._k, self._v, self._g = (B, T, H, dk), (B, T, H, dv), (H,)
         self._h = (e.num_seqs, H, dk, dv)
         self._fwd, self._bwd, self._step = (getattr(self._lib, "dr_linear_attn_" + n) for n in ("fwd", "bwd", "step"))

@@ -77,9 +77,14 @@ class DecayLayer:
         if T == 1:
             o = self.decoder.step(q, k, v, self.g, self.state)
         else:
-            p = binding.LinearAttention(B, T, self.H, self.d, self.d, scale=self.d ** -0.5, device=self.device)
+            p = binding.LinearAttention(B, T, self.H, self.d, self.d, scale=self.d ** -0.5, device=self.device,
+                                        word=self.decoder.word)
             o, self.state = p.forward(q, k, v, self.g, h0=self.state)
         return x + o.reshape(B, T, -1) @ self.w_out
+
+    def status(self):
+        """Of the steps and of all prompts, whose plans end with them."""
+        return self.decoder.status()
 
 
 class AttentionLayer:
@@ -116,6 +121,9 @@ class AttentionLayer:
         self.lens += T
         return x + o.reshape(B, T, -1) @ self.w_out
 
+    def status(self):
+        return self.cache.status()
+
 
 class HybridStack:
     """`layers` delta-rule layers (linear="delta") or linear-attention layers ("decay") with an attention layer after
@@ -138,7 +146,8 @@ class HybridStack:
         return x
 
     def status(self):
-        return max(layer.cache.status() for layer in self.layers if isinstance(layer, AttentionLayer))
+        """DR_OK, or what a call of the attention and linear-attention layers left in their status words."""
+        return max((layer.status() for layer in self.layers if not isinstance(layer, DeltaLayer)), default=binding.DR_OK)
 
 
 class _TrainedLayer:
@@ -192,6 +201,9 @@ class TrainedAttention(_TrainedLayer):
         self.grads.update(wq=dw["dwq"], wk=dw["dwk"])
         return dqkv
 
+    def status(self):
+        return self.attend.status()
+
 
 class TrainedDecay(_TrainedLayer):
     """Linear attention with a fixed decay for each head."""
@@ -209,6 +221,9 @@ class TrainedDecay(_TrainedLayer):
         dqkv = torch.zeros(1, do.shape[1], 3 * self.H, self.d, dtype=do.dtype, device=do.device)
         self.plan.backward(*self.kept, do, cu=cu, out=dict(zip(("dq", "dk", "dv"), dqkv.split(self.H, 2))))
         return dqkv
+
+    def status(self):
+        return self.plan.status()
 
 
 class TrainingStack:
@@ -236,6 +251,10 @@ class TrainingStack:
         for layer in reversed(self.layers):
             dy = layer.backward(dy, self.cu, self.pos)
         return dy
+
+    def status(self):
+        """DR_OK, or DR_ERR_TIMEOUT after a bounded wait of a mixer's kernels ran out: results are then incomplete."""
+        return max(layer.status() for layer in self.layers)
 
 
 def main():
