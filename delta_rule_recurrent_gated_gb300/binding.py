@@ -828,8 +828,8 @@ class PromptAttention(_Mixer):
     q [B, T, Hq, d], k and v [B, T, H, d], which may be head ranges of one packed projection; query head h
     reads key head h // (Hq // H).
 
-    ``seqs``: packed sequences, at most that many; B is 1, T the rows in all, and each call takes the offsets
-    ``cu`` [seqs + 1] (int32, device).  Rows of no sequence are left as they were.
+    ``seqs``: packed sequences, at most that many (2^20 at most); B is 1, T the rows in all, and each call takes
+    the offsets ``cu`` [seqs + 1] (int32, device).  Rows of no sequence are left as they were.
 
     ``word``: another plan's, so that its status() tells of this one's calls too, also when this one is gone.
 

@@ -23,9 +23,13 @@ int check_row(long long ld, long long row, int type) {
     if (ld < row || ld >= (1ll << 40)) return DR_ERR_INVALID_ARG;
     return ld * (type == DR_BF16 ? 2 : 4) % 16 ? DR_ERR_ALIGNMENT : DR_OK;
 }
+// Packed sequences of a call.  To find a tile a warp walks over their offsets, 32 in 0.3 to 1 us, while its block waits: for
+// 2^20 of them 33 ms, of the 2 s that a wait may take.  (The walk's 32-bit counters end at 2^31 - 32.)
+constexpr int kMostPacked = 1 << 20;
 int check_seqs(int B, int T, int num_seqs) {
     if (B < 0 || T < 0 || num_seqs < 0) return DR_ERR_INVALID_ARG;
     if ((long long)B * T >= (1ll << 30)) return DR_ERR_UNSUPPORTED;
+    if (num_seqs > kMostPacked && num_seqs != B) return DR_ERR_UNSUPPORTED;
     return DR_OK;
 }
 // num_seqs has to be that of the layout that the call uses.

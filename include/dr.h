@@ -431,10 +431,12 @@ int dr_cache_attn(const dr_cache* cache, const dr_cache_seqs* seqs, const dr_att
  *
  * Sequences, for both: dense, cu_seqlens NULL, num_seqs == B sequences of T tokens; or packed,
  * B == 1, T rows, sequence s in the rows cu_seqlens[s] .. cu_seqlens[s + 1] - 1 (device
- * [num_seqs + 1], read when the kernels run: a captured call takes new lengths).  Lengths may be
- * zero.  Rows of no sequence are left as they were.  An offset outside 0 .. T counts as the nearest
- * of them and a sequence that would end before it starts as empty: nothing else is touched (where
- * sequences then overlap, their results are undefined).
+ * [num_seqs + 1], read when the kernels run: a captured call takes new lengths), num_seqs at most
+ * 2^20 (every tile is looked up by a walk over the offsets: the time of many short sequences grows
+ * with the square of their number).  Lengths may be zero.  Rows of no sequence are left as they
+ * were.  An offset outside 0 .. T counts as the nearest of them and a sequence that would end
+ * before it starts as empty: nothing else is touched (where sequences then overlap, their results
+ * are undefined).
  * Tensors are rows of heads: q [B*T] rows of Hq*d values (or H*d_k), ld_q elements from one row to
  * the next, and k, v, dq, dk, dv likewise with their own distances (column ranges of one packed
  * projection, or of its gradient, will do); o, dO contiguous.  Everything is of io dtype except
