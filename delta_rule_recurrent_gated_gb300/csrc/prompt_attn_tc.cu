@@ -219,8 +219,9 @@ __device__ __forceinline__ void issue(const PromptParams& p, uint8_t* smem, Cont
 template <int D> __device__ __forceinline__ void soften(const PromptParams& p, Control& ct) {
     const int h = threadIdx.x / kHalf, r = threadIdx.x % kHalf;
     const uint32_t ts = warp_lane_base(ct.tmem) + s_col(h), to = warp_lane_base(ct.tmem) + o_col(h);
-    // scores in base 2; a zero factor and -inf make no NaN
-    const float c2 = fmaxf(fabsf(p.scale) * kLog2e, 1e-37f);
+    // Scores in base 2: c2 s, with a negative scale's sign in s.  A scale of zero makes s zero and c2 one, because zero times
+    // the -inf of what is hidden is no number.
+    const float c2 = p.scale == 0.f ? 1.f : fabsf(p.scale) * kLog2e, sign = p.scale == 0.f ? 0.f : -1.f;
     uint32_t n = 0, done = 0;
     for (long long k = 0;; ++k) {
         if (!wait(ct.dead, &ct.qfull, k & 1)) return;
@@ -239,9 +240,9 @@ template <int D> __device__ __forceinline__ void soften(const PromptParams& p, C
 #pragma unroll
             for (int c = 0; c < kStage; c += 32) tmem_ld32(ts + c, s + c);
             tmem_ld_wait();
-            if (p.scale < 0.f)
+            if (p.scale <= 0.f)
 #pragma unroll
-                for (int j = 0; j < kStage; ++j) s[j] = -s[j];
+                for (int j = 0; j < kStage; ++j) s[j] *= sign;
             if (j0 + kStage - 1 > w0 || (p.window && j0 <= w0 + 31 - p.window)) {
                 const int up = pos - j0, down = p.window ? up - p.window : -1;
 #pragma unroll
