@@ -374,7 +374,11 @@ template <typename IO> cudaError_t step_of(const StepParams& p, cudaStream_t st)
 }  // namespace
 
 // Blocks that run at once; from how many chunks on, and into how few, sequences are split.  On the tensor cores a block
-// has an SM to itself and its start costs about two chunks; on the CUDA cores two share one.
+// has an SM to itself and its start costs about two chunks; on the CUDA cores two share one.  The numbers are those of
+// 152 SMs; with others sequences would be split in other places, to the same results but for the rounding.
+// bf16, forward + gradient in us.  One sequence, 4 heads of 128, whole and split: 8 chunks 33 + 33 and 41 + 42, 12 chunks
+// 43 + 43 and 41 + 43, 20 chunks 66 + 66 and 41 + 43: split from 12 on.  Three of 2000 tokens, segments of at least 2, 4
+// and 8 chunks: 41 + 53, 48 + 53, 65 + 70; four of 4096, 8 heads of 128: 84 + 175, 84 + 175, 74 + 175.
 int scan_span(int io, long long rows, int N, int T, bool packed, int H, int dk, int dv, int scans) {
     if (rows == 0 || N == 0) return 0;
     const bool tc = io == DR_BF16;
@@ -389,7 +393,13 @@ int scan_span(int io, long long rows, int N, int T, bool packed, int H, int dk, 
         span = (chunks / N + segments - 1) / segments;
     } else {
         // Lengths are known on the device only.  On the tensor cores, where a split costs more, only what is far longer than
-        // a block's share of all chunks.
+        // a block's share of all chunks: never, from 5/2 shares on, from one on (us, forward + gradient):
+        //   16 documents of 1 to 2500 tokens, 8 heads of 64 x 128   61 + 146    71 + 163    86 + 164
+        //   64 of 1 to 600, the same heads                          59 + 175    77 + 218    80 + 219
+        //   8 of 4096, 16 heads of 128                             112 + 296   124 + 314   230 + 315
+        //   16384 and four of 50 to 1000, 8 heads of 128           368 + 366   121 + 296    77 + 151
+        //   two of 8000 and 30 of 100, 4 heads of 64               165 + 172    65 + 157    44 + 84
+        // The 10 to 43 us that a split costs where no sequence is that long are two launches with nothing to do.
         span = ((tc ? 5 : 2) * chunks * (units / N) / 2 + room - 1) / room;
     }
     return (int)std::min<long long>(std::max<long long>(span, least), 1 << 22);

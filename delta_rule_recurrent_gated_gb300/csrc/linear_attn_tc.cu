@@ -31,7 +31,8 @@ namespace dr {
 namespace {
 
 constexpr int kC = kScanChunk, kThreads = 768, kSlots = 5;
-// Registers of a thread: as launched, then of the six groups of four warps (two of them the state's).
+// Registers of a thread: as launched, then of the six groups of four warps (two of them the state's).  What is compiled for
+// 80 spills 24 bytes (64 channels), 56 (128) or 80 (64 and 128), 8 where only states are formed.
 constexpr int kRegs = 80, kWeightRegs = 88, kKeyRegs = 72, kOutRegs = 96, kStateRegs = 88, kOtherRegs = 48;
 static_assert(kWeightRegs >= kRegs && kOutRegs >= kRegs && kStateRegs >= kRegs && kKeyRegs <= kRegs && kOtherRegs <= kRegs,
               "each takes or gives, as its instruction says");

@@ -7,7 +7,8 @@
 // Two kernels, so that every sum has one owner: no atomics, no fp32 image of a gradient in memory, the same
 // bits every time.  They form S and dP = dO V^T twice, 7 products where 5 would do.  8 x 4096 tokens, 16 query heads of
 // 128, 4 key heads: dq 563 us (1460 TFLOP/s of its own three products), dk and dv 678 us (1620 TFLOP/s of their four),
-// bound by the tensor cores and the operands they read from shared memory; D = dO.o before them 49 us.
+// bound by the tensor cores and the operands they read from shared memory; D = dO.o before them 49 us.  That is each alone,
+// at 2070 MHz; in a stream of passes the power limit brings the clock to 1957 MHz and them to 601, 717 and 50 us.
 //   dq:     128 queries of a head, against 128 keys a stage: S = Q K^T, dP = dO V^T, dQ += dS K, issued as
 //           S(n + 1), dP(n + 1), dQ(n).  dP has two buffers in tensor memory, and dS takes the place of its dP.
 //   dk, dv: 128 keys of a key head, against 128 queries a stage of all query heads that read it, one after another:
@@ -654,8 +655,9 @@ template <int D> cudaError_t launch(const PromptParams& p, cudaStream_t st) {
         dq::prompt_dq_tc_kernel<D><<<blocks(most_tiles(p.s, kRows) * p.Hq), kThreads, dq::Smem<D>::bytes, st>>>(p, m[0], m[1], m[2], m[3]);
         if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     }
-    // A block for each item, so that one that is through takes the next in order: 1066 us instead of 1425 with a block for
-    // each SM and its items dealt out beforehand (b8 t4096, 16 heads of 128, four of keys).
+    // A block for each item, so that one that is through takes the next in order: with the stages of 64 that this kernel had
+    // before, 1066 us instead of 1425 with a block for each SM and its items dealt out beforehand (b8 t4096, 16 heads of
+    // 128, four of keys; 678 us with the stages of 128).
     const long long keys = most_tiles(p.s, kRows) * p.H;
     if (keys >= (1ll << 31)) return cudaErrorInvalidValue;
     TraceScope ts("prompt_dkv_tc", st);

@@ -75,7 +75,10 @@ __device__ __forceinline__ bool find_tile_in_order(const Seqs& q, int R, int lea
 // Tile number `item` of all tiles of R rows, those with the largest index in their sequence first (under a
 // causal mask the longest rows of work start first and the short ones fill the gaps); called by a whole warp.
 // Returns false where there are fewer tiles.  With many sequences, whose tiles are few, in their order: a search is
-// a pass over the offsets instead of one for each power of two of the tiles.
+// a pass over the offsets instead of one for each power of two of the tiles.  Attention, 8 heads of 64, longest first and
+// in order: 512 sequences of 1 to 500 tokens forward 397 and 235 us, gradient 1134 and 760; 256 of them 151 and 117, 436 and
+// 328; but 16 of 1 to 2500 (16 heads of 128), gradient 236 and 250.  A walk over the offsets for each tile is the square of
+// the number of sequences in time: 4096 of 1 to 16 tokens 3.5 ms forward, 65536 for one head 0.14 s.
 __device__ __forceinline__ bool find_tile(const Seqs& q, int R, long long item, int& seq, int& tile) {
     if (!q.cu) {
         const int n = (q.T + R - 1) / R;

@@ -487,8 +487,8 @@ int dr_prompt_attn_bwd(const dr_prompt_desc* desc, const void* q, const void* k,
  * sequence without tokens hands its state on (hT = h0, dh0 = dhT).
  * dr_linear_attn_fwd: o [B, T, H, d_v] and hT.  dr_linear_attn_bwd: dq, dk, dv and dh0 of
  * L = sum(dO * o) + sum(dhT * hT).  Workspace for both: dr_linear_attn_workspace_bytes (0 when desc
- * is invalid or unsupported, ld_dq, ld_dk, ld_dv not looked at; needs the device current that will run
- * the call); results do not depend on what it held.
+ * is invalid or unsupported; ld_dq, ld_dk, ld_dv are not looked at); results do not depend on what
+ * it held.
  * dr_linear_attn_step: the recurrence token by token for T tokens of every sequence, on the caller's
  * state [B, H, d_k, d_v] fp32, updated in place (fp32 arithmetic for both types; dense only; ld_dq,
  * ld_dk, ld_dv are not looked at).
