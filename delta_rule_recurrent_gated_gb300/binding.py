@@ -784,8 +784,12 @@ class _Mixer(_Calls):
         d.io_dtype = _TYPE_CODES[io]
         self.io_dtype, self._cu = _torch_type(io), None if seqs is None else (seqs + 1,)
         self._refs, self._spaces = {}, {}
+        self._zeroed = None
         if word is None:
+            cuda = self._torch.cuda
             word = self._torch.zeros(4, dtype=self._i32, device=self.device)
+            if self.device.type == "cuda" and not cuda.is_current_stream_capturing():
+                self._zeroed = cuda.current_stream(self.device).record_event()
         else:
             _address(word, self._i32, (4,), "word", self._index if self.device.type == "cuda" else -1)
         self.word = word
@@ -793,7 +797,14 @@ class _Mixer(_Calls):
 
     def status(self) -> int:
         """DR_OK, or DR_ERR_TIMEOUT after a kernel's bounded wait ran out (of any plan with the same word)."""
-        return check_status(self.word.data_ptr(), self._stream())
+        stream, zeroed = self._stream(), self._zeroed
+        if zeroed is not None:
+            # the zeros may still wait on the stream the plan was made on (a kernel's report comes two seconds after it at
+            # the earliest)
+            self._torch.cuda.current_stream(self.device).wait_event(zeroed)
+        code = check_status(self.word.data_ptr(), stream)
+        self._zeroed = None
+        return code
 
     def _ref(self, lds):
         """The descriptor of calls with these six row distances.  It is not changed afterwards: the library
