@@ -347,8 +347,8 @@ struct Control {
 };
 template <int D> struct Smem {
     static constexpr int k = 0, v = kTileBytes<D>, q = 2 * v, g = q + kFirst * kTileBytes<D>, control = g + kSecond * kTileBytes<D>,
-                         bytes = control + 3072;
-    static_assert(sizeof(Control) <= 3072, "control block");
+                         bytes = control + 3 * 1024;
+    static_assert(sizeof(Control) <= 3 * 1024, "control block");
 };
 // Dense batches in the order of the sequences, the first keys first, which have the most queries: the blocks that run at
 // the same time then read the same queries (all first keys of all sequences first, and eight sequences of 4096 tokens
